@@ -1,7 +1,7 @@
 /*
  * ssm.h: C ABI of the GB300 (sm_103a) selective state-space forward library.
  *
- * Three operations, all forward only, all on one GPU:
+ * Three scans and the operators around them, all forward only, all on one GPU:
  *
  *   ssm_ssd_fwd      Mamba-2 chunked SSD forward, (x, dt, A, B, C, D, h0) -> (y, h_final).
  *                    Definition: "Accelerating Mamba-2 with High-Performance Forward
@@ -28,10 +28,16 @@
  *                    pair combine (a1,b1).(a2,b2) = (a1 a2, a2 b1 + b2) (same page, "The
  *                    five kernels", Level 3c).
  *
+ *   ssm_conv_fwd, ssm_conv_step, ssm_selscan_fwd, ssm_selscan_step, ssm_rmsnorm_fwd,
+ *   ssm_rmsnorm_fp8_fwd
+ *                    what stands around the scan of a layer: the short causal convolution, the
+ *                    selective scan with a decay for each channel and state entry, the
+ *                    root-mean-square norm.  Strided inputs; see their section.
+ *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller; the library never
  *     allocates, frees or retains them.  Tensors are dense, row-major (C order), with a
- *     16-byte aligned base address.
+ *     16-byte aligned base address, unless an entry point says otherwise.
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL = legacy default
  *     stream).  The call returns once the kernels are enqueued.
  *   - Host-detectable errors return synchronously, before anything is enqueued.  No
@@ -219,6 +225,138 @@ SSM_API ssm_status ssm_ssd_step(const void *x, const void *dt, const float *A, c
                                 int64_t batch, int nheads, int headdim, int dstate, int ngroups,
                                 ssm_dtype dtype, ssm_stream_t stream);
 
+/*
+ * The operators around a layer's scan: the short causal convolution, the selective scan with a
+ * decay for each channel and state entry (Mamba-1 layers), each for prompts and for single
+ * tokens, and the root-mean-square norm with the residual's addition.
+ *
+ * Their token tensors are often columns of a projection's wider rows, so they are given with
+ * strides: an ssm_tokens names element (b, t, c) at ptr[b * batch_stride + t * token_stride + c],
+ * strides in elements.  ptr needs the alignment of one element only; rows that start on 16-byte
+ * boundaries (ptr and both strides) take the vector loads.  The other tensors are dense; the
+ * parameters (weights, A, D, biases) are f32.  No input may overlap an output, except a step's
+ * state (below); overlaps of the whole tensors are rejected with SSM_ERR_INVALID_ARG.
+ * The outputs and states need the alignment of one element only.
+ *
+ * lens (prompts): NULL, or [batch] int32 in device memory: sequence b has lens[b] tokens (values
+ * outside 0 .. seqlen are clamped) and the rest of its row is padding.  Padding is not read, its
+ * outputs are 0 and it leaves the states as they are, so a sequence of no tokens hands its
+ * initial state on.
+ * slots (steps): NULL (sequence b has the states' row b; then nslots must equal batch), or [batch]
+ * int32 in device memory: sequence b has row slots[b] of the nslots rows of state_in and
+ * state_out.  A slot outside 0 .. nslots-1 (-1, say) marks an unused place of the batch: its
+ * output is 0 and no state is touched.  Two places must not name the same slot.
+ */
+typedef struct {
+    const void *ptr;
+    int64_t batch_stride; /* elements from one sequence to the next */
+    int64_t token_stride; /* elements from one token to the next (steps: unused) */
+} ssm_tokens;
+
+typedef enum {
+    SSM_ACT_NONE = 0,
+    SSM_ACT_SILU = 1 /* v / (1 + exp(-v)) */
+} ssm_act;
+
+/*
+ * Short causal convolution of each channel on its own, over a prompt:
+ *     y_t[c] = act(bias[c] + sum_k w[c, k] x_{t - width + 1 + k}[c]),
+ * where tokens before the first are the carried state: x_{-1} is its last row, and so on.
+ *   x          [batch, seqlen, channels] `dtype`
+ *   w          [channels, width] f32; bias [channels] f32 or NULL (zeros)
+ *   state_in   [batch, width - 1, channels] `dtype`: the last width - 1 tokens before the
+ *              prompt, oldest first; NULL for zeros
+ *   y          [batch, seqlen, channels] `dtype`, dense
+ *   state_out  [batch, width - 1, channels] `dtype`: the same after the prompt, or NULL
+ * Sums in f32.  Sizes: batch, seqlen >= 0, channels >= 1, width 2 .. 4.  No workspace; one kernel.
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (width; a grid beyond the launch limits),
+ *   SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
+ */
+SSM_API ssm_status ssm_conv_fwd(ssm_tokens x, const float *w, const float *bias, const void *state_in,
+                                const int32_t *lens, void *y, void *state_out, int64_t batch, int64_t seqlen,
+                                int channels, int width, ssm_act act, ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * The same for ONE new token per sequence:
+ *   x [batch, channels] (batch_stride), y [batch, channels] dense,
+ *   state_in, state_out [nslots, width - 1, channels] `dtype`; state_out may be state_in (in place),
+ *   any other overlap of the two is rejected; with a state_out of its own, only the rows that
+ *   slots name are written.  state_in may be NULL (zeros).  Errors: as ssm_conv_fwd.
+ */
+SSM_API ssm_status ssm_conv_step(ssm_tokens x, const float *w, const float *bias, const void *state_in,
+                                 const int32_t *slots, void *y, void *state_out, int64_t batch, int64_t nslots,
+                                 int channels, int width, ssm_act act, ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * Selective scan over a prompt ("Selective-scan CUDA kernels", section "The problem", gives the
+ * scalar recurrence; here each channel c has dstate of them, with a_t and b_t computed from the
+ * tokens):
+ *     delta_t[c] = softplus(dt_t[c] + dt_bias[c])     (without the softplus if softplus is 0)
+ *     h_t[c, n]  = exp(delta_t[c] A[c, n]) h_{t-1}[c, n] + delta_t[c] u_t[c] B_t[g, n]
+ *     y_t[c]     = (sum_n h_t[c, n] C_t[g, n] + D[c] u_t[c]) * silu(z_t[c])
+ * with g = c / (channels / ngroups).
+ *   u, dt, z   [batch, seqlen, channels] `dtype`; z.ptr NULL: no gate
+ *   B, C       [batch, seqlen, ngroups * dstate] `dtype` (a token's groups are adjacent)
+ *   A          [channels, dstate] f32; D, dt_bias [channels] f32 or NULL (zeros)
+ *   h0         [batch, channels, dstate] f32 or NULL (zeros)
+ *   y          [batch, seqlen, channels] `dtype`, dense
+ *   h_final    [batch, channels, dstate] f32, or NULL
+ * States and sums are f32; softplus(v) is max(v, 0) + log(1 + exp(-|v|)).
+ * Sizes: batch, seqlen >= 0, ngroups >= 1 dividing channels, dstate in {8, 16, 32, 64}.
+ * Workspace: f32 end states of pieces of the time axis, where there are too few channels to fill
+ * the GPU (0 bytes where there are not); it need not be cleared and carries nothing from call to
+ * call.  Two kernels where the axis is split, one otherwise.
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_WORKSPACE,
+ *   SSM_ERR_CUDA.
+ */
+typedef struct {
+    ssm_tokens u, dt, B, C, z;
+    const float *A, *D, *dt_bias, *h0;
+    const int32_t *lens;
+    void *y;
+    float *h_final;
+    int64_t batch, seqlen;
+    int32_t channels, dstate, ngroups, softplus;
+    int32_t dtype; /* ssm_dtype */
+    int32_t reserved; /* 0 */
+} ssm_selscan_args;
+SSM_API size_t ssm_selscan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups);
+SSM_API ssm_status ssm_selscan_fwd(const ssm_selscan_args *args, void *workspace, size_t workspace_bytes,
+                                   ssm_stream_t stream);
+
+/*
+ * The same for ONE new token per sequence, over the f32 states [nslots, channels, dstate]:
+ * h0 is state_in (NULL for zeros), h_final state_out (required), which may be the same pointer (in
+ * place; any other overlap is rejected); seqlen and lens are not used.  One kernel, no workspace.
+ */
+SSM_API ssm_status ssm_selscan_step(const ssm_selscan_args *args, const int32_t *slots, int64_t nslots,
+                                    ssm_stream_t stream);
+
+/*
+ * Root-mean-square norm of rows, after the residual's addition:
+ *     r = x + residual (x alone where residual is NULL);  residual_out = r
+ *     v = r / sqrt(mean(r^2) + eps) * weight
+ * in f32; v is computed from r before residual_out's rounding.
+ *   x             [rows, width] `dtype`, x_stride elements from row to row
+ *   residual      [rows, width] dense, `res_dtype` (SSM_F32, or `dtype`); residual_out the same
+ *                 (it may be the same pointer: updated in place; NULL: not written)
+ *   weight        [width] f32
+ *   y             ssm_rmsnorm_fwd: [rows, width] `dtype`, dense: v
+ *   q, scale      ssm_rmsnorm_fp8_fwd: e4m3 codes [rows, width], dense, and f32 scales, one for
+ *                 each `group` columns of a row (group 128: [rows, ceil(width / 128)]) or for each
+ *                 row (group 0: [rows]): scale = max(max|v| / 448, 2^-126), q = e4m3(v / scale),
+ *                 round to nearest even.  A NaN in v gives NaN in q there and in its scale.
+ * Sizes: rows >= 0, width >= 1.  No workspace; one kernel.
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (group), SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
+ */
+SSM_API ssm_status ssm_rmsnorm_fwd(const void *x, int64_t x_stride, const float *weight, const void *residual,
+                                   void *residual_out, void *y, int64_t rows, int width, float eps,
+                                   ssm_dtype dtype, ssm_dtype res_dtype, ssm_stream_t stream);
+SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const float *weight, const void *residual,
+                                       void *residual_out, void *q, float *scale, int64_t rows, int width,
+                                       int group, float eps, ssm_dtype dtype, ssm_dtype res_dtype,
+                                       ssm_stream_t stream);
+
 /* Workspace size in bytes for ssm_linscan_fwd on rows x len (0 when a size is negative). */
 SSM_API size_t ssm_linscan_workspace_bytes(int64_t rows, int64_t len);
 
@@ -384,7 +522,7 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
 
 /*
  * Kernel timing (measurement aid; not needed in normal use).  Between ssm_profile_begin()
- * and ssm_profile_end(), every ssm_ssd_fwd / ssm_ssd_step / ssm_linscan_fwd call records a
+ * and ssm_profile_end(), every call that computes records a
  * CUDA event on its own stream before and after each kernel it launches (at most
  * `max_launches` launches are recorded; later ones are counted but not timed).  ssm_profile_end() synchronizes the
  * recorded events and writes, for each kernel id below, the summed device time in
@@ -393,10 +531,12 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
  * 3 ssd_state_passing, 4 ssd_chunk_scan, 5 ssd_state_fused (chunk states and state passing in
  * one pass; used instead of 2 and 3 where it applies), 6 ssd_step (ssm_ssd_step),
  * 7 linscan_baseline (ssm_linscan_baseline, all its launches), 8 ssd_state_fixup (the second
- * kernel of the one-kernel state pass with split chains).  Host-side only;
+ * kernel of the one-kernel state pass with split chains), 9 conv (ssm_conv_fwd), 10 conv_step,
+ * 11 selscan_piece (the first kernel of ssm_selscan_fwd with a split time axis), 12 selscan
+ * (ssm_selscan_fwd), 13 selscan_step, 14 rmsnorm (both forms).  Host-side only;
  * process-global; not thread-safe.
  */
-#define SSM_PROFILE_KERNELS 9
+#define SSM_PROFILE_KERNELS 15
 SSM_API ssm_status ssm_profile_begin(int max_launches);
 SSM_API ssm_status ssm_profile_end(double *ms_out, int64_t *launches_out);
 

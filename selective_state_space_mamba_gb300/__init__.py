@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) selective state-space forward: Mamba-2 chunked SSD and the scalar scan.
+"""GB300 (sm_103a) selective state-space forward: Mamba-2 chunked SSD, the scalar scan, and the
+operators around a layer's scan (short convolution, per-channel selective scan, norm).
 
 Python entry points with the names of the C ABI (include/ssm.h).  They only marshal torch
 CUDA tensors into the C calls; every step of the computation runs in the library's CUDA
@@ -7,6 +8,10 @@ kernels, enqueued on the current torch stream.  PyTorch supplies device memory a
     y, h_final = ssd_fwd(x, dt, A, B, C, D, h0=None, chunk=256)
     y_t, state = ssd_step(x_t, dt_t, A, B_t, C_t, D, state)     # one decode token
     h = linscan_fwd(a, b)
+
+    y, res = rmsnorm_fwd(x, weight, residual)                    # or rmsnorm_fp8_fwd
+    u, conv_state = conv_fwd(x, w, bias)                         # conv_step for one token
+    y, h = selscan_fwd(u, dt, A, B, C, D, z, dt_bias)            # selscan_step for one token
 
 Importing the package does not load the library; the first call does (and fails loudly if
 it cannot).
@@ -19,7 +24,22 @@ from ._lib import SSM_BF16, SSM_F32, SsmError
 __all__ = ["ssd_fwd", "ssd_step", "linscan_fwd", "linscan_baseline", "tune_ssd_fwd", "set_ssd_fwd_plan",
            "get_ssd_fwd_plan", "clear_ssd_fwd_plans", "plan_id", "tune_linscan_fwd",
            "set_linscan_shape", "get_linscan_shape", "clear_linscan_shapes", "Workspace", "check_device_status", "ssd_fwd_workspace_bytes",
-           "linscan_workspace_bytes", "SsmError", "version"]
+           "linscan_workspace_bytes", "conv_fwd", "conv_step", "selscan_fwd", "selscan_step",
+           "selscan_fwd_workspace_bytes", "rmsnorm_fwd", "rmsnorm_fp8_fwd", "SsmError", "version"]
+
+
+_LAYER = ("conv_fwd", "conv_step", "selscan_fwd", "selscan_step", "selscan_fwd_workspace_bytes", "rmsnorm_fwd",
+          "rmsnorm_fp8_fwd")
+
+
+def __getattr__(name):
+    # the operators around a layer's scan import torch, which importing the package does not
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import _layer
+    for n in _LAYER:
+        globals()[n] = getattr(_layer, n)
+    return globals()[name]
 
 
 def version() -> str:

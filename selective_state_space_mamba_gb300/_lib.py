@@ -25,9 +25,27 @@ EXPORTS = ("ssm_status_string", "ssm_version", "ssm_ssd_fwd_workspace_bytes", "s
            "ssm_ssd_fwd_set_plan", "ssm_ssd_fwd_get_plan", "ssm_ssd_fwd_clear_plans", "ssm_debug_fused_schedule",
            "ssm_debug_scan_schedule",
            "ssm_debug_build", "ssm_debug_set_bounds_fault", "ssm_linscan_fwd_tune", "ssm_linscan_set_shape",
-           "ssm_linscan_get_shape", "ssm_linscan_clear_shapes")
+           "ssm_linscan_get_shape", "ssm_linscan_clear_shapes", "ssm_conv_fwd", "ssm_conv_step",
+           "ssm_selscan_fwd_workspace_bytes", "ssm_selscan_fwd", "ssm_selscan_step", "ssm_rmsnorm_fwd",
+           "ssm_rmsnorm_fp8_fwd")
 PROFILE_KERNELS = ("linscan_lookback", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",
-                   "ssd_state_fused", "ssd_step", "linscan_baseline", "ssd_state_fixup")
+                   "ssd_state_fused", "ssd_step", "linscan_baseline", "ssd_state_fixup", "conv", "conv_step",
+                   "selscan_piece", "selscan", "selscan_step", "rmsnorm")
+SSM_ACT_NONE, SSM_ACT_SILU = 0, 1
+
+
+class SsmTokens(ctypes.Structure):
+    """ssm_tokens: a [batch, seqlen, channels] tensor with strides in elements."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class SsmSelscanArgs(ctypes.Structure):
+    """ssm_selscan_args."""
+    _fields_ = [(n, SsmTokens) for n in ("u", "dt", "B", "C", "z")] + \
+        [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias", "h0", "lens", "y", "h_final")] + \
+        [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("channels", "dstate", "ngroups", "softplus", "dtype", "reserved")]
+
 
 _lib = None
 _lock = threading.Lock()
@@ -89,6 +107,21 @@ def _declare(lib):
     lib.ssm_debug_set_bounds_fault.restype = i32
     lib.ssm_linscan_fwd_noalloc.argtypes = [vp, vp, vp, i64, i64, vp]
     lib.ssm_linscan_fwd_noalloc.restype = i32
+    lib.ssm_conv_fwd.argtypes = [SsmTokens] + [vp] * 6 + [i64, i64, i32, i32, i32, i32, vp]
+    lib.ssm_conv_fwd.restype = i32
+    lib.ssm_conv_step.argtypes = [SsmTokens] + [vp] * 6 + [i64, i64, i32, i32, i32, i32, vp]
+    lib.ssm_conv_step.restype = i32
+    lib.ssm_selscan_fwd_workspace_bytes.argtypes = [i64, i64, i32, i32, i32]
+    lib.ssm_selscan_fwd_workspace_bytes.restype = sz
+    lib.ssm_selscan_fwd.argtypes = [ctypes.POINTER(SsmSelscanArgs), vp, sz, vp]
+    lib.ssm_selscan_fwd.restype = i32
+    lib.ssm_selscan_step.argtypes = [ctypes.POINTER(SsmSelscanArgs), vp, i64, vp]
+    lib.ssm_selscan_step.restype = i32
+    f32 = ctypes.c_float
+    lib.ssm_rmsnorm_fwd.argtypes = [vp, i64, vp, vp, vp, vp, i64, i32, f32, i32, i32, vp]
+    lib.ssm_rmsnorm_fwd.restype = i32
+    lib.ssm_rmsnorm_fp8_fwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, i32, vp]
+    lib.ssm_rmsnorm_fp8_fwd.restype = i32
     lib.ssm_profile_begin.argtypes = [i32]
     lib.ssm_profile_begin.restype = i32
     lib.ssm_profile_end.argtypes = [vp, vp]

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -212,6 +213,108 @@ ssm_status check_ssd_buffers(const void* x, const void* dt, const float* A, cons
   return SSM_OK;
 }
 
+// ---- the operators around a layer's scan: argument checks ----
+bool valid_dtype(int dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
+int dtype_bytes(ssm_dtype dtype) { return dtype == SSM_F32 ? 4 : 2; }
+bool selscan_dstate(int n) { return n == 8 || n == 16 || n == 32 || n == 64; }
+
+// The byte ranges that a call's tensors span.  A tensor with no elements spans nothing.
+struct Spans {
+  struct Range {
+    uintptr_t first, end;
+  };
+  Range r[12];
+  int n = 0;
+  ssm_status bad = SSM_OK;
+
+  void add(const void* p, int elem, bool overflow, int64_t elems) {
+    if (!p || bad != SSM_OK) return;
+    int64_t bytes;
+    const uintptr_t first = reinterpret_cast<uintptr_t>(p);
+    if (overflow || __builtin_mul_overflow(elems, (int64_t)elem, &bytes) || first + (uintptr_t)bytes < first)
+      bad = SSM_ERR_INVALID_ARG;
+    else if (first % elem != 0)
+      bad = SSM_ERR_ALIGNMENT;
+    else if (bytes > 0 && n < 12)
+      r[n++] = {first, first + (uintptr_t)bytes};
+  }
+  void dense(const void* p, int elem, std::initializer_list<int64_t> sizes) {
+    int64_t elems = 1;
+    bool over = false;
+    for (int64_t v : sizes) over |= __builtin_mul_overflow(elems, v, &elems);
+    add(p, elem, over, elems);
+  }
+  void tokens(const ssm_tokens& t, int64_t batch, int64_t seqlen, int64_t channels, int elem) {
+    if (!t.ptr || batch == 0 || seqlen == 0) return;
+    int64_t a, b, elems;
+    if ((batch > 1 && t.batch_stride < 0) || (seqlen > 1 && t.token_stride < 0)) {
+      bad = SSM_ERR_INVALID_ARG;
+      return;
+    }
+    bool over = __builtin_mul_overflow(batch - 1, batch > 1 ? t.batch_stride : 0, &a);
+    over |= __builtin_mul_overflow(seqlen - 1, seqlen > 1 ? t.token_stride : 0, &b);
+    over |= __builtin_add_overflow(a, b, &elems);
+    over |= __builtin_add_overflow(elems, channels, &elems);
+    add(t.ptr, elem, over, elems);
+  }
+};
+
+// Every tensor well formed, and no output over an input or another output.
+ssm_status check_spans(const Spans& in, const Spans& out) {
+  if (in.bad != SSM_OK) return in.bad;
+  if (out.bad != SSM_OK) return out.bad;
+  for (int i = 0; i < out.n; ++i) {
+    for (int k = 0; k < in.n; ++k)
+      if (out.r[i].first < in.r[k].end && in.r[k].first < out.r[i].end) return SSM_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (out.r[i].first < out.r[k].end && out.r[k].first < out.r[i].end) return SSM_ERR_INVALID_ARG;
+  }
+  return SSM_OK;
+}
+
+ssm_status check_selscan_sizes(const ssm_selscan_args& a) {
+  if (a.batch < 0 || a.channels < 1 || a.ngroups < 1 || a.channels % a.ngroups != 0 || !valid_dtype(a.dtype))
+    return SSM_ERR_INVALID_ARG;
+  if (!selscan_dstate(a.dstate) || a.batch > 65535) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+// One launch with its events; a failed launch is reported and cleared, and no exception leaves.
+template <typename F>
+ssm_status launch_status(int kernel, cudaStream_t s, F&& launch) {
+  try {
+    if (timed_launch(kernel, s, static_cast<F&&>(launch)) == cudaSuccess) return SSM_OK;
+  } catch (...) {
+  }
+  (void)cudaGetLastError();
+  return SSM_ERR_CUDA;
+}
+
+ssm_status rmsnorm(const void* x, int64_t x_stride, const float* weight, const void* residual, void* residual_out,
+                   void* y, void* q, float* scale, int64_t rows, int width, int group, float eps, ssm_dtype dtype,
+                   ssm_dtype res_dtype, cudaStream_t s) {
+  if (rows < 0 || width < 1 || !valid_dtype(dtype) || (residual && res_dtype != SSM_F32 && res_dtype != dtype))
+    return SSM_ERR_INVALID_ARG;
+  if (rows == 0) return SSM_OK;
+  if (!x || !weight || (!q && !y) || (residual_out && !residual)) return SSM_ERR_INVALID_ARG;
+  if (rows > 0x7fffffffLL) return SSM_ERR_UNSUPPORTED;
+  const int e = dtype_bytes(dtype), re = dtype_bytes(res_dtype);
+  Spans in, out;
+  in.tokens(ssm_tokens{x, x_stride, 0}, rows, 1, width, e);
+  in.dense(weight, 4, {width});
+  if (residual != residual_out) in.dense(residual, re, {rows, width});
+  out.dense(y, e, {rows, width});
+  out.dense(q, 1, {rows, width});
+  out.dense(scale, 4, {rows, group ? (width + (int64_t)group - 1) / group : 1});
+  out.dense(residual_out, re, {rows, width});
+  const ssm_status st = check_spans(in, out);
+  if (st != SSM_OK) return st;
+  return launch_status(14, s, [&] {
+    return launch_rmsnorm(x, x_stride, weight, residual, residual_out, y, q, scale, rows, width, group, eps, dtype,
+                          res_dtype, s);
+  });
+}
+
 }  // namespace
 
 cudaError_t ensure_smem_limit(const void* func, size_t bytes) {
@@ -395,7 +498,7 @@ const char* ssm_status_string(ssm_status status) {
   return "unknown ssm_status";
 }
 
-const char* ssm_version(void) { return "0.1.0"; }
+const char* ssm_version(void) { return "0.2.0"; }
 
 size_t ssm_ssd_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim, int dstate, int ngroups,
                                    int chunk, ssm_dtype dtype) {
@@ -587,6 +690,144 @@ ssm_status ssm_ssd_step(const void* x, const void* dt, const float* A, const voi
       }) != cudaSuccess)
     return SSM_ERR_CUDA;
   return SSM_OK;
+}
+
+ssm_status ssm_conv_fwd(ssm_tokens x, const float* w, const float* bias, const void* state_in, const int32_t* lens,
+                        void* y, void* state_out, int64_t batch, int64_t seqlen, int channels, int width, ssm_act act,
+                        ssm_dtype dtype, ssm_stream_t stream) {
+  if (batch < 0 || seqlen < 0 || channels < 1 || !valid_dtype(dtype) || (act != SSM_ACT_NONE && act != SSM_ACT_SILU))
+    return SSM_ERR_INVALID_ARG;
+  if (width < 2 || width > 4) return SSM_ERR_UNSUPPORTED;
+  if (batch == 0 || (seqlen == 0 && !state_out)) return SSM_OK;
+  if (!w || (seqlen > 0 && (!x.ptr || !y))) return SSM_ERR_INVALID_ARG;
+  if (batch > 65535) return SSM_ERR_UNSUPPORTED;
+  const int e = dtype_bytes(dtype);
+  Spans in, out;
+  in.tokens(x, batch, seqlen, channels, e);
+  in.dense(w, 4, {channels, width});
+  in.dense(bias, 4, {channels});
+  in.dense(state_in, e, {batch, width - 1, channels});
+  in.dense(lens, 4, {batch});
+  out.dense(seqlen > 0 ? y : nullptr, e, {batch, seqlen, channels});
+  out.dense(state_out, e, {batch, width - 1, channels});
+  const ssm_status st = check_spans(in, out);
+  if (st != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(9, s, [&] {
+    return launch_conv_fwd(x, w, bias, state_in, lens, y, state_out, batch, seqlen, channels, width,
+                           act == SSM_ACT_SILU, dtype, s);
+  });
+}
+
+ssm_status ssm_conv_step(ssm_tokens x, const float* w, const float* bias, const void* state_in, const int32_t* slots,
+                         void* y, void* state_out, int64_t batch, int64_t nslots, int channels, int width, ssm_act act,
+                         ssm_dtype dtype, ssm_stream_t stream) {
+  if (batch < 0 || nslots < 0 || channels < 1 || !valid_dtype(dtype) ||
+      (act != SSM_ACT_NONE && act != SSM_ACT_SILU) || (!slots && nslots != batch))
+    return SSM_ERR_INVALID_ARG;
+  if (width < 2 || width > 4) return SSM_ERR_UNSUPPORTED;
+  if (batch == 0) return SSM_OK;
+  if (!x.ptr || !w || !y || (nslots > 0 && !state_out)) return SSM_ERR_INVALID_ARG;
+  if (batch > 65535) return SSM_ERR_UNSUPPORTED;
+  const int e = dtype_bytes(dtype);
+  Spans in, out;
+  in.tokens(x, batch, 1, channels, e);
+  in.dense(w, 4, {channels, width});
+  in.dense(bias, 4, {channels});
+  if (state_in != state_out) in.dense(state_in, e, {nslots, width - 1, channels});
+  in.dense(slots, 4, {batch});
+  out.dense(y, e, {batch, channels});
+  out.dense(state_out, e, {nslots, width - 1, channels});
+  const ssm_status st = check_spans(in, out);
+  if (st != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(10, s, [&] {
+    return launch_conv_step(x, w, bias, state_in, slots, y, state_out, batch, nslots, channels, width,
+                            act == SSM_ACT_SILU, dtype, s);
+  });
+}
+
+size_t ssm_selscan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
+  if (batch < 0 || seqlen < 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0 || !selscan_dstate(dstate))
+    return 0;
+  return selscan_split(batch, seqlen, channels, dstate, ngroups).bytes;
+}
+
+ssm_status ssm_selscan_fwd(const ssm_selscan_args* args, void* workspace, size_t workspace_bytes,
+                           ssm_stream_t stream) {
+  if (!args) return SSM_ERR_INVALID_ARG;
+  const ssm_selscan_args& a = *args;
+  ssm_status st = check_selscan_sizes(a);
+  if (st != SSM_OK) return st;
+  if (a.seqlen < 0) return SSM_ERR_INVALID_ARG;
+  if (a.batch == 0 || (a.seqlen == 0 && !a.h_final)) return SSM_OK;
+  if (!a.A || (a.seqlen > 0 && (!a.u.ptr || !a.dt.ptr || !a.B.ptr || !a.C.ptr || !a.y))) return SSM_ERR_INVALID_ARG;
+  const ssm_dtype dtype = (ssm_dtype)a.dtype;
+  const int e = dtype_bytes(dtype);
+  Spans in, out;
+  for (const ssm_tokens* t : {&a.u, &a.dt, &a.z}) in.tokens(*t, a.batch, a.seqlen, a.channels, e);
+  for (const ssm_tokens* t : {&a.B, &a.C}) in.tokens(*t, a.batch, a.seqlen, (int64_t)a.ngroups * a.dstate, e);
+  in.dense(a.A, 4, {a.channels, a.dstate});
+  in.dense(a.D, 4, {a.channels});
+  in.dense(a.dt_bias, 4, {a.channels});
+  in.dense(a.h0, 4, {a.batch, a.channels, a.dstate});
+  in.dense(a.lens, 4, {a.batch});
+  out.dense(a.seqlen > 0 ? a.y : nullptr, e, {a.batch, a.seqlen, a.channels});
+  out.dense(a.h_final, 4, {a.batch, a.channels, a.dstate});
+  if ((st = check_spans(in, out)) != SSM_OK) return st;
+  const SelscanSplit sp = selscan_split(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups);
+  if (sp.tiles * sp.pieces > 0x7fffffffLL) return SSM_ERR_UNSUPPORTED;
+  if (sp.bytes > 0) {
+    if (!workspace || workspace_bytes < sp.bytes) return SSM_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SSM_ERR_ALIGNMENT;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (sp.pieces > 1) {
+    st = launch_status(11, s, [&] { return launch_selscan_piece(a, sp, workspace, s); });
+    if (st != SSM_OK) return st;
+  }
+  return launch_status(12, s, [&] { return launch_selscan(a, sp, workspace, s); });
+}
+
+ssm_status ssm_selscan_step(const ssm_selscan_args* args, const int32_t* slots, int64_t nslots, ssm_stream_t stream) {
+  if (!args) return SSM_ERR_INVALID_ARG;
+  const ssm_selscan_args& a = *args;
+  ssm_status st = check_selscan_sizes(a);
+  if (st != SSM_OK) return st;
+  if (nslots < 0 || (!slots && nslots != a.batch)) return SSM_ERR_INVALID_ARG;
+  if (a.batch == 0) return SSM_OK;
+  if (!a.A || !a.u.ptr || !a.dt.ptr || !a.B.ptr || !a.C.ptr || !a.y || (nslots > 0 && !a.h_final))
+    return SSM_ERR_INVALID_ARG;
+  const int e = dtype_bytes((ssm_dtype)a.dtype);
+  Spans in, out;
+  for (const ssm_tokens* t : {&a.u, &a.dt, &a.z}) in.tokens(*t, a.batch, 1, a.channels, e);
+  for (const ssm_tokens* t : {&a.B, &a.C}) in.tokens(*t, a.batch, 1, (int64_t)a.ngroups * a.dstate, e);
+  in.dense(a.A, 4, {a.channels, a.dstate});
+  in.dense(a.D, 4, {a.channels});
+  in.dense(a.dt_bias, 4, {a.channels});
+  if (a.h0 != a.h_final) in.dense(a.h0, 4, {nslots, a.channels, a.dstate});
+  in.dense(slots, 4, {a.batch});
+  out.dense(a.y, e, {a.batch, a.channels});
+  out.dense(a.h_final, 4, {nslots, a.channels, a.dstate});
+  if ((st = check_spans(in, out)) != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(13, s, [&] { return launch_selscan_step(a, slots, nslots, s); });
+}
+
+ssm_status ssm_rmsnorm_fwd(const void* x, int64_t x_stride, const float* weight, const void* residual,
+                           void* residual_out, void* y, int64_t rows, int width, float eps, ssm_dtype dtype,
+                           ssm_dtype res_dtype, ssm_stream_t stream) {
+  return rmsnorm(x, x_stride, weight, residual, residual_out, y, nullptr, nullptr, rows, width, 0, eps, dtype,
+                 res_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ssm_status ssm_rmsnorm_fp8_fwd(const void* x, int64_t x_stride, const float* weight, const void* residual,
+                               void* residual_out, void* q, float* scale, int64_t rows, int width, int group,
+                               float eps, ssm_dtype dtype, ssm_dtype res_dtype, ssm_stream_t stream) {
+  if (group != 0 && group != 128) return group < 0 ? SSM_ERR_INVALID_ARG : SSM_ERR_UNSUPPORTED;
+  if (rows > 0 && (!q || !scale)) return SSM_ERR_INVALID_ARG;
+  return rmsnorm(x, x_stride, weight, residual, residual_out, nullptr, q, scale, rows, width, group, eps, dtype,
+                 res_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t ssm_linscan_workspace_bytes(int64_t rows, int64_t len) {

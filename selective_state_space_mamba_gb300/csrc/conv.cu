@@ -1,0 +1,220 @@
+// conv, conv_step: the short causal convolution of each channel on its own,
+//     y_t[c] = act(bias[c] + sum_k w[c, k] x_{t - W + 1 + k}[c]),   W = 2 .. 4,
+// over a prompt and for one new token.  2 W + 5 operations an element against one read and one
+// write of it: memory-bound (a step of few sequences: launch-bound).
+//
+// Prompt: a thread keeps VEC channels' weights, and the window of the last W - 1 tokens, in
+// registers and walks down `run` tokens, so each x is loaded once but for the W - 1 tokens before
+// the run (which the neighbouring run has just brought to L2).  kConvUnroll tokens are loaded
+// before the first of them is used.  Items (run of tokens, channel vector) are numbered with the
+// channel vector fastest: a warp reads 32 * VEC consecutive channels of a token, whatever the
+// number of channels.
+//
+// Tokens of padding (t >= lens[b]) are neither read nor multiplied: a NaN there stays there.
+#include "layer_common.cuh"
+
+namespace ssm {
+namespace {
+
+using namespace layer;
+
+constexpr int kConvThreads = 128;
+constexpr int kConvUnroll = 8;
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads)
+    conv_kernel(const ssm_tokens x, const float* __restrict__ w, const float* __restrict__ bias, const T* state_in,
+                const int32_t* lens, T* y, T* state_out, int64_t items, int64_t seqlen, int channels, int run,
+                bool act) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t item = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+  if (item >= items) return;
+  const int nvec = channels / VEC;
+  const int64_t seg = item / nvec;
+  const int c = (int)(item - seg * nvec) * VEC;
+  const int64_t b = blockIdx.y;
+  int64_t len = seqlen;
+  if (lens) {
+    const int64_t n = lens[b];
+    len = n < 0 ? 0 : n < seqlen ? n : seqlen;
+  }
+  const T* xb = static_cast<const T*>(x.ptr) + b * x.batch_stride + c;
+  const T* sb = state_in ? state_in + b * (W - 1) * channels + c : nullptr;
+  T* yb = y + b * seqlen * channels + c;
+  // token t of the sequence with its carried tokens in front (t >= -(W - 1))
+  const auto token = [&](int64_t t) -> Raw<T, VEC> {
+    if (t >= 0) return load_raw<T, VEC>(xb + t * x.token_stride);
+    return sb ? load_raw<T, VEC>(sb + (t + W - 1) * channels) : zero_raw<T, VEC>();
+  };
+
+  if (seg == 0 && state_out) {
+    T* so = state_out + b * (W - 1) * channels + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store_raw<T, VEC>(so + (int64_t)j * channels, token(len - (W - 1) + j));
+  }
+
+  const int64_t t0 = seg * run;
+  const int64_t t1 = t0 + run < seqlen ? t0 + run : seqlen;  // end of the run
+  const int64_t tl = t1 < len ? t1 : len;                     // end of its tokens that are no padding
+  if (t0 < tl) {
+    float wt[W][VEC], bi[VEC], win[W][VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) wt[k][i] = w[(int64_t)(c + i) * W + k];
+      bi[i] = bias ? bias[c + i] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) to_floats<T, VEC>(token(t0 - (W - 1) + k), win[k]);
+    for (int64_t t = t0; t < tl; t += kConvUnroll) {
+      Raw<T, VEC> raw[kConvUnroll];
+#pragma unroll
+      for (int j = 0; j < kConvUnroll; ++j)
+        if (t + j < tl) raw[j] = load_raw<T, VEC>(xb + (t + j) * x.token_stride);
+#pragma unroll
+      for (int j = 0; j < kConvUnroll; ++j) {
+        if (t + j >= tl) break;
+        to_floats<T, VEC>(raw[j], win[W - 1]);
+        float v[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          float a = bi[i];
+#pragma unroll
+          for (int k = 0; k < W; ++k) a = fmaf(wt[k][i], win[k][i], a);
+          v[i] = act ? silu(a) : a;
+        }
+        store_raw<T, VEC>(yb + (t + j) * channels, from_floats<T, VEC>(v));
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) win[k][i] = win[k + 1][i];
+      }
+    }
+  }
+  for (int64_t t = t0 > len ? t0 : len; t < t1; ++t) store_raw<T, VEC>(yb + t * channels, zero_raw<T, VEC>());
+}
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads)
+    conv_step_kernel(const ssm_tokens x, const float* __restrict__ w, const float* __restrict__ bias,
+                     const T* state_in, const int32_t* slots, T* y, T* state_out, int64_t nslots, int channels,
+                     bool act) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = (blockIdx.x * kConvThreads + threadIdx.x) * VEC;
+  if (c >= channels) return;
+  const int64_t b = blockIdx.y;
+  const int64_t slot = slots ? slots[b] : b;
+  T* yp = y + b * channels + c;
+  if (slot < 0 || slot >= nslots) {
+    store_raw<T, VEC>(yp, zero_raw<T, VEC>());
+    return;
+  }
+  const int64_t base = slot * (W - 1) * channels + c;
+  Raw<T, VEC> raw[W];
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k)
+    raw[k] = state_in ? load_raw<T, VEC>(state_in + base + (int64_t)k * channels) : zero_raw<T, VEC>();
+  raw[W - 1] = load_raw<T, VEC>(static_cast<const T*>(x.ptr) + b * x.batch_stride + c);
+  float a[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) a[i] = bias ? bias[c + i] : 0.f;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    float v[VEC];
+    to_floats<T, VEC>(raw[k], v);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) a[i] = fmaf(w[(int64_t)(c + i) * W + k], v[i], a[i]);
+  }
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) store_raw<T, VEC>(state_out + base + (int64_t)k * channels, raw[k + 1]);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) a[i] = act ? silu(a[i]) : a[i];
+  store_raw<T, VEC>(yp, from_floats<T, VEC>(a));
+}
+
+// Channels per thread: 4, 2 or 1, so that every row of x, y and the states starts on a vector.
+int conv_vec(const ssm_tokens& x, const void* state_in, const void* y, const void* state_out, int channels, int elem) {
+  for (int vec = 4; vec > 1; vec /= 2) {
+    const int bytes = vec * elem;
+    if (channels % vec == 0 && aligned_rows(x.ptr, x.batch_stride, x.token_stride, elem, bytes) &&
+        aligned_rows(state_in, 0, 0, elem, bytes) && aligned_rows(y, 0, 0, elem, bytes) &&
+        aligned_rows(state_out, 0, 0, elem, bytes))
+      return vec;
+  }
+  return 1;
+}
+
+template <typename F>
+cudaError_t with_width(int width, F&& f) {
+  if (width == 2) return f(std::integral_constant<int, 2>{});
+  if (width == 3) return f(std::integral_constant<int, 3>{});
+  return f(std::integral_constant<int, 4>{});
+}
+template <typename F>
+cudaError_t with_vec(int vec, F&& f) {
+  if (vec == 1) return f(std::integral_constant<int, 1>{});
+  if (vec == 2) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 4>{});
+}
+
+template <typename T>
+cudaError_t conv_fwd(const ssm_tokens& x, const float* w, const float* bias, const void* state_in, const int32_t* lens,
+                     void* y, void* state_out, int64_t batch, int64_t seqlen, int channels, int width, bool silu,
+                     cudaStream_t s) {
+  const int vec = conv_vec(x, state_in, y, state_out, channels, sizeof(T));
+  const int64_t nvec = channels / vec;
+  const int run = 32;
+  const int64_t segs = seqlen > run ? (seqlen + run - 1) / run : 1;
+  const int64_t items = segs * nvec, blocks = (items + kConvThreads - 1) / kConvThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return with_width(width, [&](auto wc) {
+    return with_vec(vec, [&](auto vc) {
+      return launch_pdl(conv_kernel<T, decltype(vc)::value, decltype(wc)::value>,
+                        dim3((unsigned)blocks, (unsigned)batch), dim3(kConvThreads), 0, s, x, w, bias,
+                        static_cast<const T*>(state_in), lens, static_cast<T*>(y), static_cast<T*>(state_out), items,
+                        seqlen, channels, run, silu);
+    });
+  });
+}
+
+template <typename T>
+cudaError_t conv_step(const ssm_tokens& x, const float* w, const float* bias, const void* state_in,
+                      const int32_t* slots, void* y, void* state_out, int64_t batch, int64_t nslots, int channels,
+                      int width, bool silu, cudaStream_t s) {
+  ssm_tokens row = x;
+  row.token_stride = 0;
+  const int vec = conv_vec(row, state_in, y, state_out, channels, sizeof(T));
+  const int blocks = (channels / vec + kConvThreads - 1) / kConvThreads;
+  return with_width(width, [&](auto wc) {
+    return with_vec(vec, [&](auto vc) {
+      return launch_pdl(conv_step_kernel<T, decltype(vc)::value, decltype(wc)::value>,
+                        dim3((unsigned)blocks, (unsigned)batch), dim3(kConvThreads), 0, s, row, w, bias,
+                        static_cast<const T*>(state_in), slots, static_cast<T*>(y), static_cast<T*>(state_out),
+                        nslots, channels, silu);
+    });
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_conv_fwd(const ssm_tokens& x, const float* w, const float* bias, const void* state_in,
+                            const int32_t* lens, void* y, void* state_out, int64_t batch, int64_t seqlen, int channels,
+                            int width, bool silu, ssm_dtype dtype, cudaStream_t s) {
+  return dtype == SSM_BF16 ? conv_fwd<__nv_bfloat16>(x, w, bias, state_in, lens, y, state_out, batch, seqlen, channels,
+                                                     width, silu, s)
+                           : conv_fwd<float>(x, w, bias, state_in, lens, y, state_out, batch, seqlen, channels, width,
+                                             silu, s);
+}
+
+cudaError_t launch_conv_step(const ssm_tokens& x, const float* w, const float* bias, const void* state_in,
+                             const int32_t* slots, void* y, void* state_out, int64_t batch, int64_t nslots,
+                             int channels, int width, bool silu, ssm_dtype dtype, cudaStream_t s) {
+  return dtype == SSM_BF16 ? conv_step<__nv_bfloat16>(x, w, bias, state_in, slots, y, state_out, batch, nslots,
+                                                      channels, width, silu, s)
+                           : conv_step<float>(x, w, bias, state_in, slots, y, state_out, batch, nslots, channels,
+                                              width, silu, s);
+}
+
+}  // namespace ssm

@@ -432,4 +432,29 @@ cudaError_t launch_ssd_step(const void* x, const void* dt, const float* A, const
                             const float* D, const float* state_in, float* state_out, void* y, int64_t batch,
                             int nheads, int headdim, int dstate, int ngroups, ssm_dtype dtype, cudaStream_t s);
 
+// The operators around a layer's scan (entry points of the same names in ssm.h).  The host has
+// checked the arguments.
+cudaError_t launch_conv_fwd(const ssm_tokens& x, const float* w, const float* bias, const void* state_in,
+                            const int32_t* lens, void* y, void* state_out, int64_t batch, int64_t seqlen, int channels,
+                            int width, bool silu, ssm_dtype dtype, cudaStream_t s);
+cudaError_t launch_conv_step(const ssm_tokens& x, const float* w, const float* bias, const void* state_in,
+                             const int32_t* slots, void* y, void* state_out, int64_t batch, int64_t nslots,
+                             int channels, int width, bool silu, ssm_dtype dtype, cudaStream_t s);
+// Pieces of the time axis that a selective scan of these sizes is split into, and their workspace:
+// the end state of each piece but the last, started from zero, and its sum of delta.
+struct SelscanSplit {
+  int pieces;            // 1: not split
+  int64_t piece_tokens;  // tokens of a piece (the last may be shorter)
+  int64_t tiles;         // channel tiles of one sequence
+  size_t bytes;
+};
+SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups);
+cudaError_t launch_selscan_piece(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace, cudaStream_t s);
+cudaError_t launch_selscan(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace, cudaStream_t s);
+cudaError_t launch_selscan_step(const ssm_selscan_args& a, const int32_t* slots, int64_t nslots, cudaStream_t s);
+// q != NULL: 8-bit output with scales (group 0: one a row), else y
+cudaError_t launch_rmsnorm(const void* x, int64_t x_stride, const float* weight, const void* residual,
+                           void* residual_out, void* y, void* q, float* scale, int64_t rows, int width, int group,
+                           float eps, ssm_dtype dtype, ssm_dtype res_dtype, cudaStream_t s);
+
 }  // namespace ssm
