@@ -8,12 +8,29 @@ for example columns of a projection's wider rows.
 """
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import _lib
 from ._lib import SsmSelscanArgs, SsmTokens
 
 _CODE = {torch.float32: _lib.SSM_F32, torch.bfloat16: _lib.SSM_BF16}
+_F32, _I32 = torch.float32, torch.int32
+_SELSCAN = struct.Struct("@15q7q2q6i")  # ssm_selscan_args, filled in one go: a third of the time of its fields one by one
+
+# A call of one token takes a few microseconds on the GPU, so what stands here is kept short: the
+# stream is asked for as a number, and a tensor is checked with the fewest questions.
+_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
+_library = None
+
+
+def _lib_handle():
+    global _library
+    if _library is None:
+        _library = _lib.load()
+    return _library
 
 
 def _code(t) -> int:
@@ -23,41 +40,51 @@ def _code(t) -> int:
     return code
 
 
-def _stream(t) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
 def _fail(name, want):
     raise ValueError(f"{name} must be {want}")
 
 
-def _tokens(name, t, shape, dtype) -> SsmTokens:
-    """A strided token tensor [batch, (seqlen,) channels] or, for B and C, [..., groups, states]."""
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
-        _fail(name, f"a CUDA tensor {list(shape)} of {dtype}")
+def _device(name, t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _fail(name, "a CUDA tensor")
+    return dev
+
+
+def _tokens(name, t, shape, dtype, dev):
+    """Pointer and strides of a token tensor, strided in all but its last dimension."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _fail(name, f"a CUDA tensor {list(shape)} of {dtype}, on the first one's device")
     s = t.stride()
     if s[-1] != 1 and shape[-1] != 1:
         _fail(name, "contiguous in its last dimension")
-    return SsmTokens(t.data_ptr(), s[0], s[1])
+    return t.data_ptr(), s[0], s[1]
 
 
-def _groups(name, t, lead, dtype):
-    """B or C [*lead, groups, states], a token's groups adjacent; returns (tokens, groups, states)."""
-    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
-        _fail(name, f"[{', '.join(map(str, lead))}, groups, states]")
-    G, N = t.shape[-2:]
-    if G > 1 and t.stride(-2) != N:
+def _groups(name, t, shape, dtype, dev):
+    """The same for B or C [..., groups, states], a token's groups adjacent."""
+    if shape[-2] > 1 and t.dim() == len(shape) and t.stride(-2) != shape[-1]:
         _fail(name, "contiguous in its last two dimensions")
-    return _tokens(name, t, t.shape, dtype), G, N
+    return _tokens(name, t, shape, dtype, dev)
 
 
-def _dense(name, t, shape, dtype):
-    """Pointer of an optional dense tensor."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _fail(name, f"a contiguous CUDA tensor {list(shape)} of {dtype}")
+def _dense(name, t, shape, dtype, dev):
+    """Pointer of a dense tensor."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _fail(name, f"a contiguous CUDA tensor {list(shape)} of {dtype}, on the first one's device")
     return t.data_ptr()
+
+
+def _out(name, t, shape, dtype, like, dev):
+    """An output, the caller's or a new one, and its pointer."""
+    if t is None:
+        t = _empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _dense(name, t, shape, dtype, dev)
+
+
+def _opt(name, t, shape, dtype, dev):
+    return 0 if t is None else _dense(name, t, shape, dtype, dev)
 
 
 def conv_fwd(x, weight, bias=None, state=None, lens=None, *, silu: bool = True, y=None, state_out=None,
@@ -69,24 +96,19 @@ def conv_fwd(x, weight, bias=None, state=None, lens=None, *, silu: bool = True, 
     int32: tokens of each sequence (None: L).  Returns (y, state_out): y [b, L, d], 0 in the
     padding, and the state after the prompt (None when return_final_state is False).
     """
-    lib = _lib.load()
     code, dtype = _code(x), x.dtype
     if x.dim() != 3 or weight.dim() != 2:
         _fail("x, weight", "[b, L, d] and [d, W]")
     b, L, d = shape = x.shape
     W = weight.shape[1]
-    xt = _tokens("x", x, shape, dtype)
+    dev = _device("x", x)
+    xt = SsmTokens(*_tokens("x", x, shape, dtype, dev))
     sshape = (b, W - 1, d)
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    if not return_final_state:
-        state_out = None
-    elif state_out is None:
-        state_out = torch.empty(sshape, dtype=dtype, device=x.device)
-    st = lib.ssm_conv_fwd(xt, _dense("weight", weight, (d, W), torch.float32), _dense("bias", bias, (d,), torch.float32),
-                          _dense("state", state, sshape, dtype), _dense("lens", lens, (b,), torch.int32),
-                          _dense("y", y, shape, dtype), _dense("state_out", state_out, sshape, dtype), b, L, d, W,
-                          1 if silu else 0, code, _stream(x))
+    y, yp = _out("y", y, shape, dtype, x, dev)
+    state_out, sp = _out("state_out", state_out, sshape, dtype, x, dev) if return_final_state else (None, 0)
+    st = _lib_handle().ssm_conv_fwd(
+        xt, _dense("weight", weight, (d, W), _F32, dev), _opt("bias", bias, (d,), _F32, dev),
+        _opt("state", state, sshape, dtype, dev), _opt("lens", lens, (b,), _I32, dev), yp, sp, b, L, d, W, 1 if silu else 0, code, _stream(dev))
     if st:
         _lib.check(st, "ssm_conv_fwd")
     return y, state_out
@@ -101,21 +123,20 @@ def conv_step(x, weight, bias=None, state=None, slots=None, *, silu: bool = True
     place).  Returns (y, new state): with ``inplace`` the new state overwrites ``state``, else
     only the named rows of state_out are written.
     """
-    lib = _lib.load()
     code, dtype = _code(x), x.dtype
     if x.dim() != 2 or weight.dim() != 2:
         _fail("x, weight", "[b, d] and [d, W]")
     b, d = shape = x.shape
     W = weight.shape[1]
-    xt = _tokens("x", x, shape, dtype)
+    dev = _device("x", x)
+    xt = SsmTokens(*_tokens("x", x, shape, dtype, dev))
     state_out, n = _step_states(state, state_out, inplace, slots, b, (W - 1, d), dtype, x.device)
     sshape = (n, W - 1, d)
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    st = lib.ssm_conv_step(xt, _dense("weight", weight, (d, W), torch.float32),
-                           _dense("bias", bias, (d,), torch.float32), _dense("state", state, sshape, dtype),
-                           _dense("slots", slots, (b,), torch.int32), _dense("y", y, shape, dtype),
-                           _dense("state_out", state_out, sshape, dtype), b, n, d, W, 1 if silu else 0, code, _stream(x))
+    y, yp = _out("y", y, shape, dtype, x, dev)
+    st = _lib_handle().ssm_conv_step(
+        xt, _dense("weight", weight, (d, W), _F32, dev), _opt("bias", bias, (d,), _F32, dev),
+        _opt("state", state, sshape, dtype, dev), _opt("slots", slots, (b,), _I32, dev), yp,
+        _dense("state_out", state_out, sshape, dtype, dev), b, n, d, W, 1 if silu else 0, code, _stream(dev))
     if st:
         _lib.check(st, "ssm_conv_step")
     return y, state_out
@@ -132,36 +153,29 @@ def _step_states(state, state_out, inplace, slots, b, inner, dtype, device):
     if state is None:
         if slots is not None:
             raise ValueError("slots need a state or a state_out")
-        return torch.empty((b, *inner), dtype=dtype, device=device), b
+        return _empty((b, *inner), dtype=dtype, device=device), b
     # rows that no slot names keep what they hold
     return (torch.empty_like(state) if slots is None else state.clone()), state.shape[0]
 
 
 def selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups=1) -> int:
     """Device memory that selscan_fwd needs besides its tensors (0 where the time axis is not split)."""
-    return int(_lib.load().ssm_selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups))
+    return int(_lib_handle().ssm_selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups))
 
 
-def _selscan_args(u, dt, A, B, C, D, z, dt_bias, softplus):
-    """The arguments that selscan_fwd and selscan_step share."""
-    a = SsmSelscanArgs()
+def _selscan_inputs(u, dt, A, B, C, D, z, dt_bias, dev):
+    """What selscan_fwd and selscan_step share: the head of ssm_selscan_args, groups and states."""
     dtype, shape = u.dtype, u.shape
-    a.dtype = _code(u)
     d = shape[-1]
-    a.u = _tokens("u", u, shape, dtype)
-    a.dt = _tokens("dt", dt, shape, dtype)
-    a.B, G, N = _groups("B", B, shape[:-1], dtype)
-    a.C, GC, NC = _groups("C", C, shape[:-1], dtype)
-    if GC != G or NC != N:
-        _fail("C", "of B's shape")
-    if z is not None:
-        a.z = _tokens("z", z, shape, dtype)
-    a.A = _dense("A", A, (d, N), torch.float32)
-    a.D = _dense("D", D, (d,), torch.float32)
-    a.dt_bias = _dense("dt_bias", dt_bias, (d,), torch.float32)
-    a.channels, a.dstate, a.ngroups, a.softplus = d, N, G, 1 if softplus else 0
-    a.batch = shape[0]
-    return a
+    bshape = B.shape
+    if bshape[:-2] != shape[:-1]:
+        _fail("B", f"[{', '.join(map(str, shape[:-1]))}, groups, states]")
+    G, N = bshape[-2:]
+    head = (*_tokens("u", u, shape, dtype, dev), *_tokens("dt", dt, shape, dtype, dev),
+            *_groups("B", B, bshape, dtype, dev), *_groups("C", C, bshape, dtype, dev),
+            *((0, 0, 0) if z is None else _tokens("z", z, shape, dtype, dev)), _dense("A", A, (d, N), _F32, dev),
+            _opt("D", D, (d,), _F32, dev), _opt("dt_bias", dt_bias, (d,), _F32, dev))
+    return head, G, N
 
 
 def selscan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lens=None, *, softplus: bool = True, y=None,
@@ -174,30 +188,23 @@ def selscan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lens=None
     in the padding, and the float32 state after the last token (None when return_final_state is
     False).  Without a workspace (Workspace), one is allocated for the call where it is needed.
     """
-    if u.dim() != 3 or A.dim() != 2:
-        _fail("u, A", "[b, L, d] and [d, N]")
-    lib = _lib.load()
+    if u.dim() != 3 or B.dim() != 4:
+        _fail("u, B", "[b, L, d] and [b, L, G, N]")
+    code, dtype, dev = _code(u), u.dtype, _device("u", u)
     b, L, d = shape = u.shape
-    a = _selscan_args(u, dt, A, B, C, D, z, dt_bias, softplus)
-    N = a.dstate
-    if y is None:
-        y = torch.empty(shape, dtype=u.dtype, device=u.device)
-    if not return_final_state:
-        h_final = None
-    elif h_final is None:
-        h_final = torch.empty((b, d, N), dtype=torch.float32, device=u.device)
-    a.seqlen = L
-    a.h0 = _dense("h0", h0, (b, d, N), torch.float32)
-    a.lens = _dense("lens", lens, (b,), torch.int32)
-    a.y = _dense("y", y, shape, u.dtype)
-    a.h_final = _dense("h_final", h_final, (b, d, N), torch.float32)
-    need = lib.ssm_selscan_fwd_workspace_bytes(b, L, d, N, a.ngroups)
+    head, G, N = _selscan_inputs(u, dt, A, B, C, D, z, dt_bias, dev)
+    y, yp = _out("y", y, shape, dtype, u, dev)
+    h_final, hp = _out("h_final", h_final, (b, d, N), _F32, u, dev) if return_final_state else (None, 0)
+    args = SsmSelscanArgs.from_buffer_copy(_SELSCAN.pack(
+        *head, _opt("h0", h0, (b, d, N), _F32, dev), _opt("lens", lens, (b,), _I32, dev), yp, hp, b, L, d, N, G, 1 if softplus else 0, code, 0))
+    lib = _lib_handle()
+    need = lib.ssm_selscan_fwd_workspace_bytes(b, L, d, N, G)
     if workspace is not None:
         workspace.ensure(need)
         buf, have = workspace.buf, workspace.nbytes
     else:
-        buf, have = torch.empty(need, dtype=torch.uint8, device=u.device) if need else None, need
-    st = lib.ssm_selscan_fwd(a, None if buf is None else buf.data_ptr(), have, _stream(u))
+        buf, have = _empty(need, dtype=torch.uint8, device=u.device) if need else None, need
+    st = lib.ssm_selscan_fwd(args, None if buf is None else buf.data_ptr(), have, _stream(dev))
     if st:
         _lib.check(st, "ssm_selscan_fwd")
     return y, h_final
@@ -212,19 +219,17 @@ def selscan_step(u, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, slots
     outside 0 .. n - 1 marks an unused place).  Returns (y, new state): with ``inplace`` the new state
     overwrites ``state``, else only the named rows of state_out are written.
     """
-    if u.dim() != 2 or A.dim() != 2:
-        _fail("u, A", "[b, d] and [d, N]")
-    lib = _lib.load()
+    if u.dim() != 2 or B.dim() != 3:
+        _fail("u, B", "[b, d] and [b, G, N]")
+    code, dtype, dev = _code(u), u.dtype, _device("u", u)
     b, d = shape = u.shape
-    a = _selscan_args(u, dt, A, B, C, D, z, dt_bias, softplus)
-    N = a.dstate
-    state_out, n = _step_states(state, state_out, inplace, slots, b, (d, N), torch.float32, u.device)
-    if y is None:
-        y = torch.empty(shape, dtype=u.dtype, device=u.device)
-    a.h0 = _dense("state", state, (n, d, N), torch.float32)
-    a.h_final = _dense("state_out", state_out, (n, d, N), torch.float32)
-    a.y = _dense("y", y, shape, u.dtype)
-    st = lib.ssm_selscan_step(a, _dense("slots", slots, (b,), torch.int32), n, _stream(u))
+    head, G, N = _selscan_inputs(u, dt, A, B, C, D, z, dt_bias, dev)
+    state_out, n = _step_states(state, state_out, inplace, slots, b, (d, N), _F32, u.device)
+    y, yp = _out("y", y, shape, dtype, u, dev)
+    args = SsmSelscanArgs.from_buffer_copy(_SELSCAN.pack(
+        *head, _opt("state", state, (n, d, N), _F32, dev), 0, yp,
+        _dense("state_out", state_out, (n, d, N), _F32, dev), b, 1, d, N, G, 1 if softplus else 0, code, 0))
+    st = _lib_handle().ssm_selscan_step(args, _opt("slots", slots, (b,), _I32, dev), n, _stream(dev))
     if st:
         _lib.check(st, "ssm_selscan_step")
     return y, state_out
@@ -232,27 +237,27 @@ def selscan_step(u, dt, A, B, C, D=None, z=None, dt_bias=None, state=None, slots
 
 def _norm_args(x, weight, residual, residual_out):
     code = _code(x)
-    d = x.shape[-1] if x.dim() else 0
-    if not x.is_cuda:
-        _fail("x", "a CUDA tensor")
+    dev = _device("x", x)
+    shape = x.shape
+    d = shape[-1] if shape else 0
     rows = x.numel() // d if d else 0
     if x.is_contiguous():
         stride = d
-    elif x.dim() == 2 and (x.stride(1) == 1 or d == 1):
-        stride = x.stride(0)
+    elif x.stride(-1) != 1 and d != 1:
+        _fail("x", "contiguous in its last dimension")
     else:
-        stride = x.view(rows, d).stride(0) if x.stride(-1) == 1 or d == 1 else _fail("x", "contiguous in its last dimension")
-    w = _dense("weight", weight, (d,), torch.float32)
+        stride = (x if x.dim() == 2 else x.view(rows, d)).stride(0)
+    w = _dense("weight", weight, (d,), _F32, dev)
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-        return code, code, d, rows, stride, w, None, None, None
-    if residual.dtype != torch.float32 and residual.dtype != x.dtype:
+        return code, code, d, rows, stride, w, 0, 0, None, dev
+    rdtype = residual.dtype
+    if rdtype is not _F32 and rdtype is not x.dtype:
         _fail("residual", f"of float32 or {x.dtype}")
-    if residual_out is None:
-        residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
-    return (code, _CODE[residual.dtype], d, rows, stride, w, _dense("residual", residual, x.shape, residual.dtype),
-            _dense("residual_out", residual_out, x.shape, residual.dtype), residual_out)
+    rp = _dense("residual", residual, shape, rdtype, dev)
+    residual_out, rop = _out("residual_out", residual_out, shape, rdtype, x, dev)
+    return code, _CODE[rdtype], d, rows, stride, w, rp, rop, residual_out, dev
 
 
 def rmsnorm_fwd(x, weight, residual=None, *, eps: float = 1e-5, y=None, residual_out=None):
@@ -262,12 +267,9 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps: float = 1e-5, y=None, residual
     shape, float32 or x's dtype.  Returns (y, residual_out): y like x, residual_out = x + residual of residual's dtype
     (None without a residual; it may be given as ``residual`` itself, to update it in place).
     """
-    lib = _lib.load()
-    code, rcode, d, rows, stride, w, rp, rop, residual_out = _norm_args(x, weight, residual, residual_out)
-    if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    st = lib.ssm_rmsnorm_fwd(x.data_ptr(), stride, w, rp, rop, _dense("y", y, x.shape, x.dtype), rows, d, eps, code, rcode,
-                             _stream(x))
+    code, rcode, d, rows, stride, w, rp, rop, residual_out, dev = _norm_args(x, weight, residual, residual_out)
+    y, yp = _out("y", y, x.shape, x.dtype, x, dev)
+    st = _lib_handle().ssm_rmsnorm_fwd(x.data_ptr(), stride, w, rp, rop, yp, rows, d, eps, code, rcode, _stream(dev))
     if st:
         _lib.check(st, "ssm_rmsnorm_fwd")
     return y, residual_out
@@ -280,16 +282,12 @@ def rmsnorm_fp8_fwd(x, weight, residual=None, *, eps: float = 1e-5, group: int =
     q float8_e4m3fn of x's shape; scale float32 [...] (group 0: one a row) or [..., ceil(d / 128)]
     (group 128: one for each 128 columns); q * scale is the norm's value.
     """
-    lib = _lib.load()
-    code, rcode, d, rows, stride, w, rp, rop, residual_out = _norm_args(x, weight, residual, residual_out)
+    code, rcode, d, rows, stride, w, rp, rop, residual_out, dev = _norm_args(x, weight, residual, residual_out)
     sshape = x.shape[:-1] if group == 0 else (*x.shape[:-1], -(-d // 128))
-    if q is None:
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    if scale is None:
-        scale = torch.empty(sshape, dtype=torch.float32, device=x.device)
-    st = lib.ssm_rmsnorm_fp8_fwd(x.data_ptr(), stride, w, rp, rop, _dense("q", q, x.shape, torch.float8_e4m3fn),
-                                 _dense("scale", scale, sshape, torch.float32), rows, d, group, eps, code, rcode,
-                                 _stream(x))
+    q, qp = _out("q", q, x.shape, torch.float8_e4m3fn, x, dev)
+    scale, sp = _out("scale", scale, sshape, _F32, x, dev)
+    st = _lib_handle().ssm_rmsnorm_fp8_fwd(x.data_ptr(), stride, w, rp, rop, qp, sp, rows, d, group, eps, code, rcode,
+                                           _stream(dev))
     if st:
         _lib.check(st, "ssm_rmsnorm_fp8_fwd")
     return q, scale, residual_out
