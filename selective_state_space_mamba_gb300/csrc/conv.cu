@@ -5,8 +5,8 @@
 //
 // Prompt: a thread keeps VEC channels' weights, and the window of the last W - 1 tokens, in
 // registers and walks down `run` tokens, so each x is loaded once but for the W - 1 tokens before
-// the run (which the neighbouring run has just brought to L2).  kConvUnroll tokens are loaded
-// before the first of them is used.  Items (run of tokens, channel vector) are numbered with the
+// the run (which the neighbouring run has just brought to L2).  The next kConvUnroll
+// tokens are loaded before the last ones are used.  Items (run of tokens, channel vector) are numbered with the
 // channel vector fastest: a warp reads 32 * VEC consecutive channels of a token, whatever the
 // number of channels.
 //
@@ -19,10 +19,12 @@ namespace {
 using namespace layer;
 
 constexpr int kConvThreads = 128;
-constexpr int kConvUnroll = 8;
+constexpr int kConvUnroll = 4;
+constexpr int kConvResident = 7;  // CTAs an SM
+constexpr int kSmCount = 152;
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, kConvResident)
     conv_kernel(const ssm_tokens x, const float* __restrict__ w, const float* __restrict__ bias, const T* state_in,
                 const int32_t* lens, T* y, T* state_out, int64_t items, int64_t seqlen, int channels, int run,
                 bool act) {
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kConvThreads)
   const int64_t t1 = t0 + run < seqlen ? t0 + run : seqlen;  // end of the run
   const int64_t tl = t1 < len ? t1 : len;                     // end of its tokens that are no padding
   if (t0 < tl) {
-    float wt[W][VEC], bi[VEC], win[W][VEC];
+    float wt[W][VEC], bi[VEC], win[W - 1 + kConvUnroll][VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
 #pragma unroll
@@ -67,30 +69,49 @@ __global__ void __launch_bounds__(kConvThreads)
     }
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) to_floats<T, VEC>(token(t0 - (W - 1) + k), win[k]);
-    for (int64_t t = t0; t < tl; t += kConvUnroll) {
-      Raw<T, VEC> raw[kConvUnroll];
+    // one token: the window's W values that end with win[W - 1 + j]
+    const auto emit = [&](int j, T* yp) {
+      float v[VEC];
 #pragma unroll
-      for (int j = 0; j < kConvUnroll; ++j)
-        if (t + j < tl) raw[j] = load_raw<T, VEC>(xb + (t + j) * x.token_stride);
+      for (int i = 0; i < VEC; ++i) v[i] = bi[i];
 #pragma unroll
-      for (int j = 0; j < kConvUnroll; ++j) {
-        if (t + j >= tl) break;
-        to_floats<T, VEC>(raw[j], win[W - 1]);
-        float v[VEC];
+      for (int k = 0; k < W; ++k) fma_n(wt[k], win[j + k], v);
+      if (act) silu_n(v, v);
+      store_raw<T, VEC>(yp, from_floats<T, VEC>(v));
+    };
+    const T* xp = xb + t0 * x.token_stride;
+    T* yp = yb + t0 * channels;
+    const int n = (int)(tl - t0), whole = n / kConvUnroll * kConvUnroll;
+    Raw<T, VEC> next[kConvUnroll];
+    if (whole > 0) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          float a = bi[i];
-#pragma unroll
-          for (int k = 0; k < W; ++k) a = fmaf(wt[k][i], win[k][i], a);
-          v[i] = act ? silu(a) : a;
-        }
-        store_raw<T, VEC>(yb + (t + j) * channels, from_floats<T, VEC>(v));
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) win[k][i] = win[k + 1][i];
-      }
+      for (int j = 0; j < kConvUnroll; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
     }
+    for (int t = 0; t < whole; t += kConvUnroll) {
+#pragma unroll
+      for (int j = 0; j < kConvUnroll; ++j) to_floats<T, VEC>(next[j], win[W - 1 + j]);
+      xp += kConvUnroll * x.token_stride;
+      if (t + kConvUnroll < whole) {
+#pragma unroll
+        for (int j = 0; j < kConvUnroll; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
+      }
+#pragma unroll
+      for (int j = 0; j < kConvUnroll; ++j) emit(j, yp + (int64_t)j * channels);
+      yp += (int64_t)kConvUnroll * channels;
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) win[k][i] = win[k + kConvUnroll][i];
+    }
+#pragma unroll
+    for (int j = 0; j < kConvUnroll - 1; ++j)
+      if (whole + j < n) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
+#pragma unroll
+    for (int j = 0; j < kConvUnroll - 1; ++j)
+      if (whole + j < n) {
+        to_floats<T, VEC>(next[j], win[W - 1 + j]);
+        emit(j, yp + (int64_t)j * channels);
+      }
   }
   for (int64_t t = t0 > len ? t0 : len; t < t1; ++t) store_raw<T, VEC>(yb + t * channels, zero_raw<T, VEC>());
 }
@@ -146,6 +167,17 @@ int conv_vec(const ssm_tokens& x, const void* state_in, const void* y, const voi
   return 1;
 }
 
+// Tokens of a run: about 32, so that the window before a run and the weights add little to it, and
+// such that the runs fill a whole number of the GPU's waves of resident threads; less than a wave
+// of them is cut shorter, to use more SMs, down to one block of kConvUnroll tokens.
+int conv_run(int64_t columns, int64_t seqlen) {
+  constexpr int64_t wave = (int64_t)kSmCount * kConvResident * kConvThreads;
+  const int64_t waves = (columns * ((seqlen + 31) / 32) + wave / 2) / wave;
+  const int64_t segs = (waves < 1 ? 1 : waves) * wave / columns;
+  const int64_t run = segs < 1 ? 32 : (seqlen + segs - 1) / segs;
+  return (int)(run < kConvUnroll ? kConvUnroll : run > 64 ? 64 : run);
+}
+
 template <typename F>
 cudaError_t with_width(int width, F&& f) {
   if (width == 2) return f(std::integral_constant<int, 2>{});
@@ -165,7 +197,7 @@ cudaError_t conv_fwd(const ssm_tokens& x, const float* w, const float* bias, con
                      cudaStream_t s) {
   const int vec = conv_vec(x, state_in, y, state_out, channels, sizeof(T));
   const int64_t nvec = channels / vec;
-  const int run = 32;
+  const int run = conv_run(nvec * batch, seqlen);
   const int64_t segs = seqlen > run ? (seqlen + run - 1) / run : 1;
   const int64_t items = segs * nvec, blocks = (items + kConvThreads - 1) / kConvThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

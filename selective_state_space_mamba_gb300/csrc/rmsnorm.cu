@@ -2,11 +2,17 @@
 // as e4m3 codes with f32 scales.  Each element is read once and written once: memory-bound (a few
 // rows: launch-bound).
 //
-// One CTA per row.  A thread owns vectors of eight consecutive columns, tid + k * threads, and
-// keeps r of the first kNormHold of them in registers between the sum of squares and the output, so
-// rows of up to kNormHold * 8 * threads columns pass through once; the rest of wider rows is read
-// again (no output is written before the last read of its element: residual_out may be residual).
-// The eight columns of 16 neighbouring lanes are a scale group of 128.
+// One CTA a row.  A thread owns vectors of eight consecutive columns, tid + k * threads; the eight
+// columns of 16 neighbouring lanes are a scale group of 128.  r of a thread's first HOLD vectors stays
+// in registers between the sum of squares and the output.
+//   Many aligned rows: up to five vectors a thread, so that a CTA has few warps to join in its sums
+//       and many CTAs are resident; a row's loads are all in flight at once.  32768 x 2560, bf16
+//       residual, 8 bits: 88 us, the rate of a copy; one vector a thread 182 us, CTAs that walk
+//       the rows and load the next one ahead 120 us (their registers leave half the CTAs).
+//   Few rows, or rows that are not aligned: one vector a thread for up to 8192 columns, the
+//       shortest way through a single row.
+// What a thread does not hold of wider rows is read again.  No output is written before the last
+// read of its element, so residual_out may be residual.
 #include "layer_common.cuh"
 
 #include <cuda_fp8.h>
@@ -16,8 +22,9 @@ namespace {
 
 using namespace layer;
 
-constexpr int kNormHold = 2;
 constexpr int kNormMaxThreads = 1024;
+constexpr int kHoldMaxThreads = 256;
+constexpr int64_t kManyRows = 152 * 4;  // four CTAs an SM
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
 
@@ -32,166 +39,235 @@ struct NormParams {
   float* scale;
   int width, group;
   float eps;
-  bool vec;  // every row of every tensor starts on 16 bytes (q: 8)
 };
 
-// The larger absolute value as bits: the order of finite values, and NaN above all of them.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger value, or NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kE4m3Max), kMinScale); }
 
-template <typename T, typename R, bool kRes, bool kFp8>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  __shared__ float sum_part[32];
-  __shared__ uint32_t max_part[32];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
-  const T* xr = static_cast<const T*>(p.x) + row * p.x_stride;
-  const R* rr = kRes ? static_cast<const R*>(p.residual) + row * p.width : nullptr;
-  const int nvec = (p.width + 7) / 8;
-
-  const auto load_r = [&](int i, float (&v)[8]) {
-    const int c = 8 * i, valid = p.width - c;
-    const bool vec = p.vec && valid >= 8;
-    load8<T>(xr + c, vec, valid, v);
-    if constexpr (kRes) {
-      float r[8];
-      load8<R>(rr + c, vec, valid, r);
+// Sum and maximum over the CTA, the same in every thread; each has its own `part`.
+__device__ __forceinline__ float block_sum(float v, float* part) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += r[j];
-    }
-  };
-
-  float held[kNormHold][8];
-  float sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < kNormHold; ++k) {
-    const int i = tid + k * threads;
-    if (i < nvec) {
-      load_r(i, held[k]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(held[k][j], held[k][j], sum);
-    }
-  }
-  for (int i = tid + kNormHold * threads; i < nvec; i += threads) {
-    float v[8];
-    load_r(i, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((tid & 31) == 0) sum_part[tid >> 5] = sum;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return v;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  sum = (tid & 31) < warps ? sum_part[tid & 31] : 0.f;
+  v = lane < warps ? part[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float rstd = rsqrtf(sum / (float)p.width + p.eps);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float block_max(float v, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return v;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < warps ? part[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
 
-  const auto normed = [&](int i, const float (&r)[8], float (&v)[8]) {
-    const int c = 8 * i, valid = p.width - c;
-    float w[8];
-    load8<float>(p.weight + c, p.vec && valid >= 8, valid, w);
+// Eight elements as they lie in memory
+template <typename T> struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = r[j] * rstd * w[j];
-  };
-
-  float row_scale = 0.f;
-  if (kFp8 && p.group == 0) {  // one scale for the row: its largest absolute value first
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < kNormHold; ++k) {
-      const int i = tid + k * threads;
-      if (i < nvec) {
-        float v[8];
-        normed(i, held[k], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-      }
-    }
-    for (int i = tid + kNormHold * threads; i < nvec; i += threads) {
-      float r[8], v[8];
-      load_r(i, r);
-      normed(i, r, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((tid & 31) == 0) max_part[tid >> 5] = m;
-    __syncthreads();
-    m = __reduce_max_sync(0xffffffffu, (tid & 31) < warps ? max_part[tid & 31] : 0u);
-    const float amax = __uint_as_float(m) / kE4m3Max;
-    row_scale = amax < kMinScale ? kMinScale : amax;  // keeps a NaN
-    if (tid == 0) p.scale[row] = row_scale;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-
-  // all lanes of a warp take part (the scale of a group is a reduction over 16 lanes)
-  const auto output = [&](int i, bool have, const float (&r)[8]) {
-    const int c = 8 * i, valid = p.width - c;
-    const bool vec = have && p.vec && valid >= 8;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    if (have) {
-      normed(i, r, v);
-      if constexpr (kRes)
-        if (p.residual_out) store8<R>(static_cast<R*>(p.residual_out) + row * p.width + c, vec, valid, r);
-    }
-    if constexpr (!kFp8) {
-      if (have) store8<T>(static_cast<T*>(p.y) + row * p.width + c, vec, valid, v);
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      to_floats<T, 8>(v[0], f);
     } else {
-      float scale = row_scale;
-      if (p.group) {
-        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float amax = __uint_as_float(m) / kE4m3Max;
-        scale = amax < kMinScale ? kMinScale : amax;
-        if (have && (i & 15) == 0) p.scale[row * ((p.width + 127) / 128) + i / 16] = scale;
-      }
-      if (have) {
-        const float inv = 1.f / scale;
-        uint32_t u[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] * inv, v[4 * h + 1] * inv), __NV_SATFINITE,
-                                                       __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] * inv, v[4 * h + 3] * inv),
-                                                       __NV_SATFINITE, __NV_E4M3);
-          u[h] = lo | (hi << 16);
-        }
-        uint8_t* qp = p.q + row * p.width + c;
-        if (vec) {
-          *reinterpret_cast<uint2*>(qp) = make_uint2(u[0], u[1]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < valid) qp[j] = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
-        }
-      }
+      for (int i = 0; i < 8; ++i) f[i] = reinterpret_cast<const float*>(v)[i];
     }
-  };
-#pragma unroll
-  for (int k = 0; k < kNormHold; ++k) {
-    const int i = tid + k * threads;
-    if (i - (tid & 31) < nvec) output(i, i < nvec, held[k]);
   }
-  for (int i = tid + kNormHold * threads; i - (tid & 31) < nvec; i += threads) {
-    float r[8] = {};
-    if (i < nvec) load_r(i, r);
-    output(i, i < nvec, r);
+};
+
+// r = x + residual of vector i of a row
+template <typename T, typename R, bool kRes, bool kVec>
+__device__ __forceinline__ void load_r(const NormParams& p, int64_t row, int i, float (&v)[8]) {
+  const int c = 8 * i, valid = p.width - c;
+  load8<T>(static_cast<const T*>(p.x) + row * p.x_stride + c, kVec, valid, v);
+  if constexpr (kRes) {
+    float r[8];
+    load8<R>(static_cast<const R*>(p.residual) + row * p.width + c, kVec, valid, r);
+    add_n(v, r, v);
+  }
+}
+template <bool kVec>
+__device__ __forceinline__ void normed(const NormParams& p, int i, const float (&r)[8], float rstd, float (&v)[8]) {
+  float w[8];
+  load8<float>(p.weight + 8 * i, kVec, p.width - 8 * i, w);
+  mul_n(r, rstd, v);
+  mul_n(v, w, v);
+}
+__device__ __forceinline__ float max8(const float (&v)[8], float m) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+  return m;
+}
+// the squares of a vector, in two sums
+__device__ __forceinline__ void add_squares(const float (&v)[8], float (&sum)[2]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float e[2] = {v[j], v[j + 1]};
+    fma_n(e, e, sum);
   }
 }
 
-template <typename T, typename R, bool kRes>
-cudaError_t launch_rows(const NormParams& p, int64_t rows, cudaStream_t s) {
+// Writes vector i of a row: residual_out, and y or q.  All lanes of a warp take part (the scale of
+// a group is a reduction over 16 lanes); `have`: this one has a vector.
+template <typename T, typename R, bool kRes, bool kFp8, bool kVec>
+__device__ __forceinline__ void output(const NormParams& p, int64_t row, int i, bool have, const float (&r)[8],
+                                       float rstd, float row_scale) {
+  const int c = 8 * i, valid = p.width - c;
+  float v[8] = {};
+  if (have) {
+    normed<kVec>(p, i, r, rstd, v);
+    if constexpr (kRes)
+      if (p.residual_out) store8<R>(static_cast<R*>(p.residual_out) + row * p.width + c, kVec, valid, r);
+  }
+  if constexpr (!kFp8) {
+    if (have) store8<T>(static_cast<T*>(p.y) + row * p.width + c, kVec, valid, v);
+  } else {
+    float scale = row_scale;
+    if (p.group) {
+      float m = max8(v, 0.f);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      scale = scale_of(m);
+      if (have && (i & 15) == 0) p.scale[row * ((p.width + 127) / 128) + i / 16] = scale;
+    }
+    if (have) {
+      mul_n(v, rcp_fast(scale), v);
+      uint32_t u[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h], v[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi =
+            __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2], v[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+        u[h] = lo | (hi << 16);
+      }
+      uint8_t* qp = p.q + row * p.width + c;
+      if (kVec) {
+        *reinterpret_cast<uint2*>(qp) = make_uint2(u[0], u[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < valid) qp[j] = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+// kVec: every row of every tensor starts on 16 bytes (q: 8), and rows are whole vectors.  HOLD > 1: rows
+// are at most HOLD vectors a thread.
+template <typename T, typename R, bool kRes, bool kFp8, bool kVec, int HOLD>
+__global__ void __launch_bounds__(HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
+    rmsnorm_kernel(const __grid_constant__ NormParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float sum_part[32];
+  __shared__ float max_part[32];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int nvec = (p.width + 7) / 8;
-  const int threads = nvec >= kNormMaxThreads ? kNormMaxThreads : (nvec + 31) / 32 * 32;
-  if (p.q)
-    return launch_pdl(rmsnorm_kernel<T, R, kRes, true>, dim3((unsigned)rows), dim3((unsigned)threads), 0, s, p);
-  return launch_pdl(rmsnorm_kernel<T, R, kRes, false>, dim3((unsigned)rows), dim3((unsigned)threads), 0, s, p);
+  const int first = HOLD > 1 ? nvec : tid + threads;  // this thread's first vector that it does not hold
+  float held[HOLD][8];
+  float sum[2] = {};
+  if constexpr (HOLD > 1) {  // all loads first
+    Raw8<T> xn[HOLD];
+    Raw8<R> rn[kRes ? HOLD : 1];
+    const T* xp = static_cast<const T*>(p.x) + row * p.x_stride;
+    const R* rp = static_cast<const R*>(p.residual) + row * p.width;
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+      const int i = tid + k * threads;
+      if (i < nvec) {
+        xn[k].load(xp + 8 * i);
+        if constexpr (kRes) rn[k].load(rp + 8 * i);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+      if (tid + k * threads < nvec) {
+        xn[k].get(held[k]);
+        if constexpr (kRes) {
+          float e[8];
+          rn[k].get(e);
+          add_n(held[k], e, held[k]);
+        }
+        add_squares(held[k], sum);
+      }
+  } else {
+    if (tid < nvec) {
+      load_r<T, R, kRes, kVec>(p, row, tid, held[0]);
+      add_squares(held[0], sum);
+    }
+    for (int i = first; i < nvec; i += threads) {
+      float v[8];
+      load_r<T, R, kRes, kVec>(p, row, i, v);
+      add_squares(v, sum);
+    }
+  }
+  const float rstd = rsqrtf(block_sum(sum[0] + sum[1], sum_part) / (float)p.width + p.eps);
+
+  float row_scale = 0.f;
+  if (kFp8 && p.group == 0) {  // one scale for the row: its largest absolute value first
+    float m = 0.f;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+      if (tid + k * threads < nvec) {
+        normed<kVec>(p, tid + k * threads, held[k], rstd, v);
+        m = max8(v, m);
+      }
+    for (int i = first; i < nvec; i += threads) {
+      float r[8];
+      load_r<T, R, kRes, kVec>(p, row, i, r);
+      normed<kVec>(p, i, r, rstd, v);
+      m = max8(v, m);
+    }
+    row_scale = scale_of(block_max(m, max_part));
+    if (tid == 0) p.scale[row] = row_scale;
+  }
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int i = tid + k * threads;
+    if (i - (tid & 31) < nvec) output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, held[k], rstd, row_scale);
+  }
+  for (int i = first; i - (tid & 31) < nvec; i += threads) {
+    float r[8] = {};
+    if (i < nvec) load_r<T, R, kRes, kVec>(p, row, i, r);
+    output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, r, rstd, row_scale);
+  }
+}
+
+template <typename T, typename R, bool kRes, bool kFp8>
+cudaError_t launch_rows(const NormParams& p, int64_t rows, bool vec, cudaStream_t s) {
+  const int nvec = (p.width + 7) / 8;
+  const auto go = [&](auto kernel, int hold) {
+    const int threads = ((nvec + hold - 1) / hold + 31) / 32 * 32;
+    return launch_pdl(kernel, dim3((unsigned)rows), dim3((unsigned)(threads < kNormMaxThreads ? threads : kNormMaxThreads)),
+                      0, s, p);
+  };
+  if (vec && rows >= kManyRows && nvec > 64 && nvec <= 5 * kHoldMaxThreads)
+    return nvec <= 192 ? go(rmsnorm_kernel<T, R, kRes, kFp8, true, 3>, 3) : go(rmsnorm_kernel<T, R, kRes, kFp8, true, 5>, 5);
+  return vec ? go(rmsnorm_kernel<T, R, kRes, kFp8, true, 1>, 1) : go(rmsnorm_kernel<T, R, kRes, kFp8, false, 1>, 1);
+}
+
+template <typename T, typename R, bool kRes>
+cudaError_t launch_type(const NormParams& p, int64_t rows, bool vec, cudaStream_t s) {
+  return p.q ? launch_rows<T, R, kRes, true>(p, rows, vec, s) : launch_rows<T, R, kRes, false>(p, rows, vec, s);
 }
 
 }  // namespace
@@ -200,16 +276,15 @@ cudaError_t launch_rmsnorm(const void* x, int64_t x_stride, const float* weight,
                            void* residual_out, void* y, void* q, float* scale, int64_t rows, int width, int group,
                            float eps, ssm_dtype dtype, ssm_dtype res_dtype, cudaStream_t s) {
   const int e = dtype == SSM_F32 ? 4 : 2, re = res_dtype == SSM_F32 ? 4 : 2;
-  NormParams p{x, x_stride, weight, residual, residual_out, y, static_cast<uint8_t*>(q), scale, width, group, eps,
-               false};
-  p.vec = aligned_rows(x, x_stride, 0, e, 16) && aligned_rows(weight, 0, 0, 4, 16) &&
-          aligned_rows(residual, width, 0, re, 16) && aligned_rows(residual_out, width, 0, re, 16) &&
-          aligned_rows(y, width, 0, e, 16) && aligned_rows(q, width, 0, 1, 8);
+  const NormParams p{x, x_stride, weight, residual, residual_out, y, static_cast<uint8_t*>(q), scale, width, group, eps};
+  const bool vec = width % 8 == 0 && aligned_rows(x, x_stride, 0, e, 16) && aligned_rows(weight, 0, 0, 4, 16) &&
+                   aligned_rows(residual, width, 0, re, 16) && aligned_rows(residual_out, width, 0, re, 16) &&
+                   aligned_rows(y, width, 0, e, 16) && aligned_rows(q, width, 0, 1, 8);
   if (dtype == SSM_F32)
-    return residual ? launch_rows<float, float, true>(p, rows, s) : launch_rows<float, float, false>(p, rows, s);
-  if (!residual) return launch_rows<__nv_bfloat16, float, false>(p, rows, s);
-  return res_dtype == SSM_F32 ? launch_rows<__nv_bfloat16, float, true>(p, rows, s)
-                              : launch_rows<__nv_bfloat16, __nv_bfloat16, true>(p, rows, s);
+    return residual ? launch_type<float, float, true>(p, rows, vec, s) : launch_type<float, float, false>(p, rows, vec, s);
+  if (!residual) return launch_type<__nv_bfloat16, float, false>(p, rows, vec, s);
+  return res_dtype == SSM_F32 ? launch_type<__nv_bfloat16, float, true>(p, rows, vec, s)
+                              : launch_type<__nv_bfloat16, __nv_bfloat16, true>(p, rows, vec, s);
 }
 
 }  // namespace ssm

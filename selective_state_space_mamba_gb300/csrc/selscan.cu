@@ -53,12 +53,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ float exp2_fast(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
 struct Params {
   ssm_selscan_args a;
   float* E;    // [pieces - 1, batch, channels, dstate]
@@ -167,7 +161,9 @@ __global__ void __launch_bounds__(kThreads) selscan_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float v = d[i] + bias[i];
-        if (a.softplus) v = softplus(v);
+        float vv[1] = {v};
+        if (a.softplus) softplus_n(vv, vv);
+        v = vv[0];
         if (!live || i >= valid) v = 0.f;  // a token that leaves the state as it is
         s_d[vt][vc + i] = make_float4(v, v, v * u[i], v * u[i]);
       }

@@ -524,3 +524,73 @@ def test_python_refusals():
         with pytest.raises(kind):
             call()
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------------ sizes that take the wide variants
+
+@pytest.mark.parametrize("group", [None, 0, 128])
+@pytest.mark.parametrize("dtype,res", [("f32", "f32"), ("bf16", "none"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("d", [1032, 1536, 2560, 4104, 10240])
+def test_rmsnorm_many_rows(d, dtype, res, group):
+    """Rows enough to fill the GPU: several vectors a thread, the last of them partly past the row."""
+    import selective_state_space_mamba_gb300 as ssm
+    rows = 613
+    x, w, residual = norm_inputs("many", rows, d, dtype, res)
+    v, err, r = ol.rmsnorm(x, w, residual)
+    if group is None:
+        y, ro = ssm.rmsnorm_fwd(dev(x, dtype), dev(w), dev(residual, res))
+        close(host(y), v, err, "y", dtype)
+    else:
+        q, scale, ro = ssm.rmsnorm_fp8_fwd(dev(x, dtype), dev(w), dev(residual, res), group=group)
+        s = host(scale).reshape(rows, -1)
+        each = np.repeat(s, group or d, axis=1)[:, :d]
+        pad = np.pad(np.abs(v), ((0, 0), (0, s.shape[1] * (group or d) - d))).reshape(rows, s.shape[1], -1).max(2)
+        assert np.all(np.abs(s * 448 - pad) <= err.max(1, keepdims=True) + 2 * ol.U * pad)
+        e4m3_close(host(q), each, v, err, "q")
+    if residual is not None:
+        close(host(ro), r, ol.U * np.abs(r), "residual", res)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,W,b,lens", [(4, 4, 1, None), (6, 3, 2, [4001, 1777]), (5376, 4, 1, None), (999, 2, 1, [3990])])
+def test_conv_long(d, W, b, lens, dtype):
+    """Several blocks of tokens a run, and a part of one at its end."""
+    import selective_state_space_mamba_gb300 as ssm
+    L = 4001 if d < 5000 else 301
+    r = rng_of("conv long", d, W, b, dtype)
+    x = rounded(r.standard_normal((b, L, d)), dtype)
+    w, bias = r.uniform(-0.5, 0.5, (d, W)).astype(np.float32), r.uniform(-0.5, 0.5, d).astype(np.float32)
+    y_ref, err, s_ref = ol.conv(x, w, bias, None, lens)
+    if lens is not None:
+        for i, n in enumerate(lens):
+            x[i, n:] = np.nan
+    y, s = ssm.conv_fwd(dev(x, dtype), dev(w), dev(bias), lens=ints(lens))
+    close(host(y), y_ref, err, "y", dtype)
+    assert np.array_equal(host(s), s_ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,N,G,pad", [(2048, 16, 1, 0), (4104, 8, 2, 3), (1030, 32, 1, 8), (516, 64, 2, 0)])
+def test_selscan_step_many(d, N, G, pad, dtype):
+    """Sequences enough that a thread takes four, the last of them fewer; unused places among them."""
+    import selective_state_space_mamba_gb300 as ssm
+    b, n = 82, 90
+    r = rng_of("step many", d, N, G, dtype)
+    inp = scan_inputs(r, (b,), d, N, G, dtype)
+    state = (0.3 * r.standard_normal((n, d, N))).astype(np.float32)
+    at = r.permutation(n)[:b]
+    at[[3, 40, 81]] = [-1, n, 1 << 20]
+    used = (at >= 0) & (at < n)
+    one = {k: (v if k in ("A", "D", "dt_bias") else v[used][:, None]) for k, v in inp.items()}
+    y1, e1, h1, eh1 = ol.selscan(**one, h0=state[at[used]])
+    want, ey, want_h, eh = np.zeros((b, d)), np.zeros((b, d)), state.astype(np.float64).copy(), np.zeros((n, d, N))
+    want[used], ey[used], want_h[at[used]], eh[at[used]] = y1[:, 0], e1[:, 0], h1, eh1
+    for k in ("u", "dt", "B", "C", "z"):
+        inp[k][~used] = np.nan
+    t = {k: strided(inp[k], dtype, pad) for k in ("u", "dt", "z")}
+    st = dev(state)
+    y, h = ssm.selscan_step(t["u"], t["dt"], dev(inp["A"]), groups_strided(inp["B"], dtype, pad),
+                            groups_strided(inp["C"], dtype, pad), dev(inp["D"]), t["z"], dev(inp["dt_bias"]), st, ints(at),
+                            inplace=True)
+    close(host(h), want_h, eh, "h")
+    close(host(y), want, ey, "y", dtype)
