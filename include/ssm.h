@@ -303,9 +303,13 @@ SSM_API ssm_status ssm_conv_step(ssm_tokens x, const float *w, const float *bias
  *   h_final    [batch, channels, dstate] f32, or NULL
  * States and sums are f32; softplus(v) is max(v, 0) + log(1 + exp(-|v|)).
  * Sizes: batch, seqlen >= 0, ngroups >= 1 dividing channels, dstate in {8, 16, 32, 64}.
- * Workspace: f32 end states of pieces of the time axis, where there are too few channels to fill
- * the GPU (0 bytes where there are not); it need not be cleared and carries nothing from call to
- * call.  Two kernels where the axis is split, one otherwise.
+ * Workspace (0 bytes where none is needed): f32 states between parts of the time axis.  It is
+ * split into parts that run at once where there are too few channels to fill the GPU (one more
+ * kernel, which runs the parts but the last from a zero state), and cut into items that the CTAs
+ * claim in order where there are somewhat more than fill it; an item then waits (bounded) for
+ * the state of the one before.  Each call clears what it needs cleared, so the workspace need not be
+ * zero-filled and carries nothing from call to call; ssm_check_device_status reports the last
+ * call's waits.  An item whose wait ran out leaves NaN in its outputs.
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_WORKSPACE,
  *   SSM_ERR_CUDA.
  */

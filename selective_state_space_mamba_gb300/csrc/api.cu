@@ -776,13 +776,13 @@ ssm_status ssm_selscan_fwd(const ssm_selscan_args* args, void* workspace, size_t
   out.dense(a.h_final, 4, {a.batch, a.channels, a.dstate});
   if ((st = check_spans(in, out)) != SSM_OK) return st;
   const SelscanSplit sp = selscan_split(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups);
-  if (sp.tiles * sp.pieces > 0x7fffffffLL) return SSM_ERR_UNSUPPORTED;
+  if (a.batch * sp.tiles * sp.split * sp.subs > 0x7ff00000LL || sp.part_tokens > 0x7fffff00LL) return SSM_ERR_UNSUPPORTED;
   if (sp.bytes > 0) {
     if (!workspace || workspace_bytes < sp.bytes) return SSM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SSM_ERR_ALIGNMENT;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (sp.pieces > 1) {
+  if (sp.split > 1) {
     st = launch_status(11, s, [&] { return launch_selscan_piece(a, sp, workspace, s); });
     if (st != SSM_OK) return st;
   }

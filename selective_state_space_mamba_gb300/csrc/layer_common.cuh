@@ -192,11 +192,9 @@ __device__ __forceinline__ void softplus_n(const float (&v)[N], float (&r)[N]) {
   constexpr float q[8] = {-0.499994934f, 0.333190978f, -0.24842982f,  0.191060066f,
                           -0.136632457f, 0.0782259554f, -0.0295052398f, 0.00523269409f};
   float e[N], p[N], c[N];
+  mul_n(v, kLog2e, e);
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = fabsf(v[i]);
-  mul_n(e, -kLog2e, e);
-#pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = exp2_fast(e[i]), p[i] = q[7];
+  for (int i = 0; i < N; ++i) e[i] = exp2_fast(-fabsf(e[i])), p[i] = q[7];
 #pragma unroll
   for (int k = 6; k >= 0; --k) {
 #pragma unroll

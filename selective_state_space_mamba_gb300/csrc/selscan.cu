@@ -2,252 +2,554 @@
 //     h_t[c, n] = exp(delta_t[c] A[c, n]) h_{t-1}[c, n] + delta_t[c] u_t[c] B_t[n]
 //     y_t[c]    = (sum_n h_t[c, n] C_t[n] + D[c] u_t[c]) silu(z_t[c]).
 // Each (token, channel, state entry) takes one exponential and four multiply-adds, against 8 bytes
-// of bf16 a (token, channel): with 16 state entries the exponentials and the FMA pipe bound it, not
-// HBM.  There is no matrix product in it: the decays differ in every term of the sums.
+// of bf16 a (token, channel): with 16 state entries arithmetic bounds it, not HBM.  There is no matrix
+// product in it: the decays differ in every term of the sums.
 //
-// A chain (channel, n) is sequential in t, so the parallelism comes from the chains: a lane holds
-// SPL state entries of one channel and the N / SPL lanes of a channel sit side by side.  Time goes
-// in tiles of kTokens tokens: the CTA's threads load a tile, eight channels of one token each,
-// compute delta and delta u once per (token, channel) and lay them out in shared memory (each
-// doubled, the operands of packed two-way f32 instructions), walk the tile, and write y of the same
-// eight channels.  The sums over n are reduced over the lanes of a channel once per N / SPL tokens
-// with a halving butterfly, so that each lane ends up with one token's y.
-//
-// With too few chains the time axis is split into pieces (selscan_split): a first kernel runs every
-// piece but the last from a zero state and stores its end state E and the sum T of its delta; then
-// every piece starts from h = exp(A T) h + E over the pieces before it.  This costs the first
-// kernel's 3/4 of the work once more, and no CTA waits for another.
+// A chain (channel, n) is sequential in t, so the parallelism comes from the chains.  Time goes in
+// tiles of kTokens, and a CTA's warps have four roles that run beside each other:
+//   copy     brings raw tiles to shared memory by tensor copies, up to kRing ahead
+//   prepare  takes eight channels of one token a thread, computes delta and delta u and lays them out by
+//            channel pair; B and C become f32
+//   scan     walks the tiles.  A lane holds four state entries of two channels (lane_of).  What shared
+//            memory hands to registers limits it, so B and C serve two channels, and lanes are laid
+//            out for the hardware's merging of loads; the sums over n end in up to four partial
+//            sums in shared memory
+//   finish   joins a tile's partial sums, adds the skip, gates and writes y
+// They meet at mbarriers, so the scan does not stop for the rest.  Each of the other roles takes
+// fewer cycles a tile than the scan, but not two of them together.
 #include "layer_common.cuh"
+#include "tc_common.cuh"
 
 namespace ssm {
 namespace {
 
 using namespace layer;
 
-constexpr int kThreads = 128;
 constexpr int kSmCount = 152;
-constexpr int kMaxPieces = 32;
+constexpr int kMaxSplit = 64;
+constexpr int kTokens = 16;      // tokens of a tile
+constexpr int kSpl = 4;          // state entries of a lane's channel
+constexpr int kBlock = 4;        // tokens between two reductions
+constexpr int kResident = 2;     // CTAs an SM
+constexpr int kSubTokens = 1024; // tokens of an item of the queue
+constexpr int kScanThreads = 128, kRoleThreads = 64, kThreads = kScanThreads + 3 * kRoleThreads;
+constexpr int kRing = 4;         // raw tiles in shared memory
 
-__host__ __device__ constexpr int states_per_lane(int n) { return n <= 16 ? 4 : n / 4; }
-__host__ __device__ constexpr int tile_channels(int n) { return kThreads * states_per_lane(n) / n; }
-__host__ __device__ constexpr int tile_tokens(int n) { return 8 * kThreads / tile_channels(n); }
+__host__ __device__ constexpr int tile_channels(int n) { return kScanThreads * kSpl * 2 / n; }
 
-// ---- two f32 in one 64-bit register pair ----
-__device__ __forceinline__ uint64_t pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 struct Params {
   ssm_selscan_args a;
-  float* E;    // [pieces - 1, batch, channels, dstate]
-  float* T;    // [pieces - 1, batch, channels]
-  int64_t piece_tokens;
-  int pieces, tiles_per_group;
-  bool vec;    // channel rows of u, dt, z and y in vectors of eight
+  SelscanSplit sp;
+  WsHeader* queue;   // claim counter and status; NULL: one item a CTA
+  uint32_t* done;    // [chains] items of the chain that are finished
+  float* hand;       // [chains, scan threads, 8] state between a chain's items
+  LookbackCtl ctl;   // wait limit and fault injection
+  float* E;          // [split - 1, batch, channels, dstate]
+  float* T;          // [split - 1, batch, channels]
+  bool vec;          // rows of u, dt, z, y, B and C in whole vectors of 16 bytes: tensor copies
+};
+struct Maps {
+  CUtensorMap u, dt, z, B, C;
 };
 
-// One piece of one channel tile.  kPiece: the first kernel (end state and sum of delta from a zero
+// Shared memory of a CTA.
+template <typename T, int N, bool kPiece>
+struct Shared {
+  static constexpr int CT = tile_channels(N);
+  static constexpr int LPC = N / kSpl;
+  static constexpr int PARTS = LPC < 4 ? LPC : 4;  // partial sums of a channel
+  static constexpr int YP = kTokens * CT + 16;     // floats from one to the next: 16 more, against bank conflicts
+  // targets of tensor copies: 128-byte aligned
+  T u[kRing][kTokens][CT];
+  T dt[kRing][kTokens][CT];
+  T z[kPiece ? 1 : kRing][kPiece ? 8 / sizeof(T) : kTokens][CT];
+  T b[kRing][kTokens][N];
+  T c[kPiece ? 1 : kRing][kTokens][N];
+  float fb[2][kTokens][N];
+  float fc[kPiece ? 1 : 2][kTokens][N];
+  float4 d[2][kTokens][CT / 2];  // (delta, delta u) of channel pair i at i ^ (i / 8 % 4), against bank conflicts
+  float y[kPiece ? 1 : 2][kPiece ? 16 : PARTS * YP];
+  float bias[CT], skip[CT];
+  // phases of the tiles: raw tile there, raw tile read, prepared, scanned, y read
+  uint64_t raw_full[kRing], raw_free[kRing], full[2], done[2], y_free[2];
+  int64_t item;
+};
+
+// A lane's place among the LPC lanes of a channel pair and the LW pairs of a warp.  A 16-byte load takes
+// half the time where lanes that differ in bit 0 (or in bit 1) read the same address: bit 0 tells the
+// lanes of a pair apart, which read the same delta, and bit 1 tells pairs apart, which read the same
+// B and C.
+template <int LPC>
+__device__ __forceinline__ void lane_of(int lane, int& sub, int& pair) {
+  constexpr int LW = 32 / LPC;
+  sub = (lane & 1) | lane / (2 * LW) << 1;
+  pair = lane >> 1 & (LW - 1);
+}
+
+template <int M>
+__device__ __forceinline__ void load_states(const float* p, float (&v)[M]) {
+#pragma unroll
+  for (int i = 0; i < M; i += 4) {
+    const float4 r = *reinterpret_cast<const float4*>(p + i);
+    v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+  }
+}
+
+// Waits until the chain has `want` finished items; false after the limit, or once another wait gave up.
+// One thread.
+__device__ __forceinline__ bool wait_done(const uint32_t* done, uint32_t want, WsHeader* hdr, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t spins = 0;; ++spins) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+    if (v >= want) return true;
+    if (spins == 0) t0 = global_timer_ns();
+    if ((spins & 15u) == 15u) {
+      if (ld_relaxed_u64(&hdr->status) != 0ull) return false;
+      if (global_timer_ns() - t0 > limit_ns) {
+        record_error(hdr, 1u, SSM_ERR_TIMEOUT);
+        return false;
+      }
+    }
+    __nanosleep(spins < 16 ? 64 : 256);
+  }
+}
+
+// What an item is: a part of one channel tile's tokens.
+struct Item {
+  int64_t chain, b, t_begin;
+  int sub, part, g, c0, cn;  // item of the chain, part of the split axis, group, first channel, channels
+  int n, live;               // tokens in all, and before the padding
+};
+template <int CT, bool kPiece>
+__device__ __forceinline__ Item item_of(const Params& p, int64_t item, int split, int64_t chains) {
+  const ssm_selscan_args& a = p.a;
+  Item it;
+  it.sub = (int)(item / chains);
+  it.chain = item - it.sub * chains;
+  it.part = (int)(it.chain % split);
+  const int64_t bt = it.chain / split;
+  it.b = bt / p.sp.tiles;
+  const int tile = (int)(bt - it.b * p.sp.tiles);
+  const int tiles_per_group = (int)(p.sp.tiles / a.ngroups), group_channels = a.channels / a.ngroups;
+  it.g = tile / tiles_per_group;
+  const int in_group = (tile - it.g * tiles_per_group) * CT;
+  it.c0 = it.g * group_channels + in_group;
+  it.cn = group_channels - in_group < CT ? group_channels - in_group : CT;
+  int64_t len = a.seqlen;
+  if (a.lens) {
+    const int64_t v = a.lens[it.b];
+    len = v < 0 ? 0 : v < a.seqlen ? v : a.seqlen;
+  }
+  it.t_begin = it.part * p.sp.part_tokens + (kPiece ? 0 : (int64_t)it.sub * p.sp.sub_tokens);
+  int64_t t_end = (it.part + 1) * p.sp.part_tokens;
+  if (!kPiece && it.t_begin + p.sp.sub_tokens < t_end) t_end = it.t_begin + p.sp.sub_tokens;
+  if (t_end > a.seqlen) t_end = a.seqlen;
+  it.n = it.t_begin < t_end ? (int)(t_end - it.t_begin) : 0;
+  it.live = it.t_begin + it.n <= len ? it.n : it.t_begin < len ? (int)(len - it.t_begin) : 0;
+  return it;
+}
+
+// Waits for the phase of `tile` of a barrier with a phase every `every` tiles; false after the limit.
+// The hardware parks the warp for up to kParkNs a try: polling warps took a quarter of the
+// instructions of this kernel, away from the scan beside them.
+__device__ __forceinline__ bool wait_tile(uint64_t* bars, uint32_t tile, uint32_t every, uint64_t limit_ns) {
+  constexpr uint32_t kParkNs = 20000;
+  const uint32_t bar = smem_addr(&bars[tile % every]), parity = (tile / every) & 1;
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kParkNs)
+        : "memory");
+    if (ok) return true;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) return false;
+  }
+}
+
+// The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
+template <typename T, int N, bool kPiece>
+__device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, const Item& it, Shared<T, N, kPiece>& s,
+                                          uint32_t tile) {
+  constexpr int CT = Shared<T, N, kPiece>::CT;
+  const ssm_selscan_args& a = p.a;
+  const int tid = threadIdx.x % kRoleThreads;
+  if (p.vec) {
+    // One thread, five tensor copies a tile.  They bring padding too, and zeros past the tensors' ends.
+    if (tid != 0) return true;
+    int t = (int)it.t_begin;
+    const uint32_t bytes = kTokens * sizeof(T) * (CT * (kPiece || !a.z.ptr ? 2 : 3) + N * (kPiece ? 1 : 2));
+    for (int rows = it.live; rows > 0; rows -= kTokens, t += kTokens, ++tile) {
+      const int ring = tile % kRing;
+      uint64_t* bar = &s.raw_full[ring];
+      if (tile >= kRing && !wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns)) return false;
+      mbar_arrive_expect_tx(bar, bytes);
+      tc::tma_load_3d(&s.dt[ring][0][0], &maps.dt, it.c0, t, (int)it.b, bar);
+      tc::tma_load_3d(&s.u[ring][0][0], &maps.u, it.c0, t, (int)it.b, bar);
+      tc::tma_load_3d(&s.b[ring][0][0], &maps.B, it.g * N, t, (int)it.b, bar);
+      if constexpr (!kPiece) {
+        tc::tma_load_3d(&s.c[ring][0][0], &maps.C, it.g * N, t, (int)it.b, bar);
+        if (a.z.ptr) tc::tma_load_3d(&s.z[ring][0][0], &maps.z, it.c0, t, (int)it.b, bar);
+      }
+    }
+    return true;
+  }
+  const auto at = [&](const ssm_tokens& t, int64_t column) {
+    return static_cast<const T*>(t.ptr) + it.b * t.batch_stride + it.t_begin * t.token_stride + column;
+  };
+  const T *u = at(a.u, it.c0), *dt = at(a.dt, it.c0), *z = a.z.ptr ? at(a.z, it.c0) : nullptr;
+  const T *B = at(a.B, (int64_t)it.g * N), *C = at(a.C, (int64_t)it.g * N);
+  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
+    const int ring = tile % kRing, have = rows < kTokens ? rows : kTokens;
+    if (tile >= kRing && !wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns)) return false;
+#pragma unroll 8
+    for (int i = tid; i < have * CT; i += kRoleThreads) {
+      const int r = i / CT, c = i % CT;
+      if (c < it.cn) {
+        s.u[ring][r][c] = u[r * a.u.token_stride + c];
+        s.dt[ring][r][c] = dt[r * a.dt.token_stride + c];
+        if constexpr (!kPiece)
+          if (z) s.z[ring][r][c] = z[r * a.z.token_stride + c];
+      }
+    }
+#pragma unroll 4
+    for (int i = tid; i < have * N; i += kRoleThreads) {
+      const int r = i / N, c = i % N;
+      s.b[ring][r][c] = B[r * a.B.token_stride + c];
+      if constexpr (!kPiece) s.c[ring][r][c] = C[r * a.C.token_stride + c];
+    }
+    u += kTokens * a.u.token_stride;
+    dt += kTokens * a.dt.token_stride;
+    if (z) z += kTokens * a.z.token_stride;
+    B += kTokens * a.B.token_stride;
+    C += kTokens * a.C.token_stride;
+    mbar_arrive(&s.raw_full[ring]);
+  }
+  return true;
+}
+
+template <typename T, int N, bool kPiece>
+__device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Shared<T, N, kPiece>& s, uint32_t tile) {
+  constexpr int CT = Shared<T, N, kPiece>::CT;
+  const int tid = threadIdx.x % kRoleThreads;
+  // this thread's eight channels from vc on, of the tokens vt, vt + VT, ...
+  constexpr int VC = CT / 8, VT = kRoleThreads / VC < kTokens ? kRoleThreads / VC : kTokens;
+  const int vt = tid / VC, vc = 8 * (tid % VC);
+  const bool works = kRoleThreads / VC <= kTokens || vt < kTokens;
+  float bias[8];
+  load_states(&s.bias[vc], bias);
+  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
+    const int ring = tile % kRing, buf = tile & 1;
+    if (!wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns)) return false;
+    if (tile >= 2 && !wait_tile(s.done, tile - 2, 2, p.ctl.spin_limit_ns)) return false;
+    if (works) {
+#pragma unroll
+      for (int t = vt; t < kTokens; t += VT) {
+        float d[8], u[8];
+        load8<T>(&s.dt[ring][t][vc], true, 8, d);
+        load8<T>(&s.u[ring][t][vc], true, 8, u);
+        add_n(d, bias, d);
+        if (p.a.softplus) softplus_n(d, d);
+        if (rows < kTokens && t >= rows) {  // padding leaves the state as it is
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = u[j] = 0.f;
+        }
+        mul_n(u, d, u);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          s.d[buf][t][(vc / 2 + q) ^ (vc >> 4 & 3)] = make_float4(d[2 * q], u[2 * q], d[2 * q + 1], u[2 * q + 1]);
+      }
+    }
+    constexpr int VB = kTokens * N / 8;  // vectors of eight of B, and as many of C
+#pragma unroll
+    for (int k = tid; k < (kPiece ? VB : 2 * VB); k += kRoleThreads) {
+      float f[8];
+      const bool is_c = !kPiece && k >= VB;
+      const int e = 8 * (is_c ? k - VB : k);
+      load8<T>((is_c ? &s.c[kPiece ? 0 : ring][0][0] : &s.b[ring][0][0]) + e, true, 8, f);
+      if (rows < kTokens && e / N >= rows) {  // not copied: may hold anything
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      }
+      store8<float>((is_c ? &s.fc[kPiece ? 0 : buf][0][0] : &s.fb[buf][0][0]) + e, true, 8, f);
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      mbar_arrive(&s.full[buf]);
+      if (kPiece) mbar_arrive(&s.raw_free[ring]);
+    }
+  }
+  return true;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false>& s, uint32_t tile) {
+  using S = Shared<T, N, false>;
+  constexpr int CT = S::CT;
+  const ssm_selscan_args& a = p.a;
+  const int tid = threadIdx.x % kRoleThreads;
+  constexpr int VC = CT / 8, VT = kRoleThreads / VC < kTokens ? kRoleThreads / VC : kTokens;
+  const int vt = tid / VC, vc = 8 * (tid % VC), valid = it.cn - vc;
+  const bool works = (kRoleThreads / VC <= kTokens || vt < kTokens) && valid > 0, vec_y = p.vec && valid >= 8;
+  T* yp = static_cast<T*>(a.y) + (it.b * a.seqlen + it.t_begin) * a.channels + it.c0 + vc;
+  T* y_item = yp + (int64_t)vt * a.channels;
+  float skip[8];
+  load_states(&s.skip[vc], skip);
+  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
+    const int ring = tile % kRing, buf = tile & 1;
+    if (!wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns) || !wait_tile(s.done, tile, 2, p.ctl.spin_limit_ns))
+      return false;
+    if (works) {
+#pragma unroll
+      for (int t = vt; t < kTokens; t += VT) {
+        if (t < rows) {
+          float y[8], w[8], u[8];
+          load_states(&s.y[buf][t * CT + vc], y);
+#pragma unroll
+          for (int k = 1; k < S::PARTS; ++k) {
+            load_states(&s.y[buf][k * S::YP + t * CT + vc], w);
+            add_n(y, w, y);
+          }
+          load8<T>(&s.u[ring][t][vc], true, 8, u);
+          fma_n(skip, u, y);
+          if (a.z.ptr) {
+            float z[8];
+            load8<T>(&s.z[ring][t][vc], true, 8, z);
+            silu_n(z, z);
+            mul_n(y, z, y);
+          }
+          store8<T>(y_item + (int64_t)(t - vt) * a.channels, vec_y, valid, y);
+        }
+      }
+      y_item += (int64_t)kTokens * a.channels;
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      mbar_arrive(&s.y_free[buf]);
+      mbar_arrive(&s.raw_free[ring]);
+    }
+  }
+  if (works) {  // padding
+    const float zero[8] = {};
+    for (int t = it.live + vt; t < it.n; t += VT) store8<T>(yp + (int64_t)t * a.channels, vec_y, valid, zero);
+  }
+  return true;
+}
+
+// The scan's part of an item: h of this thread's two channels through the tiles.
+template <typename T, int N, bool kPiece>
+__device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Shared<T, N, kPiece>& s, uint32_t tile,
+                                          const float (&A)[2][kSpl], float (&h)[2][kSpl], float (&delta_sum)[2]) {
+  using S = Shared<T, N, kPiece>;
+  constexpr int CT = S::CT, LPC = S::LPC, LW = 32 / LPC;
+  constexpr int ROUNDS = LPC <= 4 ? 0 : LPC == 8 ? 1 : 2;  // halving rounds that leave four lanes a channel pair
+  const int lane = threadIdx.x & 31;
+  int sub, pair;
+  lane_of<LPC>(lane, sub, pair);
+  pair += (threadIdx.x >> 5) * LW;
+  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
+    const int buf = tile & 1;
+    if (!wait_tile(s.full, tile, 2, p.ctl.spin_limit_ns)) return false;
+    if (!kPiece && tile >= 2 && !wait_tile(s.y_free, tile - 2, 2, p.ctl.spin_limit_ns)) return false;
+    const float* b_row = &s.fb[buf][0][sub * kSpl];
+    const float* c_row = &s.fc[kPiece ? 0 : buf][0][sub * kSpl];
+    const float4* d_row = &s.d[buf][0][pair ^ (pair >> 3 & 3)];
+    // token of value j after the rounds: bits of `sub` from the third on, then j
+    const int mine = ROUNDS == 0 ? 0 : ROUNDS == 1 ? sub >> 2 : (sub >> 2 & 1) + 2 * (sub >> 3);
+    float* y_row = kPiece ? nullptr : &s.y[kPiece ? 0 : buf][(sub & (S::PARTS - 1)) * S::YP + mine * CT + 2 * pair];
+#pragma unroll 2
+    for (int t = 0; t < kTokens; t += kBlock) {
+      float2 part[kBlock];
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) {
+        const float4 d = d_row[(t + j) * (CT / 2)];
+        const float delta[2] = {d.x, d.z}, du[2] = {d.y, d.w};
+        float B[kSpl], C[kSpl], y[2];
+        load_states(b_row + (t + j) * N, B);
+        if (!kPiece) load_states(c_row + (t + j) * N, C);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float2 acc;
+#pragma unroll
+          for (int i = 0; i < kSpl; i += 2) {
+            float2 e = __fmul2_rn(make_float2(delta[c], delta[c]), make_float2(A[c][i], A[c][i + 1]));
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            const float2 x = __fmul2_rn(make_float2(du[c], du[c]), make_float2(B[i], B[i + 1]));
+            const float2 v = __ffma2_rn(e, make_float2(h[c][i], h[c][i + 1]), x);
+            h[c][i] = v.x, h[c][i + 1] = v.y;
+            if (!kPiece)
+              acc = i == 0 ? __fmul2_rn(v, make_float2(C[i], C[i + 1])) : __ffma2_rn(v, make_float2(C[i], C[i + 1]), acc);
+          }
+          if (kPiece)
+            delta_sum[c] += delta[c];
+          else
+            y[c] = acc.x + acc.y;
+        }
+        if (!kPiece) part[j] = make_float2(y[0], y[1]);
+      }
+      if constexpr (!kPiece) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {  // each leaves the two halves of a channel's lanes half of the tokens
+          const int bit = 4 << r;
+          const bool upper = (sub & bit) != 0;
+#pragma unroll
+          for (int j = 0; j < kBlock >> (r + 1); ++j) {
+            const float2 send = upper ? part[2 * j] : part[2 * j + 1], keep = upper ? part[2 * j + 1] : part[2 * j];
+            part[j] = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, send.x, bit * LW),
+                                  keep.y + __shfl_xor_sync(0xffffffffu, send.y, bit * LW));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBlock >> ROUNDS; ++j) *reinterpret_cast<float2*>(y_row + (t + (j << ROUNDS)) * CT) = part[j];
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.done[buf]);
+  }
+  return true;
+}
+
+// kPiece: the first kernel (end state and sum of delta of each part of a split time axis, from a zero
 // state), else the second (outputs).
 template <typename T, int N, bool kPiece>
-__global__ void __launch_bounds__(kThreads) selscan_kernel(const __grid_constant__ Params p) {
-  constexpr int SPL = states_per_lane(N), P2 = SPL / 2;
-  constexpr int LPC = N / SPL;            // lanes of a channel
-  constexpr int CW = 32 / LPC;            // channels of a warp
-  constexpr int CT = tile_channels(N);    // channels of the CTA
-  constexpr int kTokens = tile_tokens(N);
-  constexpr int YS = CT + CW;             // row of y in shared memory: its padding avoids bank conflicts
-  __shared__ __align__(16) float4 s_d[kTokens][CT];  // (delta, delta, delta u, delta u)
-  __shared__ __align__(16) float s_b[kTokens][N];
-  __shared__ __align__(16) float s_c[kPiece ? 1 : kTokens][N];
-  __shared__ __align__(16) float s_y[kPiece ? 1 : kTokens][YS];
-
+__global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  using S = Shared<T, N, kPiece>;
+  constexpr int CT = S::CT, LW = 32 / S::LPC;
+  extern __shared__ __align__(128) unsigned char smem[];
+  S& s = *reinterpret_cast<S*>(smem);
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&s.raw_full[i], p.vec ? 1 : kRoleThreads);
+      mbar_init(&s.raw_free[i], kRoleThreads / 32);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.full[i], kRoleThreads / 32);
+      mbar_init(&s.done[i], kScanThreads / 32);
+      mbar_init(&s.y_free[i], kRoleThreads / 32);
+    }
+    fence_mbar_init();
+  }
   griddep_launch_dependents();
   griddep_wait();
   const ssm_selscan_args& a = p.a;
-  const int run_pieces = kPiece ? p.pieces - 1 : p.pieces;  // nothing starts from the last piece's end
-  const int piece = blockIdx.x % run_pieces;
-  const int tile = blockIdx.x / run_pieces;
-  const int64_t b = blockIdx.y;
-  const int g = tile / p.tiles_per_group;
-  const int group_channels = a.channels / a.ngroups;
-  const int in_group = (tile - g * p.tiles_per_group) * CT;
-  const int c0 = g * group_channels + in_group;                           // first channel
-  const int cn = group_channels - in_group < CT ? group_channels - in_group : CT;  // channels of this tile
-  int64_t len = a.seqlen;
-  if (a.lens) {
-    const int64_t n = a.lens[b];
-    len = n < 0 ? 0 : n < a.seqlen ? n : a.seqlen;
-  }
-  const int64_t t_begin = piece * p.piece_tokens;
-  const int64_t t_end = t_begin + p.piece_tokens < a.seqlen ? t_begin + p.piece_tokens : a.seqlen;
-  const int64_t t_live = t_end < len ? t_end : len;  // tokens from here on are padding
+  const bool scans = tid < kScanThreads;
+  int sub, cl;  // of a scan thread: its place in a channel's entries, its first channel
+  lane_of<S::LPC>(tid & 31, sub, cl);
+  cl = 2 * (cl + (tid >> 5) * LW);
+  const int split = kPiece ? p.sp.split - 1 : p.sp.split;  // nothing starts from the last part's end
+  const int64_t chains = a.batch * p.sp.tiles * split;
+  const int64_t items = chains * (kPiece ? 1 : p.sp.subs);
+  uint32_t tile0 = 0;
 
-  // this thread's chains
-  const int lane = threadIdx.x & 31, sub = lane % LPC;
-  const int cl = (threadIdx.x >> 5) * CW + lane / LPC;  // channel within the tile
-  const bool have = cl < cn;
-  const int64_t chan = c0 + (have ? cl : 0);
-  uint64_t a2[P2], h[P2];
-#pragma unroll
-  for (int k = 0; k < P2; ++k) {
-    const float* ap = a.A + chan * N + sub * SPL + 2 * k;
-    a2[k] = pack(ap[0] * kLog2e, ap[1] * kLog2e);
-    h[k] = 0;
-  }
-  if (!kPiece) {
-    if (a.h0) {
-      const float* hp = a.h0 + (b * a.channels + chan) * N + sub * SPL;
-#pragma unroll
-      for (int k = 0; k < P2; ++k) h[k] = pack(hp[2 * k], hp[2 * k + 1]);
+  for (int64_t item = blockIdx.x;;) {
+    __syncthreads();  // the last item's shared memory is read
+    if (!kPiece && p.queue) {
+      if (tid == 0) s.item = atomicAdd(&p.queue->counter, 1u);
+      __syncthreads();
+      item = s.item;
     }
-    for (int j = 0; j < piece; ++j) {  // the state that the pieces before this one leave
-      const int64_t row = ((int64_t)j * gridDim.y + b) * a.channels + chan;
-      const float t = p.T[row];
-      const float* ep = p.E + row * N + sub * SPL;
-#pragma unroll
-      for (int k = 0; k < P2; ++k) {
-        const float2 e = unpack(mul2(a2[k], pack(t, t)));
-        h[k] = fma2(pack(exp2_fast(e.x), exp2_fast(e.y)), h[k], pack(ep[2 * k], ep[2 * k + 1]));
-      }
+    if (item >= items) return;
+    const Item it = item_of<CT, kPiece>(p, item, split, chains);
+    for (int i = tid; i < CT; i += kThreads) {
+      s.bias[i] = a.dt_bias && i < it.cn ? a.dt_bias[it.c0 + i] : 0.f;
+      s.skip[i] = !kPiece && a.D && i < it.cn ? a.D[it.c0 + i] : 0.f;
     }
-  }
-  float delta_sum = 0.f;
+    bool ok = true;
+    if (!kPiece && it.sub > 0 && tid == 0)  // the chain's last item has left its state
+      ok = wait_done(&p.done[it.chain], (uint32_t)it.sub, p.queue, p.ctl.spin_limit_ns);
+    ok = __syncthreads_and(ok);
 
-  // this thread's eight channels of a tile's token
-  constexpr int kVecs = CT / 8;
-  const int vt = threadIdx.x / kVecs, vc = 8 * (threadIdx.x % kVecs);
-  const int valid = cn - vc;  // may be negative
-  const bool vec = p.vec && valid >= 8;
-  float bias[8], skip[8];
+    if (!scans) {
+      const int role = (tid - kScanThreads) / kRoleThreads;
+      if (role == 0)
+        ok = copy_role<T, N, kPiece>(p, maps, it, s, tile0);
+      else if (role == 1)
+        ok = prepare_role<T, N, kPiece>(p, it, s, tile0);
+      else if constexpr (!kPiece)
+        ok = finish_role<T, N>(p, it, s, tile0);
+    } else {
+      float A[2][kSpl], h[2][kSpl], delta_sum[2] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = a.dt_bias && i < valid ? a.dt_bias[c0 + vc + i] : 0.f;
-    skip[i] = !kPiece && a.D && i < valid ? a.D[c0 + vc + i] : 0.f;
-  }
-  const T* up = static_cast<const T*>(a.u.ptr) + b * a.u.batch_stride + c0 + vc;
-  const T* dp = static_cast<const T*>(a.dt.ptr) + b * a.dt.batch_stride + c0 + vc;
-  const T* zp = a.z.ptr ? static_cast<const T*>(a.z.ptr) + b * a.z.batch_stride + c0 + vc : nullptr;
-  T* yp = static_cast<T*>(a.y) + b * a.seqlen * a.channels + c0 + vc;
-  const T* bp = static_cast<const T*>(a.B.ptr) + b * a.B.batch_stride + (int64_t)g * N;
-  const T* cp = static_cast<const T*>(a.C.ptr) + b * a.C.batch_stride + (int64_t)g * N;
-
-  for (int64_t t0 = t_begin; t0 < t_live; t0 += kTokens) {
-    const int64_t t = t0 + vt;
-    const bool live = t < t_live && valid > 0;
-    float u[8] = {}, z[8] = {};
-    {
-      float d[8] = {};
-      if (live) {
-        load8<T>(up + t * a.u.token_stride, vec, valid, u);
-        load8<T>(dp + t * a.dt.token_stride, vec, valid, d);
-        if (!kPiece && zp) load8<T>(zp + t * a.z.token_stride, vec, valid, z);
-      }
+      for (int c = 0; c < 2; ++c) {
+        const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v = d[i] + bias[i];
-        float vv[1] = {v};
-        if (a.softplus) softplus_n(vv, vv);
-        v = vv[0];
-        if (!live || i >= valid) v = 0.f;  // a token that leaves the state as it is
-        s_d[vt][vc + i] = make_float4(v, v, v * u[i], v * u[i]);
-      }
-    }
-    for (int i = threadIdx.x; i < kTokens * N; i += kThreads) {
-      const int64_t tb = t0 + i / N;
-      s_b[i / N][i % N] = tb < t_live ? to_f32(bp[tb * a.B.token_stride + i % N]) : 0.f;
-      if (!kPiece) s_c[i / N][i % N] = tb < t_live ? to_f32(cp[tb * a.C.token_stride + i % N]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int j0 = 0; j0 < kTokens; j0 += LPC) {
-      float part[LPC];
-#pragma unroll
-      for (int j = 0; j < LPC; ++j) {
-        const ulonglong2 dd = *reinterpret_cast<const ulonglong2*>(&s_d[j0 + j][cl]);
-        const uint64_t* bb = reinterpret_cast<const uint64_t*>(&s_b[j0 + j][sub * SPL]);
-        const uint64_t* cc = reinterpret_cast<const uint64_t*>(&s_c[kPiece ? 0 : j0 + j][sub * SPL]);
-        uint64_t acc = 0;
-#pragma unroll
-        for (int k = 0; k < P2; ++k) {
-          const float2 e = unpack(mul2(dd.x, a2[k]));
-          h[k] = fma2(pack(exp2_fast(e.x), exp2_fast(e.y)), h[k], mul2(dd.y, bb[k]));
-          if (!kPiece) acc = k == 0 ? mul2(h[k], cc[k]) : fma2(h[k], cc[k], acc);
+        for (int i = 0; i < kSpl; ++i) {
+          A[c][i] = a.A[chan * N + sub * kSpl + i] * kLog2e;
+          h[c][i] = 0.f;
         }
-        if (kPiece) {
-          delta_sum += unpack(dd.x).x;
+      }
+      float4* hand = reinterpret_cast<float4*>(p.hand) + (it.chain * kScanThreads + tid) * 2;
+      if constexpr (!kPiece) {
+        if (it.sub > 0) {
+          const float4 v = __ldcg(hand), w = __ldcg(hand + 1);
+          h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
+          h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
+          if (!ok) {  // never but on a GPU that stopped: an output that cannot pass for one
+#pragma unroll
+            for (int i = 0; i < kSpl; ++i) h[0][i] = h[1][i] = __int_as_float(0x7fffffff);
+          }
         } else {
-          const float2 s = unpack(acc);
-          part[j] = s.x + s.y;
-        }
-      }
-      if (!kPiece) {
-        // each round halves the tokens a lane still holds; the lane's index is its token
 #pragma unroll
-        for (int half = LPC / 2; half > 0; half /= 2) {
-          const bool upper = (sub & half) != 0;
+          for (int c = 0; c < 2; ++c) {
+            const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
+            if (a.h0) {
 #pragma unroll
-          for (int j = 0; j < half; ++j) {
-            const float send = upper ? part[j] : part[j + half];
-            const float keep = upper ? part[j + half] : part[j];
-            part[j] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+              for (int i = 0; i < kSpl; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * kSpl + i];
+            }
+#pragma unroll 4
+            for (int j = 0; j < it.part; ++j) {  // the state that the parts before this one leave
+              const int64_t row = ((int64_t)j * a.batch + it.b) * a.channels + chan;
+              float e[kSpl], v[kSpl];
+              mul_n(A[c], p.T[row], e);
+#pragma unroll
+              for (int i = 0; i < kSpl; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * kSpl + i];
+              fma_n(e, h[c], v);
+#pragma unroll
+              for (int i = 0; i < kSpl; ++i) h[c][i] = v[i];
+            }
           }
         }
-        s_y[j0 + sub][cl] = part[0];
+      }
+      ok = scan_role<T, N, kPiece>(p, it, s, tile0, A, h, delta_sum);
+      if (!kPiece && it.sub + 1 < p.sp.subs) {
+        hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+        hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (cl + c >= it.cn) continue;
+          const int64_t chan = it.c0 + cl + c;
+          float* out = nullptr;
+          if constexpr (kPiece) {
+            const int64_t row = ((int64_t)it.part * a.batch + it.b) * a.channels + chan;
+            if (sub == 0) p.T[row] = delta_sum[c];
+            out = p.E + row * N;
+          } else if (a.h_final && it.part == split - 1) {
+            out = a.h_final + (it.b * a.channels + chan) * N;
+          }
+          if (out) {
+#pragma unroll
+            for (int i = 0; i < kSpl; ++i) out[sub * kSpl + i] = h[c][i];
+          }
+        }
       }
     }
-    __syncthreads();
-    if (!kPiece && live) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = fmaf(skip[i], u[i], s_y[vt][vc + i]);
-        if (zp) v[i] *= silu(z[i]);
-      }
-      store8<T>(yp + t * a.channels, vec, valid, v);
+    if (!__syncthreads_and(ok)) {  // a wait inside the CTA ran out
+      if (p.queue && tid == 0) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+      return;
     }
-  }
-
-  if (!kPiece) {  // padding
-    if (valid > 0) {
-      const float zero[8] = {};
-      for (int64_t t = (t_begin > len ? t_begin : len) + vt; t < t_end; t += kTokens)
-        store8<T>(yp + t * a.channels, vec, valid, zero);
+    if (kPiece || !p.queue) return;
+    if (it.sub + 1 < p.sp.subs && tid == 0 && item != p.ctl.stall_tile) {
+      __threadfence();
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&p.done[it.chain]), "r"((uint32_t)it.sub + 1) : "memory");
     }
-    if (a.h_final && piece == p.pieces - 1 && have) {
-      float* hp = a.h_final + (b * a.channels + chan) * N + sub * SPL;
-#pragma unroll
-      for (int k = 0; k < P2; ++k) {
-        const float2 v = unpack(h[k]);
-        hp[2 * k] = v.x;
-        hp[2 * k + 1] = v.y;
-      }
-    }
-  } else if (have) {
-    const int64_t row = ((int64_t)piece * gridDim.y + b) * a.channels + chan;
-    if (sub == 0) p.T[row] = delta_sum;
-    float* ep = p.E + row * N + sub * SPL;
-#pragma unroll
-    for (int k = 0; k < P2; ++k) {
-      const float2 v = unpack(h[k]);
-      ep[2 * k] = v.x;
-      ep[2 * k + 1] = v.y;
-    }
+    tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
   }
 }
 
@@ -261,46 +563,129 @@ cudaError_t with_dstate(int n, F&& f) {
   }
 }
 
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Workspace: header and finished items of every chain (each call clears both), the chains' states, E, T.
+struct Layout {
+  size_t done, hand, E, T, total;
+};
+Layout layout(const SelscanSplit& sp, int64_t batch, int channels, int dstate) {
+  Layout l{};
+  if (sp.subs == 1 && sp.split == 1) return l;
+  const size_t chains = sp.subs > 1 ? (size_t)(batch * sp.tiles * sp.split) : 0;
+  const size_t rows = (size_t)(sp.split - 1) * batch * channels;
+  l.done = kHeaderBytes;
+  l.hand = up256(l.done + 4 * chains);
+  l.E = up256(l.hand + chains * kScanThreads * 2 * kSpl * sizeof(float));
+  l.T = up256(l.E + rows * dstate * sizeof(float));
+  l.total = up256(l.T + rows * sizeof(float));
+  return l;
+}
+
 Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace) {
-  Params p{a, static_cast<float*>(workspace), nullptr, sp.piece_tokens, sp.pieces, (int)(sp.tiles / a.ngroups), false};
-  p.T = p.E + (int64_t)(sp.pieces - 1) * a.batch * a.channels * a.dstate;
+  Params p{};
+  p.a = a;
+  p.sp = sp;
+  p.ctl = next_lookback_ctl();
+  const Layout l = layout(sp, a.batch, a.channels, a.dstate);
+  char* ws = static_cast<char*>(workspace);
+  if (sp.subs > 1) {
+    p.queue = reinterpret_cast<WsHeader*>(ws);
+    p.done = reinterpret_cast<uint32_t*>(ws + l.done);
+    p.hand = reinterpret_cast<float*>(ws + l.hand);
+  }
+  if (sp.split > 1) {
+    p.E = reinterpret_cast<float*>(ws + l.E);
+    p.T = reinterpret_cast<float*>(ws + l.T);
+  }
   const int e = a.dtype == SSM_F32 ? 4 : 2;
-  p.vec = a.channels / a.ngroups % 8 == 0 && aligned_rows(a.y, a.channels, 0, e, 16);
-  for (const ssm_tokens* t : {&a.u, &a.dt, &a.z}) p.vec = p.vec && aligned_rows(t->ptr, t->batch_stride, t->token_stride, e, 16);
+  p.vec = a.seqlen > 0 && a.channels / a.ngroups % 8 == 0 && aligned_rows(a.y, a.channels, 0, e, 16);
+  for (const ssm_tokens* t : {&a.u, &a.dt, &a.z, &a.B, &a.C})
+    if (t->ptr)  // (a tensor map takes no rows that lie on one another)
+      p.vec = p.vec && aligned_rows(t->ptr, a.batch > 1 ? t->batch_stride : 0, a.seqlen > 1 ? t->token_stride : 0, e, 16) &&
+              (a.batch == 1 || t->batch_stride > 0) && (a.seqlen == 1 || t->token_stride > 0);
   return p;
+}
+
+cudaError_t make_maps(const Params& p, Maps* m) {
+  const ssm_selscan_args& a = p.a;
+  if (!p.vec) return cudaSuccess;
+  const uint64_t e = a.dtype == SSM_F32 ? 4 : 2;
+  const auto type = a.dtype == SSM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto make = [&](CUtensorMap* map, const ssm_tokens& t, int columns, int box_columns) -> cudaError_t {
+    if (!t.ptr) return cudaSuccess;
+    const uint64_t dims[3] = {(uint64_t)columns, (uint64_t)a.seqlen, (uint64_t)a.batch};
+    // the stride of an axis of one element is not used, but has to be a valid one
+    const uint64_t row = a.seqlen > 1 ? t.token_stride * e : (columns * e + 15) / 16 * 16;
+    const uint64_t strides[2] = {row, a.batch > 1 ? t.batch_stride * e : row * (uint64_t)a.seqlen};
+    const uint32_t box[3] = {(uint32_t)box_columns, (uint32_t)kTokens, 1};
+    return encode_tensor_map_3d(map, type, t.ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  const int ct = tile_channels(a.dstate), n = a.ngroups * a.dstate;
+  cudaError_t r = make(&m->u, a.u, a.channels, ct);
+  if (r == cudaSuccess) r = make(&m->dt, a.dt, a.channels, ct);
+  if (r == cudaSuccess) r = make(&m->z, a.z, a.channels, ct);
+  if (r == cudaSuccess) r = make(&m->B, a.B, n, a.dstate);
+  if (r == cudaSuccess) r = make(&m->C, a.C, n, a.dstate);
+  return r;
 }
 
 template <bool kPiece>
 cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace, cudaStream_t s) {
+  // the first kernel of a call that has a workspace follows the clearing of its header
+  const bool clears = sp.bytes > 0 && (kPiece || sp.split == 1);
+  if (clears) {
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, layout(sp, a.batch, a.channels, a.dstate).hand, s);
+    if (e != cudaSuccess) return e;
+  }
   const Params p = make_params(a, sp, workspace);
-  const dim3 grid((unsigned)(sp.tiles * (kPiece ? sp.pieces - 1 : sp.pieces)), (unsigned)a.batch);
+  Maps maps;
+  const cudaError_t me = make_maps(p, &maps);
+  if (me != cudaSuccess) return me;
   return with_dstate(a.dstate, [&](auto n) {
     constexpr int N = decltype(n)::value;
-    return a.dtype == SSM_BF16
-               ? launch_pdl(selscan_kernel<__nv_bfloat16, N, kPiece>, grid, dim3(kThreads), 0, s, p)
-               : launch_pdl(selscan_kernel<float, N, kPiece>, grid, dim3(kThreads), 0, s, p);
+    int64_t grid = a.batch * sp.tiles * (kPiece ? sp.split - 1 : sp.split);
+    const int64_t slots = (int64_t)kSmCount * kResident;
+    if (!kPiece && p.queue) grid = grid * sp.subs < slots ? grid * sp.subs : slots;
+    const auto go = [&](auto kernel, size_t bytes) {
+      const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes);
+      if (e != cudaSuccess) return e;
+      if (!clears) return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), bytes, s, p, maps);
+      kernel<<<dim3((unsigned)grid), dim3(kThreads), bytes, s>>>(p, maps);
+      return cudaGetLastError();
+    };
+    return a.dtype == SSM_BF16 ? go(selscan_kernel<__nv_bfloat16, N, kPiece>, sizeof(Shared<__nv_bfloat16, N, kPiece>)) : go(selscan_kernel<float, N, kPiece>, sizeof(Shared<float, N, kPiece>));
   });
 }
 
 }  // namespace
 
+// The time axis is split where the chains are less than 9/20 of the resident CTAs, into as many parts
+// as fill them (b1 L8192 d5120, 80 chains: 656 us in one part, 362 in four; b4, 320 chains: 823 in
+// one, more in two: the first kernel does 0.7 of the work of the second once more).  Chains that are
+// more than the resident CTAs but few of their waves go through the queue in items of kSubTokens tokens,
+// so that the last wave is short (b4 L8192 d5120: 823 us, without 1300).
 SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
-  const int ct = tile_channels(dstate), tt = tile_tokens(dstate);
+  const int ct = tile_channels(dstate);
   const int64_t group_channels = channels / ngroups;
-  SelscanSplit sp{1, seqlen, ngroups * ((group_channels + ct - 1) / ct), 0};
-  const int64_t ctas = sp.tiles * batch, time_tiles = (seqlen + tt - 1) / tt;
-  if (ctas > 0 && ctas < 4 * kSmCount && time_tiles >= 8) {
-    int64_t want = (8 * kSmCount + ctas - 1) / ctas;
-    want = want < kMaxPieces ? want : kMaxPieces;
-    want = want < time_tiles / 4 ? want : time_tiles / 4;
-    if (want > 1) {
-      sp.piece_tokens = (time_tiles + want - 1) / want * tt;
-      sp.pieces = (int)((seqlen + sp.piece_tokens - 1) / sp.piece_tokens);
-      sp.bytes = sizeof(float) * (size_t)(sp.pieces - 1) * batch * channels * (dstate + 1);
-      sp.bytes = (sp.bytes + 255) / 256 * 256;
-    }
+  SelscanSplit sp{1, 1, seqlen, seqlen, ngroups * ((group_channels + ct - 1) / ct), 0};
+  const int64_t chains = sp.tiles * batch, time_tiles = (seqlen + kTokens - 1) / kTokens;
+  const int64_t slots = (int64_t)kSmCount * kResident;
+  int64_t want = chains > 0 && 20 * chains < 9 * slots ? (slots * 15 / 16 + chains - 1) / chains : 1;
+  if (want > kMaxSplit) want = kMaxSplit;
+  if (want > time_tiles / 8) want = time_tiles / 8;
+  if (want > 1) {
+    const int64_t each = (time_tiles + want - 1) / want;
+    sp.split = (int)((time_tiles + each - 1) / each);
+    if (sp.split > 1) sp.part_tokens = each * kTokens;
   }
-  if (sp.pieces == 1) sp.piece_tokens = seqlen, sp.bytes = 0;
+  sp.sub_tokens = sp.part_tokens;
+  const int64_t all = chains * sp.split;
+  if (all > slots && all < 8 * slots && sp.part_tokens >= 2 * kSubTokens) {
+    sp.sub_tokens = kSubTokens;
+    sp.subs = (int)((sp.part_tokens + kSubTokens - 1) / kSubTokens);
+  }
+  sp.bytes = layout(sp, batch, channels, dstate).total;
   return sp;
 }
 

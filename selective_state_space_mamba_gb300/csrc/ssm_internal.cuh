@@ -440,12 +440,13 @@ cudaError_t launch_conv_fwd(const ssm_tokens& x, const float* w, const float* bi
 cudaError_t launch_conv_step(const ssm_tokens& x, const float* w, const float* bias, const void* state_in,
                              const int32_t* slots, void* y, void* state_out, int64_t batch, int64_t nslots,
                              int channels, int width, bool silu, ssm_dtype dtype, cudaStream_t s);
-// Pieces of the time axis that a selective scan of these sizes is split into, and their workspace:
-// the end state of each piece but the last, started from zero, and its sum of delta.
+// How a selective scan of these sizes is cut, and its workspace.
 struct SelscanSplit {
-  int pieces;            // 1: not split
-  int64_t piece_tokens;  // tokens of a piece (the last may be shorter)
-  int64_t tiles;         // channel tiles of one sequence
+  int split;            // parts of the time axis that run at once (1: not split)
+  int subs;             // items of a part, one after the other, that the CTAs claim from a queue (1: no queue)
+  int64_t part_tokens;  // tokens of a part (the last may be shorter)
+  int64_t sub_tokens;   // tokens of an item (likewise)
+  int64_t tiles;        // channel tiles of one sequence
   size_t bytes;
 };
 SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups);

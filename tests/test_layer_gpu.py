@@ -594,3 +594,69 @@ def test_selscan_step_many(d, N, G, pad, dtype):
                             inplace=True)
     close(host(h), want_h, eh, "h")
     close(host(y), want, ey, "y", dtype)
+
+
+QUEUE = (13, 2100, 1544)  # chains enough that the CTAs claim them in items, one after the other
+
+
+def queue_case(dtype, key):
+    """Inputs of a scan that takes the queue, and the sequences and channels that the oracle checks."""
+    b, L, d = QUEUE
+    r = rng_of("queue", dtype, key)
+    inp = scan_inputs(r, (b, L), d, 16, 1, dtype)
+    h0 = (0.3 * r.standard_normal((b, d, 16))).astype(np.float32)
+    return inp, h0, np.array([0, 5, b - 1]), np.sort(r.choice(d, 40, replace=False))
+
+
+@pytest.mark.parametrize("dtype,lens", [("bf16", None), ("f32", [2100, 1, 0, 700, 512, 513, 1024, 1040, 2048, 2047, 1536, 31, 1999])])
+def test_selscan_queue(dtype, lens):
+    """Chains of several items that the CTAs claim one after the other, a state handed on at each:
+    against the definition, and bit for bit what the same tokens give in several calls."""
+    import selective_state_space_mamba_gb300 as ssm
+    inp, h0, bs, cs = queue_case(dtype, lens is None)
+    sub = {k: (v[cs] if k in ("A", "D", "dt_bias") else v[bs] if k in ("B", "C") else v[bs][..., cs]) for k, v in inp.items()}
+    some = None if lens is None else [lens[i] for i in bs]
+    y_ref, ey, h_ref, eh = ol.selscan(**sub, h0=h0[bs][:, cs], lens=some)
+    if lens is not None:
+        for i, n in enumerate(lens):
+            for k in ("u", "dt", "B", "C", "z"):
+                inp[k][i, n:] = np.nan
+    y, h = run_scan(inp, dtype, 0, h0, lens)
+    close(host(h)[bs][:, cs], h_ref, eh, "h")
+    close(host(y)[bs][..., cs], y_ref, ey, "y", dtype)
+    t = {k: dev(inp[k], dtype) for k in ("u", "dt", "B", "C", "z")}
+    A, D, bias, state = dev(inp["A"]), dev(inp["D"]), dev(inp["dt_bias"]), dev(h0)
+    for t0 in range(0, QUEUE[1], 512):
+        p = {k: v[:, t0 : t0 + 512] for k, v in t.items()}
+        n = None if lens is None else ints([min(max(m - t0, 0), 512) for m in lens])
+        part, state = ssm.selscan_fwd(p["u"], p["dt"], A, p["B"], p["C"], D, p["z"], bias, state, n)
+        assert np.array_equal(host(part), host(y[:, t0 : t0 + 512]))
+    assert np.array_equal(host(state), host(h))
+
+
+def test_selscan_queue_wait_runs_out():
+    """An item that never publishes its state: the waits of the chain's later items run out, the call
+    reports it, its later outputs are NaN, and the workspace serves the next call."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    from selective_state_space_mamba_gb300 import _lib
+    b, L, d = QUEUE
+    g = torch.Generator("cuda").manual_seed(5)
+    u, dt = (torch.randn(b, L, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    B, C = (torch.randn(b, L, 1, 16, device="cuda", generator=g).bfloat16() for _ in range(2))
+    A = -torch.rand(d, 16, device="cuda", generator=g) - 0.1
+    ws = ssm.Workspace("cuda")
+    y, h = ssm.selscan_fwd(u, dt, A, B, C, workspace=ws)
+    assert ssm.check_device_status(ws) == 0
+    assert torch.isfinite(y).all()
+    try:
+        ssm.debug_set_lookback_fault(3, 2_000_000)
+        bad, _ = ssm.selscan_fwd(u, dt, A, B, C, workspace=ws)
+        status = ssm.check_device_status(ws)
+    finally:
+        ssm.debug_set_lookback_fault()
+    assert status == _lib.SSM_ERR_TIMEOUT
+    assert torch.isnan(bad).any() and torch.equal(bad[:, :256], y[:, :256])
+    again, h2 = ssm.selscan_fwd(u, dt, A, B, C, workspace=ws)
+    assert ssm.check_device_status(ws) == 0
+    assert torch.equal(again, y) and torch.equal(h2, h)
