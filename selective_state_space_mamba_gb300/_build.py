@@ -4,6 +4,7 @@ Each .cu under csrc/ compiles to an object in parallel, then one shared library 
 with the CUDA runtime statically.  Rebuilds only when a source or header is newer than the
 library.  build(debug=True) makes the debug library (libssm_gb300_debug.so, -DSSM_DEBUG): the
 same kernels with their device index checks compiled in (see ssm_debug_build in ssm.h).
+build_binding() makes the compiled part of the Python entry points in _layer.py.
 """
 from __future__ import annotations
 
@@ -20,6 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libssm_gb300.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libssm_gb300_debug.so")
+
+BINDING = os.path.join(HERE, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -75,6 +78,31 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
     return lib
+
+
+def build_binding(force: bool = False) -> str:
+    """Build the compiled Python entry points of the operators around a layer's scan (_binding.so, from
+    csrc/binding.cpp) with g++ against the installed torch."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_path("include"), os.path.join(home, "include"),
+           os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *[f"-I{p}" for p in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+           f"-L{os.path.join(home, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
