@@ -8,6 +8,7 @@
 // The C entry points are handed over by address (bind), so that this module and ctypes share one
 // library and its state.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -61,6 +62,8 @@ struct Like {
     code = type == at::kFloat ? SSM_F32 : SSM_BF16;
     bytes = type == at::kFloat ? 4 : 2;
   }
+  // the C call goes to the current device
+  c10::cuda::CUDAGuard guard() const { return c10::cuda::CUDAGuard(device); }
   ssm_stream_t stream() const {
     return reinterpret_cast<ssm_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
   }
@@ -163,6 +166,7 @@ int64_t step_states(Out& out, PyObject* state, PyObject* state_out, bool inplace
 PyObject* conv_fwd(PyObject* const* v) {  // x, weight, bias, state, lens, silu, y, state_out, return_final_state
   const at::Tensor &x = tensor("x", v[0]), &w = tensor("weight", v[1]);
   const Like like("x", x);
+  const auto guard = like.guard();
   if (x.dim() != 3 || w.dim() != 2) fail("x, weight", "[b, L, d] and [d, W]");
   const int64_t b = x.size(0), L = x.size(1), d = x.size(2), W = w.size(1);
   const ssm_tokens xt = tokens("x", x, {b, L, d}, like);
@@ -181,6 +185,7 @@ PyObject* conv_fwd(PyObject* const* v) {  // x, weight, bias, state, lens, silu,
 PyObject* conv_step(PyObject* const* v) {  // x, weight, bias, state, slots, silu, y, state_out, inplace
   const at::Tensor &x = tensor("x", v[0]), &w = tensor("weight", v[1]);
   const Like like("x", x);
+  const auto guard = like.guard();
   if (x.dim() != 2 || w.dim() != 2) fail("x, weight", "[b, d] and [d, W]");
   const int64_t b = x.size(0), d = x.size(1), W = w.size(1);
   const ssm_tokens xt = tokens("x", x, {b, d}, like);
@@ -226,6 +231,7 @@ ssm_selscan_args selscan_args(PyObject* const* v, const Like& like, const at::Te
 PyObject* selscan_fwd(PyObject* const* v) {
   const at::Tensor& u = tensor("u", v[0]);
   const Like like("u", u);
+  const auto guard = like.guard();
   if (u.dim() != 3) fail("u", "[b, L, d]");
   ssm_selscan_args a = selscan_args(v, like, u, 2);
   a.seqlen = u.size(1);
@@ -253,6 +259,7 @@ PyObject* selscan_fwd(PyObject* const* v) {
 PyObject* selscan_step(PyObject* const* v) {
   const at::Tensor& u = tensor("u", v[0]);
   const Like like("u", u);
+  const auto guard = like.guard();
   if (u.dim() != 2) fail("u", "[b, d]");
   ssm_selscan_args a = selscan_args(v, like, u, 1);
   a.seqlen = 1;
@@ -304,6 +311,7 @@ struct Norm {
 
 PyObject* rmsnorm_fwd(PyObject* const* v) {  // x, weight, residual, eps, y, residual_out
   Norm n(v[0], v[1], v[2], v[5]);
+  const auto guard = n.like.guard();
   const double eps = PyFloat_AsDouble(v[3]);
   if (eps == -1.0 && PyErr_Occurred()) return nullptr;
   Out y;
@@ -315,6 +323,7 @@ PyObject* rmsnorm_fwd(PyObject* const* v) {  // x, weight, residual, eps, y, res
 
 PyObject* rmsnorm_fp8_fwd(PyObject* const* v) {  // x, weight, residual, eps, group, q, scale, residual_out
   Norm n(v[0], v[1], v[2], v[7]);
+  const auto guard = n.like.guard();
   const double eps = PyFloat_AsDouble(v[3]);
   const long group = PyLong_AsLong(v[4]);
   if (PyErr_Occurred()) return nullptr;

@@ -21,13 +21,34 @@ using namespace layer;
 constexpr int kConvThreads = 128;
 constexpr int kConvUnroll = 4;
 constexpr int kConvResident = 7;  // CTAs an SM
+constexpr int kConvRun = 128;     // tokens of a run, about
 constexpr int kSmCount = 152;
+
+// The weights [VEC][W] of VEC channels from p on, by tap; vec_w: p is 16-byte aligned.
+template <int VEC, int W>
+__device__ __forceinline__ void load_weights(const float* p, bool vec_w, float (&wt)[W][VEC]) {
+  float v[VEC * W];
+  if (VEC * W % 4 == 0 && vec_w) {
+#pragma unroll
+    for (int i = 0; i + 3 < VEC * W; i += 4) {
+      const float4 r = __ldg(reinterpret_cast<const float4*>(p + i));
+      v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC * W; ++i) v[i] = __ldg(p + i);
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+#pragma unroll
+    for (int k = 0; k < W; ++k) wt[k][i] = v[i * W + k];
+}
 
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads, kConvResident)
     conv_kernel(const ssm_tokens x, const float* __restrict__ w, const float* __restrict__ bias, const T* state_in,
                 const int32_t* lens, T* y, T* state_out, int64_t items, int64_t seqlen, int channels, int run,
-                bool act) {
+                bool act, bool vec_w) {
   griddep_launch_dependents();
   griddep_wait();
   const int64_t item = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
@@ -60,15 +81,23 @@ __global__ void __launch_bounds__(kConvThreads, kConvResident)
   const int64_t t1 = t0 + run < seqlen ? t0 + run : seqlen;  // end of the run
   const int64_t tl = t1 < len ? t1 : len;                     // end of its tokens that are no padding
   if (t0 < tl) {
-    float wt[W][VEC], bi[VEC], win[W - 1 + kConvUnroll][VEC];
+    const T* xp = xb + t0 * x.token_stride;
+    T* yp = yb + t0 * channels;
+    const int n = (int)(tl - t0), whole = n / kConvUnroll * kConvUnroll;
+    // the first block, the window before it and the weights are all on their way before one is used
+    Raw<T, VEC> next[kConvUnroll], before[W - 1];
+    if (whole > 0) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-      for (int k = 0; k < W; ++k) wt[k][i] = w[(int64_t)(c + i) * W + k];
-      bi[i] = bias ? bias[c + i] : 0.f;
+      for (int j = 0; j < kConvUnroll; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
     }
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) to_floats<T, VEC>(token(t0 - (W - 1) + k), win[k]);
+    for (int k = 0; k < W - 1; ++k) before[k] = token(t0 - (W - 1) + k);
+    float wt[W][VEC], bi[VEC], win[W - 1 + kConvUnroll][VEC];
+    load_weights(w + (int64_t)c * W, vec_w, wt);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bi[i] = bias ? bias[c + i] : 0.f;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) to_floats<T, VEC>(before[k], win[k]);
     // one token: the window's W values that end with win[W - 1 + j]
     const auto emit = [&](int j, T* yp) {
       float v[VEC];
@@ -79,14 +108,6 @@ __global__ void __launch_bounds__(kConvThreads, kConvResident)
       if (act) silu_n(v, v);
       store_raw<T, VEC>(yp, from_floats<T, VEC>(v));
     };
-    const T* xp = xb + t0 * x.token_stride;
-    T* yp = yb + t0 * channels;
-    const int n = (int)(tl - t0), whole = n / kConvUnroll * kConvUnroll;
-    Raw<T, VEC> next[kConvUnroll];
-    if (whole > 0) {
-#pragma unroll
-      for (int j = 0; j < kConvUnroll; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
-    }
     for (int t = 0; t < whole; t += kConvUnroll) {
 #pragma unroll
       for (int j = 0; j < kConvUnroll; ++j) to_floats<T, VEC>(next[j], win[W - 1 + j]);
@@ -116,43 +137,65 @@ __global__ void __launch_bounds__(kConvThreads, kConvResident)
   for (int64_t t = t0 > len ? t0 : len; t < t1; ++t) store_raw<T, VEC>(yb + t * channels, zero_raw<T, VEC>());
 }
 
-template <typename T, int VEC, int W>
+// One new token of ROWS sequences a thread: the loads of all are started before the first is used, and the
+// weights are loaded once.
+template <typename T, int VEC, int W, int ROWS>
 __global__ void __launch_bounds__(kConvThreads)
     conv_step_kernel(const ssm_tokens x, const float* __restrict__ w, const float* __restrict__ bias,
-                     const T* state_in, const int32_t* slots, T* y, T* state_out, int64_t nslots, int channels,
-                     bool act) {
+                     const T* state_in, const int32_t* slots, T* y, T* state_out, int64_t batch, int64_t nslots,
+                     int channels, bool act, bool vec_w) {
   griddep_launch_dependents();
   griddep_wait();
   const int c = (blockIdx.x * kConvThreads + threadIdx.x) * VEC;
   if (c >= channels) return;
-  const int64_t b = blockIdx.y;
-  const int64_t slot = slots ? slots[b] : b;
-  T* yp = y + b * channels + c;
-  if (slot < 0 || slot >= nslots) {
-    store_raw<T, VEC>(yp, zero_raw<T, VEC>());
-    return;
+  const int64_t b0 = (int64_t)blockIdx.y * ROWS;
+  int64_t slot[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    slot[r] = -1;
+    if (b0 + r < batch) slot[r] = slots ? slots[b0 + r] : b0 + r;
   }
-  const int64_t base = slot * (W - 1) * channels + c;
-  Raw<T, VEC> raw[W];
+  Raw<T, VEC> raw[ROWS][W];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k)
-    raw[k] = state_in ? load_raw<T, VEC>(state_in + base + (int64_t)k * channels) : zero_raw<T, VEC>();
-  raw[W - 1] = load_raw<T, VEC>(static_cast<const T*>(x.ptr) + b * x.batch_stride + c);
-  float a[VEC];
+  for (int r = 0; r < ROWS; ++r)
+    if (b0 + r < batch) raw[r][W - 1] = load_raw<T, VEC>(static_cast<const T*>(x.ptr) + (b0 + r) * x.batch_stride + c);
+  float wt[W][VEC], bi[VEC];
+  load_weights(w + (int64_t)c * W, vec_w, wt);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) a[i] = bias ? bias[c + i] : 0.f;
+  for (int i = 0; i < VEC; ++i) bi[i] = bias ? bias[c + i] : 0.f;
 #pragma unroll
-  for (int k = 0; k < W; ++k) {
-    float v[VEC];
-    to_floats<T, VEC>(raw[k], v);
+  for (int r = 0; r < ROWS; ++r) {
+    if (slot[r] >= nslots) slot[r] = -1;
+    const int64_t base = slot[r] * (W - 1) * channels + c;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) a[i] = fmaf(w[(int64_t)(c + i) * W + k], v[i], a[i]);
+    for (int k = 0; k < W - 1; ++k) {
+      raw[r][k] = zero_raw<T, VEC>();
+      if (state_in && slot[r] >= 0) raw[r][k] = load_raw<T, VEC>(state_in + base + (int64_t)k * channels);
+    }
   }
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) store_raw<T, VEC>(state_out + base + (int64_t)k * channels, raw[k + 1]);
+  for (int r = 0; r < ROWS; ++r) {
+    if (b0 + r >= batch) break;
+    T* yp = y + (b0 + r) * channels + c;
+    if (slot[r] < 0) {
+      store_raw<T, VEC>(yp, zero_raw<T, VEC>());
+      continue;
+    }
+    const int64_t base = slot[r] * (W - 1) * channels + c;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) a[i] = act ? silu(a[i]) : a[i];
-  store_raw<T, VEC>(yp, from_floats<T, VEC>(a));
+    for (int k = 0; k < W - 1; ++k) store_raw<T, VEC>(state_out + base + (int64_t)k * channels, raw[r][k + 1]);
+    float a[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) a[i] = bi[i];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      float v[VEC];
+      to_floats<T, VEC>(raw[r][k], v);
+      fma_n(wt[k], v, a);
+    }
+    if (act) silu_n(a, a);
+    store_raw<T, VEC>(yp, from_floats<T, VEC>(a));
+  }
 }
 
 // Channels per thread: 4, 2 or 1, so that every row of x, y and the states starts on a vector.
@@ -167,15 +210,16 @@ int conv_vec(const ssm_tokens& x, const void* state_in, const void* y, const voi
   return 1;
 }
 
-// Tokens of a run: about 32, so that the window before a run and the weights add little to it, and
-// such that the runs fill a whole number of the GPU's waves of resident threads; less than a wave
-// of them is cut shorter, to use more SMs, down to one block of kConvUnroll tokens.
+// Tokens of a run: about kConvRun, so that the window before a run and the weights add little to it,
+// and such that the runs fill a whole number of the GPU's waves of resident threads; less than a wave
+// of them is cut shorter, to use more SMs, down to one block of kConvUnroll tokens.  b4 L8192 d5376 of
+// wider rows: 123 us with 128, 126 with 32.
 int conv_run(int64_t columns, int64_t seqlen) {
   constexpr int64_t wave = (int64_t)kSmCount * kConvResident * kConvThreads;
-  const int64_t waves = (columns * ((seqlen + 31) / 32) + wave / 2) / wave;
+  const int64_t waves = (columns * ((seqlen + kConvRun - 1) / kConvRun) + wave / 2) / wave;
   const int64_t segs = (waves < 1 ? 1 : waves) * wave / columns;
-  const int64_t run = segs < 1 ? 32 : (seqlen + segs - 1) / segs;
-  return (int)(run < kConvUnroll ? kConvUnroll : run > 64 ? 64 : run);
+  const int64_t run = segs < 1 ? kConvRun : (seqlen + segs - 1) / segs;
+  return (int)(run < kConvUnroll ? kConvUnroll : run > 2 * kConvRun ? 2 * kConvRun : run);
 }
 
 template <typename F>
@@ -206,7 +250,7 @@ cudaError_t conv_fwd(const ssm_tokens& x, const float* w, const float* bias, con
       return launch_pdl(conv_kernel<T, decltype(vc)::value, decltype(wc)::value>,
                         dim3((unsigned)blocks, (unsigned)batch), dim3(kConvThreads), 0, s, x, w, bias,
                         static_cast<const T*>(state_in), lens, static_cast<T*>(y), static_cast<T*>(state_out), items,
-                        seqlen, channels, run, silu);
+                        seqlen, channels, run, silu, aligned_rows(w, 0, 0, 4, 16));
     });
   });
 }
@@ -219,12 +263,16 @@ cudaError_t conv_step(const ssm_tokens& x, const float* w, const float* bias, co
   row.token_stride = 0;
   const int vec = conv_vec(row, state_in, y, state_out, channels, sizeof(T));
   const int blocks = (channels / vec + kConvThreads - 1) / kConvThreads;
+  const bool many = blocks * batch >= 8 * kSmCount;  // CTAs enough with four sequences a thread
   return with_width(width, [&](auto wc) {
     return with_vec(vec, [&](auto vc) {
-      return launch_pdl(conv_step_kernel<T, decltype(vc)::value, decltype(wc)::value>,
-                        dim3((unsigned)blocks, (unsigned)batch), dim3(kConvThreads), 0, s, row, w, bias,
-                        static_cast<const T*>(state_in), slots, static_cast<T*>(y), static_cast<T*>(state_out),
-                        nslots, channels, silu);
+      constexpr int V = decltype(vc)::value, W = decltype(wc)::value;
+      const auto go = [&](auto kernel, int rows) {
+        return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)((batch + rows - 1) / rows)), dim3(kConvThreads), 0, s,
+                          row, w, bias, static_cast<const T*>(state_in), slots, static_cast<T*>(y),
+                          static_cast<T*>(state_out), batch, nslots, channels, silu, aligned_rows(w, 0, 0, 4, 16));
+      };
+      return many ? go(conv_step_kernel<T, V, W, 4>, 4) : go(conv_step_kernel<T, V, W, 1>, 1);
     });
   });
 }

@@ -5,8 +5,9 @@
 //
 // A lane holds four state entries of a channel; the N / 4 lanes of a channel sit side by side, so a
 // warp's access covers 512 consecutive bytes of a state.  state_out may be state_in: each entry is
-// read and then written by one lane.  A thread takes kStepRows sequences, whose states it loads
-// before it uses the first, with one load of its part of A.
+// read and then written by one lane.  With sequences enough a thread takes kStepRows of them, whose
+// states it loads before it uses the first, with one load of its part of A (b256 d5120 N16: 33 us with
+// four, 38 with two or eight, 54 with one; eight CTAs an SM, 8 % less time than five).
 #include "layer_common.cuh"
 
 namespace ssm {
@@ -44,9 +45,9 @@ __device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
   }
 }
 
-// ROWS sequences a thread (1 or 4).  kVec: states and A in vectors of four, and B and C.
+// ROWS sequences a thread.  kVec: states and A in vectors of four, and B and C.
 template <typename T, int N, int ROWS, bool kVec>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, ROWS > 1 ? 8 : 1)
     selscan_step_kernel(const __grid_constant__ ssm_selscan_args a, const int32_t* slots, int64_t nslots) {
   constexpr int LPC = N / 4;
   // What is one a (sequence, channel), delta, u and the gate, is the work of one of the channel's
