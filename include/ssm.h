@@ -268,7 +268,8 @@ typedef enum {
  *              prompt, oldest first; NULL for zeros
  *   y          [batch, seqlen, channels] `dtype`, dense
  *   state_out  [batch, width - 1, channels] `dtype`: the same after the prompt, or NULL
- * Sums in f32.  Sizes: batch, seqlen >= 0, channels >= 1, width 2 .. 4.  No workspace; one kernel.
+ * Sums in f32.  Sizes: batch 0 .. 65535, seqlen >= 0, channels 1 .. 2^30, width 2 .. 4.  No
+ * workspace; one kernel.
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (width; a grid beyond the launch limits),
  *   SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
  */
@@ -302,7 +303,8 @@ SSM_API ssm_status ssm_conv_step(ssm_tokens x, const float *w, const float *bias
  *   y          [batch, seqlen, channels] `dtype`, dense
  *   h_final    [batch, channels, dstate] f32, or NULL
  * States and sums are f32; softplus(v) is max(v, 0) + log(1 + exp(-|v|)).
- * Sizes: batch, seqlen >= 0, ngroups >= 1 dividing channels, dstate in {8, 16, 32, 64}.
+ * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing channels, dstate in {8, 16, 32, 64},
+ * channels * dstate <= 2^30.
  * Workspace (0 bytes where none is needed): f32 states between parts of the time axis.  It is
  * split into parts that run at once where there are too few channels to fill the GPU (one more
  * kernel, which runs the parts but the last from a zero state), and cut into items that the CTAs
@@ -350,7 +352,7 @@ SSM_API ssm_status ssm_selscan_step(const ssm_selscan_args *args, const int32_t 
  *                 each `group` columns of a row (group 128: [rows, ceil(width / 128)]) or for each
  *                 row (group 0: [rows]): scale = max(max|v| / 448, 2^-126), q = e4m3(v / scale),
  *                 round to nearest even.  A NaN in v gives NaN in q there and in its scale.
- * Sizes: rows >= 0, width >= 1.  No workspace; one kernel.
+ * Sizes: rows 0 .. 2^31 - 1, width 1 .. 2^30.  No workspace; one kernel.
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (group), SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
  */
 SSM_API ssm_status ssm_rmsnorm_fwd(const void *x, int64_t x_stride, const float *weight, const void *residual,

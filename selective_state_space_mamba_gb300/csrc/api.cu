@@ -216,6 +216,7 @@ ssm_status check_ssd_buffers(const void* x, const void* dt, const float* A, cons
 // ---- the operators around a layer's scan: argument checks ----
 bool valid_dtype(int dtype) { return dtype == SSM_F32 || dtype == SSM_BF16; }
 int dtype_bytes(ssm_dtype dtype) { return dtype == SSM_F32 ? 4 : 2; }
+constexpr int kMaxColumns = 1 << 30;  // kernels index a row's columns with 32 bits, a little past its end
 bool selscan_dstate(int n) { return n == 8 || n == 16 || n == 32 || n == 64; }
 
 // The byte ranges that a call's tensors span.  A tensor with no elements spans nothing.
@@ -275,7 +276,7 @@ ssm_status check_spans(const Spans& in, const Spans& out) {
 ssm_status check_selscan_sizes(const ssm_selscan_args& a) {
   if (a.batch < 0 || a.channels < 1 || a.ngroups < 1 || a.channels % a.ngroups != 0 || !valid_dtype(a.dtype))
     return SSM_ERR_INVALID_ARG;
-  if (!selscan_dstate(a.dstate) || a.batch > 65535) return SSM_ERR_UNSUPPORTED;
+  if (!selscan_dstate(a.dstate) || a.batch > 65535 || a.channels > kMaxColumns / a.dstate) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -297,7 +298,7 @@ ssm_status rmsnorm(const void* x, int64_t x_stride, const float* weight, const v
     return SSM_ERR_INVALID_ARG;
   if (rows == 0) return SSM_OK;
   if (!x || !weight || (!q && !y) || (residual_out && !residual)) return SSM_ERR_INVALID_ARG;
-  if (rows > 0x7fffffffLL) return SSM_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffffLL || width > kMaxColumns) return SSM_ERR_UNSUPPORTED;
   const int e = dtype_bytes(dtype), re = dtype_bytes(res_dtype);
   Spans in, out;
   in.tokens(ssm_tokens{x, x_stride, 0}, rows, 1, width, e);
@@ -697,7 +698,7 @@ ssm_status ssm_conv_fwd(ssm_tokens x, const float* w, const float* bias, const v
                         ssm_dtype dtype, ssm_stream_t stream) {
   if (batch < 0 || seqlen < 0 || channels < 1 || !valid_dtype(dtype) || (act != SSM_ACT_NONE && act != SSM_ACT_SILU))
     return SSM_ERR_INVALID_ARG;
-  if (width < 2 || width > 4) return SSM_ERR_UNSUPPORTED;
+  if (width < 2 || width > 4 || channels > kMaxColumns) return SSM_ERR_UNSUPPORTED;
   if (batch == 0 || (seqlen == 0 && !state_out)) return SSM_OK;
   if (!w || (seqlen > 0 && (!x.ptr || !y))) return SSM_ERR_INVALID_ARG;
   if (batch > 65535) return SSM_ERR_UNSUPPORTED;
@@ -725,7 +726,7 @@ ssm_status ssm_conv_step(ssm_tokens x, const float* w, const float* bias, const 
   if (batch < 0 || nslots < 0 || channels < 1 || !valid_dtype(dtype) ||
       (act != SSM_ACT_NONE && act != SSM_ACT_SILU) || (!slots && nslots != batch))
     return SSM_ERR_INVALID_ARG;
-  if (width < 2 || width > 4) return SSM_ERR_UNSUPPORTED;
+  if (width < 2 || width > 4 || channels > kMaxColumns) return SSM_ERR_UNSUPPORTED;
   if (batch == 0) return SSM_OK;
   if (!x.ptr || !w || !y || (nslots > 0 && !state_out)) return SSM_ERR_INVALID_ARG;
   if (batch > 65535) return SSM_ERR_UNSUPPORTED;
@@ -748,7 +749,8 @@ ssm_status ssm_conv_step(ssm_tokens x, const float* w, const float* bias, const 
 }
 
 size_t ssm_selscan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
-  if (batch < 0 || seqlen < 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0 || !selscan_dstate(dstate))
+  if (batch < 0 || seqlen < 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0 || !selscan_dstate(dstate) ||
+      channels > kMaxColumns / dstate)
     return 0;
   return selscan_split(batch, seqlen, channels, dstate, ngroups).bytes;
 }

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kConvThreads)
                      int channels, bool act, bool vec_w) {
   griddep_launch_dependents();
   griddep_wait();
-  const int c = (blockIdx.x * kConvThreads + threadIdx.x) * VEC;
+  const int c = (blockIdx.x * kConvThreads + threadIdx.x) * VEC;  // below channels + 512: no overflow
   if (c >= channels) return;
   const int64_t b0 = (int64_t)blockIdx.y * ROWS;
   int64_t slot[ROWS];

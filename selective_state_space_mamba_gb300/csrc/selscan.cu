@@ -68,12 +68,19 @@ struct Shared {
   float fb[2][kTokens][N];
   float fc[kPiece ? 1 : 2][kTokens][N];
   float4 d[2][kTokens][CT / 2];  // (delta, delta u) of channel pair i at i ^ (i / 8 % 4), against bank conflicts
-  float y[kPiece ? 1 : 2][kPiece ? 16 : PARTS * YP];
+  float y[kPiece ? 1 : 2][kPiece ? 16 : PARTS * YP];  // four channels at i at i ^ (i / 8 % 2), likewise
   float bias[CT], skip[CT];
   // phases of the tiles: raw tile there, raw tile read, prepared, scanned, y read
   uint64_t raw_full[kRing], raw_free[kRing], full[2], done[2], y_free[2];
   int64_t item;
 };
+
+// Channels vc to vc + 7 of a row of Shared::y.
+__device__ __forceinline__ void load_y(const float* row, int vc, float (&v)[8]) {
+  const int swap = vc >> 3 & 4;
+  const float4 a = *reinterpret_cast<const float4*>(row + (vc ^ swap)), b = *reinterpret_cast<const float4*>(row + (vc ^ swap ^ 4));
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
 
 // A lane's place among the LPC lanes of a channel pair and the LW pairs of a warp.  A 16-byte load takes
 // half the time where lanes that differ in bit 0 (or in bit 1) read the same address: bit 0 tells the
@@ -308,10 +315,10 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
       for (int t = vt; t < kTokens; t += VT) {
         if (t < rows) {
           float y[8], w[8], u[8];
-          load_states(&s.y[buf][t * CT + vc], y);
+          load_y(&s.y[buf][t * CT], vc, y);
 #pragma unroll
           for (int k = 1; k < S::PARTS; ++k) {
-            load_states(&s.y[buf][k * S::YP + t * CT + vc], w);
+            load_y(&s.y[buf][k * S::YP + t * CT], vc, w);
             add_n(y, w, y);
           }
           load8<T>(&s.u[ring][t][vc], true, 8, u);
@@ -360,7 +367,7 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Share
     const float4* d_row = &s.d[buf][0][pair ^ (pair >> 3 & 3)];
     // token of value j after the rounds: bits of `sub` from the third on, then j
     const int mine = ROUNDS == 0 ? 0 : ROUNDS == 1 ? sub >> 2 : (sub >> 2 & 1) + 2 * (sub >> 3);
-    float* y_row = kPiece ? nullptr : &s.y[kPiece ? 0 : buf][(sub & (S::PARTS - 1)) * S::YP + mine * CT + 2 * pair];
+    float* y_row = kPiece ? nullptr : &s.y[kPiece ? 0 : buf][(sub & (S::PARTS - 1)) * S::YP + mine * CT + 2 * (pair ^ (pair >> 3 & 2))];
 #pragma unroll 2
     for (int t = 0; t < kTokens; t += kBlock) {
       float2 part[kBlock];
