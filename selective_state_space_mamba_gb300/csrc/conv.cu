@@ -10,6 +10,9 @@
 // channel vector fastest: a warp reads 32 * VEC consecutive channels of a token, whatever the
 // number of channels.
 //
+// b4 L8192 d5376 of wider rows, bf16: 124 us, 5.7 TB/s (a copy: 6.7); it waits for memory.  A step of 128
+// sequences takes 4.4 us, of which the launch and the host call are all but one.
+//
 // Tokens of padding (t >= lens[b]) are neither read nor multiplied: a NaN there stays there.
 #include "layer_common.cuh"
 

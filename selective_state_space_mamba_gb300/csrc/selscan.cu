@@ -15,8 +15,13 @@
 //            out for the hardware's merging of loads; the sums over n end in up to four partial
 //            sums in shared memory
 //   finish   joins a tile's partial sums, adds the skip, gates and writes y
-// They meet at mbarriers, so the scan does not stop for the rest.  Each of the other roles takes
-// fewer cycles a tile than the scan, but not two of them together.
+// They meet at mbarriers, so the scan does not stop for the rest, and each goes through the CTA's items
+// by itself, so that an item's first tiles come in beside the last ones of the item before.
+//
+// b4 L8192 d5120 N16 in bf16: 770 us, and b1 L65521 d1536 in f32: 814 us, against 200 and 243 us of
+// memory and 280 and 170 of exponentials.  The multiply-adds of two state entries read three register
+// pairs, which takes 3.2 cycles a warp instruction and not 2: the scan alone takes 109 cycles a token
+// for the two CTAs of an SM, the same as in registers only; with the other roles beside it, 177.
 #include "layer_common.cuh"
 #include "tc_common.cuh"
 
@@ -31,7 +36,7 @@ constexpr int kTokens = 16;      // tokens of a tile
 constexpr int kSpl = 4;          // state entries of a lane's channel
 constexpr int kBlock = 4;        // tokens between two reductions
 constexpr int kResident = 2;     // CTAs an SM
-constexpr int kSubTokens = 1024; // tokens of an item of the queue
+constexpr int kSubTokens = 512;  // tokens of an item of the queue (short sequences: half of it)
 constexpr int kScanThreads = 128, kRoleThreads = 64, kThreads = kScanThreads + 3 * kRoleThreads;
 constexpr int kRing = 4;         // raw tiles in shared memory
 
@@ -52,6 +57,14 @@ struct Maps {
   CUtensorMap u, dt, z, B, C;
 };
 
+// What an item is: a part of one channel tile's tokens.
+struct Item {
+  int64_t id, chain, b, t_begin;
+  int sub, part, g, c0, cn;  // item of the chain, part of the split axis, group, first channel, channels
+  int n, live;               // tokens in all (negative: there is no further item), and before the padding
+  bool ready;                // the item of the chain before this one has left its state
+};
+
 // Shared memory of a CTA.
 template <typename T, int N, bool kPiece>
 struct Shared {
@@ -69,10 +82,11 @@ struct Shared {
   float fc[kPiece ? 1 : 2][kTokens][N];
   float4 d[2][kTokens][CT / 2];  // (delta, delta u) of channel pair i at i ^ (i / 8 % 4), against bank conflicts
   float y[kPiece ? 1 : 2][kPiece ? 16 : PARTS * YP];  // four channels at i at i ^ (i / 8 % 2), likewise
-  float bias[CT], skip[CT];
-  // phases of the tiles: raw tile there, raw tile read, prepared, scanned, y read
+  Item item[2];
+  // phases of the tiles: raw tile there, raw tile read, prepared, scanned, y read; and of the items
   uint64_t raw_full[kRing], raw_free[kRing], full[2], done[2], y_free[2];
-  int64_t item;
+  // and of the items: written down, read, scanned (the finish role may be two items behind the scan)
+  uint64_t item_full[2], item_free[2], item_done[4];
 };
 
 // Channels vc to vc + 7 of a row of Shared::y.
@@ -102,14 +116,28 @@ __device__ __forceinline__ void load_states(const float* p, float (&v)[M]) {
   }
 }
 
+// Past L1, and never before the wait for it.
+__device__ __forceinline__ float4 load_hand(const float4* p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t load_done(const uint32_t* done) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+  return v;
+}
+
 // Waits until the chain has `want` finished items; false after the limit, or once another wait gave up.
 // One thread.
 __device__ __forceinline__ bool wait_done(const uint32_t* done, uint32_t want, WsHeader* hdr, uint64_t limit_ns) {
   uint64_t t0 = 0;
   for (uint32_t spins = 0;; ++spins) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
-    if (v >= want) return true;
+    if (load_done(done) >= want) return true;
     if (spins == 0) t0 = global_timer_ns();
     if ((spins & 15u) == 15u) {
       if (ld_relaxed_u64(&hdr->status) != 0ull) return false;
@@ -122,16 +150,11 @@ __device__ __forceinline__ bool wait_done(const uint32_t* done, uint32_t want, W
   }
 }
 
-// What an item is: a part of one channel tile's tokens.
-struct Item {
-  int64_t chain, b, t_begin;
-  int sub, part, g, c0, cn;  // item of the chain, part of the split axis, group, first channel, channels
-  int n, live;               // tokens in all, and before the padding
-};
 template <int CT, bool kPiece>
 __device__ __forceinline__ Item item_of(const Params& p, int64_t item, int split, int64_t chains) {
   const ssm_selscan_args& a = p.a;
   Item it;
+  it.id = item;
   it.sub = (int)(item / chains);
   it.chain = item - it.sub * chains;
   it.part = (int)(it.chain % split);
@@ -158,8 +181,9 @@ __device__ __forceinline__ Item item_of(const Params& p, int64_t item, int split
 }
 
 // Waits for the phase of `tile` of a barrier with a phase every `every` tiles; false after the limit.
-// The hardware parks the warp for up to kParkNs a try: polling warps took a quarter of the
-// instructions of this kernel, away from the scan beside them.
+// The hardware parks the warp for up to kParkNs a try.  Such a wait may stand behind one of wait_done's,
+// so it is given twice its time.  Lanes ask each for itself: a role's lanes agree on the answer once a tile
+// (a vote in each wait costs 1 % of the whole).
 __device__ __forceinline__ bool wait_tile(uint64_t* bars, uint32_t tile, uint32_t every, uint64_t limit_ns) {
   constexpr uint32_t kParkNs = 20000;
   const uint32_t bar = smem_addr(&bars[tile % every]), parity = (tile / every) & 1;
@@ -174,8 +198,50 @@ __device__ __forceinline__ bool wait_tile(uint64_t* bars, uint32_t tile, uint32_
     if (ok) return true;
     const uint64_t now = global_timer_ns();
     if (t0 == 0) t0 = now;
-    if (now - t0 > limit_ns) return false;
+    if (now - t0 > 2 * limit_ns) return false;
   }
+}
+
+// After a wait that ran out (never but on a GPU that stopped): a state that cannot pass for one.
+__device__ __forceinline__ void set_nan(float (&h)[2][kSpl]) {
+#pragma unroll
+  for (int i = 0; i < kSpl; ++i) h[0][i] = h[1][i] = __int_as_float(0x7fffffff);
+}
+
+// Whether all lanes of the warp say so; memory accesses before and after it are in order.
+__device__ __forceinline__ bool all_lanes(bool ok) {
+  ok = __all_sync(0xffffffffu, ok);
+  __syncwarp();
+  return ok;
+}
+
+// The CTA's k-th item, as the first copy thread has written it down; false if the wait ran out.  Whole
+// warps.
+template <typename S>
+__device__ __forceinline__ bool next_item(const Params& p, S& s, uint32_t k, Item& it) {
+  if (!all_lanes(wait_tile(s.item_full, k, 2, p.ctl.spin_limit_ns))) return false;
+  it = s.item[k & 1];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&s.item_free[k & 1]);
+  return true;
+}
+
+// Claims the k-th item and writes it down for the other roles.  The first copy thread.
+template <typename T, int N, bool kPiece>
+__device__ __forceinline__ bool claim_item(const Params& p, Shared<T, N, kPiece>& s, uint32_t k, Item& it) {
+  const int split = kPiece ? p.sp.split - 1 : p.sp.split;  // nothing starts from the last part's end
+  const int64_t chains = p.a.batch * p.sp.tiles * split;
+  const int64_t id = !kPiece && p.queue ? (int64_t)atomicAdd(&p.queue->counter, 1u) : blockIdx.x;
+  if (id < chains * (kPiece ? 1 : p.sp.subs)) {
+    it = item_of<tile_channels(N), kPiece>(p, id, split, chains);
+    it.ready = it.sub == 0 || load_done(&p.done[it.chain]) >= (uint32_t)it.sub;
+  } else {
+    it = Item{}, it.n = -1;
+  }
+  if (k >= 2 && !wait_tile(s.item_free, k - 2, 2, p.ctl.spin_limit_ns)) return false;
+  s.item[k & 1] = it;
+  mbar_arrive(&s.item_full[k & 1]);
+  return true;
 }
 
 // The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
@@ -212,7 +278,7 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
   const T *B = at(a.B, (int64_t)it.g * N), *C = at(a.C, (int64_t)it.g * N);
   for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
     const int ring = tile % kRing, have = rows < kTokens ? rows : kTokens;
-    if (tile >= kRing && !wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns)) return false;
+    if (!all_lanes(tile < kRing || wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns))) return false;
 #pragma unroll 8
     for (int i = tid; i < have * CT; i += kRoleThreads) {
       const int r = i / CT, c = i % CT;
@@ -248,11 +314,12 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
   const int vt = tid / VC, vc = 8 * (tid % VC);
   const bool works = kRoleThreads / VC <= kTokens || vt < kTokens;
   float bias[8];
-  load_states(&s.bias[vc], bias);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bias[j] = p.a.dt_bias && vc + j < it.cn ? __ldg(p.a.dt_bias + it.c0 + vc + j) : 0.f;
   for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
     const int ring = tile % kRing, buf = tile & 1;
-    if (!wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns)) return false;
-    if (tile >= 2 && !wait_tile(s.done, tile - 2, 2, p.ctl.spin_limit_ns)) return false;
+    const bool ok = wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns) &&
+                    (tile < 2 || wait_tile(s.done, tile - 2, 2, p.ctl.spin_limit_ns));
     if (works) {
 #pragma unroll
       for (int t = vt; t < kTokens; t += VT) {
@@ -284,7 +351,7 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
       }
       store8<float>((is_c ? &s.fc[kPiece ? 0 : buf][0][0] : &s.fb[buf][0][0]) + e, true, 8, f);
     }
-    __syncwarp();
+    if (!all_lanes(ok)) return false;
     if ((threadIdx.x & 31) == 0) {
       mbar_arrive(&s.full[buf]);
       if (kPiece) mbar_arrive(&s.raw_free[ring]);
@@ -293,8 +360,18 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
   return true;
 }
 
+// Lets the chain's next item go, once the scan has left the state for it.  The finish role.
+template <typename S>
+__device__ __forceinline__ bool publish(const Params& p, const Item& it, S& s, uint32_t k) {
+  if (it.sub + 1 >= p.sp.subs) return true;
+  if (!wait_tile(s.item_done, k, 4, p.ctl.spin_limit_ns)) return false;
+  if (threadIdx.x == kScanThreads + 2 * kRoleThreads && it.id != p.ctl.stall_tile)
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&p.done[it.chain]), "r"((uint32_t)it.sub + 1) : "memory");
+  return true;
+}
+
 template <typename T, int N>
-__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false>& s, uint32_t tile) {
+__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false>& s, uint32_t tile, uint32_t k) {
   using S = Shared<T, N, false>;
   constexpr int CT = S::CT;
   const ssm_selscan_args& a = p.a;
@@ -305,12 +382,13 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
   T* yp = static_cast<T*>(a.y) + (it.b * a.seqlen + it.t_begin) * a.channels + it.c0 + vc;
   T* y_item = yp + (int64_t)vt * a.channels;
   float skip[8];
-  load_states(&s.skip[vc], skip);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) skip[j] = a.D && vc + j < it.cn ? __ldg(a.D + it.c0 + vc + j) : 0.f;
   for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
     const int ring = tile % kRing, buf = tile & 1;
-    if (!wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns) || !wait_tile(s.done, tile, 2, p.ctl.spin_limit_ns))
-      return false;
-    if (works) {
+    bool ok = wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns) && wait_tile(s.done, tile, 2, p.ctl.spin_limit_ns);
+    if (rows <= kTokens) ok = ok && publish(p, it, s, k);
+    if (works && ok) {
 #pragma unroll
       for (int t = vt; t < kTokens; t += VT) {
         if (t < rows) {
@@ -332,14 +410,15 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
           store8<T>(y_item + (int64_t)(t - vt) * a.channels, vec_y, valid, y);
         }
       }
-      y_item += (int64_t)kTokens * a.channels;
     }
-    __syncwarp();
+    y_item += (int64_t)kTokens * a.channels;
+    if (!all_lanes(ok)) return false;
     if ((threadIdx.x & 31) == 0) {
       mbar_arrive(&s.y_free[buf]);
       mbar_arrive(&s.raw_free[ring]);
     }
   }
+  if (it.live == 0 && !all_lanes(publish(p, it, s, k))) return false;
   if (works) {  // padding
     const float zero[8] = {};
     for (int t = it.live + vt; t < it.n; t += VT) store8<T>(yp + (int64_t)t * a.channels, vec_y, valid, zero);
@@ -360,8 +439,8 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Share
   pair += (threadIdx.x >> 5) * LW;
   for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
     const int buf = tile & 1;
-    if (!wait_tile(s.full, tile, 2, p.ctl.spin_limit_ns)) return false;
-    if (!kPiece && tile >= 2 && !wait_tile(s.y_free, tile - 2, 2, p.ctl.spin_limit_ns)) return false;
+    const bool ok = wait_tile(s.full, tile, 2, p.ctl.spin_limit_ns) &&
+                    (kPiece || tile < 2 || wait_tile(s.y_free, tile - 2, 2, p.ctl.spin_limit_ns));
     const float* b_row = &s.fb[buf][0][sub * kSpl];
     const float* c_row = &s.fc[kPiece ? 0 : buf][0][sub * kSpl];
     const float4* d_row = &s.d[buf][0][pair ^ (pair >> 3 & 3)];
@@ -415,7 +494,7 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Share
         for (int j = 0; j < kBlock >> ROUNDS; ++j) *reinterpret_cast<float2*>(y_row + (t + (j << ROUNDS)) * CT) = part[j];
       }
     }
-    __syncwarp();
+    if (!all_lanes(ok)) return false;
     if (lane == 0) mbar_arrive(&s.done[buf]);
   }
   return true;
@@ -426,7 +505,7 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Share
 template <typename T, int N, bool kPiece>
 __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shared<T, N, kPiece>;
-  constexpr int CT = S::CT, LW = 32 / S::LPC;
+  constexpr int LW = 32 / S::LPC;
   extern __shared__ __align__(128) unsigned char smem[];
   S& s = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x;
@@ -439,124 +518,133 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
       mbar_init(&s.full[i], kRoleThreads / 32);
       mbar_init(&s.done[i], kScanThreads / 32);
       mbar_init(&s.y_free[i], kRoleThreads / 32);
+      mbar_init(&s.item_full[i], 1);
+      // warps that read it; with tensor copies the copy role is the one thread that wrote it
+      mbar_init(&s.item_free[i], (kThreads - kRoleThreads * (p.vec ? 1 : 0)) / 32);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&s.item_done[i], kScanThreads / 32);
     fence_mbar_init();
   }
   griddep_launch_dependents();
   griddep_wait();
+  __syncthreads();
   const ssm_selscan_args& a = p.a;
-  const bool scans = tid < kScanThreads;
-  int sub, cl;  // of a scan thread: its place in a channel's entries, its first channel
+  // Each role goes through the CTA's items by itself, so the copies of an item come in beside the
+  // scan of the one before.  Without a queue there is one item.
+  uint32_t tile0 = 0;
+  if (tid >= kScanThreads) {
+    const int role = (tid - kScanThreads) / kRoleThreads;
+    const bool claims = tid == kScanThreads;
+    if (role == 0 && p.vec && !claims) return;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      Item it;
+      if (claims) ok = claim_item<T, N, kPiece>(p, s, k, it);
+      if (role != 0 || !p.vec) {
+        __syncwarp();
+        ok = next_item(p, s, k, it) && ok;
+      }
+      if (!ok || it.n < 0) break;
+      const uint32_t tile = tile0;
+      tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
+      if (role == 0)
+        ok = copy_role<T, N, kPiece>(p, maps, it, s, tile);
+      else if (role == 1)
+        ok = prepare_role<T, N, kPiece>(p, it, s, tile);
+      else if constexpr (!kPiece)
+        ok = finish_role<T, N>(p, it, s, tile, k);
+      if (kPiece || !p.queue) break;
+    }
+    if (role == 0 && p.vec)  // shared memory stays until the copies are there, whatever the other roles do
+      for (uint32_t t = tile0 < kRing ? 0 : tile0 - kRing; t < tile0; ++t)
+        ok = wait_tile(s.raw_full, t, kRing, p.ctl.spin_limit_ns) && ok;
+    if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+    return;
+  }
+
+  int sub, cl;  // a scan thread's place in a channel's entries, and its first channel
   lane_of<S::LPC>(tid & 31, sub, cl);
   cl = 2 * (cl + (tid >> 5) * LW);
-  const int split = kPiece ? p.sp.split - 1 : p.sp.split;  // nothing starts from the last part's end
-  const int64_t chains = a.batch * p.sp.tiles * split;
-  const int64_t items = chains * (kPiece ? 1 : p.sp.subs);
-  uint32_t tile0 = 0;
-
-  for (int64_t item = blockIdx.x;;) {
-    __syncthreads();  // the last item's shared memory is read
-    if (!kPiece && p.queue) {
-      if (tid == 0) s.item = atomicAdd(&p.queue->counter, 1u);
-      __syncthreads();
-      item = s.item;
+  for (uint32_t k = 0;; ++k) {
+    Item it;
+    bool ok = next_item(p, s, k, it);
+    if (!ok || it.n < 0) {
+      if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+      return;
     }
-    if (item >= items) return;
-    const Item it = item_of<CT, kPiece>(p, item, split, chains);
-    for (int i = tid; i < CT; i += kThreads) {
-      s.bias[i] = a.dt_bias && i < it.cn ? a.dt_bias[it.c0 + i] : 0.f;
-      s.skip[i] = !kPiece && a.D && i < it.cn ? a.D[it.c0 + i] : 0.f;
+    float A[2][kSpl], h[2][kSpl], delta_sum[2] = {};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
+#pragma unroll
+      for (int i = 0; i < kSpl; ++i) {
+        A[c][i] = a.A[chan * N + sub * kSpl + i] * kLog2e;
+        h[c][i] = 0.f;
+      }
     }
-    bool ok = true;
-    if (!kPiece && it.sub > 0 && tid == 0)  // the chain's last item has left its state
-      ok = wait_done(&p.done[it.chain], (uint32_t)it.sub, p.queue, p.ctl.spin_limit_ns);
-    ok = __syncthreads_and(ok);
-
-    if (!scans) {
-      const int role = (tid - kScanThreads) / kRoleThreads;
-      if (role == 0)
-        ok = copy_role<T, N, kPiece>(p, maps, it, s, tile0);
-      else if (role == 1)
-        ok = prepare_role<T, N, kPiece>(p, it, s, tile0);
-      else if constexpr (!kPiece)
-        ok = finish_role<T, N>(p, it, s, tile0);
-    } else {
-      float A[2][kSpl], h[2][kSpl], delta_sum[2] = {};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
-#pragma unroll
-        for (int i = 0; i < kSpl; ++i) {
-          A[c][i] = a.A[chan * N + sub * kSpl + i] * kLog2e;
-          h[c][i] = 0.f;
-        }
-      }
-      float4* hand = reinterpret_cast<float4*>(p.hand) + (it.chain * kScanThreads + tid) * 2;
-      if constexpr (!kPiece) {
-        if (it.sub > 0) {
-          const float4 v = __ldcg(hand), w = __ldcg(hand + 1);
-          h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
-          h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
-          if (!ok) {  // never but on a GPU that stopped: an output that cannot pass for one
-#pragma unroll
-            for (int i = 0; i < kSpl; ++i) h[0][i] = h[1][i] = __int_as_float(0x7fffffff);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
-            if (a.h0) {
-#pragma unroll
-              for (int i = 0; i < kSpl; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * kSpl + i];
-            }
-#pragma unroll 4
-            for (int j = 0; j < it.part; ++j) {  // the state that the parts before this one leave
-              const int64_t row = ((int64_t)j * a.batch + it.b) * a.channels + chan;
-              float e[kSpl], v[kSpl];
-              mul_n(A[c], p.T[row], e);
-#pragma unroll
-              for (int i = 0; i < kSpl; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * kSpl + i];
-              fma_n(e, h[c], v);
-#pragma unroll
-              for (int i = 0; i < kSpl; ++i) h[c][i] = v[i];
-            }
-          }
-        }
-      }
-      ok = scan_role<T, N, kPiece>(p, it, s, tile0, A, h, delta_sum);
-      if (!kPiece && it.sub + 1 < p.sp.subs) {
-        hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
-        hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+    float4* hand = reinterpret_cast<float4*>(p.hand) + (it.chain * kScanThreads + tid) * 2;
+    if constexpr (!kPiece) {
+      if (it.sub > 0) {
+        if ((tid & 31) == 0 && !it.ready)
+          ok = wait_done(&p.done[it.chain], (uint32_t)it.sub, p.queue, p.ctl.spin_limit_ns);
+        ok = all_lanes(ok);
+        const float4 v = load_hand(hand), w = load_hand(hand + 1);
+        h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
+        h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
+        if (!ok) set_nan(h);
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (cl + c >= it.cn) continue;
-          const int64_t chan = it.c0 + cl + c;
-          float* out = nullptr;
-          if constexpr (kPiece) {
-            const int64_t row = ((int64_t)it.part * a.batch + it.b) * a.channels + chan;
-            if (sub == 0) p.T[row] = delta_sum[c];
-            out = p.E + row * N;
-          } else if (a.h_final && it.part == split - 1) {
-            out = a.h_final + (it.b * a.channels + chan) * N;
-          }
-          if (out) {
+          const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
+          if (a.h0) {
 #pragma unroll
-            for (int i = 0; i < kSpl; ++i) out[sub * kSpl + i] = h[c][i];
+            for (int i = 0; i < kSpl; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * kSpl + i];
+          }
+#pragma unroll 4
+          for (int j = 0; j < it.part; ++j) {  // the state that the parts before this one leave
+            const int64_t row = ((int64_t)j * a.batch + it.b) * a.channels + chan;
+            float e[kSpl], v[kSpl];
+            mul_n(A[c], p.T[row], e);
+#pragma unroll
+            for (int i = 0; i < kSpl; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * kSpl + i];
+            fma_n(e, h[c], v);
+#pragma unroll
+            for (int i = 0; i < kSpl; ++i) h[c][i] = v[i];
           }
         }
       }
     }
-    if (!__syncthreads_and(ok)) {  // a wait inside the CTA ran out
-      if (p.queue && tid == 0) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
-      return;
+    ok = scan_role<T, N, kPiece>(p, it, s, tile0, A, h, delta_sum) && ok;
+    if (!ok) set_nan(h);
+    tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
+    if (!kPiece && it.sub + 1 < p.sp.subs) {
+      hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+      hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (cl + c >= it.cn) continue;
+        const int64_t chan = it.c0 + cl + c;
+        float* out = nullptr;
+        if constexpr (kPiece) {
+          const int64_t row = ((int64_t)it.part * a.batch + it.b) * a.channels + chan;
+          if (sub == 0) p.T[row] = delta_sum[c];
+          out = p.E + row * N;
+        } else if (a.h_final && it.part == p.sp.split - 1) {
+          out = a.h_final + (it.b * a.channels + chan) * N;
+        }
+        if (out) {
+#pragma unroll
+          for (int i = 0; i < kSpl; ++i) out[sub * kSpl + i] = h[c][i];
+        }
+      }
     }
     if (kPiece || !p.queue) return;
-    if (it.sub + 1 < p.sp.subs && tid == 0 && item != p.ctl.stall_tile) {
-      __threadfence();
-      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&p.done[it.chain]), "r"((uint32_t)it.sub + 1) : "memory");
+    if (!all_lanes(ok)) {  // the other roles' waits, and those of the chain's later items, run out
+      record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+      return;
     }
-    tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
+    if ((tid & 31) == 0) mbar_arrive(&s.item_done[k & 3]);
   }
 }
 
@@ -667,20 +755,26 @@ cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
 
 }  // namespace
 
-// The time axis is split where the chains are less than 9/20 of the resident CTAs, into as many parts
-// as fill them (b1 L8192 d5120, 80 chains: 656 us in one part, 362 in four; b4, 320 chains: 823 in
-// one, more in two: the first kernel does 0.7 of the work of the second once more).  Chains that are
-// more than the resident CTAs but few of their waves go through the queue in items of kSubTokens tokens,
-// so that the last wave is short (b4 L8192 d5120: 823 us, without 1300).
+// The time axis is split where the chains are less than 3/5 of the resident CTAs, into as many parts as
+// fill them; from half of them on into four, as two leave half of the GPU to the first kernel (d5120
+// L8192, in one / two / four parts: 80 chains 628 / 523 / 342 us, 160 chains 696 / 663 / 624; 240 chains
+// L4096: 352 / 417 / 449, as the first kernel does 0.7 of the second's work once more).  That pays from
+// 24 tiles of tokens on (24 chains, L256: 17 us in one part, 19 in four; L384: 24, 20), in four from 128
+// (160 chains, L1024: 92, 103; L2048: 178, 175).
+// Chains that are more than the resident CTAs but few of their waves go through the queue in items of
+// kSubTokens tokens, so that the last wave is short (b4 L8192 d5120: 770 us, without 1300; items of 256
+// or 1024 tokens 776, 785; from eight waves on 1428 us either way).
 SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
   const int ct = tile_channels(dstate);
   const int64_t group_channels = channels / ngroups;
   SelscanSplit sp{1, 1, seqlen, seqlen, ngroups * ((group_channels + ct - 1) / ct), 0};
   const int64_t chains = sp.tiles * batch, time_tiles = (seqlen + kTokens - 1) / kTokens;
   const int64_t slots = (int64_t)kSmCount * kResident;
-  int64_t want = chains > 0 && 20 * chains < 9 * slots ? (slots * 15 / 16 + chains - 1) / chains : 1;
+  const bool few = 2 * chains < slots;
+  int64_t want = 1;
+  if (chains > 0 && 5 * chains < 3 * slots && time_tiles >= (few ? 24 : 128)) want = few ? (slots + chains - 1) / chains : 4;
   if (want > kMaxSplit) want = kMaxSplit;
-  if (want > time_tiles / 8) want = time_tiles / 8;
+  if (want > time_tiles / 4) want = time_tiles / 4;
   if (want > 1) {
     const int64_t each = (time_tiles + want - 1) / want;
     sp.split = (int)((time_tiles + each - 1) / each);
@@ -688,9 +782,9 @@ SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dsta
   }
   sp.sub_tokens = sp.part_tokens;
   const int64_t all = chains * sp.split;
-  if (all > slots && all < 8 * slots && sp.part_tokens >= 2 * kSubTokens) {
-    sp.sub_tokens = kSubTokens;
-    sp.subs = (int)((sp.part_tokens + kSubTokens - 1) / kSubTokens);
+  if (all > slots && all < 8 * slots && sp.part_tokens >= kSubTokens) {
+    sp.sub_tokens = sp.part_tokens < 2 * kSubTokens ? kSubTokens / 2 : kSubTokens;
+    sp.subs = (int)((sp.part_tokens + sp.sub_tokens - 1) / sp.sub_tokens);
   }
   sp.bytes = layout(sp, batch, channels, dstate).total;
   return sp;

@@ -6,7 +6,7 @@
 // A lane holds four state entries of a channel; the N / 4 lanes of a channel sit side by side, so a
 // warp's access covers 512 consecutive bytes of a state.  state_out may be state_in: each entry is
 // read and then written by one lane.  With sequences enough a thread takes kStepRows of them, whose
-// states it loads before it uses the first, with one load of its part of A (b256 d5120 N16: 33 us with
+// states it loads before it uses the first, with one load of its part of A (b256 d5120 N16: 32 us with
 // four, 38 with two or eight, 54 with one; eight CTAs an SM, 8 % less time than five).
 #include "layer_common.cuh"
 

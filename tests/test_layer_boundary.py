@@ -137,6 +137,20 @@ def test_rmsnorm_refusals(lib):
     assert norm(lib, True, scale=None) == INVALID and norm(lib, True, scale=FAR + 4) == INVALID
 
 
+def test_size_limits(lib):
+    """Sizes whose columns or items no longer fit the kernels' 32-bit indexes are refused."""
+    wide = (1 << 30) + 1
+    assert conv(lib, d=wide) == UNSUPPORTED and conv(lib, True, L=2, d=wide) == UNSUPPORTED
+    for step in (False, True):
+        assert scan(lib, step, channels=wide) == UNSUPPORTED
+        assert scan(lib, step, channels=(1 << 26) + 1) == UNSUPPORTED      # channels * dstate
+    assert lib.ssm_selscan_fwd_workspace_bytes(1, 8, (1 << 26) + 1, 16, 1) == 0
+    assert norm(lib, d=wide) == UNSUPPORTED and norm(lib, True, d=wide) == UNSUPPORTED
+    # 65535 sequences of 2^20 channel tiles
+    far = dict(y=1 << 50, h_final=1 << 58, dstate=64, channels=1 << 24, batch=65535, seqlen=1, bs=0)
+    assert scan(lib, **far) == UNSUPPORTED
+
+
 def test_struct_layout():
     """The ctypes views have the C structs' sizes and offsets (natural alignment, no padding)."""
     assert ctypes.sizeof(SsmTokens) == 24
