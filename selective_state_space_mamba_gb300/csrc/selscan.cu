@@ -525,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
     for (int i = 0; i < 4; ++i) mbar_init(&s.item_done[i], kScanThreads / 32);
     fence_mbar_init();
   }
-  griddep_launch_dependents();
   griddep_wait();
   __syncthreads();
   const ssm_selscan_args& a = p.a;
@@ -555,6 +554,9 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
         ok = finish_role<T, N>(p, it, s, tile, k);
       if (kPiece || !p.queue) break;
     }
+    // The next kernel's CTAs may come now.  Earlier, they would wait in places of this kernel's, two of
+    // which then share an SM beside empty ones (160 chains, L8192: 696 us instead of 448).
+    if (claims) griddep_launch_dependents();
     if (role == 0 && p.vec)  // shared memory stays until the copies are there, whatever the other roles do
       for (uint32_t t = tile0 < kRing ? 0 : tile0 - kRing; t < tile0; ++t)
         ok = wait_tile(s.raw_full, t, kRing, p.ctl.spin_limit_ns) && ok;
@@ -740,8 +742,7 @@ cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
   return with_dstate(a.dstate, [&](auto n) {
     constexpr int N = decltype(n)::value;
     int64_t grid = a.batch * sp.tiles * (kPiece ? sp.split - 1 : sp.split);
-    const int64_t slots = (int64_t)kSmCount * kResident;
-    if (!kPiece && p.queue) grid = grid * sp.subs < slots ? grid * sp.subs : slots;
+    if (!kPiece && p.queue) grid = sp.ctas;
     const auto go = [&](auto kernel, size_t bytes) {
       const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes);
       if (e != cudaSuccess) return e;
@@ -755,24 +756,31 @@ cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
 
 }  // namespace
 
-// The time axis is split where the chains are less than 3/5 of the resident CTAs, into as many parts as
-// fill them; from half of them on into four, as two leave half of the GPU to the first kernel (d5120
-// L8192, in one / two / four parts: 80 chains 628 / 523 / 342 us, 160 chains 696 / 663 / 624; 240 chains
-// L4096: 352 / 417 / 449, as the first kernel does 0.7 of the second's work once more).  That pays from
-// 24 tiles of tokens on (24 chains, L256: 17 us in one part, 19 in four; L384: 24, 20), in four from 128
-// (160 chains, L1024: 92, 103; L2048: 178, 175).
-// Chains that are more than the resident CTAs but few of their waves go through the queue in items of
-// kSubTokens tokens, so that the last wave is short (b4 L8192 d5120: 770 us, without 1300; items of 256
-// or 1024 tokens 776, 785; from eight waves on 1428 us either way).
+// A CTA alone on its SM takes 113 cycles a token, two 177 together.  All times below: d5120 or the like,
+// N16, bf16.
+//
+// The time axis is split where the chains are less than a third of the resident CTAs and the sequence is
+// long enough, into as many parts as fill them; the first kernel does 0.7 of the second's work once more
+// (80 chains: L8192 344 us in four parts, 428 in one, L2048 99 and 110, L1024 63 and 57; 24 chains: L384
+// 20 and 24, L256 19 and 17; 110 chains L4096: 236 in three parts, 217 in one).  Parts too short for the
+// queue are as many as run at once (50 chains L1024: 38 us in six parts, 48 in seven).
+//
+// A queue of items of kSubTokens tokens serves chains that are more than the resident CTAs but few of
+// their waves, so that the last wave is short (320 chains L8192: 770 us, without 1300; items of 256 or
+// 1024 tokens 776, 785; from eight waves on 1428 us either way), and chains that are a little more than
+// the SMs: with a CTA an SM they share the SMs alike (160 chains L8192: 498 us, without 695; 180 chains
+// L4096: 285, 351; 240 chains L4096 365, 351).
 SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
   const int ct = tile_channels(dstate);
   const int64_t group_channels = channels / ngroups;
-  SelscanSplit sp{1, 1, seqlen, seqlen, ngroups * ((group_channels + ct - 1) / ct), 0};
+  SelscanSplit sp{1, 1, 0, seqlen, seqlen, ngroups * ((group_channels + ct - 1) / ct), 0};
   const int64_t chains = sp.tiles * batch, time_tiles = (seqlen + kTokens - 1) / kTokens;
   const int64_t slots = (int64_t)kSmCount * kResident;
-  const bool few = 2 * chains < slots;
   int64_t want = 1;
-  if (chains > 0 && 5 * chains < 3 * slots && time_tiles >= (few ? 24 : 128)) want = few ? (slots + chains - 1) / chains : 4;
+  if (chains > 0 && time_tiles * (slots / 3 - chains) > 1600) {
+    want = (slots + chains - 1) / chains;
+    if (seqlen < want * kSubTokens) want = slots / chains;
+  }
   if (want > kMaxSplit) want = kMaxSplit;
   if (want > time_tiles / 4) want = time_tiles / 4;
   if (want > 1) {
@@ -782,7 +790,9 @@ SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dsta
   }
   sp.sub_tokens = sp.part_tokens;
   const int64_t all = chains * sp.split;
-  if (all > slots && all < 8 * slots && sp.part_tokens >= kSubTokens) {
+  const bool one = all <= slots * 3 / 4;  // CTA an SM
+  if (all > kSmCount && (one ? sp.part_tokens >= 2 * kSubTokens : all > slots && all < 8 * slots && sp.part_tokens >= kSubTokens)) {
+    sp.ctas = one ? kSmCount : slots;
     sp.sub_tokens = sp.part_tokens < 2 * kSubTokens ? kSubTokens / 2 : kSubTokens;
     sp.subs = (int)((sp.part_tokens + sp.sub_tokens - 1) / sp.sub_tokens);
   }

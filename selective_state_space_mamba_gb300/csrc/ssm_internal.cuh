@@ -444,6 +444,7 @@ cudaError_t launch_conv_step(const ssm_tokens& x, const float* w, const float* b
 struct SelscanSplit {
   int split;            // parts of the time axis that run at once (1: not split)
   int subs;             // items of a part, one after the other, that the CTAs claim from a queue (1: no queue)
+  int ctas;             // with a queue: CTAs that claim them
   int64_t part_tokens;  // tokens of a part (the last may be shorter)
   int64_t sub_tokens;   // tokens of an item (likewise)
   int64_t tiles;        // channel tiles of one sequence
