@@ -2,15 +2,16 @@
 // as e4m3 codes with f32 scales.  Each element is read once and written once: memory-bound (a few
 // rows: launch-bound).
 //
-// One CTA a row.  A thread owns vectors of eight consecutive columns, tid + k * threads; the eight
-// columns of 16 neighbouring lanes are a scale group of 128.  r of a thread's first HOLD vectors stays
-// in registers between the sum of squares and the output.
-//   Many aligned rows: up to five vectors a thread, so that a CTA has few warps to join in its sums
+// One CTA a row.  A thread owns vectors of eight columns, tid + k * threads: consecutive columns where
+// rows are aligned, so that the columns of 16 neighbouring lanes are a scale group of 128; else every
+// 32nd of the warp's 256, so that its lanes still access neighbouring elements (odd rows of 2561 bf16,
+// 8 bits, 16384 of them: 82 us, with consecutive columns 224; 2560 columns: 48).  r of a thread's first
+// HOLD vectors stays in registers between the sum of squares and the output.
+//   Many rows: up to five vectors a thread, so that a CTA has few warps to join in its sums
 //       and many CTAs are resident; a row's loads are all in flight at once.  32768 x 2560, bf16
 //       residual, 8 bits: 88 us, the rate of a copy; one vector a thread 182 us, CTAs that walk
 //       the rows and load the next one ahead 120 us (their registers leave half the CTAs).
-//   Few rows, or rows that are not aligned: one vector a thread for up to 8192 columns, the
-//       shortest way through a single row.
+//   Few rows: one vector a thread for up to 8192 columns, the shortest way through a single row.
 // What a thread does not hold of wider rows is read again.  No output is written before the last
 // read of its element, so residual_out may be residual.
 #include "layer_common.cuh"
@@ -92,21 +93,52 @@ template <typename T> struct Raw8 {
   }
 };
 
+// Vectors of a row, and the columns of one: consecutive or 32 apart, from first_column on.
+template <bool kVec>
+__host__ __device__ __forceinline__ int vectors(int width) {
+  return kVec ? (width + 7) / 8 : (width + 255) / 256 * 32;
+}
+template <bool kVec>
+__device__ __forceinline__ int first_column(int i) {
+  return kVec ? 8 * i : (i >> 5) * 256 + (i & 31);
+}
+
+// The columns from c on of a row of `width`; zeros past its end.
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_columns(const T* row, int c, int width, float (&v)[8]) {
+  if constexpr (kVec) {
+    load8<T>(row + c, true, 8, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + 32 * j < width ? to_f32(row[c + 32 * j]) : 0.f;
+  }
+}
+template <bool kVec, typename T>
+__device__ __forceinline__ void store_columns(T* row, int c, int width, const float (&v)[8]) {
+  if constexpr (kVec) {
+    store8<T>(row + c, true, 8, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + 32 * j < width) row[c + 32 * j] = from_f32<T>(v[j]);
+  }
+}
+
 // r = x + residual of vector i of a row
 template <typename T, typename R, bool kRes, bool kVec>
 __device__ __forceinline__ void load_r(const NormParams& p, int64_t row, int i, float (&v)[8]) {
-  const int c = 8 * i, valid = p.width - c;
-  load8<T>(static_cast<const T*>(p.x) + row * p.x_stride + c, kVec, valid, v);
+  const int c = first_column<kVec>(i);
+  load_columns<kVec>(static_cast<const T*>(p.x) + row * p.x_stride, c, p.width, v);
   if constexpr (kRes) {
     float r[8];
-    load8<R>(static_cast<const R*>(p.residual) + row * p.width + c, kVec, valid, r);
+    load_columns<kVec>(static_cast<const R*>(p.residual) + row * p.width, c, p.width, r);
     add_n(v, r, v);
   }
 }
 template <bool kVec>
 __device__ __forceinline__ void normed(const NormParams& p, int i, const float (&r)[8], float rstd, float (&v)[8]) {
   float w[8];
-  load8<float>(p.weight + 8 * i, kVec, p.width - 8 * i, w);
+  load_columns<kVec>(p.weight, first_column<kVec>(i), p.width, w);
   mul_n(r, rstd, v);
   mul_n(v, w, v);
 }
@@ -125,30 +157,47 @@ __device__ __forceinline__ void add_squares(const float (&v)[8], float (&sum)[2]
 }
 
 // Writes vector i of a row: residual_out, and y or q.  All lanes of a warp take part (the scale of
-// a group is a reduction over 16 lanes); `have`: this one has a vector.
+// a group is a reduction over lanes); `have`: this one has a vector.
 template <typename T, typename R, bool kRes, bool kFp8, bool kVec>
 __device__ __forceinline__ void output(const NormParams& p, int64_t row, int i, bool have, const float (&r)[8],
                                        float rstd, float row_scale) {
-  const int c = 8 * i, valid = p.width - c;
+  const int c = first_column<kVec>(i);
   float v[8] = {};
   if (have) {
     normed<kVec>(p, i, r, rstd, v);
     if constexpr (kRes)
-      if (p.residual_out) store8<R>(static_cast<R*>(p.residual_out) + row * p.width + c, kVec, valid, r);
+      if (p.residual_out) store_columns<kVec>(static_cast<R*>(p.residual_out) + row * p.width, c, p.width, r);
   }
   if constexpr (!kFp8) {
-    if (have) store8<T>(static_cast<T*>(p.y) + row * p.width + c, kVec, valid, v);
+    if (have) store_columns<kVec>(static_cast<T*>(p.y) + row * p.width, c, p.width, v);
   } else {
-    float scale = row_scale;
+    float scale[2] = {row_scale, row_scale};  // of the first and the last four columns
     if (p.group) {
-      float m = max8(v, 0.f);
+      const int groups = (p.width + 127) / 128;
+      float* out = p.scale + row * groups;
+      if constexpr (kVec) {
+        float m = max8(v, 0.f);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      scale = scale_of(m);
-      if (have && (i & 15) == 0) p.scale[row * ((p.width + 127) / 128) + i / 16] = scale;
+        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        scale[0] = scale[1] = scale_of(m);
+        if (have && (i & 15) == 0) out[i / 16] = scale[0];
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float m = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) m = max_nan(m, fabsf(v[4 * h + j]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+          scale[h] = scale_of(m);
+          if (have && (i & 31) == 0 && i / 16 + h < groups) out[i / 16 + h] = scale[h];
+        }
+      }
     }
     if (have) {
-      mul_n(v, rcp_fast(scale), v);
+      const float s0 = rcp_fast(scale[0]), s1 = rcp_fast(scale[1]);
+      const float inv[8] = {s0, s0, s0, s0, s1, s1, s1, s1};
+      mul_n(v, inv, v);
       uint32_t u[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -163,7 +212,7 @@ __device__ __forceinline__ void output(const NormParams& p, int64_t row, int i, 
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j < valid) qp[j] = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
+          if (c + 32 * j < p.width) qp[32 * j] = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
       }
     }
   }
@@ -180,11 +229,18 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
   __shared__ float max_part[32];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, threads = blockDim.x;
-  const int nvec = (p.width + 7) / 8;
+  const int nvec = vectors<kVec>(p.width);
   const int first = HOLD > 1 ? nvec : tid + threads;  // this thread's first vector that it does not hold
   float held[HOLD][8];
   float sum[2] = {};
-  if constexpr (HOLD > 1) {  // all loads first
+  if constexpr (HOLD > 1 && !kVec) {
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+      if (tid + k * threads < nvec) load_r<T, R, kRes, kVec>(p, row, tid + k * threads, held[k]);
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+      if (tid + k * threads < nvec) add_squares(held[k], sum);
+  } else if constexpr (HOLD > 1) {  // all loads first
     Raw8<T> xn[HOLD];
     Raw8<R> rn[kRes ? HOLD : 1];
     const T* xp = static_cast<const T*>(p.x) + row * p.x_stride;
@@ -254,15 +310,18 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
 
 template <typename T, typename R, bool kRes, bool kFp8>
 cudaError_t launch_rows(const NormParams& p, int64_t rows, bool vec, cudaStream_t s) {
-  const int nvec = (p.width + 7) / 8;
-  const auto go = [&](auto kernel, int hold) {
-    const int threads = ((nvec + hold - 1) / hold + 31) / 32 * 32;
-    return launch_pdl(kernel, dim3((unsigned)rows), dim3((unsigned)(threads < kNormMaxThreads ? threads : kNormMaxThreads)),
-                      0, s, p);
+  const auto with = [&](auto kvec) {
+    constexpr bool kVec = decltype(kvec)::value;
+    const int nvec = vectors<kVec>(p.width);
+    const auto go = [&](auto kernel, int hold) {
+      const int threads = ((nvec + hold - 1) / hold + 31) / 32 * 32;
+      return launch_pdl(kernel, dim3((unsigned)rows),
+                        dim3((unsigned)(threads < kNormMaxThreads ? threads : kNormMaxThreads)), 0, s, p);
+    };
+    if (rows < kManyRows || nvec <= 64 || nvec > 5 * kHoldMaxThreads) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1>, 1);
+    return nvec <= 192 ? go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3>, 3) : go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5>, 5);
   };
-  if (vec && rows >= kManyRows && nvec > 64 && nvec <= 5 * kHoldMaxThreads)
-    return nvec <= 192 ? go(rmsnorm_kernel<T, R, kRes, kFp8, true, 3>, 3) : go(rmsnorm_kernel<T, R, kRes, kFp8, true, 5>, 5);
-  return vec ? go(rmsnorm_kernel<T, R, kRes, kFp8, true, 1>, 1) : go(rmsnorm_kernel<T, R, kRes, kFp8, false, 1>, 1);
+  return vec ? with(std::true_type{}) : with(std::false_type{});
 }
 
 template <typename T, typename R, bool kRes>

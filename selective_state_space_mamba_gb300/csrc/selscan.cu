@@ -52,6 +52,7 @@ struct Params {
   float* E;          // [split - 1, batch, channels, dstate]
   float* T;          // [split - 1, batch, channels]
   bool vec;          // rows of u, dt, z, y, B and C in whole vectors of 16 bytes: tensor copies
+  bool pairs;        // else: rows of u, dt, z, B and C in whole words of 4 bytes
 };
 struct Maps {
   CUtensorMap u, dt, z, B, C;
@@ -94,6 +95,12 @@ __device__ __forceinline__ void load_y(const float* row, int vc, float (&v)[8]) 
   const int swap = vc >> 3 & 4;
   const float4 a = *reinterpret_cast<const float4*>(row + (vc ^ swap)), b = *reinterpret_cast<const float4*>(row + (vc ^ swap ^ 4));
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+__device__ __forceinline__ void store_y(float* row, int vc, const float (&v)[8]) {
+  const int swap = vc >> 3 & 4;
+  *reinterpret_cast<float4*>(row + (vc ^ swap)) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(row + (vc ^ swap ^ 4)) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // A lane's place among the LPC lanes of a channel pair and the LW pairs of a warp.  A 16-byte load takes
@@ -245,13 +252,94 @@ __device__ __forceinline__ bool claim_item(const Params& p, Shared<T, N, kPiece>
 }
 
 // The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
-template <typename T, int N, bool kPiece>
+
+// Rows that tensor copies cannot take, in words of U.  A thread has its words of two tensors of a tile (of
+// half a tile of 128 channels) in flight before it stores the first.
+template <typename T, int N, bool kPiece, typename U>
+__device__ __forceinline__ bool copy_rows(const Params& p, const Item& it, Shared<T, N, kPiece>& s, uint32_t tile) {
+  constexpr int CT = Shared<T, N, kPiece>::CT, W = sizeof(U) / sizeof(T);
+  constexpr int CW = CT / W, NW = N / W;  // words of a row
+  constexpr int HALVES = kTokens * CW / kRoleThreads > 16 ? 2 : 1, ROWS = kTokens / HALVES;
+  constexpr int PER = ROWS * CW / kRoleThreads, PER_N = (kTokens * NW + kRoleThreads - 1) / kRoleThreads;
+  const ssm_selscan_args& a = p.a;
+  const int tid = threadIdx.x % kRoleThreads;
+  const auto at = [&](const ssm_tokens& t, int64_t column) {
+    return static_cast<const T*>(t.ptr) + it.b * t.batch_stride + it.t_begin * t.token_stride + column;
+  };
+  const T *u = at(a.u, it.c0), *dt = at(a.dt, it.c0), *z = a.z.ptr ? at(a.z, it.c0) : nullptr;
+  const T *B = at(a.B, (int64_t)it.g * N), *C = at(a.C, (int64_t)it.g * N);
+  const int words = it.cn / W;
+  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
+    const int ring = tile % kRing;
+    if (!all_lanes(tile < kRing || wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns))) return false;
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const auto load = [&](const T* src, int64_t stride, U (&v)[PER]) {
+        src += (h * ROWS + tid / CW) * stride;
+        asm volatile("" : "+l"(stride));  // else the compiler keeps all rows' offsets in registers
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int w = tid + i * kRoleThreads, r = h * ROWS + w / CW, c = w % CW;
+          if (r < rows && c < words) v[i] = *reinterpret_cast<const U*>(src + c * W);
+          if ((i + 1) * kRoleThreads % CW == 0) src += (CW < kRoleThreads ? kRoleThreads / CW : 1) * stride;
+        }
+      };
+      const auto store = [&](T (*dst)[CT], const U (&v)[PER]) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int w = tid + i * kRoleThreads, r = h * ROWS + w / CW, c = w % CW;
+          *reinterpret_cast<U*>(&dst[r][c * W]) = v[i];
+        }
+      };
+      const auto load_n = [&](const T* src, int64_t stride, U (&v)[PER_N]) {
+        src += tid / NW * stride;
+        asm volatile("" : "+l"(stride));
+#pragma unroll
+        for (int i = 0; i < PER_N; ++i) {
+          const int r = (tid + i * kRoleThreads) / NW;
+          if (r < kTokens && r < rows) v[i] = *reinterpret_cast<const U*>(src + tid % NW * W);
+          src += kRoleThreads / NW * stride;
+        }
+      };
+      const auto store_n = [&](T (*dst)[N], const U (&v)[PER_N]) {
+#pragma unroll
+        for (int i = 0; i < PER_N; ++i) {
+          const int w = tid + i * kRoleThreads, r = w / NW;
+          if (r < kTokens) *reinterpret_cast<U*>(&dst[r][w % NW * W]) = v[i];
+        }
+      };
+      U v[PER] = {}, vd[PER] = {}, vb[PER_N] = {};
+      load(u, a.u.token_stride, v);
+      load(dt, a.dt.token_stride, vd);
+      if (h == 0) load_n(B, a.B.token_stride, vb);
+      store(s.u[ring], v);
+      if constexpr (!kPiece)
+        if (z) load(z, a.z.token_stride, v);
+      store(s.dt[ring], vd);
+      if (h == 0) store_n(s.b[ring], vb);
+      if constexpr (!kPiece) {
+        if (h == 0) load_n(C, a.C.token_stride, vb);
+        if (z) store(s.z[ring], v);
+        if (h == 0) store_n(s.c[ring], vb);
+      }
+    }
+    u += kTokens * a.u.token_stride;
+    dt += kTokens * a.dt.token_stride;
+    if (z) z += kTokens * a.z.token_stride;
+    B += kTokens * a.B.token_stride;
+    C += kTokens * a.C.token_stride;
+    mbar_arrive(&s.raw_full[ring]);
+  }
+  return true;
+}
+
+template <typename T, int N, bool kPiece, bool kVec>
 __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, const Item& it, Shared<T, N, kPiece>& s,
                                           uint32_t tile) {
   constexpr int CT = Shared<T, N, kPiece>::CT;
-  const ssm_selscan_args& a = p.a;
-  const int tid = threadIdx.x % kRoleThreads;
-  if (p.vec) {
+  if constexpr (kVec) {
+    const ssm_selscan_args& a = p.a;
+    const int tid = threadIdx.x % kRoleThreads;
     // One thread, five tensor copies a tile.  They bring padding too, and zeros past the tensors' ends.
     if (tid != 0) return true;
     int t = (int)it.t_begin;
@@ -271,38 +359,11 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
     }
     return true;
   }
-  const auto at = [&](const ssm_tokens& t, int64_t column) {
-    return static_cast<const T*>(t.ptr) + it.b * t.batch_stride + it.t_begin * t.token_stride + column;
-  };
-  const T *u = at(a.u, it.c0), *dt = at(a.dt, it.c0), *z = a.z.ptr ? at(a.z, it.c0) : nullptr;
-  const T *B = at(a.B, (int64_t)it.g * N), *C = at(a.C, (int64_t)it.g * N);
-  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
-    const int ring = tile % kRing, have = rows < kTokens ? rows : kTokens;
-    if (!all_lanes(tile < kRing || wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns))) return false;
-#pragma unroll 8
-    for (int i = tid; i < have * CT; i += kRoleThreads) {
-      const int r = i / CT, c = i % CT;
-      if (c < it.cn) {
-        s.u[ring][r][c] = u[r * a.u.token_stride + c];
-        s.dt[ring][r][c] = dt[r * a.dt.token_stride + c];
-        if constexpr (!kPiece)
-          if (z) s.z[ring][r][c] = z[r * a.z.token_stride + c];
-      }
-    }
-#pragma unroll 4
-    for (int i = tid; i < have * N; i += kRoleThreads) {
-      const int r = i / N, c = i % N;
-      s.b[ring][r][c] = B[r * a.B.token_stride + c];
-      if constexpr (!kPiece) s.c[ring][r][c] = C[r * a.C.token_stride + c];
-    }
-    u += kTokens * a.u.token_stride;
-    dt += kTokens * a.dt.token_stride;
-    if (z) z += kTokens * a.z.token_stride;
-    B += kTokens * a.B.token_stride;
-    C += kTokens * a.C.token_stride;
-    mbar_arrive(&s.raw_full[ring]);
+  if constexpr (!kVec) {
+    if constexpr (sizeof(T) == 2)
+      if (!p.pairs) return copy_rows<T, N, kPiece, uint16_t>(p, it, s, tile);
+    return copy_rows<T, N, kPiece, uint32_t>(p, it, s, tile);
   }
-  return true;
 }
 
 template <typename T, int N, bool kPiece>
@@ -370,7 +431,7 @@ __device__ __forceinline__ bool publish(const Params& p, const Item& it, S& s, u
   return true;
 }
 
-template <typename T, int N>
+template <typename T, int N, bool kVec>
 __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false>& s, uint32_t tile, uint32_t k) {
   using S = Shared<T, N, false>;
   constexpr int CT = S::CT;
@@ -378,9 +439,9 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
   const int tid = threadIdx.x % kRoleThreads;
   constexpr int VC = CT / 8, VT = kRoleThreads / VC < kTokens ? kRoleThreads / VC : kTokens;
   const int vt = tid / VC, vc = 8 * (tid % VC), valid = it.cn - vc;
-  const bool works = (kRoleThreads / VC <= kTokens || vt < kTokens) && valid > 0, vec_y = p.vec && valid >= 8;
+  const bool works = (kRoleThreads / VC <= kTokens || vt < kTokens) && valid > 0;
   T* yp = static_cast<T*>(a.y) + (it.b * a.seqlen + it.t_begin) * a.channels + it.c0 + vc;
-  T* y_item = yp + (int64_t)vt * a.channels;
+  T *y_item = yp + (int64_t)vt * a.channels, *y_tile = yp - vc;
   float skip[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) skip[j] = a.D && vc + j < it.cn ? __ldg(a.D + it.c0 + vc + j) : 0.f;
@@ -407,9 +468,25 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
             silu_n(z, z);
             mul_n(y, z, y);
           }
-          store8<T>(y_item + (int64_t)(t - vt) * a.channels, vec_y, valid, y);
+          if (kVec)  // then rows are whole vectors
+            store8<T>(y_item + (int64_t)(t - vt) * a.channels, true, 8, y);
+          else
+            store_y(&s.y[buf][t * CT], vc, y);
         }
       }
+    }
+    if (!kVec) {  // a warp has whole rows: through shared memory, so that its lanes write neighbouring channels
+      __syncwarp();
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int q = 0; q < 32 / VC; ++q)
+#pragma unroll
+        for (int t = (tid >> 5) * (32 / VC) + q; t < kTokens; t += VT) {
+          if (t < rows && ok)
+            for (int c = lane; c < it.cn; c += 32)
+              y_tile[(int64_t)t * a.channels + c] = from_f32<T>(s.y[buf][t * CT + (c ^ (c >> 3 & 4))]);
+        }
+      y_tile += (int64_t)kTokens * a.channels;
     }
     y_item += (int64_t)kTokens * a.channels;
     if (!all_lanes(ok)) return false;
@@ -419,9 +496,13 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
     }
   }
   if (it.live == 0 && !all_lanes(publish(p, it, s, k))) return false;
-  if (works) {  // padding
+  if (kVec) {  // padding
     const float zero[8] = {};
-    for (int t = it.live + vt; t < it.n; t += VT) store8<T>(yp + (int64_t)t * a.channels, vec_y, valid, zero);
+    if (works)
+      for (int t = it.live + vt; t < it.n; t += VT) store8<T>(yp + (int64_t)t * a.channels, true, 8, zero);
+  } else {
+    for (int t = it.live + (tid >> 5); t < it.n; t += kRoleThreads / 32)
+      for (int c = threadIdx.x & 31; c < it.cn; c += 32) yp[(int64_t)t * a.channels + c - vc] = from_f32<T>(0.f);
   }
   return true;
 }
@@ -500,9 +581,9 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Share
   return true;
 }
 
-// kPiece: the first kernel (end state and sum of delta of each part of a split time axis, from a zero
+// kVec: Params::vec.  kPiece: the first kernel (end state and sum of delta of each part of a split time axis, from a zero
 // state), else the second (outputs).
-template <typename T, int N, bool kPiece>
+template <typename T, int N, bool kPiece, bool kVec>
 __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shared<T, N, kPiece>;
   constexpr int LW = 32 / S::LPC;
@@ -511,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
   const int tid = threadIdx.x;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&s.raw_full[i], p.vec ? 1 : kRoleThreads);
+      mbar_init(&s.raw_full[i], kVec ? 1 : kRoleThreads);
       mbar_init(&s.raw_free[i], kRoleThreads / 32);
     }
     for (int i = 0; i < 2; ++i) {
@@ -520,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
       mbar_init(&s.y_free[i], kRoleThreads / 32);
       mbar_init(&s.item_full[i], 1);
       // warps that read it; with tensor copies the copy role is the one thread that wrote it
-      mbar_init(&s.item_free[i], (kThreads - kRoleThreads * (p.vec ? 1 : 0)) / 32);
+      mbar_init(&s.item_free[i], (kThreads - kRoleThreads * (kVec ? 1 : 0)) / 32);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&s.item_done[i], kScanThreads / 32);
     fence_mbar_init();
@@ -534,12 +615,12 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
   if (tid >= kScanThreads) {
     const int role = (tid - kScanThreads) / kRoleThreads;
     const bool claims = tid == kScanThreads;
-    if (role == 0 && p.vec && !claims) return;
+    if (role == 0 && kVec && !claims) return;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Item it;
       if (claims) ok = claim_item<T, N, kPiece>(p, s, k, it);
-      if (role != 0 || !p.vec) {
+      if (role != 0 || !kVec) {
         __syncwarp();
         ok = next_item(p, s, k, it) && ok;
       }
@@ -547,17 +628,17 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
       const uint32_t tile = tile0;
       tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
       if (role == 0)
-        ok = copy_role<T, N, kPiece>(p, maps, it, s, tile);
+        ok = copy_role<T, N, kPiece, kVec>(p, maps, it, s, tile);
       else if (role == 1)
         ok = prepare_role<T, N, kPiece>(p, it, s, tile);
       else if constexpr (!kPiece)
-        ok = finish_role<T, N>(p, it, s, tile, k);
+        ok = finish_role<T, N, kVec>(p, it, s, tile, k);
       if (kPiece || !p.queue) break;
     }
     // The next kernel's CTAs may come now.  Earlier, they would wait in places of this kernel's, two of
     // which then share an SM beside empty ones (160 chains, L8192: 696 us instead of 448).
     if (claims) griddep_launch_dependents();
-    if (role == 0 && p.vec)  // shared memory stays until the copies are there, whatever the other roles do
+    if (role == 0 && kVec)  // shared memory stays until the copies are there, whatever the other roles do
       for (uint32_t t = tile0 < kRing ? 0 : tile0 - kRing; t < tile0; ++t)
         ok = wait_tile(s.raw_full, t, kRing, p.ctl.spin_limit_ns) && ok;
     if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
@@ -701,6 +782,9 @@ Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
     if (t->ptr)  // (a tensor map takes no rows that lie on one another)
       p.vec = p.vec && aligned_rows(t->ptr, a.batch > 1 ? t->batch_stride : 0, a.seqlen > 1 ? t->token_stride : 0, e, 16) &&
               (a.batch == 1 || t->batch_stride > 0) && (a.seqlen == 1 || t->token_stride > 0);
+  p.pairs = a.channels / a.ngroups * e % 4 == 0;
+  for (const ssm_tokens* t : {&a.u, &a.dt, &a.z, &a.B, &a.C})
+    if (t->ptr) p.pairs = p.pairs && aligned_rows(t->ptr, t->batch_stride, t->token_stride, e, 4);
   return p;
 }
 
@@ -750,7 +834,12 @@ cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
       kernel<<<dim3((unsigned)grid), dim3(kThreads), bytes, s>>>(p, maps);
       return cudaGetLastError();
     };
-    return a.dtype == SSM_BF16 ? go(selscan_kernel<__nv_bfloat16, N, kPiece>, sizeof(Shared<__nv_bfloat16, N, kPiece>)) : go(selscan_kernel<float, N, kPiece>, sizeof(Shared<float, N, kPiece>));
+    const auto typed = [&](auto zero) {
+      using T = decltype(zero);
+      constexpr size_t bytes = sizeof(Shared<T, N, kPiece>);
+      return p.vec ? go(selscan_kernel<T, N, kPiece, true>, bytes) : go(selscan_kernel<T, N, kPiece, false>, bytes);
+    };
+    return a.dtype == SSM_BF16 ? typed(__nv_bfloat16{}) : typed(0.f);
   });
 }
 
