@@ -7,7 +7,7 @@
 //
 // A chain (channel, n) is sequential in t, so the parallelism comes from the chains.  Time goes in
 // tiles of kTokens, and a CTA's warps have four roles that run beside each other:
-//   copy     brings raw tiles to shared memory by tensor copies, up to kRing ahead
+//   copy     brings raw tiles to shared memory by tensor copies, some tiles ahead
 //   prepare  takes eight channels of one token a thread, computes delta and delta u and lays them out by
 //            channel pair; B and C become f32
 //   scan     walks the tiles.  A lane holds four state entries of two channels (lane_of).  What shared
@@ -38,7 +38,6 @@ constexpr int kBlock = 4;        // tokens between two reductions
 constexpr int kResident = 2;     // CTAs an SM
 constexpr int kSubTokens = 512;  // tokens of an item of the queue (short sequences: half of it)
 constexpr int kScanThreads = 128, kRoleThreads = 64, kThreads = kScanThreads + 3 * kRoleThreads;
-constexpr int kRing = 4;         // raw tiles in shared memory
 
 __host__ __device__ constexpr int tile_channels(int n) { return kScanThreads * kSpl * 2 / n; }
 
@@ -52,7 +51,7 @@ struct Params {
   float* E;          // [split - 1, batch, channels, dstate]
   float* T;          // [split - 1, batch, channels]
   bool vec;          // rows of u, dt, z, y, B and C in whole vectors of 16 bytes: tensor copies
-  bool pairs;        // else: rows of u, dt, z, B and C in whole words of 4 bytes
+  bool dense;        // without them: some rows are less than 16 bytes apart
 };
 struct Maps {
   CUtensorMap u, dt, z, B, C;
@@ -67,25 +66,27 @@ struct Item {
 };
 
 // Shared memory of a CTA.
-template <typename T, int N, bool kPiece>
+template <typename T, int N, bool kPiece, bool kVec>
 struct Shared {
   static constexpr int CT = tile_channels(N);
+  static constexpr int RING = kVec || sizeof(T) == 2 ? 4 : 3;  // raw tiles: two CTAs an SM have to fit
+  static constexpr int PAD = kVec ? 0 : 16 / sizeof(T);        // a row that starts anywhere in its first 16 bytes
   static constexpr int LPC = N / kSpl;
   static constexpr int PARTS = LPC < 4 ? LPC : 4;  // partial sums of a channel
   static constexpr int YP = kTokens * CT + 16;     // floats from one to the next: 16 more, against bank conflicts
   // targets of tensor copies: 128-byte aligned
-  T u[kRing][kTokens][CT];
-  T dt[kRing][kTokens][CT];
-  T z[kPiece ? 1 : kRing][kPiece ? 8 / sizeof(T) : kTokens][CT];
-  T b[kRing][kTokens][N];
-  T c[kPiece ? 1 : kRing][kTokens][N];
+  T u[RING][kTokens][CT + PAD];
+  T dt[RING][kTokens][CT + PAD];
+  T z[kPiece ? 1 : RING][kPiece ? 8 / sizeof(T) : kTokens][CT + PAD];
+  T b[RING][kTokens][N + PAD];
+  T c[kPiece ? 1 : RING][kTokens][N + PAD];
   float fb[2][kTokens][N];
   float fc[kPiece ? 1 : 2][kTokens][N];
   float4 d[2][kTokens][CT / 2];  // (delta, delta u) of channel pair i at i ^ (i / 8 % 4), against bank conflicts
   float y[kPiece ? 1 : 2][kPiece ? 16 : PARTS * YP];  // four channels at i at i ^ (i / 8 % 2), likewise
   Item item[2];
   // phases of the tiles: raw tile there, raw tile read, prepared, scanned, y read; and of the items
-  uint64_t raw_full[kRing], raw_free[kRing], full[2], done[2], y_free[2];
+  uint64_t raw_full[RING], raw_free[RING], full[2], done[2], y_free[2];
   // and of the items: written down, read, scanned (the finish role may be two items behind the scan)
   uint64_t item_full[2], item_free[2], item_done[4];
 };
@@ -95,12 +96,6 @@ __device__ __forceinline__ void load_y(const float* row, int vc, float (&v)[8]) 
   const int swap = vc >> 3 & 4;
   const float4 a = *reinterpret_cast<const float4*>(row + (vc ^ swap)), b = *reinterpret_cast<const float4*>(row + (vc ^ swap ^ 4));
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-__device__ __forceinline__ void store_y(float* row, int vc, const float (&v)[8]) {
-  const int swap = vc >> 3 & 4;
-  *reinterpret_cast<float4*>(row + (vc ^ swap)) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(row + (vc ^ swap ^ 4)) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // A lane's place among the LPC lanes of a channel pair and the LW pairs of a warp.  A 16-byte load takes
@@ -234,8 +229,8 @@ __device__ __forceinline__ bool next_item(const Params& p, S& s, uint32_t k, Ite
 }
 
 // Claims the k-th item and writes it down for the other roles.  The first copy thread.
-template <typename T, int N, bool kPiece>
-__device__ __forceinline__ bool claim_item(const Params& p, Shared<T, N, kPiece>& s, uint32_t k, Item& it) {
+template <int N, bool kPiece, typename S>
+__device__ __forceinline__ bool claim_item(const Params& p, S& s, uint32_t k, Item& it) {
   const int split = kPiece ? p.sp.split - 1 : p.sp.split;  // nothing starts from the last part's end
   const int64_t chains = p.a.batch * p.sp.tiles * split;
   const int64_t id = !kPiece && p.queue ? (int64_t)atomicAdd(&p.queue->counter, 1u) : blockIdx.x;
@@ -253,122 +248,133 @@ __device__ __forceinline__ bool claim_item(const Params& p, Shared<T, N, kPiece>
 
 // The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
 
-// Rows that tensor copies cannot take, in words of U.  A thread has its words of two tensors of a tile (of
-// half a tile of 128 channels) in flight before it stores the first.
-template <typename T, int N, bool kPiece, typename U>
-__device__ __forceinline__ bool copy_rows(const Params& p, const Item& it, Shared<T, N, kPiece>& s, uint32_t tile) {
-  constexpr int CT = Shared<T, N, kPiece>::CT, W = sizeof(U) / sizeof(T);
-  constexpr int CW = CT / W, NW = N / W;  // words of a row
-  constexpr int HALVES = kTokens * CW / kRoleThreads > 16 ? 2 : 1, ROWS = kTokens / HALVES;
-  constexpr int PER = ROWS * CW / kRoleThreads, PER_N = (kTokens * NW + kRoleThreads - 1) / kRoleThreads;
+// Elements from the 16-byte boundary at or before the columns from `column` on of sequence b to them, at its
+// token t.  (Only the low bits count, so 32-bit arithmetic does.)
+template <typename T>
+__device__ __forceinline__ int offset_in_16(const ssm_tokens& x, int64_t b, int64_t t, int64_t column) {
+  const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(x.ptr) / sizeof(T)) + (uint32_t)column;
+  return (int)((first + (uint32_t)b * (uint32_t)x.batch_stride + (uint32_t)t * (uint32_t)x.token_stride) % (16 / sizeof(T)));
+}
+
+// Rows that tensor copies cannot take: `n` columns of consecutive tokens from t on, in asynchronous copies of
+// whole aligned 16 bytes, which leave a row at its offset_in_16.  What they bring beside the columns
+// is the tensor's too (its span has no holes that are not its row's).
+template <typename T, int COLUMNS>
+struct Rows {
+  static constexpr int E = 16 / sizeof(T), PITCH = COLUMNS + E, CHUNKS = PITCH / E;
+  static constexpr int LANES = CHUNKS <= 4 ? 4 : CHUNKS <= 8 ? 8 : CHUNKS <= 16 ? 16 : CHUNKS <= 32 ? 32 : 64;  // of a row
+  static constexpr int STEP = kRoleThreads / LANES, PASSES = kTokens / STEP;
+  uintptr_t at, step;  // address of this thread's column in its next row, and STEP rows
+  int over;            // the 16 bytes of a row that starts at more than this are in use
+
+  __device__ __forceinline__ Rows(const ssm_tokens& x, int64_t b, int64_t t, int64_t column, int n) {
+    const int tid = threadIdx.x % kRoleThreads, c = tid % LANES;
+    at = reinterpret_cast<uintptr_t>(x.ptr) + 16 * c +
+         sizeof(T) * (b * x.batch_stride + (t + tid / LANES) * x.token_stride + column);
+    step = sizeof(T) * (STEP * x.token_stride);
+    over = c < CHUNKS ? 16 * c - (int)sizeof(T) * n : 16;
+  }
+  // kTokens rows
+  __device__ __forceinline__ void copy(T (*dst)[PITCH]) {
+    const int tid = threadIdx.x % kRoleThreads;
+    const uint32_t to = smem_addr(&dst[tid / LANES][E * (tid % LANES < CHUNKS ? tid % LANES : 0)]);
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i, at += step)
+      if ((int)(at & 15) > over)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * STEP * PITCH * (int)sizeof(T)),
+                     "l"(at & ~(uintptr_t)15)
+                     : "memory");
+  }
+};
+// The same rows element by element, where 16 bytes may hold what is not the tensor's.
+template <typename T, int PITCH>
+__device__ __forceinline__ void copy_elements(const ssm_tokens& x, int64_t b, int64_t t, int64_t column, int n, int rows,
+                                              T (*dst)[PITCH]) {
+  const uint32_t offset = offset_in_16<T>(x, b, t, column);
+  const T* src = static_cast<const T*>(x.ptr) + b * x.batch_stride + t * x.token_stride + column;
+#pragma unroll 1
+  for (int i = threadIdx.x % kRoleThreads; i < rows * n; i += kRoleThreads) {
+    const int r = i / n, c = i % n;
+    dst[r][c + (offset + r * (uint32_t)x.token_stride) % (16 / (uint32_t)sizeof(T))] = src[r * x.token_stride + c];
+  }
+}
+
+// Such rows are read from shared memory by columns, where a row's offset is no matter: this column of
+// eight tokens from t on (of them all tokens of x, `row0` the first's row in shared memory).
+template <typename T, int PITCH>
+__device__ __forceinline__ void load_column8(const ssm_tokens& x, int64_t b, int64_t t, int64_t column, const T (*row0)[PITCH],
+                                             int c, float (&v)[8]) {
+  constexpr uint32_t kMask = 16 / sizeof(T) - 1;
+  const uint32_t offset = offset_in_16<T>(x, b, t, column);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = to_f32(row0[j][c + ((offset + j * (uint32_t)x.token_stride) & kMask)]);
+}
+
+template <typename T, int N, bool kPiece, bool kVec>
+__device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, const Item& it,
+                                          Shared<T, N, kPiece, kVec>& s, uint32_t tile) {
+  constexpr int CT = tile_channels(N), RING = Shared<T, N, kPiece, kVec>::RING;
   const ssm_selscan_args& a = p.a;
-  const int tid = threadIdx.x % kRoleThreads;
-  const auto at = [&](const ssm_tokens& t, int64_t column) {
-    return static_cast<const T*>(t.ptr) + it.b * t.batch_stride + it.t_begin * t.token_stride + column;
-  };
-  const T *u = at(a.u, it.c0), *dt = at(a.dt, it.c0), *z = a.z.ptr ? at(a.z, it.c0) : nullptr;
-  const T *B = at(a.B, (int64_t)it.g * N), *C = at(a.C, (int64_t)it.g * N);
-  const int words = it.cn / W;
-  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
-    const int ring = tile % kRing;
-    if (!all_lanes(tile < kRing || wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns))) return false;
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h) {
-      const auto load = [&](const T* src, int64_t stride, U (&v)[PER]) {
-        src += (h * ROWS + tid / CW) * stride;
-        asm volatile("" : "+l"(stride));  // else the compiler keeps all rows' offsets in registers
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int w = tid + i * kRoleThreads, r = h * ROWS + w / CW, c = w % CW;
-          if (r < rows && c < words) v[i] = *reinterpret_cast<const U*>(src + c * W);
-          if ((i + 1) * kRoleThreads % CW == 0) src += (CW < kRoleThreads ? kRoleThreads / CW : 1) * stride;
-        }
-      };
-      const auto store = [&](T (*dst)[CT], const U (&v)[PER]) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int w = tid + i * kRoleThreads, r = h * ROWS + w / CW, c = w % CW;
-          *reinterpret_cast<U*>(&dst[r][c * W]) = v[i];
-        }
-      };
-      const auto load_n = [&](const T* src, int64_t stride, U (&v)[PER_N]) {
-        src += tid / NW * stride;
-        asm volatile("" : "+l"(stride));
-#pragma unroll
-        for (int i = 0; i < PER_N; ++i) {
-          const int r = (tid + i * kRoleThreads) / NW;
-          if (r < kTokens && r < rows) v[i] = *reinterpret_cast<const U*>(src + tid % NW * W);
-          src += kRoleThreads / NW * stride;
-        }
-      };
-      const auto store_n = [&](T (*dst)[N], const U (&v)[PER_N]) {
-#pragma unroll
-        for (int i = 0; i < PER_N; ++i) {
-          const int w = tid + i * kRoleThreads, r = w / NW;
-          if (r < kTokens) *reinterpret_cast<U*>(&dst[r][w % NW * W]) = v[i];
-        }
-      };
-      U v[PER] = {}, vd[PER] = {}, vb[PER_N] = {};
-      load(u, a.u.token_stride, v);
-      load(dt, a.dt.token_stride, vd);
-      if (h == 0) load_n(B, a.B.token_stride, vb);
-      store(s.u[ring], v);
-      if constexpr (!kPiece)
-        if (z) load(z, a.z.token_stride, v);
-      store(s.dt[ring], vd);
-      if (h == 0) store_n(s.b[ring], vb);
+  int64_t t = it.t_begin;
+  if constexpr (kVec) {
+    const int tid = threadIdx.x % kRoleThreads;
+    // One thread, five tensor copies a tile.  They bring padding too, and zeros past the tensors' ends.
+    if (tid != 0) return true;
+    const uint32_t bytes = kTokens * sizeof(T) * (CT * (kPiece || !a.z.ptr ? 2 : 3) + N * (kPiece ? 1 : 2));
+    for (int rows = it.live; rows > 0; rows -= kTokens, t += kTokens, ++tile) {
+      const int ring = tile % RING;
+      uint64_t* bar = &s.raw_full[ring];
+      if (tile >= RING && !wait_tile(s.raw_free, tile - RING, RING, p.ctl.spin_limit_ns)) return false;
+      mbar_arrive_expect_tx(bar, bytes);
+      tc::tma_load_3d(&s.dt[ring][0][0], &maps.dt, it.c0, (int)t, (int)it.b, bar);
+      tc::tma_load_3d(&s.u[ring][0][0], &maps.u, it.c0, (int)t, (int)it.b, bar);
+      tc::tma_load_3d(&s.b[ring][0][0], &maps.B, it.g * N, (int)t, (int)it.b, bar);
       if constexpr (!kPiece) {
-        if (h == 0) load_n(C, a.C.token_stride, vb);
-        if (z) store(s.z[ring], v);
-        if (h == 0) store_n(s.c[ring], vb);
+        tc::tma_load_3d(&s.c[ring][0][0], &maps.C, it.g * N, (int)t, (int)it.b, bar);
+        if (a.z.ptr) tc::tma_load_3d(&s.z[ring][0][0], &maps.z, it.c0, (int)t, (int)it.b, bar);
       }
     }
-    u += kTokens * a.u.token_stride;
-    dt += kTokens * a.dt.token_stride;
-    if (z) z += kTokens * a.z.token_stride;
-    B += kTokens * a.B.token_stride;
-    C += kTokens * a.C.token_stride;
-    mbar_arrive(&s.raw_full[ring]);
+  } else {
+    Rows<T, CT> dt(a.dt, it.b, t, it.c0, it.cn), u(a.u, it.b, t, it.c0, it.cn);
+    Rows<T, CT> z(kPiece || !a.z.ptr ? a.u : a.z, it.b, t, it.c0, it.cn);
+    Rows<T, N> B(a.B, it.b, t, it.g * N, N), C(a.C, it.b, t, it.g * N, N);
+    for (int rows = it.live; rows > 0; rows -= kTokens, t += kTokens, ++tile) {
+      const int ring = tile % RING;
+      if (!all_lanes(tile < RING || wait_tile(s.raw_free, tile - RING, RING, p.ctl.spin_limit_ns))) return false;
+      const bool edge = p.dense || (it.b == 0 && t == 0) || (it.b == a.batch - 1 && t + kTokens >= a.seqlen);
+      if (rows < kTokens || edge) {
+        const int have = rows < kTokens ? rows : kTokens;
+        copy_elements<T>(a.dt, it.b, t, it.c0, it.cn, have, s.dt[ring]);
+        copy_elements<T>(a.u, it.b, t, it.c0, it.cn, have, s.u[ring]);
+        copy_elements<T>(a.B, it.b, t, it.g * N, N, have, s.b[ring]);
+        if constexpr (!kPiece) {
+          copy_elements<T>(a.C, it.b, t, it.g * N, N, have, s.c[ring]);
+          if (a.z.ptr) copy_elements<T>(a.z, it.b, t, it.c0, it.cn, have, s.z[ring]);
+        }
+        dt.at += dt.step * dt.PASSES, u.at += u.step * u.PASSES, z.at += z.step * z.PASSES;
+        B.at += B.step * B.PASSES, C.at += C.step * C.PASSES;
+      } else {
+        dt.copy(s.dt[ring]);
+        u.copy(s.u[ring]);
+        B.copy(s.b[ring]);
+        if constexpr (!kPiece) {
+          C.copy(s.c[ring]);
+          if (a.z.ptr) z.copy(s.z[ring]);
+        }
+      }
+      // once for the copies in flight, once for what is stored already
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&s.raw_full[ring])) : "memory");
+      mbar_arrive(&s.raw_full[ring]);
+    }
   }
   return true;
 }
 
 template <typename T, int N, bool kPiece, bool kVec>
-__device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, const Item& it, Shared<T, N, kPiece>& s,
-                                          uint32_t tile) {
-  constexpr int CT = Shared<T, N, kPiece>::CT;
-  if constexpr (kVec) {
-    const ssm_selscan_args& a = p.a;
-    const int tid = threadIdx.x % kRoleThreads;
-    // One thread, five tensor copies a tile.  They bring padding too, and zeros past the tensors' ends.
-    if (tid != 0) return true;
-    int t = (int)it.t_begin;
-    const uint32_t bytes = kTokens * sizeof(T) * (CT * (kPiece || !a.z.ptr ? 2 : 3) + N * (kPiece ? 1 : 2));
-    for (int rows = it.live; rows > 0; rows -= kTokens, t += kTokens, ++tile) {
-      const int ring = tile % kRing;
-      uint64_t* bar = &s.raw_full[ring];
-      if (tile >= kRing && !wait_tile(s.raw_free, tile - kRing, kRing, p.ctl.spin_limit_ns)) return false;
-      mbar_arrive_expect_tx(bar, bytes);
-      tc::tma_load_3d(&s.dt[ring][0][0], &maps.dt, it.c0, t, (int)it.b, bar);
-      tc::tma_load_3d(&s.u[ring][0][0], &maps.u, it.c0, t, (int)it.b, bar);
-      tc::tma_load_3d(&s.b[ring][0][0], &maps.B, it.g * N, t, (int)it.b, bar);
-      if constexpr (!kPiece) {
-        tc::tma_load_3d(&s.c[ring][0][0], &maps.C, it.g * N, t, (int)it.b, bar);
-        if (a.z.ptr) tc::tma_load_3d(&s.z[ring][0][0], &maps.z, it.c0, t, (int)it.b, bar);
-      }
-    }
-    return true;
-  }
-  if constexpr (!kVec) {
-    if constexpr (sizeof(T) == 2)
-      if (!p.pairs) return copy_rows<T, N, kPiece, uint16_t>(p, it, s, tile);
-    return copy_rows<T, N, kPiece, uint32_t>(p, it, s, tile);
-  }
-}
-
-template <typename T, int N, bool kPiece>
-__device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Shared<T, N, kPiece>& s, uint32_t tile) {
-  constexpr int CT = Shared<T, N, kPiece>::CT;
+__device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Shared<T, N, kPiece, kVec>& s, uint32_t tile) {
+  constexpr int CT = tile_channels(N), RING = Shared<T, N, kPiece, kVec>::RING;
+  const ssm_selscan_args& a = p.a;
+  int64_t t0 = it.t_begin;
   const int tid = threadIdx.x % kRoleThreads;
   // this thread's eight channels from vc on, of the tokens vt, vt + VT, ...
   constexpr int VC = CT / 8, VT = kRoleThreads / VC < kTokens ? kRoleThreads / VC : kTokens;
@@ -377,26 +383,47 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
   float bias[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) bias[j] = p.a.dt_bias && vc + j < it.cn ? __ldg(p.a.dt_bias + it.c0 + vc + j) : 0.f;
-  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
-    const int ring = tile % kRing, buf = tile & 1;
-    const bool ok = wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns) &&
+  for (int rows = it.live; rows > 0; rows -= kTokens, t0 += kTokens, ++tile) {
+    const int ring = tile % RING, buf = tile & 1;
+    const bool ok = wait_tile(s.raw_full, tile, RING, p.ctl.spin_limit_ns) &&
                     (tile < 2 || wait_tile(s.done, tile - 2, 2, p.ctl.spin_limit_ns));
-    if (works) {
+    if constexpr (kVec) {
+      if (works) {
 #pragma unroll
-      for (int t = vt; t < kTokens; t += VT) {
-        float d[8], u[8];
-        load8<T>(&s.dt[ring][t][vc], true, 8, d);
-        load8<T>(&s.u[ring][t][vc], true, 8, u);
-        add_n(d, bias, d);
-        if (p.a.softplus) softplus_n(d, d);
-        if (rows < kTokens && t >= rows) {  // padding leaves the state as it is
+        for (int t = vt; t < kTokens; t += VT) {
+          float d[8], u[8];
+          load8<T>(&s.dt[ring][t][vc], true, 8, d);
+          load8<T>(&s.u[ring][t][vc], true, 8, u);
+          add_n(d, bias, d);
+          if (a.softplus) softplus_n(d, d);
+          if (rows < kTokens && t >= rows) {  // padding leaves the state as it is
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = u[j] = 0.f;
+            for (int j = 0; j < 8; ++j) d[j] = u[j] = 0.f;
+          }
+          mul_n(u, d, u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            s.d[buf][t][(vc / 2 + q) ^ (vc >> 4 & 3)] = make_float4(d[2 * q], u[2 * q], d[2 * q + 1], u[2 * q + 1]);
         }
+      }
+    } else {
+#pragma unroll 2
+      for (int i = tid; i < CT * kTokens / 8; i += kRoleThreads) {
+        const int c = i % CT, t = i / CT * 8;
+        float d[8], u[8];
+        load_column8<T>(a.dt, it.b, t0 + t, it.c0, &s.dt[ring][t], c, d);
+        load_column8<T>(a.u, it.b, t0 + t, it.c0, &s.u[ring][t], c, u);
+        add_n(d, a.dt_bias && c < it.cn ? __ldg(a.dt_bias + it.c0 + c) : 0.f, d);
+        if (a.softplus) softplus_n(d, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (t + j >= rows) d[j] = u[j] = 0.f;
         mul_n(u, d, u);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          s.d[buf][t][(vc / 2 + q) ^ (vc >> 4 & 3)] = make_float4(d[2 * q], u[2 * q], d[2 * q + 1], u[2 * q + 1]);
+        for (int j = 0; j < 8; ++j) {
+          float2* pairs = reinterpret_cast<float2*>(s.d[buf][t + j]);
+          pairs[2 * (c / 2 ^ (c >> 4 & 3)) + c % 2] = make_float2(d[j], u[j]);
+        }
       }
     }
     constexpr int VB = kTokens * N / 8;  // vectors of eight of B, and as many of C
@@ -404,9 +431,16 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
     for (int k = tid; k < (kPiece ? VB : 2 * VB); k += kRoleThreads) {
       float f[8];
       const bool is_c = !kPiece && k >= VB;
-      const int e = 8 * (is_c ? k - VB : k);
-      load8<T>((is_c ? &s.c[kPiece ? 0 : ring][0][0] : &s.b[ring][0][0]) + e, true, 8, f);
-      if (rows < kTokens && e / N >= rows) {  // not copied: may hold anything
+      const int e = 8 * (is_c ? k - VB : k), t = e / N;
+      const T* row = is_c ? s.c[kPiece ? 0 : ring][t] : s.b[ring][t];
+      if constexpr (kVec) {
+        load8<T>(row + e % N, true, 8, f);
+      } else {
+        row += offset_in_16<T>(is_c ? a.C : a.B, it.b, t0 + t, it.g * N);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = to_f32(row[e % N + j]);
+      }
+      if (rows < kTokens && t >= rows) {  // not copied: may hold anything
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = 0.f;
       }
@@ -432,9 +466,10 @@ __device__ __forceinline__ bool publish(const Params& p, const Item& it, S& s, u
 }
 
 template <typename T, int N, bool kVec>
-__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false>& s, uint32_t tile, uint32_t k) {
-  using S = Shared<T, N, false>;
-  constexpr int CT = S::CT;
+__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false, kVec>& s, uint32_t tile, uint32_t k) {
+  using S = Shared<T, N, false, kVec>;
+  constexpr int CT = S::CT, RING = S::RING;
+  int64_t t0 = it.t_begin;
   const ssm_selscan_args& a = p.a;
   const int tid = threadIdx.x % kRoleThreads;
   constexpr int VC = CT / 8, VT = kRoleThreads / VC < kTokens ? kRoleThreads / VC : kTokens;
@@ -445,47 +480,61 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
   float skip[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) skip[j] = a.D && vc + j < it.cn ? __ldg(a.D + it.c0 + vc + j) : 0.f;
-  for (int rows = it.live; rows > 0; rows -= kTokens, ++tile) {
-    const int ring = tile % kRing, buf = tile & 1;
-    bool ok = wait_tile(s.raw_full, tile, kRing, p.ctl.spin_limit_ns) && wait_tile(s.done, tile, 2, p.ctl.spin_limit_ns);
+  for (int rows = it.live; rows > 0; rows -= kTokens, t0 += kTokens, ++tile) {
+    const int ring = tile % RING, buf = tile & 1;
+    bool ok = wait_tile(s.raw_full, tile, RING, p.ctl.spin_limit_ns) && wait_tile(s.done, tile, 2, p.ctl.spin_limit_ns);
     if (rows <= kTokens) ok = ok && publish(p, it, s, k);
-    if (works && ok) {
+    if constexpr (kVec) {
+      if (works && ok) {
 #pragma unroll
-      for (int t = vt; t < kTokens; t += VT) {
-        if (t < rows) {
-          float y[8], w[8], u[8];
-          load_y(&s.y[buf][t * CT], vc, y);
+        for (int t = vt; t < kTokens; t += VT) {
+          if (t < rows) {
+            float y[8], w[8], u[8];
+            load_y(&s.y[buf][t * CT], vc, y);
 #pragma unroll
-          for (int k = 1; k < S::PARTS; ++k) {
-            load_y(&s.y[buf][k * S::YP + t * CT], vc, w);
-            add_n(y, w, y);
-          }
-          load8<T>(&s.u[ring][t][vc], true, 8, u);
-          fma_n(skip, u, y);
-          if (a.z.ptr) {
-            float z[8];
-            load8<T>(&s.z[ring][t][vc], true, 8, z);
-            silu_n(z, z);
-            mul_n(y, z, y);
-          }
-          if (kVec)  // then rows are whole vectors
+            for (int k = 1; k < S::PARTS; ++k) {
+              load_y(&s.y[buf][k * S::YP + t * CT], vc, w);
+              add_n(y, w, y);
+            }
+            load8<T>(&s.u[ring][t][vc], true, 8, u);
+            fma_n(skip, u, y);
+            if (a.z.ptr) {
+              float z[8];
+              load8<T>(&s.z[ring][t][vc], true, 8, z);
+              silu_n(z, z);
+              mul_n(y, z, y);
+            }
             store8<T>(y_item + (int64_t)(t - vt) * a.channels, true, 8, y);
-          else
-            store_y(&s.y[buf][t * CT], vc, y);
+          }
         }
       }
-    }
-    if (!kVec) {  // a warp has whole rows: through shared memory, so that its lanes write neighbouring channels
-      __syncwarp();
-      const int lane = threadIdx.x & 31;
+    } else if (ok) {
+#pragma unroll 2
+      for (int i = tid; i < CT * kTokens / 8; i += kRoleThreads) {
+        const int c = i % CT, t = i / CT * 8;
+        if (c >= it.cn) continue;
+        float y[8], w[8], u[8], z[8];
 #pragma unroll
-      for (int q = 0; q < 32 / VC; ++q)
+        for (int j = 0; j < 8; ++j) y[j] = s.y[buf][(t + j) * CT + (c ^ (c >> 3 & 4))];
 #pragma unroll
-        for (int t = (tid >> 5) * (32 / VC) + q; t < kTokens; t += VT) {
-          if (t < rows && ok)
-            for (int c = lane; c < it.cn; c += 32)
-              y_tile[(int64_t)t * a.channels + c] = from_f32<T>(s.y[buf][t * CT + (c ^ (c >> 3 & 4))]);
+        for (int k = 1; k < S::PARTS; ++k) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = s.y[buf][k * S::YP + (t + j) * CT + (c ^ (c >> 3 & 4))];
+          add_n(y, w, y);
         }
+        load_column8<T>(a.u, it.b, t0 + t, it.c0, &s.u[ring][t], c, u);
+        const float d = a.D ? __ldg(a.D + it.c0 + c) : 0.f;
+        fma_n(u, d, y, y);
+        if (a.z.ptr) {
+          load_column8<T>(a.z, it.b, t0 + t, it.c0, &s.z[ring][t], c, z);
+          silu_n(z, z);
+          mul_n(y, z, y);
+        }
+        T* out = y_tile + (int64_t)t * a.channels + c;
+#pragma unroll
+        for (int j = 0; j < 8; ++j, out += a.channels)
+          if (t + j < rows) *out = from_f32<T>(y[j]);
+      }
       y_tile += (int64_t)kTokens * a.channels;
     }
     y_item += (int64_t)kTokens * a.channels;
@@ -508,10 +557,9 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
 }
 
 // The scan's part of an item: h of this thread's two channels through the tiles.
-template <typename T, int N, bool kPiece>
-__device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Shared<T, N, kPiece>& s, uint32_t tile,
+template <int N, bool kPiece, typename S>
+__device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s, uint32_t tile,
                                           const float (&A)[2][kSpl], float (&h)[2][kSpl], float (&delta_sum)[2]) {
-  using S = Shared<T, N, kPiece>;
   constexpr int CT = S::CT, LPC = S::LPC, LW = 32 / LPC;
   constexpr int ROUNDS = LPC <= 4 ? 0 : LPC == 8 ? 1 : 2;  // halving rounds that leave four lanes a channel pair
   const int lane = threadIdx.x & 31;
@@ -585,14 +633,14 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, Share
 // state), else the second (outputs).
 template <typename T, int N, bool kPiece, bool kVec>
 __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
-  using S = Shared<T, N, kPiece>;
+  using S = Shared<T, N, kPiece, kVec>;
   constexpr int LW = 32 / S::LPC;
   extern __shared__ __align__(128) unsigned char smem[];
   S& s = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x;
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&s.raw_full[i], kVec ? 1 : kRoleThreads);
+    for (int i = 0; i < S::RING; ++i) {
+      mbar_init(&s.raw_full[i], kVec ? 1 : 2 * kRoleThreads);
       mbar_init(&s.raw_free[i], kRoleThreads / 32);
     }
     for (int i = 0; i < 2; ++i) {
@@ -619,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Item it;
-      if (claims) ok = claim_item<T, N, kPiece>(p, s, k, it);
+      if (claims) ok = claim_item<N, kPiece>(p, s, k, it);
       if (role != 0 || !kVec) {
         __syncwarp();
         ok = next_item(p, s, k, it) && ok;
@@ -630,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
       if (role == 0)
         ok = copy_role<T, N, kPiece, kVec>(p, maps, it, s, tile);
       else if (role == 1)
-        ok = prepare_role<T, N, kPiece>(p, it, s, tile);
+        ok = prepare_role<T, N, kPiece, kVec>(p, it, s, tile);
       else if constexpr (!kPiece)
         ok = finish_role<T, N, kVec>(p, it, s, tile, k);
       if (kPiece || !p.queue) break;
@@ -638,9 +686,9 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
     // The next kernel's CTAs may come now.  Earlier, they would wait in places of this kernel's, two of
     // which then share an SM beside empty ones (160 chains, L8192: 696 us instead of 448).
     if (claims) griddep_launch_dependents();
-    if (role == 0 && kVec)  // shared memory stays until the copies are there, whatever the other roles do
-      for (uint32_t t = tile0 < kRing ? 0 : tile0 - kRing; t < tile0; ++t)
-        ok = wait_tile(s.raw_full, t, kRing, p.ctl.spin_limit_ns) && ok;
+    if (claims || (role == 0 && !kVec))  // shared memory stays until the copies are there, whatever the other roles do
+      for (uint32_t t = tile0 < S::RING ? 0 : tile0 - S::RING; t < tile0; ++t)
+        ok = wait_tile(s.raw_full, t, S::RING, p.ctl.spin_limit_ns) && ok;
     if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
     return;
   }
@@ -697,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
         }
       }
     }
-    ok = scan_role<T, N, kPiece>(p, it, s, tile0, A, h, delta_sum) && ok;
+    ok = scan_role<N, kPiece>(p, it, s, tile0, A, h, delta_sum) && ok;
     if (!ok) set_nan(h);
     tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
     if (!kPiece && it.sub + 1 < p.sp.subs) {
@@ -782,9 +830,9 @@ Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
     if (t->ptr)  // (a tensor map takes no rows that lie on one another)
       p.vec = p.vec && aligned_rows(t->ptr, a.batch > 1 ? t->batch_stride : 0, a.seqlen > 1 ? t->token_stride : 0, e, 16) &&
               (a.batch == 1 || t->batch_stride > 0) && (a.seqlen == 1 || t->token_stride > 0);
-  p.pairs = a.channels / a.ngroups * e % 4 == 0;
   for (const ssm_tokens* t : {&a.u, &a.dt, &a.z, &a.B, &a.C})
-    if (t->ptr) p.pairs = p.pairs && aligned_rows(t->ptr, t->batch_stride, t->token_stride, e, 4);
+    if (t->ptr)
+      p.dense = p.dense || (a.batch > 1 && t->batch_stride * e < 16) || (a.seqlen > 1 && t->token_stride * e < 16);
   return p;
 }
 
@@ -836,8 +884,8 @@ cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
     };
     const auto typed = [&](auto zero) {
       using T = decltype(zero);
-      constexpr size_t bytes = sizeof(Shared<T, N, kPiece>);
-      return p.vec ? go(selscan_kernel<T, N, kPiece, true>, bytes) : go(selscan_kernel<T, N, kPiece, false>, bytes);
+      return p.vec ? go(selscan_kernel<T, N, kPiece, true>, sizeof(Shared<T, N, kPiece, true>))
+                   : go(selscan_kernel<T, N, kPiece, false>, sizeof(Shared<T, N, kPiece, false>));
     };
     return a.dtype == SSM_BF16 ? typed(__nv_bfloat16{}) : typed(0.f);
   });
