@@ -285,20 +285,29 @@ struct Rows {
                      "l"(at & ~(uintptr_t)15)
                      : "memory");
   }
-};
-// The same rows element by element, where 16 bytes may hold what is not the tensor's.
-template <typename T, int PITCH>
-__device__ __forceinline__ void copy_elements(const ssm_tokens& x, int64_t b, int64_t t, int64_t column, int n, int rows,
-                                              T (*dst)[PITCH]) {
-  const uint32_t offset = offset_in_16<T>(x, b, t, column);
-  const T* src = static_cast<const T*>(x.ptr) + b * x.batch_stride + t * x.token_stride + column;
+  // `rows` of them, any of which may be the tensor's first or last: 16 bytes that hold what is not the
+  // tensor's go element by element
+  __device__ __forceinline__ void copy_edge(const ssm_tokens& x, const Params& p, int width, int n, int rows, T (*dst)[PITCH]) {
+    const int tid = threadIdx.x % kRoleThreads, c = tid % LANES;
+    const uintptr_t base = reinterpret_cast<uintptr_t>(x.ptr);
+    const uintptr_t end = base + sizeof(T) * ((p.a.batch - 1) * x.batch_stride + (p.a.seqlen - 1) * x.token_stride + width);
 #pragma unroll 1
-  for (int i = threadIdx.x % kRoleThreads; i < rows * n; i += kRoleThreads) {
-    const int r = i / n, c = i % n;
-    dst[r][c + (offset + r * (uint32_t)x.token_stride) % (16 / (uint32_t)sizeof(T))] = src[r * x.token_stride + c];
+    for (int r = tid / LANES; r < kTokens; r += STEP, at += step) {
+      const uintptr_t src = at & ~(uintptr_t)15, row = at - 16 * c;
+      if (r >= rows || (int)(at & 15) <= over) continue;
+      T* to = &dst[r][E * c];
+      if (src >= base && src + 16 <= end) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(src) : "memory");
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const uintptr_t e = src + sizeof(T) * j;
+          if (e >= row && e < row + sizeof(T) * n) to[j] = *reinterpret_cast<const T*>(e);
+        }
+      }
+    }
   }
-}
-
+};
 // Such rows are read from shared memory by columns, where a row's offset is no matter: this column of
 // eight tokens from t on (of them all tokens of x, `row0` the first's row in shared memory).
 template <typename T, int PITCH>
@@ -343,16 +352,14 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
       if (!all_lanes(tile < RING || wait_tile(s.raw_free, tile - RING, RING, p.ctl.spin_limit_ns))) return false;
       const bool edge = p.dense || (it.b == 0 && t == 0) || (it.b == a.batch - 1 && t + kTokens >= a.seqlen);
       if (rows < kTokens || edge) {
-        const int have = rows < kTokens ? rows : kTokens;
-        copy_elements<T>(a.dt, it.b, t, it.c0, it.cn, have, s.dt[ring]);
-        copy_elements<T>(a.u, it.b, t, it.c0, it.cn, have, s.u[ring]);
-        copy_elements<T>(a.B, it.b, t, it.g * N, N, have, s.b[ring]);
+        const int wide = a.ngroups * N;
+        dt.copy_edge(a.dt, p, a.channels, it.cn, rows, s.dt[ring]);
+        u.copy_edge(a.u, p, a.channels, it.cn, rows, s.u[ring]);
+        B.copy_edge(a.B, p, wide, N, rows, s.b[ring]);
         if constexpr (!kPiece) {
-          copy_elements<T>(a.C, it.b, t, it.g * N, N, have, s.c[ring]);
-          if (a.z.ptr) copy_elements<T>(a.z, it.b, t, it.c0, it.cn, have, s.z[ring]);
+          C.copy_edge(a.C, p, wide, N, rows, s.c[ring]);
+          if (a.z.ptr) z.copy_edge(a.z, p, a.channels, it.cn, rows, s.z[ring]);
         }
-        dt.at += dt.step * dt.PASSES, u.at += u.step * u.PASSES, z.at += z.step * z.PASSES;
-        B.at += B.step * B.PASSES, C.at += C.step * C.PASSES;
       } else {
         dt.copy(s.dt[ring]);
         u.copy(s.u[ring]);

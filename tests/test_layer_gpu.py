@@ -660,3 +660,79 @@ def test_selscan_queue_wait_runs_out():
     again, h2 = ssm.selscan_fwd(u, dt, A, B, C, workspace=ws)
     assert ssm.check_device_status(ws) == 0
     assert torch.equal(again, y) and torch.equal(h2, h)
+
+
+# ------------------------------------------------------------------------------ rows that are not aligned
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [
+    (2, 131, 263, 16, 1, 0, True, [131, 113], True, True),
+    (3, 64, 197, 8, 1, 1, False, None, True, True),
+    (2, 97, 146, 16, 2, 2, True, None, True, False),           # groups of 73 channels
+    (2, 80, 101, 32, 1, 3, True, [80, 16], False, True),
+    (1, 33, 75, 64, 1, 7, True, None, True, True),
+    (2, 48, 132, 16, 1, 4, True, [17, 48], True, True),        # rows on 8 bytes (bf16), on 16 (f32) but d4
+    (1, 1500, 65, 16, 1, 0, True, None, True, True),           # and the time axis in pieces
+], ids=str)
+def test_selscan_ragged_rows(case, dtype):
+    """Several channel tiles and tiles of tokens of rows that tensor copies cannot take."""
+    test_selscan_prompt(case, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 67, 3])
+def test_selscan_rows_on_one_another(d, dtype):
+    """Inputs broadcast over sequences (B, C) or tokens (dt, z), or overlapping rows one element apart (u)."""
+    import selective_state_space_mamba_gb300 as ssm
+    b, L, N = 2, 50, 16
+    r = rng_of("broadcast", d, dtype)
+    inp = scan_inputs(r, (b, L), d, N, 1, dtype)
+    line = rounded(r.standard_normal(b * L + d), dtype)
+    inp["u"] = np.lib.stride_tricks.sliding_window_view(line, d)[: b * L].reshape(b, L, d)
+    inp["dt"], inp["z"] = (np.broadcast_to(inp[k][:, :1], (b, L, d)) for k in ("dt", "z"))
+    inp["B"], inp["C"] = (np.broadcast_to(inp[k][:1], (b, L, 1, N)) for k in ("B", "C"))
+    y_ref, ey, h_ref, eh = ol.selscan(**inp)
+    t = {k: dev(inp[k][:, :1], dtype).expand(b, L, d) for k in ("dt", "z")}
+    g = {k: dev(inp[k][:1], dtype).expand(b, L, 1, N) for k in ("B", "C")}
+    u = dev(line, dtype).as_strided((b, L, d), (L, 1, 1))
+    y, h = ssm.selscan_fwd(u, t["dt"], dev(inp["A"]), g["B"], g["C"], dev(inp["D"]), t["z"], dev(inp["dt_bias"]))
+    close(host(h), h_ref, eh, "h")
+    close(host(y), y_ref, ey, "y", dtype)
+
+
+@pytest.mark.parametrize("b,L,d,dtype,pad", [
+    (13, 1100, 1537, "bf16", 0),    # more chains than places, odd rows
+    (13, 530, 1541, "f32", 3),
+    (7, 1300, 1472, "f32", 0),      # a few more chains than SMs: a CTA an SM
+    (7, 1300, 1425, "bf16", 1),
+])
+def test_selscan_more_queues(b, L, d, dtype, pad):
+    """Against the definition, and bit for bit what the same tokens give in several calls."""
+    import selective_state_space_mamba_gb300 as ssm
+    r = rng_of("more queues", b, L, d, dtype)
+    inp = scan_inputs(r, (b, L), d, 16, 1, dtype)
+    h0 = (0.3 * r.standard_normal((b, d, 16))).astype(np.float32)
+    lens = [L - 37 * i for i in range(b)]
+    bs, cs = np.array([0, 3, b - 1]), np.sort(r.choice(d, 24, replace=False))
+    sub = {k: (v[cs] if k in ("A", "D", "dt_bias") else v[bs] if k in ("B", "C") else v[bs][..., cs]) for k, v in inp.items()}
+    y_ref, ey, h_ref, eh = ol.selscan(**sub, h0=h0[bs][:, cs], lens=[lens[i] for i in bs])
+    for i, n in enumerate(lens):
+        for k in ("u", "dt", "B", "C", "z"):
+            inp[k][i, n:] = np.nan
+    y, h = run_scan(inp, dtype, pad, h0, lens)
+    close(host(h)[bs][:, cs], h_ref, eh, "h")
+    close(host(y)[bs][..., cs], y_ref, ey, "y", dtype)
+    state, parts = h0, []
+    for t0 in range(0, L, 256):
+        p = {k: (v[:, t0 : t0 + 256] if k in ("u", "dt", "B", "C", "z") else v) for k, v in inp.items()}
+        part, state = run_scan(p, dtype, pad, state, [min(max(n - t0, 0), 256) for n in lens])
+        parts.append(host(part))
+        state = host(state)
+    assert np.array_equal(np.concatenate(parts, 1), host(y)) and np.array_equal(state, host(h))
+
+
+@pytest.mark.parametrize("group", [None, 0, 128])
+@pytest.mark.parametrize("dtype,res", [("f32", "f32"), ("bf16", "none"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("d", [513, 1031, 1540, 2561, 4099, 10243])
+def test_rmsnorm_many_ragged_rows(d, dtype, res, group):
+    test_rmsnorm_many_rows(d, dtype, res, group)
