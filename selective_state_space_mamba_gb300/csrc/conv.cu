@@ -5,8 +5,8 @@
 //
 // Prompt: a thread keeps VEC channels' weights, and the window of the last W - 1 tokens, in
 // registers and walks down `run` tokens, so each x is loaded once but for the W - 1 tokens before
-// the run (which the neighbouring run has just brought to L2).  The next kConvUnroll
-// tokens are loaded before the last ones are used.  Items (run of tokens, channel vector) are numbered with the
+// the run (which the neighbouring run has just brought to L2).  The next block of
+// tokens (conv_unroll) is loaded before the last ones are used.  Items (run of tokens, channel vector) are numbered with the
 // channel vector fastest: a warp reads 32 * VEC consecutive channels of a token, whatever the
 // number of channels.
 //
@@ -22,7 +22,10 @@ namespace {
 using namespace layer;
 
 constexpr int kConvThreads = 128;
-constexpr int kConvUnroll = 4;
+// Tokens in flight of a thread, by its channels (b4 L4096 d2689, one channel: bf16 62 us with 4, 49 with
+// 8, 46 with 16, f32 80, 64, 62; d2690, two: bf16 42 us with 4, 35 with 8)
+__host__ __device__ constexpr int conv_unroll(int vec) { return 16 / vec; }
+constexpr int kConvLeast = 4;     // tokens of a run, at least
 constexpr int kConvResident = 7;  // CTAs an SM
 constexpr int kConvRun = 128;     // tokens of a run, about
 constexpr int kSmCount = 152;
@@ -52,6 +55,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvResident)
     conv_kernel(const ssm_tokens x, const float* __restrict__ w, const float* __restrict__ bias, const T* state_in,
                 const int32_t* lens, T* y, T* state_out, int64_t items, int64_t seqlen, int channels, int run,
                 bool act, bool vec_w) {
+  constexpr int U = conv_unroll(VEC);
   griddep_launch_dependents();
   griddep_wait();
   const int64_t item = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
@@ -86,16 +90,16 @@ __global__ void __launch_bounds__(kConvThreads, kConvResident)
   if (t0 < tl) {
     const T* xp = xb + t0 * x.token_stride;
     T* yp = yb + t0 * channels;
-    const int n = (int)(tl - t0), whole = n / kConvUnroll * kConvUnroll;
+    const int n = (int)(tl - t0), whole = n / U * U;
     // the first block, the window before it and the weights are all on their way before one is used
-    Raw<T, VEC> next[kConvUnroll], before[W - 1];
+    Raw<T, VEC> next[U], before[W - 1];
     if (whole > 0) {
 #pragma unroll
-      for (int j = 0; j < kConvUnroll; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
+      for (int j = 0; j < U; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
     }
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) before[k] = token(t0 - (W - 1) + k);
-    float wt[W][VEC], bi[VEC], win[W - 1 + kConvUnroll][VEC];
+    float wt[W][VEC], bi[VEC], win[W - 1 + U][VEC];
     load_weights(w + (int64_t)c * W, vec_w, wt);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) bi[i] = bias ? bias[c + i] : 0.f;
@@ -111,27 +115,27 @@ __global__ void __launch_bounds__(kConvThreads, kConvResident)
       if (act) silu_n(v, v);
       store_raw<T, VEC>(yp, from_floats<T, VEC>(v));
     };
-    for (int t = 0; t < whole; t += kConvUnroll) {
+    for (int t = 0; t < whole; t += U) {
 #pragma unroll
-      for (int j = 0; j < kConvUnroll; ++j) to_floats<T, VEC>(next[j], win[W - 1 + j]);
-      xp += kConvUnroll * x.token_stride;
-      if (t + kConvUnroll < whole) {
+      for (int j = 0; j < U; ++j) to_floats<T, VEC>(next[j], win[W - 1 + j]);
+      xp += U * x.token_stride;
+      if (t + U < whole) {
 #pragma unroll
-        for (int j = 0; j < kConvUnroll; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
+        for (int j = 0; j < U; ++j) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
       }
 #pragma unroll
-      for (int j = 0; j < kConvUnroll; ++j) emit(j, yp + (int64_t)j * channels);
-      yp += (int64_t)kConvUnroll * channels;
+      for (int j = 0; j < U; ++j) emit(j, yp + (int64_t)j * channels);
+      yp += (int64_t)U * channels;
 #pragma unroll
       for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) win[k][i] = win[k + kConvUnroll][i];
+        for (int i = 0; i < VEC; ++i) win[k][i] = win[k + U][i];
     }
 #pragma unroll
-    for (int j = 0; j < kConvUnroll - 1; ++j)
+    for (int j = 0; j < U - 1; ++j)
       if (whole + j < n) next[j] = load_raw<T, VEC>(xp + j * x.token_stride);
 #pragma unroll
-    for (int j = 0; j < kConvUnroll - 1; ++j)
+    for (int j = 0; j < U - 1; ++j)
       if (whole + j < n) {
         to_floats<T, VEC>(next[j], win[W - 1 + j]);
         emit(j, yp + (int64_t)j * channels);
@@ -201,9 +205,9 @@ __global__ void __launch_bounds__(kConvThreads)
   }
 }
 
-// Channels per thread: 4, 2 or 1, so that every row of x, y and the states starts on a vector.
-int conv_vec(const ssm_tokens& x, const void* state_in, const void* y, const void* state_out, int channels, int elem) {
-  for (int vec = 4; vec > 1; vec /= 2) {
+// Channels per thread: `most` (4 or 2), 2 or 1, so that every row of x, y and the states starts on a vector.
+int conv_vec(int most, const ssm_tokens& x, const void* state_in, const void* y, const void* state_out, int channels, int elem) {
+  for (int vec = most; vec > 1; vec /= 2) {
     const int bytes = vec * elem;
     if (channels % vec == 0 && aligned_rows(x.ptr, x.batch_stride, x.token_stride, elem, bytes) &&
         aligned_rows(state_in, 0, 0, elem, bytes) && aligned_rows(y, 0, 0, elem, bytes) &&
@@ -215,14 +219,14 @@ int conv_vec(const ssm_tokens& x, const void* state_in, const void* y, const voi
 
 // Tokens of a run: about kConvRun, so that the window before a run and the weights add little to it,
 // and such that the runs fill a whole number of the GPU's waves of resident threads; less than a wave
-// of them is cut shorter, to use more SMs, down to one block of kConvUnroll tokens.  b4 L8192 d5376 of
+// of them is cut shorter, to use more SMs, down to kConvLeast.  b4 L8192 d5376 of
 // wider rows: 123 us with 128, 126 with 32.
 int conv_run(int64_t columns, int64_t seqlen) {
   constexpr int64_t wave = (int64_t)kSmCount * kConvResident * kConvThreads;
   const int64_t waves = (columns * ((seqlen + kConvRun - 1) / kConvRun) + wave / 2) / wave;
   const int64_t segs = (waves < 1 ? 1 : waves) * wave / columns;
   const int64_t run = segs < 1 ? kConvRun : (seqlen + segs - 1) / segs;
-  return (int)(run < kConvUnroll ? kConvUnroll : run > 2 * kConvRun ? 2 * kConvRun : run);
+  return (int)(run < kConvLeast ? kConvLeast : run > 2 * kConvRun ? 2 * kConvRun : run);
 }
 
 template <typename F>
@@ -231,25 +235,26 @@ cudaError_t with_width(int width, F&& f) {
   if (width == 3) return f(std::integral_constant<int, 3>{});
   return f(std::integral_constant<int, 4>{});
 }
-template <typename F>
+template <int MOST, typename F>
 cudaError_t with_vec(int vec, F&& f) {
   if (vec == 1) return f(std::integral_constant<int, 1>{});
-  if (vec == 2) return f(std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 4>{});
+  if (MOST == 2 || vec == 2) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, MOST>{});
 }
 
 template <typename T>
 cudaError_t conv_fwd(const ssm_tokens& x, const float* w, const float* bias, const void* state_in, const int32_t* lens,
                      void* y, void* state_out, int64_t batch, int64_t seqlen, int channels, int width, bool silu,
                      cudaStream_t s) {
-  const int vec = conv_vec(x, state_in, y, state_out, channels, sizeof(T));
+  constexpr int kMost = 8 / sizeof(T);  // f32 in 16 bytes: 66 us at b4 L4096 d2688, in 8 bytes 61
+  const int vec = conv_vec(kMost, x, state_in, y, state_out, channels, sizeof(T));
   const int64_t nvec = channels / vec;
   const int run = conv_run(nvec * batch, seqlen);
   const int64_t segs = seqlen > run ? (seqlen + run - 1) / run : 1;
   const int64_t items = segs * nvec, blocks = (items + kConvThreads - 1) / kConvThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return with_width(width, [&](auto wc) {
-    return with_vec(vec, [&](auto vc) {
+    return with_vec<kMost>(vec, [&](auto vc) {
       return launch_pdl(conv_kernel<T, decltype(vc)::value, decltype(wc)::value>,
                         dim3((unsigned)blocks, (unsigned)batch), dim3(kConvThreads), 0, s, x, w, bias,
                         static_cast<const T*>(state_in), lens, static_cast<T*>(y), static_cast<T*>(state_out), items,
@@ -264,11 +269,11 @@ cudaError_t conv_step(const ssm_tokens& x, const float* w, const float* bias, co
                       int width, bool silu, cudaStream_t s) {
   ssm_tokens row = x;
   row.token_stride = 0;
-  const int vec = conv_vec(row, state_in, y, state_out, channels, sizeof(T));
+  const int vec = conv_vec(4, row, state_in, y, state_out, channels, sizeof(T));
   const int blocks = (channels / vec + kConvThreads - 1) / kConvThreads;
   const bool many = blocks * batch >= 8 * kSmCount;  // CTAs enough with four sequences a thread
   return with_width(width, [&](auto wc) {
-    return with_vec(vec, [&](auto vc) {
+    return with_vec<4>(vec, [&](auto vc) {
       constexpr int V = decltype(vc)::value, W = decltype(wc)::value;
       const auto go = [&](auto kernel, int rows) {
         return launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)((batch + rows - 1) / rows)), dim3(kConvThreads), 0, s,
