@@ -10,7 +10,7 @@
 //   copy     brings raw tiles to shared memory by tensor copies, some tiles ahead
 //   prepare  takes eight channels of one token a thread, computes delta and delta u and lays them out by
 //            channel pair; B and C become f32
-//   scan     walks the tiles.  A lane holds four state entries of two channels (lane_of).  What shared
+//   scan     walks the tiles.  A lane holds four (lane_states) state entries of two channels (lane_of).  What shared
 //            memory hands to registers limits it, so B and C serve two channels, and lanes are laid
 //            out for the hardware's merging of loads; the sums over n end in up to four partial
 //            sums in shared memory
@@ -33,20 +33,24 @@ using namespace layer;
 constexpr int kSmCount = 152;
 constexpr int kMaxSplit = 64;
 constexpr int kTokens = 16;      // tokens of a tile
-constexpr int kSpl = 4;          // state entries of a lane's channel
 constexpr int kBlock = 4;        // tokens between two reductions
 constexpr int kResident = 2;     // CTAs an SM
 constexpr int kSubTokens = 512;  // tokens of an item of the queue (short sequences: half of it)
 constexpr int kScanThreads = 128, kRoleThreads = 64, kThreads = kScanThreads + 3 * kRoleThreads;
 
-__host__ __device__ constexpr int tile_channels(int n) { return kScanThreads * kSpl * 2 / n; }
+constexpr int kHand = 8;  // floats of a scan thread in the workspace
+
+// State entries of a lane's channel.  With two for 8 entries a tile has 64 channels like those of 16 entries:
+// the other roles take the time of 128 (b4 L4096 d2560: 221 us, with four 261).
+__host__ __device__ constexpr int lane_states(int n) { return n == 8 ? 2 : 4; }
+__host__ __device__ constexpr int tile_channels(int n) { return kScanThreads * lane_states(n) * 2 / n; }
 
 struct Params {
   ssm_selscan_args a;
   SelscanSplit sp;
   WsHeader* queue;   // claim counter and status; NULL: one item a CTA
   uint32_t* done;    // [chains] items of the chain that are finished
-  float* hand;       // [chains, scan threads, 8] state between a chain's items
+  float* hand;       // [chains, scan threads, kHand] state between a chain's items
   LookbackCtl ctl;   // wait limit and fault injection
   float* E;          // [split - 1, batch, channels, dstate]
   float* T;          // [split - 1, batch, channels]
@@ -71,7 +75,7 @@ struct Shared {
   static constexpr int CT = tile_channels(N);
   static constexpr int RING = kVec || sizeof(T) == 2 ? 4 : 3;  // raw tiles: two CTAs an SM have to fit
   static constexpr int PAD = kVec ? 0 : 16 / sizeof(T);        // a row that starts anywhere in its first 16 bytes
-  static constexpr int LPC = N / kSpl;
+  static constexpr int SPL = lane_states(N), LPC = N / SPL;
   static constexpr int PARTS = LPC < 4 ? LPC : 4;  // partial sums of a channel
   static constexpr int YP = kTokens * CT + 16;     // floats from one to the next: 16 more, against bank conflicts
   // targets of tensor copies: 128-byte aligned
@@ -109,12 +113,16 @@ __device__ __forceinline__ void lane_of(int lane, int& sub, int& pair) {
   pair = lane >> 1 & (LW - 1);
 }
 
-template <int M>
+template <int M>  // even
 __device__ __forceinline__ void load_states(const float* p, float (&v)[M]) {
 #pragma unroll
-  for (int i = 0; i < M; i += 4) {
+  for (int i = 0; i + 3 < M; i += 4) {
     const float4 r = *reinterpret_cast<const float4*>(p + i);
     v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+  }
+  if (M % 4 != 0) {
+    const float2 r = *reinterpret_cast<const float2*>(p + M - 2);
+    v[M - 2] = r.x, v[M - 1] = r.y;
   }
 }
 
@@ -205,9 +213,10 @@ __device__ __forceinline__ bool wait_tile(uint64_t* bars, uint32_t tile, uint32_
 }
 
 // After a wait that ran out (never but on a GPU that stopped): a state that cannot pass for one.
-__device__ __forceinline__ void set_nan(float (&h)[2][kSpl]) {
+template <int SPL>
+__device__ __forceinline__ void set_nan(float (&h)[2][SPL]) {
 #pragma unroll
-  for (int i = 0; i < kSpl; ++i) h[0][i] = h[1][i] = __int_as_float(0x7fffffff);
+  for (int i = 0; i < SPL; ++i) h[0][i] = h[1][i] = __int_as_float(0x7fffffff);
 }
 
 // Whether all lanes of the warp say so; memory accesses before and after it are in order.
@@ -566,8 +575,8 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
 // The scan's part of an item: h of this thread's two channels through the tiles.
 template <int N, bool kPiece, typename S>
 __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s, uint32_t tile,
-                                          const float (&A)[2][kSpl], float (&h)[2][kSpl], float (&delta_sum)[2]) {
-  constexpr int CT = S::CT, LPC = S::LPC, LW = 32 / LPC;
+                                          const float (&A)[2][S::SPL], float (&h)[2][S::SPL], float (&delta_sum)[2]) {
+  constexpr int CT = S::CT, SPL = S::SPL, LPC = S::LPC, LW = 32 / LPC;
   constexpr int ROUNDS = LPC <= 4 ? 0 : LPC == 8 ? 1 : 2;  // halving rounds that leave four lanes a channel pair
   const int lane = threadIdx.x & 31;
   int sub, pair;
@@ -577,8 +586,8 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
     const int buf = tile & 1;
     const bool ok = wait_tile(s.full, tile, 2, p.ctl.spin_limit_ns) &&
                     (kPiece || tile < 2 || wait_tile(s.y_free, tile - 2, 2, p.ctl.spin_limit_ns));
-    const float* b_row = &s.fb[buf][0][sub * kSpl];
-    const float* c_row = &s.fc[kPiece ? 0 : buf][0][sub * kSpl];
+    const float* b_row = &s.fb[buf][0][sub * SPL];
+    const float* c_row = &s.fc[kPiece ? 0 : buf][0][sub * SPL];
     const float4* d_row = &s.d[buf][0][pair ^ (pair >> 3 & 3)];
     // token of value j after the rounds: bits of `sub` from the third on, then j
     const int mine = ROUNDS == 0 ? 0 : ROUNDS == 1 ? sub >> 2 : (sub >> 2 & 1) + 2 * (sub >> 3);
@@ -590,14 +599,14 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
       for (int j = 0; j < kBlock; ++j) {
         const float4 d = d_row[(t + j) * (CT / 2)];
         const float delta[2] = {d.x, d.z}, du[2] = {d.y, d.w};
-        float B[kSpl], C[kSpl], y[2];
+        float B[SPL], C[SPL], y[2];
         load_states(b_row + (t + j) * N, B);
         if (!kPiece) load_states(c_row + (t + j) * N, C);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float2 acc;
 #pragma unroll
-          for (int i = 0; i < kSpl; i += 2) {
+          for (int i = 0; i < SPL; i += 2) {
             float2 e = __fmul2_rn(make_float2(delta[c], delta[c]), make_float2(A[c][i], A[c][i + 1]));
             e.x = exp2_fast(e.x);
             e.y = exp2_fast(e.y);
@@ -641,7 +650,7 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
 template <typename T, int N, bool kPiece, bool kVec>
 __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shared<T, N, kPiece, kVec>;
-  constexpr int LW = 32 / S::LPC;
+  constexpr int SPL = S::SPL, LW = 32 / S::LPC;
   extern __shared__ __align__(128) unsigned char smem[];
   S& s = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x;
@@ -710,25 +719,30 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
       if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
       return;
     }
-    float A[2][kSpl], h[2][kSpl], delta_sum[2] = {};
+    float A[2][SPL], h[2][SPL], delta_sum[2] = {};
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
 #pragma unroll
-      for (int i = 0; i < kSpl; ++i) {
-        A[c][i] = a.A[chan * N + sub * kSpl + i] * kLog2e;
+      for (int i = 0; i < SPL; ++i) {
+        A[c][i] = a.A[chan * N + sub * SPL + i] * kLog2e;
         h[c][i] = 0.f;
       }
     }
-    float4* hand = reinterpret_cast<float4*>(p.hand) + (it.chain * kScanThreads + tid) * 2;
+    float4* hand = reinterpret_cast<float4*>(p.hand + (it.chain * kScanThreads + tid) * kHand);
     if constexpr (!kPiece) {
       if (it.sub > 0) {
         if ((tid & 31) == 0 && !it.ready)
           ok = wait_done(&p.done[it.chain], (uint32_t)it.sub, p.queue, p.ctl.spin_limit_ns);
         ok = all_lanes(ok);
-        const float4 v = load_hand(hand), w = load_hand(hand + 1);
-        h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
-        h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
+        if constexpr (SPL == 4) {
+          const float4 v = load_hand(hand), w = load_hand(hand + 1);
+          h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
+          h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
+        } else {
+          const float4 v = load_hand(hand);
+          h[0][0] = v.x, h[0][1] = v.y, h[1][0] = v.z, h[1][1] = v.w;
+        }
         if (!ok) set_nan(h);
       } else {
 #pragma unroll
@@ -736,18 +750,18 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
           const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
           if (a.h0) {
 #pragma unroll
-            for (int i = 0; i < kSpl; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * kSpl + i];
+            for (int i = 0; i < SPL; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * SPL + i];
           }
 #pragma unroll 4
           for (int j = 0; j < it.part; ++j) {  // the state that the parts before this one leave
             const int64_t row = ((int64_t)j * a.batch + it.b) * a.channels + chan;
-            float e[kSpl], v[kSpl];
+            float e[SPL], v[SPL];
             mul_n(A[c], p.T[row], e);
 #pragma unroll
-            for (int i = 0; i < kSpl; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * kSpl + i];
+            for (int i = 0; i < SPL; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * SPL + i];
             fma_n(e, h[c], v);
 #pragma unroll
-            for (int i = 0; i < kSpl; ++i) h[c][i] = v[i];
+            for (int i = 0; i < SPL; ++i) h[c][i] = v[i];
           }
         }
       }
@@ -756,8 +770,12 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
     if (!ok) set_nan(h);
     tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
     if (!kPiece && it.sub + 1 < p.sp.subs) {
-      hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
-      hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+      if constexpr (SPL == 4) {
+        hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+        hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+      } else {
+        hand[0] = make_float4(h[0][0], h[0][1], h[1][0], h[1][1]);
+      }
     } else {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -773,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __gr
         }
         if (out) {
 #pragma unroll
-          for (int i = 0; i < kSpl; ++i) out[sub * kSpl + i] = h[c][i];
+          for (int i = 0; i < SPL; ++i) out[sub * SPL + i] = h[c][i];
         }
       }
     }
@@ -809,7 +827,7 @@ Layout layout(const SelscanSplit& sp, int64_t batch, int channels, int dstate) {
   const size_t rows = (size_t)(sp.split - 1) * batch * channels;
   l.done = kHeaderBytes;
   l.hand = up256(l.done + 4 * chains);
-  l.E = up256(l.hand + chains * kScanThreads * 2 * kSpl * sizeof(float));
+  l.E = up256(l.hand + chains * kScanThreads * kHand * sizeof(float));
   l.T = up256(l.E + rows * dstate * sizeof(float));
   l.total = up256(l.T + rows * sizeof(float));
   return l;
