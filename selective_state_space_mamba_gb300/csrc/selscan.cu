@@ -7,19 +7,19 @@
 //
 // A chain (channel, n) is sequential in t, so the parallelism comes from the chains.  Time goes in
 // tiles of kTokens, and a CTA's warps have four roles that run beside each other:
-//   copy     brings raw tiles to shared memory by tensor copies, some tiles ahead
+//   copy     brings raw tiles to shared memory by tensor copies (rows that are not aligned: Rows), some
+//            tiles ahead
 //   prepare  takes eight channels of one token a thread, computes delta and delta u and lays them out by
 //            channel pair; B and C become f32
-//   scan     walks the tiles.  A lane holds four (lane_states) state entries of two channels (lane_of).  What shared
-//            memory hands to registers limits it, so B and C serve two channels, and lanes are laid
-//            out for the hardware's merging of loads; the sums over n end in up to four partial
-//            sums in shared memory
+//   scan     walks the tiles.  A lane holds four (lane_states) state entries of two channels (lane_of):
+//            B and C serve both channels, and lanes are laid out for the hardware's merging of
+//            loads; the sums over n end in up to four partial sums in shared memory
 //   finish   joins a tile's partial sums, adds the skip, gates and writes y
 // They meet at mbarriers, so the scan does not stop for the rest, and each goes through the CTA's items
 // by itself, so that an item's first tiles come in beside the last ones of the item before.
 //
-// b4 L8192 d5120 N16 in bf16: 770 us, and b1 L65521 d1536 in f32: 814 us, against 200 and 243 us of
-// memory and 280 and 170 of exponentials.  The multiply-adds of two state entries read three register
+// b4 L8192 d5120 N16 in bf16: 765 us, and b1 L65521 d1536 in f32: 807 us, against 200 and 243 us of
+// memory and 277 and 168 of exponentials.  The multiply-adds of two state entries read three register
 // pairs, which takes 3.2 cycles a warp instruction and not 2: the scan alone takes 109 cycles a token
 // for the two CTAs of an SM, the same as in registers only; with the other roles beside it, 177.
 #include "layer_common.cuh"
