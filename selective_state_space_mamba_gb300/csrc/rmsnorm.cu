@@ -2,15 +2,18 @@
 // as e4m3 codes with f32 scales.  Each element is read once and written once: memory-bound (a few
 // rows: launch-bound).
 //
-// One CTA a row.  A thread owns vectors of eight columns, tid + k * threads: consecutive columns where
+// A CTA or a warp a row.  A thread owns vectors of eight columns, tid + k * threads: consecutive columns where
 // rows are aligned, so that the columns of 16 neighbouring lanes are a scale group of 128; else every
 // 32nd of the warp's 256, so that its lanes still access neighbouring elements (odd rows of 2561 bf16,
-// 8 bits, 16384 of them: 82 us, with consecutive columns 224; 2560 columns: 48).  r of a thread's first
+// 8 bits, 16384 of them: 85 us, with consecutive columns 224; 2560 columns: 48).  r of a thread's first
 // HOLD vectors stays in registers between the sum of squares and the output.
 //   Many rows: up to five vectors a thread, so that a CTA has few warps to join in its sums
 //       and many CTAs are resident; a row's loads are all in flight at once.  32768 x 2560, bf16
 //       residual, 8 bits: 88 us, the rate of a copy; one vector a thread 182 us, CTAs that walk
 //       the rows and load the next one ahead 120 us (their registers leave half the CTAs).
+//   Many narrow rows, of up to five vectors a lane: a warp a row, four in a CTA, as the GPU starts about one
+//       CTA a ns (16384 x 256 with a residual: 17 us with a CTA a row, 6.4 so; x 1024: 22.6, 21.5, without a
+//       residual 19.5, 12.3).
 //   Few rows: one vector a thread for up to 8192 columns, the shortest way through a single row.
 // What a thread does not hold of wider rows is read again.  No output is written before the last
 // read of its element, so residual_out may be residual.
@@ -24,8 +27,9 @@ namespace {
 using namespace layer;
 
 constexpr int kNormMaxThreads = 1024;
-constexpr int kHoldMaxThreads = 256;
+constexpr int kHoldMaxThreads = 512;
 constexpr int64_t kManyRows = 152 * 4;  // four CTAs an SM
+constexpr int kWarpRows = 4;  // rows of a CTA where a warp does for one
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
 
@@ -38,6 +42,7 @@ struct NormParams {
   void* y;
   uint8_t* q;
   float* scale;
+  int64_t rows;
   int width, group;
   float eps;
 };
@@ -50,12 +55,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kE4m3Max), kMinScale); }
 
-// Sum and maximum over the CTA, the same in every thread; each has its own `part`.
-__device__ __forceinline__ float block_sum(float v, float* part) {
+// Sum and maximum over a row's threads (the CTA, or where it has ROWS > 1 of them a warp), the same in each
+// of them; each has its own `part`.
+template <int ROWS>
+__device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return v;
+  if (ROWS > 1 || warps == 1) return v;
   if (lane == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = lane < warps ? part[lane] : 0.f;
@@ -63,11 +70,12 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float block_max(float v, float* part) {
+template <int ROWS>
+__device__ __forceinline__ float row_max(float v, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return v;
+  if (ROWS > 1 || warps == 1) return v;
   if (lane == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = lane < warps ? part[lane] : 0.f;
@@ -220,15 +228,16 @@ __device__ __forceinline__ void output(const NormParams& p, int64_t row, int i, 
 
 // kVec: every row of every tensor starts on 16 bytes (q: 8), and rows are whole vectors.  HOLD > 1: rows
 // are at most HOLD vectors a thread.
-template <typename T, typename R, bool kRes, bool kFp8, bool kVec, int HOLD>
-__global__ void __launch_bounds__(HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
+template <typename T, typename R, bool kRes, bool kFp8, bool kVec, int HOLD, int ROWS>
+__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
     rmsnorm_kernel(const __grid_constant__ NormParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float sum_part[32];
-  __shared__ float max_part[32];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, threads = blockDim.x;
+  __shared__ float sum_part[ROWS > 1 ? 1 : 32];
+  __shared__ float max_part[ROWS > 1 ? 1 : 32];
+  const int64_t row = ROWS > 1 ? (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 5) : blockIdx.x;
+  if (ROWS > 1 && row >= p.rows) return;
+  const int tid = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x, threads = ROWS > 1 ? 32 : blockDim.x;
   const int nvec = vectors<kVec>(p.width);
   const int first = HOLD > 1 ? nvec : tid + threads;  // this thread's first vector that it does not hold
   float held[HOLD][8];
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
       add_squares(v, sum);
     }
   }
-  const float rstd = rsqrtf(block_sum(sum[0] + sum[1], sum_part) / (float)p.width + p.eps);
+  const float rstd = rsqrtf(row_sum<ROWS>(sum[0] + sum[1], sum_part) / (float)p.width + p.eps);
 
   float row_scale = 0.f;
   if (kFp8 && p.group == 0) {  // one scale for the row: its largest absolute value first
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldMaxThreads : kNormMaxThreads)
       normed<kVec>(p, i, r, rstd, v);
       m = max8(v, m);
     }
-    row_scale = scale_of(block_max(m, max_part));
+    row_scale = scale_of(row_max<ROWS>(m, max_part));
     if (tid == 0) p.scale[row] = row_scale;
   }
 #pragma unroll
@@ -318,8 +327,14 @@ cudaError_t launch_rows(const NormParams& p, int64_t rows, bool vec, cudaStream_
       return launch_pdl(kernel, dim3((unsigned)rows),
                         dim3((unsigned)(threads < kNormMaxThreads ? threads : kNormMaxThreads)), 0, s, p);
     };
-    if (rows < kManyRows || nvec <= 64 || nvec > 5 * kHoldMaxThreads) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1>, 1);
-    return nvec <= 192 ? go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3>, 3) : go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5>, 5);
+    const auto warps = [&](auto kernel) {
+      return launch_pdl(kernel, dim3((unsigned)((rows + kWarpRows - 1) / kWarpRows)), dim3(32 * kWarpRows), 0, s, p);
+    };
+    if (rows < kManyRows || nvec > 5 * kHoldMaxThreads) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1, 1>, 1);
+    if (nvec <= 32) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1, kWarpRows>);
+    if (nvec <= 96) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, kWarpRows>);
+    if (nvec <= 160) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, kWarpRows>);
+    return nvec <= 192 ? go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, 1>, 3) : go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, 1>, 5);
   };
   return vec ? with(std::true_type{}) : with(std::false_type{});
 }
@@ -335,7 +350,7 @@ cudaError_t launch_rmsnorm(const void* x, int64_t x_stride, const float* weight,
                            void* residual_out, void* y, void* q, float* scale, int64_t rows, int width, int group,
                            float eps, ssm_dtype dtype, ssm_dtype res_dtype, cudaStream_t s) {
   const int e = dtype == SSM_F32 ? 4 : 2, re = res_dtype == SSM_F32 ? 4 : 2;
-  const NormParams p{x, x_stride, weight, residual, residual_out, y, static_cast<uint8_t*>(q), scale, width, group, eps};
+  const NormParams p{x, x_stride, weight, residual, residual_out, y, static_cast<uint8_t*>(q), scale, rows, width, group, eps};
   const bool vec = width % 8 == 0 && aligned_rows(x, x_stride, 0, e, 16) && aligned_rows(weight, 0, 0, 4, 16) &&
                    aligned_rows(residual, width, 0, re, 16) && aligned_rows(residual_out, width, 0, re, 16) &&
                    aligned_rows(y, width, 0, e, 16) && aligned_rows(q, width, 0, 1, 8);

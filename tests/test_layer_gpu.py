@@ -736,3 +736,28 @@ def test_selscan_more_queues(b, L, d, dtype, pad):
 @pytest.mark.parametrize("d", [513, 1031, 1540, 2561, 4099, 10243])
 def test_rmsnorm_many_ragged_rows(d, dtype, res, group):
     test_rmsnorm_many_rows(d, dtype, res, group)
+
+
+@pytest.mark.parametrize("group", [None, 0, 128])
+@pytest.mark.parametrize("dtype,res", [("f32", "f32"), ("bf16", "none"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("d", [1, 8, 100, 256, 257, 768, 1000, 1280, 12288])
+def test_rmsnorm_many_narrow_rows(d, dtype, res, group):
+    """A warp a row, four rows a CTA (613 rows: the last CTA has one); and rows of more than 10240.  With one
+    column x + residual is 0 in a row, whose scale is the least."""
+    import selective_state_space_mamba_gb300 as ssm
+    rows = 613
+    x, w, residual = norm_inputs("many", rows, d, dtype, res)
+    v, err, r = ol.rmsnorm(x, w, residual)
+    if group is None:
+        y, ro = ssm.rmsnorm_fwd(dev(x, dtype), dev(w), dev(residual, res))
+        close(host(y), v, err, "y", dtype)
+    else:
+        q, scale, ro = ssm.rmsnorm_fp8_fwd(dev(x, dtype), dev(w), dev(residual, res), group=group)
+        s = host(scale).reshape(rows, -1)
+        each = np.repeat(s, group or d, axis=1)[:, :d]
+        pad = np.pad(np.abs(v), ((0, 0), (0, s.shape[1] * (group or d) - d))).reshape(rows, s.shape[1], -1).max(2)
+        least = 448 * 2.0 ** -126
+        assert np.all(np.abs(s * 448 - np.maximum(pad, least)) <= err.max(1, keepdims=True) + 2 * ol.U * np.maximum(pad, least))
+        e4m3_close(host(q), each, v, err, "q")
+    if residual is not None:
+        close(host(ro), r, ol.U * np.abs(r), "residual", res)
