@@ -5,9 +5,9 @@
 //
 // Prompt: a thread keeps VEC channels' weights, and the window of the last W - 1 tokens, in
 // registers and walks down `run` tokens, so each x is loaded once but for the W - 1 tokens before
-// the run (which the neighbouring run has just brought to L2).  The next block of
-// tokens (conv_unroll) is loaded before the last ones are used.  Items (run of tokens, channel vector) are numbered with the
-// channel vector fastest: a warp reads 32 * VEC consecutive channels of a token, whatever the
+// the run (which the neighbouring run has just brought to L2).  The next block of tokens (conv_unroll)
+// is loaded before the last ones are used.  Items (run of tokens, channel vector) are numbered with
+// the channel vector fastest: a warp reads 32 * VEC consecutive channels of a token, whatever the
 // number of channels.
 //
 // b4 L8192 d5376 of wider rows, bf16: 124 us, 5.7 TB/s (a copy: 6.7); it waits for memory.  A step of 128
@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kConvThreads)
 }
 
 // Channels per thread: `most` (4 or 2), 2 or 1, so that every row of x, y and the states starts on a vector.
-int conv_vec(int most, const ssm_tokens& x, const void* state_in, const void* y, const void* state_out, int channels, int elem) {
+int conv_vec(int most, const ssm_tokens& x, const void* state_in, const void* y, const void* state_out, int channels,
+             int elem) {
   for (int vec = most; vec > 1; vec /= 2) {
     const int bytes = vec * elem;
     if (channels % vec == 0 && aligned_rows(x.ptr, x.batch_stride, x.token_stride, elem, bytes) &&

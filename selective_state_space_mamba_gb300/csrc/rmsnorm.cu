@@ -334,7 +334,8 @@ cudaError_t launch_rows(const NormParams& p, int64_t rows, bool vec, cudaStream_
     if (nvec <= 32) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1, kWarpRows>);
     if (nvec <= 96) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, kWarpRows>);
     if (nvec <= 160) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, kWarpRows>);
-    return nvec <= 192 ? go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, 1>, 3) : go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, 1>, 5);
+    if (nvec <= 192) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, 1>, 3);
+    return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, 1>, 5);
   };
   return vec ? with(std::true_type{}) : with(std::false_type{});
 }
@@ -350,7 +351,8 @@ cudaError_t launch_rmsnorm(const void* x, int64_t x_stride, const float* weight,
                            void* residual_out, void* y, void* q, float* scale, int64_t rows, int width, int group,
                            float eps, ssm_dtype dtype, ssm_dtype res_dtype, cudaStream_t s) {
   const int e = dtype == SSM_F32 ? 4 : 2, re = res_dtype == SSM_F32 ? 4 : 2;
-  const NormParams p{x, x_stride, weight, residual, residual_out, y, static_cast<uint8_t*>(q), scale, rows, width, group, eps};
+  const NormParams p{x, x_stride, weight, residual, residual_out, y, static_cast<uint8_t*>(q),
+                     scale, rows, width, group, eps};
   const bool vec = width % 8 == 0 && aligned_rows(x, x_stride, 0, e, 16) && aligned_rows(weight, 0, 0, 4, 16) &&
                    aligned_rows(residual, width, 0, re, 16) && aligned_rows(residual_out, width, 0, re, 16) &&
                    aligned_rows(y, width, 0, e, 16) && aligned_rows(q, width, 0, 1, 8);

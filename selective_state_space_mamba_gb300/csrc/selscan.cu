@@ -98,7 +98,8 @@ struct Shared {
 // Channels vc to vc + 7 of a row of Shared::y.
 __device__ __forceinline__ void load_y(const float* row, int vc, float (&v)[8]) {
   const int swap = vc >> 3 & 4;
-  const float4 a = *reinterpret_cast<const float4*>(row + (vc ^ swap)), b = *reinterpret_cast<const float4*>(row + (vc ^ swap ^ 4));
+  const float4 a = *reinterpret_cast<const float4*>(row + (vc ^ swap));
+  const float4 b = *reinterpret_cast<const float4*>(row + (vc ^ swap ^ 4));
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
@@ -255,14 +256,13 @@ __device__ __forceinline__ bool claim_item(const Params& p, S& s, uint32_t k, It
   return true;
 }
 
-// The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
-
 // Elements from the 16-byte boundary at or before the columns from `column` on of sequence b to them, at its
 // token t.  (Only the low bits count, so 32-bit arithmetic does.)
 template <typename T>
 __device__ __forceinline__ int offset_in_16(const ssm_tokens& x, int64_t b, int64_t t, int64_t column) {
   const uint32_t first = (uint32_t)(reinterpret_cast<uintptr_t>(x.ptr) / sizeof(T)) + (uint32_t)column;
-  return (int)((first + (uint32_t)b * (uint32_t)x.batch_stride + (uint32_t)t * (uint32_t)x.token_stride) % (16 / sizeof(T)));
+  const uint32_t row = first + (uint32_t)b * (uint32_t)x.batch_stride + (uint32_t)t * (uint32_t)x.token_stride;
+  return (int)(row % (16 / sizeof(T)));
 }
 
 // Rows that tensor copies cannot take: `n` columns of consecutive tokens from t on, in asynchronous copies of
@@ -271,10 +271,11 @@ __device__ __forceinline__ int offset_in_16(const ssm_tokens& x, int64_t b, int6
 template <typename T, int COLUMNS>
 struct Rows {
   static constexpr int E = 16 / sizeof(T), PITCH = COLUMNS + E, CHUNKS = PITCH / E;
-  static constexpr int LANES = CHUNKS <= 4 ? 4 : CHUNKS <= 8 ? 8 : CHUNKS <= 16 ? 16 : CHUNKS <= 32 ? 32 : 64;  // of a row
+  // of a row
+  static constexpr int LANES = CHUNKS <= 4 ? 4 : CHUNKS <= 8 ? 8 : CHUNKS <= 16 ? 16 : CHUNKS <= 32 ? 32 : 64;
   static constexpr int STEP = kRoleThreads / LANES, PASSES = kTokens / STEP;
   uintptr_t at, step;  // address of this thread's column in its next row, and STEP rows
-  int over;            // the 16 bytes of a row that starts at more than this are in use
+  int over;            // this thread's 16 bytes of a row are in use if it starts at more than this
 
   __device__ __forceinline__ Rows(const ssm_tokens& x, int64_t b, int64_t t, int64_t column, int n) {
     const int tid = threadIdx.x % kRoleThreads, c = tid % LANES;
@@ -296,10 +297,12 @@ struct Rows {
   }
   // `rows` of them, any of which may be the tensor's first or last: 16 bytes that hold what is not the
   // tensor's go element by element
-  __device__ __forceinline__ void copy_edge(const ssm_tokens& x, const Params& p, int width, int n, int rows, T (*dst)[PITCH]) {
+  __device__ __forceinline__ void copy_edge(const ssm_tokens& x, const Params& p, int width, int n, int rows,
+                                            T (*dst)[PITCH]) {
     const int tid = threadIdx.x % kRoleThreads, c = tid % LANES;
     const uintptr_t base = reinterpret_cast<uintptr_t>(x.ptr);
-    const uintptr_t end = base + sizeof(T) * ((p.a.batch - 1) * x.batch_stride + (p.a.seqlen - 1) * x.token_stride + width);
+    const int64_t last = (p.a.batch - 1) * x.batch_stride + (p.a.seqlen - 1) * x.token_stride;
+    const uintptr_t end = base + sizeof(T) * (last + width);
 #pragma unroll 1
     for (int r = tid / LANES; r < kTokens; r += STEP, at += step) {
       const uintptr_t src = at & ~(uintptr_t)15, row = at - 16 * c;
@@ -317,17 +320,18 @@ struct Rows {
     }
   }
 };
-// Such rows are read from shared memory by columns, where a row's offset is no matter: this column of
-// eight tokens from t on (of them all tokens of x, `row0` the first's row in shared memory).
+// Such rows are read from shared memory by columns, where a row's offset is no matter: column c of eight
+// tokens of x from t on; row0 is the first one's row in shared memory.
 template <typename T, int PITCH>
-__device__ __forceinline__ void load_column8(const ssm_tokens& x, int64_t b, int64_t t, int64_t column, const T (*row0)[PITCH],
-                                             int c, float (&v)[8]) {
+__device__ __forceinline__ void load_column8(const ssm_tokens& x, int64_t b, int64_t t, int64_t column,
+                                             const T (*row0)[PITCH], int c, float (&v)[8]) {
   constexpr uint32_t kMask = 16 / sizeof(T) - 1;
   const uint32_t offset = offset_in_16<T>(x, b, t, column);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = to_f32(row0[j][c + ((offset + j * (uint32_t)x.token_stride) & kMask)]);
 }
 
+// The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
 template <typename T, int N, bool kPiece, bool kVec>
 __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, const Item& it,
                                           Shared<T, N, kPiece, kVec>& s, uint32_t tile) {
@@ -379,7 +383,8 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
         }
       }
       // once for the copies in flight, once for what is stored already
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&s.raw_full[ring])) : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&s.raw_full[ring]))
+                   : "memory");
       mbar_arrive(&s.raw_full[ring]);
     }
   }
@@ -387,7 +392,8 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
 }
 
 template <typename T, int N, bool kPiece, bool kVec>
-__device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Shared<T, N, kPiece, kVec>& s, uint32_t tile) {
+__device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Shared<T, N, kPiece, kVec>& s,
+                                             uint32_t tile) {
   constexpr int CT = tile_channels(N), RING = Shared<T, N, kPiece, kVec>::RING;
   const ssm_selscan_args& a = p.a;
   int64_t t0 = it.t_begin;
@@ -482,7 +488,8 @@ __device__ __forceinline__ bool publish(const Params& p, const Item& it, S& s, u
 }
 
 template <typename T, int N, bool kVec>
-__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false, kVec>& s, uint32_t tile, uint32_t k) {
+__device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Shared<T, N, false, kVec>& s,
+                                            uint32_t tile, uint32_t k) {
   using S = Shared<T, N, false, kVec>;
   constexpr int CT = S::CT, RING = S::RING;
   int64_t t0 = it.t_begin;
@@ -591,7 +598,8 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
     const float4* d_row = &s.d[buf][0][pair ^ (pair >> 3 & 3)];
     // token of value j after the rounds: bits of `sub` from the third on, then j
     const int mine = ROUNDS == 0 ? 0 : ROUNDS == 1 ? sub >> 2 : (sub >> 2 & 1) + 2 * (sub >> 3);
-    float* y_row = kPiece ? nullptr : &s.y[kPiece ? 0 : buf][(sub & (S::PARTS - 1)) * S::YP + mine * CT + 2 * (pair ^ (pair >> 3 & 2))];
+    const int y_at = (sub & (S::PARTS - 1)) * S::YP + mine * CT + 2 * (pair ^ (pair >> 3 & 2));
+    float* y_row = kPiece ? nullptr : &s.y[kPiece ? 0 : buf][y_at];
 #pragma unroll 2
     for (int t = 0; t < kTokens; t += kBlock) {
       float2 part[kBlock];
@@ -636,7 +644,8 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
           }
         }
 #pragma unroll
-        for (int j = 0; j < kBlock >> ROUNDS; ++j) *reinterpret_cast<float2*>(y_row + (t + (j << ROUNDS)) * CT) = part[j];
+        for (int j = 0; j < kBlock >> ROUNDS; ++j)
+          *reinterpret_cast<float2*>(y_row + (t + (j << ROUNDS)) * CT) = part[j];
       }
     }
     if (!all_lanes(ok)) return false;
@@ -645,10 +654,11 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
   return true;
 }
 
-// kVec: Params::vec.  kPiece: the first kernel (end state and sum of delta of each part of a split time axis, from a zero
-// state), else the second (outputs).
+// kVec: Params::vec.  kPiece: the first kernel (end state and sum of delta of each part of a split time
+// axis, from a zero state), else the second (outputs).
 template <typename T, int N, bool kPiece, bool kVec>
-__global__ void __launch_bounds__(kThreads, kResident) selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, kResident)
+    selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shared<T, N, kPiece, kVec>;
   constexpr int SPL = S::SPL, LW = 32 / S::LPC;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -953,7 +963,9 @@ SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dsta
   sp.sub_tokens = sp.part_tokens;
   const int64_t all = chains * sp.split;
   const bool one = all <= slots * 3 / 4;  // CTA an SM
-  if (all > kSmCount && (one ? sp.part_tokens >= 2 * kSubTokens : all > slots && all < 8 * slots && sp.part_tokens >= kSubTokens)) {
+  const bool queued = one ? all > kSmCount && sp.part_tokens >= 2 * kSubTokens
+                          : all > slots && all < 8 * slots && sp.part_tokens >= kSubTokens;
+  if (queued) {
     sp.ctas = one ? kSmCount : slots;
     sp.sub_tokens = sp.part_tokens < 2 * kSubTokens ? kSubTokens / 2 : kSubTokens;
     sp.subs = (int)((sp.part_tokens + sp.sub_tokens - 1) / sp.sub_tokens);
