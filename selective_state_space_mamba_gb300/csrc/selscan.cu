@@ -22,6 +22,8 @@
 // memory and 277 and 168 of exponentials.  The multiply-adds of two state entries read three register
 // pairs, which takes 3.2 cycles a warp instruction and not 2: the scan alone takes 109 cycles a token
 // for the two CTAs of an SM, the same as in registers only; with the other roles beside it, 177.
+#include <cstddef>
+
 #include "layer_common.cuh"
 #include "tc_common.cuh"
 
@@ -40,6 +42,18 @@ constexpr int kScanThreads = 128, kRoleThreads = 64, kThreads = kScanThreads + 3
 
 constexpr int kHand = 8;  // floats of a scan thread in the workspace
 
+// The queue's words lie in the workspace behind its header, in rows of kRowWords of which a call uses and clears
+// the first kRowUsed: the claim counter in the first row, the finished items of four chains in each later one.
+// So one 2-D clearing takes the header's status as the row in front of them and leaves the flag epoch beside it,
+// which the look-back kernels keep there from call to call.
+constexpr int kRowWords = 8, kRowUsed = 4;
+constexpr size_t kRowBytes = kRowWords * sizeof(uint32_t);
+static_assert(offsetof(WsHeader, epoch) == kRowUsed * sizeof(uint32_t) && kHeaderBytes % kRowBytes == 0,
+              "the status is in the first words of the header, the epoch behind them");
+// Tag of this kernel's errors in the status word: no epoch of a look-back call, whose waits a leftover error
+// would end.
+constexpr uint32_t kErrorTag = 0xffffffffu;
+
 // State entries of a lane's channel.  With two for 8 entries a tile has 64 channels like those of 16 entries:
 // the other roles take the time of 128 (b4 L4096 d2560: 221 us, with four 261).
 __host__ __device__ constexpr int lane_states(int n) { return n == 8 ? 2 : 4; }
@@ -48,8 +62,8 @@ __host__ __device__ constexpr int tile_channels(int n) { return kScanThreads * l
 struct Params {
   ssm_selscan_args a;
   SelscanSplit sp;
-  WsHeader* queue;   // claim counter and status; NULL: one item a CTA
-  uint32_t* done;    // [chains] items of the chain that are finished
+  WsHeader* hdr;     // status; NULL without a workspace
+  uint32_t* queue;   // claim counter, then finished items of each chain (finished); NULL: one item a CTA
   float* hand;       // [chains, scan threads, kHand] state between a chain's items
   LookbackCtl ctl;   // wait limit and fault injection
   float* E;          // [split - 1, batch, channels, dstate]
@@ -60,6 +74,10 @@ struct Params {
 struct Maps {
   CUtensorMap u, dt, z, B, C;
 };
+
+__device__ __forceinline__ uint32_t* finished(const Params& p, int64_t chain) {
+  return p.queue + kRowWords * (1 + chain / kRowUsed) + chain % kRowUsed;
+}
 
 // What an item is: a part of one channel tile's tokens.
 struct Item {
@@ -153,7 +171,7 @@ __device__ __forceinline__ bool wait_done(const uint32_t* done, uint32_t want, W
     if ((spins & 15u) == 15u) {
       if (ld_relaxed_u64(&hdr->status) != 0ull) return false;
       if (global_timer_ns() - t0 > limit_ns) {
-        record_error(hdr, 1u, SSM_ERR_TIMEOUT);
+        record_error(hdr, kErrorTag, SSM_ERR_TIMEOUT);
         return false;
       }
     }
@@ -243,10 +261,10 @@ template <int N, bool kPiece, typename S>
 __device__ __forceinline__ bool claim_item(const Params& p, S& s, uint32_t k, Item& it) {
   const int split = kPiece ? p.sp.split - 1 : p.sp.split;  // nothing starts from the last part's end
   const int64_t chains = p.a.batch * p.sp.tiles * split;
-  const int64_t id = !kPiece && p.queue ? (int64_t)atomicAdd(&p.queue->counter, 1u) : blockIdx.x;
+  const int64_t id = !kPiece && p.queue ? (int64_t)atomicAdd(p.queue, 1u) : blockIdx.x;
   if (id < chains * (kPiece ? 1 : p.sp.subs)) {
     it = item_of<tile_channels(N), kPiece>(p, id, split, chains);
-    it.ready = it.sub == 0 || load_done(&p.done[it.chain]) >= (uint32_t)it.sub;
+    it.ready = it.sub == 0 || load_done(finished(p, it.chain)) >= (uint32_t)it.sub;
   } else {
     it = Item{}, it.n = -1;
   }
@@ -483,7 +501,7 @@ __device__ __forceinline__ bool publish(const Params& p, const Item& it, S& s, u
   if (it.sub + 1 >= p.sp.subs) return true;
   if (!wait_tile(s.item_done, k, 4, p.ctl.spin_limit_ns)) return false;
   if (threadIdx.x == kScanThreads + 2 * kRoleThreads && it.id != p.ctl.stall_tile)
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&p.done[it.chain]), "r"((uint32_t)it.sub + 1) : "memory");
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(finished(p, it.chain)), "r"((uint32_t)it.sub + 1) : "memory");
   return true;
 }
 
@@ -715,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     if (claims || (role == 0 && !kVec))  // shared memory stays until the copies are there, whatever the other roles do
       for (uint32_t t = tile0 < S::RING ? 0 : tile0 - S::RING; t < tile0; ++t)
         ok = wait_tile(s.raw_full, t, S::RING, p.ctl.spin_limit_ns) && ok;
-    if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+    if (!ok && p.queue) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
     return;
   }
 
@@ -726,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     Item it;
     bool ok = next_item(p, s, k, it);
     if (!ok || it.n < 0) {
-      if (!ok && p.queue) record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+      if (!ok && p.queue) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
       return;
     }
     float A[2][SPL], h[2][SPL], delta_sum[2] = {};
@@ -743,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     if constexpr (!kPiece) {
       if (it.sub > 0) {
         if ((tid & 31) == 0 && !it.ready)
-          ok = wait_done(&p.done[it.chain], (uint32_t)it.sub, p.queue, p.ctl.spin_limit_ns);
+          ok = wait_done(finished(p, it.chain), (uint32_t)it.sub, p.hdr, p.ctl.spin_limit_ns);
         ok = all_lanes(ok);
         if constexpr (SPL == 4) {
           const float4 v = load_hand(hand), w = load_hand(hand + 1);
@@ -807,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     }
     if (kPiece || !p.queue) return;
     if (!all_lanes(ok)) {  // the other roles' waits, and those of the chain's later items, run out
-      record_error(p.queue, 1u, SSM_ERR_TIMEOUT);
+      record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
       return;
     }
     if ((tid & 31) == 0) mbar_arrive(&s.item_done[k & 3]);
@@ -826,17 +844,17 @@ cudaError_t with_dstate(int n, F&& f) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: header and finished items of every chain (each call clears both), the chains' states, E, T.
+// Workspace: header, queue (each call clears its words and the header's status), the chains' states, E, T.
 struct Layout {
-  size_t done, hand, E, T, total;
+  size_t queue_rows, hand, E, T, total;
 };
 Layout layout(const SelscanSplit& sp, int64_t batch, int channels, int dstate) {
   Layout l{};
   if (sp.subs == 1 && sp.split == 1) return l;
   const size_t chains = sp.subs > 1 ? (size_t)(batch * sp.tiles * sp.split) : 0;
   const size_t rows = (size_t)(sp.split - 1) * batch * channels;
-  l.done = kHeaderBytes;
-  l.hand = up256(l.done + 4 * chains);
+  l.queue_rows = chains > 0 ? 1 + (chains + kRowUsed - 1) / kRowUsed : 0;
+  l.hand = up256(kHeaderBytes + l.queue_rows * kRowBytes);
   l.E = up256(l.hand + chains * kScanThreads * kHand * sizeof(float));
   l.T = up256(l.E + rows * dstate * sizeof(float));
   l.total = up256(l.T + rows * sizeof(float));
@@ -850,9 +868,9 @@ Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
   p.ctl = next_lookback_ctl();
   const Layout l = layout(sp, a.batch, a.channels, a.dstate);
   char* ws = static_cast<char*>(workspace);
+  if (sp.bytes > 0) p.hdr = reinterpret_cast<WsHeader*>(ws);
   if (sp.subs > 1) {
-    p.queue = reinterpret_cast<WsHeader*>(ws);
-    p.done = reinterpret_cast<uint32_t*>(ws + l.done);
+    p.queue = reinterpret_cast<uint32_t*>(ws + kHeaderBytes);
     p.hand = reinterpret_cast<float*>(ws + l.hand);
   }
   if (sp.split > 1) {
@@ -896,10 +914,12 @@ cudaError_t make_maps(const Params& p, Maps* m) {
 
 template <bool kPiece>
 cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace, cudaStream_t s) {
-  // the first kernel of a call that has a workspace follows the clearing of its header
+  // the first kernel of a call that has a workspace follows the clearing of the status and the queue
   const bool clears = sp.bytes > 0 && (kPiece || sp.split == 1);
   if (clears) {
-    const cudaError_t e = cudaMemsetAsync(workspace, 0, layout(sp, a.batch, a.channels, a.dstate).hand, s);
+    const size_t queue_rows = layout(sp, a.batch, a.channels, a.dstate).queue_rows;
+    const size_t rows = queue_rows > 0 ? kHeaderBytes / kRowBytes + queue_rows : 1;
+    const cudaError_t e = cudaMemset2DAsync(workspace, kRowBytes, 0, kRowUsed * sizeof(uint32_t), rows, s);
     if (e != cudaSuccess) return e;
   }
   const Params p = make_params(a, sp, workspace);
