@@ -246,6 +246,8 @@ PyObject* selscan_fwd(PyObject* const* v) {
   at::Tensor ws;
   if (v[14] != Py_None) {
     ws = tensor("workspace", v[14]);
+    if (ws.device() != like.device || ws.scalar_type() != at::kByte || !ws.is_contiguous())
+      fail("workspace", "contiguous bytes on u's device");
   } else {
     const size_t need = g_fn.selscan_fwd_workspace_bytes(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups);
     if (need) ws = like.empty({(int64_t)need}, at::kByte);

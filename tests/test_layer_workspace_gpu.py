@@ -115,3 +115,25 @@ def test_leftover_error_ends_no_wait_of_another_operation():
     h = ssm.linscan_fwd(P.to_dev(inp["a"]), P.to_dev(inp["b"]), workspace=ws)
     P.assert_rows_close(P.to_np(h), native.linscan(inp["a"], inp["b"]), "linscan after the error")
     assert ssm.check_device_status(ws) == _lib.SSM_ERR_TIMEOUT and ssm.check_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("case", [(1, 8, 16), SPLIT], ids=str)
+def test_workspace_of_another_device_or_type_is_refused(case):
+    """On the host: the kernels would follow its pointer."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+
+    class Floats(ssm.Workspace):
+        def ensure(self, nbytes):
+            return super().ensure(nbytes).view(torch.float32)
+
+    class EverySecond(ssm.Workspace):
+        def ensure(self, nbytes):
+            return super().ensure(2 * nbytes)[::2]
+
+    args = scan_case(case, 1)
+    for ws in (ssm.Workspace("cpu"), Floats("cuda"), EverySecond("cuda")):
+        with pytest.raises(ValueError, match="workspace"):
+            ssm.selscan_fwd(*args, workspace=ws)
+    ssm.selscan_fwd(*args, workspace=ssm.Workspace("cuda"))
+    torch.cuda.synchronize()
