@@ -36,6 +36,14 @@ struct Refusal {
   throw Refusal{PyExc_ValueError, std::string(name) + " must be " + want};
 }
 
+// A size that the C entry points take in 32 bits.  They refuse what is too many for the kernels, but not what a
+// cast has made small before they see it.
+struct Unsupported {};
+int narrow(int64_t v) {
+  if (v != (int64_t)(int)v) throw Unsupported{};
+  return (int)v;
+}
+
 using Sizes = c10::IntArrayRef;
 std::string text_of(Sizes s) {
   std::string r = "[";
@@ -50,20 +58,23 @@ const at::Tensor& tensor(const char* name, PyObject* o) {
 
 // The first tensor's type and device, which the others are held to.
 struct Like {
+  const char* name;
   c10::ScalarType type;
   c10::Device device;
   ssm_dtype code;
   int bytes;
 
-  explicit Like(const char* name, const at::Tensor& t) : type(t.scalar_type()), device(t.device()) {
+  explicit Like(const char* name, const at::Tensor& t) : name(name), type(t.scalar_type()), device(t.device()) {
     if (type != at::kFloat && type != at::kBFloat16)
       throw Refusal{PyExc_TypeError, std::string("unsupported dtype ") + c10::toString(type) + " (float32 or bfloat16)"};
-    if (!device.is_cuda()) fail(name, "a CUDA tensor");
     code = type == at::kFloat ? SSM_F32 : SSM_BF16;
     bytes = type == at::kFloat ? 4 : 2;
   }
   // the C call goes to the current device
-  c10::cuda::CUDAGuard guard() const { return c10::cuda::CUDAGuard(device); }
+  c10::cuda::CUDAGuard guard() const {
+    if (!device.is_cuda()) fail(name, "a CUDA tensor");
+    return c10::cuda::CUDAGuard(device);
+  }
   ssm_stream_t stream() const {
     return reinterpret_cast<ssm_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
   }
@@ -166,9 +177,10 @@ int64_t step_states(Out& out, PyObject* state, PyObject* state_out, bool inplace
 PyObject* conv_fwd(PyObject* const* v) {  // x, weight, bias, state, lens, silu, y, state_out, return_final_state
   const at::Tensor &x = tensor("x", v[0]), &w = tensor("weight", v[1]);
   const Like like("x", x);
-  const auto guard = like.guard();
   if (x.dim() != 3 || w.dim() != 2) fail("x, weight", "[b, L, d] and [d, W]");
-  const int64_t b = x.size(0), L = x.size(1), d = x.size(2), W = w.size(1);
+  const int64_t b = x.size(0), L = x.size(1);
+  const int d = narrow(x.size(2)), W = narrow(w.size(1));
+  const auto guard = like.guard();
   const ssm_tokens xt = tokens("x", x, {b, L, d}, like);
   const float* wp = static_cast<const float*>(dense("weight", w, {d, W}, at::kFloat, like));
   const float* bias = floats("bias", v[2], {d}, like);
@@ -177,7 +189,7 @@ PyObject* conv_fwd(PyObject* const* v) {  // x, weight, bias, state, lens, silu,
   Out y, so;
   y.set("y", v[6], {b, L, d}, like.type, like);
   if (PyObject_IsTrue(v[8])) so.set("state_out", v[7], {b, W - 1, d}, like.type, like);
-  const ssm_status st = g_fn.conv_fwd(xt, wp, bias, state, lens, y.ptr, so.ptr, b, L, (int)d, (int)W,
+  const ssm_status st = g_fn.conv_fwd(xt, wp, bias, state, lens, y.ptr, so.ptr, b, L, d, W,
                                       PyObject_IsTrue(v[5]) ? SSM_ACT_SILU : SSM_ACT_NONE, like.code, like.stream());
   return result(st, y, so);
 }
@@ -185,9 +197,10 @@ PyObject* conv_fwd(PyObject* const* v) {  // x, weight, bias, state, lens, silu,
 PyObject* conv_step(PyObject* const* v) {  // x, weight, bias, state, slots, silu, y, state_out, inplace
   const at::Tensor &x = tensor("x", v[0]), &w = tensor("weight", v[1]);
   const Like like("x", x);
-  const auto guard = like.guard();
   if (x.dim() != 2 || w.dim() != 2) fail("x, weight", "[b, d] and [d, W]");
-  const int64_t b = x.size(0), d = x.size(1), W = w.size(1);
+  const int64_t b = x.size(0);
+  const int d = narrow(x.size(1)), W = narrow(w.size(1));
+  const auto guard = like.guard();
   const ssm_tokens xt = tokens("x", x, {b, d}, like);
   const float* wp = static_cast<const float*>(dense("weight", w, {d, W}, at::kFloat, like));
   const float* bias = floats("bias", v[2], {d}, like);
@@ -196,7 +209,7 @@ PyObject* conv_step(PyObject* const* v) {  // x, weight, bias, state, slots, sil
   const int64_t n = step_states(so, v[3], v[7], PyObject_IsTrue(v[8]), slots, b, W - 1, d, like.type, like);
   const void* state = optional("state", v[3], {n, W - 1, d}, like.type, like);
   y.set("y", v[6], {b, d}, like.type, like);
-  const ssm_status st = g_fn.conv_step(xt, wp, bias, state, slots, y.ptr, so.ptr, b, n, (int)d, (int)W,
+  const ssm_status st = g_fn.conv_step(xt, wp, bias, state, slots, y.ptr, so.ptr, b, n, d, W,
                                        PyObject_IsTrue(v[5]) ? SSM_ACT_SILU : SSM_ACT_NONE, like.code, like.stream());
   return result(st, y, so);
 }
@@ -205,11 +218,10 @@ PyObject* conv_step(PyObject* const* v) {  // x, weight, bias, state, slots, sil
 ssm_selscan_args selscan_args(PyObject* const* v, const Like& like, const at::Tensor& u, int lead) {
   ssm_selscan_args a{};
   const Sizes sizes = u.sizes();
-  const int64_t d = sizes.back();
   const at::Tensor &B = tensor("B", v[3]), &C = tensor("C", v[4]);
   if (B.dim() != lead + 2 || B.sizes().slice(0, lead) != sizes.slice(0, lead))
     fail("B", text_of(sizes.slice(0, lead)) + " and groups, states");
-  const int64_t G = B.size(lead), N = B.size(lead + 1);
+  const int d = narrow(sizes.back()), G = narrow(B.size(lead)), N = narrow(B.size(lead + 1));
   a.u = tokens("u", u, sizes, like);
   a.dt = tokens("dt", tensor("dt", v[1]), sizes, like);
   a.B = tokens("B", B, B.sizes(), like);
@@ -220,9 +232,9 @@ ssm_selscan_args selscan_args(PyObject* const* v, const Like& like, const at::Te
   a.D = floats("D", v[5], {d}, like);
   a.dt_bias = floats("dt_bias", v[7], {d}, like);
   a.batch = sizes[0];
-  a.channels = (int32_t)d;
-  a.dstate = (int32_t)N;
-  a.ngroups = (int32_t)G;
+  a.channels = d;
+  a.dstate = N;
+  a.ngroups = G;
   a.dtype = like.code;
   return a;
 }
@@ -231,9 +243,9 @@ ssm_selscan_args selscan_args(PyObject* const* v, const Like& like, const at::Te
 PyObject* selscan_fwd(PyObject* const* v) {
   const at::Tensor& u = tensor("u", v[0]);
   const Like like("u", u);
-  const auto guard = like.guard();
   if (u.dim() != 3) fail("u", "[b, L, d]");
   ssm_selscan_args a = selscan_args(v, like, u, 2);
+  const auto guard = like.guard();
   a.seqlen = u.size(1);
   a.softplus = PyObject_IsTrue(v[10]);
   a.h0 = floats("h0", v[8], {a.batch, a.channels, a.dstate}, like);
@@ -261,9 +273,9 @@ PyObject* selscan_fwd(PyObject* const* v) {
 PyObject* selscan_step(PyObject* const* v) {
   const at::Tensor& u = tensor("u", v[0]);
   const Like like("u", u);
-  const auto guard = like.guard();
   if (u.dim() != 2) fail("u", "[b, d]");
   ssm_selscan_args a = selscan_args(v, like, u, 1);
+  const auto guard = like.guard();
   a.seqlen = 1;
   a.softplus = PyObject_IsTrue(v[10]);
   const int32_t* slots = ints("slots", v[9], a.batch, like);
@@ -281,15 +293,17 @@ PyObject* selscan_step(PyObject* const* v) {
 struct Norm {
   const at::Tensor& x;
   Like like;
-  int64_t d, rows, stride;
+  int d;
+  c10::cuda::CUDAGuard guard;
+  int64_t rows, stride;
   const float* w;
   const void* residual = nullptr;
   ssm_dtype res_code;
   Out residual_out;
 
-  Norm(PyObject* xo, PyObject* wo, PyObject* ro, PyObject* oo) : x(tensor("x", xo)), like("x", x) {
+  Norm(PyObject* xo, PyObject* wo, PyObject* ro, PyObject* oo)
+      : x(tensor("x", xo)), like("x", x), d(x.dim() ? narrow(x.size(-1)) : 0), guard(like.guard()) {
     const Sizes sizes = x.sizes();
-    d = sizes.empty() ? 0 : sizes.back();
     rows = d ? x.numel() / d : 0;
     if (x.is_contiguous())
       stride = d;
@@ -313,30 +327,29 @@ struct Norm {
 
 PyObject* rmsnorm_fwd(PyObject* const* v) {  // x, weight, residual, eps, y, residual_out
   Norm n(v[0], v[1], v[2], v[5]);
-  const auto guard = n.like.guard();
   const double eps = PyFloat_AsDouble(v[3]);
   if (eps == -1.0 && PyErr_Occurred()) return nullptr;
   Out y;
   y.set("y", v[4], n.x.sizes(), n.like.type, n.like);
-  return result(g_fn.rmsnorm_fwd(n.x.data_ptr(), n.stride, n.w, n.residual, n.residual_out.ptr, y.ptr, n.rows, (int)n.d,
+  return result(g_fn.rmsnorm_fwd(n.x.data_ptr(), n.stride, n.w, n.residual, n.residual_out.ptr, y.ptr, n.rows, n.d,
                                  (float)eps, n.like.code, n.res_code, n.like.stream()),
                 y, n.residual_out);
 }
 
 PyObject* rmsnorm_fp8_fwd(PyObject* const* v) {  // x, weight, residual, eps, group, q, scale, residual_out
-  Norm n(v[0], v[1], v[2], v[7]);
-  const auto guard = n.like.guard();
   const double eps = PyFloat_AsDouble(v[3]);
-  const long group = PyLong_AsLong(v[4]);
+  const long of = PyLong_AsLong(v[4]);
   if (PyErr_Occurred()) return nullptr;
+  const int group = narrow(of);
+  Norm n(v[0], v[1], v[2], v[7]);
   Out q, scale;
   q.set("q", v[5], n.x.sizes(), at::kFloat8_e4m3fn, n.like);
   c10::SmallVector<int64_t, 8> sizes(n.x.sizes().begin(), n.x.sizes().end());
   if (!sizes.empty()) sizes.pop_back();
-  if (group != 0) sizes.push_back((n.d + 127) / 128);
+  if (group != 0) sizes.push_back(((int64_t)n.d + 127) / 128);
   scale.set("scale", v[6], sizes, at::kFloat, n.like);
   const ssm_status st = g_fn.rmsnorm_fp8_fwd(n.x.data_ptr(), n.stride, n.w, n.residual, n.residual_out.ptr, q.ptr,
-                                             static_cast<float*>(scale.ptr), n.rows, (int)n.d, (int)group, (float)eps,
+                                             static_cast<float*>(scale.ptr), n.rows, n.d, group, (float)eps,
                                              n.like.code, n.res_code, n.like.stream());
   if (st != SSM_OK) return PyLong_FromLong(st);
   PyObject* t = PyTuple_New(3);
@@ -354,6 +367,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != ARGS) throw Refusal{PyExc_TypeError, "wrong number of arguments"};
     if (!g_fn.conv_fwd) throw Refusal{PyExc_RuntimeError, "the library is not bound"};
     return F(args);
+  } catch (const Unsupported&) {
+    return PyLong_FromLong(SSM_ERR_UNSUPPORTED);
   } catch (const Refusal& r) {
     PyErr_SetString(r.kind, r.text.c_str());
   } catch (const c10::OutOfMemoryError& e) {

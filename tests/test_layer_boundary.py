@@ -224,3 +224,39 @@ def test_oracle_rmsnorm():
     x, res, w = r.standard_normal((3, 10)), r.standard_normal((3, 10)), r.standard_normal(10)
     v, err, s = ol.rmsnorm(x, w, res, eps=0.0)
     assert np.allclose(s, x + res) and np.allclose((v / w) ** 2 @ np.ones(10), 10) and (err >= 0).all()
+
+
+# ------------------------------------------------------------------------------ sizes that 32 bits do not hold
+
+WRAPS = (1 << 32) + 256  # 256 in 32 bits
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_python_sizes_that_wrap_are_refused(dtype):
+    """Columns, widths, states, groups: refused as any other size beyond the kernels, not taken for the size that
+    is left of them in 32 bits.  (Tensors without memory: the sizes are looked at before the device is.)"""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    t = lambda *n: torch.empty(n, device="meta", dtype=getattr(torch, dtype))  # noqa: E731
+    f = lambda *n: torch.empty(n, device="meta")  # noqa: E731
+    n = WRAPS
+    calls = [
+        lambda: ssm.conv_fwd(t(1, 1, n), f(n, 4)), lambda: ssm.conv_fwd(t(1, 1, 8), f(8, (1 << 32) + 4)),
+        lambda: ssm.conv_step(t(1, n), f(n, 4)), lambda: ssm.conv_step(t(1, 8), f(8, (1 << 32) + 4)),
+        lambda: ssm.selscan_fwd(t(1, 1, n), t(1, 1, n), f(n, 16), t(1, 1, 1, 16), t(1, 1, 1, 16)),
+        lambda: ssm.selscan_fwd(t(1, 1, 8), t(1, 1, 8), f(8, n), t(1, 1, 1, n), t(1, 1, 1, n)),
+        lambda: ssm.selscan_fwd(t(1, 1, 8), t(1, 1, 8), f(8, 16), t(1, 1, n, 16), t(1, 1, n, 16)),
+        lambda: ssm.selscan_step(t(1, n), t(1, n), f(n, 16), t(1, 1, 16), t(1, 1, 16)),
+        lambda: ssm.selscan_step(t(1, 8), t(1, 8), f(8, n), t(1, 1, n), t(1, 1, n)),
+        lambda: ssm.selscan_step(t(1, 8), t(1, 8), f(8, 16), t(1, n, 16), t(1, n, 16)),
+        lambda: ssm.rmsnorm_fwd(t(1, n), f(n)), lambda: ssm.rmsnorm_fp8_fwd(t(1, n), f(n)),
+        lambda: ssm.rmsnorm_fp8_fwd(t(1, 8), f(8), group=1 << 32),
+        lambda: ssm.rmsnorm_fp8_fwd(t(1, 8), f(8), group=(1 << 32) + 128),
+        lambda: ssm.rmsnorm_fp8_fwd(t(1, 8), f(8), group=-(1 << 32)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ssm.SsmError, match="SSM_ERR_UNSUPPORTED"):
+            call()
+            pytest.fail(f"call {i} was taken")
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ssm.conv_fwd(t(1, 1, 8), f(8, 4))
