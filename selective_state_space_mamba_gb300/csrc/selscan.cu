@@ -42,14 +42,6 @@ constexpr int kScanThreads = 128, kRoleThreads = 64, kThreads = kScanThreads + 3
 
 constexpr int kHand = 8;  // floats of a scan thread in the workspace
 
-// The queue's words lie in the workspace behind its header, in rows of kRowWords of which a call uses and clears
-// the first kRowUsed: the claim counter in the first row, the finished items of four chains in each later one.
-// So one 2-D clearing takes the header's status as the row in front of them and leaves the flag epoch beside it,
-// which the look-back kernels keep there from call to call.
-constexpr int kRowWords = 8, kRowUsed = 4;
-constexpr size_t kRowBytes = kRowWords * sizeof(uint32_t);
-static_assert(offsetof(WsHeader, epoch) == kRowUsed * sizeof(uint32_t) && kHeaderBytes % kRowBytes == 0,
-              "the status is in the first words of the header, the epoch behind them");
 // Tag of this kernel's errors in the status word: no epoch of a look-back call, whose waits a leftover error
 // would end.
 constexpr uint32_t kErrorTag = 0xffffffffu;
@@ -63,7 +55,7 @@ struct Params {
   ssm_selscan_args a;
   SelscanSplit sp;
   WsHeader* hdr;     // status; NULL without a workspace
-  uint32_t* queue;   // claim counter, then finished items of each chain (finished); NULL: one item a CTA
+  uint32_t* queue;   // claim counter, then finished items of each chain; NULL: one item a CTA
   float* hand;       // [chains, scan threads, kHand] state between a chain's items
   LookbackCtl ctl;   // wait limit and fault injection
   float* E;          // [split - 1, batch, channels, dstate]
@@ -76,7 +68,7 @@ struct Maps {
 };
 
 __device__ __forceinline__ uint32_t* finished(const Params& p, int64_t chain) {
-  return p.queue + kRowWords * (1 + chain / kRowUsed) + chain % kRowUsed;
+  return p.queue + 1 + chain;
 }
 
 // What an item is: a part of one channel tile's tokens.
@@ -699,6 +691,10 @@ __global__ void __launch_bounds__(kThreads, kResident)
     fence_mbar_init();
   }
   griddep_wait();
+  if (kPiece && p.queue) {
+    const int64_t words = 1 + p.a.batch * p.sp.tiles * p.sp.split;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < words; i += (int64_t)gridDim.x * kThreads) p.queue[i] = 0;
+  }
   __syncthreads();
   const ssm_selscan_args& a = p.a;
   // Each role goes through the CTA's items by itself, so the copies of an item come in beside the
@@ -844,17 +840,18 @@ cudaError_t with_dstate(int n, F&& f) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: header, queue (each call clears its words and the header's status), the chains' states, E, T.
+// Workspace: header, queue, the chains' states, E, T.  Each call clears the queue and the header's status; the flag
+// epoch behind it is the look-back kernels', which keep it there from call to call.
 struct Layout {
-  size_t queue_rows, hand, E, T, total;
+  size_t queue_words, hand, E, T, total;
 };
 Layout layout(const SelscanSplit& sp, int64_t batch, int channels, int dstate) {
   Layout l{};
   if (sp.subs == 1 && sp.split == 1) return l;
   const size_t chains = sp.subs > 1 ? (size_t)(batch * sp.tiles * sp.split) : 0;
   const size_t rows = (size_t)(sp.split - 1) * batch * channels;
-  l.queue_rows = chains > 0 ? 1 + (chains + kRowUsed - 1) / kRowUsed : 0;
-  l.hand = up256(kHeaderBytes + l.queue_rows * kRowBytes);
+  l.queue_words = chains > 0 ? 1 + chains : 0;
+  l.hand = up256(kHeaderBytes + l.queue_words * sizeof(uint32_t));
   l.E = up256(l.hand + chains * kScanThreads * kHand * sizeof(float));
   l.T = up256(l.E + rows * dstate * sizeof(float));
   l.total = up256(l.T + rows * sizeof(float));
@@ -914,12 +911,14 @@ cudaError_t make_maps(const Params& p, Maps* m) {
 
 template <bool kPiece>
 cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace, cudaStream_t s) {
-  // the first kernel of a call that has a workspace follows the clearing of the status and the queue
+  // the first kernel of a call that has a workspace follows the clearing of the status, and of the queue unless it is
+  // the piece kernel, which clears that for the second (a clearing is a launch of 1.1 us, one in 2-D for both 3.6)
   const bool clears = sp.bytes > 0 && (kPiece || sp.split == 1);
   if (clears) {
-    const size_t queue_rows = layout(sp, a.batch, a.channels, a.dstate).queue_rows;
-    const size_t rows = queue_rows > 0 ? kHeaderBytes / kRowBytes + queue_rows : 1;
-    const cudaError_t e = cudaMemset2DAsync(workspace, kRowBytes, 0, kRowUsed * sizeof(uint32_t), rows, s);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, offsetof(WsHeader, epoch), s);
+    if (e == cudaSuccess && !kPiece && sp.subs > 1)
+      e = cudaMemsetAsync(static_cast<char*>(workspace) + kHeaderBytes, 0,
+                          layout(sp, a.batch, a.channels, a.dstate).queue_words * sizeof(uint32_t), s);
     if (e != cudaSuccess) return e;
   }
   const Params p = make_params(a, sp, workspace);
