@@ -310,8 +310,10 @@ SSM_API ssm_status ssm_conv_step(ssm_tokens x, const float *w, const float *bias
  * kernel, which runs the parts but the last from a zero state), and cut into items that the CTAs
  * claim in order where there are somewhat more than fill it; an item then waits (bounded) for
  * the state of the one before.  Each call clears what it needs cleared, so the workspace need not be
- * zero-filled and carries nothing from call to call; ssm_check_device_status reports the last
- * call's waits.  An item whose wait ran out leaves NaN in its outputs.
+ * zero-filled and carries nothing from call to call.  It clears the status word too, so
+ * ssm_check_device_status reports the waits of the last call that used the workspace (a call that
+ * needs none does not touch it, and has no status).  Waits are bounded; after one that ran out
+ * every element of y and h_final is right or NaN, with or without a workspace.
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_WORKSPACE,
  *   SSM_ERR_CUDA.
  */
@@ -482,6 +484,8 @@ SSM_API ssm_status ssm_check_device_status(void *workspace, ssm_stream_t stream)
  * kernel skips publishing its aggregate and prefix, and every wait gives up after
  * `spin_limit_ns` nanoseconds (0: the default of 1 s).  The waiting tiles then record
  * SSM_ERR_TIMEOUT in the status word and return; no kernel waits without a limit.
+ * In ssm_selscan_fwd the index is an item's: of its queue, or without one the CTA's; at
+ * 2^40 + its index the item's copies give up instead.
  */
 SSM_API void ssm_debug_set_lookback_fault(int64_t stall_tile, uint64_t spin_limit_ns);
 

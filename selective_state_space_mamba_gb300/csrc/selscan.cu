@@ -45,6 +45,11 @@ constexpr int kHand = 8;  // floats of a scan thread in the workspace
 // Tag of this kernel's errors in the status word: no epoch of a look-back call, whose waits a leftover error
 // would end.
 constexpr uint32_t kErrorTag = 0xffffffffu;
+// In a chain's word for its finished items: an item's state is lost, and so are those after it.
+constexpr uint32_t kLost = 0x80000000u;
+constexpr uint64_t kCopiesNs = 1000000000;  // for copies in flight, whatever the limit of the other waits
+// Test hook (ssm_debug_set_lookback_fault): at this and an item's number its copies give up.
+constexpr int64_t kStallCopies = (int64_t)1 << 40;
 
 // State entries of a lane's channel.  With two for 8 entries a tile has 64 channels like those of 16 entries:
 // the other roles take the time of 128 (b4 L4096 d2560: 221 us, with four 261).
@@ -103,6 +108,11 @@ struct Shared {
   uint64_t raw_full[RING], raw_free[RING], full[2], done[2], y_free[2];
   // and of the items: written down, read, scanned (the finish role may be two items behind the scan)
   uint64_t item_full[2], item_free[2], item_done[4];
+  // What void_items needs once a wait has run out: the last items' numbers and how many were claimed, how many each
+  // scan and finish warp is through with, the phase at which all warps have left, and whether one gave up.
+  int64_t claimed[8];
+  uint32_t claims, closed[(kScanThreads + kRoleThreads) / 32], failed;
+  uint64_t left;
 };
 
 // Channels vc to vc + 7 of a row of Shared::y.
@@ -153,12 +163,18 @@ __device__ __forceinline__ uint32_t load_done(const uint32_t* done) {
   return v;
 }
 
-// Waits until the chain has `want` finished items; false after the limit, or once another wait gave up.
-// One thread.
+// The item after which the chain's state is there (or lost); it never goes back.
+__device__ __forceinline__ void raise_done(uint32_t* done, uint32_t to) {
+  asm volatile("red.release.gpu.global.max.u32 [%0], %1;" ::"l"(done), "r"(to) : "memory");
+}
+
+// Waits until the chain has `want` finished items; false after the limit, once another wait gave up, or if
+// its state is lost.  One thread.
 __device__ __forceinline__ bool wait_done(const uint32_t* done, uint32_t want, WsHeader* hdr, uint64_t limit_ns) {
   uint64_t t0 = 0;
   for (uint32_t spins = 0;; ++spins) {
-    if (load_done(done) >= want) return true;
+    const uint32_t v = load_done(done);
+    if (v >= want) return v < kLost;
     if (spins == 0) t0 = global_timer_ns();
     if ((spins & 15u) == 15u) {
       if (ld_relaxed_u64(&hdr->status) != 0ull) return false;
@@ -223,6 +239,17 @@ __device__ __forceinline__ bool wait_tile(uint64_t* bars, uint32_t tile, uint32_
   }
 }
 
+// Whether a barrier's phase of this parity is complete.
+__device__ __forceinline__ bool mbar_phase_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // After a wait that ran out (never but on a GPU that stopped): a state that cannot pass for one.
 template <int SPL>
 __device__ __forceinline__ void set_nan(float (&h)[2][SPL]) {
@@ -256,7 +283,10 @@ __device__ __forceinline__ bool claim_item(const Params& p, S& s, uint32_t k, It
   const int64_t id = !kPiece && p.queue ? (int64_t)atomicAdd(p.queue, 1u) : blockIdx.x;
   if (id < chains * (kPiece ? 1 : p.sp.subs)) {
     it = item_of<tile_channels(N), kPiece>(p, id, split, chains);
-    it.ready = it.sub == 0 || load_done(finished(p, it.chain)) >= (uint32_t)it.sub;
+    const uint32_t v = it.sub == 0 ? 0 : load_done(finished(p, it.chain));
+    it.ready = v >= (uint32_t)it.sub && v < kLost;
+    s.claimed[k & 7] = id;
+    s.claims = k + 1;
   } else {
     it = Item{}, it.n = -1;
   }
@@ -341,12 +371,14 @@ __device__ __forceinline__ void load_column8(const ssm_tokens& x, int64_t b, int
   for (int j = 0; j < 8; ++j) v[j] = to_f32(row0[j][c + ((offset + j * (uint32_t)x.token_stride) & kMask)]);
 }
 
-// The roles' parts of an item.  `tile`: the CTA's tiles before it.  False if a wait ran out.
+// The roles' parts of an item.  `tile`: the CTA's tiles before it (of the copy role, which counts its own on: tiles
+// whose copies it has started).  False if a wait ran out.
 template <typename T, int N, bool kPiece, bool kVec>
 __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, const Item& it,
-                                          Shared<T, N, kPiece, kVec>& s, uint32_t tile) {
+                                          Shared<T, N, kPiece, kVec>& s, uint32_t& tile) {
   constexpr int CT = tile_channels(N), RING = Shared<T, N, kPiece, kVec>::RING;
   const ssm_selscan_args& a = p.a;
+  if (it.id + kStallCopies == p.ctl.stall_tile) return false;
   int64_t t = it.t_begin;
   if constexpr (kVec) {
     const int tid = threadIdx.x % kRoleThreads;
@@ -493,7 +525,7 @@ __device__ __forceinline__ bool publish(const Params& p, const Item& it, S& s, u
   if (it.sub + 1 >= p.sp.subs) return true;
   if (!wait_tile(s.item_done, k, 4, p.ctl.spin_limit_ns)) return false;
   if (threadIdx.x == kScanThreads + 2 * kRoleThreads && it.id != p.ctl.stall_tile)
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(finished(p, it.chain)), "r"((uint32_t)it.sub + 1) : "memory");
+    raise_done(finished(p, it.chain), (uint32_t)it.sub + 1);
   return true;
 }
 
@@ -664,6 +696,67 @@ __device__ __forceinline__ bool scan_role(const Params& p, const Item& it, S& s,
   return true;
 }
 
+// NaN in the outputs of an item and, for the items of its chain that follow, in place of its state.  Any number of
+// lanes.
+template <typename T, int N, bool kPiece>
+__device__ void void_item(const Params& p, const Item& it, int lane, int lanes) {
+  const ssm_selscan_args& a = p.a;
+  const float nan = __int_as_float(0x7fffffff);
+  const bool last = !kPiece && it.sub + 1 == p.sp.subs && it.part == p.sp.split - 1;
+  float* state = kPiece ? p.E + ((int64_t)it.part * a.batch + it.b) * a.channels * N
+                        : last && a.h_final ? a.h_final + it.b * a.channels * N : nullptr;
+  if (state)
+    for (int64_t i = lane; i < (int64_t)it.cn * N; i += lanes) state[(int64_t)it.c0 * N + i] = nan;
+  if constexpr (kPiece) {
+    float* sum = p.T + ((int64_t)it.part * a.batch + it.b) * a.channels + it.c0;
+    for (int c = lane; c < it.cn; c += lanes) sum[c] = 0.f;
+  } else {
+    T* y = static_cast<T*>(a.y) + (it.b * a.seqlen + it.t_begin) * a.channels + it.c0;
+    for (int t = 0; t < it.n; ++t, y += a.channels)
+      for (int c = lane; c < it.cn; c += lanes) y[c] = from_f32<T>(t < it.live ? nan : 0.f);
+    if (lane == 0 && !last && p.queue) raise_done(finished(p, it.chain), kLost);
+  }
+}
+
+// After a wait between the roles ran out: what this CTA has claimed and not written, and what nobody has claimed yet
+// (the other CTAs may have given up too).
+template <typename T, int N, bool kPiece, bool kVec>
+__device__ __forceinline__ void void_items(const Params& p, const Shared<T, N, kPiece, kVec>& s, int lane, int lanes) {
+  const int split = kPiece ? p.sp.split - 1 : p.sp.split;
+  const int64_t chains = p.a.batch * p.sp.tiles * split;
+  uint32_t k = s.claims;
+  for (int w = 0; w < (kPiece ? kScanThreads : kScanThreads + kRoleThreads) / 32; ++w) k = min(k, s.closed[w]);
+  for (; k < s.claims; ++k)
+    void_item<T, N, kPiece>(p, item_of<tile_channels(N), kPiece>(p, s.claimed[k & 7], split, chains), lane, lanes);
+  while (!kPiece && p.queue) {
+    int64_t id = 0;
+    if (lane == 0) id = atomicAdd(p.queue, 1u);
+    if (lanes > 1) id = __shfl_sync(0xffffffffu, id, 0);
+    if (id >= chains * p.sp.subs) return;
+    void_item<T, N, kPiece>(p, item_of<tile_channels(N), kPiece>(p, id, split, chains), lane, lanes);
+  }
+}
+
+// The last thing of each warp (of tensor copies: of the one thread).  The last of them to leave writes what a wait
+// that ran out has left unwritten.  (Two may take themselves for the last, and then write the same.)
+template <typename T, int N, bool kPiece, bool kVec>
+__device__ __forceinline__ void leave(const Params& p, Shared<T, N, kPiece, kVec>& s, bool ok, int lanes) {
+  const int lane = lanes > 1 ? (int)(threadIdx.x & 31) : 0;
+  if (lanes > 1) ok = all_lanes(ok);
+  bool clear = false;
+  if (lane == 0) {
+    volatile uint32_t* failed = &s.failed;
+    if (!ok) {
+      *failed = 1;
+      if (p.hdr) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
+    }
+    mbar_arrive(&s.left);
+    clear = mbar_phase_done(&s.left, 0) && *failed != 0;
+  }
+  if (lanes > 1) clear = __any_sync(0xffffffffu, clear);
+  if (clear) void_items<T, N, kPiece, kVec>(p, s, lane, lanes);
+}
+
 // kVec: Params::vec.  kPiece: the first kernel (end state and sum of delta of each part of a split time
 // axis, from a zero state), else the second (outputs).
 template <typename T, int N, bool kPiece, bool kVec>
@@ -671,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     selscan_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shared<T, N, kPiece, kVec>;
   constexpr int SPL = S::SPL, LW = 32 / S::LPC;
+  static_assert(kResident * (sizeof(S) + 1024) <= 228 * 1024, "the resident CTAs share an SM's shared memory");
   extern __shared__ __align__(128) unsigned char smem[];
   S& s = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x;
@@ -688,6 +782,9 @@ __global__ void __launch_bounds__(kThreads, kResident)
       mbar_init(&s.item_free[i], (kThreads - kRoleThreads * (kVec ? 1 : 0)) / 32);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&s.item_done[i], kScanThreads / 32);
+    mbar_init(&s.left, (kThreads - (kVec ? kRoleThreads : 0)) / 32 + (kVec ? 1 : 0));
+    s.claims = s.failed = 0;
+    for (uint32_t& c : s.closed) c = 0;
     fence_mbar_init();
   }
   griddep_wait();
@@ -697,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
   }
   __syncthreads();
   const ssm_selscan_args& a = p.a;
+  bool ok = true;
   // Each role goes through the CTA's items by itself, so the copies of an item come in beside the
   // scan of the one before.  Without a queue there is one item.
   uint32_t tile0 = 0;
@@ -704,7 +802,6 @@ __global__ void __launch_bounds__(kThreads, kResident)
     const int role = (tid - kScanThreads) / kRoleThreads;
     const bool claims = tid == kScanThreads;
     if (role == 0 && kVec && !claims) return;
-    bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Item it;
       if (claims) ok = claim_item<N, kPiece>(p, s, k, it);
@@ -713,14 +810,18 @@ __global__ void __launch_bounds__(kThreads, kResident)
         ok = next_item(p, s, k, it) && ok;
       }
       if (!ok || it.n < 0) break;
-      const uint32_t tile = tile0;
-      tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
-      if (role == 0)
-        ok = copy_role<T, N, kPiece, kVec>(p, maps, it, s, tile);
-      else if (role == 1)
-        ok = prepare_role<T, N, kPiece, kVec>(p, it, s, tile);
-      else if constexpr (!kPiece)
-        ok = finish_role<T, N, kVec>(p, it, s, tile, k);
+      if (role == 0) {
+        ok = copy_role<T, N, kPiece, kVec>(p, maps, it, s, tile0);
+      } else {
+        const uint32_t tile = tile0;
+        tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
+        if (role == 1) {
+          ok = prepare_role<T, N, kPiece, kVec>(p, it, s, tile);
+        } else if constexpr (!kPiece) {
+          ok = finish_role<T, N, kVec>(p, it, s, tile, k);
+          if (ok && (tid & 31) == 0) s.closed[(tid - 2 * kRoleThreads) / 32] = k + 1;
+        }
+      }
       if (kPiece || !p.queue) break;
     }
     // The next kernel's CTAs may come now.  Earlier, they would wait in places of this kernel's, two of
@@ -728,104 +829,104 @@ __global__ void __launch_bounds__(kThreads, kResident)
     if (claims) griddep_launch_dependents();
     if (claims || (role == 0 && !kVec))  // shared memory stays until the copies are there, whatever the other roles do
       for (uint32_t t = tile0 < S::RING ? 0 : tile0 - S::RING; t < tile0; ++t)
-        ok = wait_tile(s.raw_full, t, S::RING, p.ctl.spin_limit_ns) && ok;
-    if (!ok && p.queue) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
-    return;
-  }
-
-  int sub, cl;  // a scan thread's place in a channel's entries, and its first channel
-  lane_of<S::LPC>(tid & 31, sub, cl);
-  cl = 2 * (cl + (tid >> 5) * LW);
-  for (uint32_t k = 0;; ++k) {
-    Item it;
-    bool ok = next_item(p, s, k, it);
-    if (!ok || it.n < 0) {
-      if (!ok && p.queue) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
-      return;
-    }
-    float A[2][SPL], h[2][SPL], delta_sum[2] = {};
+        ok = wait_tile(s.raw_full, t, S::RING, kCopiesNs) && ok;
+  } else {
+    int sub, cl;  // a scan thread's place in a channel's entries, and its first channel
+    lane_of<S::LPC>(tid & 31, sub, cl);
+    cl = 2 * (cl + (tid >> 5) * LW);
+    for (uint32_t k = 0; ok; ++k) {
+      Item it;
+      ok = next_item(p, s, k, it);
+      if (!ok || it.n < 0) break;
+      float A[2][SPL], h[2][SPL], delta_sum[2] = {};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
+      for (int c = 0; c < 2; ++c) {
+        const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
 #pragma unroll
-      for (int i = 0; i < SPL; ++i) {
-        A[c][i] = a.A[chan * N + sub * SPL + i] * kLog2e;
-        h[c][i] = 0.f;
-      }
-    }
-    float4* hand = reinterpret_cast<float4*>(p.hand + (it.chain * kScanThreads + tid) * kHand);
-    if constexpr (!kPiece) {
-      if (it.sub > 0) {
-        if ((tid & 31) == 0 && !it.ready)
-          ok = wait_done(finished(p, it.chain), (uint32_t)it.sub, p.hdr, p.ctl.spin_limit_ns);
-        ok = all_lanes(ok);
-        if constexpr (SPL == 4) {
-          const float4 v = load_hand(hand), w = load_hand(hand + 1);
-          h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
-          h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
-        } else {
-          const float4 v = load_hand(hand);
-          h[0][0] = v.x, h[0][1] = v.y, h[1][0] = v.z, h[1][1] = v.w;
+        for (int i = 0; i < SPL; ++i) {
+          A[c][i] = a.A[chan * N + sub * SPL + i] * kLog2e;
+          h[c][i] = 0.f;
         }
-        if (!ok) set_nan(h);
+      }
+      float4* hand = reinterpret_cast<float4*>(p.hand + (it.chain * kScanThreads + tid) * kHand);
+      if constexpr (!kPiece) {
+        if (it.sub > 0) {
+          bool there = it.ready;
+          if ((tid & 31) == 0 && !there) {
+            there = wait_done(finished(p, it.chain), (uint32_t)it.sub, p.hdr, p.ctl.spin_limit_ns);
+            if (!there) raise_done(finished(p, it.chain), kLost);
+          }
+          there = __shfl_sync(0xffffffffu, there, 0);
+          __syncwarp();
+          if constexpr (SPL == 4) {
+            const float4 v = load_hand(hand), w = load_hand(hand + 1);
+            h[0][0] = v.x, h[0][1] = v.y, h[0][2] = v.z, h[0][3] = v.w;
+            h[1][0] = w.x, h[1][1] = w.y, h[1][2] = w.z, h[1][3] = w.w;
+          } else {
+            const float4 v = load_hand(hand);
+            h[0][0] = v.x, h[0][1] = v.y, h[1][0] = v.z, h[1][1] = v.w;
+          }
+          if (!there) set_nan(h);  // the item goes on with it, and leaves it to the next
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
+            if (a.h0) {
+#pragma unroll
+              for (int i = 0; i < SPL; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * SPL + i];
+            }
+#pragma unroll 4
+            for (int j = 0; j < it.part; ++j) {  // the state that the parts before this one leave
+              const int64_t row = ((int64_t)j * a.batch + it.b) * a.channels + chan;
+              float e[SPL], v[SPL];
+              mul_n(A[c], p.T[row], e);
+#pragma unroll
+              for (int i = 0; i < SPL; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * SPL + i];
+              fma_n(e, h[c], v);
+#pragma unroll
+              for (int i = 0; i < SPL; ++i) h[c][i] = v[i];
+            }
+          }
+        }
+      }
+      ok = scan_role<N, kPiece>(p, it, s, tile0, A, h, delta_sum);
+      if (!ok) break;
+      tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
+      if (!kPiece && it.sub + 1 < p.sp.subs) {
+        if constexpr (SPL == 4) {
+          hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
+          hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
+        } else {
+          hand[0] = make_float4(h[0][0], h[0][1], h[1][0], h[1][1]);
+        }
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
-          if (a.h0) {
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) h[c][i] = a.h0[(it.b * a.channels + chan) * N + sub * SPL + i];
+          if (cl + c >= it.cn) continue;
+          const int64_t chan = it.c0 + cl + c;
+          float* out = nullptr;
+          if constexpr (kPiece) {
+            const int64_t row = ((int64_t)it.part * a.batch + it.b) * a.channels + chan;
+            if (sub == 0) p.T[row] = delta_sum[c];
+            out = p.E + row * N;
+          } else if (a.h_final && it.part == p.sp.split - 1) {
+            out = a.h_final + (it.b * a.channels + chan) * N;
           }
-#pragma unroll 4
-          for (int j = 0; j < it.part; ++j) {  // the state that the parts before this one leave
-            const int64_t row = ((int64_t)j * a.batch + it.b) * a.channels + chan;
-            float e[SPL], v[SPL];
-            mul_n(A[c], p.T[row], e);
+          if (out) {
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * SPL + i];
-            fma_n(e, h[c], v);
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) h[c][i] = v[i];
+            for (int i = 0; i < SPL; ++i) out[sub * SPL + i] = h[c][i];
           }
         }
       }
-    }
-    ok = scan_role<N, kPiece>(p, it, s, tile0, A, h, delta_sum) && ok;
-    if (!ok) set_nan(h);
-    tile0 += (uint32_t)((it.live + kTokens - 1) / kTokens);
-    if (!kPiece && it.sub + 1 < p.sp.subs) {
-      if constexpr (SPL == 4) {
-        hand[0] = make_float4(h[0][0], h[0][1], h[0][2], h[0][3]);
-        hand[1] = make_float4(h[1][0], h[1][1], h[1][2], h[1][3]);
-      } else {
-        hand[0] = make_float4(h[0][0], h[0][1], h[1][0], h[1][1]);
+      __syncwarp();
+      if ((tid & 31) == 0) {
+        s.closed[tid >> 5] = k + 1;
+        if (!kPiece && p.queue) mbar_arrive(&s.item_done[k & 3]);
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (cl + c >= it.cn) continue;
-        const int64_t chan = it.c0 + cl + c;
-        float* out = nullptr;
-        if constexpr (kPiece) {
-          const int64_t row = ((int64_t)it.part * a.batch + it.b) * a.channels + chan;
-          if (sub == 0) p.T[row] = delta_sum[c];
-          out = p.E + row * N;
-        } else if (a.h_final && it.part == p.sp.split - 1) {
-          out = a.h_final + (it.b * a.channels + chan) * N;
-        }
-        if (out) {
-#pragma unroll
-          for (int i = 0; i < SPL; ++i) out[sub * SPL + i] = h[c][i];
-        }
-      }
+      if (kPiece || !p.queue) break;
     }
-    if (kPiece || !p.queue) return;
-    if (!all_lanes(ok)) {  // the other roles' waits, and those of the chain's later items, run out
-      record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
-      return;
-    }
-    if ((tid & 31) == 0) mbar_arrive(&s.item_done[k & 3]);
   }
+  leave(p, s, ok, kVec && tid >= kScanThreads && tid < kScanThreads + kRoleThreads ? 1 : 32);
 }
 
 template <typename F>

@@ -137,3 +137,107 @@ def test_workspace_of_another_device_or_type_is_refused(case):
             ssm.selscan_fwd(*args, workspace=ws)
     ssm.selscan_fwd(*args, workspace=ssm.Workspace("cuda"))
     torch.cuda.synchronize()
+
+
+STALL_COPIES = 1 << 40  # this and an item's index: the item's copies give up
+
+
+def run_with_fault(args, stall, lens=None, workspace=None):
+    """(y, h_final, what is right, their values without the fault).  Outputs start as a value that is nobody's."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    y0, h0 = ssm.selscan_fwd(*args, lens=lens)
+    y, h = torch.full_like(y0, 777.0), torch.full_like(h0, 777.0)
+    try:
+        ssm.debug_set_lookback_fault(stall, 2_000_000)
+        ssm.selscan_fwd(*args, lens=lens, y=y, h_final=h, workspace=workspace)
+        torch.cuda.synchronize()
+    finally:
+        ssm.debug_set_lookback_fault()
+    return y, h, y0, h0
+
+
+def all_right_or_nan(got, want, what):
+    import torch
+    bad = ~(torch.isnan(got) | (got == want))
+    assert not bad.any(), f"{what}: {int(bad.sum())} elements are neither right nor NaN, first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case,lens", [(QUEUE_ONE, None), (QUEUE_TWO, None), (QUEUE_TWO, [1100, 0, 300, 256, 257, 1, 700] + 6 * [900])],
+                         ids=str)
+def test_an_item_that_hands_no_state_on(case, lens, dtype):
+    """The rest of its chain is NaN, everything else right or NaN, and the call reports it."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    from selective_state_space_mamba_gb300 import _lib
+    b, L, d = case
+    ws = ssm.Workspace("cuda")
+    n = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    args = scan_case(case, 4, dtype)
+    y, h, y0, h0 = run_with_fault(args, 3, n, ws)
+    assert ssm.check_device_status(ws) == _lib.SSM_ERR_TIMEOUT
+    all_right_or_nan(y, y0, "y")
+    all_right_or_nan(h, h0, "h_final")
+    # item 3 of the queue: the first 512 tokens of channels 192 to 255 of sequence 0
+    assert torch.equal(y[:, :512], y0[:, :512])
+    assert torch.isnan(y[0, 512:, 192:256]).all() and torch.isnan(h[0, 192:256]).all()
+    again, h2 = ssm.selscan_fwd(*args, lens=n, workspace=ws)
+    assert ssm.check_device_status(ws) == 0 and torch.equal(again, y0) and torch.equal(h2, h0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case,item,where", [
+    ((2, 70, 72), 1, (0, slice(0, None), slice(64, None))),           # an item a CTA, no workspace
+    ((2, 70, 73), 2, (1, slice(0, None), slice(0, 64))),              # rows that are not aligned
+    (SPLIT, 1, (0, slice(200, None), slice(0, None))),                # a part of the time axis, both kernels
+    (QUEUE_ONE, 5, (0, slice(0, 256), slice(320, 384))),              # the first item of a CTA
+    (QUEUE_ONE, 200, None), (QUEUE_TWO, 330, None), (QUEUE_TWO, 900, None),  # others are in its hands
+    ((13, 1100, 1537), 700, None)], ids=str)
+def test_an_item_whose_copies_give_up(case, item, where, dtype):
+    """The waits between a CTA's warps run out: what it had claimed is NaN, nothing is left unwritten."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    from selective_state_space_mamba_gb300 import _lib
+    b, L, d = case
+    ws = ssm.Workspace("cuda", 1 << 20)
+    args = scan_case(case, 5, dtype)
+    y, h, y0, h0 = run_with_fault(args, STALL_COPIES + item, None, ws)
+    need = ssm.selscan_fwd_workspace_bytes(b, L, d, 16)
+    assert ssm.check_device_status(ws) == (_lib.SSM_ERR_TIMEOUT if need else 0)
+    all_right_or_nan(y, y0, "y")
+    all_right_or_nan(h, h0, "h_final")
+    assert torch.isnan(y).any() and torch.isnan(h).any()
+    if where is not None:
+        assert torch.isnan(y[where]).all()
+    again, h2 = ssm.selscan_fwd(*args, workspace=ws)
+    assert ssm.check_device_status(ws) == 0 and torch.equal(again, y0) and torch.equal(h2, h0)
+
+
+def test_padding_and_empty_sequences_after_a_fault():
+    """Items without a token pass the lost state on, and padding stays 0 where it is written."""
+    import torch
+    case = (13, 1100, 1544)
+    n = torch.tensor([0, 1100] + 11 * [30], dtype=torch.int32, device="cuda")
+    y, h, y0, h0 = run_with_fault(scan_case(case, 6), STALL_COPIES + 40, n)
+    all_right_or_nan(y, y0, "y")
+    all_right_or_nan(h, h0, "h_final")
+    assert not y[0].any() and not y[2:, 30:].any()
+
+
+def test_every_wait_with_no_time_at_all():
+    """A limit of a nanosecond: whichever waits run out, the outputs are right or NaN."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    for case in ((2, 70, 72), (2, 70, 73), SPLIT, QUEUE_ONE, QUEUE_TWO):
+        args = scan_case(case, 7)
+        y0, h0 = ssm.selscan_fwd(*args)
+        y, h = torch.full_like(y0, 777.0), torch.full_like(h0, 777.0)
+        try:
+            ssm.debug_set_lookback_fault(-1, 1)
+            ssm.selscan_fwd(*args, y=y, h_final=h)
+            torch.cuda.synchronize()
+        finally:
+            ssm.debug_set_lookback_fault()
+        all_right_or_nan(y, y0, f"y {case}")
+        all_right_or_nan(h, h0, f"h_final {case}")
