@@ -353,11 +353,18 @@ def linscan_baseline(a, b, algo: str, *, h=None, workspace: Workspace | None = N
 
 
 def check_device_status(workspace: Workspace | None = None, kind: str = "ssd", device=None) -> int:
-    """Synchronise and return (and clear) the device status word of a workspace (0 = OK)."""
+    """Synchronise and return (and clear) the device status word of a workspace (0 = OK).
+
+    Without a workspace: that of the last call of ``kind`` ("ssd", "linscan", "scan_" and a baseline's
+    name, or "selscan") that was given none."""
     torch = _torch()
     lib = _lib.load()
     if workspace is None:
         dev = torch.device(device if device is not None else "cuda")
+        if kind == "selscan":
+            from . import _layer
+            buf = _layer.kept_workspace(dev.index if dev.index is not None else torch.cuda.current_device())
+            return 0 if buf is None else int(lib.ssm_check_device_status(_ptr(buf), _stream_ptr(buf.device)))
         workspace = _default_ws.get((kind, dev.index if dev.index is not None else torch.cuda.current_device()))
         if workspace is None:
             return 0

@@ -72,6 +72,11 @@ def selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups=1) -> i
     return int(_lib.load().ssm_selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups))
 
 
+def kept_workspace(device_index: int):
+    """The memory that the last selscan_fwd without a workspace allocated, or None (for check_device_status)."""
+    return (_native or _load()).kept_workspace(device_index)
+
+
 def selscan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lens=None, *, softplus: bool = True, y=None,
                 h_final=None, return_final_state: bool = True, workspace=None):
     """Selective scan over a prompt (ssm_selscan_fwd).
@@ -81,8 +86,8 @@ def selscan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lens=None
     sequence (None: L); N in {8, 16, 32, 64}; channel c reads group c // (d / G).  Returns (y, h_final):
     y [b, L, d], 0 in the padding, and the float32 state after the last token (None when
     return_final_state is False).  Without a workspace (Workspace), one is allocated for the call
-    where it is needed; with one, check_device_status(workspace) tells whether a wait inside
-    the call ran out.
+    where it is needed.  check_device_status(workspace), or check_device_status(kind="selscan") without
+    one, tells whether a wait inside the last call that needed one ran out.
     """
     buf = None
     if workspace is not None:

@@ -9,6 +9,7 @@
 // library and its state.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAMacros.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -239,6 +240,9 @@ ssm_selscan_args selscan_args(PyObject* const* v, const Like& like, const at::Te
   return a;
 }
 
+// The workspace of each device's last scan that was given none: its status can still be read (kept_workspace).
+PyObject* g_kept[C10_COMPILE_TIME_MAX_GPUS] = {};
+
 // u, dt, A, B, C, D, z, dt_bias, h0, lens, softplus, y, h_final, return_final_state, workspace buffer
 PyObject* selscan_fwd(PyObject* const* v) {
   const at::Tensor& u = tensor("u", v[0]);
@@ -262,7 +266,12 @@ PyObject* selscan_fwd(PyObject* const* v) {
       fail("workspace", "contiguous bytes on u's device");
   } else {
     const size_t need = g_fn.selscan_fwd_workspace_bytes(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups);
-    if (need) ws = like.empty({(int64_t)need}, at::kByte);
+    if (need) {
+      ws = like.empty({(int64_t)need}, at::kByte);
+      PyObject*& kept = g_kept[like.device.index()];
+      Py_XDECREF(kept);
+      kept = THPVariable_Wrap(ws);
+    }
   }
   return result(g_fn.selscan_fwd(&a, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0,
                                  like.stream()),
@@ -324,6 +333,14 @@ struct Norm {
     residual_out.set("residual_out", oo, sizes, r.scalar_type(), like);
   }
 };
+
+PyObject* kept_workspace(PyObject* const* v) {  // device index
+  const long i = PyLong_AsLong(v[0]);
+  if (PyErr_Occurred()) return nullptr;
+  PyObject* o = i >= 0 && i < C10_COMPILE_TIME_MAX_GPUS && g_kept[i] ? g_kept[i] : Py_None;
+  Py_INCREF(o);
+  return o;
+}
 
 PyObject* rmsnorm_fwd(PyObject* const* v) {  // x, weight, residual, eps, y, residual_out
   Norm n(v[0], v[1], v[2], v[5]);
@@ -414,6 +431,7 @@ PyMethodDef g_methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                            {"selscan_fwd", fast(entry<selscan_fwd, 15>), METH_FASTCALL, nullptr},
                            {"selscan_step", fast(entry<selscan_step, 14>), METH_FASTCALL, nullptr},
                            {"rmsnorm_fwd", fast(entry<rmsnorm_fwd, 6>), METH_FASTCALL, nullptr},
+                           {"kept_workspace", fast(entry<kept_workspace, 1>), METH_FASTCALL, nullptr},
                            {"rmsnorm_fp8_fwd", fast(entry<rmsnorm_fp8_fwd, 8>), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

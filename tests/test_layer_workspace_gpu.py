@@ -241,3 +241,23 @@ def test_every_wait_with_no_time_at_all():
             ssm.debug_set_lookback_fault()
         all_right_or_nan(y, y0, f"y {case}")
         all_right_or_nan(h, h0, f"h_final {case}")
+
+
+@pytest.mark.parametrize("case", [SPLIT, QUEUE_ONE], ids=str)
+def test_status_of_a_call_without_a_workspace(case):
+    """The workspace that such a call allocates is kept until the next one, for its status."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    from selective_state_space_mamba_gb300 import _lib
+    args = scan_case(case, 8)
+    run_with_fault(args, STALL_COPIES + 1)
+    small = scan_case((1, 4, 16), 8)
+    ssm.selscan_fwd(*small)  # needs none
+    assert ssm.check_device_status(kind="selscan") == _lib.SSM_ERR_TIMEOUT
+    assert ssm.check_device_status(kind="selscan") == 0
+    run_with_fault(args, STALL_COPIES + 1)
+    ssm.selscan_fwd(*args)
+    assert ssm.check_device_status(kind="selscan", device="cuda:0") == 0
+    run_with_fault(args, STALL_COPIES + 1, None, ssm.Workspace("cuda"))  # not the kept one
+    assert ssm.check_device_status(kind="selscan") == 0
+    torch.cuda.synchronize()
