@@ -510,6 +510,7 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
       }
       store8<float>((is_c ? &s.fc[kPiece ? 0 : buf][0][0] : &s.fb[buf][0][0]) + e, true, 8, f);
     }
+    if constexpr (kVec) fence_proxy_async_smem();  // these reads of the raw tile, before the tensor copies refill it
     if (!all_lanes(ok)) return false;
     if ((threadIdx.x & 31) == 0) {
       mbar_arrive(&s.full[buf]);
@@ -603,6 +604,7 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
       y_tile += (int64_t)kTokens * a.channels;
     }
     y_item += (int64_t)kTokens * a.channels;
+    if constexpr (kVec) fence_proxy_async_smem();  // as in prepare_role
     if (!all_lanes(ok)) return false;
     if ((threadIdx.x & 31) == 0) {
       mbar_arrive(&s.y_free[buf]);
