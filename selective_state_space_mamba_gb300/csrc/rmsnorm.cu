@@ -310,10 +310,12 @@ __global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : HOLD > 1 ? kHoldMaxThre
     const int i = tid + k * threads;
     if (i - (tid & 31) < nvec) output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, held[k], rstd, row_scale);
   }
-  for (int i = first; i - (tid & 31) < nvec; i += threads) {
-    float r[8] = {};
-    if (i < nvec) load_r<T, R, kRes, kVec>(p, row, i, r);
-    output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, r, rstd, row_scale);
+  if constexpr (HOLD == 1) {  // whole warps: i - (tid & 31) is the same in a warp's lanes
+    for (int i = first; i - (tid & 31) < nvec; i += threads) {
+      float r[8] = {};
+      if (i < nvec) load_r<T, R, kRes, kVec>(p, row, i, r);
+      output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, r, rstd, row_scale);
+    }
   }
 }
 
