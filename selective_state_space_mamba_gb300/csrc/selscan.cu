@@ -555,15 +555,18 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
 #pragma unroll
         for (int t = vt; t < kTokens; t += VT) {
           if (t < rows) {
-            float y[8], w[8], u[8];
+            float y[8], w[8];
             load_y(&s.y[buf][t * CT], vc, y);
 #pragma unroll
             for (int k = 1; k < S::PARTS; ++k) {
               load_y(&s.y[buf][k * S::YP + t * CT], vc, w);
               add_n(y, w, y);
             }
-            load8<T>(&s.u[ring][t][vc], true, 8, u);
-            fma_n(skip, u, y);
+            if (a.D) {  // (0 times an infinite u would be NaN)
+              float u[8];
+              load8<T>(&s.u[ring][t][vc], true, 8, u);
+              fma_n(skip, u, y);
+            }
             if (a.z.ptr) {
               float z[8];
               load8<T>(&s.z[ring][t][vc], true, 8, z);
@@ -579,7 +582,7 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
       for (int i = tid; i < CT * kTokens / 8; i += kRoleThreads) {
         const int c = i % CT, t = i / CT * 8;
         if (c >= it.cn) continue;
-        float y[8], w[8], u[8], z[8];
+        float y[8], w[8], z[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = s.y[buf][(t + j) * CT + (c ^ (c >> 3 & 4))];
 #pragma unroll
@@ -588,9 +591,11 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
           for (int j = 0; j < 8; ++j) w[j] = s.y[buf][k * S::YP + (t + j) * CT + (c ^ (c >> 3 & 4))];
           add_n(y, w, y);
         }
-        load_column8<T>(a.u, it.b, t0 + t, it.c0, &s.u[ring][t], c, u);
-        const float d = a.D ? __ldg(a.D + it.c0 + c) : 0.f;
-        fma_n(u, d, y, y);
+        if (a.D) {
+          float u[8];
+          load_column8<T>(a.u, it.b, t0 + t, it.c0, &s.u[ring][t], c, u);
+          fma_n(u, __ldg(a.D + it.c0 + c), y, y);
+        }
         if (a.z.ptr) {
           load_column8<T>(a.z, it.b, t0 + t, it.c0, &s.z[ring][t], c, z);
           silu_n(z, z);

@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kStepThreads, ROWS > 1 ? 8 : 1)
     for (int k = 0; k < OWN; ++k) {
       const int64_t b = b0 + sub + SHARE * k;
       if (b < a.batch) {
-        float v = fmaf(skip, to_f32(u_raw[k]), sum[k * SHARE]);
+        float v = sum[k * SHARE];
+        if (a.D) v = fmaf(skip, to_f32(u_raw[k]), v);  // (0 times an infinite u would be NaN)
         if (a.z.ptr) v *= silu(to_f32(z_raw[k]));
         int64_t mine = slot[0];
 #pragma unroll
