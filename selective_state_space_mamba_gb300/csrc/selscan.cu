@@ -889,7 +889,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
               float e[SPL], v[SPL];
               mul_n(A[c], p.T[row], e);
 #pragma unroll
-              for (int i = 0; i < SPL; ++i) e[i] = exp2_fast(e[i]), v[i] = p.E[row * N + sub * SPL + i];
+              for (int i = 0; i < SPL; ++i) {
+                // a state of 0 or infinity stays one token by token, also where the part's decay is out of range
+                e[i] = h[c][i] == 0.f || isinf(h[c][i]) ? 1.f : exp2_fast(e[i]);
+                v[i] = p.E[row * N + sub * SPL + i];
+              }
               fma_n(e, h[c], v);
 #pragma unroll
               for (int i = 0; i < SPL; ++i) h[c][i] = v[i];
