@@ -67,10 +67,12 @@ struct Params {
   float* T;          // [split - 1, batch, channels]
   bool vec;          // rows of u, dt, z, y, B and C in whole vectors of 16 bytes: tensor copies
   bool dense;        // without them: some rows are less than 16 bytes apart
+  uint32_t inner;    // tensors (kU ...) whose sequences lie inside their tokens
 };
 struct Maps {
   CUtensorMap u, dt, z, B, C;
 };
+constexpr uint32_t kU = 1, kDt = 2, kZ = 4, kB = 8, kC = 16;
 
 __device__ __forceinline__ uint32_t* finished(const Params& p, int64_t chain) {
   return p.queue + 1 + chain;
@@ -390,12 +392,16 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
       uint64_t* bar = &s.raw_full[ring];
       if (tile >= RING && !wait_tile(s.raw_free, tile - RING, RING, p.ctl.spin_limit_ns)) return false;
       mbar_arrive_expect_tx(bar, bytes);
-      tc::tma_load_3d(&s.dt[ring][0][0], &maps.dt, it.c0, (int)t, (int)it.b, bar);
-      tc::tma_load_3d(&s.u[ring][0][0], &maps.u, it.c0, (int)t, (int)it.b, bar);
-      tc::tma_load_3d(&s.b[ring][0][0], &maps.B, it.g * N, (int)t, (int)it.b, bar);
+      const auto load = [&](T* dst, const CUtensorMap* map, int c, uint32_t which) {
+        const bool inner = (p.inner & which) != 0;
+        tc::tma_load_3d(dst, map, c, inner ? (int)it.b : (int)t, inner ? (int)t : (int)it.b, bar);
+      };
+      load(&s.dt[ring][0][0], &maps.dt, it.c0, kDt);
+      load(&s.u[ring][0][0], &maps.u, it.c0, kU);
+      load(&s.b[ring][0][0], &maps.B, it.g * N, kB);
       if constexpr (!kPiece) {
-        tc::tma_load_3d(&s.c[ring][0][0], &maps.C, it.g * N, (int)t, (int)it.b, bar);
-        if (a.z.ptr) tc::tma_load_3d(&s.z[ring][0][0], &maps.z, it.c0, (int)t, (int)it.b, bar);
+        load(&s.c[ring][0][0], &maps.C, it.g * N, kC);
+        if (a.z.ptr) load(&s.z[ring][0][0], &maps.z, it.c0, kZ);
       }
     }
   } else {
@@ -971,6 +977,27 @@ Layout layout(const SelscanSplit& sp, int64_t batch, int channels, int dstate) {
   return l;
 }
 
+// How a tensor map takes a tensor's rows: the two outer dimensions in the order of their strides, the second a whole
+// number of the first, which covers the dimension below it, as the map's definition has them.  A map has 32-bit
+// coordinates, and takes no rows that lie on one another.  An axis of one element has any stride that fits.
+struct Nesting {
+  bool fits, inner;      // inner: sequences inside tokens
+  uint64_t strides[2];   // bytes
+};
+Nesting nesting(const ssm_tokens& t, int64_t batch, int64_t seqlen, int64_t columns, int64_t e) {
+  const int64_t row = (columns * e + 15) / 16 * 16;
+  if (!aligned_rows(t.ptr, batch > 1 ? t.batch_stride : 0, seqlen > 1 ? t.token_stride : 0, (int)e, 16) ||
+      seqlen > 0x7fffffff - kTokens)
+    return {};
+  const int64_t bs = batch > 1 ? t.batch_stride * e : 0, ts = seqlen > 1 ? t.token_stride * e : 0;
+  const bool inner = batch > 1 && bs < ts;
+  const int64_t low = inner ? bs : seqlen > 1 ? ts : batch > 1 ? bs : row, count = inner ? batch : seqlen;
+  if (low < columns * e || low >= (int64_t)1 << 40 || count >= ((int64_t)1 << 40) / low) return {};
+  const int64_t high = inner ? ts : batch > 1 ? bs : low * count;
+  if (high < low * count || high % low != 0 || high >= (int64_t)1 << 40) return {};
+  return {true, inner, {(uint64_t)low, (uint64_t)high}};
+}
+
 Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* workspace) {
   Params p{};
   p.a = a;
@@ -989,10 +1016,17 @@ Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
   }
   const int e = a.dtype == SSM_F32 ? 4 : 2;
   p.vec = a.seqlen > 0 && a.channels / a.ngroups % 8 == 0 && aligned_rows(a.y, a.channels, 0, e, 16);
-  for (const ssm_tokens* t : {&a.u, &a.dt, &a.z, &a.B, &a.C})
-    if (t->ptr)  // (a tensor map takes no rows that lie on one another)
-      p.vec = p.vec && aligned_rows(t->ptr, a.batch > 1 ? t->batch_stride : 0, a.seqlen > 1 ? t->token_stride : 0, e, 16) &&
-              (a.batch == 1 || t->batch_stride > 0) && (a.seqlen == 1 || t->token_stride > 0);
+  const auto look = [&](const ssm_tokens& t, int64_t columns, uint32_t which) {
+    if (!t.ptr || !p.vec) return;
+    const Nesting n = nesting(t, a.batch, a.seqlen, columns, e);
+    p.vec = n.fits;
+    if (n.inner) p.inner |= which;
+  };
+  look(a.u, a.channels, kU);
+  look(a.dt, a.channels, kDt);
+  look(a.z, a.channels, kZ);
+  look(a.B, (int64_t)a.ngroups * a.dstate, kB);
+  look(a.C, (int64_t)a.ngroups * a.dstate, kC);
   for (const ssm_tokens* t : {&a.u, &a.dt, &a.z, &a.B, &a.C})
     if (t->ptr)
       p.dense = p.dense || (a.batch > 1 && t->batch_stride * e < 16) || (a.seqlen > 1 && t->token_stride * e < 16);
@@ -1002,16 +1036,16 @@ Params make_params(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
 cudaError_t make_maps(const Params& p, Maps* m) {
   const ssm_selscan_args& a = p.a;
   if (!p.vec) return cudaSuccess;
-  const uint64_t e = a.dtype == SSM_F32 ? 4 : 2;
+  const int64_t e = a.dtype == SSM_F32 ? 4 : 2;
   const auto type = a.dtype == SSM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto make = [&](CUtensorMap* map, const ssm_tokens& t, int columns, int box_columns) -> cudaError_t {
     if (!t.ptr) return cudaSuccess;
-    const uint64_t dims[3] = {(uint64_t)columns, (uint64_t)a.seqlen, (uint64_t)a.batch};
-    // the stride of an axis of one element is not used, but has to be a valid one
-    const uint64_t row = a.seqlen > 1 ? t.token_stride * e : (columns * e + 15) / 16 * 16;
-    const uint64_t strides[2] = {row, a.batch > 1 ? t.batch_stride * e : row * (uint64_t)a.seqlen};
-    const uint32_t box[3] = {(uint32_t)box_columns, (uint32_t)kTokens, 1};
-    return encode_tensor_map_3d(map, type, t.ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    const Nesting n = nesting(t, a.batch, a.seqlen, columns, e);
+    const uint64_t outer[2] = {(uint64_t)a.seqlen, (uint64_t)a.batch};
+    const uint32_t tokens[2] = {(uint32_t)kTokens, 1};
+    const uint64_t dims[3] = {(uint64_t)columns, outer[n.inner], outer[!n.inner]};
+    const uint32_t box[3] = {(uint32_t)box_columns, tokens[n.inner], tokens[!n.inner]};
+    return encode_tensor_map_3d(map, type, t.ptr, dims, n.strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
   };
   const int ct = tile_channels(a.dstate), n = a.ngroups * a.dstate;
   cudaError_t r = make(&m->u, a.u, a.channels, ct);
