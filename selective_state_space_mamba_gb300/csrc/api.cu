@@ -749,8 +749,8 @@ ssm_status ssm_conv_step(ssm_tokens x, const float* w, const float* bias, const 
 }
 
 size_t ssm_selscan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
-  if (batch < 0 || seqlen < 0 || channels < 1 || ngroups < 1 || channels % ngroups != 0 || !selscan_dstate(dstate) ||
-      channels > kMaxColumns / dstate)
+  if (batch < 0 || batch > 65535 || seqlen < 0 || seqlen > (int64_t)1 << 40 || channels < 1 || ngroups < 1 ||
+      channels % ngroups != 0 || !selscan_dstate(dstate) || channels > kMaxColumns / dstate)
     return 0;
   return selscan_split(batch, seqlen, channels, dstate, ngroups).bytes;
 }

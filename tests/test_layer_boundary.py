@@ -260,3 +260,17 @@ def test_python_sizes_that_wrap_are_refused(dtype):
             pytest.fail(f"call {i} was taken")
     with pytest.raises(ValueError, match="CUDA tensor"):
         ssm.conv_fwd(t(1, 1, 8), f(8, 4))
+
+
+def test_selscan_workspace_of_sizes_that_are_refused(lib):
+    """0 bytes, as for every other invalid size: more sequences than a call takes (their product with the tiles went
+    beyond 64 bits)."""
+    f = lib.ssm_selscan_fwd_workspace_bytes
+    assert f(65535, 4, 8, 16, 1) == 0
+    for batch in (65536, 1 << 40, (1 << 62) + 1, (1 << 63) - 1):
+        assert f(batch, 1 << 20, 1 << 16, 16, 1) == 0, batch
+    for seqlen in ((1 << 40) + 1, 1 << 62, (1 << 63) - 1):
+        assert f(1, seqlen, 8, 16, 1) == 0, seqlen
+    assert scan(lib, batch=65536) == UNSUPPORTED
+    # one channel of 2^41 tokens: the parts of its time axis have too many
+    assert scan(lib, batch=1, seqlen=1 << 41, channels=1, ts=0, y=1 << 58, h_final=1 << 60) == UNSUPPORTED
