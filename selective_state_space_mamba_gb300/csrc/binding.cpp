@@ -45,6 +45,14 @@ int narrow(int64_t v) {
   return (int)v;
 }
 
+// An exception of Python's own is set already.
+struct Raised {};
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+
 using Sizes = c10::IntArrayRef;
 std::string text_of(Sizes s) {
   std::string r = "[";
@@ -189,9 +197,9 @@ PyObject* conv_fwd(PyObject* const* v) {  // x, weight, bias, state, lens, silu,
   const int32_t* lens = ints("lens", v[4], b, like);
   Out y, so;
   y.set("y", v[6], {b, L, d}, like.type, like);
-  if (PyObject_IsTrue(v[8])) so.set("state_out", v[7], {b, W - 1, d}, like.type, like);
+  if (truth(v[8])) so.set("state_out", v[7], {b, W - 1, d}, like.type, like);
   const ssm_status st = g_fn.conv_fwd(xt, wp, bias, state, lens, y.ptr, so.ptr, b, L, d, W,
-                                      PyObject_IsTrue(v[5]) ? SSM_ACT_SILU : SSM_ACT_NONE, like.code, like.stream());
+                                      truth(v[5]) ? SSM_ACT_SILU : SSM_ACT_NONE, like.code, like.stream());
   return result(st, y, so);
 }
 
@@ -207,11 +215,11 @@ PyObject* conv_step(PyObject* const* v) {  // x, weight, bias, state, slots, sil
   const float* bias = floats("bias", v[2], {d}, like);
   const int32_t* slots = ints("slots", v[4], b, like);
   Out y, so;
-  const int64_t n = step_states(so, v[3], v[7], PyObject_IsTrue(v[8]), slots, b, W - 1, d, like.type, like);
+  const int64_t n = step_states(so, v[3], v[7], truth(v[8]), slots, b, W - 1, d, like.type, like);
   const void* state = optional("state", v[3], {n, W - 1, d}, like.type, like);
   y.set("y", v[6], {b, d}, like.type, like);
   const ssm_status st = g_fn.conv_step(xt, wp, bias, state, slots, y.ptr, so.ptr, b, n, d, W,
-                                       PyObject_IsTrue(v[5]) ? SSM_ACT_SILU : SSM_ACT_NONE, like.code, like.stream());
+                                       truth(v[5]) ? SSM_ACT_SILU : SSM_ACT_NONE, like.code, like.stream());
   return result(st, y, so);
 }
 
@@ -251,13 +259,13 @@ PyObject* selscan_fwd(PyObject* const* v) {
   ssm_selscan_args a = selscan_args(v, like, u, 2);
   const auto guard = like.guard();
   a.seqlen = u.size(1);
-  a.softplus = PyObject_IsTrue(v[10]);
+  a.softplus = truth(v[10]);
   a.h0 = floats("h0", v[8], {a.batch, a.channels, a.dstate}, like);
   a.lens = ints("lens", v[9], a.batch, like);
   Out y, h;
   y.set("y", v[11], u.sizes(), like.type, like);
   a.y = y.ptr;
-  if (PyObject_IsTrue(v[13])) h.set("h_final", v[12], {a.batch, a.channels, a.dstate}, at::kFloat, like);
+  if (truth(v[13])) h.set("h_final", v[12], {a.batch, a.channels, a.dstate}, at::kFloat, like);
   a.h_final = static_cast<float*>(h.ptr);
   at::Tensor ws;
   if (v[14] != Py_None) {
@@ -286,11 +294,11 @@ PyObject* selscan_step(PyObject* const* v) {
   ssm_selscan_args a = selscan_args(v, like, u, 1);
   const auto guard = like.guard();
   a.seqlen = 1;
-  a.softplus = PyObject_IsTrue(v[10]);
+  a.softplus = truth(v[10]);
   const int32_t* slots = ints("slots", v[9], a.batch, like);
   Out y, so;
   const int64_t n =
-      step_states(so, v[8], v[12], PyObject_IsTrue(v[13]), slots, a.batch, a.channels, a.dstate, at::kFloat, like);
+      step_states(so, v[8], v[12], truth(v[13]), slots, a.batch, a.channels, a.dstate, at::kFloat, like);
   a.h0 = floats("state", v[8], {n, a.channels, a.dstate}, like);
   a.h_final = static_cast<float*>(so.ptr);
   y.set("y", v[11], u.sizes(), like.type, like);
@@ -384,6 +392,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != ARGS) throw Refusal{PyExc_TypeError, "wrong number of arguments"};
     if (!g_fn.conv_fwd) throw Refusal{PyExc_RuntimeError, "the library is not bound"};
     return F(args);
+  } catch (const Raised&) {
   } catch (const Unsupported&) {
     return PyLong_FromLong(SSM_ERR_UNSUPPORTED);
   } catch (const Refusal& r) {
