@@ -534,9 +534,10 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
  * Kernel timing (measurement aid; not needed in normal use).  Between ssm_profile_begin()
  * and ssm_profile_end(), every call that computes records a
  * CUDA event on its own stream before and after each kernel it launches (at most
- * `max_launches` launches are recorded; later ones are counted but not timed).  ssm_profile_end() synchronizes the
- * recorded events and writes, for each kernel id below, the summed device time in
- * milliseconds and the number of launches (arrays of length SSM_PROFILE_KERNELS).
+ * `max_launches` launches are recorded; later ones are counted but not timed).  ssm_profile_end_n() synchronizes the
+ * recorded events and writes, for each of the first `n` kernel ids below, the summed device time in
+ * milliseconds and the number of launches (arrays of n; either may be NULL; 0 past the last id).  ssm_profile_end()
+ * is the same for the first SSM_PROFILE_END_KERNELS ids, which that name has always written.
  * Kernel ids: 0 linscan_lookback, 1 ssd_chunk_cumsum, 2 ssd_chunk_state,
  * 3 ssd_state_passing, 4 ssd_chunk_scan, 5 ssd_state_fused (chunk states and state passing in
  * one pass; used instead of 2 and 3 where it applies), 6 ssd_step (ssm_ssd_step),
@@ -547,8 +548,10 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
  * process-global; not thread-safe.
  */
 #define SSM_PROFILE_KERNELS 15
+#define SSM_PROFILE_END_KERNELS 9
 SSM_API ssm_status ssm_profile_begin(int max_launches);
 SSM_API ssm_status ssm_profile_end(double *ms_out, int64_t *launches_out);
+SSM_API ssm_status ssm_profile_end_n(double *ms_out, int64_t *launches_out, int n);
 
 #ifdef __cplusplus
 }

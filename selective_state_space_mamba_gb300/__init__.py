@@ -380,7 +380,7 @@ class KernelTimer:
     """Per-kernel device times of the library's launches inside a ``with`` block.
 
     Uses the library's own CUDA events, recorded on the stream of each launch
-    (ssm_profile_begin / ssm_profile_end in include/ssm.h).  After the block, ``ms`` maps kernel
+    (ssm_profile_begin / ssm_profile_end_n in include/ssm.h).  After the block, ``ms`` maps kernel
     name -> summed milliseconds and ``launches`` kernel name -> launch count.
     """
 
@@ -398,8 +398,8 @@ class KernelTimer:
         n = len(_lib.PROFILE_KERNELS)
         ms = (ctypes.c_double * n)()
         cnt = (ctypes.c_int64 * n)()
-        _lib.check(_lib.load().ssm_profile_end(ctypes.cast(ms, ctypes.c_void_p), ctypes.cast(cnt, ctypes.c_void_p)),
-                   "ssm_profile_end")
+        _lib.check(_lib.load().ssm_profile_end_n(ctypes.cast(ms, ctypes.c_void_p), ctypes.cast(cnt, ctypes.c_void_p), n),
+                   "ssm_profile_end_n")
         self.ms = {k: float(ms[i]) for i, k in enumerate(_lib.PROFILE_KERNELS)}
         self.launches = {k: int(cnt[i]) for i, k in enumerate(_lib.PROFILE_KERNELS)}
         return False

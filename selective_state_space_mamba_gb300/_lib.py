@@ -20,7 +20,7 @@ SSM_SCAN_BLELLOCH, SSM_SCAN_THREE_PASS, SSM_SCAN_LOOKBACK_SERIAL, SSM_SCAN_LOOKB
 # Every symbol the header declares (checked by the CPU test suite).
 EXPORTS = ("ssm_status_string", "ssm_version", "ssm_ssd_fwd_workspace_bytes", "ssm_ssd_fwd",
            "ssm_linscan_workspace_bytes", "ssm_linscan_fwd", "ssm_check_device_status",
-           "ssm_debug_set_lookback_fault", "ssm_profile_begin", "ssm_profile_end", "ssm_linscan_fwd_noalloc",
+           "ssm_debug_set_lookback_fault", "ssm_profile_begin", "ssm_profile_end", "ssm_profile_end_n", "ssm_linscan_fwd_noalloc",
            "ssm_ssd_step", "ssm_linscan_baseline_workspace_bytes", "ssm_linscan_baseline", "ssm_ssd_fwd_tune",
            "ssm_ssd_fwd_set_plan", "ssm_ssd_fwd_get_plan", "ssm_ssd_fwd_clear_plans", "ssm_debug_fused_schedule",
            "ssm_debug_scan_schedule",
@@ -126,6 +126,8 @@ def _declare(lib):
     lib.ssm_profile_begin.restype = i32
     lib.ssm_profile_end.argtypes = [vp, vp]
     lib.ssm_profile_end.restype = i32
+    lib.ssm_profile_end_n.argtypes = [vp, vp, i32]
+    lib.ssm_profile_end_n.restype = i32
 
 
 def library_path() -> str:

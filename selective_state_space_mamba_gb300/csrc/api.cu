@@ -1014,6 +1014,11 @@ ssm_status ssm_profile_begin(int max_launches) {
 }
 
 ssm_status ssm_profile_end(double* ms_out, int64_t* launches_out) {
+  return ssm_profile_end_n(ms_out, launches_out, SSM_PROFILE_END_KERNELS);
+}
+
+ssm_status ssm_profile_end_n(double* ms_out, int64_t* launches_out, int n) {
+  if (n < 0) return SSM_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   g_prof_on = false;
   double ms[SSM_PROFILE_KERNELS] = {0};
@@ -1027,9 +1032,9 @@ ssm_status ssm_profile_end(double* ms_out, int64_t* launches_out) {
     g_prof_pool.push_back(r.stop);
   }
   g_prof_records.clear();
-  for (int k = 0; k < SSM_PROFILE_KERNELS; ++k) {
-    if (ms_out) ms_out[k] = ms[k];
-    if (launches_out) launches_out[k] = g_prof_counts[k];
+  for (int k = 0; k < n; ++k) {
+    if (ms_out) ms_out[k] = k < SSM_PROFILE_KERNELS ? ms[k] : 0.0;
+    if (launches_out) launches_out[k] = k < SSM_PROFILE_KERNELS ? g_prof_counts[k] : 0;
   }
   return st;
 }

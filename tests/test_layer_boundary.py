@@ -274,3 +274,23 @@ def test_selscan_workspace_of_sizes_that_are_refused(lib):
     assert scan(lib, batch=65536) == UNSUPPORTED
     # one channel of 2^41 tokens: the parts of its time axis have too many
     assert scan(lib, batch=1, seqlen=1 << 41, channels=1, ts=0, y=1 << 58, h_final=1 << 60) == UNSUPPORTED
+
+
+def test_profile_arrays_of_an_older_header(lib):
+    """ssm_profile_end writes the nine kernels it wrote before the layer operators came; ssm_profile_end_n as many as it
+    is told."""
+    foreign = -7
+
+    def run(call, size):
+        ms, n = (ctypes.c_double * size)(*[foreign] * size), (ctypes.c_int64 * size)(*[foreign] * size)
+        assert call(ctypes.cast(ms, ctypes.c_void_p), ctypes.cast(n, ctypes.c_void_p)) == _lib.SSM_OK
+        written = [a != foreign for a in ms]
+        assert written == [a != foreign for a in n] and written == sorted(written, reverse=True)
+        return sum(written)
+
+    assert run(lib.ssm_profile_end, 20) == 9
+    for k in (0, 3, 9, 15, 18):
+        assert run(lambda a, b: lib.ssm_profile_end_n(a, b, k), 20) == k  # noqa: B023
+    assert lib.ssm_profile_end_n(None, None, 15) == _lib.SSM_OK and lib.ssm_profile_end(None, None) == _lib.SSM_OK
+    assert lib.ssm_profile_end_n(None, None, -1) == INVALID
+    assert len(_lib.PROFILE_KERNELS) == 15
