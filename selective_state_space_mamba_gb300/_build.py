@@ -23,6 +23,7 @@ BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libssm_gb300_debug.so")
 
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_KEY = os.path.join(BUILD, "binding.key")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -82,27 +83,46 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
 
 def build_binding(force: bool = False) -> str:
     """Build the compiled Python entry points of the operators around a layer's scan (_binding.so, from
-    csrc/binding.cpp) with g++ against the installed torch."""
-    src = os.path.join(CSRC, "binding.cpp")
-    deps = [src] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
-        return BINDING
+    csrc/binding.cpp) with g++ against the installed torch.
+
+    It holds inline code and object layouts of the torch and Python that it was compiled with, so a key beside it (their
+    versions and the command) says which they were; with others, or without a key, it is built anew."""
     import sysconfig
 
     import torch
+    src = os.path.join(CSRC, "binding.cpp")
     home = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_path("include"), os.path.join(home, "include"),
-           os.path.join(home, "include", "torch", "csrc", "api", "include"),
-           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
-    tmp = BINDING + f".tmp{os.getpid()}"
+           os.path.join(home, "include", "torch", "csrc", "api", "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *[f"-I{p}" for p in inc],
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src,
            f"-L{os.path.join(home, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    key = "\n".join([torch.__version__, str(torch.version.git_version), str(sysconfig.get_config_var("EXT_SUFFIX")), *cmd])
+    if not force and _binding_is_current(src, key):
+        return BINDING
+    os.makedirs(BUILD, exist_ok=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")  # (needed to build only)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run([*cmd, f"-I{cuda}", "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(BINDING_KEY):
+        os.remove(BINDING_KEY)  # never a new key beside an old module
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY + f".tmp{os.getpid()}", "w") as f:
+        f.write(key)
+    os.replace(f.name, BINDING_KEY)
     return BINDING
+
+
+def _binding_is_current(src, key) -> bool:
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_KEY):
+        return False
+    with open(BINDING_KEY) as f:
+        if f.read() != key:
+            return False
+    built = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(p) <= built for p in [src, *glob.glob(os.path.join(INCLUDE, "*.h"))])
 
 
 if __name__ == "__main__":
