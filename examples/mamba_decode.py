@@ -1,12 +1,13 @@
 """A small Mamba-1 language model of random weights on this package's operators: prompts of unequal
 lengths in one padded batch, then tokens one by one, with the carried states in slots of a cache.
 
-    python examples/mamba_decode.py [--dtype bf16|f32] [--fp8] [--layers N] [--tokens N]
+    python examples/mamba_decode.py [--dtype bf16|f32] [--fp8] [--group 0|128] [--layers N] [--tokens N]
 
 Each layer is  residual += out_proj(selscan(conv(in_proj(norm(residual)))), gated by z):
 rmsnorm_fwd adds the last layer's output to the residual and normalises, conv_fwd and selscan_fwd
 read their inputs as columns of the projections' rows, and conv_step and selscan_step update the
-cache in place.  With --fp8 the norm's output goes through rmsnorm_fp8_fwd's codes and scales.
+cache in place.  With --fp8 the norm's output goes through rmsnorm_fp8_fwd's codes and scales (one a row, or with
+--group 128 one for each 128 columns).
 
 At the end it prefills prompt and generated tokens in one go and prints how far the logits are from
 those of the token-by-token run.
@@ -24,7 +25,7 @@ import selective_state_space_mamba_gb300 as ssm  # noqa: E402
 
 class Mamba:
     def __init__(self, layers=4, d_model=512, d_inner=1024, d_state=16, width=4, vocab=1000, dtype=torch.bfloat16,
-                 fp8=False, seed=0):
+                 fp8=False, seed=0, group=0):
         g = torch.Generator("cuda").manual_seed(seed)
 
         def linear(n_out, n_in):
@@ -33,7 +34,8 @@ class Mamba:
         def uniform(*shape):
             return torch.rand(shape, device="cuda", generator=g)
 
-        self.dtype, self.fp8, self.d_inner, self.d_state, self.width, self.rank = dtype, fp8, d_inner, d_state, width, d_model // 16
+        self.dtype, self.fp8, self.group = dtype, fp8, group
+        self.d_inner, self.d_state, self.width, self.rank = d_inner, d_state, width, d_model // 16
         self.embedding = (0.02 * torch.randn(vocab, d_model, device="cuda", generator=g)).to(dtype)
         self.head = linear(vocab, d_model)
         self.norm = torch.ones(d_model, device="cuda")
@@ -59,8 +61,9 @@ class Mamba:
             residual, x = x.float(), torch.zeros_like(x)
         if not self.fp8:
             return ssm.rmsnorm_fwd(x, weight, residual, residual_out=residual)
-        q, scale, residual = ssm.rmsnorm_fp8_fwd(x, weight, residual, residual_out=residual)
-        return (q.float() * scale[..., None]).to(self.dtype), residual
+        q, scale, residual = ssm.rmsnorm_fp8_fwd(x, weight, residual, group=self.group, residual_out=residual)
+        scale = scale.repeat_interleave(128, -1)[..., : x.shape[-1]] if self.group else scale[..., None]
+        return (q.float() * scale).to(self.dtype), residual
 
     def _steps(self, p, u):
         """dt, B and C of the convolved tokens."""
@@ -99,9 +102,9 @@ class Mamba:
         return (x @ self.head.T).float()
 
 
-def run(dtype=torch.bfloat16, fp8=False, layers=4, new_tokens=16, lens=(37, 5, 64, 1), seed=0):
+def run(dtype=torch.bfloat16, fp8=False, layers=4, new_tokens=16, lens=(37, 5, 64, 1), seed=0, group=0):
     """Generates greedily; returns the tokens and the distance of its logits from a prefill of everything."""
-    model = Mamba(layers=layers, dtype=dtype, fp8=fp8, seed=seed)
+    model = Mamba(layers=layers, dtype=dtype, fp8=fp8, seed=seed, group=group)
     b, L = len(lens), max(lens)
     g = torch.Generator("cuda").manual_seed(seed + 1)
     prompts = torch.randint(0, model.embedding.shape[0], (b, L), device="cuda", generator=g)
@@ -126,10 +129,12 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--dtype", choices=("bf16", "f32"), default="bf16")
     ap.add_argument("--fp8", action="store_true")
+    ap.add_argument("--group", type=int, choices=(0, 128), default=0)
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--tokens", type=int, default=16)
     args = ap.parse_args()
-    out, distance = run(torch.bfloat16 if args.dtype == "bf16" else torch.float32, args.fp8, args.layers, args.tokens)
+    out, distance = run(torch.bfloat16 if args.dtype == "bf16" else torch.float32, args.fp8, args.layers, args.tokens,
+                        group=args.group)
     for row in out.tolist():
         print(*row)
     print(f"relative distance of the last logits from one prefill: {distance:.2e}")
