@@ -68,35 +68,23 @@ __device__ __forceinline__ Raw<T, VEC> from_floats(const float (&v)[VEC]) {
   return r;
 }
 
-// Eight consecutive elements, `valid` of them inside the tensor: two or one 16-byte accesses
-// where `vec` says that the address is 16-byte aligned and all eight are valid, else one by one.
+// Eight consecutive elements from a 16-byte aligned address on, in one or two accesses.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, int valid, float (&v)[8]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      to_floats<T, 8>(load_raw<T, 8>(p), v);
-    }
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < valid ? to_f32(p[i]) : 0.f;
+    to_floats<T, 8>(load_raw<T, 8>(p), v);
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, bool vec, int valid, const float (&v)[8]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      store_raw<T, 8>(p, from_floats<T, 8>(v));
-    }
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < valid) p[i] = from_f32<T>(v[i]);
+    store_raw<T, 8>(p, from_floats<T, 8>(v));
   }
 }
 

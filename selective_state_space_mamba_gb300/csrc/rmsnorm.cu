@@ -115,7 +115,7 @@ __device__ __forceinline__ int first_column(int i) {
 template <bool kVec, typename T>
 __device__ __forceinline__ void load_columns(const T* row, int c, int width, float (&v)[8]) {
   if constexpr (kVec) {
-    load8<T>(row + c, true, 8, v);
+    load8<T>(row + c, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c + 32 * j < width ? to_f32(row[c + 32 * j]) : 0.f;
@@ -124,7 +124,7 @@ __device__ __forceinline__ void load_columns(const T* row, int c, int width, flo
 template <bool kVec, typename T>
 __device__ __forceinline__ void store_columns(T* row, int c, int width, const float (&v)[8]) {
   if constexpr (kVec) {
-    store8<T>(row + c, true, 8, v);
+    store8<T>(row + c, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)

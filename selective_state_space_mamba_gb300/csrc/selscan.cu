@@ -462,8 +462,8 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
 #pragma unroll
         for (int t = vt; t < kTokens; t += VT) {
           float d[8], u[8];
-          load8<T>(&s.dt[ring][t][vc], true, 8, d);
-          load8<T>(&s.u[ring][t][vc], true, 8, u);
+          load8<T>(&s.dt[ring][t][vc], d);
+          load8<T>(&s.u[ring][t][vc], u);
           add_n(d, bias, d);
           if (a.softplus) softplus_n(d, d);
           if (rows < kTokens && t >= rows) {  // padding leaves the state as it is
@@ -504,7 +504,7 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
       const int e = 8 * (is_c ? k - VB : k), t = e / N;
       const T* row = is_c ? s.c[kPiece ? 0 : ring][t] : s.b[ring][t];
       if constexpr (kVec) {
-        load8<T>(row + e % N, true, 8, f);
+        load8<T>(row + e % N, f);
       } else {
         row += offset_in_16<T>(is_c ? a.C : a.B, it.b, t0 + t, it.g * N);
 #pragma unroll
@@ -514,7 +514,7 @@ __device__ __forceinline__ bool prepare_role(const Params& p, const Item& it, Sh
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = 0.f;
       }
-      store8<float>((is_c ? &s.fc[kPiece ? 0 : buf][0][0] : &s.fb[buf][0][0]) + e, true, 8, f);
+      store8<float>((is_c ? &s.fc[kPiece ? 0 : buf][0][0] : &s.fb[buf][0][0]) + e, f);
     }
     if constexpr (kVec) fence_proxy_async_smem();  // these reads of the raw tile, before the tensor copies refill it
     if (!all_lanes(ok)) return false;
@@ -570,17 +570,17 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
               load_y(&s.y[buf][k * S::YP + t * CT], vc, w);
               add_n(y, w, y);
             }
-            load8<T>(&s.u[ring][t][vc], true, 8, u);
+            load8<T>(&s.u[ring][t][vc], u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[j] = skips ? u[j] : 0.f;
             fma_n(skip, u, y);
             if (a.z.ptr) {
               float z[8];
-              load8<T>(&s.z[ring][t][vc], true, 8, z);
+              load8<T>(&s.z[ring][t][vc], z);
               silu_n(z, z);
               mul_n(y, z, y);
             }
-            store8<T>(y_item + (int64_t)(t - vt) * a.channels, true, 8, y);
+            store8<T>(y_item + (int64_t)(t - vt) * a.channels, y);
           }
         }
       }
@@ -627,7 +627,7 @@ __device__ __forceinline__ bool finish_role(const Params& p, const Item& it, Sha
   if (kVec) {  // padding
     const float zero[8] = {};
     if (works)
-      for (int t = it.live + vt; t < it.n; t += VT) store8<T>(yp + (int64_t)t * a.channels, true, 8, zero);
+      for (int t = it.live + vt; t < it.n; t += VT) store8<T>(yp + (int64_t)t * a.channels, zero);
   } else {
     for (int t = it.live + (tid >> 5); t < it.n; t += kRoleThreads / 32)
       for (int c = threadIdx.x & 31; c < it.cn; c += 32) yp[(int64_t)t * a.channels + c - vc] = from_f32<T>(0.f);
