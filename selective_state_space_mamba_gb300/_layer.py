@@ -68,7 +68,9 @@ def conv_step(x, weight, bias=None, state=None, slots=None, *, silu: bool = True
 
 
 def selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups=1) -> int:
-    """Device memory that selscan_fwd needs besides its tensors (0 where it needs none)."""
+    """Device memory that selscan_fwd needs besides its tensors (0 where it needs none, or refuses the sizes)."""
+    if max(channels, dstate, ngroups) >> 31 or max(batch, seqlen) >> 63:
+        return 0  # ctypes would hand on what is left of them in 32 or 64 bits
     return int(_lib.load().ssm_selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups))
 
 

@@ -294,3 +294,13 @@ def test_profile_arrays_of_an_older_header(lib):
     assert lib.ssm_profile_end_n(None, None, 15) == _lib.SSM_OK and lib.ssm_profile_end(None, None) == _lib.SSM_OK
     assert lib.ssm_profile_end_n(None, None, -1) == INVALID
     assert len(_lib.PROFILE_KERNELS) == 15
+
+
+def test_python_workspace_sizes_that_wrap(lib):
+    """0, as for all sizes that are refused, and not the bytes of what is left of them in 32 bits."""
+    import selective_state_space_mamba_gb300 as ssm
+    f = ssm.selscan_fwd_workspace_bytes
+    assert f(1, 4096, 64, 16, 1) > 0
+    assert f(1, 4096, (1 << 32) + 64, 16, 1) == 0 and f(1, 4096, 64, (1 << 32) + 16, 1) == 0
+    assert f(1, 4096, 64, 16, (1 << 32) + 1) == 0 and f((1 << 64) + 1, 4096, 64, 16, 1) == 0 and f(1, (1 << 64) + 4096, 64, 16) == 0
+    assert f(-1, 4096, 64, 16, 1) == 0 and f(1, 4096, -64, 16, 1) == 0
