@@ -100,6 +100,13 @@ __device__ __forceinline__ float rcp_fast(float v) {
   return r;
 }
 
+// A decay rate for exp2_fast, finite where A is: a step of 0 (padding has one) leaves the state as it is, and
+// 0 times an infinity would not.
+__device__ __forceinline__ float rate_of(float A) {
+  const float v = A * kLog2e;
+  return isinf(v) ? copysignf(3.402823466e38f, v) : v;
+}
+
 // Pointwise functions on N values.  Products and sums go two at a time (packed f32), which
 // halves their instructions; N = 1 takes the scalar forms.
 template <int N>

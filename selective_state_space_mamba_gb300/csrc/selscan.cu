@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
         const int64_t chan = it.c0 + (cl + c < it.cn ? cl + c : 0);
 #pragma unroll
         for (int i = 0; i < SPL; ++i) {
-          A[c][i] = a.A[chan * N + sub * SPL + i] * kLog2e;
+          A[c][i] = rate_of(a.A[chan * N + sub * SPL + i]);
           h[c][i] = 0.f;
         }
       }

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kStepThreads, ROWS > 1 ? 8 : 1)
 #pragma unroll
   for (int k = 0; k < OWN; ++k) du[k] = delta[k] * to_f32(u_raw[k]);
   A4.get(A);
-  mul_n(A, kLog2e, A);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = rate_of(A[i]);
   float sum[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {

@@ -55,3 +55,43 @@ def test_selscan_growing_states_of_zero_cross_the_parts():
     dt, A, bc = torch.ones(1, 400, 16, device="cuda"), torch.ones(16, 16, device="cuda"), torch.ones(1, 400, 1, 16, device="cuda")
     y, h = ssm.selscan_fwd(u, dt, A, bc, bc)
     assert not y[0, :390].any() and torch.isfinite(y).all() and torch.isfinite(h).all() and (y[0, 390:] > 0).all()
+
+
+@pytest.mark.parametrize("rate", ["lowest", "infinite"])
+@pytest.mark.parametrize("d", [16, 17])
+def test_selscan_decay_rates_at_the_end_of_the_range(d, rate):
+    """A of the lowest value, or minus infinity: a token forgets all before it, a step of 0 and padding change nothing."""
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    b, L, N = 2, 37, 16
+    g = torch.Generator("cuda").manual_seed(2)
+    u, B, C = (torch.randn(*n, device="cuda", generator=g) for n in ((b, L, d), (b, L, 1, N), (b, L, 1, N)))
+    low = torch.finfo(torch.float32).min if rate == "lowest" else float("-inf")
+    A, h0 = torch.full((d, N), low, device="cuda"), torch.randn(b, d, N, device="cuda", generator=g)
+    dt = torch.full((b, L, d), 0.5, device="cuda")
+    lens = torch.tensor([L, 20], dtype=torch.int32, device="cuda")
+    y, h = ssm.selscan_fwd(u, dt, A, B, C, h0=h0, lens=lens, softplus=False)
+    own = 0.5 * u[..., None] * B  # [b, L, d, N]
+    want = (own * C).sum(-1)
+    want[1, 20:] = 0
+    assert torch.allclose(y, want, rtol=1e-5, atol=1e-5)
+    assert torch.equal(h, torch.stack([own[0, -1], own[1, 19]]))
+    y1, h1 = ssm.selscan_step(u[:, 0], dt[:, 0], A, B[:, 0], C[:, 0], state=h0, softplus=False)
+    assert torch.equal(h1, own[:, 0]) and torch.allclose(y1, want[:, 0], rtol=1e-5, atol=1e-5)
+    y, h = ssm.selscan_fwd(u, 0 * dt, A, B, C, h0=h0, lens=lens, softplus=False)
+    assert torch.equal(h, h0) and torch.isfinite(y).all()
+    y1, h1 = ssm.selscan_step(u[:, 0], 0 * dt[:, 0], A, B[:, 0], C[:, 0], state=h0, softplus=False)
+    assert torch.equal(h1, h0) and torch.isfinite(y1).all()
+
+
+def test_selscan_a_rate_that_is_no_number_stays_none():
+    import torch
+    import selective_state_space_mamba_gb300 as ssm
+    A = -torch.ones(8, 16, device="cuda")
+    A[3, 5] = float("nan")
+    x, bc = torch.ones(1, 5, 8, device="cuda"), torch.ones(1, 5, 1, 16, device="cuda")
+    y, h = ssm.selscan_fwd(x, x, A, bc, bc)
+    y1, h1 = ssm.selscan_step(x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0])
+    for a, s in ((y[0], h[0]), (y1, h1[0])):
+        assert torch.isnan(a[:, 3]).all() and torch.isnan(s[3, 5])
+        assert torch.isfinite(a[:, :3]).all() and torch.isfinite(a[:, 4:]).all() and int(torch.isnan(s).sum()) == 1
