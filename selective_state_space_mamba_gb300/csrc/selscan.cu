@@ -110,11 +110,10 @@ struct Shared {
   uint64_t raw_full[RING], raw_free[RING], full[2], done[2], y_free[2];
   // and of the items: written down, read, scanned (the finish role may be two items behind the scan)
   uint64_t item_full[2], item_free[2], item_done[4];
-  // What void_items needs once a wait has run out: the last items' numbers and how many were claimed, how many each
-  // scan and finish warp is through with, the phase at which all warps have left, and whether one gave up.
+  // What give_up needs: the last items' numbers and how many were claimed, how many each scan and finish warp is
+  // through with, and whether a wait ran out.
   int64_t claimed[8];
   uint32_t claims, closed[(kScanThreads + kRoleThreads) / 32], failed;
-  uint64_t left;
 };
 
 // Channels vc to vc + 7 of a row of Shared::y.
@@ -239,17 +238,6 @@ __device__ __forceinline__ bool wait_tile(uint64_t* bars, uint32_t tile, uint32_
     if (t0 == 0) t0 = now;
     if (now - t0 > 2 * limit_ns) return false;
   }
-}
-
-// Whether a barrier's phase of this parity is complete.
-__device__ __forceinline__ bool mbar_phase_done(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // After a wait that ran out (never but on a GPU that stopped): a state that cannot pass for one.
@@ -387,23 +375,27 @@ __device__ __forceinline__ bool copy_role(const Params& p, const Maps& maps, con
     // One thread, five tensor copies a tile.  They bring padding too, and zeros past the tensors' ends.
     if (tid != 0) return true;
     const uint32_t bytes = kTokens * sizeof(T) * (CT * (kPiece || !a.z.ptr ? 2 : 3) + N * (kPiece ? 1 : 2));
-    for (int rows = it.live; rows > 0; rows -= kTokens, t += kTokens, ++tile) {
-      const int ring = tile % RING;
-      uint64_t* bar = &s.raw_full[ring];
-      if (tile >= RING && !wait_tile(s.raw_free, tile - RING, RING, p.ctl.spin_limit_ns)) return false;
-      mbar_arrive_expect_tx(bar, bytes);
-      const auto load = [&](T* dst, const CUtensorMap* map, int c, uint32_t which) {
-        const bool inner = (p.inner & which) != 0;
-        tc::tma_load_3d(dst, map, c, inner ? (int)it.b : (int)t, inner ? (int)t : (int)it.b, bar);
-      };
-      load(&s.dt[ring][0][0], &maps.dt, it.c0, kDt);
-      load(&s.u[ring][0][0], &maps.u, it.c0, kU);
-      load(&s.b[ring][0][0], &maps.B, it.g * N, kB);
-      if constexpr (!kPiece) {
-        load(&s.c[ring][0][0], &maps.C, it.g * N, kC);
-        if (a.z.ptr) load(&s.z[ring][0][0], &maps.z, it.c0, kZ);
+    const auto tiles = [&](auto any_inner) {  // (asked in every tile, it costs 0.5 % of the whole)
+      for (int rows = it.live; rows > 0; rows -= kTokens, t += kTokens, ++tile) {
+        const int ring = tile % RING;
+        uint64_t* bar = &s.raw_full[ring];
+        if (tile >= RING && !wait_tile(s.raw_free, tile - RING, RING, p.ctl.spin_limit_ns)) return false;
+        mbar_arrive_expect_tx(bar, bytes);
+        const auto load = [&](T* dst, const CUtensorMap* map, int c, uint32_t which) {
+          const bool inner = decltype(any_inner)::value && (p.inner & which) != 0;
+          tc::tma_load_3d(dst, map, c, inner ? (int)it.b : (int)t, inner ? (int)t : (int)it.b, bar);
+        };
+        load(&s.dt[ring][0][0], &maps.dt, it.c0, kDt);
+        load(&s.u[ring][0][0], &maps.u, it.c0, kU);
+        load(&s.b[ring][0][0], &maps.B, it.g * N, kB);
+        if constexpr (!kPiece) {
+          load(&s.c[ring][0][0], &maps.C, it.g * N, kC);
+          if (a.z.ptr) load(&s.z[ring][0][0], &maps.z, it.c0, kZ);
+        }
       }
-    }
+      return true;
+    };
+    return p.inner == 0 ? tiles(std::false_type{}) : tiles(std::true_type{});
   } else {
     Rows<T, CT> dt(a.dt, it.b, t, it.c0, it.cn), u(a.u, it.b, t, it.c0, it.cn);
     Rows<T, CT> z(kPiece || !a.z.ptr ? a.u : a.z, it.b, t, it.c0, it.cn);
@@ -732,15 +724,22 @@ __device__ void void_item(const Params& p, const Item& it, int lane, int lanes) 
   }
 }
 
-// After a wait between the roles ran out: what this CTA has claimed and not written, and what nobody has claimed yet
-// (the other CTAs may have given up too).
+// The last thing of a warp (of tensor copies: of the one thread) whose wait for another role ran out: NaN to what this
+// CTA has claimed and not written, and to what nobody has claimed yet (the other CTAs may have given up too).  Other
+// warps may be at an item still: its elements get what is right from them or NaN from here.
 template <typename T, int N, bool kPiece, bool kVec>
-__device__ __forceinline__ void void_items(const Params& p, const Shared<T, N, kPiece, kVec>& s, int lane, int lanes) {
+__device__ __forceinline__ void give_up(const Params& p, Shared<T, N, kPiece, kVec>& s, int lanes) {
+  const int lane = lanes > 1 ? (int)(threadIdx.x & 31) : 0;
   const int split = kPiece ? p.sp.split - 1 : p.sp.split;
   const int64_t chains = p.a.batch * p.sp.tiles * split;
-  uint32_t k = s.claims;
-  for (int w = 0; w < (kPiece ? kScanThreads : kScanThreads + kRoleThreads) / 32; ++w) k = min(k, s.closed[w]);
-  for (; k < s.claims; ++k)
+  *reinterpret_cast<volatile uint32_t*>(&s.failed) = 1;
+  if (lane == 0 && p.hdr) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
+  __threadfence_block();  // what is claimed from now on, the claiming thread gives up itself
+  const volatile uint32_t *claims = &s.claims, *closed = s.closed;
+  const uint32_t end = *claims;
+  uint32_t k = end;
+  for (int w = 0; w < (kPiece ? kScanThreads : kScanThreads + kRoleThreads) / 32; ++w) k = min(k, closed[w]);
+  for (; k < end; ++k)
     void_item<T, N, kPiece>(p, item_of<tile_channels(N), kPiece>(p, s.claimed[k & 7], split, chains), lane, lanes);
   while (!kPiece && p.queue) {
     int64_t id = 0;
@@ -749,26 +748,6 @@ __device__ __forceinline__ void void_items(const Params& p, const Shared<T, N, k
     if (id >= chains * p.sp.subs) return;
     void_item<T, N, kPiece>(p, item_of<tile_channels(N), kPiece>(p, id, split, chains), lane, lanes);
   }
-}
-
-// The last thing of each warp (of tensor copies: of the one thread).  The last of them to leave writes what a wait
-// that ran out has left unwritten.  (Two may take themselves for the last, and then write the same.)
-template <typename T, int N, bool kPiece, bool kVec>
-__device__ __forceinline__ void leave(const Params& p, Shared<T, N, kPiece, kVec>& s, bool ok, int lanes) {
-  const int lane = lanes > 1 ? (int)(threadIdx.x & 31) : 0;
-  if (lanes > 1) ok = all_lanes(ok);
-  bool clear = false;
-  if (lane == 0) {
-    volatile uint32_t* failed = &s.failed;
-    if (!ok) {
-      *failed = 1;
-      if (p.hdr) record_error(p.hdr, kErrorTag, SSM_ERR_TIMEOUT);
-    }
-    mbar_arrive(&s.left);
-    clear = mbar_phase_done(&s.left, 0) && *failed != 0;
-  }
-  if (lanes > 1) clear = __any_sync(0xffffffffu, clear);
-  if (clear) void_items<T, N, kPiece, kVec>(p, s, lane, lanes);
 }
 
 // kVec: Params::vec.  kPiece: the first kernel (end state and sum of delta of each part of a split time
@@ -782,23 +761,22 @@ __global__ void __launch_bounds__(kThreads, kResident)
   extern __shared__ __align__(128) unsigned char smem[];
   S& s = *reinterpret_cast<S*>(smem);
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    for (int i = 0; i < S::RING; ++i) {
-      mbar_init(&s.raw_full[i], kVec ? 1 : 2 * kRoleThreads);
-      mbar_init(&s.raw_free[i], kRoleThreads / 32);
+  if (tid < 8) {  // a thread the i-th of each kind of barrier
+    if (tid < S::RING) {
+      mbar_init(&s.raw_full[tid], kVec ? 1 : 2 * kRoleThreads);
+      mbar_init(&s.raw_free[tid], kRoleThreads / 32);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.full[i], kRoleThreads / 32);
-      mbar_init(&s.done[i], kScanThreads / 32);
-      mbar_init(&s.y_free[i], kRoleThreads / 32);
-      mbar_init(&s.item_full[i], 1);
+    if (tid < 2) {
+      mbar_init(&s.full[tid], kRoleThreads / 32);
+      mbar_init(&s.done[tid], kScanThreads / 32);
+      mbar_init(&s.y_free[tid], kRoleThreads / 32);
+      mbar_init(&s.item_full[tid], 1);
       // warps that read it; with tensor copies the copy role is the one thread that wrote it
-      mbar_init(&s.item_free[i], (kThreads - kRoleThreads * (kVec ? 1 : 0)) / 32);
+      mbar_init(&s.item_free[tid], (kThreads - kRoleThreads * (kVec ? 1 : 0)) / 32);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&s.item_done[i], kScanThreads / 32);
-    mbar_init(&s.left, (kThreads - (kVec ? kRoleThreads : 0)) / 32 + (kVec ? 1 : 0));
-    s.claims = s.failed = 0;
-    for (uint32_t& c : s.closed) c = 0;
+    if (tid < 4) mbar_init(&s.item_done[tid], kScanThreads / 32);
+    if (tid < (kScanThreads + kRoleThreads) / 32) s.closed[tid] = 0;
+    if (tid == 0) s.claims = s.failed = 0;
     fence_mbar_init();
   }
   griddep_wait();
@@ -844,6 +822,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
     if (claims || (role == 0 && !kVec))  // shared memory stays until the copies are there, whatever the other roles do
       for (uint32_t t = tile0 < S::RING ? 0 : tile0 - S::RING; t < tile0; ++t)
         ok = wait_tile(s.raw_full, t, S::RING, kCopiesNs) && ok;
+    if (claims) {  // items that it claimed after another warp gave up
+      __threadfence_block();
+      ok = *reinterpret_cast<volatile uint32_t*>(&s.failed) == 0 && ok;
+    }
+    if (role == 0 && !kVec) ok = all_lanes(ok);
   } else {
     int sub, cl;  // a scan thread's place in a channel's entries, and its first channel
     lane_of<S::LPC>(tid & 31, sub, cl);
@@ -944,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
       if (kPiece || !p.queue) break;
     }
   }
-  leave(p, s, ok, kVec && tid >= kScanThreads && tid < kScanThreads + kRoleThreads ? 1 : 32);
+  if (!ok) give_up<T, N, kPiece, kVec>(p, s, kVec && tid >= kScanThreads && tid < kScanThreads + kRoleThreads ? 1 : 32);
 }
 
 template <typename F>
