@@ -16,7 +16,7 @@
 //       residual 19.5, 12.3).
 //   Few rows: one vector a thread for up to 8192 columns, the shortest way through a single row.
 // What a thread does not hold of wider rows is read again.  No output is written before the last
-// read of its element, so residual_out may be residual.
+// read of its element, so residual_out may be residual; what is held is written to it at once.
 #include "layer_common.cuh"
 
 #include <cuda_fp8.h>
@@ -164,16 +164,16 @@ __device__ __forceinline__ void add_squares(const float (&v)[8], float (&sum)[2]
   }
 }
 
-// Writes vector i of a row: residual_out, and y or q.  All lanes of a warp take part (the scale of
-// a group is a reduction over lanes); `have`: this one has a vector.
-template <typename T, typename R, bool kRes, bool kFp8, bool kVec>
+// Writes vector i of a row: residual_out unless it is written already (kEarly), and y or q.  All lanes of a warp take
+// part (the scale of a group is a reduction over lanes); `have`: this one has a vector.
+template <typename T, typename R, bool kRes, bool kFp8, bool kVec, bool kEarly>
 __device__ __forceinline__ void output(const NormParams& p, int64_t row, int i, bool have, const float (&r)[8],
                                        float rstd, float row_scale) {
   const int c = first_column<kVec>(i);
   float v[8] = {};
   if (have) {
     normed<kVec>(p, i, r, rstd, v);
-    if constexpr (kRes)
+    if constexpr (kRes && !kEarly)
       if (p.residual_out) store_columns<kVec>(static_cast<R*>(p.residual_out) + row * p.width, c, p.width, r);
   }
   if constexpr (!kFp8) {
@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : HOLD > 1 ? kHoldMaxThre
           float e[8];
           rn[k].get(e);
           add_n(held[k], e, held[k]);
+          if (p.residual_out)  // here, beside the loads and the sum (16384 x 12288: 202 us, with the output 247)
+            store_columns<kVec>(static_cast<R*>(p.residual_out) + row * p.width, 8 * (tid + k * threads), p.width, held[k]);
         }
         add_squares(held[k], sum);
       }
@@ -309,13 +311,13 @@ __global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : HOLD > 1 ? kHoldMaxThre
   for (int k = 0; k < HOLD; ++k) {
     const int i = tid + k * threads;
     if (i - (tid & 31) >= nvec) break;  // (asked before each output, the whole takes 1 % longer)
-    output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, held[k], rstd, row_scale);
+    output<T, R, kRes, kFp8, kVec, (HOLD > 1 && kVec)>(p, row, i, i < nvec, held[k], rstd, row_scale);
   }
   if constexpr (HOLD == 1) {  // whole warps: i - (tid & 31) is the same in a warp's lanes
     for (int i = first; i - (tid & 31) < nvec; i += threads) {
       float r[8] = {};
       if (i < nvec) load_r<T, R, kRes, kVec>(p, row, i, r);
-      output<T, R, kRes, kFp8, kVec>(p, row, i, i < nvec, r, rstd, row_scale);
+      output<T, R, kRes, kFp8, kVec, false>(p, row, i, i < nvec, r, rstd, row_scale);
     }
   }
 }
