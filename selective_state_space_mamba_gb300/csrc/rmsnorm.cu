@@ -338,8 +338,13 @@ cudaError_t launch_rows(const NormParams& p, int64_t rows, bool vec, cudaStream_
     if (rows < kManyRows || nvec > 5 * kHoldMaxThreads) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1, 1>, 1);
     if (nvec <= 32) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 1, kWarpRows>);
     if (nvec <= 96) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, kWarpRows>);
-    if (nvec <= 160) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, kWarpRows>);
-    if (nvec <= 192) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, 1>, 3);
+    // Rows that are not aligned, bf16 or with a residual: three vectors a thread, not five (16384 rows, model's type, bf16:
+    // 2561 47 us, with five 75; 1031 without a warp a row 22, with 26; with a bf16 residual 70, 80 and 31, 47.  f32 without
+    // a residual, 8 bits, 4099: with three 83, with five 74).
+    constexpr bool three = !kVec && (kRes || sizeof(T) == 2);
+    if constexpr (!three)
+      if (nvec <= 160) return warps(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, kWarpRows>);
+    if (nvec <= (three ? 3 * kHoldMaxThreads : 192)) return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 3, 1>, 3);
     return go(rmsnorm_kernel<T, R, kRes, kFp8, kVec, 5, 1>, 5);
   };
   return vec ? with(std::true_type{}) : with(std::false_type{});
