@@ -239,9 +239,10 @@ SSM_API ssm_status ssm_ssd_step(const void *x, const void *dt, const float *A, c
  * The outputs and states need the alignment of one element only.
  *
  * lens (prompts): NULL, or [batch] int32 in device memory: sequence b has lens[b] tokens (values
- * outside 0 .. seqlen are clamped) and the rest of its row is padding.  Padding is not read, its
- * outputs are 0 and it leaves the states as they are, so a sequence of no tokens hands its
- * initial state on.
+ * outside 0 .. seqlen are clamped) and the rest of its row is padding.  Padding is not used (the
+ * scan's copies may read what of it lies in the last 16 tokens that a sequence reaches into; its
+ * values, NaN too, go nowhere), its outputs are 0 and it leaves the states as they are, so a sequence
+ * of no tokens hands its initial state on.
  * slots (steps): NULL (sequence b has the states' row b; then nslots must equal batch), or [batch]
  * int32 in device memory: sequence b has row slots[b] of the nslots rows of state_in and
  * state_out.  A slot outside 0 .. nslots-1 (-1, say) marks an unused place of the batch: its
@@ -353,7 +354,9 @@ SSM_API ssm_status ssm_selscan_step(const ssm_selscan_args *args, const int32_t 
  *   q, scale      ssm_rmsnorm_fp8_fwd: e4m3 codes [rows, width], dense, and f32 scales, one for
  *                 each `group` columns of a row (group 128: [rows, ceil(width / 128)]) or for each
  *                 row (group 0: [rows]): scale = max(max|v| / 448, 2^-126), q = e4m3(v / scale),
- *                 round to nearest even.  A NaN in v gives NaN in q there and in its scale.
+ *                 round to nearest even.  Both divisions are products with a reciprocal (good to
+ *                 2 ulp of f32, as v itself is to a few): a v that close to a tie may have the code
+ *                 on its other side.  A NaN in v gives NaN in q there and in its scale.
  * Sizes: rows 0 .. 2^31 - 1, width 1 .. 2^30.  No workspace; one kernel.
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED (group), SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
  */

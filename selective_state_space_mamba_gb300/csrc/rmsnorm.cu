@@ -5,7 +5,7 @@
 // A CTA or a warp a row.  A thread owns vectors of eight columns, tid + k * threads: consecutive columns where
 // rows are aligned, so that the columns of 16 neighbouring lanes are a scale group of 128; else every
 // 32nd of the warp's 256, so that its lanes still access neighbouring elements (odd rows of 2561 bf16,
-// 8 bits, 16384 of them: 85 us, with consecutive columns 224; 2560 columns: 48).  r of a thread's first
+// 8 bits, 16384 of them: 80 us, with consecutive columns 224; 2560 columns: 47).  r of a thread's first
 // HOLD vectors stays in registers between the sum of squares and the output.
 //   Many rows: up to five vectors a thread, so that a CTA has few warps to join in its sums
 //       and many CTAs are resident; a row's loads are all in flight at once.  32768 x 2560, bf16

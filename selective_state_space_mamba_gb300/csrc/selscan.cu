@@ -18,10 +18,10 @@
 // They meet at mbarriers, so the scan does not stop for the rest, and each goes through the CTA's items
 // by itself, so that an item's first tiles come in beside the last ones of the item before.
 //
-// b4 L8192 d5120 N16 in bf16: 765 us, and b1 L65521 d1536 in f32: 807 us, against 200 and 243 us of
+// b4 L8192 d5120 N16 in bf16: 776 us, and b1 L65521 d1536 in f32: 810 us, against 200 and 243 us of
 // memory and 277 and 168 of exponentials.  The multiply-adds of two state entries read three register
 // pairs, which takes 3.2 cycles a warp instruction and not 2: the scan alone takes 109 cycles a token
-// for the two CTAs of an SM, the same as in registers only; with the other roles beside it, 177.
+// for the two CTAs of an SM, the same as in registers only; with the other roles beside it, 180.
 #include <cstddef>
 
 #include "layer_common.cuh"
@@ -52,7 +52,7 @@ constexpr uint64_t kCopiesNs = 1000000000;  // for copies in flight, whatever th
 constexpr int64_t kStallCopies = (int64_t)1 << 40;
 
 // State entries of a lane's channel.  With two for 8 entries a tile has 64 channels like those of 16 entries:
-// the other roles take the time of 128 (b4 L4096 d2560: 221 us, with four 261).
+// the other roles take the time of 128 (b4 L4096 d2560: 230 us; before the roles' fences 221, with four 261).
 __host__ __device__ constexpr int lane_states(int n) { return n == 8 ? 2 : 4; }
 __host__ __device__ constexpr int tile_channels(int n) { return kScanThreads * lane_states(n) * 2 / n; }
 
@@ -1077,19 +1077,19 @@ cudaError_t launch(const ssm_selscan_args& a, const SelscanSplit& sp, void* work
 
 }  // namespace
 
-// A CTA alone on its SM takes 113 cycles a token, two 177 together.  All times below: d5120 or the like,
+// A CTA alone on its SM takes 115 cycles a token, two 180 together.  All times below: d5120 or the like,
 // N16, bf16.
 //
 // The time axis is split where the chains are less than a third of the resident CTAs and the sequence is
 // long enough, into as many parts as fill them; the first kernel does 0.7 of the second's work once more
-// (80 chains: L8192 344 us in four parts, 428 in one, L2048 99 and 110, L1024 63 and 57; 24 chains: L384
+// (80 chains: L8192 344 us in four parts (now 349), 428 in one, L2048 99 and 110, L1024 63 and 57; 24 chains: L384
 // 20 and 24, L256 19 and 17; 110 chains L4096: 236 in three parts, 217 in one).  Parts too short for the
 // queue are as many as run at once (50 chains L1024: 38 us in six parts, 48 in seven).
 //
 // A queue of items of kSubTokens tokens serves chains that are more than the resident CTAs but few of
-// their waves, so that the last wave is short (320 chains L8192: 770 us, without 1300; items of 256 or
+// their waves, so that the last wave is short (320 chains L8192: 770 us (now 776), without 1300; items of 256 or
 // 1024 tokens 776, 785; from eight waves on 1428 us either way), and chains that are a little more than
-// the SMs: with a CTA an SM they share the SMs alike (160 chains L8192: 498 us, without 695; 180 chains
+// the SMs: with a CTA an SM they share the SMs alike (160 chains L8192: 498 us (now 485), without 695; 180 chains
 // L4096: 285, 351; 240 chains L4096 365, 351).
 SelscanSplit selscan_split(int64_t batch, int64_t seqlen, int channels, int dstate, int ngroups) {
   const int ct = tile_channels(dstate);
