@@ -368,6 +368,85 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
                                        int group, float eps, ssm_dtype dtype, ssm_dtype res_dtype,
                                        ssm_stream_t stream);
 
+/*
+ * The gated delta rule: a state that is corrected where it answers a key wrongly, beside the decay.
+ * Per sequence and head, over tokens t (state S of headdim x dstate, dstate contiguous, as ssm_ssd_fwd's):
+ *     a_t    = exp(A[h] softplus(dt_t[h] + dt_bias[h]))     (without the softplus if softplus is 0)
+ *     beta_t = sigmoid(beta_t[h])                           (as it is if sigmoid is 0)
+ *     k_t, q_t divided by sqrt(sum of their squares + 1e-6) (as they are if l2norm is 0)
+ *     S_t    = a_t S_{t-1} + beta_t (v_t - a_t S_{t-1} k_t) k_t^T
+ *     y_t    = scale S_t q_t
+ *   q, k       [batch, seqlen, ngroups * dstate] `dtype` (a token's groups are adjacent); head h reads
+ *              group h / (nheads / ngroups)
+ *   v          [batch, seqlen, nheads * headdim] `dtype`
+ *   dt, beta   [batch, seqlen, nheads] `dtype`
+ *   A          [nheads] f32 (A < 0 for a decay); dt_bias [nheads] f32 or NULL (zeros)
+ *   h0         [batch, nheads, headdim, dstate] f32 or NULL (zeros)
+ *   y          [batch, seqlen, nheads * headdim] `dtype`, dense
+ *   h_final    like h0, or NULL
+ * lens as above: padding is not used, its outputs are 0, and the state is that after a sequence's last token.
+ * States and sums are f32; a decay below 2^-150 is 0.
+ * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing nheads, dstate in {32, 64, 128}, headdim >= 1,
+ * nheads * headdim and ngroups * dstate <= 2^30.
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
+ */
+typedef struct {
+    ssm_tokens q, k, v, dt, beta;
+    const float *A, *dt_bias, *h0;
+    const int32_t *lens;
+    void *y;
+    float *h_final;
+    int64_t batch, seqlen;
+    int32_t nheads, headdim, dstate, ngroups;
+    int32_t softplus, sigmoid, l2norm;
+    float scale;
+    int32_t dtype; /* ssm_dtype */
+    int32_t reserved; /* 0 */
+} ssm_delta_args;
+SSM_API ssm_status ssm_delta_fwd(const ssm_delta_args *args, ssm_stream_t stream);
+
+/*
+ * The same for ONE new token per sequence, over the f32 states [nslots, nheads, headdim, dstate]:
+ * h0 is state_in (NULL for zeros), h_final state_out (required), which may be the same pointer (in
+ * place; any other overlap is rejected); seqlen and lens are not used.  One kernel, no workspace.
+ */
+SSM_API ssm_status ssm_delta_step(const ssm_delta_args *args, const int32_t *slots, int64_t nslots,
+                                  ssm_stream_t stream);
+
+/*
+ * The norm of a scan's output with its gate, before the output projection:
+ *     y = rms(x) * weight * silu(z)          (gate_first 0)
+ *     y = rms(x * silu(z)) * weight          (gate_first 1)
+ * in f32, rms(v) = v / sqrt(mean(v^2) + eps) over each `group` columns of a row (0: the whole row).
+ *   x, z     [rows, width] `dtype`, x_stride and z_stride elements from row to row
+ *   weight   [weight_width] f32: one for each column (width), or shared by the groups (group)
+ *   y        [rows, width] `dtype`, dense
+ * Sizes: rows 0 .. 2^31 - 1, width 1 .. 2^30, group dividing width, rows * groups < 2^31.  No workspace; one kernel.
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
+ */
+SSM_API ssm_status ssm_gatednorm_fwd(const void *x, int64_t x_stride, const void *z, int64_t z_stride,
+                                     const float *weight, int weight_width, void *y, int64_t rows, int width, int group,
+                                     int gate_first, float eps, ssm_dtype dtype, ssm_stream_t stream);
+
+/*
+ * The norm after a block, the residual, and the norm before the next block:
+ *     r = alpha residual + rms(x) * weight [* silu(z)];  residual_out = r
+ *     y = rms(r) * next_weight
+ * in f32 over whole rows; y is computed from r before residual_out's rounding.
+ *   x             [rows, width] `dtype`, x_stride elements from row to row: the block's output
+ *   z             the same with z_stride, or NULL: no gate
+ *   weight, next_weight [width] f32
+ *   residual      [rows, width] dense, `res_dtype` (SSM_F32, or `dtype`); residual_out the same
+ *                 (it may be the same pointer: updated in place; NULL: not written)
+ *   y             [rows, width] `dtype`, dense
+ * Sizes: rows 0 .. 2^31 - 1, width 1 .. 2^30.  No workspace; one kernel.
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
+ */
+SSM_API ssm_status ssm_blocknorm_fwd(const void *x, int64_t x_stride, const float *weight, const void *z,
+                                     int64_t z_stride, const void *residual, void *residual_out,
+                                     const float *next_weight, void *y, int64_t rows, int width, float alpha, float eps,
+                                     ssm_dtype dtype, ssm_dtype res_dtype, ssm_stream_t stream);
+
 /* Workspace size in bytes for ssm_linscan_fwd on rows x len (0 when a size is negative). */
 SSM_API size_t ssm_linscan_workspace_bytes(int64_t rows, int64_t len);
 
@@ -547,10 +626,11 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
  * 7 linscan_baseline (ssm_linscan_baseline, all its launches), 8 ssd_state_fixup (the second
  * kernel of the one-kernel state pass with split chains), 9 conv (ssm_conv_fwd), 10 conv_step,
  * 11 selscan_piece (the first kernel of ssm_selscan_fwd with a split time axis), 12 selscan
- * (ssm_selscan_fwd), 13 selscan_step, 14 rmsnorm (both forms).  Host-side only;
+ * (ssm_selscan_fwd), 13 selscan_step, 14 rmsnorm (both forms), 15 delta (ssm_delta_fwd), 16 delta_step,
+ * 17 gatednorm, 18 blocknorm.  Host-side only;
  * process-global; not thread-safe.
  */
-#define SSM_PROFILE_KERNELS 15
+#define SSM_PROFILE_KERNELS 19
 #define SSM_PROFILE_END_KERNELS 9
 SSM_API ssm_status ssm_profile_begin(int max_launches);
 SSM_API ssm_status ssm_profile_end(double *ms_out, int64_t *launches_out);

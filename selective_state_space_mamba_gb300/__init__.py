@@ -1,5 +1,5 @@
 """GB300 (sm_103a) selective state-space forward: Mamba-2 chunked SSD, the scalar scan, and the
-operators around a layer's scan (short convolution, per-channel selective scan, norm).
+operators around a layer's scan (short convolution, per-channel selective scan, gated delta rule, norms).
 
 Python entry points with the names of the C ABI (include/ssm.h).  They only marshal torch
 CUDA tensors into the C calls; every step of the computation runs in the library's CUDA
@@ -12,6 +12,9 @@ kernels, enqueued on the current torch stream.  PyTorch supplies device memory a
     y, res = rmsnorm_fwd(x, weight, residual)                    # or rmsnorm_fp8_fwd
     u, conv_state = conv_fwd(x, w, bias)                         # conv_step for one token
     y, h = selscan_fwd(u, dt, A, B, C, D, z, dt_bias)            # selscan_step for one token
+    y, h = delta_fwd(q, k, v, dt, beta, A, dt_bias)              # gated delta rule; delta_step for one token
+    y = gatednorm_fwd(y, z, weight, group=64)                    # behind a scan
+    y, res = blocknorm_fwd(x, weight, residual, next_weight)     # between two blocks
 
 Importing the package does not load the library; the first call does (and fails loudly if
 it cannot).
@@ -25,11 +28,12 @@ __all__ = ["ssd_fwd", "ssd_step", "linscan_fwd", "linscan_baseline", "tune_ssd_f
            "get_ssd_fwd_plan", "clear_ssd_fwd_plans", "plan_id", "tune_linscan_fwd",
            "set_linscan_shape", "get_linscan_shape", "clear_linscan_shapes", "Workspace", "check_device_status", "ssd_fwd_workspace_bytes",
            "linscan_workspace_bytes", "conv_fwd", "conv_step", "selscan_fwd", "selscan_step",
-           "selscan_fwd_workspace_bytes", "rmsnorm_fwd", "rmsnorm_fp8_fwd", "SsmError", "version"]
+           "selscan_fwd_workspace_bytes", "rmsnorm_fwd", "rmsnorm_fp8_fwd", "delta_fwd", "delta_step", "gatednorm_fwd",
+           "blocknorm_fwd", "SsmError", "version"]
 
 
 _LAYER = ("conv_fwd", "conv_step", "selscan_fwd", "selscan_step", "selscan_fwd_workspace_bytes", "rmsnorm_fwd",
-          "rmsnorm_fp8_fwd")
+          "rmsnorm_fp8_fwd", "delta_fwd", "delta_step", "gatednorm_fwd", "blocknorm_fwd")
 
 
 def __getattr__(name):
@@ -395,11 +399,12 @@ class KernelTimer:
 
     def __exit__(self, *exc):
         import ctypes
-        n = len(_lib.PROFILE_KERNELS)
+        names = _lib.PROFILE_KERNELS + _lib.PROFILE_KERNELS_MORE
+        n = len(names)
         ms = (ctypes.c_double * n)()
         cnt = (ctypes.c_int64 * n)()
         _lib.check(_lib.load().ssm_profile_end_n(ctypes.cast(ms, ctypes.c_void_p), ctypes.cast(cnt, ctypes.c_void_p), n),
                    "ssm_profile_end_n")
-        self.ms = {k: float(ms[i]) for i, k in enumerate(_lib.PROFILE_KERNELS)}
-        self.launches = {k: int(cnt[i]) for i, k in enumerate(_lib.PROFILE_KERNELS)}
+        self.ms = {k: float(ms[i]) for i, k in enumerate(names)}
+        self.launches = {k: int(cnt[i]) for i, k in enumerate(names)}
         return False

@@ -1,8 +1,8 @@
 """Python entry points of the operators around a layer's scan (include/ssm.h, the section of
 ssm_tokens): the short causal convolution and the selective scan, for prompts and for single
-tokens, and the root-mean-square norm.
+tokens, the root-mean-square norm, the gated delta rule and the norms with a gate and a residual.
 
-Token tensors (x, u, dt, z, B, C) may be strided in all but the last dimension, for example
+Token tensors (x, u, dt, z, B, C, q, k, v, beta) may be strided in all but the last dimension, for example
 columns of a projection's wider rows.  The checks of shapes and types, the allocation of outputs
 and the C calls are in the compiled module _binding (csrc/binding.cpp), because a call for one
 token takes less time on the GPU than they take in Python; it is built in-tree beside the
@@ -18,7 +18,8 @@ import torch  # noqa: F401 - _binding needs its libraries loaded
 from . import _build, _lib
 
 _BOUND = ("ssm_conv_fwd", "ssm_conv_step", "ssm_selscan_fwd_workspace_bytes", "ssm_selscan_fwd", "ssm_selscan_step",
-          "ssm_rmsnorm_fwd", "ssm_rmsnorm_fp8_fwd")
+          "ssm_rmsnorm_fwd", "ssm_rmsnorm_fp8_fwd", "ssm_delta_fwd", "ssm_delta_step", "ssm_gatednorm_fwd",
+          "ssm_blocknorm_fwd")
 _native = None
 
 
@@ -134,3 +135,57 @@ def rmsnorm_fp8_fwd(x, weight, residual=None, *, eps: float = 1e-5, group: int =
     """
     r = (_native or _load()).rmsnorm_fp8_fwd(x, weight, residual, eps, group, q, scale, residual_out)
     return _checked(r, "ssm_rmsnorm_fp8_fwd")
+
+
+def delta_fwd(q, k, v, dt, beta, A, dt_bias=None, h0=None, lens=None, *, scale=None, softplus: bool = True,
+              sigmoid: bool = True, l2norm: bool = True, y=None, h_final=None, return_final_state: bool = True):
+    """Gated delta rule over a prompt (ssm_delta_fwd).
+
+    q, k [b, L, G, N], v [b, L, nh, H], dt, beta [b, L, nh] (all float32 or all bfloat16; strided in all but
+    the last dimension, heads and groups of a token adjacent), A, dt_bias [nh] float32, h0 [b, nh, H, N] float32
+    (None: zeros), lens [b] int32: tokens of each sequence (None: L); N in {32, 64, 128}; head h reads
+    group h // (nh / G).  scale: None for N ** -0.5.  Without softplus the decay is exp(A (dt + dt_bias)), without
+    sigmoid beta is taken as it is, without l2norm q and k are.  Returns (y, h_final): y [b, L, nh, H], 0 in
+    the padding, and the float32 state after the last token (None when return_final_state is False).
+    """
+    r = (_native or _load()).delta_fwd(q, k, v, dt, beta, A, dt_bias, h0, lens, scale, softplus, sigmoid, l2norm, y, h_final,
+                                       return_final_state)
+    return _checked(r, "ssm_delta_fwd")
+
+
+def delta_step(q, k, v, dt, beta, A, dt_bias=None, state=None, slots=None, *, scale=None, softplus: bool = True,
+               sigmoid: bool = True, l2norm: bool = True, y=None, state_out=None, inplace: bool = False):
+    """Gated delta rule of one new token per sequence (ssm_delta_step).
+
+    q, k [b, G, N], v [b, nh, H], dt, beta [b, nh]; the others as delta_fwd; state [n, nh, H, N] float32 (None:
+    zeros, n = b), slots [b] int32: each sequence's row of it (None: its own index, n = b; a row outside
+    0 .. n - 1 marks an unused place).  Returns (y, new state): with ``inplace`` the new state overwrites
+    ``state``, else only the named rows of state_out are written.
+    """
+    r = (_native or _load()).delta_step(q, k, v, dt, beta, A, dt_bias, state, slots, scale, softplus, sigmoid, l2norm, y,
+                                        state_out, inplace)
+    return _checked(r, "ssm_delta_step")
+
+
+def gatednorm_fwd(x, z, weight, *, group: int = 0, gate_first: bool = False, eps: float = 1e-5, y=None):
+    """Root-mean-square norm with a gate (ssm_gatednorm_fwd): rms(x) * weight * silu(z), or with gate_first
+    rms(x * silu(z)) * weight.
+
+    x, z [..., d] float32 or bfloat16 (rows may be strided), weight float32 [d], or [group] for all groups; the
+    mean square is taken over each ``group`` columns (0: the row), which divide d.  Returns y like x, dense.
+    """
+    r = (_native or _load()).gatednorm_fwd(x, z, weight, group, gate_first, eps, y)
+    return _checked(r, "ssm_gatednorm_fwd")
+
+
+def blocknorm_fwd(x, weight, residual, next_weight, z=None, *, alpha: float = 1.0, eps: float = 1e-5, y=None,
+                  residual_out=None):
+    """The norm after a block, the residual, and the norm before the next (ssm_blocknorm_fwd):
+    r = alpha * residual + rms(x) * weight [* silu(z)], y = rms(r) * next_weight.
+
+    x, z [..., d] float32 or bfloat16 (rows may be strided), weight, next_weight [d] float32, residual like x in
+    shape, float32 or x's dtype.  Returns (y, residual_out): y like x, residual_out = r of residual's dtype (it may be
+    given as ``residual`` itself, to update it in place).
+    """
+    r = (_native or _load()).blocknorm_fwd(x, weight, residual, next_weight, z, alpha, eps, y, residual_out)
+    return _checked(r, "ssm_blocknorm_fwd")

@@ -280,6 +280,23 @@ ssm_status check_selscan_sizes(const ssm_selscan_args& a) {
   return SSM_OK;
 }
 
+ssm_status check_delta_sizes(const ssm_delta_args& a) {
+  if (a.batch < 0 || a.nheads < 1 || a.headdim < 1 || a.ngroups < 1 || a.nheads % a.ngroups != 0 || !valid_dtype(a.dtype))
+    return SSM_ERR_INVALID_ARG;
+  if ((a.dstate != 32 && a.dstate != 64 && a.dstate != 128) || a.batch > 65535 || a.nheads > kMaxColumns / a.headdim ||
+      a.ngroups > kMaxColumns / a.dstate || delta_ctas(a) > 0x7fffffffLL)
+    return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+void delta_inputs(Spans& in, const ssm_delta_args& a, int64_t seqlen) {
+  const int e = dtype_bytes((ssm_dtype)a.dtype);
+  for (const ssm_tokens* t : {&a.q, &a.k}) in.tokens(*t, a.batch, seqlen, (int64_t)a.ngroups * a.dstate, e);
+  in.tokens(a.v, a.batch, seqlen, (int64_t)a.nheads * a.headdim, e);
+  for (const ssm_tokens* t : {&a.dt, &a.beta}) in.tokens(*t, a.batch, seqlen, a.nheads, e);
+  in.dense(a.A, 4, {a.nheads});
+  in.dense(a.dt_bias, 4, {a.nheads});
+}
+
 // One launch with its events; a failed launch is reported and cleared, and no exception leaves.
 template <typename F>
 ssm_status launch_status(int kernel, cudaStream_t s, F&& launch) {
@@ -830,6 +847,97 @@ ssm_status ssm_rmsnorm_fp8_fwd(const void* x, int64_t x_stride, const float* wei
   if (rows > 0 && (!q || !scale)) return SSM_ERR_INVALID_ARG;
   return rmsnorm(x, x_stride, weight, residual, residual_out, nullptr, q, scale, rows, width, group, eps, dtype,
                  res_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ssm_status ssm_delta_fwd(const ssm_delta_args* args, ssm_stream_t stream) {
+  if (!args) return SSM_ERR_INVALID_ARG;
+  const ssm_delta_args& a = *args;
+  ssm_status st = check_delta_sizes(a);
+  if (st != SSM_OK) return st;
+  if (a.seqlen < 0) return SSM_ERR_INVALID_ARG;
+  if (a.batch == 0 || (a.seqlen == 0 && !a.h_final)) return SSM_OK;
+  if (!a.A || (a.seqlen > 0 && (!a.q.ptr || !a.k.ptr || !a.v.ptr || !a.dt.ptr || !a.beta.ptr || !a.y)))
+    return SSM_ERR_INVALID_ARG;
+  Spans in, out;
+  delta_inputs(in, a, a.seqlen);
+  in.dense(a.h0, 4, {a.batch, a.nheads, a.headdim, a.dstate});
+  in.dense(a.lens, 4, {a.batch});
+  out.dense(a.seqlen > 0 ? a.y : nullptr, dtype_bytes((ssm_dtype)a.dtype), {a.batch, a.seqlen, a.nheads, a.headdim});
+  out.dense(a.h_final, 4, {a.batch, a.nheads, a.headdim, a.dstate});
+  if ((st = check_spans(in, out)) != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(15, s, [&] { return launch_delta(a, s); });
+}
+
+ssm_status ssm_delta_step(const ssm_delta_args* args, const int32_t* slots, int64_t nslots, ssm_stream_t stream) {
+  if (!args) return SSM_ERR_INVALID_ARG;
+  const ssm_delta_args& a = *args;
+  ssm_status st = check_delta_sizes(a);
+  if (st != SSM_OK) return st;
+  if (nslots < 0 || (!slots && nslots != a.batch)) return SSM_ERR_INVALID_ARG;
+  if (a.batch == 0) return SSM_OK;
+  if (!a.A || !a.q.ptr || !a.k.ptr || !a.v.ptr || !a.dt.ptr || !a.beta.ptr || !a.y || (nslots > 0 && !a.h_final))
+    return SSM_ERR_INVALID_ARG;
+  Spans in, out;
+  delta_inputs(in, a, 1);
+  if (a.h0 != a.h_final) in.dense(a.h0, 4, {nslots, a.nheads, a.headdim, a.dstate});
+  in.dense(slots, 4, {a.batch});
+  out.dense(a.y, dtype_bytes((ssm_dtype)a.dtype), {a.batch, a.nheads, a.headdim});
+  out.dense(a.h_final, 4, {nslots, a.nheads, a.headdim, a.dstate});
+  if ((st = check_spans(in, out)) != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(16, s, [&] { return launch_delta_step(a, slots, nslots, s); });
+}
+
+ssm_status ssm_gatednorm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const float* weight,
+                             int weight_width, void* y, int64_t rows, int width, int group, int gate_first, float eps,
+                             ssm_dtype dtype, ssm_stream_t stream) {
+  if (rows < 0 || width < 1 || group < 0 || !valid_dtype(dtype)) return SSM_ERR_INVALID_ARG;
+  if (group == 0) group = width;
+  if (width % group != 0 || (weight_width != width && weight_width != group)) return SSM_ERR_INVALID_ARG;
+  if (rows == 0) return SSM_OK;
+  if (!x || !z || !weight || !y) return SSM_ERR_INVALID_ARG;
+  if (width > kMaxColumns || rows > 0x7fffffffLL / (width / group)) return SSM_ERR_UNSUPPORTED;
+  const int e = dtype_bytes(dtype);
+  Spans in, out;
+  in.tokens(ssm_tokens{x, x_stride, 0}, rows, 1, width, e);
+  in.tokens(ssm_tokens{z, z_stride, 0}, rows, 1, width, e);
+  in.dense(weight, 4, {weight_width});
+  out.dense(y, e, {rows, width});
+  const ssm_status st = check_spans(in, out);
+  if (st != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(17, s, [&] {
+    return launch_gatednorm(x, x_stride, z, z_stride, weight, weight_width, y, rows, width, group, gate_first != 0, eps,
+                            dtype, s);
+  });
+}
+
+ssm_status ssm_blocknorm_fwd(const void* x, int64_t x_stride, const float* weight, const void* z, int64_t z_stride,
+                             const void* residual, void* residual_out, const float* next_weight, void* y, int64_t rows,
+                             int width, float alpha, float eps, ssm_dtype dtype, ssm_dtype res_dtype,
+                             ssm_stream_t stream) {
+  if (rows < 0 || width < 1 || !valid_dtype(dtype) || (res_dtype != SSM_F32 && res_dtype != dtype))
+    return SSM_ERR_INVALID_ARG;
+  if (rows == 0) return SSM_OK;
+  if (!x || !weight || !residual || !next_weight || !y) return SSM_ERR_INVALID_ARG;
+  if (rows > 0x7fffffffLL || width > kMaxColumns) return SSM_ERR_UNSUPPORTED;
+  const int e = dtype_bytes(dtype), re = dtype_bytes(res_dtype);
+  Spans in, out;
+  in.tokens(ssm_tokens{x, x_stride, 0}, rows, 1, width, e);
+  in.tokens(ssm_tokens{z, z_stride, 0}, rows, 1, width, e);
+  in.dense(weight, 4, {width});
+  in.dense(next_weight, 4, {width});
+  if (residual != residual_out) in.dense(residual, re, {rows, width});
+  out.dense(y, e, {rows, width});
+  out.dense(residual_out, re, {rows, width});
+  const ssm_status st = check_spans(in, out);
+  if (st != SSM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(18, s, [&] {
+    return launch_blocknorm(x, x_stride, weight, z, z_stride, residual, residual_out, next_weight, y, rows, width, alpha,
+                            eps, dtype, res_dtype, s);
+  });
 }
 
 size_t ssm_linscan_workspace_bytes(int64_t rows, int64_t len) {

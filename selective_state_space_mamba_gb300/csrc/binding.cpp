@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "../../include/ssm.h"
@@ -27,6 +28,10 @@ struct {
   decltype(&ssm_selscan_step) selscan_step;
   decltype(&ssm_rmsnorm_fwd) rmsnorm_fwd;
   decltype(&ssm_rmsnorm_fp8_fwd) rmsnorm_fp8_fwd;
+  decltype(&ssm_delta_fwd) delta_fwd;
+  decltype(&ssm_delta_step) delta_step;
+  decltype(&ssm_gatednorm_fwd) gatednorm_fwd;
+  decltype(&ssm_blocknorm_fwd) blocknorm_fwd;
 } g_fn;
 
 struct Refusal {
@@ -159,8 +164,8 @@ PyObject* result(ssm_status st, Out& a, Out& b) {
 
 // A step's new states: in place, the caller's, or new ones (a copy where slots name some of the rows
 // only: the others keep what they hold).  Returns the number of rows.
-int64_t step_states(Out& out, PyObject* state, PyObject* state_out, bool inplace, bool slots, int64_t batch, int64_t d1,
-                    int64_t d2, c10::ScalarType type, const Like& like) {
+int64_t step_states(Out& out, PyObject* state, PyObject* state_out, bool inplace, bool slots, int64_t batch, Sizes inner,
+                    c10::ScalarType type, const Like& like) {
   if (inplace && (state == Py_None || state_out != Py_None))
     throw Refusal{PyExc_ValueError, "inplace needs a state and no state_out"};
   PyObject* target = inplace ? state : state_out;
@@ -170,7 +175,7 @@ int64_t step_states(Out& out, PyObject* state, PyObject* state_out, bool inplace
   PyObject* rows = target != Py_None ? target : state;
   if (rows != Py_None) {
     const at::Tensor& t = tensor("state", rows);
-    if (t.dim() != 3) fail("state", "of three dimensions");
+    if (t.dim() != 1 + (int64_t)inner.size()) fail("state", inner.size() == 2 ? "of three dimensions" : "of four dimensions");
     n = t.size(0);
   }
   if (target == Py_None && state != Py_None && slots) {
@@ -178,7 +183,9 @@ int64_t step_states(Out& out, PyObject* state, PyObject* state_out, bool inplace
     out.ptr = t.data_ptr();
     out.object = THPVariable_Wrap(std::move(t));
   } else {
-    out.set("state_out", target, {n, d1, d2}, type, like);
+    c10::SmallVector<int64_t, 4> sizes(1, n);
+    sizes.append(inner.begin(), inner.end());
+    out.set("state_out", target, sizes, type, like);
   }
   return n;
 }
@@ -215,7 +222,7 @@ PyObject* conv_step(PyObject* const* v) {  // x, weight, bias, state, slots, sil
   const float* bias = floats("bias", v[2], {d}, like);
   const int32_t* slots = ints("slots", v[4], b, like);
   Out y, so;
-  const int64_t n = step_states(so, v[3], v[7], truth(v[8]), slots, b, W - 1, d, like.type, like);
+  const int64_t n = step_states(so, v[3], v[7], truth(v[8]), slots, b, {W - 1, d}, like.type, like);
   const void* state = optional("state", v[3], {n, W - 1, d}, like.type, like);
   y.set("y", v[6], {b, d}, like.type, like);
   const ssm_status st = g_fn.conv_step(xt, wp, bias, state, slots, y.ptr, so.ptr, b, n, d, W,
@@ -298,7 +305,7 @@ PyObject* selscan_step(PyObject* const* v) {
   const int32_t* slots = ints("slots", v[9], a.batch, like);
   Out y, so;
   const int64_t n =
-      step_states(so, v[8], v[12], truth(v[13]), slots, a.batch, a.channels, a.dstate, at::kFloat, like);
+      step_states(so, v[8], v[12], truth(v[13]), slots, a.batch, {a.channels, a.dstate}, at::kFloat, like);
   a.h0 = floats("state", v[8], {n, a.channels, a.dstate}, like);
   a.h_final = static_cast<float*>(so.ptr);
   y.set("y", v[11], u.sizes(), like.type, like);
@@ -385,6 +392,132 @@ PyObject* rmsnorm_fp8_fwd(PyObject* const* v) {  // x, weight, residual, eps, gr
   return t;
 }
 
+// q, k, v, dt, beta, A, dt_bias, and scale, softplus, sigmoid, l2norm from v[9] on: what delta_fwd and delta_step share.
+// `lead`: dimensions before the heads.
+ssm_delta_args delta_args(PyObject* const* v, const Like& like, const at::Tensor& q, int lead) {
+  ssm_delta_args a{};
+  const at::Tensor &k = tensor("k", v[1]), &x = tensor("v", v[2]);
+  const Sizes first = q.sizes().slice(0, lead);
+  if (x.dim() != lead + 2 || x.sizes().slice(0, lead) != first) fail("v", text_of(first) + " and heads, their size");
+  const int G = narrow(q.size(lead)), N = narrow(q.size(lead + 1));
+  const int nh = narrow(x.size(lead)), H = narrow(x.size(lead + 1));
+  a.q = tokens("q", q, q.sizes(), like);
+  a.k = tokens("k", k, q.sizes(), like);
+  a.v = tokens("v", x, x.sizes(), like);
+  if (G > 1 && (q.stride(lead) != N || k.stride(lead) != N)) fail("q, k", "contiguous in their last two dimensions");
+  if (nh > 1 && x.stride(lead) != H) fail("v", "contiguous in its last two dimensions");
+  c10::SmallVector<int64_t, 4> gates(first.begin(), first.end());
+  gates.push_back(nh);
+  a.dt = tokens("dt", tensor("dt", v[3]), gates, like);
+  a.beta = tokens("beta", tensor("beta", v[4]), gates, like);
+  a.A = static_cast<const float*>(dense("A", tensor("A", v[5]), {nh}, at::kFloat, like));
+  a.dt_bias = floats("dt_bias", v[6], {nh}, like);
+  a.batch = first[0];
+  a.nheads = nh;
+  a.headdim = H;
+  a.dstate = N;
+  a.ngroups = G;
+  a.scale = N > 0 ? 1.f / std::sqrt((float)N) : 1.f;
+  if (v[9] != Py_None) {
+    const double scale = PyFloat_AsDouble(v[9]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+    a.scale = (float)scale;
+  }
+  a.softplus = truth(v[10]);
+  a.sigmoid = truth(v[11]);
+  a.l2norm = truth(v[12]);
+  a.dtype = like.code;
+  return a;
+}
+
+// q, k, v, dt, beta, A, dt_bias, h0, lens, scale, softplus, sigmoid, l2norm, y, h_final, return_final_state
+PyObject* delta_fwd(PyObject* const* v) {
+  const at::Tensor& q = tensor("q", v[0]);
+  const Like like("q", q);
+  if (q.dim() != 4) fail("q", "[b, L, G, N]");
+  ssm_delta_args a = delta_args(v, like, q, 2);
+  const auto guard = like.guard();
+  a.seqlen = q.size(1);
+  const int64_t state[] = {a.batch, a.nheads, a.headdim, a.dstate};
+  a.h0 = floats("h0", v[7], state, like);
+  a.lens = ints("lens", v[8], a.batch, like);
+  Out y, h;
+  y.set("y", v[13], {a.batch, a.seqlen, a.nheads, a.headdim}, like.type, like);
+  a.y = y.ptr;
+  if (truth(v[15])) h.set("h_final", v[14], state, at::kFloat, like);
+  a.h_final = static_cast<float*>(h.ptr);
+  return result(g_fn.delta_fwd(&a, like.stream()), y, h);
+}
+
+// q, k, v, dt, beta, A, dt_bias, state, slots, scale, softplus, sigmoid, l2norm, y, state_out, inplace
+PyObject* delta_step(PyObject* const* v) {
+  const at::Tensor& q = tensor("q", v[0]);
+  const Like like("q", q);
+  if (q.dim() != 3) fail("q", "[b, G, N]");
+  ssm_delta_args a = delta_args(v, like, q, 1);
+  const auto guard = like.guard();
+  a.seqlen = 1;
+  const int32_t* slots = ints("slots", v[8], a.batch, like);
+  Out y, so;
+  const int64_t n =
+      step_states(so, v[7], v[14], truth(v[15]), slots, a.batch, {a.nheads, a.headdim, a.dstate}, at::kFloat, like);
+  a.h0 = floats("state", v[7], {n, a.nheads, a.headdim, a.dstate}, like);
+  a.h_final = static_cast<float*>(so.ptr);
+  y.set("y", v[13], {a.batch, a.nheads, a.headdim}, like.type, like);
+  a.y = y.ptr;
+  return result(g_fn.delta_step(&a, slots, n, like.stream()), y, so);
+}
+
+// Rows of a tensor [..., d]: its pointer, and the elements from row to row.
+int64_t row_stride(const char* name, const at::Tensor& t, int64_t rows, int d) {
+  if (t.is_contiguous()) return d;
+  if (t.stride(-1) != 1 && d != 1) fail(name, "contiguous in its last dimension");
+  return (t.dim() == 2 ? t : t.view({rows, d})).stride(0);
+}
+
+PyObject* gatednorm_fwd(PyObject* const* v) {  // x, z, weight, group, gate_first, eps, y
+  const at::Tensor &x = tensor("x", v[0]), &z = tensor("z", v[1]), &w = tensor("weight", v[2]);
+  const Like like("x", x);
+  const long of = PyLong_AsLong(v[3]);
+  const double eps = of == -1 && PyErr_Occurred() ? 0.0 : PyFloat_AsDouble(v[5]);
+  if (PyErr_Occurred()) return nullptr;
+  const int d = x.dim() ? narrow(x.size(-1)) : 0, group = narrow(of);
+  const auto guard = like.guard();
+  held("z", z, x.sizes(), like.type, like, "a CUDA tensor ");
+  const int64_t rows = d ? x.numel() / d : 0;
+  const int ww = w.dim() == 1 ? narrow(w.size(0)) : -1;
+  if (ww != d && ww != group) fail("weight", "[" + std::to_string(d) + "], or of one group");
+  const float* wp = static_cast<const float*>(dense("weight", w, {ww}, at::kFloat, like));
+  Out y;
+  y.set("y", v[6], x.sizes(), like.type, like);
+  const ssm_status st =
+      g_fn.gatednorm_fwd(x.data_ptr(), row_stride("x", x, rows, d), z.data_ptr(), row_stride("z", z, rows, d), wp, ww, y.ptr,
+                         rows, d, group, truth(v[4]), (float)eps, like.code, like.stream());
+  return st != SSM_OK ? PyLong_FromLong(st) : y.give();
+}
+
+PyObject* blocknorm_fwd(PyObject* const* v) {  // x, weight, residual, next_weight, z, alpha, eps, y, residual_out
+  if (v[2] == Py_None) fail("residual", "a tensor");
+  const double alpha = PyFloat_AsDouble(v[5]);
+  const double eps = alpha == -1.0 && PyErr_Occurred() ? 0.0 : PyFloat_AsDouble(v[6]);
+  if (PyErr_Occurred()) return nullptr;
+  Norm n(v[0], v[1], v[2], v[8]);
+  const float* next = static_cast<const float*>(dense("next_weight", tensor("next_weight", v[3]), {n.d}, at::kFloat, n.like));
+  const void* z = nullptr;
+  int64_t z_stride = 0;
+  if (v[4] != Py_None) {
+    const at::Tensor& t = tensor("z", v[4]);
+    held("z", t, n.x.sizes(), n.like.type, n.like, "a CUDA tensor ");
+    z = t.data_ptr();
+    z_stride = row_stride("z", t, n.rows, n.d);
+  }
+  Out y;
+  y.set("y", v[7], n.x.sizes(), n.like.type, n.like);
+  return result(g_fn.blocknorm_fwd(n.x.data_ptr(), n.stride, n.w, z, z_stride, n.residual, n.residual_out.ptr, next, y.ptr,
+                                   n.rows, n.d, (float)alpha, (float)eps, n.like.code, n.res_code, n.like.stream()),
+                y, n.residual_out);
+}
+
 // No C++ exception leaves a Python entry point.
 template <PyObject* (*F)(PyObject* const*), int ARGS>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -411,14 +544,15 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-// bind(addresses of the seven C entry points, in the order of g_fn)
+// bind(addresses of the C entry points, in the order of g_fn)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* p[7];
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "seven addresses");
+  constexpr int kFns = 11;
+  void* p[kFns];
+  if (n != kFns) {
+    PyErr_SetString(PyExc_TypeError, "eleven addresses");
     return nullptr;
   }
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < kFns; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -428,7 +562,11 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
           reinterpret_cast<decltype(g_fn.selscan_fwd)>(p[3]),
           reinterpret_cast<decltype(g_fn.selscan_step)>(p[4]),
           reinterpret_cast<decltype(g_fn.rmsnorm_fwd)>(p[5]),
-          reinterpret_cast<decltype(g_fn.rmsnorm_fp8_fwd)>(p[6])};
+          reinterpret_cast<decltype(g_fn.rmsnorm_fp8_fwd)>(p[6]),
+          reinterpret_cast<decltype(g_fn.delta_fwd)>(p[7]),
+          reinterpret_cast<decltype(g_fn.delta_step)>(p[8]),
+          reinterpret_cast<decltype(g_fn.gatednorm_fwd)>(p[9]),
+          reinterpret_cast<decltype(g_fn.blocknorm_fwd)>(p[10])};
   Py_RETURN_NONE;
 }
 
@@ -442,6 +580,10 @@ PyMethodDef g_methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                            {"rmsnorm_fwd", fast(entry<rmsnorm_fwd, 6>), METH_FASTCALL, nullptr},
                            {"kept_workspace", fast(entry<kept_workspace, 1>), METH_FASTCALL, nullptr},
                            {"rmsnorm_fp8_fwd", fast(entry<rmsnorm_fp8_fwd, 8>), METH_FASTCALL, nullptr},
+                           {"delta_fwd", fast(entry<delta_fwd, 16>), METH_FASTCALL, nullptr},
+                           {"delta_step", fast(entry<delta_step, 16>), METH_FASTCALL, nullptr},
+                           {"gatednorm_fwd", fast(entry<gatednorm_fwd, 7>), METH_FASTCALL, nullptr},
+                           {"blocknorm_fwd", fast(entry<blocknorm_fwd, 9>), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,359 @@
+// The norms before and after a block, fused with its gate and its residual:
+//   gatednorm   y = rms(x) w silu(z)   or   rms(x silu(z)) w,   over groups of a row's columns
+//   blocknorm   r = alpha residual + rms(x) w [silu(z)],   y = rms(r) w2
+// with rms(v) = v / sqrt(mean(v^2) + eps).  Each element is read once and written once: memory-bound (a few rows:
+// launch-bound).
+//
+// A thread owns vectors of eight columns: consecutive ones where rows are aligned, else every 32nd of the
+// warp's 256, so that its lanes still access neighbouring elements.  A team of threads has a group (gatednorm) or a row,
+// and what its threads hold stays in registers between the sums of squares and the output; what they do not
+// hold of wider rows is read again.
+#include "layer_common.cuh"
+
+namespace ssm {
+namespace {
+
+using namespace layer;
+
+constexpr int kMaxThreads = 1024;
+constexpr int kHoldThreads = 512;
+constexpr int64_t kManyRows = 152 * 4;  // four CTAs an SM
+
+// Eight elements of a row as they lie in memory: columns c, c + 1, ... (kVec) or c, c + 32, ...
+template <typename T, bool kVec> struct Eight {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* row, int c, int) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(row + c)[i];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      to_floats<T, 8>(v[0], f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = reinterpret_cast<const float*>(v)[i];
+    }
+  }
+};
+template <typename T> struct Eight<T, false> {
+  T v[8];
+  __device__ __forceinline__ void load(const T* row, int c, int width) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + 32 * j < width ? row[c + 32 * j] : from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = to_f32(v[j]);
+  }
+};
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_columns(const T* row, int c, int width, float (&f)[8]) {
+  Eight<T, kVec> e;
+  e.load(row, c, width);
+  e.get(f);
+}
+template <bool kVec, typename T>
+__device__ __forceinline__ void store_columns(T* row, int c, int width, const float (&v)[8]) {
+  if constexpr (kVec) {
+    store8<T>(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + 32 * j < width) row[c + 32 * j] = from_f32<T>(v[j]);
+  }
+}
+
+// Vectors of `width` columns, and the first column of vector i
+template <bool kVec>
+__host__ __device__ __forceinline__ int vectors(int width) {
+  return kVec ? width / 8 : (width + 255) / 256 * 32;
+}
+template <bool kVec>
+__device__ __forceinline__ int first_column(int i) {
+  return kVec ? 8 * i : (i >> 5) * 256 + (i & 31);
+}
+
+// Sum over the CTA, the same in every thread; `part` is the call's own.
+__device__ __forceinline__ float cta_sum(float v, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return v;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < warps ? part[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// the squares of a vector, in two sums
+__device__ __forceinline__ void add_squares(const float (&v)[8], float (&sum)[2]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float e[2] = {v[j], v[j + 1]};
+    fma_n(e, e, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------------- gatednorm
+
+struct GatedParams {
+  const void *x, *z;
+  int64_t x_stride, z_stride;
+  const float* weight;
+  int weight_width;  // of the weight: the row's or a group's
+  void* y;
+  int64_t rows;
+  int width, group, groups;
+  float eps;
+};
+
+// x and z of a vector, and the value whose squares are summed
+template <typename T, bool kVec, bool kFirst>
+struct GatedVector {
+  Eight<T, kVec> x, z;
+  __device__ __forceinline__ void load(const T* xr, const T* zr, int c, int width) {
+    x.load(xr, c, width);
+    z.load(zr, c, width);
+  }
+  __device__ __forceinline__ void value(float (&v)[8]) const {
+    x.get(v);
+    if constexpr (kFirst) {
+      float g[8];
+      z.get(g);
+      silu_n(g, g);
+      mul_n(v, g, v);
+    }
+  }
+  __device__ __forceinline__ void output(const float* weight, T* yr, int c, int width, float rstd) const {
+    float v[8], w[8];
+    value(v);
+    load_columns<kVec>(weight, c, width, w);
+    mul_n(v, rstd, v);
+    mul_n(v, w, v);
+    if constexpr (!kFirst) {
+      float g[8];
+      z.get(g);
+      silu_n(g, g);
+      mul_n(v, g, v);
+    }
+    store_columns<kVec>(yr, c, width, v);
+  }
+};
+
+// A CTA a group of a row.
+template <typename T, bool kVec, bool kFirst, int HOLD>
+__global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
+    gatednorm_kernel(const __grid_constant__ GatedParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float part[32];
+  const int64_t row = blockIdx.x / p.groups;
+  const int g0 = (int)(blockIdx.x % p.groups) * p.group;
+  const T* xr = static_cast<const T*>(p.x) + row * p.x_stride + g0;
+  const T* zr = static_cast<const T*>(p.z) + row * p.z_stride + g0;
+  T* yr = static_cast<T*>(p.y) + row * p.width + g0;
+  const float* w = p.weight + (p.weight_width == p.width ? g0 : 0);
+  const int nvec = vectors<kVec>(p.group), tid = threadIdx.x, threads = blockDim.x;
+  GatedVector<T, kVec, kFirst> held[HOLD];
+  float sum[2] = {}, v[8];
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (tid + k * threads < nvec) held[k].load(xr, zr, first_column<kVec>(tid + k * threads), p.group);
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (tid + k * threads < nvec) {
+      held[k].value(v);
+      add_squares(v, sum);
+    }
+  for (int i = tid + HOLD * threads; i < nvec; i += threads) {
+    GatedVector<T, kVec, kFirst> e;
+    e.load(xr, zr, first_column<kVec>(i), p.group);
+    e.value(v);
+    add_squares(v, sum);
+  }
+  const float rstd = rsqrtf(cta_sum(sum[0] + sum[1], part) / (float)p.group + p.eps);
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (tid + k * threads < nvec) held[k].output(w, yr, first_column<kVec>(tid + k * threads), p.group, rstd);
+  for (int i = tid + HOLD * threads; i < nvec; i += threads) {
+    GatedVector<T, kVec, kFirst> e;
+    e.load(xr, zr, first_column<kVec>(i), p.group);
+    e.output(w, yr, first_column<kVec>(i), p.group, rstd);
+  }
+}
+
+template <typename T, bool kVec, bool kFirst>
+cudaError_t launch_gated_rows(const GatedParams& p, cudaStream_t s) {
+  const int nvec = vectors<kVec>(p.group);
+  const auto go = [&](auto kernel, int hold) {
+    const int threads = ((nvec + hold - 1) / hold + 31) / 32 * 32;
+    return launch_pdl(kernel, dim3((unsigned)(p.rows * p.groups)),
+                      dim3((unsigned)(threads < kMaxThreads ? threads : kMaxThreads)), 0, s, p);
+  };
+  if (p.rows * p.groups < kManyRows || nvec > 4 * kHoldThreads) return go(gatednorm_kernel<T, kVec, kFirst, 1>, 1);
+  return go(gatednorm_kernel<T, kVec, kFirst, 4>, 4);
+}
+
+template <typename T>
+cudaError_t launch_gated_type(const GatedParams& p, bool vec, bool first, cudaStream_t s) {
+  if (vec) return first ? launch_gated_rows<T, true, true>(p, s) : launch_gated_rows<T, true, false>(p, s);
+  return first ? launch_gated_rows<T, false, true>(p, s) : launch_gated_rows<T, false, false>(p, s);
+}
+
+// ---------------------------------------------------------------------------------- blocknorm
+
+struct BlockParams {
+  const void *x, *z;  // z NULL: no gate
+  int64_t x_stride, z_stride;
+  const float *weight, *next_weight;
+  const void* residual;
+  void *residual_out, *y;
+  int64_t rows;
+  int width;
+  float alpha, eps;
+};
+
+// A CTA a row.  HOLD vectors of x, the gate and the residual a thread; r replaces them after the first sum.
+template <typename T, typename R, bool kGate, bool kVec, int HOLD>
+__global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
+    blocknorm_kernel(const __grid_constant__ BlockParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float part[2][32];
+  const int64_t row = blockIdx.x;
+  const T* xr = static_cast<const T*>(p.x) + row * p.x_stride;
+  const T* zr = static_cast<const T*>(p.z) + row * p.z_stride;
+  const R* rr = static_cast<const R*>(p.residual) + row * p.width;
+  R* ro = p.residual_out ? static_cast<R*>(p.residual_out) + row * p.width : nullptr;
+  T* yr = static_cast<T*>(p.y) + row * p.width;
+  const int nvec = vectors<kVec>(p.width), tid = threadIdx.x, threads = blockDim.x;
+  const auto joined = [&](const Eight<T, kVec>& x, const Eight<T, kVec>& z, const Eight<R, kVec>& res, int c, float rstd,
+                          float (&r)[8]) {
+    float w[8], e[8];
+    x.get(r);
+    mul_n(r, rstd, r);
+    load_columns<kVec>(p.weight, c, p.width, w);
+    mul_n(r, w, r);
+    if constexpr (kGate) {
+      z.get(e);
+      silu_n(e, e);
+      mul_n(r, e, r);
+    }
+    res.get(e);
+    fma_n(e, p.alpha, r, r);
+  };
+  Eight<T, kVec> x[HOLD], z[kGate ? HOLD : 1];
+  Eight<R, kVec> res[HOLD];
+  float sum[2] = {}, v[8];
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int i = tid + k * threads, c = first_column<kVec>(i);
+    if (i < nvec) {
+      x[k].load(xr, c, p.width);
+      res[k].load(rr, c, p.width);
+      if constexpr (kGate) z[k].load(zr, c, p.width);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (tid + k * threads < nvec) {
+      x[k].get(v);
+      add_squares(v, sum);
+    }
+  for (int i = tid + HOLD * threads; i < nvec; i += threads) {
+    load_columns<kVec>(xr, first_column<kVec>(i), p.width, v);
+    add_squares(v, sum);
+  }
+  const float rstd = rsqrtf(cta_sum(sum[0] + sum[1], part[0]) / (float)p.width + p.eps);
+  // r of the vectors that a thread does not hold is computed twice: with residual_out in place of residual, it is written
+  // with the second time
+  const auto again = [&](int c, float (&r)[8]) {
+    Eight<T, kVec> xe, ze;
+    Eight<R, kVec> re;
+    xe.load(xr, c, p.width);
+    re.load(rr, c, p.width);
+    if constexpr (kGate) ze.load(zr, c, p.width);
+    joined(xe, ze, re, c, rstd, r);
+  };
+  float held[HOLD][8];
+  sum[0] = sum[1] = 0.f;
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int i = tid + k * threads, c = first_column<kVec>(i);
+    if (i < nvec) {
+      joined(x[k], z[kGate ? k : 0], res[k], c, rstd, held[k]);
+      add_squares(held[k], sum);
+      if (ro) store_columns<kVec>(ro, c, p.width, held[k]);
+    }
+  }
+  for (int i = tid + HOLD * threads; i < nvec; i += threads) {
+    again(first_column<kVec>(i), v);
+    add_squares(v, sum);
+  }
+  const float next = rsqrtf(cta_sum(sum[0] + sum[1], part[1]) / (float)p.width + p.eps);
+  const auto output = [&](int c, const float (&r)[8]) {
+    float w[8], o[8];
+    load_columns<kVec>(p.next_weight, c, p.width, w);
+    mul_n(r, next, o);
+    mul_n(o, w, o);
+    store_columns<kVec>(yr, c, p.width, o);
+  };
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    if (tid + k * threads < nvec) output(first_column<kVec>(tid + k * threads), held[k]);
+  for (int i = tid + HOLD * threads; i < nvec; i += threads) {
+    const int c = first_column<kVec>(i);
+    again(c, v);
+    if (ro) store_columns<kVec>(ro, c, p.width, v);
+    output(c, v);
+  }
+}
+
+template <typename T, typename R, bool kGate, bool kVec>
+cudaError_t launch_block_rows(const BlockParams& p, cudaStream_t s) {
+  const int nvec = vectors<kVec>(p.width);
+  const auto go = [&](auto kernel, int hold) {
+    const int threads = ((nvec + hold - 1) / hold + 31) / 32 * 32;
+    return launch_pdl(kernel, dim3((unsigned)p.rows), dim3((unsigned)(threads < kMaxThreads ? threads : kMaxThreads)), 0, s,
+                      p);
+  };
+  if (p.rows < kManyRows || nvec > 3 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 1>, 1);
+  return go(blocknorm_kernel<T, R, kGate, kVec, 3>, 3);
+}
+
+template <typename T, typename R>
+cudaError_t launch_block_type(const BlockParams& p, bool vec, cudaStream_t s) {
+  if (vec) return p.z ? launch_block_rows<T, R, true, true>(p, s) : launch_block_rows<T, R, false, true>(p, s);
+  return p.z ? launch_block_rows<T, R, true, false>(p, s) : launch_block_rows<T, R, false, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gatednorm(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const float* weight,
+                             int weight_width, void* y, int64_t rows, int width, int group, bool gate_first, float eps,
+                             ssm_dtype dtype, cudaStream_t s) {
+  const int e = dtype == SSM_F32 ? 4 : 2;
+  const GatedParams p{x, z, x_stride, z_stride, weight, weight_width, y, rows, width, group, width / group, eps};
+  const bool vec = group % 8 == 0 && aligned_rows(x, x_stride, 0, e, 16) && aligned_rows(z, z_stride, 0, e, 16) &&
+                   aligned_rows(weight, 0, 0, 4, 16) && aligned_rows(y, width, 0, e, 16);
+  return dtype == SSM_F32 ? launch_gated_type<float>(p, vec, gate_first, s)
+                          : launch_gated_type<__nv_bfloat16>(p, vec, gate_first, s);
+}
+
+cudaError_t launch_blocknorm(const void* x, int64_t x_stride, const float* weight, const void* z, int64_t z_stride,
+                             const void* residual, void* residual_out, const float* next_weight, void* y, int64_t rows,
+                             int width, float alpha, float eps, ssm_dtype dtype, ssm_dtype res_dtype, cudaStream_t s) {
+  const int e = dtype == SSM_F32 ? 4 : 2, re = res_dtype == SSM_F32 ? 4 : 2;
+  const BlockParams p{x, z, x_stride, z_stride, weight, next_weight, residual, residual_out, y, rows, width, alpha, eps};
+  const bool vec = width % 8 == 0 && aligned_rows(x, x_stride, 0, e, 16) && (!z || aligned_rows(z, z_stride, 0, e, 16)) &&
+                   aligned_rows(weight, 0, 0, 4, 16) && aligned_rows(next_weight, 0, 0, 4, 16) &&
+                   aligned_rows(residual, width, 0, re, 16) && aligned_rows(residual_out, width, 0, re, 16) &&
+                   aligned_rows(y, width, 0, e, 16);
+  if (dtype == SSM_F32) return launch_block_type<float, float>(p, vec, s);
+  return res_dtype == SSM_F32 ? launch_block_type<__nv_bfloat16, float>(p, vec, s)
+                              : launch_block_type<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
+}
+
+}  // namespace ssm
