@@ -17,6 +17,7 @@ using namespace layer;
 
 constexpr int kMaxThreads = 1024;
 constexpr int kHoldThreads = 512;
+constexpr int kTeamThreads = 128;
 constexpr int64_t kManyRows = 152 * 4;  // four CTAs an SM
 
 // Eight elements of a row as they lie in memory: columns c, c + 1, ... (kVec) or c, c + 32, ...
@@ -184,6 +185,55 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
   }
 }
 
+// A team of TEAM lanes a group, each lane with HOLD vectors of it, of UNITS groups: all loads first.  Neighbouring teams have
+// neighbouring groups.
+template <typename T, bool kVec, bool kFirst, int TEAM, int UNITS, int HOLD>
+__global__ void __launch_bounds__(kTeamThreads) gatednorm_team_kernel(const __grid_constant__ GatedParams p) {
+  constexpr int TEAMS = kTeamThreads / TEAM;
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t units = (uint32_t)(p.rows * p.groups), first = blockIdx.x * (uint32_t)(TEAMS * UNITS) + threadIdx.x / TEAM;
+  const int lane = threadIdx.x % TEAM, nvec = vectors<kVec>(p.group);
+  GatedVector<T, kVec, kFirst> held[UNITS][HOLD];
+#pragma unroll
+  for (int k = 0; k < UNITS; ++k) {
+    const uint32_t u = first + k * TEAMS;
+    if (u < units) {
+      const int64_t row = u / (uint32_t)p.groups, g0 = (int64_t)(u % (uint32_t)p.groups) * p.group;
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i)
+        if (lane + TEAM * i < nvec)
+          held[k][i].load(static_cast<const T*>(p.x) + row * p.x_stride + g0,
+                          static_cast<const T*>(p.z) + row * p.z_stride + g0, first_column<kVec>(lane + TEAM * i), p.group);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < UNITS; ++k) {
+    const uint32_t u = first + k * TEAMS;
+    float sum[2] = {}, v[8];
+    if (u < units) {
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i)
+        if (lane + TEAM * i < nvec) {
+          held[k][i].value(v);
+          add_squares(v, sum);
+        }
+    }
+    float all = sum[0] + sum[1];
+#pragma unroll
+    for (int o = TEAM / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (u < units) {
+      const float rstd = rsqrtf(all / (float)p.group + p.eps);
+      const int64_t row = u / (uint32_t)p.groups, g0 = (int64_t)(u % (uint32_t)p.groups) * p.group;
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i)
+        if (lane + TEAM * i < nvec)
+          held[k][i].output(p.weight + (p.weight_width == p.width ? g0 : 0), static_cast<T*>(p.y) + row * p.width + g0,
+                            first_column<kVec>(lane + TEAM * i), p.group, rstd);
+    }
+  }
+}
+
 template <typename T, bool kVec, bool kFirst>
 cudaError_t launch_gated_rows(const GatedParams& p, cudaStream_t s) {
   const int nvec = vectors<kVec>(p.group);
@@ -192,6 +242,21 @@ cudaError_t launch_gated_rows(const GatedParams& p, cudaStream_t s) {
     return launch_pdl(kernel, dim3((unsigned)(p.rows * p.groups)),
                       dim3((unsigned)(threads < kMaxThreads ? threads : kMaxThreads)), 0, s, p);
   };
+  const auto teams = [&](auto kernel, int units) {
+    return launch_pdl(kernel, dim3((unsigned)((p.rows * p.groups + units - 1) / units)), dim3(kTeamThreads), 0, s, p);
+  };
+  if constexpr (kVec) {
+    if (nvec <= 16) {
+      const bool many = p.rows * p.groups >= 16 * kManyRows;
+      if (nvec <= 8)
+        return many ? teams(gatednorm_team_kernel<T, kVec, kFirst, 8, 4, 1>, 64)
+                    : teams(gatednorm_team_kernel<T, kVec, kFirst, 8, 1, 1>, 16);
+      return many ? teams(gatednorm_team_kernel<T, kVec, kFirst, 16, 4, 1>, 32)
+                  : teams(gatednorm_team_kernel<T, kVec, kFirst, 16, 1, 1>, 8);
+    }
+  }
+  if (nvec <= 32) return teams(gatednorm_team_kernel<T, kVec, kFirst, 32, 2, 1>, 8);
+  if (p.rows * p.groups >= kManyRows && nvec <= 128) return teams(gatednorm_team_kernel<T, kVec, kFirst, 32, 1, 4>, 4);
   if (p.rows * p.groups < kManyRows || nvec > 4 * kHoldThreads) return go(gatednorm_kernel<T, kVec, kFirst, 1>, 1);
   return go(gatednorm_kernel<T, kVec, kFirst, 4>, 4);
 }
