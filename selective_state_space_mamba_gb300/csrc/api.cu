@@ -866,6 +866,8 @@ ssm_status ssm_delta_fwd(const ssm_delta_args* args, ssm_stream_t stream) {
   out.dense(a.h_final, 4, {a.batch, a.nheads, a.headdim, a.dstate});
   if ((st = check_spans(in, out)) != SSM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.seqlen >= 16 && delta_tc_supported(a))
+    return launch_status(19, s, [&] { return launch_delta_tc(a, next_lookback_ctl(), s); });
   return launch_status(15, s, [&] { return launch_delta(a, s); });
 }
 

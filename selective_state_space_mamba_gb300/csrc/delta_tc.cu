@@ -1,0 +1,723 @@
+// delta_tc: the gated delta rule over bf16 prompts in chunks of 64 tokens on the tensor cores (tcgen05, TMEM, TMA).
+//
+// With G_i the sum of the chunk's log-decays up to token i, the tokens' corrections d_i = beta_i (v_i - a_i S_{i-1} k_i) of
+// a chunk that enters with state S solve a triangular system (i > j: N_ij = beta_i e^(G_i - G_j) k_i.k_j):
+//     (I + N) d = diag(beta) (V - diag(e^G) K S^T),      T = (I + N)^-1 diag(beta)
+//     y_i = scale (e^(G_i) S q_i + sum_{j <= i} e^(G_i - G_j) (q_i.k_j) d_j)
+//     S'  = e^(G_last) S + sum_j e^(G_last - G_j) d_j k_j^T
+// A CTA runs one chain: the chunks of one head, one after the other, for up to 128 rows of its state (the rows of S do
+// not touch one another).  Rows are the MMAs' M, so that S, S k and d stay in TMEM lanes, one row a lane, and go
+// from one product to the next without a transposition:
+//     X = S K^T        A = S (TMEM), B = K             per chunk: 128 x 64 x dstate
+//     D = V^T T^T + (X diag(-e^G)) T^T                 A = V^T (smem), then X (TMEM); B = T
+//     Q = S Q^T        A = S (TMEM), B = Q
+//     U = (D diag(e^(G_last - G))) K                   A = D (TMEM), B = K: S' = e^(G_last) S + U
+//     O = D P^T        A = D (TMEM), B = P
+//     [K; Q] K^T       of the chunk after the next: what N and P are made of
+//
+// Rounding.  q, k and v are bf16 and enter as they are (lengths and decays are factors beside the products).  S is kept in f32
+// registers; as operands S, X, T and the D of the update are split into two bf16 halves (hi + lo, 2^-18 together; lo x lo is
+// left out), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P and D are rounded
+// once.
+//
+// Warps: 0-7 state (two threads a row, each half of the columns), 8-11 prepare (gates, lengths, N, its inverse, P), 12
+// copies, 13 MMAs.  Every wait is bounded; after one that ran out the CTA's outputs are NaN.
+#include "delta_common.cuh"
+#include "tc_common.cuh"
+
+namespace ssm {
+namespace {
+
+using namespace layer;
+
+constexpr int kC = 64;             // tokens of a chunk
+constexpr int kM = 128;            // rows of a tile
+constexpr int kStages = 3;         // K, Q, V of a chunk
+constexpr int kStateWarps = 8, kPrepWarps = 4;
+constexpr int kCopyWarp = kStateWarps + kPrepWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kTile = kC * 128;    // bytes of 64 rows of 128
+constexpr int kLd = 68;            // floats of a row of N: rows four banks apart
+constexpr uint32_t kPrepBar = 1;
+
+// TMEM columns
+constexpr uint32_t kColHi = 0, kColLo = 64;   // S, two columns of the state each
+constexpr uint32_t kColU = 128;               // U over X and D
+constexpr uint32_t kColX = 128, kColD = 192;
+constexpr uint32_t kColOp = 256;              // X, then D of the update: hi, lo; between them [K; Q] K^T
+constexpr uint32_t kColDo = 320;              // D of the output
+constexpr uint32_t kColQ = 352, kColO = 416;
+constexpr uint32_t kTmemCols = 512;
+
+enum Bar {
+  kFull = 0,                  // K, Q, V have landed
+  kEmpty = kFull + kStages,   // ... and are read
+  kReady = kEmpty + kStages,  // ... and are 0 past the last token
+  kTReady = kReady + kStages, // T, P and the factors of a chunk
+  kDone = kTReady + 2,        // its last product
+  kSFree = kDone + 2,         // its factors are read
+  kKq = kSFree + 2, kKqFree, kSReady, kXFull, kXReady, kDFull, kDReady, kUFull, kLast, kNumBars
+};
+
+struct Factors {  // of a chunk
+  float x[kC], u[kC], y[kC], last[4];
+};
+
+template <int DK>
+struct Layout {
+  static constexpr int kHalves = DK / 64;
+  static constexpr int kStage = kHalves * 2 * kTile + 2 * kTile;  // [half][K rows, Q rows], [64 rows of S][tokens]
+  static constexpr int kT0 = kStages * kStage;                    // [2][hi, lo]
+  static constexpr int kP0 = kT0 + 2 * 2 * kTile;                 // [2]
+  static constexpr int kN0 = kP0 + 2 * kTile;
+  static constexpr int kY0 = kN0 + kC * kLd * 4;                  // products inside the inversion
+  static constexpr int kG0 = kY0 + 32 * 36 * 4;                   // float4 a token: G (hi, lo), beta, 1 / length of k
+  static constexpr int kF0 = kG0 + kC * 16;
+  static constexpr int kBars = kF0 + 2 * (int)sizeof(Factors);
+  static constexpr int kTotal = kBars + kNumBars * 8 + 32;
+};
+
+struct Params {
+  ssm_delta_args a;
+  int tiles;     // of a head's rows
+  uint32_t inner;  // tensors whose map has sequences inside tokens
+  LookbackCtl ctl;
+};
+constexpr uint32_t kMapQ = 1, kMapK = 2, kMapV = 4;
+
+// Two f32 as bf16 pairs hi + lo.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(a, b);
+  float ha, hb;
+  unpack2(hi, ha, hb);
+  const float2 r = __fadd2_rn(make_float2(a, b), make_float2(-ha, -hb));
+  lo = pack2(r.x, r.y);
+}
+
+// a + b as hi + lo
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float h, float l) {
+  const float s = __fadd_rn(hi, h), t = __fsub_rn(s, hi);
+  const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(h, t));
+  lo = __fadd_rn(lo, __fadd_rn(l, e));
+  hi = s;
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+    delta_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+  using L = Layout<DK>;
+  constexpr int kHalves = L::kHalves;
+  extern __shared__ unsigned char raw[];
+  unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kBars + kNumBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* total = reinterpret_cast<float*>(tmem_slot + 2);  // the first 32 tokens' G
+  float* sN = reinterpret_cast<float*>(base + L::kN0);
+  float* sY = reinterpret_cast<float*>(base + L::kY0);
+  float4* sG = reinterpret_cast<float4*>(base + L::kG0);
+  Factors* sF = reinterpret_cast<Factors*>(base + L::kF0);
+
+  const ssm_delta_args& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = (int)(blockIdx.x % p.tiles) * kM;
+  const int64_t bh = blockIdx.x / p.tiles;
+  const int h = (int)(bh % a.nheads), g = h / (a.nheads / a.ngroups);
+  const int64_t b = bh / a.nheads;
+  const int rows = min(kM, a.headdim - m0);
+  const int v_boxes = rows > 64 ? 2 : 1;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    const auto init = [&](int first, int n, uint32_t count) {
+      for (int i = 0; i < n; ++i) mbar_init(&bars[first + i], count);
+    };
+    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kReady, kStages, kPrepWarps), init(kTReady, 2, kPrepWarps);
+    init(kDone, 2, 1), init(kSFree, 2, kStateWarps), init(kKq, 1, 1), init(kKqFree, 1, kPrepWarps);
+    init(kSReady, 1, kStateWarps), init(kXFull, 1, 1), init(kXReady, 1, kStateWarps), init(kDFull, 1, 1);
+    init(kDReady, 1, kStateWarps), init(kUFull, 1, 1), init(kLast, 1, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (v_boxes == 1)  // rows that no copy brings
+    for (int i = threadIdx.x; i < kStages * kTile / 16; i += kThreads)
+      *reinterpret_cast<uint4*>(base + i / (kTile / 16) * L::kStage + kHalves * 2 * kTile + kTile + i % (kTile / 16) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  int64_t tokens = a.seqlen;
+  if (a.lens) tokens = min(tokens, (int64_t)max(a.lens[b], 0));
+  const int n = (int)((tokens + kC - 1) / kC);
+
+  // A bounded wait, the same answer in every lane of a warp
+  const auto wait_one = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+      if (*abort_flag || global_timer_ns() - t0 > p.ctl.spin_limit_ns) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+  const auto wait = [&](int bar, int64_t phase) -> bool {
+    return __all_sync(0xffffffffu, wait_one(&bars[bar], (uint32_t)phase & 1u));
+  };
+  const auto arrive = [&](int bar) {  // one of a warp, after all its lanes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[bar]);
+  };
+
+  if (warp < kStateWarps) {
+    // ------------------------------ state: S in registers, the operands in TMEM ----------------------------
+    constexpr int CW = DK / 2;  // columns of S a thread
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
+    const bool have = row < rows;
+    const int64_t at = ((bh * a.headdim + m0 + row) * DK) + half * CW;
+    float s[CW];
+#pragma unroll
+    for (int i = 0; i < CW; ++i) s[i] = 0.f;
+    if (a.h0 && have) {
+#pragma unroll
+      for (int i = 0; i < CW; ++i) s[i] = a.h0[at + i];
+    }
+    __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0 + row;
+    const int64_t y_stride = (int64_t)a.nheads * a.headdim;
+    float last = 1.f;  // e^(G_last) of the chunk before
+
+    // S <- last S + U
+    const auto update = [&](int q) {
+      uint32_t r[16];
+      tc::tmem_ld16(tm + kColU + half * CW + 16 * q, r);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float2 v = __ffma2_rn(make_float2(s[16 * q + j], s[16 * q + j + 1]), make_float2(last, last),
+                                    make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+        s[16 * q + j] = v.x, s[16 * q + j + 1] = v.y;
+      }
+    };
+    // y of chunk c: this thread's row, 32 tokens
+    const auto output = [&](int c) -> bool {
+      if (!wait(kDone + (c & 1), c >> 1)) return false;
+      tc::fence_after_sync();
+      const Factors& f = sF[c & 1];
+      const int64_t t0 = (int64_t)c * kC + half * 32;
+      const int m = (int)min((int64_t)32, tokens - t0);
+      __nv_bfloat16* yc = yp + t0 * y_stride;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t sq[16], od[16];
+        tc::tmem_ld16(tm + kColQ + half * 32 + 16 * q, sq);
+        tc::tmem_ld16(tm + kColO + half * 32 + 16 * q, od);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float v = fmaf(__uint_as_float(sq[j]), f.y[half * 32 + 16 * q + j], __uint_as_float(od[j]));
+          if (have && 16 * q + j < m) yc[(16 * q + j) * y_stride] = __float2bfloat16_rn(v);
+        }
+      }
+      tc::fence_before_sync();
+      arrive(kSFree + (c & 1));
+      return true;
+    };
+
+    bool ok = true;
+    for (int c = 0; c < n && ok; ++c) {
+      const int bf = c & 1;
+      if (c > 0) {
+        ok = wait(kUFull, c - 1);
+        tc::fence_after_sync();
+      }
+#pragma unroll
+      for (int q = 0; q < CW / 16; ++q) {
+        if (c > 0) update(q);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split2(s[16 * q + 2 * j], s[16 * q + 2 * j + 1], hi[j], lo[j]);
+        tc::tmem_st8(tm + kColHi + (half * CW) / 2 + 8 * q, hi);
+        tc::tmem_st8(tm + kColLo + (half * CW) / 2 + 8 * q, lo);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      arrive(kSReady);
+      if (c > 0) ok = ok && output(c - 1);
+      const Factors& f = sF[bf];
+      // X, scaled, as an operand; its place may still hold [K; Q] K^T of the next chunk
+      ok = ok && wait(kTReady + bf, c >> 1) && (c + 1 >= n || wait(kKqFree, c + 1)) && wait(kXFull, c);
+      if (!ok) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t r[16], hi[8], lo[8];
+        tc::tmem_ld16(tm + kColX + half * 32 + 16 * q, r);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 w = *reinterpret_cast<const float2*>(&f.x[half * 32 + 16 * q + 2 * j]);
+          const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), w);
+          split2(v.x, v.y, hi[j], lo[j]);
+        }
+        tc::tmem_st8(tm + kColOp + half * 16 + 8 * q, hi);
+        tc::tmem_st8(tm + kColOp + 32 + half * 16 + 8 * q, lo);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      arrive(kXReady);
+      // D, for the output and scaled for the update
+      if (!(ok = wait(kDFull, c))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t r[16], d[8], hi[8], lo[8];
+        tc::tmem_ld16(tm + kColD + half * 32 + 16 * q, r);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 e = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          const float2 w = *reinterpret_cast<const float2*>(&f.u[half * 32 + 16 * q + 2 * j]);
+          d[j] = pack2(e.x, e.y);
+          const float2 v = __fmul2_rn(e, w);
+          split2(v.x, v.y, hi[j], lo[j]);
+        }
+        tc::tmem_st8(tm + kColOp + half * 16 + 8 * q, hi);
+        tc::tmem_st8(tm + kColOp + 32 + half * 16 + 8 * q, lo);
+        tc::tmem_st8(tm + kColDo + half * 16 + 8 * q, d);
+      }
+      last = f.last[0];
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      arrive(kDReady);
+    }
+    if (n > 0 && ok) {
+      ok = wait(kUFull, n - 1);
+      tc::fence_after_sync();
+#pragma unroll
+      for (int q = 0; q < CW / 16; ++q) update(q);
+      ok = ok && output(n - 1);
+    }
+    if (ok && a.h_final && have) {
+#pragma unroll
+      for (int i = 0; i < CW; ++i) a.h_final[at + i] = s[i];
+    }
+    tc::fence_before_sync();
+  } else if (warp < kCopyWarp) {
+    // ------------------------------ prepare: gates, lengths, N, T, P ---------------------------------------
+    const int t = threadIdx.x - 32 * kStateWarps, w = warp - kStateWarps;
+    const int i = t & 63;            // a token: of k (t < 64) or of q
+    const bool is_k = t < 64;
+    const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
+    const delta::Gate gate(a, h);
+    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt.ptr) + b * a.dt.batch_stride + h;
+    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta.ptr) + b * a.beta.batch_stride + h;
+    const auto gates = [&](int c, __nv_bfloat16& dt, __nv_bfloat16& be) {
+      const int64_t tok = (int64_t)c * kC + i;
+      dt = be = __float2bfloat16_rn(0.f);
+      if (is_k && tok < tokens) {
+        dt = dp[tok * a.dt.token_stride];
+        be = bp[tok * a.beta.token_stride];
+      }
+    };
+    __nv_bfloat16 dt_raw, be_raw;
+    gates(0, dt_raw, be_raw);
+    for (int c = 0; c < n; ++c) {
+      const int st = c % kStages, bf = c & 1;
+      unsigned char* kq = base + st * L::kStage;
+      const int live = (int)min((int64_t)kC, tokens - (int64_t)c * kC);
+      // sums of the log-decays
+      float gh = 0.f, gl = 0.f, beta = 0.f;
+      if (is_k) {
+        if (i < live) {
+          gh = gate.log2_decay(__bfloat162float(dt_raw));
+          beta = gate.beta(__bfloat162float(be_raw));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const float ph = __shfl_up_sync(0xffffffffu, gh, o), pl = __shfl_up_sync(0xffffffffu, gl, o);
+          if (lane >= o) add_exact(gh, gl, ph, pl);
+        }
+        if (t == 31) total[0] = gh, total[1] = gl;
+      }
+      gates(c + 1, dt_raw, be_raw);
+      bool bad = !wait(kFull + st, c / kStages);
+      if (live < kC && !bad) {  // zeros past the last token
+        for (int j = t; j < (kC - live) * (L::kStage / kTile) * 8; j += 32 * kPrepWarps) {
+          const int r = live + j / ((L::kStage / kTile) * 8), o = j % ((L::kStage / kTile) * 8);
+          *reinterpret_cast<uint4*>(kq + (o >> 3) * kTile + r * 128 + (o & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      float rq = 0.f;
+      if (live == kC) arrive(kReady + st);  // at once
+      if (named_bar_any(kPrepBar, 32 * kPrepWarps, bad)) break;
+      if (live < kC) arrive(kReady + st);
+      if (is_k) {
+        if (w == 1) add_exact(gh, gl, total[0], total[1]);
+        sG[i] = make_float4(gh, gl, beta, 1.f);
+      } else if (gate.unit) {  // the length of q
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int o = 0; o < kHalves * 8; ++o) {
+          const uint4 e = *reinterpret_cast<const uint4*>(kq + (o >> 3) * 2 * kTile + kTile + i * 128 + (((o & 7) ^ (i & 7)) << 4));
+          const uint32_t u[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 v;
+            unpack2(u[j], v.x, v.y);
+            sum = __ffma2_rn(v, v, sum);
+          }
+        }
+        rq = a.scale * gate.inverse_length(sum.x + sum.y);
+      } else {
+        rq = a.scale;
+      }
+      bad = !wait(kKq, c);
+      tc::fence_after_sync();
+      uint32_t r[kC];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t e[32];
+        tc::tmem_ld32(tm + kColOp + 32 * q, e);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[32 * q + j] = e[j];
+      }
+      tc::fence_before_sync();
+      arrive(kKqFree);
+      if (is_k && gate.unit) {
+        float kk = 0.f;
+#pragma unroll
+        for (int j = 0; j < kC; ++j)
+          if (j == i) kk = __uint_as_float(r[j]);
+        sG[i].w = gate.inverse_length(kk);
+      }
+      if (c >= 2) bad = bad || !wait(kSFree + bf, (c >> 1) - 1) || !wait(kDone + bf, (c >> 1) - 1);
+      if (named_bar_any(kPrepBar, 32 * kPrepWarps, bad)) break;
+      const float4 gi = sG[i];
+      const float rowf = is_k ? gi.z * gi.w : rq;
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const float4 gj = sG[j];
+        const float e = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * gj.w * rowf * __uint_as_float(r[j]);
+        r[j] = __float_as_uint(is_k ? (j < i ? e : 0.f) : (j <= i ? e : 0.f));
+      }
+      const float4 gl4 = sG[kC - 1];
+      if (is_k) {
+#pragma unroll
+        for (int j = 0; j < kC; j += 4)
+          *reinterpret_cast<uint4*>(&sN[i * kLd + j]) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+        sF[bf].x[i] = -exp2_fast(gi.x + gi.y) * gi.w;
+        sF[bf].u[i] = exp2_fast((gl4.x - gi.x) + (gl4.y - gi.y)) * gi.w;
+        if (i == 0) sF[bf].last[0] = exp2_fast(gl4.x + gl4.y);
+      } else {
+        unsigned char* pr = base + L::kP0 + bf * kTile + i * 128;
+#pragma unroll
+        for (int o = 0; o < 8; ++o) {
+          uint4 v;
+          v.x = pack2(__uint_as_float(r[8 * o]), __uint_as_float(r[8 * o + 1]));
+          v.y = pack2(__uint_as_float(r[8 * o + 2]), __uint_as_float(r[8 * o + 3]));
+          v.z = pack2(__uint_as_float(r[8 * o + 4]), __uint_as_float(r[8 * o + 5]));
+          v.w = pack2(__uint_as_float(r[8 * o + 6]), __uint_as_float(r[8 * o + 7]));
+          *reinterpret_cast<uint4*>(pr + ((o ^ (i & 7)) << 4)) = v;
+        }
+        sF[bf].y[i] = rq * exp2_fast(gi.x + gi.y);
+      }
+      named_bar_sync(kPrepBar, 32 * kPrepWarps);
+      // (I + N)^-1 in place: the diagonal blocks of 16, then twice the blocks below the diagonal,
+      // T_10 = -T_11 (N_10 T_00)
+      {
+        float x[16];
+        const int o = 16 * w, col = lane & 15;
+#pragma unroll
+        for (int rr = 0; rr < 16; ++rr) {
+          float v = rr == col ? 1.f : 0.f;
+#pragma unroll
+          for (int k = 0; k < rr; ++k) v = fmaf(-sN[(o + rr) * kLd + o + k], x[k], v);
+          x[rr] = v;
+        }
+        __syncwarp();
+        if (lane < 16)
+#pragma unroll
+          for (int rr = 0; rr < 16; ++rr) sN[(o + rr) * kLd + o + col] = x[rr];
+      }
+      named_bar_sync(kPrepBar, 32 * kPrepWarps);
+      {
+        const int o = (t >> 6) * 32, rr = (t & 63) >> 2, cc = (t & 3) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const auto product = [&](const float* left, const float* right, int ld) {  // a row of left, four columns of right
+          v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float f = left[k];
+            const float4 e = *reinterpret_cast<const float4*>(right + k * ld);
+            v.x = fmaf(f, e.x, v.x), v.y = fmaf(f, e.y, v.y), v.z = fmaf(f, e.z, v.z), v.w = fmaf(f, e.w, v.w);
+          }
+        };
+        product(&sN[(o + 16 + rr) * kLd + o], &sN[o * kLd + o + cc], kLd);
+        *reinterpret_cast<float4*>(&sY[((t >> 6) * 16 + rr) * 36 + cc]) = v;
+        named_bar_sync(kPrepBar, 32 * kPrepWarps);
+        product(&sN[(o + 16 + rr) * kLd + o + 16], &sY[(t >> 6) * 16 * 36 + cc], 36);
+        *reinterpret_cast<float4*>(&sN[(o + 16 + rr) * kLd + o + cc]) = make_float4(-v.x, -v.y, -v.z, -v.w);
+      }
+      named_bar_sync(kPrepBar, 32 * kPrepWarps);
+      {
+        const int rr = (t >> 3) * 2, cc = (t & 7) * 4;
+        float2 v[2][2];
+        const auto product = [&](const float* left, const float* right, int ld) {  // two rows of left
+          v[0][0] = v[0][1] = v[1][0] = v[1][1] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 f0 = *reinterpret_cast<const float4*>(left + k), f1 = *reinterpret_cast<const float4*>(left + kLd + k);
+            const float l0[4] = {f0.x, f0.y, f0.z, f0.w}, l1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 e = *reinterpret_cast<const float4*>(right + (k + j) * ld);
+              const float2 e0 = make_float2(e.x, e.y), e1 = make_float2(e.z, e.w);
+              v[0][0] = __ffma2_rn(make_float2(l0[j], l0[j]), e0, v[0][0]);
+              v[0][1] = __ffma2_rn(make_float2(l0[j], l0[j]), e1, v[0][1]);
+              v[1][0] = __ffma2_rn(make_float2(l1[j], l1[j]), e0, v[1][0]);
+              v[1][1] = __ffma2_rn(make_float2(l1[j], l1[j]), e1, v[1][1]);
+            }
+          }
+        };
+        product(&sN[(32 + rr) * kLd], &sN[cc], kLd);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4*>(&sY[(rr + j) * 36 + cc]) = make_float4(v[j][0].x, v[j][0].y, v[j][1].x, v[j][1].y);
+        named_bar_sync(kPrepBar, 32 * kPrepWarps);
+        product(&sN[(32 + rr) * kLd + 32], &sY[cc], 36);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4*>(&sN[(32 + rr + j) * kLd + cc]) =
+              make_float4(-v[j][0].x, -v[j][0].y, -v[j][1].x, -v[j][1].y);
+      }
+      named_bar_sync(kPrepBar, 32 * kPrepWarps);
+      {  // T = inverse diag(beta), hi and lo
+        const int rr = t >> 1, half = t & 1;
+        unsigned char* th = base + L::kT0 + bf * 2 * kTile + rr * 128;
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int col = half * 32 + 8 * o + 2 * j;
+            split2(sN[rr * kLd + col] * sG[col].z, sN[rr * kLd + col + 1] * sG[col + 1].z, hi[j], lo[j]);
+          }
+          const int at = ((half * 4 + o) ^ (rr & 7)) << 4;
+          *reinterpret_cast<uint4*>(th + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(th + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      arrive(kTReady + bf);
+      named_bar_sync(kPrepBar, 32 * kPrepWarps);  // sG and sN are read before the next chunk's
+    }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------ copies -------------------------------------------------------------------
+    if (lane == 0) {
+      int c = 0;
+      const int copies = p.ctl.stall_tile == (int64_t)blockIdx.x ? 0 : n;  // (the test hook)
+      for (; c < copies; ++c) {
+        const int st = c % kStages;
+        if (c >= kStages && !wait_one(&bars[kEmpty + st], (uint32_t)(c / kStages - 1) & 1u)) break;
+        unsigned char* kq = base + st * L::kStage;
+        mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * 2 + v_boxes) * kTile);
+        const auto load = [&](int place, const CUtensorMap* map, int x, uint32_t which) {
+          const bool inner = (p.inner & which) != 0;
+          const int tok = c * kC;
+          tc::tma_load_3d(kq + place * kTile, map, x, inner ? (int)b : tok, inner ? tok : (int)b, &bars[kFull + st]);
+        };
+        for (int j = 0; j < kHalves; ++j) {
+          load(2 * j, &map_k, g * DK + 64 * j, kMapK);
+          load(2 * j + 1, &map_q, g * DK + 64 * j, kMapQ);
+        }
+        for (int j = 0; j < v_boxes; ++j) load(2 * kHalves + j, &map_v, h * a.headdim + m0 + 64 * j, kMapV);
+      }
+      for (int j = max(0, c - kStages); j < c; ++j)  // no copy is left in flight
+        mbar_wait(&bars[kFull + j % kStages], (uint32_t)(j / kStages) & 1u, p.ctl.spin_limit_ns);
+    }
+  } else if (lane == 0 && n > 0) {
+    // ------------------------------ MMAs ---------------------------------------------------------------------
+    constexpr uint32_t id64 = tc::idesc_bf16_f32(128, 64, false, false);     // A, B K-major
+    constexpr uint32_t id64v = tc::idesc_bf16_f32(128, 64, true, false);     // A = V^T
+    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, DK, false, true);      // B = K, columns of the state as N
+    const uint32_t sb = smem_addr(base);
+    const auto kq_at = [&](int c) { return sb + (c % kStages) * L::kStage; };
+    // k-step ks of a K-major tile of 64-column blocks
+    const auto k_major = [&](uint32_t at, int ks, uint32_t block) {
+      return tc::sdesc_sw128(at + (ks >> 2) * block + (ks & 3) * 32, 16, 1024);
+    };
+    int kqs = 0;
+    const auto products_kq = [&](int c) -> bool {  // [K; Q] K^T of chunk c
+      if (!wait_one(&bars[kReady + c % kStages], (uint32_t)(c / kStages) & 1u)) return false;
+      if (c > 0 && !wait_one(&bars[kKqFree], (uint32_t)(c - 1) & 1u)) return false;
+      tc::fence_after_sync();
+      const uint32_t at = kq_at(c);
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        const uint64_t d = k_major(at, ks, 2 * kTile);
+        tc::mma_bf16(tmem + kColOp, d, d, id64, ks > 0);
+      }
+      tc::mma_commit(&bars[kKq]);
+      kqs = c + 1;
+      return true;
+    };
+    bool ok = products_kq(0) && (n < 2 || products_kq(1));
+    int c = 0;  // chunks whose last commit was made
+    for (; c < n && ok; ++c) {
+      const int bf = c & 1;
+      const uint32_t kt = kq_at(c), qt = kt + kTile, vt = kt + kHalves * 2 * kTile;
+      const uint32_t th = sb + L::kT0 + bf * 2 * kTile, tl = th + kTile;
+      if (!(ok = wait_one(&bars[kSReady], (uint32_t)c & 1u))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        const uint64_t d = k_major(kt, ks, 2 * kTile);
+        tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, id64, ks > 0);
+        tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, id64, true);
+      }
+      tc::mma_commit(&bars[kXFull]);
+      if (!(ok = wait_one(&bars[kTReady + bf], (uint32_t)(c >> 1) & 1u))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        const uint64_t v = tc::sdesc_sw128(vt + ks * 2048, kTile, 1024);
+        tc::mma_bf16(tmem + kColD, v, k_major(th, ks, 0), id64v, ks > 0);
+        tc::mma_bf16(tmem + kColD, v, k_major(tl, ks, 0), id64v, true);
+      }
+      if (!(ok = wait_one(&bars[kXReady], (uint32_t)c & 1u))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id64, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(tl, ks, 0), id64, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 32 + 8 * ks, k_major(th, ks, 0), id64, true);
+      }
+      tc::mma_commit(&bars[kDFull]);
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        const uint64_t d = k_major(qt, ks, 2 * kTile);
+        tc::mma_bf16_ts(tmem + kColQ, tmem + kColHi + 8 * ks, d, id64, ks > 0);
+        tc::mma_bf16_ts(tmem + kColQ, tmem + kColLo + 8 * ks, d, id64, true);
+      }
+      if (!(ok = wait_one(&bars[kDReady], (uint32_t)c & 1u))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        const uint64_t d = tc::sdesc_sw128(kt + ks * 2048, 2 * kTile, 1024);
+        tc::mma_bf16_ts(tmem + kColU, tmem + kColOp + 8 * ks, d, id_u, ks > 0);
+        tc::mma_bf16_ts(tmem + kColU, tmem + kColOp + 32 + 8 * ks, d, id_u, true);
+      }
+      tc::mma_commit(&bars[kUFull]);
+#pragma unroll
+      for (int ks = 0; ks < kC / 16; ++ks)
+        tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, k_major(sb + L::kP0 + bf * kTile, ks, 0), id64, ks > 0);
+      tc::mma_commit(&bars[kDone + bf]);
+      tc::mma_commit(&bars[kEmpty + c % kStages]);
+      // its place holds the operand of U until that is done
+      if (c + 2 < n) {
+        if (!wait_one(&bars[kUFull], (uint32_t)c & 1u) || !products_kq(c + 2)) {
+          ok = false;
+          ++c;
+          break;
+        }
+      }
+    }
+    // Every MMA has completed, and no commit's arrival is still due.
+    tc::mma_commit(&bars[kLast]);
+    mbar_wait(&bars[kLast], 0, p.ctl.spin_limit_ns);
+    const auto drained = [&](int bar, int count) {
+      if (count > 0) mbar_wait(&bars[bar], (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
+    };
+    drained(kKq, kqs);
+    if (ok) drained(kXFull, c), drained(kDFull, c);
+    drained(kUFull, c);
+    for (int x = 0; x < 2; ++x) drained(kDone + x, (c - x + 1) / 2);
+    for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+  // padding, or everything after a wait that ran out
+  const bool lost = *abort_flag != 0;
+  __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0;
+  const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
+  for (int64_t j = (lost ? 0 : tokens) * rows + threadIdx.x; j < a.seqlen * rows; j += kThreads)
+    yt[j / rows * a.nheads * a.headdim + j % rows] = fill;
+  if (lost && a.h_final)
+    for (int j = threadIdx.x; j < rows * DK; j += kThreads)
+      a.h_final[(bh * a.headdim + m0) * DK + j] = __uint_as_float(0x7fc00000u);
+}
+
+// How a tensor map takes a tensor's rows: the two outer dimensions in the order of their strides, which nest (see selscan.cu).
+struct Nesting {
+  bool fits, inner;
+  uint64_t strides[2];  // bytes
+};
+Nesting nesting(const ssm_tokens& t, int64_t batch, int64_t seqlen, int64_t columns) {
+  const int64_t e = 2, row = (columns * e + 15) / 16 * 16;
+  if (!aligned_rows(t.ptr, batch > 1 ? t.batch_stride : 0, seqlen > 1 ? t.token_stride : 0, (int)e, 16)) return {};
+  const int64_t bs = batch > 1 ? t.batch_stride * e : 0, ts = seqlen > 1 ? t.token_stride * e : 0;
+  const bool inner = batch > 1 && bs < ts;
+  const int64_t low = inner ? bs : seqlen > 1 ? ts : batch > 1 ? bs : row, count = inner ? batch : seqlen;
+  if (low < columns * e || low >= (int64_t)1 << 40 || count >= ((int64_t)1 << 40) / low) return {};
+  const int64_t high = inner ? ts : batch > 1 ? bs : low * count;
+  if (high < low * count || high % low != 0 || high >= (int64_t)1 << 40) return {};
+  return {true, inner, {(uint64_t)low, (uint64_t)high}};
+}
+
+}  // namespace
+
+bool delta_tc_supported(const ssm_delta_args& a) {
+  if (a.dtype != SSM_BF16 || (a.dstate != 64 && a.dstate != 128) || a.headdim % 8 != 0 || a.seqlen < 1 ||
+      a.seqlen > 0x7fffffff - kC)
+    return false;
+  const int64_t n = (int64_t)a.ngroups * a.dstate;
+  return nesting(a.q, a.batch, a.seqlen, n).fits && nesting(a.k, a.batch, a.seqlen, n).fits &&
+         nesting(a.v, a.batch, a.seqlen, (int64_t)a.nheads * a.headdim).fits;
+}
+
+cudaError_t launch_delta_tc(const ssm_delta_args& a, const LookbackCtl& ctl, cudaStream_t s) {
+  Params p{};
+  p.a = a;
+  p.tiles = (a.headdim + kM - 1) / kM;
+  p.ctl = ctl;
+  CUtensorMap maps[3];
+  const ssm_tokens* t[3] = {&a.q, &a.k, &a.v};
+  const int64_t columns[3] = {(int64_t)a.ngroups * a.dstate, (int64_t)a.ngroups * a.dstate, (int64_t)a.nheads * a.headdim};
+  for (int i = 0; i < 3; ++i) {
+    const Nesting n = nesting(*t[i], a.batch, a.seqlen, columns[i]);
+    if (n.inner) p.inner |= 1u << i;
+    const uint64_t outer[2] = {(uint64_t)a.seqlen, (uint64_t)a.batch};
+    const uint32_t box_outer[2] = {(uint32_t)kC, 1};
+    const uint64_t dims[3] = {(uint64_t)columns[i], outer[n.inner], outer[!n.inner]};
+    const uint32_t box[3] = {64, box_outer[n.inner], box_outer[!n.inner]};
+    const cudaError_t e = encode_tensor_map_3d(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t[i]->ptr, dims, n.strides, box,
+                                               CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  }
+  const auto go = [&](auto kernel, size_t bytes) {
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes + 1024);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)(a.batch * a.nheads * p.tiles)), dim3(kThreads), bytes + 1024, s, maps[0], maps[1],
+                      maps[2], p);
+  };
+  return a.dstate == 64 ? go(delta_tc_kernel<64>, Layout<64>::kTotal) : go(delta_tc_kernel<128>, Layout<128>::kTotal);
+}
+
+}  // namespace ssm
