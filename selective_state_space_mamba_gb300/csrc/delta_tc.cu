@@ -20,8 +20,8 @@
 // left out), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P and D are rounded
 // once.
 //
-// Warps: 0-7 state (two threads a row, each half of the columns), 8-11 prepare (gates, lengths, N, its inverse, P), 12
-// copies, 13 MMAs.  Every wait is bounded; after one that ran out the CTA's outputs are NaN.
+// Warps: 0-15 state (four threads a row, each a quarter of its columns), 16-23 prepare (lengths, N, its inverse, P), 24 copies,
+// 25 MMAs, 26 gates.  Every wait is bounded; after one that ran out the CTA's outputs are NaN.
 #include "delta_common.cuh"
 #include "tc_common.cuh"
 
@@ -33,11 +33,14 @@ using namespace layer;
 constexpr int kC = 64;             // tokens of a chunk
 constexpr int kM = 128;            // rows of a tile
 constexpr int kStages = 3;         // K, Q, V of a chunk
-constexpr int kStateWarps = 8, kPrepWarps = 4;
-constexpr int kCopyWarp = kStateWarps + kPrepWarps, kMmaWarp = kCopyWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kParts = 4;          // state threads of a row
+constexpr int kStateWarps = 4 * kParts, kPrepWarps = 8;
+constexpr int kCopyWarp = kStateWarps + kPrepWarps, kMmaWarp = kCopyWarp + 1, kGateWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kGateWarp + 1);
+constexpr int kPrep = 32 * kPrepWarps;
 constexpr int kTile = kC * 128;    // bytes of 64 rows of 128
 constexpr int kLd = 68;            // floats of a row of N: rows four banks apart
+constexpr int kLdY = 36;
 constexpr uint32_t kPrepBar = 1;
 
 // TMEM columns
@@ -45,7 +48,7 @@ constexpr uint32_t kColHi = 0, kColLo = 64;   // S, two columns of the state eac
 constexpr uint32_t kColU = 128;               // U over X and D
 constexpr uint32_t kColX = 128, kColD = 192;
 constexpr uint32_t kColOp = 256;              // X, then D of the update: hi, lo; between them [K; Q] K^T
-constexpr uint32_t kColDo = 320;              // D of the output
+constexpr uint32_t kColDo = 320, kColDoLo = 480;  // D of the output
 constexpr uint32_t kColQ = 352, kColO = 416;
 constexpr uint32_t kTmemCols = 512;
 
@@ -53,14 +56,26 @@ enum Bar {
   kFull = 0,                  // K, Q, V have landed
   kEmpty = kFull + kStages,   // ... and are read
   kReady = kEmpty + kStages,  // ... and are 0 past the last token
-  kTReady = kReady + kStages, // T, P and the factors of a chunk
+  kGates = kReady + kStages,  // a chunk's sums of log-decays and betas
+  kGatesFree = kGates + 2,
+  kTReady = kGatesFree + 2,   // T, P and the factors of a chunk
   kDone = kTReady + 2,        // its last product
   kSFree = kDone + 2,         // its factors are read
-  kKq = kSFree + 2, kKqFree, kSReady, kXFull, kXReady, kDFull, kDReady, kUFull, kLast, kNumBars
+  kSReady = kSFree + 2,       // S as an operand, 64 of its columns each
+  kUFull = kSReady + 2,       // U, likewise
+  kKq = kUFull + 2, kKqFree, kXFull, kXReady, kDFull, kDReady, kOReady, kLast, kNumBars
 };
 
 struct Factors {  // of a chunk
   float x[kC], u[kC], y[kC], last[4];
+};
+struct Tokens {  // of a chunk, for the prepare warps
+  float4 e[kC / 2];   // of two tokens: G minus log2 of 1 / length of k, hi and lo
+  float2 g[kC];       // G hi, lo
+  float row[kC];      // beta / length of k
+  float col[kC / 2];  // first half: e^(G_31 - G_j) / length of k
+  float up[kC / 2];   // second half: e^(G_i - G_31)
+  float beta[kC], rk[kC], rq[kC];
 };
 
 template <int DK>
@@ -71,15 +86,16 @@ struct Layout {
   static constexpr int kP0 = kT0 + 2 * 2 * kTile;                 // [2]
   static constexpr int kN0 = kP0 + 2 * kTile;
   static constexpr int kY0 = kN0 + kC * kLd * 4;                  // products inside the inversion
-  static constexpr int kG0 = kY0 + 32 * 36 * 4;                   // float4 a token: G (hi, lo), beta, 1 / length of k
-  static constexpr int kF0 = kG0 + kC * 16;
+  static constexpr int kG0 = kY0 + 32 * kLdY * 4;                 // [2] float4 a token: G (hi, lo), beta
+  static constexpr int kE0 = kG0 + 2 * kC * 16;
+  static constexpr int kF0 = kE0 + (int)sizeof(Tokens);
   static constexpr int kBars = kF0 + 2 * (int)sizeof(Factors);
-  static constexpr int kTotal = kBars + kNumBars * 8 + 32;
+  static constexpr int kTotal = kBars + kNumBars * 8 + 16;
 };
 
 struct Params {
   ssm_delta_args a;
-  int tiles;     // of a head's rows
+  int tiles;       // of a head's rows
   uint32_t inner;  // tensors whose map has sequences inside tokens
   LookbackCtl ctl;
 };
@@ -113,10 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kBars + kNumBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* total = reinterpret_cast<float*>(tmem_slot + 2);  // the first 32 tokens' G
   float* sN = reinterpret_cast<float*>(base + L::kN0);
   float* sY = reinterpret_cast<float*>(base + L::kY0);
-  float4* sG = reinterpret_cast<float4*>(base + L::kG0);
+  Tokens& tk = *reinterpret_cast<Tokens*>(base + L::kE0);
   Factors* sF = reinterpret_cast<Factors*>(base + L::kF0);
 
   const ssm_delta_args& a = p.a;
@@ -133,10 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto init = [&](int first, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(&bars[first + i], count);
     };
-    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kReady, kStages, kPrepWarps), init(kTReady, 2, kPrepWarps);
-    init(kDone, 2, 1), init(kSFree, 2, kStateWarps), init(kKq, 1, 1), init(kKqFree, 1, kPrepWarps);
-    init(kSReady, 1, kStateWarps), init(kXFull, 1, 1), init(kXReady, 1, kStateWarps), init(kDFull, 1, 1);
-    init(kDReady, 1, kStateWarps), init(kUFull, 1, 1), init(kLast, 1, 1);
+    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kReady, kStages, kPrepWarps);
+    init(kGates, 2, 1), init(kGatesFree, 2, kPrepWarps), init(kTReady, 2, kPrepWarps), init(kDone, 2, 1);
+    init(kSFree, 2, kStateWarps), init(kSReady, 2, kStateWarps / kHalves), init(kUFull, 2, 1), init(kKq, 1, 1);
+    init(kKqFree, 1, kPrepWarps - 2), init(kXFull, 1, 1), init(kXReady, 1, kStateWarps), init(kDFull, 1, 1);
+    init(kDReady, 1, kStateWarps), init(kOReady, 1, kStateWarps), init(kLast, 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -144,10 +160,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
+  const auto zero = [&](int at, int bytes) {
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
+      *reinterpret_cast<uint4*>(base + at + i) = make_uint4(0u, 0u, 0u, 0u);
+  };
   if (v_boxes == 1)  // rows that no copy brings
-    for (int i = threadIdx.x; i < kStages * kTile / 16; i += kThreads)
-      *reinterpret_cast<uint4*>(base + i / (kTile / 16) * L::kStage + kHalves * 2 * kTile + kTile + i % (kTile / 16) * 16) =
-          make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kStages; ++i) zero(i * L::kStage + (kHalves * 2 + 1) * kTile, kTile);
+  zero(L::kP0, 2 * kTile);  // above the diagonal blocks nothing is written
+  zero(L::kN0, kC * kLd * 4);
   fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
@@ -180,11 +200,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kStateWarps) {
     // ------------------------------ state: S in registers, the operands in TMEM ----------------------------
-    constexpr int CW = DK / 2;  // columns of S a thread
-    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane;
+    constexpr int CW = DK / kParts;  // columns of S a thread
+    constexpr int TW = kC / kParts;  // tokens of X, D and y a thread
+    const int quad = warp & 3, part = warp >> 2, row = quad * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
+    const int u_half = DK == 128 ? part >> 1 : 0;
     const bool have = row < rows;
-    const int64_t at = ((bh * a.headdim + m0 + row) * DK) + half * CW;
+    const int64_t at = ((bh * a.headdim + m0 + row) * DK) + part * CW;
     float s[CW];
 #pragma unroll
     for (int i = 0; i < CW; ++i) s[i] = 0.f;
@@ -199,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // S <- last S + U
     const auto update = [&](int q) {
       uint32_t r[16];
-      tc::tmem_ld16(tm + kColU + half * CW + 16 * q, r);
+      tc::tmem_ld16(tm + kColU + part * CW + 16 * q, r);
       tc::tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
@@ -208,28 +230,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         s[16 * q + j] = v.x, s[16 * q + j + 1] = v.y;
       }
     };
-    // y of chunk c: this thread's row, 32 tokens
+    // y of chunk c: this thread's row and tokens
     const auto output = [&](int c) -> bool {
       if (!wait(kDone + (c & 1), c >> 1)) return false;
       tc::fence_after_sync();
-      const Factors& f = sF[c & 1];
-      const int64_t t0 = (int64_t)c * kC + half * 32;
-      const int m = (int)min((int64_t)32, tokens - t0);
+      const float* f = sF[c & 1].y + part * TW;
+      const int64_t t0 = (int64_t)c * kC + part * TW;
+      const int m = (int)min((int64_t)TW, tokens - t0);
       __nv_bfloat16* yc = yp + t0 * y_stride;
+      uint32_t sq[16], od[16];
+      tc::tmem_ld16(tm + kColQ + part * TW, sq);
+      tc::tmem_ld16(tm + kColO + part * TW, od);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t sq[16], od[16];
-        tc::tmem_ld16(tm + kColQ + half * 32 + 16 * q, sq);
-        tc::tmem_ld16(tm + kColO + half * 32 + 16 * q, od);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float v = fmaf(__uint_as_float(sq[j]), f.y[half * 32 + 16 * q + j], __uint_as_float(od[j]));
-          if (have && 16 * q + j < m) yc[(16 * q + j) * y_stride] = __float2bfloat16_rn(v);
-        }
+      for (int j = 0; j < TW; j += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(f + j);
+        const float2 v0 = __ffma2_rn(make_float2(__uint_as_float(sq[j]), __uint_as_float(sq[j + 1])), make_float2(w.x, w.y),
+                                     make_float2(__uint_as_float(od[j]), __uint_as_float(od[j + 1])));
+        const float2 v1 =
+            __ffma2_rn(make_float2(__uint_as_float(sq[j + 2]), __uint_as_float(sq[j + 3])), make_float2(w.z, w.w),
+                       make_float2(__uint_as_float(od[j + 2]), __uint_as_float(od[j + 3])));
+        sq[j / 2] = pack2(v0.x, v0.y), sq[j / 2 + 1] = pack2(v1.x, v1.y);
       }
       tc::fence_before_sync();
       arrive(kSFree + (c & 1));
+      if (have) {
+        uint16_t* yo = reinterpret_cast<uint16_t*>(yc);
+        if (m == TW) {
+#pragma unroll
+          for (int j = 0; j < TW; ++j, yo += y_stride) *yo = (uint16_t)(sq[j / 2] >> (16 * (j & 1)));
+        } else {
+#pragma unroll
+          for (int j = 0; j < TW; ++j, yo += y_stride)
+            if (j < m) *yo = (uint16_t)(sq[j / 2] >> (16 * (j & 1)));
+        }
+      }
       return true;
     };
 
@@ -237,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < n && ok; ++c) {
       const int bf = c & 1;
       if (c > 0) {
-        ok = wait(kUFull, c - 1);
+        ok = wait(kUFull + u_half, c - 1);
         tc::fence_after_sync();
       }
 #pragma unroll
@@ -246,62 +281,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) split2(s[16 * q + 2 * j], s[16 * q + 2 * j + 1], hi[j], lo[j]);
-        tc::tmem_st8(tm + kColHi + (half * CW) / 2 + 8 * q, hi);
-        tc::tmem_st8(tm + kColLo + (half * CW) / 2 + 8 * q, lo);
+        tc::tmem_st8(tm + kColHi + (part * CW) / 2 + 8 * q, hi);
+        tc::tmem_st8(tm + kColLo + (part * CW) / 2 + 8 * q, lo);
       }
       tc::tmem_st_wait();
       tc::fence_before_sync();
-      arrive(kSReady);
+      arrive(kSReady + u_half);
       if (c > 0) ok = ok && output(c - 1);
       const Factors& f = sF[bf];
       // X, scaled, as an operand; its place may still hold [K; Q] K^T of the next chunk
       ok = ok && wait(kTReady + bf, c >> 1) && (c + 1 >= n || wait(kKqFree, c + 1)) && wait(kXFull, c);
       if (!ok) break;
       tc::fence_after_sync();
+      uint32_t r[16], hi[8], lo[8];
+      tc::tmem_ld16(tm + kColX + part * TW, r);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t r[16], hi[8], lo[8];
-        tc::tmem_ld16(tm + kColX + half * 32 + 16 * q, r);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 w = *reinterpret_cast<const float2*>(&f.x[half * 32 + 16 * q + 2 * j]);
-          const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), w);
-          split2(v.x, v.y, hi[j], lo[j]);
-        }
-        tc::tmem_st8(tm + kColOp + half * 16 + 8 * q, hi);
-        tc::tmem_st8(tm + kColOp + 32 + half * 16 + 8 * q, lo);
+      for (int j = 0; j < 8; ++j) {
+        const float2 w = *reinterpret_cast<const float2*>(&f.x[part * TW + 2 * j]);
+        const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), w);
+        split2(v.x, v.y, hi[j], lo[j]);
       }
+      tc::tmem_st8(tm + kColOp + part * TW / 2, hi);
+      tc::tmem_st8(tm + kColOp + 32 + part * TW / 2, lo);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kXReady);
-      // D, for the output and scaled for the update
+      // D: scaled for the update, then as it is for the output
       if (!(ok = wait(kDFull, c))) break;
       tc::fence_after_sync();
+      tc::tmem_ld16(tm + kColD + part * TW, r);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t r[16], d[8], hi[8], lo[8];
-        tc::tmem_ld16(tm + kColD + half * 32 + 16 * q, r);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 e = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-          const float2 w = *reinterpret_cast<const float2*>(&f.u[half * 32 + 16 * q + 2 * j]);
-          d[j] = pack2(e.x, e.y);
-          const float2 v = __fmul2_rn(e, w);
-          split2(v.x, v.y, hi[j], lo[j]);
-        }
-        tc::tmem_st8(tm + kColOp + half * 16 + 8 * q, hi);
-        tc::tmem_st8(tm + kColOp + 32 + half * 16 + 8 * q, lo);
-        tc::tmem_st8(tm + kColDo + half * 16 + 8 * q, d);
+      for (int j = 0; j < 8; ++j) {
+        const float2 w = *reinterpret_cast<const float2*>(&f.u[part * TW + 2 * j]);
+        const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), w);
+        split2(v.x, v.y, hi[j], lo[j]);
       }
       last = f.last[0];
+      tc::tmem_st8(tm + kColOp + part * TW / 2, hi);
+      tc::tmem_st8(tm + kColOp + 32 + part * TW / 2, lo);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kDReady);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), hi[j], lo[j]);
+      tc::tmem_st8(tm + kColDo + part * TW / 2, hi);
+      tc::tmem_st8(tm + kColDoLo + part * TW / 2, lo);
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      arrive(kOReady);
     }
     if (n > 0 && ok) {
-      ok = wait(kUFull, n - 1);
+      ok = wait(kUFull + u_half, n - 1);
       tc::fence_after_sync();
 #pragma unroll
       for (int q = 0; q < CW / 16; ++q) update(q);
@@ -313,215 +345,285 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::fence_before_sync();
   } else if (warp < kCopyWarp) {
-    // ------------------------------ prepare: gates, lengths, N, T, P ---------------------------------------
+    // ------------------------------ prepare: lengths, N, T, P ----------------------------------------------
     const int t = threadIdx.x - 32 * kStateWarps, w = warp - kStateWarps;
-    const int i = t & 63;            // a token: of k (t < 64) or of q
-    const bool is_k = t < 64;
-    const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
-    const delta::Gate gate(a, h);
-    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt.ptr) + b * a.dt.batch_stride + h;
-    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta.ptr) + b * a.beta.batch_stride + h;
-    const auto gates = [&](int c, __nv_bfloat16& dt, __nv_bfloat16& be) {
-      const int64_t tok = (int64_t)c * kC + i;
-      dt = be = __float2bfloat16_rn(0.f);
-      if (is_k && tok < tokens) {
-        dt = dp[tok * a.dt.token_stride];
-        be = bp[tok * a.beta.token_stride];
-      }
-    };
-    __nv_bfloat16 dt_raw, be_raw;
-    gates(0, dt_raw, be_raw);
+    // of [K; Q] K^T a warp has 32 rows (of K, of Q) and 32 columns
+    const int quad = w & 3, half = w >> 2, i = (quad & 1) * 32 + lane;
+    const bool is_k = quad < 2;
+    const bool above = (quad & 1) == 0 && half == 1;  // all above the diagonal
+    const bool diagonal = (quad & 1) == half;
+    const bool unit = a.l2norm != 0;
     for (int c = 0; c < n; ++c) {
       const int st = c % kStages, bf = c & 1;
       unsigned char* kq = base + st * L::kStage;
       const int live = (int)min((int64_t)kC, tokens - (int64_t)c * kC);
-      // sums of the log-decays
-      float gh = 0.f, gl = 0.f, beta = 0.f;
-      if (is_k) {
-        if (i < live) {
-          gh = gate.log2_decay(__bfloat162float(dt_raw));
-          beta = gate.beta(__bfloat162float(be_raw));
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const float ph = __shfl_up_sync(0xffffffffu, gh, o), pl = __shfl_up_sync(0xffffffffu, gl, o);
-          if (lane >= o) add_exact(gh, gl, ph, pl);
-        }
-        if (t == 31) total[0] = gh, total[1] = gl;
-      }
-      gates(c + 1, dt_raw, be_raw);
       bool bad = !wait(kFull + st, c / kStages);
-      if (live < kC && !bad) {  // zeros past the last token
-        for (int j = t; j < (kC - live) * (L::kStage / kTile) * 8; j += 32 * kPrepWarps) {
-          const int r = live + j / ((L::kStage / kTile) * 8), o = j % ((L::kStage / kTile) * 8);
-          *reinterpret_cast<uint4*>(kq + (o >> 3) * kTile + r * 128 + (o & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
+      if (live == kC) {
+        arrive(kReady + st);
+      } else {  // zeros past the last token
+        constexpr int kRow = L::kStage / kTile * 8;  // 16-byte units of a token
+        if (!bad)
+          for (int j = t; j < (kC - live) * kRow; j += kPrep)
+            *reinterpret_cast<uint4*>(kq + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
+        if (named_bar_any(kPrepBar, kPrep, bad)) break;
+        arrive(kReady + st);
       }
-      float rq = 0.f;
-      if (live == kC) arrive(kReady + st);  // at once
-      if (named_bar_any(kPrepBar, 32 * kPrepWarps, bad)) break;
-      if (live < kC) arrive(kReady + st);
-      if (is_k) {
-        if (w == 1) add_exact(gh, gl, total[0], total[1]);
-        sG[i] = make_float4(gh, gl, beta, 1.f);
-      } else if (gate.unit) {  // the length of q
-        float2 sum = make_float2(0.f, 0.f);
+      if (unit) {  // lengths of k and q, two threads a row
+        const int rr = t >> 1;
+        const unsigned char* at = kq + (rr >> 6) * kTile + (rr & 63) * 128;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int o = 0; o < kHalves * 8; ++o) {
-          const uint4 e = *reinterpret_cast<const uint4*>(kq + (o >> 3) * 2 * kTile + kTile + i * 128 + (((o & 7) ^ (i & 7)) << 4));
+        for (int o = 0; o < kHalves * 4; ++o) {
+          const uint4 e = *reinterpret_cast<const uint4*>(at + (o >> 2) * 2 * kTile + ((((o & 3) + 4 * (t & 1)) ^ (rr & 7)) << 4));
           const uint32_t u[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float2 v;
             unpack2(u[j], v.x, v.y);
-            sum = __ffma2_rn(v, v, sum);
+            sum[j & 1] = __ffma2_rn(v, v, sum[j & 1]);
           }
         }
-        rq = a.scale * gate.inverse_length(sum.x + sum.y);
-      } else {
-        rq = a.scale;
+        float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        all += __shfl_xor_sync(0xffffffffu, all, 1);
+        if ((t & 1) == 0) (rr < 64 ? tk.rk[rr] : tk.rq[rr - 64]) = rsqrtf(all + delta::kLengthEps);
+      } else if (t < kC) {
+        tk.rk[t] = tk.rq[t] = 1.f;
       }
+      bad = bad || !wait(kGates + bf, c >> 1);
+      if (named_bar_any(kPrepBar, kPrep, bad)) break;
+      const float4* sG = reinterpret_cast<const float4*>(base + L::kG0) + bf * kC;
+      if (t < kC) {
+        const float4 gi = sG[t], gm = sG[kC / 2 - 1];
+        const float rk = tk.rk[t];
+        float eh = gi.x, el = gi.y;
+        if (unit) add_exact(eh, el, -__log2f(rk), 0.f);
+        reinterpret_cast<float*>(&tk.e[t >> 1])[t & 1] = eh;
+        reinterpret_cast<float*>(&tk.e[t >> 1])[2 + (t & 1)] = el;
+        tk.g[t] = make_float2(gi.x, gi.y);
+        tk.row[t] = gi.z * rk;
+        tk.beta[t] = gi.z;
+        if (t < kC / 2)
+          tk.col[t] = exp2_fast((gm.x - gi.x) + (gm.y - gi.y)) * rk;
+        else
+          tk.up[t - kC / 2] = exp2_fast((gi.x - gm.x) + (gi.y - gm.y));
+      }
+      named_bar_sync(kPrepBar, kPrep);
       bad = !wait(kKq, c);
       tc::fence_after_sync();
-      uint32_t r[kC];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      float r[32];
+      if (!above) {
         uint32_t e[32];
-        tc::tmem_ld32(tm + kColOp + 32 * q, e);
+        tc::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kColOp + 32 * half, e);
         tc::tmem_ld_wait();
+        tc::fence_before_sync();
+        arrive(kKqFree);
+        const float2 g = tk.g[i];
+        float f = is_k ? tk.row[i] : a.scale * tk.rq[i];
+        if (diagonal) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) r[32 * q + j] = e[j];
-      }
-      tc::fence_before_sync();
-      arrive(kKqFree);
-      if (is_k && gate.unit) {
-        float kk = 0.f;
+          for (int j = 0; j < 32; j += 2) {
+            const float4 q = tk.e[(32 * half + j) >> 1];
+            const float2 d = __fadd2_rn(__fadd2_rn(make_float2(g.x, g.x), make_float2(-q.x, -q.y)),
+                                        __fadd2_rn(make_float2(g.y, g.y), make_float2(-q.z, -q.w)));
+            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(exp2_fast(d.x), exp2_fast(d.y)), make_float2(f, f)),
+                                        make_float2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])));
+            r[j] = j < lane || (j == lane && !is_k) ? v.x : 0.f;
+            r[j + 1] = j + 1 < lane || (j + 1 == lane && !is_k) ? v.y : 0.f;
+          }
+        } else {  // below: e^(G_i - G_j) through the first half's last token
+          f *= tk.up[lane];
 #pragma unroll
-        for (int j = 0; j < kC; ++j)
-          if (j == i) kk = __uint_as_float(r[j]);
-        sG[i].w = gate.inverse_length(kk);
+          for (int j = 0; j < 32; j += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(&tk.col[j]);
+            const float2 v0 = __fmul2_rn(__fmul2_rn(make_float2(q.x, q.y), make_float2(f, f)),
+                                         make_float2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])));
+            const float2 v1 = __fmul2_rn(__fmul2_rn(make_float2(q.z, q.w), make_float2(f, f)),
+                                         make_float2(__uint_as_float(e[j + 2]), __uint_as_float(e[j + 3])));
+            r[j] = v0.x, r[j + 1] = v0.y, r[j + 2] = v1.x, r[j + 3] = v1.y;
+          }
+        }
+        if (is_k) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(&sN[i * kLd + 32 * half + j]) = make_float4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+        }
       }
+      // the factors and the T and P of the chunk before the last are read
       if (c >= 2) bad = bad || !wait(kSFree + bf, (c >> 1) - 1) || !wait(kDone + bf, (c >> 1) - 1);
-      if (named_bar_any(kPrepBar, 32 * kPrepWarps, bad)) break;
-      const float4 gi = sG[i];
-      const float rowf = is_k ? gi.z * gi.w : rq;
-#pragma unroll
-      for (int j = 0; j < kC; ++j) {
-        const float4 gj = sG[j];
-        const float e = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * gj.w * rowf * __uint_as_float(r[j]);
-        r[j] = __float_as_uint(is_k ? (j < i ? e : 0.f) : (j <= i ? e : 0.f));
-      }
-      const float4 gl4 = sG[kC - 1];
-      if (is_k) {
-#pragma unroll
-        for (int j = 0; j < kC; j += 4)
-          *reinterpret_cast<uint4*>(&sN[i * kLd + j]) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-        sF[bf].x[i] = -exp2_fast(gi.x + gi.y) * gi.w;
-        sF[bf].u[i] = exp2_fast((gl4.x - gi.x) + (gl4.y - gi.y)) * gi.w;
-        if (i == 0) sF[bf].last[0] = exp2_fast(gl4.x + gl4.y);
-      } else {
+      if (!above && !is_k) {
         unsigned char* pr = base + L::kP0 + bf * kTile + i * 128;
 #pragma unroll
-        for (int o = 0; o < 8; ++o) {
-          uint4 v;
-          v.x = pack2(__uint_as_float(r[8 * o]), __uint_as_float(r[8 * o + 1]));
-          v.y = pack2(__uint_as_float(r[8 * o + 2]), __uint_as_float(r[8 * o + 3]));
-          v.z = pack2(__uint_as_float(r[8 * o + 4]), __uint_as_float(r[8 * o + 5]));
-          v.w = pack2(__uint_as_float(r[8 * o + 6]), __uint_as_float(r[8 * o + 7]));
-          *reinterpret_cast<uint4*>(pr + ((o ^ (i & 7)) << 4)) = v;
-        }
-        sF[bf].y[i] = rq * exp2_fast(gi.x + gi.y);
+        for (int o = 0; o < 4; ++o)
+          *reinterpret_cast<uint4*>(pr + (((4 * half + o) ^ (i & 7)) << 4)) =
+              make_uint4(pack2(r[8 * o], r[8 * o + 1]), pack2(r[8 * o + 2], r[8 * o + 3]), pack2(r[8 * o + 4], r[8 * o + 5]),
+                         pack2(r[8 * o + 6], r[8 * o + 7]));
       }
-      named_bar_sync(kPrepBar, 32 * kPrepWarps);
-      // (I + N)^-1 in place: the diagonal blocks of 16, then twice the blocks below the diagonal,
-      // T_10 = -T_11 (N_10 T_00)
-      {
+      if (above) {  // the chunk's factors
+        const float4 gl = sG[kC - 1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int tok = lane + 32 * k;
+          const float2 g = tk.g[tok];
+          const float from_start = exp2_fast(g.x + g.y);
+          if (is_k) {
+            sF[bf].x[tok] = -from_start * tk.rk[tok];
+            sF[bf].u[tok] = exp2_fast((gl.x - g.x) + (gl.y - g.y)) * tk.rk[tok];
+            if (tok == kC - 1) sF[bf].last[0] = from_start;
+          } else {
+            sF[bf].y[tok] = from_start * a.scale * tk.rq[tok];
+          }
+        }
+      }
+      if (named_bar_any(kPrepBar, kPrep, bad)) break;
+      arrive(kGatesFree + bf);
+      // (I + N)^-1 in place: the diagonal blocks of 16, a column a lane, then twice the blocks below the
+      // diagonal, T_10 = -T_11 (N_10 T_00)
+      if (w < 4) {
         float x[16];
-        const int o = 16 * w, col = lane & 15;
+        const float* blk = &sN[16 * w * kLd + 16 * w];
+        const int col = lane & 15;
 #pragma unroll
         for (int rr = 0; rr < 16; ++rr) {
-          float v = rr == col ? 1.f : 0.f;
+          float v0 = rr == col ? 1.f : 0.f, v1 = 0.f;
 #pragma unroll
-          for (int k = 0; k < rr; ++k) v = fmaf(-sN[(o + rr) * kLd + o + k], x[k], v);
-          x[rr] = v;
+          for (int k = 0; k < rr; k += 4) {
+            const float4 e = *reinterpret_cast<const float4*>(&blk[rr * kLd + k]);
+            v0 = fmaf(-e.x, x[k], v0);
+            if (k + 1 < rr) v1 = fmaf(-e.y, x[k + 1], v1);
+            if (k + 2 < rr) v0 = fmaf(-e.z, x[k + 2], v0);
+            if (k + 3 < rr) v1 = fmaf(-e.w, x[k + 3], v1);
+          }
+          x[rr] = v0 + v1;
         }
         __syncwarp();
         if (lane < 16)
 #pragma unroll
-          for (int rr = 0; rr < 16; ++rr) sN[(o + rr) * kLd + o + col] = x[rr];
+          for (int rr = 0; rr < 16; ++rr) sN[(16 * w + rr) * kLd + 16 * w + col] = x[rr];
       }
-      named_bar_sync(kPrepBar, 32 * kPrepWarps);
+      named_bar_sync(kPrepBar, kPrep);
       {
-        const int o = (t >> 6) * 32, rr = (t & 63) >> 2, cc = (t & 3) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        const auto product = [&](const float* left, const float* right, int ld) {  // a row of left, four columns of right
-          v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int pair = t >> 7, o = pair * 32, rr = (t & 127) >> 3, cc = (t & 7) * 2;
+        const auto product = [&](const float* left, const float* right, int ld) {  // a row of left, two columns of right
+          float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float f = left[k];
-            const float4 e = *reinterpret_cast<const float4*>(right + k * ld);
-            v.x = fmaf(f, e.x, v.x), v.y = fmaf(f, e.y, v.y), v.z = fmaf(f, e.z, v.z), v.w = fmaf(f, e.w, v.w);
+          for (int k = 0; k < 16; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(left + k);
+            const float l[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v = __ffma2_rn(make_float2(l[j], l[j]), *reinterpret_cast<const float2*>(right + (k + j) * ld), v);
           }
+          return v;
         };
-        product(&sN[(o + 16 + rr) * kLd + o], &sN[o * kLd + o + cc], kLd);
-        *reinterpret_cast<float4*>(&sY[((t >> 6) * 16 + rr) * 36 + cc]) = v;
-        named_bar_sync(kPrepBar, 32 * kPrepWarps);
-        product(&sN[(o + 16 + rr) * kLd + o + 16], &sY[(t >> 6) * 16 * 36 + cc], 36);
-        *reinterpret_cast<float4*>(&sN[(o + 16 + rr) * kLd + o + cc]) = make_float4(-v.x, -v.y, -v.z, -v.w);
+        float2 v = product(&sN[(o + 16 + rr) * kLd + o], &sN[o * kLd + o + cc], kLd);
+        *reinterpret_cast<float2*>(&sY[(pair * 16 + rr) * kLdY + cc]) = v;
+        named_bar_sync(kPrepBar, kPrep);
+        v = product(&sN[(o + 16 + rr) * kLd + o + 16], &sY[pair * 16 * kLdY + cc], kLdY);
+        *reinterpret_cast<float2*>(&sN[(o + 16 + rr) * kLd + o + cc]) = make_float2(-v.x, -v.y);
       }
-      named_bar_sync(kPrepBar, 32 * kPrepWarps);
+      named_bar_sync(kPrepBar, kPrep);
       {
-        const int rr = (t >> 3) * 2, cc = (t & 7) * 4;
-        float2 v[2][2];
-        const auto product = [&](const float* left, const float* right, int ld) {  // two rows of left
-          v[0][0] = v[0][1] = v[1][0] = v[1][1] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 f0 = *reinterpret_cast<const float4*>(left + k), f1 = *reinterpret_cast<const float4*>(left + kLd + k);
-            const float l0[4] = {f0.x, f0.y, f0.z, f0.w}, l1[4] = {f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 e = *reinterpret_cast<const float4*>(right + (k + j) * ld);
-              const float2 e0 = make_float2(e.x, e.y), e1 = make_float2(e.z, e.w);
-              v[0][0] = __ffma2_rn(make_float2(l0[j], l0[j]), e0, v[0][0]);
-              v[0][1] = __ffma2_rn(make_float2(l0[j], l0[j]), e1, v[0][1]);
-              v[1][0] = __ffma2_rn(make_float2(l1[j], l1[j]), e0, v[1][0]);
-              v[1][1] = __ffma2_rn(make_float2(l1[j], l1[j]), e1, v[1][1]);
-            }
-          }
-        };
-        product(&sN[(32 + rr) * kLd], &sN[cc], kLd);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4*>(&sY[(rr + j) * 36 + cc]) = make_float4(v[j][0].x, v[j][0].y, v[j][1].x, v[j][1].y);
-        named_bar_sync(kPrepBar, 32 * kPrepWarps);
-        product(&sN[(32 + rr) * kLd + 32], &sY[cc], 36);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4*>(&sN[(32 + rr + j) * kLd + cc]) =
-              make_float4(-v[j][0].x, -v[j][0].y, -v[j][1].x, -v[j][1].y);
-      }
-      named_bar_sync(kPrepBar, 32 * kPrepWarps);
-      {  // T = inverse diag(beta), hi and lo
-        const int rr = t >> 1, half = t & 1;
-        unsigned char* th = base + L::kT0 + bf * 2 * kTile + rr * 128;
-#pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          uint32_t hi[4], lo[4];
+        // four columns of N_10 T_00, whose rows above those columns are 0, a row a lane
+        float2 v[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int k = 4 * w; k < 32; k += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sN[(32 + lane) * kLd + k]);
+          const float l[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int col = half * 32 + 8 * o + 2 * j;
-            split2(sN[rr * kLd + col] * sG[col].z, sN[rr * kLd + col + 1] * sG[col + 1].z, hi[j], lo[j]);
+            const float4 e = *reinterpret_cast<const float4*>(&sN[(k + j) * kLd + 4 * w]);
+            v[0] = __ffma2_rn(make_float2(l[j], l[j]), make_float2(e.x, e.y), v[0]);
+            v[1] = __ffma2_rn(make_float2(l[j], l[j]), make_float2(e.z, e.w), v[1]);
           }
-          const int at = ((half * 4 + o) ^ (rr & 7)) << 4;
+        }
+        *reinterpret_cast<float4*>(&sY[lane * kLdY + 4 * w]) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        named_bar_sync(kPrepBar, kPrep);
+        // four rows of T_11 times that, whose columns behind those rows are 0, a column a lane
+        const int r0 = 28 - 4 * w;
+        float u[4] = {};
+        for (int k = 0; k <= r0; k += 4) {
+          float y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = sY[(k + j) * kLdY + lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 f = *reinterpret_cast<const float4*>(&sN[(32 + r0 + j) * kLd + 32 + k]);
+            u[j] = fmaf(f.x, y[0], u[j]), u[j] = fmaf(f.y, y[1], u[j]);
+            u[j] = fmaf(f.z, y[2], u[j]), u[j] = fmaf(f.w, y[3], u[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sN[(32 + r0 + j) * kLd + lane] = -u[j];
+      }
+      named_bar_sync(kPrepBar, kPrep);
+      {  // T = inverse diag(beta), hi and lo
+        const int rr = t >> 2, c0 = (t & 3) * 16;
+        unsigned char* th = base + L::kT0 + bf * 2 * kTile + rr * 128;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int col = c0 + 8 * o + 4 * j;
+            const float4 e = *reinterpret_cast<const float4*>(&sN[rr * kLd + col]);
+            const float4 be = *reinterpret_cast<const float4*>(&tk.beta[col]);
+            split2(e.x * be.x, e.y * be.y, hi[2 * j], lo[2 * j]);
+            split2(e.z * be.z, e.w * be.w, hi[2 * j + 1], lo[2 * j + 1]);
+          }
+          const int at = (((t & 3) * 2 + o) ^ (rr & 7)) << 4;
           *reinterpret_cast<uint4*>(th + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(th + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_proxy_async_smem();
       arrive(kTReady + bf);
-      named_bar_sync(kPrepBar, 32 * kPrepWarps);  // sG and sN are read before the next chunk's
+      // (the next chunk's first barrier stands between these reads and its writes of tk's and N's places, but for rk and rq)
+    }
+  } else if (warp == kGateWarp) {
+    // ------------------------------ gates: two neighbouring tokens a lane ------------------------------------
+    const delta::Gate gate(a, h);
+    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt.ptr) + b * a.dt.batch_stride + h;
+    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta.ptr) + b * a.beta.batch_stride + h;
+    __nv_bfloat16 dt[2], be[2];
+    const auto load = [&](int c) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t tok = (int64_t)c * kC + 2 * lane + k;
+        dt[k] = be[k] = __float2bfloat16_rn(0.f);
+        if (tok < tokens) {
+          dt[k] = dp[tok * a.dt.token_stride];
+          be[k] = bp[tok * a.beta.token_stride];
+        }
+      }
+    };
+    load(0);
+    for (int c = 0; c < n; ++c) {
+      const int bf = c & 1;
+      float g[2], beta[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool in = (int64_t)c * kC + 2 * lane + k < tokens;
+        g[k] = in ? gate.log2_decay(__bfloat162float(dt[k])) : 0.f;
+        beta[k] = in ? gate.beta(__bfloat162float(be[k])) : 0.f;
+      }
+      load(c + 1);
+      float hi = g[0], lo = 0.f;  // of the lane's tokens, then of all up to them
+      add_exact(hi, lo, g[1], 0.f);
+      float sh = hi, sl = lo;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const float ph = __shfl_up_sync(0xffffffffu, sh, o), pl = __shfl_up_sync(0xffffffffu, sl, o);
+        if (lane >= o) add_exact(sh, sl, ph, pl);
+      }
+      float bh_ = __shfl_up_sync(0xffffffffu, sh, 1), bl = __shfl_up_sync(0xffffffffu, sl, 1);
+      if (lane == 0) bh_ = bl = 0.f;
+      if (c >= 2 && !wait(kGatesFree + bf, (c >> 1) - 1)) break;
+      float4* sG = reinterpret_cast<float4*>(base + L::kG0) + bf * kC;
+      add_exact(bh_, bl, g[0], 0.f);
+      sG[2 * lane] = make_float4(bh_, bl, beta[0], 0.f);
+      sG[2 * lane + 1] = make_float4(sh, sl, beta[1], 0.f);
+      arrive(kGates + bf);
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------ copies -------------------------------------------------------------------
@@ -549,9 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (lane == 0 && n > 0) {
     // ------------------------------ MMAs ---------------------------------------------------------------------
-    constexpr uint32_t id64 = tc::idesc_bf16_f32(128, 64, false, false);     // A, B K-major
-    constexpr uint32_t id64v = tc::idesc_bf16_f32(128, 64, true, false);     // A = V^T
-    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, DK, false, true);      // B = K, columns of the state as N
+    constexpr uint32_t id64 = tc::idesc_bf16_f32(128, 64, false, false);  // A, B K-major
+    constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 64, true, false);   // A = V^T
+    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 64, false, true);   // B = K, 64 columns of the state as N
     const uint32_t sb = smem_addr(base);
     const auto kq_at = [&](int c) { return sb + (c % kStages) * L::kStage; };
     // k-step ks of a K-major tile of 64-column blocks
@@ -579,22 +681,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int bf = c & 1;
       const uint32_t kt = kq_at(c), qt = kt + kTile, vt = kt + kHalves * 2 * kTile;
       const uint32_t th = sb + L::kT0 + bf * 2 * kTile, tl = th + kTile;
-      if (!(ok = wait_one(&bars[kSReady], (uint32_t)c & 1u))) break;
-      tc::fence_after_sync();
 #pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        const uint64_t d = k_major(kt, ks, 2 * kTile);
-        tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, id64, ks > 0);
-        tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, id64, true);
+      for (int x = 0; x < kHalves && ok; ++x) {  // (X takes the place of the first 64 columns of U, which are read by then)
+        if (!(ok = wait_one(&bars[kSReady + x], (uint32_t)c & 1u))) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int ks = 4 * x; ks < 4 * x + 4; ++ks) {
+          const uint64_t d = k_major(kt, ks, 2 * kTile);
+          tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, id64, ks > 0);
+          tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, id64, true);
+        }
       }
+      if (!ok) break;
       tc::mma_commit(&bars[kXFull]);
       if (!(ok = wait_one(&bars[kTReady + bf], (uint32_t)(c >> 1) & 1u))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
         const uint64_t v = tc::sdesc_sw128(vt + ks * 2048, kTile, 1024);
-        tc::mma_bf16(tmem + kColD, v, k_major(th, ks, 0), id64v, ks > 0);
-        tc::mma_bf16(tmem + kColD, v, k_major(tl, ks, 0), id64v, true);
+        tc::mma_bf16(tmem + kColD, v, k_major(th, ks, 0), id_v, ks > 0);
+        tc::mma_bf16(tmem + kColD, v, k_major(tl, ks, 0), id_v, true);
       }
       if (!(ok = wait_one(&bars[kXReady], (uint32_t)c & 1u))) break;
       tc::fence_after_sync();
@@ -614,24 +720,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_one(&bars[kDReady], (uint32_t)c & 1u))) break;
       tc::fence_after_sync();
 #pragma unroll
-      for (int ks = 0; ks < kC / 16; ++ks) {
-        const uint64_t d = tc::sdesc_sw128(kt + ks * 2048, 2 * kTile, 1024);
-        tc::mma_bf16_ts(tmem + kColU, tmem + kColOp + 8 * ks, d, id_u, ks > 0);
-        tc::mma_bf16_ts(tmem + kColU, tmem + kColOp + 32 + 8 * ks, d, id_u, true);
-      }
-      tc::mma_commit(&bars[kUFull]);
+      for (int x = 0; x < kHalves; ++x) {
 #pragma unroll
-      for (int ks = 0; ks < kC / 16; ++ks)
-        tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, k_major(sb + L::kP0 + bf * kTile, ks, 0), id64, ks > 0);
+        for (int ks = 0; ks < kC / 16; ++ks) {
+          const uint64_t d = tc::sdesc_sw128(kt + x * 2 * kTile + ks * 2048, 0, 1024);
+          tc::mma_bf16_ts(tmem + kColU + 64 * x, tmem + kColOp + 8 * ks, d, id_u, ks > 0);
+          tc::mma_bf16_ts(tmem + kColU + 64 * x, tmem + kColOp + 32 + 8 * ks, d, id_u, true);
+        }
+        tc::mma_commit(&bars[kUFull + x]);
+      }
+      if (!(ok = wait_one(&bars[kOReady], (uint32_t)c & 1u))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        const uint64_t d = k_major(sb + L::kP0 + bf * kTile, ks, 0);
+        tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, d, id64, ks > 0);
+        tc::mma_bf16_ts(tmem + kColO, tmem + kColDoLo + 8 * ks, d, id64, true);
+      }
       tc::mma_commit(&bars[kDone + bf]);
       tc::mma_commit(&bars[kEmpty + c % kStages]);
       // its place holds the operand of U until that is done
-      if (c + 2 < n) {
-        if (!wait_one(&bars[kUFull], (uint32_t)c & 1u) || !products_kq(c + 2)) {
-          ok = false;
-          ++c;
-          break;
-        }
+      if (c + 2 < n && (!wait_one(&bars[kUFull + kHalves - 1], (uint32_t)c & 1u) || !products_kq(c + 2))) {
+        ok = false;
+        ++c;
+        break;
       }
     }
     // Every MMA has completed, and no commit's arrival is still due.
@@ -642,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     drained(kKq, kqs);
     if (ok) drained(kXFull, c), drained(kDFull, c);
-    drained(kUFull, c);
+    for (int x = 0; x < kHalves; ++x) drained(kUFull + x, c);
     for (int x = 0; x < 2; ++x) drained(kDone + x, (c - x + 1) / 2);
     for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
   }
