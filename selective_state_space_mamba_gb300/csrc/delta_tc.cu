@@ -12,13 +12,12 @@
 //     D = V^T T^T + (X diag(-e^G)) T^T                 A = V^T (smem), then X (TMEM); B = T
 //     Q = S Q^T        A = S (TMEM), B = Q
 //     U = (D diag(e^(G_last - G))) K                   A = D (TMEM), B = K: S' = e^(G_last) S + U
-//     O = D P^T        A = D (TMEM), B = P
+//     O = Q diag(scale e^G) + D P^T    A = D (TMEM), B = P
 //     [K; Q] K^T       of the chunk after the next: what N and P are made of
 //
 // Rounding.  q, k and v are bf16 and enter as they are (lengths and decays are factors beside the products).  S is kept in f32
 // registers; as operands S, X, T and the D of the update are split into two bf16 halves (hi + lo, 2^-18 together; lo x lo is
-// left out), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P and D are rounded
-// once.
+// left out of U), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P is rounded once.
 //
 // Warps: 0-15 state (four threads a row, each a quarter of its columns), 16-23 prepare (lengths, N, its inverse, P), 24 copies,
 // 25 MMAs, 26 gates.  Every wait is bounded; after one that ran out the CTA's outputs are NaN.
@@ -43,13 +42,15 @@ constexpr int kLd = 68;            // floats of a row of N: rows four banks apar
 constexpr int kLdY = 36;
 constexpr uint32_t kPrepBar = 1;
 
-// TMEM columns
-constexpr uint32_t kColHi = 0, kColLo = 64;   // S, two columns of the state each
-constexpr uint32_t kColU = 128;               // U over X and D
-constexpr uint32_t kColX = 128, kColD = 192;
-constexpr uint32_t kColOp = 256;              // X, then D of the update: hi, lo; between them [K; Q] K^T
-constexpr uint32_t kColDo = 320, kColDoLo = 480;  // D of the output
-constexpr uint32_t kColQ = 352, kColO = 416;
+// TMEM columns.  S as an operand (hi, lo) is dead once X and Q are there: X, then D of the update, as operands take its place.
+// D comes in two halves, from the inverse's hi and lo; U takes their place.
+constexpr uint32_t kColHi = 0, kColLo = 64;
+constexpr uint32_t kColOp = 0, kColOpLo = 32;
+constexpr uint32_t kColX = 128, kColQ = 192;
+constexpr uint32_t kColD = 256, kColDlo = 320, kColU = 256;
+constexpr uint32_t kColDo = 384, kColDoLo = 416;  // D of the output; between them [K; Q] K^T
+constexpr uint32_t kColKq = 384;
+constexpr uint32_t kColO = 448;
 constexpr uint32_t kTmemCols = 512;
 
 enum Bar {
@@ -60,10 +61,8 @@ enum Bar {
   kGatesFree = kGates + 2,
   kTReady = kGatesFree + 2,   // T, P and the factors of a chunk
   kDone = kTReady + 2,        // its last product
-  kSFree = kDone + 2,         // its factors are read
-  kSReady = kSFree + 2,       // S as an operand, 64 of its columns each
-  kUFull = kSReady + 2,       // U, likewise
-  kKq = kUFull + 2, kKqFree, kXFull, kXReady, kDFull, kDReady, kOReady, kLast, kNumBars
+  kSReady = kDone + 2,        // S as an operand, 64 of its columns each
+  kKq = kSReady + 2, kKqFree, kUFull, kXFull, kXReady, kDFull, kDReady, kOReady, kLast, kNumBars
 };
 
 struct Factors {  // of a chunk
@@ -106,8 +105,22 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   hi = pack2(a, b);
   float ha, hb;
   unpack2(hi, ha, hb);
-  const float2 r = __fadd2_rn(make_float2(a, b), make_float2(-ha, -hb));
+  const float2 r = __ffma2_rn(make_float2(ha, hb), make_float2(-1.f, -1.f), make_float2(a, b));
   lo = pack2(r.x, r.y);
+}
+
+// The bits of v in bf16
+__device__ __forceinline__ uint16_t bf16_of(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// mbar_try_wait that may park the warp for up to 20 us.
+__device__ __forceinline__ bool try_wait_parked(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
 }
 
 // a + b as hi + lo
@@ -150,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kReady, kStages, kPrepWarps);
     init(kGates, 2, 1), init(kGatesFree, 2, kPrepWarps), init(kTReady, 2, kPrepWarps), init(kDone, 2, 1);
-    init(kSFree, 2, kStateWarps), init(kSReady, 2, kStateWarps / kHalves), init(kUFull, 2, 1), init(kKq, 1, 1);
+    init(kSReady, 2, kStateWarps / kHalves), init(kUFull, 1, 1), init(kKq, 1, 1);
     init(kKqFree, 1, kPrepWarps - 2), init(kXFull, 1, 1), init(kXReady, 1, kStateWarps), init(kDFull, 1, 1);
     init(kDReady, 1, kStateWarps), init(kOReady, 1, kStateWarps), init(kLast, 1, 1);
     *abort_flag = 0;
@@ -180,9 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // A bounded wait, the same answer in every lane of a warp
   const auto wait_one = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait_parked(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!try_wait_parked(bar, parity)) {
       if (*abort_flag || global_timer_ns() - t0 > p.ctl.spin_limit_ns) {
         *abort_flag = 1;
         return false;
@@ -204,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int TW = kC / kParts;  // tokens of X, D and y a thread
     const int quad = warp & 3, part = warp >> 2, row = quad * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
-    const int u_half = DK == 128 ? part >> 1 : 0;
+    const int s_half = DK == 128 ? part >> 1 : 0;
     const bool have = row < rows;
     const int64_t at = ((bh * a.headdim + m0 + row) * DK) + part * CW;
     float s[CW];
@@ -234,45 +247,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto output = [&](int c) -> bool {
       if (!wait(kDone + (c & 1), c >> 1)) return false;
       tc::fence_after_sync();
-      const float* f = sF[c & 1].y + part * TW;
-      const int64_t t0 = (int64_t)c * kC + part * TW;
-      const int m = (int)min((int64_t)TW, tokens - t0);
-      __nv_bfloat16* yc = yp + t0 * y_stride;
-      uint32_t sq[16], od[16];
-      tc::tmem_ld16(tm + kColQ + part * TW, sq);
-      tc::tmem_ld16(tm + kColO + part * TW, od);
+      uint32_t o[TW];
+      tc::tmem_ld16(tm + kColO + part * TW, o);
       tc::tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < TW; j += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(f + j);
-        const float2 v0 = __ffma2_rn(make_float2(__uint_as_float(sq[j]), __uint_as_float(sq[j + 1])), make_float2(w.x, w.y),
-                                     make_float2(__uint_as_float(od[j]), __uint_as_float(od[j + 1])));
-        const float2 v1 =
-            __ffma2_rn(make_float2(__uint_as_float(sq[j + 2]), __uint_as_float(sq[j + 3])), make_float2(w.z, w.w),
-                       make_float2(__uint_as_float(od[j + 2]), __uint_as_float(od[j + 3])));
-        sq[j / 2] = pack2(v0.x, v0.y), sq[j / 2 + 1] = pack2(v1.x, v1.y);
-      }
       tc::fence_before_sync();
-      arrive(kSFree + (c & 1));
-      if (have) {
-        uint16_t* yo = reinterpret_cast<uint16_t*>(yc);
-        if (m == TW) {
+      const int64_t t0 = (int64_t)c * kC + part * TW;
+      const int m = have ? (int)min((int64_t)TW, tokens - t0) : 0;
+      uint16_t* yo = reinterpret_cast<uint16_t*>(yp + t0 * y_stride);
+      if (m == TW) {
 #pragma unroll
-          for (int j = 0; j < TW; ++j, yo += y_stride) *yo = (uint16_t)(sq[j / 2] >> (16 * (j & 1)));
-        } else {
+        for (int j = 0; j < TW; ++j, yo += y_stride) *yo = bf16_of(__uint_as_float(o[j]));
+      } else {
 #pragma unroll
-          for (int j = 0; j < TW; ++j, yo += y_stride)
-            if (j < m) *yo = (uint16_t)(sq[j / 2] >> (16 * (j & 1)));
-        }
+        for (int j = 0; j < TW; ++j, yo += y_stride)
+          if (j < m) *yo = bf16_of(__uint_as_float(o[j]));
       }
       return true;
+    };
+    // a part's 16 values, scaled, as an operand
+    const auto operand = [&](const uint32_t (&r)[16], const float* f, uint32_t hi_at, uint32_t lo_at) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(f + 2 * j);
+        const float2 v0 = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), make_float2(w.x, w.y));
+        const float2 v1 =
+            __fmul2_rn(make_float2(__uint_as_float(r[2 * j + 2]), __uint_as_float(r[2 * j + 3])), make_float2(w.z, w.w));
+        split2(v0.x, v0.y, hi[j], lo[j]);
+        split2(v1.x, v1.y, hi[j + 1], lo[j + 1]);
+      }
+      tc::tmem_st8(tm + hi_at + part * TW / 2, hi);
+      tc::tmem_st8(tm + lo_at + part * TW / 2, lo);
     };
 
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
       const int bf = c & 1;
       if (c > 0) {
-        ok = wait(kUFull + u_half, c - 1);
+        ok = wait(kUFull, c - 1);
         tc::fence_after_sync();
       }
 #pragma unroll
@@ -286,54 +298,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::tmem_st_wait();
       tc::fence_before_sync();
-      arrive(kSReady + u_half);
+      arrive(kSReady + s_half);
       if (c > 0) ok = ok && output(c - 1);
       const Factors& f = sF[bf];
-      // X, scaled, as an operand; its place may still hold [K; Q] K^T of the next chunk
-      ok = ok && wait(kTReady + bf, c >> 1) && (c + 1 >= n || wait(kKqFree, c + 1)) && wait(kXFull, c);
+      // X, scaled, as an operand
+      ok = ok && wait(kTReady + bf, c >> 1) && wait(kXFull, c);
       if (!ok) break;
       tc::fence_after_sync();
-      uint32_t r[16], hi[8], lo[8];
+      uint32_t r[16];
       tc::tmem_ld16(tm + kColX + part * TW, r);
       tc::tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 w = *reinterpret_cast<const float2*>(&f.x[part * TW + 2 * j]);
-        const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), w);
-        split2(v.x, v.y, hi[j], lo[j]);
-      }
-      tc::tmem_st8(tm + kColOp + part * TW / 2, hi);
-      tc::tmem_st8(tm + kColOp + 32 + part * TW / 2, lo);
+      operand(r, f.x + part * TW, kColOp, kColOpLo);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kXReady);
-      // D: scaled for the update, then as it is for the output
+      // D scaled as an operand of the update
       if (!(ok = wait(kDFull, c))) break;
       tc::fence_after_sync();
-      tc::tmem_ld16(tm + kColD + part * TW, r);
-      tc::tmem_ld_wait();
+      {
+        uint32_t e[16];
+        tc::tmem_ld16(tm + kColD + part * TW, r);
+        tc::tmem_ld16(tm + kColDlo + part * TW, e);
+        tc::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 w = *reinterpret_cast<const float2*>(&f.u[part * TW + 2 * j]);
-        const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), w);
-        split2(v.x, v.y, hi[j], lo[j]);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 v = __fadd2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                      make_float2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])));
+          r[j] = __float_as_uint(v.x), r[j + 1] = __float_as_uint(v.y);
+        }
       }
+      operand(r, f.u + part * TW, kColOp, kColOpLo);
       last = f.last[0];
-      tc::tmem_st8(tm + kColOp + part * TW / 2, hi);
-      tc::tmem_st8(tm + kColOp + 32 + part * TW / 2, lo);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kDReady);
+      // D as it is, and Q scaled as what O adds to; the place of D may still hold [K; Q] K^T of the chunk after the next
+      if (c + 2 < n && !(ok = wait(kKqFree, c + 2))) break;
+      tc::fence_after_sync();
+      {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) split2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), hi[j], lo[j]);
-      tc::tmem_st8(tm + kColDo + part * TW / 2, hi);
-      tc::tmem_st8(tm + kColDoLo + part * TW / 2, lo);
+        for (int j = 0; j < 8; ++j) split2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), hi[j], lo[j]);
+        tc::tmem_st8(tm + kColDo + part * TW / 2, hi);
+        tc::tmem_st8(tm + kColDoLo + part * TW / 2, lo);
+      }
+      tc::tmem_ld16(tm + kColQ + part * TW, r);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(&f.y[part * TW + j]);
+        r[j] = __float_as_uint(__uint_as_float(r[j]) * w.x), r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * w.y);
+        r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * w.z), r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * w.w);
+      }
+      tc::tmem_st16(tm + kColO + part * TW, r);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kOReady);
     }
     if (n > 0 && ok) {
-      ok = wait(kUFull + u_half, n - 1);
+      ok = wait(kUFull, n - 1);
       tc::fence_after_sync();
 #pragma unroll
       for (int q = 0; q < CW / 16; ++q) update(q);
@@ -415,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float r[32];
       if (!above) {
         uint32_t e[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kColOp + 32 * half, e);
+        tc::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kColKq + 32 * half, e);
         tc::tmem_ld_wait();
         tc::fence_before_sync();
         arrive(kKqFree);
@@ -451,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the factors and the T and P of the chunk before the last are read
-      if (c >= 2) bad = bad || !wait(kSFree + bf, (c >> 1) - 1) || !wait(kDone + bf, (c >> 1) - 1);
+      if (c >= 2) bad = bad || !wait(kDone + bf, (c >> 1) - 1);
       if (!above && !is_k) {
         unsigned char* pr = base + L::kP0 + bf * kTile + i * 128;
 #pragma unroll
@@ -527,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         // four columns of N_10 T_00, whose rows above those columns are 0, a row a lane
         float2 v[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 4
         for (int k = 4 * w; k < 32; k += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&sN[(32 + lane) * kLd + k]);
           const float l[4] = {f.x, f.y, f.z, f.w};
@@ -542,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // four rows of T_11 times that, whose columns behind those rows are 0, a column a lane
         const int r0 = 28 - 4 * w;
         float u[4] = {};
+#pragma unroll 4
         for (int k = 0; k <= r0; k += 4) {
           float y[4];
 #pragma unroll
@@ -651,9 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (lane == 0 && n > 0) {
     // ------------------------------ MMAs ---------------------------------------------------------------------
+    // Products with 64 columns take as long as those with 128 (64 cycles a step of 16), so what shares an A goes in one:
+    // K with Q, the inverse's hi with its lo.
     constexpr uint32_t id64 = tc::idesc_bf16_f32(128, 64, false, false);  // A, B K-major
-    constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 64, true, false);   // A = V^T
-    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 64, false, true);   // B = K, 64 columns of the state as N
+    constexpr uint32_t id128 = tc::idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 128, true, false);  // A = V^T
+    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, DK, false, true);   // B = K, columns of the state as N
     const uint32_t sb = smem_addr(base);
     const auto kq_at = [&](int c) { return sb + (c % kStages) * L::kStage; };
     // k-step ks of a K-major tile of 64-column blocks
@@ -669,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {
         const uint64_t d = k_major(at, ks, 2 * kTile);
-        tc::mma_bf16(tmem + kColOp, d, d, id64, ks > 0);
+        tc::mma_bf16(tmem + kColKq, d, d, id64, ks > 0);
       }
       tc::mma_commit(&bars[kKq]);
       kqs = c + 1;
@@ -679,17 +707,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int c = 0;  // chunks whose last commit was made
     for (; c < n && ok; ++c) {
       const int bf = c & 1;
-      const uint32_t kt = kq_at(c), qt = kt + kTile, vt = kt + kHalves * 2 * kTile;
-      const uint32_t th = sb + L::kT0 + bf * 2 * kTile, tl = th + kTile;
+      const uint32_t kt = kq_at(c), vt = kt + kHalves * 2 * kTile, th = sb + L::kT0 + bf * 2 * kTile;
 #pragma unroll
-      for (int x = 0; x < kHalves && ok; ++x) {  // (X takes the place of the first 64 columns of U, which are read by then)
+      for (int x = 0; x < kHalves && ok; ++x) {
         if (!(ok = wait_one(&bars[kSReady + x], (uint32_t)c & 1u))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int ks = 4 * x; ks < 4 * x + 4; ++ks) {
           const uint64_t d = k_major(kt, ks, 2 * kTile);
-          tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, id64, ks > 0);
-          tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, id64, true);
+          tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, id128, ks > 0);
+          tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, id128, true);
         }
       }
       if (!ok) break;
@@ -697,54 +724,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_one(&bars[kTReady + bf], (uint32_t)(c >> 1) & 1u))) break;
       tc::fence_after_sync();
 #pragma unroll
-      for (int ks = 0; ks < kC / 16; ++ks) {
-        const uint64_t v = tc::sdesc_sw128(vt + ks * 2048, kTile, 1024);
-        tc::mma_bf16(tmem + kColD, v, k_major(th, ks, 0), id_v, ks > 0);
-        tc::mma_bf16(tmem + kColD, v, k_major(tl, ks, 0), id_v, true);
-      }
+      for (int ks = 0; ks < kC / 16; ++ks)
+        tc::mma_bf16(tmem + kColD, tc::sdesc_sw128(vt + ks * 2048, kTile, 1024), k_major(th, ks, 0), id_v, ks > 0);
       if (!(ok = wait_one(&bars[kXReady], (uint32_t)c & 1u))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id64, true);
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(tl, ks, 0), id64, true);
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 32 + 8 * ks, k_major(th, ks, 0), id64, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id128, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOpLo + 8 * ks, k_major(th, ks, 0), id128, true);
       }
       tc::mma_commit(&bars[kDFull]);
-#pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        const uint64_t d = k_major(qt, ks, 2 * kTile);
-        tc::mma_bf16_ts(tmem + kColQ, tmem + kColHi + 8 * ks, d, id64, ks > 0);
-        tc::mma_bf16_ts(tmem + kColQ, tmem + kColLo + 8 * ks, d, id64, true);
-      }
+      if (c + 2 < n && !(ok = products_kq(c + 2))) break;  // (beside the state warps' work on D)
       if (!(ok = wait_one(&bars[kDReady], (uint32_t)c & 1u))) break;
       tc::fence_after_sync();
 #pragma unroll
-      for (int x = 0; x < kHalves; ++x) {
-#pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks) {
-          const uint64_t d = tc::sdesc_sw128(kt + x * 2 * kTile + ks * 2048, 0, 1024);
-          tc::mma_bf16_ts(tmem + kColU + 64 * x, tmem + kColOp + 8 * ks, d, id_u, ks > 0);
-          tc::mma_bf16_ts(tmem + kColU + 64 * x, tmem + kColOp + 32 + 8 * ks, d, id_u, true);
-        }
-        tc::mma_commit(&bars[kUFull + x]);
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        const uint64_t d = tc::sdesc_sw128(kt + ks * 2048, 2 * kTile, 1024);
+        tc::mma_bf16_ts(tmem + kColU, tmem + kColOp + 8 * ks, d, id_u, ks > 0);
+        tc::mma_bf16_ts(tmem + kColU, tmem + kColOpLo + 8 * ks, d, id_u, true);
       }
+      tc::mma_commit(&bars[kUFull]);
       if (!(ok = wait_one(&bars[kOReady], (uint32_t)c & 1u))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
         const uint64_t d = k_major(sb + L::kP0 + bf * kTile, ks, 0);
-        tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, d, id64, ks > 0);
+        tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, d, id64, true);
         tc::mma_bf16_ts(tmem + kColO, tmem + kColDoLo + 8 * ks, d, id64, true);
       }
       tc::mma_commit(&bars[kDone + bf]);
       tc::mma_commit(&bars[kEmpty + c % kStages]);
-      // its place holds the operand of U until that is done
-      if (c + 2 < n && (!wait_one(&bars[kUFull + kHalves - 1], (uint32_t)c & 1u) || !products_kq(c + 2))) {
-        ok = false;
-        ++c;
-        break;
-      }
     }
     // Every MMA has completed, and no commit's arrival is still due.
     tc::mma_commit(&bars[kLast]);
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     drained(kKq, kqs);
     if (ok) drained(kXFull, c), drained(kDFull, c);
-    for (int x = 0; x < kHalves; ++x) drained(kUFull + x, c);
+    drained(kUFull, c);
     for (int x = 0; x < 2; ++x) drained(kDone + x, (c - x + 1) / 2);
     for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
   }
