@@ -388,7 +388,14 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
  * States and sums are f32; a decay below 2^-150 is 0.
  * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing nheads, dstate in {32, 64, 128}, headdim >= 1,
  * nheads * headdim and ngroups * dstate <= 2^30.
- * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_CUDA.
+ * bf16 prompts of at least 16 tokens, with dstate 64 or 128 and headdim a multiple of 8, whose q, k and v have rows on 16-byte
+ * boundaries, go through the tensor cores in chunks of 64 tokens (one kernel for what does not depend on the
+ * state, one for the chain of states); the others go token by token.  In chunks, a NaN or an infinity in a token may
+ * reach the outputs of the up to 63 tokens before it in its chunk.
+ * Workspace (0 bytes where the sizes need none): 25,600 bytes for each head and chunk, of long prompts for a segment at a
+ * time.  It need not be zero-filled and carries nothing from call to call; a call that uses it clears the status word
+ * and ssm_check_device_status reports its waits (bounded: after one that ran out y and h_final are NaN from there on).
+ * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_WORKSPACE, SSM_ERR_CUDA.
  */
 typedef struct {
     ssm_tokens q, k, v, dt, beta;
@@ -403,7 +410,9 @@ typedef struct {
     int32_t dtype; /* ssm_dtype */
     int32_t reserved; /* 0 */
 } ssm_delta_args;
-SSM_API ssm_status ssm_delta_fwd(const ssm_delta_args *args, ssm_stream_t stream);
+SSM_API size_t ssm_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim, int dstate, int ngroups,
+                                             ssm_dtype dtype);
+SSM_API ssm_status ssm_delta_fwd(const ssm_delta_args *args, void *workspace, size_t workspace_bytes, ssm_stream_t stream);
 
 /*
  * The same for ONE new token per sequence, over the f32 states [nslots, nheads, headdim, dstate]:
@@ -568,6 +577,8 @@ SSM_API ssm_status ssm_check_device_status(void *workspace, ssm_stream_t stream)
  * SSM_ERR_TIMEOUT in the status word and return; no kernel waits without a limit.
  * In ssm_selscan_fwd the index is an item's: of its queue, or without one the CTA's; at
  * 2^40 + its index the item's copies give up instead.
+ * In ssm_delta_fwd through the tensor cores the index is a CTA's of the kernel that prepares the chunks (it gives up); at
+ * 2^40 + its index a CTA of the chain's kernel makes no copies, so that its waits run out.
  */
 SSM_API void ssm_debug_set_lookback_fault(int64_t stall_tile, uint64_t spin_limit_ns);
 
@@ -627,10 +638,10 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
  * kernel of the one-kernel state pass with split chains), 9 conv (ssm_conv_fwd), 10 conv_step,
  * 11 selscan_piece (the first kernel of ssm_selscan_fwd with a split time axis), 12 selscan
  * (ssm_selscan_fwd), 13 selscan_step, 14 rmsnorm (both forms), 15 delta (ssm_delta_fwd, token by token), 16 delta_step,
- * 17 gatednorm, 18 blocknorm, 19 delta_tc (ssm_delta_fwd on the tensor cores).  Host-side only;
+ * 17 gatednorm, 18 blocknorm, 19 delta_prepare and 20 delta_chain (ssm_delta_fwd on the tensor cores).  Host-side only;
  * process-global; not thread-safe.
  */
-#define SSM_PROFILE_KERNELS 20
+#define SSM_PROFILE_KERNELS 21
 #define SSM_PROFILE_END_KERNELS 9
 SSM_API ssm_status ssm_profile_begin(int max_launches);
 SSM_API ssm_status ssm_profile_end(double *ms_out, int64_t *launches_out);

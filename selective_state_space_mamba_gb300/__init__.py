@@ -28,12 +28,12 @@ __all__ = ["ssd_fwd", "ssd_step", "linscan_fwd", "linscan_baseline", "tune_ssd_f
            "get_ssd_fwd_plan", "clear_ssd_fwd_plans", "plan_id", "tune_linscan_fwd",
            "set_linscan_shape", "get_linscan_shape", "clear_linscan_shapes", "Workspace", "check_device_status", "ssd_fwd_workspace_bytes",
            "linscan_workspace_bytes", "conv_fwd", "conv_step", "selscan_fwd", "selscan_step",
-           "selscan_fwd_workspace_bytes", "rmsnorm_fwd", "rmsnorm_fp8_fwd", "delta_fwd", "delta_step", "gatednorm_fwd",
+           "selscan_fwd_workspace_bytes", "rmsnorm_fwd", "rmsnorm_fp8_fwd", "delta_fwd", "delta_fwd_workspace_bytes", "delta_step", "gatednorm_fwd",
            "blocknorm_fwd", "SsmError", "version"]
 
 
 _LAYER = ("conv_fwd", "conv_step", "selscan_fwd", "selscan_step", "selscan_fwd_workspace_bytes", "rmsnorm_fwd",
-          "rmsnorm_fp8_fwd", "delta_fwd", "delta_step", "gatednorm_fwd", "blocknorm_fwd")
+          "rmsnorm_fp8_fwd", "delta_fwd", "delta_fwd_workspace_bytes", "delta_step", "gatednorm_fwd", "blocknorm_fwd")
 
 
 def __getattr__(name):

@@ -18,7 +18,7 @@ import torch  # noqa: F401 - _binding needs its libraries loaded
 from . import _build, _lib
 
 _BOUND = ("ssm_conv_fwd", "ssm_conv_step", "ssm_selscan_fwd_workspace_bytes", "ssm_selscan_fwd", "ssm_selscan_step",
-          "ssm_rmsnorm_fwd", "ssm_rmsnorm_fp8_fwd", "ssm_delta_fwd", "ssm_delta_step", "ssm_gatednorm_fwd",
+          "ssm_rmsnorm_fwd", "ssm_rmsnorm_fp8_fwd", "ssm_delta_fwd_workspace_bytes", "ssm_delta_fwd", "ssm_delta_step", "ssm_gatednorm_fwd",
           "ssm_blocknorm_fwd")
 _native = None
 
@@ -137,8 +137,17 @@ def rmsnorm_fp8_fwd(x, weight, residual=None, *, eps: float = 1e-5, group: int =
     return _checked(r, "ssm_rmsnorm_fp8_fwd")
 
 
+def delta_fwd_workspace_bytes(batch, seqlen, nheads, headdim, dstate, ngroups=1, *, dtype=torch.bfloat16) -> int:
+    """Device memory that delta_fwd needs besides its tensors (0 where it needs none, or refuses the sizes)."""
+    if max(nheads, headdim, dstate, ngroups) >> 31 or max(batch, seqlen) >> 63:
+        return 0  # ctypes would hand on what is left of them in 32 or 64 bits
+    code = _lib.SSM_BF16 if dtype == torch.bfloat16 else _lib.SSM_F32
+    return int(_lib.load().ssm_delta_fwd_workspace_bytes(batch, seqlen, nheads, headdim, dstate, ngroups, code))
+
+
 def delta_fwd(q, k, v, dt, beta, A, dt_bias=None, h0=None, lens=None, *, scale=None, softplus: bool = True,
-              sigmoid: bool = True, l2norm: bool = True, y=None, h_final=None, return_final_state: bool = True):
+              sigmoid: bool = True, l2norm: bool = True, y=None, h_final=None, return_final_state: bool = True,
+              workspace=None):
     """Gated delta rule over a prompt (ssm_delta_fwd).
 
     q, k [b, L, G, N], v [b, L, nh, H], dt, beta [b, L, nh] (all float32 or all bfloat16; strided in all but
@@ -147,9 +156,15 @@ def delta_fwd(q, k, v, dt, beta, A, dt_bias=None, h0=None, lens=None, *, scale=N
     group h // (nh / G).  scale: None for N ** -0.5.  Without softplus the decay is exp(A (dt + dt_bias)), without
     sigmoid beta is taken as it is, without l2norm q and k are.  Returns (y, h_final): y [b, L, nh, H], 0 in
     the padding, and the float32 state after the last token (None when return_final_state is False).
+    Without a workspace (Workspace), one is allocated for the call where it is needed; with one,
+    check_device_status(workspace) tells whether a wait inside the last call that needed it ran out.
     """
+    buf = None
+    if workspace is not None:
+        (b, L, nh, H), (G, N) = v.shape, q.shape[-2:]
+        buf = workspace.ensure(delta_fwd_workspace_bytes(b, L, nh, H, N, G, dtype=v.dtype))
     r = (_native or _load()).delta_fwd(q, k, v, dt, beta, A, dt_bias, h0, lens, scale, softplus, sigmoid, l2norm, y, h_final,
-                                       return_final_state)
+                                       return_final_state, buf)
     return _checked(r, "ssm_delta_fwd")
 
 

@@ -27,11 +27,11 @@ EXPORTS = ("ssm_status_string", "ssm_version", "ssm_ssd_fwd_workspace_bytes", "s
            "ssm_debug_build", "ssm_debug_set_bounds_fault", "ssm_linscan_fwd_tune", "ssm_linscan_set_shape",
            "ssm_linscan_get_shape", "ssm_linscan_clear_shapes", "ssm_conv_fwd", "ssm_conv_step",
            "ssm_selscan_fwd_workspace_bytes", "ssm_selscan_fwd", "ssm_selscan_step", "ssm_rmsnorm_fwd",
-           "ssm_rmsnorm_fp8_fwd", "ssm_delta_fwd", "ssm_delta_step", "ssm_gatednorm_fwd", "ssm_blocknorm_fwd")
+           "ssm_rmsnorm_fp8_fwd", "ssm_delta_fwd_workspace_bytes", "ssm_delta_fwd", "ssm_delta_step", "ssm_gatednorm_fwd", "ssm_blocknorm_fwd")
 PROFILE_KERNELS = ("linscan_lookback", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",
                    "ssd_state_fused", "ssd_step", "linscan_baseline", "ssd_state_fixup", "conv", "conv_step",
                    "selscan_piece", "selscan", "selscan_step", "rmsnorm")
-PROFILE_KERNELS_MORE = ("delta", "delta_step", "gatednorm", "blocknorm", "delta_tc")  # the ids after those
+PROFILE_KERNELS_MORE = ("delta", "delta_step", "gatednorm", "blocknorm", "delta_prepare", "delta_chain")  # the ids after those
 SSM_ACT_NONE, SSM_ACT_SILU = 0, 1
 
 
@@ -133,7 +133,9 @@ def _declare(lib):
     lib.ssm_rmsnorm_fwd.restype = i32
     lib.ssm_rmsnorm_fp8_fwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, i32, vp]
     lib.ssm_rmsnorm_fp8_fwd.restype = i32
-    lib.ssm_delta_fwd.argtypes = [ctypes.POINTER(SsmDeltaArgs), vp]
+    lib.ssm_delta_fwd_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i32, i32]
+    lib.ssm_delta_fwd_workspace_bytes.restype = sz
+    lib.ssm_delta_fwd.argtypes = [ctypes.POINTER(SsmDeltaArgs), vp, sz, vp]
     lib.ssm_delta_fwd.restype = i32
     lib.ssm_delta_step.argtypes = [ctypes.POINTER(SsmDeltaArgs), vp, i64, vp]
     lib.ssm_delta_step.restype = i32

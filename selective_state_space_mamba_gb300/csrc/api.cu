@@ -849,7 +849,16 @@ ssm_status ssm_rmsnorm_fp8_fwd(const void* x, int64_t x_stride, const float* wei
                  res_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
-ssm_status ssm_delta_fwd(const ssm_delta_args* args, ssm_stream_t stream) {
+size_t ssm_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim, int dstate, int ngroups,
+                                     ssm_dtype dtype) {
+  ssm_delta_args a{};
+  a.batch = batch, a.seqlen = seqlen, a.nheads = nheads, a.headdim = headdim, a.dstate = dstate, a.ngroups = ngroups;
+  a.dtype = dtype;
+  if (batch < 1 || check_delta_sizes(a) != SSM_OK || !delta_tc_sizes(a)) return 0;
+  return delta_tc_workspace(a);
+}
+
+ssm_status ssm_delta_fwd(const ssm_delta_args* args, void* workspace, size_t workspace_bytes, ssm_stream_t stream) {
   if (!args) return SSM_ERR_INVALID_ARG;
   const ssm_delta_args& a = *args;
   ssm_status st = check_delta_sizes(a);
@@ -866,8 +875,21 @@ ssm_status ssm_delta_fwd(const ssm_delta_args* args, ssm_stream_t stream) {
   out.dense(a.h_final, 4, {a.batch, a.nheads, a.headdim, a.dstate});
   if ((st = check_spans(in, out)) != SSM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (a.seqlen >= 16 && delta_tc_supported(a))
-    return launch_status(19, s, [&] { return launch_delta_tc(a, next_lookback_ctl(), s); });
+  if (delta_tc_sizes(a)) {
+    if (!workspace || workspace_bytes < delta_tc_workspace(a)) return SSM_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SSM_ERR_ALIGNMENT;
+    if (delta_tc_supported(a)) {
+      try {
+        if (launch_delta_tc(a, workspace, next_lookback_ctl(), s,
+                            [&](int kernel, const std::function<cudaError_t()>& f) { return timed_launch(kernel, s, f); }) ==
+            cudaSuccess)
+          return SSM_OK;
+      } catch (...) {
+      }
+      (void)cudaGetLastError();
+      return SSM_ERR_CUDA;
+    }
+  }
   return launch_status(15, s, [&] { return launch_delta(a, s); });
 }
 

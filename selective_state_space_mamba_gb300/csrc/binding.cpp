@@ -28,6 +28,7 @@ struct {
   decltype(&ssm_selscan_step) selscan_step;
   decltype(&ssm_rmsnorm_fwd) rmsnorm_fwd;
   decltype(&ssm_rmsnorm_fp8_fwd) rmsnorm_fp8_fwd;
+  decltype(&ssm_delta_fwd_workspace_bytes) delta_fwd_workspace_bytes;
   decltype(&ssm_delta_fwd) delta_fwd;
   decltype(&ssm_delta_step) delta_step;
   decltype(&ssm_gatednorm_fwd) gatednorm_fwd;
@@ -430,7 +431,7 @@ ssm_delta_args delta_args(PyObject* const* v, const Like& like, const at::Tensor
   return a;
 }
 
-// q, k, v, dt, beta, A, dt_bias, h0, lens, scale, softplus, sigmoid, l2norm, y, h_final, return_final_state
+// q, k, v, dt, beta, A, dt_bias, h0, lens, scale, softplus, sigmoid, l2norm, y, h_final, return_final_state, workspace buffer
 PyObject* delta_fwd(PyObject* const* v) {
   const at::Tensor& q = tensor("q", v[0]);
   const Like like("q", q);
@@ -446,7 +447,19 @@ PyObject* delta_fwd(PyObject* const* v) {
   a.y = y.ptr;
   if (truth(v[15])) h.set("h_final", v[14], state, at::kFloat, like);
   a.h_final = static_cast<float*>(h.ptr);
-  return result(g_fn.delta_fwd(&a, like.stream()), y, h);
+  at::Tensor ws;
+  if (v[16] != Py_None) {
+    ws = tensor("workspace", v[16]);
+    if (ws.device() != like.device || ws.scalar_type() != at::kByte || !ws.is_contiguous())
+      fail("workspace", "contiguous bytes on q's device");
+  } else {
+    const size_t need =
+        g_fn.delta_fwd_workspace_bytes(a.batch, a.seqlen, a.nheads, a.headdim, a.dstate, a.ngroups, like.code);
+    if (need) ws = like.empty({(int64_t)need}, at::kByte);
+  }
+  return result(g_fn.delta_fwd(&a, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0,
+                               like.stream()),
+                y, h);
 }
 
 // q, k, v, dt, beta, A, dt_bias, state, slots, scale, softplus, sigmoid, l2norm, y, state_out, inplace
@@ -546,10 +559,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // bind(addresses of the C entry points, in the order of g_fn)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  constexpr int kFns = 11;
+  constexpr int kFns = 12;
   void* p[kFns];
   if (n != kFns) {
-    PyErr_SetString(PyExc_TypeError, "eleven addresses");
+    PyErr_SetString(PyExc_TypeError, "twelve addresses");
     return nullptr;
   }
   for (int i = 0; i < kFns; ++i) {
@@ -563,10 +576,11 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
           reinterpret_cast<decltype(g_fn.selscan_step)>(p[4]),
           reinterpret_cast<decltype(g_fn.rmsnorm_fwd)>(p[5]),
           reinterpret_cast<decltype(g_fn.rmsnorm_fp8_fwd)>(p[6]),
-          reinterpret_cast<decltype(g_fn.delta_fwd)>(p[7]),
-          reinterpret_cast<decltype(g_fn.delta_step)>(p[8]),
-          reinterpret_cast<decltype(g_fn.gatednorm_fwd)>(p[9]),
-          reinterpret_cast<decltype(g_fn.blocknorm_fwd)>(p[10])};
+          reinterpret_cast<decltype(g_fn.delta_fwd_workspace_bytes)>(p[7]),
+          reinterpret_cast<decltype(g_fn.delta_fwd)>(p[8]),
+          reinterpret_cast<decltype(g_fn.delta_step)>(p[9]),
+          reinterpret_cast<decltype(g_fn.gatednorm_fwd)>(p[10]),
+          reinterpret_cast<decltype(g_fn.blocknorm_fwd)>(p[11])};
   Py_RETURN_NONE;
 }
 
@@ -580,7 +594,7 @@ PyMethodDef g_methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                            {"rmsnorm_fwd", fast(entry<rmsnorm_fwd, 6>), METH_FASTCALL, nullptr},
                            {"kept_workspace", fast(entry<kept_workspace, 1>), METH_FASTCALL, nullptr},
                            {"rmsnorm_fp8_fwd", fast(entry<rmsnorm_fp8_fwd, 8>), METH_FASTCALL, nullptr},
-                           {"delta_fwd", fast(entry<delta_fwd, 16>), METH_FASTCALL, nullptr},
+                           {"delta_fwd", fast(entry<delta_fwd, 17>), METH_FASTCALL, nullptr},
                            {"delta_step", fast(entry<delta_step, 16>), METH_FASTCALL, nullptr},
                            {"gatednorm_fwd", fast(entry<gatednorm_fwd, 7>), METH_FASTCALL, nullptr},
                            {"blocknorm_fwd", fast(entry<blocknorm_fwd, 9>), METH_FASTCALL, nullptr},

@@ -5,22 +5,26 @@
 //     (I + N) d = diag(beta) (V - diag(e^G) K S^T),      T = (I + N)^-1 diag(beta)
 //     y_i = scale (e^(G_i) S q_i + sum_{j <= i} e^(G_i - G_j) (q_i.k_j) d_j)
 //     S'  = e^(G_last) S + sum_j e^(G_last - G_j) d_j k_j^T
-// A CTA runs one chain: the chunks of one head, one after the other, for up to 128 rows of its state (the rows of S do
-// not touch one another).  Rows are the MMAs' M, so that S, S k and d stay in TMEM lanes, one row a lane, and go
-// from one product to the next without a transposition:
-//     X = S K^T        A = S (TMEM), B = K             per chunk: 128 x 64 x dstate
-//     D = V^T T^T + (X diag(-e^G)) T^T                 A = V^T (smem), then X (TMEM); B = T
-//     Q = S Q^T        A = S (TMEM), B = Q
-//     U = (D diag(e^(G_last - G))) K                   A = D (TMEM), B = K: S' = e^(G_last) S + U
-//     O = Q diag(scale e^G) + D P^T    A = D (TMEM), B = P
-//     [K; Q] K^T       of the chunk after the next: what N and P are made of
+//
+// delta_prepare computes what does not depend on S, for all chunks at once: T, the weights P of the output's sum, and a
+// token's factors.  A CTA takes a chunk of one group of heads, whose products K K^T and Q K^T the heads share.  A warp
+// has 16 rows of N and 16 of P in mma.sync fragments: these products are small (64 x 64 x dstate) and end in
+// element-wise work and an inversion by blocks of 16, all in registers.  Its bound is instructions.
+//
+// delta_chain runs the chunks of one head one after the other, a CTA a chain, for up to 128 rows of the state (the rows
+// of S do not touch one another).  Rows are the MMAs' M, so that S, S k and d stay in TMEM lanes, one row a lane,
+// and go from one product to the next without a transposition:
+//     X, Q = S [K; Q]^T                    A = S (TMEM), B = K and Q          128 x 128 x dstate
+//     D = V^T T^T + (X diag(-e^G)) T^T     A = V^T (smem), then X (TMEM); B = T
+//     U = (D diag(e^(G_last - G))) K       A = D (TMEM), B = K: S' = e^(G_last) S + U
+//     O = Q diag(scale e^G) + D P^T        A = D (TMEM), B = P
+// Its bound is the chain of a chunk: three products, and the three conversions between them.
 //
 // Rounding.  q, k and v are bf16 and enter as they are (lengths and decays are factors beside the products).  S is kept in f32
 // registers; as operands S, X, T and the D of the update are split into two bf16 halves (hi + lo, 2^-18 together; lo x lo is
 // left out of U), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P is rounded once.
 //
-// Warps: 0-15 state (four threads a row, each a quarter of its columns), 16-23 prepare (lengths, N, its inverse, P), 24 copies,
-// 25 MMAs, 26 gates.  Every wait is bounded; after one that ran out the CTA's outputs are NaN.
+// Every wait is bounded; after one that ran out the CTA's outputs are NaN.
 #include "delta_common.cuh"
 #include "tc_common.cuh"
 
@@ -30,75 +34,36 @@ namespace {
 using namespace layer;
 
 constexpr int kC = 64;             // tokens of a chunk
-constexpr int kM = 128;            // rows of a tile
-constexpr int kStages = 3;         // K, Q, V of a chunk
-constexpr int kParts = 4;          // state threads of a row
-constexpr int kStateWarps = 4 * kParts, kPrepWarps = 8;
-constexpr int kCopyWarp = kStateWarps + kPrepWarps, kMmaWarp = kCopyWarp + 1, kGateWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kGateWarp + 1);
-constexpr int kPrep = 32 * kPrepWarps;
 constexpr int kTile = kC * 128;    // bytes of 64 rows of 128
-constexpr int kLd = 68;            // floats of a row of N: rows four banks apart
-constexpr int kLdY = 36;
-constexpr uint32_t kPrepBar = 1;
 
-// TMEM columns.  S as an operand (hi, lo) is dead once X and Q are there: X, then D of the update, as operands take its place.
-// D comes in two halves, from the inverse's hi and lo; U takes their place.
-constexpr uint32_t kColHi = 0, kColLo = 64;
-constexpr uint32_t kColOp = 0, kColOpLo = 32;
-constexpr uint32_t kColX = 128, kColQ = 192;
-constexpr uint32_t kColD = 256, kColDlo = 320, kColU = 256;
-constexpr uint32_t kColDo = 384, kColDoLo = 416;  // D of the output; between them [K; Q] K^T
-constexpr uint32_t kColKq = 384;
-constexpr uint32_t kColO = 448;
-constexpr uint32_t kTmemCols = 512;
-
-enum Bar {
-  kFull = 0,                  // K, Q, V have landed
-  kEmpty = kFull + kStages,   // ... and are read
-  kReady = kEmpty + kStages,  // ... and are 0 past the last token
-  kGates = kReady + kStages,  // a chunk's sums of log-decays and betas
-  kGatesFree = kGates + 2,
-  kTReady = kGatesFree + 2,   // T, P and the factors of a chunk
-  kDone = kTReady + 2,        // its last product
-  kSReady = kDone + 2,        // S as an operand, 64 of its columns each
-  kKq = kSReady + 2, kKqFree, kUFull, kXFull, kXReady, kDFull, kDReady, kOReady, kLast, kNumBars
-};
-
-struct Factors {  // of a chunk
+struct Factors {  // of a chunk's tokens: of X, of D in the update, of Q; e^(G_last)
   float x[kC], u[kC], y[kC], last[4];
 };
-struct Tokens {  // of a chunk, for the prepare warps
-  float4 e[kC / 2];   // of two tokens: G minus log2 of 1 / length of k, hi and lo
-  float2 g[kC];       // G hi, lo
-  float row[kC];      // beta / length of k
-  float col[kC / 2];  // first half: e^(G_31 - G_j) / length of k
-  float up[kC / 2];   // second half: e^(G_i - G_31)
-  float beta[kC], rk[kC], rq[kC];
-};
-
-template <int DK>
-struct Layout {
-  static constexpr int kHalves = DK / 64;
-  static constexpr int kStage = kHalves * 2 * kTile + 2 * kTile;  // [half][K rows, Q rows], [64 rows of S][tokens]
-  static constexpr int kT0 = kStages * kStage;                    // [2][hi, lo]
-  static constexpr int kP0 = kT0 + 2 * 2 * kTile;                 // [2]
-  static constexpr int kN0 = kP0 + 2 * kTile;
-  static constexpr int kY0 = kN0 + kC * kLd * 4;                  // products inside the inversion
-  static constexpr int kG0 = kY0 + 32 * kLdY * 4;                 // [2] float4 a token: G (hi, lo), beta
-  static constexpr int kE0 = kG0 + 2 * kC * 16;
-  static constexpr int kF0 = kE0 + (int)sizeof(Tokens);
-  static constexpr int kBars = kF0 + 2 * (int)sizeof(Factors);
-  static constexpr int kTotal = kBars + kNumBars * 8 + 16;
-};
+// What delta_prepare leaves of a chunk of one head: T hi, T lo, P as 128-byte rows of 64 columns with swizzled 16-byte
+// units, and the factors.
+constexpr int kRecord = 3 * kTile + 1024;
+constexpr uint32_t kRecordCopied = 3 * kTile + sizeof(Factors);
+static_assert(sizeof(Factors) <= 1024 && kRecordCopied % 16 == 0, "record");
 
 struct Params {
   ssm_delta_args a;
-  int tiles;       // of a head's rows
-  uint32_t inner;  // tensors whose map has sequences inside tokens
+  unsigned char* records;  // [batch][nheads][chunks of the segment]
+  float* states;           // between segments: [batch][nheads][headdim][dstate]
+  WsHeader* hdr;
+  int first, chunks;       // of the segment
+  int tiles;               // of a head's rows
+  int batches;             // of a group's heads, kHeads each (delta_prepare)
+  bool begins, ends;       // the segment is the first, the last
+  uint32_t inner;          // tensors whose map has sequences inside tokens
   LookbackCtl ctl;
 };
 constexpr uint32_t kMapQ = 1, kMapK = 2, kMapV = 4;
+
+__device__ __forceinline__ int64_t tokens_of(const ssm_delta_args& a, int64_t b) {
+  return a.lens ? min(a.seqlen, (int64_t)max(a.lens[b], 0)) : a.seqlen;
+}
+// Byte of column c of row r in a tile of 128-byte rows with swizzled 16-byte units
+__device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; }
 
 // Two f32 as bf16 pairs hi + lo.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -108,7 +73,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   const float2 r = __ffma2_rn(make_float2(ha, hb), make_float2(-1.f, -1.f), make_float2(a, b));
   lo = pack2(r.x, r.y);
 }
-
 // The bits of v in bf16
 __device__ __forceinline__ uint16_t bf16_of(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
@@ -131,10 +95,434 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float h, float l
   hi = s;
 }
 
+// ---------------------------------------------------------------------------------- delta_prepare
+
+constexpr int kHeads = 4;  // heads of a CTA at most: a warp has one's gates
+constexpr int kPrepThreads = 128;
+
+// A 16 x 16 block in accumulator fragments: v[4 t + 2 r + e] is row lane / 4 + 8 r, column 8 t + 2 (lane % 4) + e.
+struct Block {
+  float v[8];
+};
+// A 16 x 16 block as an A operand: hi and lo, for one k-step.
+struct Left {
+  uint32_t hi[4], lo[4];
+  __device__ __forceinline__ void set(const Block& b) {
+    split2(b.v[0], b.v[1], hi[0], lo[0]);
+    split2(b.v[2], b.v[3], hi[1], lo[1]);
+    split2(b.v[4], b.v[5], hi[2], lo[2]);
+    split2(b.v[6], b.v[7], hi[3], lo[3]);
+  }
+};
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// c += a b, 16 x 8 x 16
+__device__ __forceinline__ void mma16(float* c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c += left right, where right is block (k, j) of the tiles hi and lo
+__device__ __forceinline__ void multiply(Block& c, const Left& left, uint32_t hi, uint32_t lo, int k, int j) {
+  const int lane = threadIdx.x & 31;
+  const int at = swizzled(16 * k + (lane & 15), 16 * j + 8 * (lane >> 4));
+  uint32_t h[4], l[4];  // rows 0-7, 8-15 of the first eight columns, then of the others
+  ldmatrix4_trans(h, hi + at);
+  ldmatrix4_trans(l, lo + at);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    mma16(c.v + 4 * t, left.hi, h[2 * t], h[2 * t + 1]);
+    mma16(c.v + 4 * t, left.hi, l[2 * t], l[2 * t + 1]);
+    mma16(c.v + 4 * t, left.lo, h[2 * t], h[2 * t + 1]);
+  }
+}
+
+template <int DK>
+struct PrepShared {
+  unsigned char k[DK / 64][2][kTile];  // K, Q
+  unsigned char hi[kTile], lo[kTile];  // N below the diagonal blocks, their inverses on the diagonal
+  float diagonal[4][16][20];
+  float4 gates[kHeads][kC];            // G hi, lo, beta
+  float rk[kC], rq[kC];
+  uint64_t full;
+};
+
+// Row block I of N, its part of the inverse, and row block J = 3 - I of P, so that the warps have as much to do.
+template <int DK, int I>
+__device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p, int heads, int h0, int64_t b, int c) {
+  constexpr int J = 3 - I;
+  const int lane = threadIdx.x & 31, rr = lane >> 2, cc = 2 * (lane & 3);
+  const uint32_t kt = smem_addr(sm.k);
+  // ---- products of the rows with K
+  Block kk[I + 1] = {}, qk[J + 1] = {}, qq = {};
+#pragma unroll
+  for (int ks = 0; ks < DK / 16; ++ks) {
+    const uint32_t kb = kt + (ks >> 2) * 2 * kTile, qb = kb + kTile;
+    const int a_row = lane & 15, a_col = (ks & 3) * 16 + 8 * (lane >> 4);
+    const int b_row = (lane & 7) + 8 * (lane >> 4), b_col = (ks & 3) * 16 + 8 * ((lane >> 3) & 1);
+    uint32_t ka[4], qa[4], bq[4];
+    ldmatrix4(ka, kb + swizzled(16 * I + a_row, a_col));
+    ldmatrix4(qa, qb + swizzled(16 * J + a_row, a_col));
+    ldmatrix4(bq, qb + swizzled(16 * J + b_row, b_col));
+    mma16(qq.v, qa, bq[0], bq[1]);
+    mma16(qq.v + 4, qa, bq[2], bq[3]);
+#pragma unroll
+    for (int j = 0; j <= (I > J ? I : J); ++j) {
+      uint32_t kr[4];
+      ldmatrix4(kr, kb + swizzled(16 * j + b_row, b_col));
+      if (j <= I) mma16(kk[j <= I ? j : 0].v, ka, kr[0], kr[1]), mma16(kk[j <= I ? j : 0].v + 4, ka, kr[2], kr[3]);
+      if (j <= J) mma16(qk[j <= J ? j : 0].v, qa, kr[0], kr[1]), mma16(qk[j <= J ? j : 0].v + 4, qa, kr[2], kr[3]);
+    }
+  }
+  // ---- lengths: the diagonals of K K^T and Q Q^T
+  const bool unit = p.a.l2norm != 0;
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (rr == cc + e) {
+        sm.rk[16 * I + 8 * r + rr] = unit ? rsqrtf(kk[I].v[4 * r + 2 * r + e] + delta::kLengthEps) : 1.f;
+        sm.rq[16 * J + 8 * r + rr] = p.a.scale * (unit ? rsqrtf(qq.v[4 * r + 2 * r + e] + delta::kLengthEps) : 1.f);
+      }
+  __syncthreads();
+  const uint32_t hi = smem_addr(sm.hi), lo = smem_addr(sm.lo);
+
+  for (int hh = 0; hh < heads; ++hh) {
+    const float4* gates = sm.gates[hh];
+    unsigned char* rec = p.records + ((b * p.a.nheads + h0 + hh) * p.chunks + (c - p.first)) * (int64_t)kRecord;
+    // an element's weight is e^(G_i - G_j) / length of k_j times the row's factor; in blocks below the diagonal the
+    // exponential goes through the token before the row block
+    const auto weigh = [&](const Block& in, Block& out, int row_block, int j, const float (&f)[2], bool with_diagonal) {
+      const bool diagonal = row_block == j;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int col = 16 * j + 8 * t + cc;
+        const float4 g0 = gates[col], g1 = gates[col + 1];
+        const float2 rk = *reinterpret_cast<const float2*>(&sm.rk[col]);
+        if (diagonal) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = 8 * r + rr;
+            const float4 g = gates[16 * row_block + row];
+            const float e0 = exp2_fast((g.x - g0.x) + (g.y - g0.y)) * rk.x * f[r];
+            const float e1 = exp2_fast((g.x - g1.x) + (g.y - g1.y)) * rk.y * f[r];
+            const int d = row - (8 * t + cc);  // row minus column
+            out.v[4 * t + 2 * r] = d > 0 || (d == 0 && with_diagonal) ? in.v[4 * t + 2 * r] * e0 : 0.f;
+            out.v[4 * t + 2 * r + 1] = d > 1 || (d == 1 && with_diagonal) ? in.v[4 * t + 2 * r + 1] * e1 : 0.f;
+          }
+        } else {
+          const float4 m = gates[16 * row_block - 1];
+          const float c0 = exp2_fast((m.x - g0.x) + (m.y - g0.y)) * rk.x, c1 = exp2_fast((m.x - g1.x) + (m.y - g1.y)) * rk.y;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            out.v[4 * t + 2 * r] = in.v[4 * t + 2 * r] * (c0 * f[r]);
+            out.v[4 * t + 2 * r + 1] = in.v[4 * t + 2 * r + 1] * (c1 * f[r]);
+          }
+        }
+      }
+    };
+    // e^(G_i - G) through the token before a row block
+    const auto after = [&](int row_block, float (&e)[2]) {
+      const float4 m = row_block > 0 ? gates[16 * row_block - 1] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float4 g = gates[16 * row_block + 8 * r + rr];
+        e[r] = exp2_fast((g.x - m.x) + (g.y - m.y));
+      }
+    };
+    float bt[2], up[2], fb[2];
+    after(I, up);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = 16 * I + 8 * r + rr;
+      bt[r] = gates[i].z * sm.rk[i];
+      fb[r] = bt[r] * up[r];
+    }
+    // ---- N: the diagonal block in f32, the others as operands
+    {
+      Block d;
+      weigh(kk[I], d, I, I, bt, false);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float2*>(&sm.diagonal[I][8 * r + rr][8 * t + cc]) = make_float2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1]);
+    }
+    const auto put = [&](const Block& d, int row_block, int j) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t h, l;
+          split2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1], h, l);
+          const int at = swizzled(16 * row_block + 8 * r + rr, 16 * j + 8 * t + cc);
+          *reinterpret_cast<uint32_t*>(sm.hi + at) = h;
+          *reinterpret_cast<uint32_t*>(sm.lo + at) = l;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < I; ++j) {
+      Block d;
+      weigh(kk[j], d, I, j, fb, false);
+      put(d, I, j);
+    }
+    __syncwarp();
+    // ---- the inverse of the diagonal block of I + N, a column a lane
+    {
+      float x[16];
+      const int col = lane & 15;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float v0 = k == col ? 1.f : 0.f, v1 = 0.f;
+#pragma unroll
+        for (int m = 0; m < k; m += 4) {
+          const float4 e = *reinterpret_cast<const float4*>(&sm.diagonal[I][k][m]);
+          v0 = fmaf(-e.x, x[m], v0);
+          if (m + 1 < k) v1 = fmaf(-e.y, x[m + 1], v1);
+          if (m + 2 < k) v0 = fmaf(-e.z, x[m + 2], v0);
+          if (m + 3 < k) v1 = fmaf(-e.w, x[m + 3], v1);
+        }
+        x[k] = v0 + v1;
+      }
+      __syncwarp();
+      if (lane < 16)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sm.diagonal[I][k][col] = x[k];
+      __syncwarp();
+    }
+    Block inv;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 e = *reinterpret_cast<const float2*>(&sm.diagonal[I][8 * r + rr][8 * t + cc]);
+        inv.v[4 * t + 2 * r] = e.x, inv.v[4 * t + 2 * r + 1] = e.y;
+      }
+    put(inv, I, I);
+    // ---- P
+    {
+      float f[2], fu[2];
+      after(J, up);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        f[r] = sm.rq[16 * J + 8 * r + rr];
+        fu[r] = f[r] * up[r];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Block d = {};
+        if (j <= J) weigh(qk[j <= J ? j : 0], d, J, j, j == J ? f : fu, true);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<uint32_t*>(rec + 2 * kTile + swizzled(16 * J + 8 * r + rr, 16 * j + 8 * t + cc)) =
+                pack2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1]);
+      }
+    }
+    // ---- factors, 16 tokens a warp
+    if (lane < 16) {
+      Factors* f = reinterpret_cast<Factors*>(rec + 3 * kTile);
+      const int i = 16 * I + lane;
+      const float4 g = gates[i], gl = gates[kC - 1];
+      const float from_start = exp2_fast(g.x + g.y);
+      f->x[i] = -from_start * sm.rk[i];
+      f->u[i] = exp2_fast((gl.x - g.x) + (gl.y - g.y)) * sm.rk[i];
+      f->y[i] = from_start * sm.rq[i];
+      if (i == kC - 1) f->last[0] = from_start;
+    }
+    // T's row block j of row I, times beta
+    const auto give = [&](const Block& d, int j) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float b0 = gates[16 * j + 8 * t + cc].z, b1 = gates[16 * j + 8 * t + cc + 1].z;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t h, l;
+          split2(d.v[4 * t + 2 * r] * b0, d.v[4 * t + 2 * r + 1] * b1, h, l);
+          unsigned char* at = rec + swizzled(16 * I + 8 * r + rr, 16 * j + 8 * t + cc);
+          *reinterpret_cast<uint32_t*>(at) = h;
+          *reinterpret_cast<uint32_t*>(at + kTile) = l;
+        }
+      }
+    };
+#pragma unroll
+    for (int j = I + 1; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          unsigned char* at = rec + swizzled(16 * I + 8 * r + rr, 16 * j + 8 * t + cc);
+          *reinterpret_cast<uint32_t*>(at) = 0u;
+          *reinterpret_cast<uint32_t*>(at + kTile) = 0u;
+        }
+    give(inv, I);
+    __syncthreads();  // N and the diagonal blocks' inverses of all rows
+    // ---- the rest of the inverse's row: T_ij = -(sum_{j < k <= i} T_ik N_kj) T_jj
+    Left row[I + 1];
+    row[I].set(inv);
+#pragma unroll
+    for (int j = I - 1; j >= 0; --j) {
+      Block sum = {};
+#pragma unroll
+      for (int k = j + 1; k <= I; ++k) multiply(sum, row[k], hi, lo, k, j);
+      Left s;
+      s.set(sum);
+      Block out = {};
+      multiply(out, s, hi, lo, j, j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out.v[e] = -out.v[e];
+      if (j > 0) row[j].set(out);
+      give(out, j);
+    }
+    if (hh + 1 < heads) __syncthreads();  // they are read before the next head's
+  }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kPrepThreads, 4)
+    delta_prepare_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ Params p) {
+  extern __shared__ unsigned char raw[];
+  PrepShared<DK>& sm = *reinterpret_cast<PrepShared<DK>*>(raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u));
+  const ssm_delta_args& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full, 1);
+    fence_mbar_init();
+  }
+  // a chunk's groups side by side
+  const int per_chunk = a.ngroups * p.batches;
+  const int c = p.first + (int)(blockIdx.x / per_chunk % p.chunks);
+  const int64_t b = blockIdx.x / per_chunk / p.chunks;
+  const int g = (int)(blockIdx.x % per_chunk) / p.batches, hpg = a.nheads / a.ngroups;
+  const int first = (int)(blockIdx.x % per_chunk) % p.batches * kHeads, heads = min(kHeads, hpg - first), h0 = g * hpg + first;
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.begins) p.hdr->status = 0;
+  const int64_t tokens = tokens_of(a, b) - (int64_t)c * kC;
+  if (tokens <= 0) return;
+  const int live = (int)min((int64_t)kC, tokens);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(&sm.full, DK / 64 * 2 * kTile);
+    const auto load = [&](void* to, const CUtensorMap* map, int x, uint32_t which) {
+      const bool inner = (p.inner & which) != 0;
+      tc::tma_load_3d(to, map, x, inner ? (int)b : c * kC, inner ? c * kC : (int)b, &sm.full);
+    };
+    for (int j = 0; j < DK / 64; ++j) {
+      load(sm.k[j][0], &map_k, g * DK + 64 * j, kMapK);
+      load(sm.k[j][1], &map_q, g * DK + 64 * j, kMapQ);
+    }
+  }
+  // gates: a warp a head, two neighbouring tokens a lane
+  if (warp < heads) {
+    const int h = h0 + warp;
+    const delta::Gate gate(a, h);
+    float gd[2], beta[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int tok = 2 * lane + k;
+      gd[k] = beta[k] = 0.f;
+      if (tok < live) {
+        const int64_t at = (int64_t)c * kC + tok;
+        gd[k] = gate.log2_decay(to_f32(
+            static_cast<const __nv_bfloat16*>(a.dt.ptr)[b * a.dt.batch_stride + at * a.dt.token_stride + h]));
+        beta[k] = gate.beta(to_f32(
+            static_cast<const __nv_bfloat16*>(a.beta.ptr)[b * a.beta.batch_stride + at * a.beta.token_stride + h]));
+      }
+    }
+    float sh = gd[0], sl = 0.f;  // of the lane's tokens, then of all up to them
+    add_exact(sh, sl, gd[1], 0.f);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const float ph = __shfl_up_sync(0xffffffffu, sh, o), pl = __shfl_up_sync(0xffffffffu, sl, o);
+      if (lane >= o) add_exact(sh, sl, ph, pl);
+    }
+    float eh = __shfl_up_sync(0xffffffffu, sh, 1), el = __shfl_up_sync(0xffffffffu, sl, 1);
+    if (lane == 0) eh = el = 0.f;
+    add_exact(eh, el, gd[0], 0.f);
+    sm.gates[warp][2 * lane] = make_float4(eh, el, beta[0], 0.f);
+    sm.gates[warp][2 * lane + 1] = make_float4(sh, sl, beta[1], 0.f);
+  }
+  // every thread sees the copies' end, or all give up: the records then hold NaN
+  const bool lost = __syncthreads_or(!mbar_wait(&sm.full, 0, p.ctl.spin_limit_ns) || p.ctl.stall_tile == (int64_t)blockIdx.x);
+  if (lost) {
+    if (threadIdx.x == 0) record_error(p.hdr, p.ctl.epoch, SSM_ERR_TIMEOUT);
+    for (int hh = 0; hh < heads; ++hh) {
+      unsigned char* rec = p.records + ((b * a.nheads + h0 + hh) * p.chunks + (c - p.first)) * (int64_t)kRecord;
+      for (int i = threadIdx.x; i < kRecord / 4; i += kPrepThreads) reinterpret_cast<uint32_t*>(rec)[i] = 0x7fc07fc0u;
+    }
+    mbar_wait(&sm.full, 0, p.ctl.spin_limit_ns);  // no copy is left in flight
+    return;
+  }
+  if (live < kC) {  // zeros past the last token
+    constexpr int kRow = DK / 64 * 2 * 8;  // 16-byte units of a token
+    for (int j = threadIdx.x; j < (kC - live) * kRow; j += kPrepThreads)
+      *reinterpret_cast<uint4*>(&sm.k[0][0][0] + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
+  if (warp == 0)
+    prepare_rows<DK, 0>(sm, p, heads, h0, b, c);
+  else if (warp == 1)
+    prepare_rows<DK, 1>(sm, p, heads, h0, b, c);
+  else if (warp == 2)
+    prepare_rows<DK, 2>(sm, p, heads, h0, b, c);
+  else
+    prepare_rows<DK, 3>(sm, p, heads, h0, b, c);
+}
+
+// ---------------------------------------------------------------------------------- delta_chain
+
+constexpr int kM = 128;            // rows of a tile
+constexpr int kStages = 3;         // K, Q, V and the record of a chunk
+constexpr int kParts = 4;          // state threads of a row
+constexpr int kStateWarps = 4 * kParts, kCopyWarp = kStateWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+
+// TMEM columns.  S as an operand (hi, lo) is dead once X and Q are there: X, then D of the update, as operands take its place.
+// D comes in two halves, from the inverse's hi and lo; U takes their place.
+constexpr uint32_t kColHi = 0, kColLo = 64;
+constexpr uint32_t kColOp = 0, kColOpLo = 32;
+constexpr uint32_t kColX = 128, kColQ = 192;
+constexpr uint32_t kColD = 256, kColDlo = 320, kColU = 256;
+constexpr uint32_t kColDo = 384, kColDoLo = 416;  // D of the output
+constexpr uint32_t kColO = 448;
+constexpr uint32_t kTmemCols = 512;
+
+enum Bar {
+  kFull = 0,                  // a chunk has landed
+  kEmpty = kFull + kStages,   // ... and is read
+  kSReady = kEmpty + kStages, // S as an operand, 64 of its columns each
+  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kLast, kNumBars
+};
+
+template <int DK>
+struct Layout {
+  static constexpr int kHalves = DK / 64;
+  // [half][K rows, Q rows], [64 rows of S][tokens], record
+  static constexpr int kV = kHalves * 2 * kTile, kT = kV + 2 * kTile, kP = kT + 2 * kTile, kF = kP + kTile;
+  static constexpr int kStage = kF + 1024;
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kTotal = kBars + kNumBars * 8 + 16;
+};
+
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
-    delta_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+    delta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
   using L = Layout<DK>;
   constexpr int kHalves = L::kHalves;
   extern __shared__ unsigned char raw[];
@@ -142,10 +530,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kBars + kNumBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* sN = reinterpret_cast<float*>(base + L::kN0);
-  float* sY = reinterpret_cast<float*>(base + L::kY0);
-  Tokens& tk = *reinterpret_cast<Tokens*>(base + L::kE0);
-  Factors* sF = reinterpret_cast<Factors*>(base + L::kF0);
 
   const ssm_delta_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -161,11 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto init = [&](int first, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(&bars[first + i], count);
     };
-    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kReady, kStages, kPrepWarps);
-    init(kGates, 2, 1), init(kGatesFree, 2, kPrepWarps), init(kTReady, 2, kPrepWarps), init(kDone, 2, 1);
-    init(kSReady, 2, kStateWarps / kHalves), init(kUFull, 1, 1), init(kKq, 1, 1);
-    init(kKqFree, 1, kPrepWarps - 2), init(kXFull, 1, 1), init(kXReady, 1, kStateWarps), init(kDFull, 1, 1);
-    init(kDReady, 1, kStateWarps), init(kOReady, 1, kStateWarps), init(kLast, 1, 1);
+    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps / kHalves), init(kXFull, 1, 1);
+    init(kXReady, 1, kStateWarps), init(kDFull, 1, 1), init(kDReady, 1, kStateWarps), init(kUFull, 1, 1);
+    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kLast, 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -173,29 +555,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
-  const auto zero = [&](int at, int bytes) {
-    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
-      *reinterpret_cast<uint4*>(base + at + i) = make_uint4(0u, 0u, 0u, 0u);
-  };
   if (v_boxes == 1)  // rows that no copy brings
-    for (int i = 0; i < kStages; ++i) zero(i * L::kStage + (kHalves * 2 + 1) * kTile, kTile);
-  zero(L::kP0, 2 * kTile);  // above the diagonal blocks nothing is written
-  zero(L::kN0, kC * kLd * 4);
+    for (int i = threadIdx.x; i < kStages * kTile / 16; i += kThreads)
+      *reinterpret_cast<uint4*>(base + i / (kTile / 16) * L::kStage + L::kV + kTile + i % (kTile / 16) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
-  int64_t tokens = a.seqlen;
-  if (a.lens) tokens = min(tokens, (int64_t)max(a.lens[b], 0));
+  const int64_t all_tokens = tokens_of(a, b);
+  const int64_t tokens = min(max(all_tokens - (int64_t)p.first * kC, (int64_t)0), (int64_t)p.chunks * kC);  // of the segment
   const int n = (int)((tokens + kC - 1) / kC);
 
   // A bounded wait, the same answer in every lane of a warp
-  const auto wait_one = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (try_wait_parked(bar, parity)) return true;
+  const auto wait_one = [&](int bar, int64_t phase) -> bool {
+    const uint32_t parity = (uint32_t)phase & 1u;
+    if (try_wait_parked(&bars[bar], parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!try_wait_parked(bar, parity)) {
+    while (!try_wait_parked(&bars[bar], parity)) {
       if (*abort_flag || global_timer_ns() - t0 > p.ctl.spin_limit_ns) {
         *abort_flag = 1;
         return false;
@@ -203,9 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  const auto wait = [&](int bar, int64_t phase) -> bool {
-    return __all_sync(0xffffffffu, wait_one(&bars[bar], (uint32_t)phase & 1u));
-  };
+  const auto wait = [&](int bar, int64_t phase) -> bool { return __all_sync(0xffffffffu, wait_one(bar, phase)); };
   const auto arrive = [&](int bar) {  // one of a warp, after all its lanes
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[bar]);
@@ -220,14 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s_half = DK == 128 ? part >> 1 : 0;
     const bool have = row < rows;
     const int64_t at = ((bh * a.headdim + m0 + row) * DK) + part * CW;
+    const float* from = p.begins ? a.h0 : p.states;
+    float* to = p.ends ? a.h_final : p.states;
     float s[CW];
 #pragma unroll
     for (int i = 0; i < CW; ++i) s[i] = 0.f;
-    if (a.h0 && have) {
+    if (from && have) {
 #pragma unroll
-      for (int i = 0; i < CW; ++i) s[i] = a.h0[at + i];
+      for (int i = 0; i < CW; ++i) s[i] = from[at + i];
     }
-    __nv_bfloat16* yp = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0 + row;
+    __nv_bfloat16* yp =
+        static_cast<__nv_bfloat16*>(a.y) + ((b * a.seqlen + (int64_t)p.first * kC) * a.nheads + h) * a.headdim + m0 + row;
     const int64_t y_stride = (int64_t)a.nheads * a.headdim;
     float last = 1.f;  // e^(G_last) of the chunk before
 
@@ -245,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // y of chunk c: this thread's row and tokens
     const auto output = [&](int c) -> bool {
-      if (!wait(kDone + (c & 1), c >> 1)) return false;
+      if (!wait(kDone, c)) return false;
       tc::fence_after_sync();
       uint32_t o[TW];
       tc::tmem_ld16(tm + kColO + part * TW, o);
@@ -265,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     // a part's 16 values, scaled, as an operand
-    const auto operand = [&](const uint32_t (&r)[16], const float* f, uint32_t hi_at, uint32_t lo_at) {
+    const auto operand = [&](const uint32_t (&r)[16], const float* f) {
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -276,13 +656,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         split2(v0.x, v0.y, hi[j], lo[j]);
         split2(v1.x, v1.y, hi[j + 1], lo[j + 1]);
       }
-      tc::tmem_st8(tm + hi_at + part * TW / 2, hi);
-      tc::tmem_st8(tm + lo_at + part * TW / 2, lo);
+      tc::tmem_st8(tm + kColOp + part * TW / 2, hi);
+      tc::tmem_st8(tm + kColOpLo + part * TW / 2, lo);
     };
 
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
-      const int bf = c & 1;
+      const int st = c % kStages;
+      unsigned char* stage = base + st * L::kStage;
+      const Factors& f = *reinterpret_cast<const Factors*>(stage + L::kF);
+      const int live = (int)min((int64_t)kC, tokens - (int64_t)c * kC);
       if (c > 0) {
         ok = wait(kUFull, c - 1);
         tc::fence_after_sync();
@@ -296,19 +679,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_st8(tm + kColHi + (part * CW) / 2 + 8 * q, hi);
         tc::tmem_st8(tm + kColLo + (part * CW) / 2 + 8 * q, lo);
       }
+      if (live < kC && ok) {  // the last chunk: zeros past the last token, before its first product
+        ok = wait(kFull + st, c / kStages);
+        constexpr int kRow = (L::kV + 2 * kTile) / kTile * 8;  // 16-byte units of a token
+        if (ok)
+          for (int j = threadIdx.x; j < (kC - live) * kRow; j += 32 * kStateWarps)
+            *reinterpret_cast<uint4*>(stage + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kSReady + s_half);
       if (c > 0) ok = ok && output(c - 1);
-      const Factors& f = sF[bf];
       // X, scaled, as an operand
-      ok = ok && wait(kTReady + bf, c >> 1) && wait(kXFull, c);
+      ok = ok && wait(kFull + st, c / kStages) && wait(kXFull, c);
       if (!ok) break;
       tc::fence_after_sync();
       uint32_t r[16];
       tc::tmem_ld16(tm + kColX + part * TW, r);
       tc::tmem_ld_wait();
-      operand(r, f.x + part * TW, kColOp, kColOpLo);
+      operand(r, f.x + part * TW);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kXReady);
@@ -327,14 +718,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           r[j] = __float_as_uint(v.x), r[j + 1] = __float_as_uint(v.y);
         }
       }
-      operand(r, f.u + part * TW, kColOp, kColOpLo);
+      operand(r, f.u + part * TW);
       last = f.last[0];
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kDReady);
-      // D as it is, and Q scaled as what O adds to; the place of D may still hold [K; Q] K^T of the chunk after the next
-      if (c + 2 < n && !(ok = wait(kKqFree, c + 2))) break;
-      tc::fence_after_sync();
+      // D as it is, and Q scaled as what O adds to
       {
         uint32_t hi[8], lo[8];
 #pragma unroll
@@ -353,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_st16(tm + kColO + part * TW, r);
       tc::tmem_st_wait();
       tc::fence_before_sync();
+      fence_proxy_async_smem();  // the factors are read before the stage's next copies
       arrive(kOReady);
     }
     if (n > 0 && ok) {
@@ -362,313 +752,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < CW / 16; ++q) update(q);
       ok = ok && output(n - 1);
     }
-    if (ok && a.h_final && have) {
+    if (ok && to && have) {
 #pragma unroll
-      for (int i = 0; i < CW; ++i) a.h_final[at + i] = s[i];
+      for (int i = 0; i < CW; ++i) to[at + i] = s[i];
     }
     tc::fence_before_sync();
-  } else if (warp < kCopyWarp) {
-    // ------------------------------ prepare: lengths, N, T, P ----------------------------------------------
-    const int t = threadIdx.x - 32 * kStateWarps, w = warp - kStateWarps;
-    // of [K; Q] K^T a warp has 32 rows (of K, of Q) and 32 columns
-    const int quad = w & 3, half = w >> 2, i = (quad & 1) * 32 + lane;
-    const bool is_k = quad < 2;
-    const bool above = (quad & 1) == 0 && half == 1;  // all above the diagonal
-    const bool diagonal = (quad & 1) == half;
-    const bool unit = a.l2norm != 0;
-    for (int c = 0; c < n; ++c) {
-      const int st = c % kStages, bf = c & 1;
-      unsigned char* kq = base + st * L::kStage;
-      const int live = (int)min((int64_t)kC, tokens - (int64_t)c * kC);
-      bool bad = !wait(kFull + st, c / kStages);
-      if (live == kC) {
-        arrive(kReady + st);
-      } else {  // zeros past the last token
-        constexpr int kRow = L::kStage / kTile * 8;  // 16-byte units of a token
-        if (!bad)
-          for (int j = t; j < (kC - live) * kRow; j += kPrep)
-            *reinterpret_cast<uint4*>(kq + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        if (named_bar_any(kPrepBar, kPrep, bad)) break;
-        arrive(kReady + st);
-      }
-      if (unit) {  // lengths of k and q, two threads a row
-        const int rr = t >> 1;
-        const unsigned char* at = kq + (rr >> 6) * kTile + (rr & 63) * 128;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int o = 0; o < kHalves * 4; ++o) {
-          const uint4 e = *reinterpret_cast<const uint4*>(at + (o >> 2) * 2 * kTile + ((((o & 3) + 4 * (t & 1)) ^ (rr & 7)) << 4));
-          const uint32_t u[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 v;
-            unpack2(u[j], v.x, v.y);
-            sum[j & 1] = __ffma2_rn(v, v, sum[j & 1]);
-          }
-        }
-        float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        all += __shfl_xor_sync(0xffffffffu, all, 1);
-        if ((t & 1) == 0) (rr < 64 ? tk.rk[rr] : tk.rq[rr - 64]) = rsqrtf(all + delta::kLengthEps);
-      } else if (t < kC) {
-        tk.rk[t] = tk.rq[t] = 1.f;
-      }
-      bad = bad || !wait(kGates + bf, c >> 1);
-      if (named_bar_any(kPrepBar, kPrep, bad)) break;
-      const float4* sG = reinterpret_cast<const float4*>(base + L::kG0) + bf * kC;
-      if (t < kC) {
-        const float4 gi = sG[t], gm = sG[kC / 2 - 1];
-        const float rk = tk.rk[t];
-        float eh = gi.x, el = gi.y;
-        if (unit) add_exact(eh, el, -__log2f(rk), 0.f);
-        reinterpret_cast<float*>(&tk.e[t >> 1])[t & 1] = eh;
-        reinterpret_cast<float*>(&tk.e[t >> 1])[2 + (t & 1)] = el;
-        tk.g[t] = make_float2(gi.x, gi.y);
-        tk.row[t] = gi.z * rk;
-        tk.beta[t] = gi.z;
-        if (t < kC / 2)
-          tk.col[t] = exp2_fast((gm.x - gi.x) + (gm.y - gi.y)) * rk;
-        else
-          tk.up[t - kC / 2] = exp2_fast((gi.x - gm.x) + (gi.y - gm.y));
-      }
-      named_bar_sync(kPrepBar, kPrep);
-      bad = !wait(kKq, c);
-      tc::fence_after_sync();
-      float r[32];
-      if (!above) {
-        uint32_t e[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + kColKq + 32 * half, e);
-        tc::tmem_ld_wait();
-        tc::fence_before_sync();
-        arrive(kKqFree);
-        const float2 g = tk.g[i];
-        float f = is_k ? tk.row[i] : a.scale * tk.rq[i];
-        if (diagonal) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float4 q = tk.e[(32 * half + j) >> 1];
-            const float2 d = __fadd2_rn(__fadd2_rn(make_float2(g.x, g.x), make_float2(-q.x, -q.y)),
-                                        __fadd2_rn(make_float2(g.y, g.y), make_float2(-q.z, -q.w)));
-            const float2 v = __fmul2_rn(__fmul2_rn(make_float2(exp2_fast(d.x), exp2_fast(d.y)), make_float2(f, f)),
-                                        make_float2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])));
-            r[j] = j < lane || (j == lane && !is_k) ? v.x : 0.f;
-            r[j + 1] = j + 1 < lane || (j + 1 == lane && !is_k) ? v.y : 0.f;
-          }
-        } else {  // below: e^(G_i - G_j) through the first half's last token
-          f *= tk.up[lane];
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(&tk.col[j]);
-            const float2 v0 = __fmul2_rn(__fmul2_rn(make_float2(q.x, q.y), make_float2(f, f)),
-                                         make_float2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])));
-            const float2 v1 = __fmul2_rn(__fmul2_rn(make_float2(q.z, q.w), make_float2(f, f)),
-                                         make_float2(__uint_as_float(e[j + 2]), __uint_as_float(e[j + 3])));
-            r[j] = v0.x, r[j + 1] = v0.y, r[j + 2] = v1.x, r[j + 3] = v1.y;
-          }
-        }
-        if (is_k) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(&sN[i * kLd + 32 * half + j]) = make_float4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-        }
-      }
-      // the factors and the T and P of the chunk before the last are read
-      if (c >= 2) bad = bad || !wait(kDone + bf, (c >> 1) - 1);
-      if (!above && !is_k) {
-        unsigned char* pr = base + L::kP0 + bf * kTile + i * 128;
-#pragma unroll
-        for (int o = 0; o < 4; ++o)
-          *reinterpret_cast<uint4*>(pr + (((4 * half + o) ^ (i & 7)) << 4)) =
-              make_uint4(pack2(r[8 * o], r[8 * o + 1]), pack2(r[8 * o + 2], r[8 * o + 3]), pack2(r[8 * o + 4], r[8 * o + 5]),
-                         pack2(r[8 * o + 6], r[8 * o + 7]));
-      }
-      if (above) {  // the chunk's factors
-        const float4 gl = sG[kC - 1];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int tok = lane + 32 * k;
-          const float2 g = tk.g[tok];
-          const float from_start = exp2_fast(g.x + g.y);
-          if (is_k) {
-            sF[bf].x[tok] = -from_start * tk.rk[tok];
-            sF[bf].u[tok] = exp2_fast((gl.x - g.x) + (gl.y - g.y)) * tk.rk[tok];
-            if (tok == kC - 1) sF[bf].last[0] = from_start;
-          } else {
-            sF[bf].y[tok] = from_start * a.scale * tk.rq[tok];
-          }
-        }
-      }
-      if (named_bar_any(kPrepBar, kPrep, bad)) break;
-      arrive(kGatesFree + bf);
-      // (I + N)^-1 in place: the diagonal blocks of 16, a column a lane, then twice the blocks below the
-      // diagonal, T_10 = -T_11 (N_10 T_00)
-      if (w < 4) {
-        float x[16];
-        const float* blk = &sN[16 * w * kLd + 16 * w];
-        const int col = lane & 15;
-#pragma unroll
-        for (int rr = 0; rr < 16; ++rr) {
-          float v0 = rr == col ? 1.f : 0.f, v1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < rr; k += 4) {
-            const float4 e = *reinterpret_cast<const float4*>(&blk[rr * kLd + k]);
-            v0 = fmaf(-e.x, x[k], v0);
-            if (k + 1 < rr) v1 = fmaf(-e.y, x[k + 1], v1);
-            if (k + 2 < rr) v0 = fmaf(-e.z, x[k + 2], v0);
-            if (k + 3 < rr) v1 = fmaf(-e.w, x[k + 3], v1);
-          }
-          x[rr] = v0 + v1;
-        }
-        __syncwarp();
-        if (lane < 16)
-#pragma unroll
-          for (int rr = 0; rr < 16; ++rr) sN[(16 * w + rr) * kLd + 16 * w + col] = x[rr];
-      }
-      named_bar_sync(kPrepBar, kPrep);
-      {
-        const int pair = t >> 7, o = pair * 32, rr = (t & 127) >> 3, cc = (t & 7) * 2;
-        const auto product = [&](const float* left, const float* right, int ld) {  // a row of left, two columns of right
-          float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(left + k);
-            const float l[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v = __ffma2_rn(make_float2(l[j], l[j]), *reinterpret_cast<const float2*>(right + (k + j) * ld), v);
-          }
-          return v;
-        };
-        float2 v = product(&sN[(o + 16 + rr) * kLd + o], &sN[o * kLd + o + cc], kLd);
-        *reinterpret_cast<float2*>(&sY[(pair * 16 + rr) * kLdY + cc]) = v;
-        named_bar_sync(kPrepBar, kPrep);
-        v = product(&sN[(o + 16 + rr) * kLd + o + 16], &sY[pair * 16 * kLdY + cc], kLdY);
-        *reinterpret_cast<float2*>(&sN[(o + 16 + rr) * kLd + o + cc]) = make_float2(-v.x, -v.y);
-      }
-      named_bar_sync(kPrepBar, kPrep);
-      {
-        // four columns of N_10 T_00, whose rows above those columns are 0, a row a lane
-        float2 v[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 4
-        for (int k = 4 * w; k < 32; k += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sN[(32 + lane) * kLd + k]);
-          const float l[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 e = *reinterpret_cast<const float4*>(&sN[(k + j) * kLd + 4 * w]);
-            v[0] = __ffma2_rn(make_float2(l[j], l[j]), make_float2(e.x, e.y), v[0]);
-            v[1] = __ffma2_rn(make_float2(l[j], l[j]), make_float2(e.z, e.w), v[1]);
-          }
-        }
-        *reinterpret_cast<float4*>(&sY[lane * kLdY + 4 * w]) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-        named_bar_sync(kPrepBar, kPrep);
-        // four rows of T_11 times that, whose columns behind those rows are 0, a column a lane
-        const int r0 = 28 - 4 * w;
-        float u[4] = {};
-#pragma unroll 4
-        for (int k = 0; k <= r0; k += 4) {
-          float y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = sY[(k + j) * kLdY + lane];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 f = *reinterpret_cast<const float4*>(&sN[(32 + r0 + j) * kLd + 32 + k]);
-            u[j] = fmaf(f.x, y[0], u[j]), u[j] = fmaf(f.y, y[1], u[j]);
-            u[j] = fmaf(f.z, y[2], u[j]), u[j] = fmaf(f.w, y[3], u[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sN[(32 + r0 + j) * kLd + lane] = -u[j];
-      }
-      named_bar_sync(kPrepBar, kPrep);
-      {  // T = inverse diag(beta), hi and lo
-        const int rr = t >> 2, c0 = (t & 3) * 16;
-        unsigned char* th = base + L::kT0 + bf * 2 * kTile + rr * 128;
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int col = c0 + 8 * o + 4 * j;
-            const float4 e = *reinterpret_cast<const float4*>(&sN[rr * kLd + col]);
-            const float4 be = *reinterpret_cast<const float4*>(&tk.beta[col]);
-            split2(e.x * be.x, e.y * be.y, hi[2 * j], lo[2 * j]);
-            split2(e.z * be.z, e.w * be.w, hi[2 * j + 1], lo[2 * j + 1]);
-          }
-          const int at = (((t & 3) * 2 + o) ^ (rr & 7)) << 4;
-          *reinterpret_cast<uint4*>(th + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(th + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      arrive(kTReady + bf);
-      // (the next chunk's first barrier stands between these reads and its writes of tk's and N's places, but for rk and rq)
-    }
-  } else if (warp == kGateWarp) {
-    // ------------------------------ gates: two neighbouring tokens a lane ------------------------------------
-    const delta::Gate gate(a, h);
-    const __nv_bfloat16* dp = static_cast<const __nv_bfloat16*>(a.dt.ptr) + b * a.dt.batch_stride + h;
-    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta.ptr) + b * a.beta.batch_stride + h;
-    __nv_bfloat16 dt[2], be[2];
-    const auto load = [&](int c) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int64_t tok = (int64_t)c * kC + 2 * lane + k;
-        dt[k] = be[k] = __float2bfloat16_rn(0.f);
-        if (tok < tokens) {
-          dt[k] = dp[tok * a.dt.token_stride];
-          be[k] = bp[tok * a.beta.token_stride];
-        }
-      }
-    };
-    load(0);
-    for (int c = 0; c < n; ++c) {
-      const int bf = c & 1;
-      float g[2], beta[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bool in = (int64_t)c * kC + 2 * lane + k < tokens;
-        g[k] = in ? gate.log2_decay(__bfloat162float(dt[k])) : 0.f;
-        beta[k] = in ? gate.beta(__bfloat162float(be[k])) : 0.f;
-      }
-      load(c + 1);
-      float hi = g[0], lo = 0.f;  // of the lane's tokens, then of all up to them
-      add_exact(hi, lo, g[1], 0.f);
-      float sh = hi, sl = lo;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const float ph = __shfl_up_sync(0xffffffffu, sh, o), pl = __shfl_up_sync(0xffffffffu, sl, o);
-        if (lane >= o) add_exact(sh, sl, ph, pl);
-      }
-      float bh_ = __shfl_up_sync(0xffffffffu, sh, 1), bl = __shfl_up_sync(0xffffffffu, sl, 1);
-      if (lane == 0) bh_ = bl = 0.f;
-      if (c >= 2 && !wait(kGatesFree + bf, (c >> 1) - 1)) break;
-      float4* sG = reinterpret_cast<float4*>(base + L::kG0) + bf * kC;
-      add_exact(bh_, bl, g[0], 0.f);
-      sG[2 * lane] = make_float4(bh_, bl, beta[0], 0.f);
-      sG[2 * lane + 1] = make_float4(sh, sl, beta[1], 0.f);
-      arrive(kGates + bf);
-    }
   } else if (warp == kCopyWarp) {
     // ------------------------------ copies -------------------------------------------------------------------
     if (lane == 0) {
+      const unsigned char* rec = p.records + bh * p.chunks * (int64_t)kRecord;
       int c = 0;
-      const int copies = p.ctl.stall_tile == (int64_t)blockIdx.x ? 0 : n;  // (the test hook)
+      const int copies = p.ctl.stall_tile == ((int64_t)1 << 40) + blockIdx.x ? 0 : n;  // (the test hook)
       for (; c < copies; ++c) {
         const int st = c % kStages;
-        if (c >= kStages && !wait_one(&bars[kEmpty + st], (uint32_t)(c / kStages - 1) & 1u)) break;
-        unsigned char* kq = base + st * L::kStage;
-        mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * 2 + v_boxes) * kTile);
+        if (c >= kStages && !wait_one(kEmpty + st, c / kStages - 1)) break;
+        unsigned char* stage = base + st * L::kStage;
+        mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * 2 + v_boxes) * kTile + kRecordCopied);
         const auto load = [&](int place, const CUtensorMap* map, int x, uint32_t which) {
           const bool inner = (p.inner & which) != 0;
-          const int tok = c * kC;
-          tc::tma_load_3d(kq + place * kTile, map, x, inner ? (int)b : tok, inner ? tok : (int)b, &bars[kFull + st]);
+          const int tok = (p.first + c) * kC;
+          tc::tma_load_3d(stage + place * kTile, map, x, inner ? (int)b : tok, inner ? tok : (int)b, &bars[kFull + st]);
         };
         for (int j = 0; j < kHalves; ++j) {
           load(2 * j, &map_k, g * DK + 64 * j, kMapK);
           load(2 * j + 1, &map_q, g * DK + 64 * j, kMapQ);
         }
+        bulk_g2s(stage + L::kT, rec + c * (int64_t)kRecord, kRecordCopied, &bars[kFull + st]);
         for (int j = 0; j < v_boxes; ++j) load(2 * kHalves + j, &map_v, h * a.headdim + m0 + 64 * j, kMapV);
       }
       for (int j = max(0, c - kStages); j < c; ++j)  // no copy is left in flight
@@ -683,34 +792,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 128, true, false);  // A = V^T
     constexpr uint32_t id_u = tc::idesc_bf16_f32(128, DK, false, true);   // B = K, columns of the state as N
     const uint32_t sb = smem_addr(base);
-    const auto kq_at = [&](int c) { return sb + (c % kStages) * L::kStage; };
     // k-step ks of a K-major tile of 64-column blocks
     const auto k_major = [&](uint32_t at, int ks, uint32_t block) {
       return tc::sdesc_sw128(at + (ks >> 2) * block + (ks & 3) * 32, 16, 1024);
     };
-    int kqs = 0;
-    const auto products_kq = [&](int c) -> bool {  // [K; Q] K^T of chunk c
-      if (!wait_one(&bars[kReady + c % kStages], (uint32_t)(c / kStages) & 1u)) return false;
-      if (c > 0 && !wait_one(&bars[kKqFree], (uint32_t)(c - 1) & 1u)) return false;
-      tc::fence_after_sync();
-      const uint32_t at = kq_at(c);
-#pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        const uint64_t d = k_major(at, ks, 2 * kTile);
-        tc::mma_bf16(tmem + kColKq, d, d, id64, ks > 0);
-      }
-      tc::mma_commit(&bars[kKq]);
-      kqs = c + 1;
-      return true;
-    };
-    bool ok = products_kq(0) && (n < 2 || products_kq(1));
+    bool ok = true;
     int c = 0;  // chunks whose last commit was made
     for (; c < n && ok; ++c) {
-      const int bf = c & 1;
-      const uint32_t kt = kq_at(c), vt = kt + kHalves * 2 * kTile, th = sb + L::kT0 + bf * 2 * kTile;
+      const int st = c % kStages;
+      const uint32_t kt = sb + st * L::kStage, vt = kt + L::kV, th = kt + L::kT, pt = kt + L::kP;
+      if (!(ok = wait_one(kFull + st, c / kStages))) break;
 #pragma unroll
       for (int x = 0; x < kHalves && ok; ++x) {
-        if (!(ok = wait_one(&bars[kSReady + x], (uint32_t)c & 1u))) break;
+        if (!(ok = wait_one(kSReady + x, c))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int ks = 4 * x; ks < 4 * x + 4; ++ks) {
@@ -721,12 +815,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tc::mma_commit(&bars[kXFull]);
-      if (!(ok = wait_one(&bars[kTReady + bf], (uint32_t)(c >> 1) & 1u))) break;
-      tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks)
         tc::mma_bf16(tmem + kColD, tc::sdesc_sw128(vt + ks * 2048, kTile, 1024), k_major(th, ks, 0), id_v, ks > 0);
-      if (!(ok = wait_one(&bars[kXReady], (uint32_t)c & 1u))) break;
+      if (!(ok = wait_one(kXReady, c))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
@@ -734,8 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_bf16_ts(tmem + kColD, tmem + kColOpLo + 8 * ks, k_major(th, ks, 0), id128, true);
       }
       tc::mma_commit(&bars[kDFull]);
-      if (c + 2 < n && !(ok = products_kq(c + 2))) break;  // (beside the state warps' work on D)
-      if (!(ok = wait_one(&bars[kDReady], (uint32_t)c & 1u))) break;
+      if (!(ok = wait_one(kDReady, c))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
@@ -744,16 +835,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_bf16_ts(tmem + kColU, tmem + kColOpLo + 8 * ks, d, id_u, true);
       }
       tc::mma_commit(&bars[kUFull]);
-      if (!(ok = wait_one(&bars[kOReady], (uint32_t)c & 1u))) break;
+      if (!(ok = wait_one(kOReady, c))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
-        const uint64_t d = k_major(sb + L::kP0 + bf * kTile, ks, 0);
+        const uint64_t d = k_major(pt, ks, 0);
         tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, d, id64, true);
         tc::mma_bf16_ts(tmem + kColO, tmem + kColDoLo + 8 * ks, d, id64, true);
       }
-      tc::mma_commit(&bars[kDone + bf]);
-      tc::mma_commit(&bars[kEmpty + c % kStages]);
+      tc::mma_commit(&bars[kDone]);
+      tc::mma_commit(&bars[kEmpty + st]);
     }
     // Every MMA has completed, and no commit's arrival is still due.
     tc::mma_commit(&bars[kLast]);
@@ -761,10 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto drained = [&](int bar, int count) {
       if (count > 0) mbar_wait(&bars[bar], (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
     };
-    drained(kKq, kqs);
-    if (ok) drained(kXFull, c), drained(kDFull, c);
-    drained(kUFull, c);
-    for (int x = 0; x < 2; ++x) drained(kDone + x, (c - x + 1) / 2);
+    drained(kXFull, c), drained(kDFull, c), drained(kUFull, c), drained(kDone, c);
     for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
   }
 
@@ -774,15 +862,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
-  // padding, or everything after a wait that ran out
+  // padding, or after a wait that ran out everything of the segment
   const bool lost = *abort_flag != 0;
+  if (lost && threadIdx.x == 0) record_error(p.hdr, p.ctl.epoch, SSM_ERR_TIMEOUT);
   __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0;
   const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
-  for (int64_t j = (lost ? 0 : tokens) * rows + threadIdx.x; j < a.seqlen * rows; j += kThreads)
+  const int64_t end = p.ends ? a.seqlen : min(a.seqlen, (int64_t)(p.first + p.chunks) * kC);
+  for (int64_t j = ((int64_t)p.first * kC + (lost ? 0 : tokens)) * rows + threadIdx.x; j < end * rows; j += kThreads)
     yt[j / rows * a.nheads * a.headdim + j % rows] = fill;
-  if (lost && a.h_final)
+  float* to = p.ends ? a.h_final : p.states;
+  if (lost && to)
     for (int j = threadIdx.x; j < rows * DK; j += kThreads)
-      a.h_final[(bh * a.headdim + m0) * DK + j] = __uint_as_float(0x7fc00000u);
+      to[(bh * a.headdim + m0) * DK + j] = __uint_as_float(0x7fc00000u);
 }
 
 // How a tensor map takes a tensor's rows: the two outer dimensions in the order of their strides, which nest (see selscan.cu).
@@ -802,21 +893,80 @@ Nesting nesting(const ssm_tokens& t, int64_t batch, int64_t seqlen, int64_t colu
   return {true, inner, {(uint64_t)low, (uint64_t)high}};
 }
 
+
+// Records of all chunks take kRecord bytes a chunk and head; a long prompt goes in segments whose records take at most this.
+constexpr int64_t kMaxRecords = (int64_t)1024 << 20;
+struct Segments {
+  int64_t chunks, of;  // of the prompt, of a segment
+  size_t records, total;
+};
+Segments segments(const ssm_delta_args& a) {
+  Segments g{};
+  const int64_t heads = a.batch * a.nheads;
+  g.chunks = (a.seqlen + kC - 1) / kC;
+  const int64_t most = kMaxRecords / kRecord / heads;
+  g.of = g.chunks <= most ? g.chunks : most;
+  g.records = (size_t)(heads * g.of) * kRecord;
+  g.total = kHeaderBytes + g.records;
+  if (g.of < g.chunks) g.total += (size_t)heads * a.headdim * a.dstate * sizeof(float);
+  return g;
+}
+
 }  // namespace
 
+bool delta_tc_sizes(const ssm_delta_args& a) {
+  return a.dtype == SSM_BF16 && (a.dstate == 64 || a.dstate == 128) && a.headdim % 8 == 0 && a.seqlen >= 16 &&
+         a.seqlen <= 0x7fffffff - kC && a.batch * a.nheads <= kMaxRecords / kRecord;
+}
+size_t delta_tc_workspace(const ssm_delta_args& a) { return segments(a).total; }
+
 bool delta_tc_supported(const ssm_delta_args& a) {
-  if (a.dtype != SSM_BF16 || (a.dstate != 64 && a.dstate != 128) || a.headdim % 8 != 0 || a.seqlen < 1 ||
-      a.seqlen > 0x7fffffff - kC)
-    return false;
+  if (!delta_tc_sizes(a)) return false;
   const int64_t n = (int64_t)a.ngroups * a.dstate;
   return nesting(a.q, a.batch, a.seqlen, n).fits && nesting(a.k, a.batch, a.seqlen, n).fits &&
          nesting(a.v, a.batch, a.seqlen, (int64_t)a.nheads * a.headdim).fits;
 }
 
-cudaError_t launch_delta_tc(const ssm_delta_args& a, const LookbackCtl& ctl, cudaStream_t s) {
+namespace {
+
+template <int DK>
+cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[3], const Segments& g, void* workspace, cudaStream_t s,
+                            const DeltaTimer& timed) {
+  const ssm_delta_args& a = p.a;
+  const size_t prep_bytes = sizeof(PrepShared<DK>) + 1024, chain_bytes = Layout<DK>::kTotal + 1024;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(delta_prepare_kernel<DK>), prep_bytes);
+  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK>), chain_bytes);
+  if (e != cudaSuccess) return e;
+  for (int64_t first = 0; first < g.chunks; first += g.of) {
+    p.first = (int)first;
+    p.chunks = (int)(g.chunks - first < g.of ? g.chunks - first : g.of);
+    p.begins = first == 0;
+    p.ends = first + g.of >= g.chunks;
+    const unsigned prep = (unsigned)(a.batch * p.chunks * a.ngroups * p.batches), chains = (unsigned)(a.batch * a.nheads * p.tiles);
+    e = timed(19, [&] {
+      return launch_pdl(delta_prepare_kernel<DK>, dim3(prep), dim3(kPrepThreads), prep_bytes, s, maps[0], maps[1], p);
+    });
+    if (e != cudaSuccess) return e;
+    e = timed(20, [&] {
+      return launch_pdl(delta_chain_kernel<DK>, dim3(chains), dim3(kThreads), chain_bytes, s, maps[0], maps[1], maps[2], p);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const LookbackCtl& ctl, cudaStream_t s,
+                            const DeltaTimer& timed) {
+  const Segments g = segments(a);
   Params p{};
   p.a = a;
+  p.hdr = static_cast<WsHeader*>(workspace);
+  p.records = static_cast<unsigned char*>(workspace) + kHeaderBytes;
+  p.states = reinterpret_cast<float*>(p.records + g.records);
   p.tiles = (a.headdim + kM - 1) / kM;
+  p.batches = (a.nheads / a.ngroups + kHeads - 1) / kHeads;
   p.ctl = ctl;
   CUtensorMap maps[3];
   const ssm_tokens* t[3] = {&a.q, &a.k, &a.v};
@@ -832,13 +982,7 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, const LookbackCtl& ctl, cud
                                                CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
-  const auto go = [&](auto kernel, size_t bytes) {
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes + 1024);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)(a.batch * a.nheads * p.tiles)), dim3(kThreads), bytes + 1024, s, maps[0], maps[1],
-                      maps[2], p);
-  };
-  return a.dstate == 64 ? go(delta_tc_kernel<64>, Layout<64>::kTotal) : go(delta_tc_kernel<128>, Layout<128>::kTotal);
+  return a.dstate == 64 ? launch_segments<64>(p, maps, g, workspace, s, timed) : launch_segments<128>(p, maps, g, workspace, s, timed);
 }
 
 }  // namespace ssm

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <functional>
+
 #include "../../include/ssm.h"
 
 namespace ssm {
@@ -462,8 +464,13 @@ cudaError_t launch_rmsnorm(const void* x, int64_t x_stride, const float* weight,
 // The gated delta rule, and the norms with a gate and a residual (likewise).
 int64_t delta_ctas(const ssm_delta_args& a);  // CTAs that launch_delta takes at most
 cudaError_t launch_delta(const ssm_delta_args& a, cudaStream_t s);
+// delta_tc: the sizes that it takes, and the strides too; its workspace.  `timed` runs a launch of a kernel id.
+bool delta_tc_sizes(const ssm_delta_args& a);
 bool delta_tc_supported(const ssm_delta_args& a);
-cudaError_t launch_delta_tc(const ssm_delta_args& a, const LookbackCtl& ctl, cudaStream_t s);
+size_t delta_tc_workspace(const ssm_delta_args& a);
+using DeltaTimer = std::function<cudaError_t(int, const std::function<cudaError_t()>&)>;
+cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const LookbackCtl& ctl, cudaStream_t s,
+                            const DeltaTimer& timed);
 cudaError_t launch_delta_step(const ssm_delta_args& a, const int32_t* slots, int64_t nslots, cudaStream_t s);
 cudaError_t launch_gatednorm(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const float* weight,
                              int weight_width, void* y, int64_t rows, int width, int group, bool gate_first, float eps,

@@ -9,7 +9,8 @@ from selective_state_space_mamba_gb300._lib import SsmDeltaArgs, SsmTokens
 
 FAKE = 0x10000  # never dereferenced: every call below fails validation first, or enqueues nothing
 FAR = 1 << 40   # the outputs' place, away from the inputs'
-INVALID, UNSUPPORTED, ALIGNMENT = _lib.SSM_ERR_INVALID_ARG, _lib.SSM_ERR_UNSUPPORTED, _lib.SSM_ERR_ALIGNMENT
+INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = (_lib.SSM_ERR_INVALID_ARG, _lib.SSM_ERR_UNSUPPORTED, _lib.SSM_ERR_ALIGNMENT,
+                                              _lib.SSM_ERR_WORKSPACE)
 OK = _lib.SSM_OK
 
 
@@ -18,7 +19,7 @@ def lib():
     return _lib.load()
 
 
-def delta(lib, step=False, slots=None, nslots=None, **kw):
+def delta(lib, step=False, slots=None, nslots=None, ws=(3 * FAR, 1 << 40), **kw):
     a = SsmDeltaArgs()
     v = dict(q=FAKE, k=FAKE, v=FAKE, dt=FAKE, beta=FAKE, A=FAKE, dt_bias=None, h0=None, lens=None, y=FAR, h_final=2 * FAR,
              batch=2, seqlen=64, nheads=4, headdim=64, dstate=64, ngroups=2, softplus=1, sigmoid=1, l2norm=1, scale=1.0,
@@ -31,7 +32,7 @@ def delta(lib, step=False, slots=None, nslots=None, **kw):
         setattr(a, k, v[k])
     if step:
         return lib.ssm_delta_step(a, slots, v["batch"] if nslots is None else nslots, None)
-    return lib.ssm_delta_fwd(a, None)
+    return lib.ssm_delta_fwd(a, ws[0], ws[1], None)
 
 
 def test_delta_refusals(lib):
@@ -59,8 +60,23 @@ def test_delta_refusals(lib):
     assert delta(lib, True, h_final=None) == INVALID
     assert delta(lib, batch=0) == OK and delta(lib, True, batch=0) == OK
     assert delta(lib, seqlen=0, h_final=None) == OK
-    assert lib.ssm_delta_fwd(None, None) == INVALID
+    assert lib.ssm_delta_fwd(None, None, 0, None) == INVALID
     assert lib.ssm_delta_step(None, None, 0, None) == INVALID
+
+
+def test_delta_workspace(lib):
+    f = lib.ssm_delta_fwd_workspace_bytes
+    for bad in ((-1, 64, 4, 64, 64, 2, 1), (1, -1, 4, 64, 64, 2, 1), (1, 64, 0, 64, 64, 1, 1), (1, 64, 4, 64, 65, 2, 1),
+                (1, 64, 4, 64, 64, 3, 1), (65536, 64, 4, 64, 64, 2, 1), (0, 64, 4, 64, 64, 2, 1)):
+        assert f(*bad) == 0
+    assert f(1, 64, 4, 64, 64, 2, 0) == 0 and f(1, 64, 4, 64, 32, 2, 1) == 0 and f(1, 64, 4, 60, 64, 2, 1) == 0
+    assert f(1, 1, 4, 64, 64, 2, 1) == 0                       # one token
+    one, two = f(1, 64, 4, 64, 64, 2, 1), f(1, 65, 4, 64, 64, 2, 1)
+    assert two - one == one - 256 == 4 * 25600 and one % 256 == 0
+    long = f(4, 1 << 20, 32, 128, 128, 16, 1)                  # in segments, with the states between them
+    assert 4 * 32 * 128 * 128 * 4 < long < 4 * 32 * (1 << 14) * 25600
+    assert delta(lib, ws=(None, 0)) == WORKSPACE and delta(lib, ws=(3 * FAR, 2 * one - 512)) == WORKSPACE
+    assert delta(lib, ws=(3 * FAR + 16, 1 << 40)) == ALIGNMENT
 
 
 def gated(lib, **kw):
