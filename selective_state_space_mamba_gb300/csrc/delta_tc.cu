@@ -95,6 +95,12 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float h, float l
   hi = s;
 }
 
+// 1-D bulk copy shared -> global (16-byte aligned addresses, size a multiple of 16), in a bulk group.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------------- delta_prepare
 
 constexpr int kHeads = 4;  // heads of a CTA at most: a warp has one's gates
@@ -150,39 +156,48 @@ __device__ __forceinline__ void multiply(Block& c, const Left& left, uint32_t hi
 
 template <int DK>
 struct PrepShared {
-  unsigned char k[DK / 64][2][kTile];  // K, Q
+  static constexpr int kKq = DK / 64 * 2 * kTile, kDiagonal = 4 * 16 * 20 * 4;
+  // K and Q by halves of the columns; once their products are in registers, a head's record and the diagonal blocks
+  unsigned char kq[kKq > kRecord + kDiagonal ? kKq : kRecord + kDiagonal];
   unsigned char hi[kTile], lo[kTile];  // N below the diagonal blocks, their inverses on the diagonal
-  float diagonal[4][16][20];
   float4 gates[kHeads][kC];            // G hi, lo, beta
   float rk[kC], rq[kC];
   uint64_t full;
 };
 
-// Row block I of N, its part of the inverse, and row block J = 3 - I of P, so that the warps have as much to do.
-template <int DK, int I>
+// Row block I = warp of N, its part of the inverse, and row block J = 3 - I of P, so that the warps have as much to do.  Blocks
+// of a row are counted from the diagonal to the left, so that all warps run the same instructions (a code of its own for
+// each row block took longer: the instruction cache).
+template <int DK>
 __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p, int heads, int h0, int64_t b, int c) {
-  constexpr int J = 3 - I;
+  const int I = threadIdx.x >> 5, J = 3 - I;
   const int lane = threadIdx.x & 31, rr = lane >> 2, cc = 2 * (lane & 3);
-  const uint32_t kt = smem_addr(sm.k);
+  const uint32_t kt = smem_addr(sm.kq);
   // ---- products of the rows with K
-  Block kk[I + 1] = {}, qk[J + 1] = {}, qq = {};
-#pragma unroll
+  Block kk[4] = {}, qk[4] = {}, qq = {};
+#pragma unroll 2
   for (int ks = 0; ks < DK / 16; ++ks) {
     const uint32_t kb = kt + (ks >> 2) * 2 * kTile, qb = kb + kTile;
     const int a_row = lane & 15, a_col = (ks & 3) * 16 + 8 * (lane >> 4);
     const int b_row = (lane & 7) + 8 * (lane >> 4), b_col = (ks & 3) * 16 + 8 * ((lane >> 3) & 1);
-    uint32_t ka[4], qa[4], bq[4];
+    uint32_t ka[4], qa[4], r[4];
     ldmatrix4(ka, kb + swizzled(16 * I + a_row, a_col));
     ldmatrix4(qa, qb + swizzled(16 * J + a_row, a_col));
-    ldmatrix4(bq, qb + swizzled(16 * J + b_row, b_col));
-    mma16(qq.v, qa, bq[0], bq[1]);
-    mma16(qq.v + 4, qa, bq[2], bq[3]);
+    ldmatrix4(r, qb + swizzled(16 * J + b_row, b_col));
+    mma16(qq.v, qa, r[0], r[1]);
+    mma16(qq.v + 4, qa, r[2], r[3]);
 #pragma unroll
-    for (int j = 0; j <= (I > J ? I : J); ++j) {
-      uint32_t kr[4];
-      ldmatrix4(kr, kb + swizzled(16 * j + b_row, b_col));
-      if (j <= I) mma16(kk[j <= I ? j : 0].v, ka, kr[0], kr[1]), mma16(kk[j <= I ? j : 0].v + 4, ka, kr[2], kr[3]);
-      if (j <= J) mma16(qk[j <= J ? j : 0].v, qa, kr[0], kr[1]), mma16(qk[j <= J ? j : 0].v + 4, qa, kr[2], kr[3]);
+    for (int d = 0; d < 4; ++d) {
+      if (d <= I) {
+        ldmatrix4(r, kb + swizzled(16 * (I - d) + b_row, b_col));
+        mma16(kk[d].v, ka, r[0], r[1]);
+        mma16(kk[d].v + 4, ka, r[2], r[3]);
+      }
+      if (d <= J) {
+        ldmatrix4(r, kb + swizzled(16 * (J - d) + b_row, b_col));
+        mma16(qk[d].v, qa, r[0], r[1]);
+        mma16(qk[d].v + 4, qa, r[2], r[3]);
+      }
     }
   }
   // ---- lengths: the diagonals of K K^T and Q Q^T
@@ -192,34 +207,46 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (rr == cc + e) {
-        sm.rk[16 * I + 8 * r + rr] = unit ? rsqrtf(kk[I].v[4 * r + 2 * r + e] + delta::kLengthEps) : 1.f;
-        sm.rq[16 * J + 8 * r + rr] = p.a.scale * (unit ? rsqrtf(qq.v[4 * r + 2 * r + e] + delta::kLengthEps) : 1.f);
+        sm.rk[16 * I + 8 * r + rr] = unit ? rsqrtf(kk[0].v[6 * r + e] + delta::kLengthEps) : 1.f;
+        sm.rq[16 * J + 8 * r + rr] = p.a.scale * (unit ? rsqrtf(qq.v[6 * r + e] + delta::kLengthEps) : 1.f);
       }
-  __syncthreads();
+  __syncthreads();  // the products of all rows, and the lengths
   const uint32_t hi = smem_addr(sm.hi), lo = smem_addr(sm.lo);
+  unsigned char* rec = sm.kq;
+  float(*diagonal)[20] = reinterpret_cast<float(*)[20]>(sm.kq + kRecord) + 16 * I;
+  // the record above the diagonal blocks
+#pragma unroll
+  for (int d = 1; d < 4; ++d) {
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const int unit16 = (lane >> 4) << 4;  // of the two 16-byte units of a block's row
+    if (I + d < 4) {
+      const int to = swizzled(16 * I + (lane & 15), 16 * (I + d)) ^ unit16;
+      *reinterpret_cast<uint4*>(rec + to) = none;
+      *reinterpret_cast<uint4*>(rec + kTile + to) = none;
+    }
+    if (J + d < 4) *reinterpret_cast<uint4*>(rec + 2 * kTile + (swizzled(16 * J + (lane & 15), 16 * (J + d)) ^ unit16)) = none;
+  }
 
   for (int hh = 0; hh < heads; ++hh) {
     const float4* gates = sm.gates[hh];
-    unsigned char* rec = p.records + ((b * p.a.nheads + h0 + hh) * p.chunks + (c - p.first)) * (int64_t)kRecord;
     // an element's weight is e^(G_i - G_j) / length of k_j times the row's factor; in blocks below the diagonal the
     // exponential goes through the token before the row block
-    const auto weigh = [&](const Block& in, Block& out, int row_block, int j, const float (&f)[2], bool with_diagonal) {
-      const bool diagonal = row_block == j;
+    const auto weigh = [&](const Block& in, Block& out, int row_block, int d, const float (&f)[2], bool with_diagonal) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int col = 16 * j + 8 * t + cc;
+        const int col = 16 * (row_block - d) + 8 * t + cc;
         const float4 g0 = gates[col], g1 = gates[col + 1];
         const float2 rk = *reinterpret_cast<const float2*>(&sm.rk[col]);
-        if (diagonal) {
+        if (d == 0) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int row = 8 * r + rr;
             const float4 g = gates[16 * row_block + row];
             const float e0 = exp2_fast((g.x - g0.x) + (g.y - g0.y)) * rk.x * f[r];
             const float e1 = exp2_fast((g.x - g1.x) + (g.y - g1.y)) * rk.y * f[r];
-            const int d = row - (8 * t + cc);  // row minus column
-            out.v[4 * t + 2 * r] = d > 0 || (d == 0 && with_diagonal) ? in.v[4 * t + 2 * r] * e0 : 0.f;
-            out.v[4 * t + 2 * r + 1] = d > 1 || (d == 1 && with_diagonal) ? in.v[4 * t + 2 * r + 1] * e1 : 0.f;
+            const int below = row - (8 * t + cc);
+            out.v[4 * t + 2 * r] = below > 0 || (below == 0 && with_diagonal) ? in.v[4 * t + 2 * r] * e0 : 0.f;
+            out.v[4 * t + 2 * r + 1] = below > 1 || (below == 1 && with_diagonal) ? in.v[4 * t + 2 * r + 1] * e1 : 0.f;
           }
         } else {
           const float4 m = gates[16 * row_block - 1];
@@ -232,34 +259,16 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
         }
       }
     };
-    // e^(G_i - G) through the token before a row block
-    const auto after = [&](int row_block, float (&e)[2]) {
+    // f times e^(G_i - G) through the token before a row block
+    const auto after = [&](int row_block, const float (&f)[2], float (&e)[2]) {
       const float4 m = row_block > 0 ? gates[16 * row_block - 1] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float4 g = gates[16 * row_block + 8 * r + rr];
-        e[r] = exp2_fast((g.x - m.x) + (g.y - m.y));
+        e[r] = f[r] * exp2_fast((g.x - m.x) + (g.y - m.y));
       }
     };
-    float bt[2], up[2], fb[2];
-    after(I, up);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = 16 * I + 8 * r + rr;
-      bt[r] = gates[i].z * sm.rk[i];
-      fb[r] = bt[r] * up[r];
-    }
-    // ---- N: the diagonal block in f32, the others as operands
-    {
-      Block d;
-      weigh(kk[I], d, I, I, bt, false);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          *reinterpret_cast<float2*>(&sm.diagonal[I][8 * r + rr][8 * t + cc]) = make_float2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1]);
-    }
-    const auto put = [&](const Block& d, int row_block, int j) {
+    const auto put = [&](const Block& d, int row_block, int j, unsigned char* to_hi, unsigned char* to_lo) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -267,18 +276,44 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
           uint32_t h, l;
           split2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1], h, l);
           const int at = swizzled(16 * row_block + 8 * r + rr, 16 * j + 8 * t + cc);
-          *reinterpret_cast<uint32_t*>(sm.hi + at) = h;
-          *reinterpret_cast<uint32_t*>(sm.lo + at) = l;
+          *reinterpret_cast<uint32_t*>(to_hi + at) = h;
+          *reinterpret_cast<uint32_t*>(to_lo + at) = l;
         }
     };
+    // T: the inverse's block times beta
+    const auto give = [&](const Block& d, int j) {
+      Block e;
 #pragma unroll
-    for (int j = 0; j < I; ++j) {
+      for (int t = 0; t < 2; ++t) {
+        const float b0 = gates[16 * j + 8 * t + cc].z, b1 = gates[16 * j + 8 * t + cc + 1].z;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) e.v[4 * t + 2 * r] = d.v[4 * t + 2 * r] * b0, e.v[4 * t + 2 * r + 1] = d.v[4 * t + 2 * r + 1] * b1;
+      }
+      put(e, I, j, rec, rec + kTile);
+    };
+    // ---- N: the diagonal block in f32, the others as operands
+    {
+      float f[2], fu[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) f[r] = gates[16 * I + 8 * r + rr].z * sm.rk[16 * I + 8 * r + rr];
       Block d;
-      weigh(kk[j], d, I, j, fb, false);
-      put(d, I, j);
+      weigh(kk[0], d, I, 0, f, false);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float2*>(&diagonal[8 * r + rr][8 * t + cc]) = make_float2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1]);
+      after(I, f, fu);
+#pragma unroll
+      for (int e = 1; e < 4; ++e)
+        if (e <= I) {
+          weigh(kk[e], d, I, e, fu, false);
+          put(d, I, I - e, sm.hi, sm.lo);
+        }
     }
     __syncwarp();
     // ---- the inverse of the diagonal block of I + N, a column a lane
+    Block inv;
     {
       float x[16];
       const int col = lane & 15;
@@ -287,7 +322,7 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
         float v0 = k == col ? 1.f : 0.f, v1 = 0.f;
 #pragma unroll
         for (int m = 0; m < k; m += 4) {
-          const float4 e = *reinterpret_cast<const float4*>(&sm.diagonal[I][k][m]);
+          const float4 e = *reinterpret_cast<const float4*>(&diagonal[k][m]);
           v0 = fmaf(-e.x, x[m], v0);
           if (m + 1 < k) v1 = fmaf(-e.y, x[m + 1], v1);
           if (m + 2 < k) v0 = fmaf(-e.z, x[m + 2], v0);
@@ -298,38 +333,38 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
       __syncwarp();
       if (lane < 16)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) sm.diagonal[I][k][col] = x[k];
+        for (int k = 0; k < 16; ++k) diagonal[k][col] = x[k];
       __syncwarp();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 e = *reinterpret_cast<const float2*>(&diagonal[8 * r + rr][8 * t + cc]);
+          inv.v[4 * t + 2 * r] = e.x, inv.v[4 * t + 2 * r + 1] = e.y;
+        }
     }
-    Block inv;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float2 e = *reinterpret_cast<const float2*>(&sm.diagonal[I][8 * r + rr][8 * t + cc]);
-        inv.v[4 * t + 2 * r] = e.x, inv.v[4 * t + 2 * r + 1] = e.y;
-      }
-    put(inv, I, I);
+    put(inv, I, I, sm.hi, sm.lo);
     // ---- P
     {
       float f[2], fu[2];
-      after(J, up);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        f[r] = sm.rq[16 * J + 8 * r + rr];
-        fu[r] = f[r] * up[r];
-      }
+      for (int r = 0; r < 2; ++r) f[r] = sm.rq[16 * J + 8 * r + rr];
+      after(J, f, fu);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Block d = {};
-        if (j <= J) weigh(qk[j <= J ? j : 0], d, J, j, j == J ? f : fu, true);
+      for (int e = 0; e < 4; ++e)
+        if (e <= J) {
+          Block d;
+          if (e == 0)
+            weigh(qk[0], d, J, 0, f, true);
+          else
+            weigh(qk[e], d, J, e, fu, true);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<uint32_t*>(rec + 2 * kTile + swizzled(16 * J + 8 * r + rr, 16 * j + 8 * t + cc)) =
-                pack2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1]);
-      }
+            for (int r = 0; r < 2; ++r)
+              *reinterpret_cast<uint32_t*>(rec + 2 * kTile + swizzled(16 * J + 8 * r + rr, 16 * (J - e) + 8 * t + cc)) =
+                  pack2(d.v[4 * t + 2 * r], d.v[4 * t + 2 * r + 1]);
+        }
     }
     // ---- factors, 16 tokens a warp
     if (lane < 16) {
@@ -342,52 +377,37 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
       f->y[i] = from_start * sm.rq[i];
       if (i == kC - 1) f->last[0] = from_start;
     }
-    // T's row block j of row I, times beta
-    const auto give = [&](const Block& d, int j) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float b0 = gates[16 * j + 8 * t + cc].z, b1 = gates[16 * j + 8 * t + cc + 1].z;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint32_t h, l;
-          split2(d.v[4 * t + 2 * r] * b0, d.v[4 * t + 2 * r + 1] * b1, h, l);
-          unsigned char* at = rec + swizzled(16 * I + 8 * r + rr, 16 * j + 8 * t + cc);
-          *reinterpret_cast<uint32_t*>(at) = h;
-          *reinterpret_cast<uint32_t*>(at + kTile) = l;
-        }
-      }
-    };
-#pragma unroll
-    for (int j = I + 1; j < 4; ++j)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          unsigned char* at = rec + swizzled(16 * I + 8 * r + rr, 16 * j + 8 * t + cc);
-          *reinterpret_cast<uint32_t*>(at) = 0u;
-          *reinterpret_cast<uint32_t*>(at + kTile) = 0u;
-        }
     give(inv, I);
     __syncthreads();  // N and the diagonal blocks' inverses of all rows
     // ---- the rest of the inverse's row: T_ij = -(sum_{j < k <= i} T_ik N_kj) T_jj
-    Left row[I + 1];
-    row[I].set(inv);
+    Left row[3];
+    row[0].set(inv);
 #pragma unroll
-    for (int j = I - 1; j >= 0; --j) {
-      Block sum = {};
+    for (int d = 1; d < 4; ++d)
+      if (d <= I) {
+        Block sum = {}, out = {};
 #pragma unroll
-      for (int k = j + 1; k <= I; ++k) multiply(sum, row[k], hi, lo, k, j);
-      Left s;
-      s.set(sum);
-      Block out = {};
-      multiply(out, s, hi, lo, j, j);
+        for (int e = 0; e < d; ++e) multiply(sum, row[e], hi, lo, I - e, I - d);
+        Left s;
+        s.set(sum);
+        multiply(out, s, hi, lo, I - d, I - d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out.v[e] = -out.v[e];
-      if (j > 0) row[j].set(out);
-      give(out, j);
+        for (int e = 0; e < 8; ++e) out.v[e] = -out.v[e];
+        if (d < 3) row[d < 3 ? d : 0].set(out);
+        give(out, I - d);
+      }
+    // ---- the record
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned char* to = p.records + ((b * p.a.nheads + h0 + hh) * p.chunks + (c - p.first)) * (int64_t)kRecord;
+      bulk_s2g(to, rec, kRecordCopied);
+      bulk_commit();
+      bulk_wait_read<0>();
     }
-    if (hh + 1 < heads) __syncthreads();  // they are read before the next head's
+    if (hh + 1 < heads) __syncthreads();
   }
+  if (threadIdx.x == 0) bulk_wait<0>();
 }
 
 template <int DK>
@@ -422,8 +442,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       tc::tma_load_3d(to, map, x, inner ? (int)b : c * kC, inner ? c * kC : (int)b, &sm.full);
     };
     for (int j = 0; j < DK / 64; ++j) {
-      load(sm.k[j][0], &map_k, g * DK + 64 * j, kMapK);
-      load(sm.k[j][1], &map_q, g * DK + 64 * j, kMapQ);
+      load(sm.kq + 2 * j * kTile, &map_k, g * DK + 64 * j, kMapK);
+      load(sm.kq + (2 * j + 1) * kTile, &map_q, g * DK + 64 * j, kMapQ);
     }
   }
   // gates: a warp a head, two neighbouring tokens a lane
@@ -470,18 +490,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   if (live < kC) {  // zeros past the last token
     constexpr int kRow = DK / 64 * 2 * 8;  // 16-byte units of a token
     for (int j = threadIdx.x; j < (kC - live) * kRow; j += kPrepThreads)
-      *reinterpret_cast<uint4*>(&sm.k[0][0][0] + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
+      *reinterpret_cast<uint4*>(sm.kq + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
           make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  if (warp == 0)
-    prepare_rows<DK, 0>(sm, p, heads, h0, b, c);
-  else if (warp == 1)
-    prepare_rows<DK, 1>(sm, p, heads, h0, b, c);
-  else if (warp == 2)
-    prepare_rows<DK, 2>(sm, p, heads, h0, b, c);
-  else
-    prepare_rows<DK, 3>(sm, p, heads, h0, b, c);
+  prepare_rows<DK>(sm, p, heads, h0, b, c);
 }
 
 // ---------------------------------------------------------------------------------- delta_chain
