@@ -499,11 +499,19 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 
 // ---------------------------------------------------------------------------------- delta_chain
 
+// Store of a 4-D box; elements outside the tensor are not written.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
 constexpr int kM = 128;            // rows of a tile
 constexpr int kStages = 3;         // K, Q, V and the record of a chunk
 constexpr int kParts = 4;          // state threads of a row
-constexpr int kStateWarps = 4 * kParts, kCopyWarp = kStateWarps, kMmaWarp = kCopyWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kStateWarps = 4 * kParts, kCopyWarp = kStateWarps, kMmaWarp = kCopyWarp + 1, kStoreWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kStoreWarp + 1);
 
 // TMEM columns.  S as an operand (hi, lo) is dead once X and Q are there: X, then D of the update, as operands take its place.
 // D comes in two halves, from the inverse's hi and lo; U takes their place.
@@ -519,7 +527,7 @@ enum Bar {
   kFull = 0,                  // a chunk has landed
   kEmpty = kFull + kStages,   // ... and is read
   kSReady = kEmpty + kStages, // S as an operand, 64 of its columns each
-  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kLast, kNumBars
+  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kYReady, kLast, kNumBars
 };
 
 template <int DK>
@@ -535,7 +543,8 @@ struct Layout {
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_y,
+                       const __grid_constant__ Params p) {
   using L = Layout<DK>;
   constexpr int kHalves = L::kHalves;
   extern __shared__ unsigned char raw[];
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps / kHalves), init(kXFull, 1, 1);
     init(kXReady, 1, kStateWarps), init(kDFull, 1, 1), init(kDReady, 1, kStateWarps), init(kUFull, 1, 1);
-    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kLast, 1, 1);
+    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, 1, kStateWarps), init(kLast, 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -619,24 +628,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < CW; ++i) s[i] = from[at + i];
     }
-    __nv_bfloat16* yp =
-        static_cast<__nv_bfloat16*>(a.y) + ((b * a.seqlen + (int64_t)p.first * kC) * a.nheads + h) * a.headdim + m0 + row;
-    const int64_t y_stride = (int64_t)a.nheads * a.headdim;
     float last = 1.f;  // e^(G_last) of the chunk before
 
     // S <- last S + U
-    const auto update = [&](int q) {
-      uint32_t r[16];
-      tc::tmem_ld16(tm + kColU + part * CW + 16 * q, r);
+    const auto update = [&]() {
+      uint32_t r[CW / 16][16];
+#pragma unroll
+      for (int q = 0; q < CW / 16; ++q) tc::tmem_ld16(tm + kColU + part * CW + 16 * q, r[q]);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const float2 v = __ffma2_rn(make_float2(s[16 * q + j], s[16 * q + j + 1]), make_float2(last, last),
-                                    make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
-        s[16 * q + j] = v.x, s[16 * q + j + 1] = v.y;
+      for (int j = 0; j < CW; j += 2) {
+        const float2 v = __ffma2_rn(make_float2(s[j], s[j + 1]), make_float2(last, last),
+                                    make_float2(__uint_as_float(r[j / 16][j % 16]), __uint_as_float(r[j / 16][j % 16 + 1])));
+        s[j] = v.x, s[j + 1] = v.y;
       }
     };
-    // y of chunk c: this thread's row and tokens
+    // y of chunk c: this thread's row and tokens, into the chunk's V, which its products have read; 0 past the last token
     const auto output = [&](int c) -> bool {
       if (!wait(kDone, c)) return false;
       tc::fence_after_sync();
@@ -644,17 +651,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_ld16(tm + kColO + part * TW, o);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
-      const int64_t t0 = (int64_t)c * kC + part * TW;
-      const int m = have ? (int)min((int64_t)TW, tokens - t0) : 0;
-      uint16_t* yo = reinterpret_cast<uint16_t*>(yp + t0 * y_stride);
-      if (m == TW) {
+      const int64_t left = tokens - ((int64_t)c * kC + part * TW);
+      if (left < TW) {
 #pragma unroll
-        for (int j = 0; j < TW; ++j, yo += y_stride) *yo = bf16_of(__uint_as_float(o[j]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < TW; ++j, yo += y_stride)
-          if (j < m) *yo = bf16_of(__uint_as_float(o[j]));
+        for (int j = 0; j < TW; ++j)
+          if (j >= left) o[j] = 0u;
       }
+      // (the swizzle of a token's 16-byte units goes by token % 8, the same for all parts)
+      unsigned char* tile = base + c % kStages * L::kStage + L::kV + (row >> 6) * kTile + part * TW * 128;
+#pragma unroll
+      for (int j = 0; j < TW; ++j)
+        *reinterpret_cast<uint16_t*>(tile + j * 128 + ((((row & 63) >> 3) ^ (j & 7)) << 4) + (row & 7) * 2) =
+            bf16_of(__uint_as_float(o[j]));
+      fence_proxy_async_smem();
+      arrive(kYReady);
       return true;
     };
     // a part's 16 values, scaled, as an operand
@@ -682,10 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c > 0) {
         ok = wait(kUFull, c - 1);
         tc::fence_after_sync();
+        update();
       }
 #pragma unroll
       for (int q = 0; q < CW / 16; ++q) {
-        if (c > 0) update(q);
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) split2(s[16 * q + 2 * j], s[16 * q + 2 * j + 1], hi[j], lo[j]);
@@ -761,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n > 0 && ok) {
       ok = wait(kUFull, n - 1);
       tc::fence_after_sync();
-#pragma unroll
-      for (int q = 0; q < CW / 16; ++q) update(q);
+      update();
       ok = ok && output(n - 1);
     }
     if (ok && to && have) {
@@ -795,6 +804,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = max(0, c - kStages); j < c; ++j)  // no copy is left in flight
         mbar_wait(&bars[kFull + j % kStages], (uint32_t)(j / kStages) & 1u, p.ctl.spin_limit_ns);
+    }
+  } else if (warp == kStoreWarp) {
+    // ------------------------------ y ------------------------------------------------------------------------
+    if (lane == 0) {
+      for (int c = 0; c < n && wait_one(kYReady, c); ++c) {
+        for (int j = 0; j < v_boxes; ++j)
+          tma_store_4d(&map_y, base + c % kStages * L::kStage + L::kV + j * kTile, m0 + 64 * j, h, (p.first + c) * kC, (int)b);
+        bulk_commit();
+        bulk_wait_read<0>();
+        mbar_arrive(&bars[kEmpty + c % kStages]);  // every product of the chunk was done before its y
+      }
+      bulk_wait<0>();
     }
   } else if (lane == 0 && n > 0) {
     // ------------------------------ MMAs ---------------------------------------------------------------------
@@ -857,7 +878,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_bf16_ts(tmem + kColO, tmem + kColDoLo + 8 * ks, d, id64, true);
       }
       tc::mma_commit(&bars[kDone]);
-      tc::mma_commit(&bars[kEmpty + st]);
     }
     // Every MMA has completed, and no commit's arrival is still due.
     tc::mma_commit(&bars[kLast]);
@@ -866,7 +886,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (count > 0) mbar_wait(&bars[bar], (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
     };
     drained(kXFull, c), drained(kDFull, c), drained(kUFull, c), drained(kDone, c);
-    for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
   }
 
   tc::fence_before_sync();
@@ -877,11 +896,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // padding, or after a wait that ran out everything of the segment
   const bool lost = *abort_flag != 0;
+  const int64_t stored = min((int64_t)n * kC, a.seqlen - (int64_t)p.first * kC);
   if (lost && threadIdx.x == 0) record_error(p.hdr, p.ctl.epoch, SSM_ERR_TIMEOUT);
   __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0;
   const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
   const int64_t end = p.ends ? a.seqlen : min(a.seqlen, (int64_t)(p.first + p.chunks) * kC);
-  for (int64_t j = ((int64_t)p.first * kC + (lost ? 0 : tokens)) * rows + threadIdx.x; j < end * rows; j += kThreads)
+  for (int64_t j = ((int64_t)p.first * kC + (lost ? 0 : stored)) * rows + threadIdx.x; j < end * rows; j += kThreads)
     yt[j / rows * a.nheads * a.headdim + j % rows] = fill;
   float* to = p.ends ? a.h_final : p.states;
   if (lost && to)
@@ -937,13 +957,14 @@ bool delta_tc_supported(const ssm_delta_args& a) {
   if (!delta_tc_sizes(a)) return false;
   const int64_t n = (int64_t)a.ngroups * a.dstate;
   return nesting(a.q, a.batch, a.seqlen, n).fits && nesting(a.k, a.batch, a.seqlen, n).fits &&
-         nesting(a.v, a.batch, a.seqlen, (int64_t)a.nheads * a.headdim).fits;
+         nesting(a.v, a.batch, a.seqlen, (int64_t)a.nheads * a.headdim).fits && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
+         a.seqlen * a.nheads * a.headdim < (int64_t)1 << 39;
 }
 
 namespace {
 
 template <int DK>
-cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[3], const Segments& g, void* workspace, cudaStream_t s,
+cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segments& g, void* workspace, cudaStream_t s,
                             const DeltaTimer& timed) {
   const ssm_delta_args& a = p.a;
   const size_t prep_bytes = sizeof(PrepShared<DK>) + 1024, chain_bytes = Layout<DK>::kTotal + 1024;
@@ -961,7 +982,8 @@ cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[3], const Segme
     });
     if (e != cudaSuccess) return e;
     e = timed(20, [&] {
-      return launch_pdl(delta_chain_kernel<DK>, dim3(chains), dim3(kThreads), chain_bytes, s, maps[0], maps[1], maps[2], p);
+      return launch_pdl(delta_chain_kernel<DK>, dim3(chains), dim3(kThreads), chain_bytes, s, maps[0], maps[1], maps[2],
+                        maps[3], p);
     });
     if (e != cudaSuccess) return e;
   }
@@ -981,7 +1003,7 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
   p.tiles = (a.headdim + kM - 1) / kM;
   p.batches = (a.nheads / a.ngroups + kHeads - 1) / kHeads;
   p.ctl = ctl;
-  CUtensorMap maps[3];
+  CUtensorMap maps[4];
   const ssm_tokens* t[3] = {&a.q, &a.k, &a.v};
   const int64_t columns[3] = {(int64_t)a.ngroups * a.dstate, (int64_t)a.ngroups * a.dstate, (int64_t)a.nheads * a.headdim};
   for (int i = 0; i < 3; ++i) {
@@ -995,6 +1017,13 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
                                                CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
+  // y by heads, so that a box ends with its head's rows
+  const uint64_t dims[4] = {(uint64_t)a.headdim, (uint64_t)a.nheads, (uint64_t)a.seqlen, (uint64_t)a.batch};
+  const uint64_t row = (uint64_t)a.headdim * 2, strides[3] = {row, row * a.nheads, row * a.nheads * a.seqlen};
+  const uint32_t box[4] = {64, 1, (uint32_t)kC, 1};
+  const cudaError_t e =
+      encode_tensor_map_4d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
   return a.dstate == 64 ? launch_segments<64>(p, maps, g, workspace, s, timed) : launch_segments<128>(p, maps, g, workspace, s, timed);
 }
 
