@@ -65,27 +65,19 @@ __device__ __forceinline__ int64_t tokens_of(const ssm_delta_args& a, int64_t b)
 // Byte of column c of row r in a tile of 128-byte rows with swizzled 16-byte units
 __device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; }
 
-// Two f32 as bf16 pairs hi + lo.
+// Two f32 as bf16 pairs hi + lo.  The remainder a - hi is exact; its product with -1 takes hi as it lies in the pair (1 % less
+// for the whole prompt than with two instructions that unpack it).
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack2(a, b);
-  float ha, hb;
-  unpack2(hi, ha, hb);
-  const float2 r = __ffma2_rn(make_float2(ha, hb), make_float2(-1.f, -1.f), make_float2(a, b));
-  lo = pack2(r.x, r.y);
+  float la, lb;
+  asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %2;\n mov.b16 m, 0xBF80;\n"
+      " fma.rn.f32.bf16 %0, l, m, %3;\n fma.rn.f32.bf16 %1, h, m, %4;\n}"
+      : "=f"(la), "=f"(lb)
+      : "r"(hi), "f"(a), "f"(b));
+  lo = pack2(la, lb);
 }
 // The bits of v in bf16
 __device__ __forceinline__ uint16_t bf16_of(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
-// mbar_try_wait that may park the warp for up to 20 us.
-__device__ __forceinline__ bool try_wait_parked(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
 
 // a + b as hi + lo
 __device__ __forceinline__ void add_exact(float& hi, float& lo, float h, float l) {
@@ -527,7 +519,7 @@ enum Bar {
   kFull = 0,                  // a chunk has landed
   kEmpty = kFull + kStages,   // ... and is read
   kSReady = kEmpty + kStages, // S as an operand, 64 of its columns each
-  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kYReady, kLast, kNumBars
+  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kYReady, kLoaded, kLast, kNumBars
 };
 
 template <int DK>
@@ -569,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps / kHalves), init(kXFull, 1, 1);
     init(kXReady, 1, kStateWarps), init(kDFull, 1, 1), init(kDReady, 1, kStateWarps), init(kUFull, 1, 1);
-    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, 1, kStateWarps), init(kLast, 1, 1);
+    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, 1, kStateWarps), init(kLoaded, 1, kStateWarps), init(kLast, 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -594,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A bounded wait, the same answer in every lane of a warp
   const auto wait_one = [&](int bar, int64_t phase) -> bool {
     const uint32_t parity = (uint32_t)phase & 1u;
-    if (try_wait_parked(&bars[bar], parity)) return true;
+    if (mbar_try_wait(&bars[bar], parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!try_wait_parked(&bars[bar], parity)) {
+    while (!mbar_try_wait(&bars[bar], parity)) {
       if (*abort_flag || global_timer_ns() - t0 > p.ctl.spin_limit_ns) {
         *abort_flag = 1;
         return false;
@@ -618,15 +610,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
     const int s_half = DK == 128 ? part >> 1 : 0;
     const bool have = row < rows;
-    const int64_t at = ((bh * a.headdim + m0 + row) * DK) + part * CW;
     const float* from = p.begins ? a.h0 : p.states;
     float* to = p.ends ? a.h_final : p.states;
     float s[CW];
 #pragma unroll
     for (int i = 0; i < CW; ++i) s[i] = 0.f;
-    if (from && have) {
+    // States go through a stage's shared memory, in rows of kRowS floats: a thread's columns lie a row from its
+    // neighbour's.  move(stage, f): f on each four floats of the tile, there and in global memory (its elements in order).
+    constexpr int kRowS = DK + 4;
+    static_assert(kM * kRowS * 4 <= L::kStage, "a state fits a stage");
+    const int64_t at = (bh * a.headdim + m0) * DK;
+    const auto move = [&](int stage, auto f) {
+      float* rows_at = reinterpret_cast<float*>(base + stage * L::kStage);
+      for (int i = 4 * threadIdx.x; i < rows * DK; i += 4 * 32 * kStateWarps) f(rows_at + i / DK * kRowS + i % DK, i);
+    };
+    const auto own = [&](int stage) {
+      return reinterpret_cast<float4*>(reinterpret_cast<float*>(base + stage * L::kStage) + row * kRowS + part * CW);
+    };
+    if (from) {
+      const bool vec = reinterpret_cast<uintptr_t>(from) % 16 == 0;
+      move(kStages - 1, [&](float* to, int i) {
+        const float* e = from + at + i;
+        *reinterpret_cast<float4*>(to) = vec ? *reinterpret_cast<const float4*>(e) : make_float4(e[0], e[1], e[2], e[3]);
+      });
+      named_bar_sync(1, 32 * kStateWarps);
+      if (have) {
 #pragma unroll
-      for (int i = 0; i < CW; ++i) s[i] = from[at + i];
+        for (int i = 0; i < CW; i += 4) *reinterpret_cast<float4*>(&s[i]) = own(kStages - 1)[i / 4];
+      }
+      fence_proxy_async_smem();
+      arrive(kLoaded);
     }
     float last = 1.f;  // e^(G_last) of the chunk before
 
@@ -774,9 +787,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       update();
       ok = ok && output(n - 1);
     }
-    if (ok && to && have) {
+    // the stage of the chunk that would be next: all that used it is done with the y of the chunk three before
+    const int free_stage = n % kStages;
+    if (n >= kStages) ok = ok && wait(kEmpty + free_stage, n / kStages - 1);
+    if (to && !named_bar_any(1, 32 * kStateWarps, !ok)) {
+      if (have) {
 #pragma unroll
-      for (int i = 0; i < CW; ++i) to[at + i] = s[i];
+        for (int i = 0; i < CW; i += 4) own(free_stage)[i / 4] = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+      }
+      named_bar_sync(1, 32 * kStateWarps);
+      const bool vec = reinterpret_cast<uintptr_t>(to) % 16 == 0;
+      move(free_stage, [&](const float* mine, int i) {
+        const float4 e = *reinterpret_cast<const float4*>(mine);
+        float* o = to + at + i;
+        if (vec)
+          *reinterpret_cast<float4*>(o) = e;
+        else
+          o[0] = e.x, o[1] = e.y, o[2] = e.z, o[3] = e.w;
+      });
     }
     tc::fence_before_sync();
   } else if (warp == kCopyWarp) {
@@ -788,6 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; c < copies; ++c) {
         const int st = c % kStages;
         if (c >= kStages && !wait_one(kEmpty + st, c / kStages - 1)) break;
+        if (c == kStages - 1 && (p.begins ? a.h0 : p.states) && !wait_one(kLoaded, 0)) break;  // the state came there
         unsigned char* stage = base + st * L::kStage;
         mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * 2 + v_boxes) * kTile + kRecordCopied);
         const auto load = [&](int place, const CUtensorMap* map, int x, uint32_t which) {
