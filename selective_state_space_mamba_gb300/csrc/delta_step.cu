@@ -5,6 +5,9 @@
 // A warp takes kVecs vectors of four columns a lane, 4 KB of consecutive rows of one head, all loaded before the
 // first is used.  S k and S q both come from the old state, so one reduction over the lanes serves them: its halving
 // rounds leave each lane with one of the rows' sums.
+// b128 nh32 128x128 (537 MB of states read and written): 78.8 us, the rate of a copy.  Three CTAs an SM with 80 registers a
+// thread keep all eight loads in flight; with four of 64, or with four vectors a lane, 85 and 106 us.  States are streamed
+// (evicted first): without that 92 us, 97 in place.
 #include "delta_common.cuh"
 
 namespace ssm {
@@ -17,12 +20,12 @@ constexpr int kVecs = 8;
 
 template <bool kVec>
 __device__ __forceinline__ float4 load4(const float* p) {
-  return kVec ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+  return kVec ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(p[0], p[1], p[2], p[3]);
 }
 template <bool kVec>
 __device__ __forceinline__ void store4(float* p, const float4& v) {
   if (kVec)
-    *reinterpret_cast<float4*>(p) = v;
+    __stcs(reinterpret_cast<float4*>(p), v);
   else
     p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
 }
@@ -36,7 +39,7 @@ __device__ __forceinline__ float dot(const float4& a, const float4& b) {
 
 // kVec: the states are aligned to 16 bytes.
 template <typename T, int DK, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
     delta_step_kernel(const __grid_constant__ ssm_delta_args a, const int32_t* slots, int64_t nslots) {
   constexpr int LPR = DK / 4;        // lanes of a row
   constexpr int SIDE = 32 / LPR;     // rows side by side in a warp
