@@ -18,6 +18,7 @@ using namespace layer;
 constexpr int kMaxThreads = 1024;
 constexpr int kHoldThreads = 512;
 constexpr int kTeamThreads = 128;
+constexpr int kWarpRows = 4;  // rows of a CTA where a warp does for one
 constexpr int64_t kManyRows = 152 * 4;  // four CTAs an SM
 
 // Eight elements of a row as they lie in memory: columns c, c + 1, ... (kVec) or c, c + 32, ...
@@ -74,12 +75,13 @@ __device__ __forceinline__ int first_column(int i) {
   return kVec ? 8 * i : (i >> 5) * 256 + (i & 31);
 }
 
-// Sum over the CTA, the same in every thread; `part` is the call's own.
-__device__ __forceinline__ float cta_sum(float v, float* part) {
+// Sum over the CTA (where it has ROWS > 1 rows over the warp), the same in every thread; `part` is the call's own.
+template <int ROWS>
+__device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return v;
+  if (ROWS > 1 || warps == 1) return v;
   if (lane == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = lane < warps ? part[lane] : 0.f;
@@ -108,37 +110,47 @@ struct GatedParams {
   int64_t rows;
   int width, group, groups;
   float eps;
+  // u / groups for u below 2^31: (u magic) >> (32 + shift), magic = ceil(2^(32 + shift) / groups), 2^shift >= groups
+  uint32_t magic, shift;
+  __device__ __forceinline__ uint32_t row_of(uint32_t u) const { return groups == 1 ? u : (__umulhi(u, magic)) >> shift; }
 };
 
-// x and z of a vector, and the value whose squares are summed
+// x and z of a vector; with the gate first their product takes their place once its squares are summed.
 template <typename T, bool kVec, bool kFirst>
 struct GatedVector {
   Eight<T, kVec> x, z;
+  float product[kFirst ? 8 : 1];
   __device__ __forceinline__ void load(const T* xr, const T* zr, int c, int width) {
     x.load(xr, c, width);
     z.load(zr, c, width);
   }
-  __device__ __forceinline__ void value(float (&v)[8]) const {
+  __device__ __forceinline__ void sum(float (&squares)[2]) {
+    float v[8];
     x.get(v);
     if constexpr (kFirst) {
       float g[8];
       z.get(g);
       silu_n(g, g);
-      mul_n(v, g, v);
+      mul_n(v, g, product);
+      add_squares(product, squares);
+    } else {
+      add_squares(v, squares);
     }
   }
   __device__ __forceinline__ void output(const float* weight, T* yr, int c, int width, float rstd) const {
     float v[8], w[8];
-    value(v);
     load_columns<kVec>(weight, c, width, w);
-    mul_n(v, rstd, v);
-    mul_n(v, w, v);
-    if constexpr (!kFirst) {
+    if constexpr (kFirst) {
+      mul_n(product, rstd, v);
+    } else {
       float g[8];
+      x.get(v);
+      mul_n(v, rstd, v);
       z.get(g);
       silu_n(g, g);
       mul_n(v, g, v);
     }
+    mul_n(v, w, v);
     store_columns<kVec>(yr, c, width, v);
   }
 };
@@ -158,29 +170,27 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
   const float* w = p.weight + (p.weight_width == p.width ? g0 : 0);
   const int nvec = vectors<kVec>(p.group), tid = threadIdx.x, threads = blockDim.x;
   GatedVector<T, kVec, kFirst> held[HOLD];
-  float sum[2] = {}, v[8];
+  float sum[2] = {};
 #pragma unroll
   for (int k = 0; k < HOLD; ++k)
     if (tid + k * threads < nvec) held[k].load(xr, zr, first_column<kVec>(tid + k * threads), p.group);
 #pragma unroll
   for (int k = 0; k < HOLD; ++k)
-    if (tid + k * threads < nvec) {
-      held[k].value(v);
-      add_squares(v, sum);
-    }
+    if (tid + k * threads < nvec) held[k].sum(sum);
   for (int i = tid + HOLD * threads; i < nvec; i += threads) {
     GatedVector<T, kVec, kFirst> e;
     e.load(xr, zr, first_column<kVec>(i), p.group);
-    e.value(v);
-    add_squares(v, sum);
+    e.sum(sum);
   }
-  const float rstd = rsqrtf(cta_sum(sum[0] + sum[1], part) / (float)p.group + p.eps);
+  const float rstd = rsqrtf(row_sum<1>(sum[0] + sum[1], part) / (float)p.group + p.eps);
 #pragma unroll
   for (int k = 0; k < HOLD; ++k)
     if (tid + k * threads < nvec) held[k].output(w, yr, first_column<kVec>(tid + k * threads), p.group, rstd);
   for (int i = tid + HOLD * threads; i < nvec; i += threads) {
     GatedVector<T, kVec, kFirst> e;
     e.load(xr, zr, first_column<kVec>(i), p.group);
+    float unused[2] = {};
+    e.sum(unused);  // (the product with the gate)
     e.output(w, yr, first_column<kVec>(i), p.group, rstd);
   }
 }
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(kTeamThreads) gatednorm_team_kernel(const __gr
   for (int k = 0; k < UNITS; ++k) {
     const uint32_t u = first + k * TEAMS;
     if (u < units) {
-      const int64_t row = u / (uint32_t)p.groups, g0 = (int64_t)(u % (uint32_t)p.groups) * p.group;
+      const int64_t row = p.row_of(u), g0 = (int64_t)(u - (uint32_t)row * (uint32_t)p.groups) * p.group;
 #pragma unroll
       for (int i = 0; i < HOLD; ++i)
         if (lane + TEAM * i < nvec)
@@ -210,21 +220,18 @@ __global__ void __launch_bounds__(kTeamThreads) gatednorm_team_kernel(const __gr
 #pragma unroll
   for (int k = 0; k < UNITS; ++k) {
     const uint32_t u = first + k * TEAMS;
-    float sum[2] = {}, v[8];
+    float sum[2] = {};
     if (u < units) {
 #pragma unroll
       for (int i = 0; i < HOLD; ++i)
-        if (lane + TEAM * i < nvec) {
-          held[k][i].value(v);
-          add_squares(v, sum);
-        }
+        if (lane + TEAM * i < nvec) held[k][i].sum(sum);
     }
     float all = sum[0] + sum[1];
 #pragma unroll
     for (int o = TEAM / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     if (u < units) {
       const float rstd = rsqrtf(all / (float)p.group + p.eps);
-      const int64_t row = u / (uint32_t)p.groups, g0 = (int64_t)(u % (uint32_t)p.groups) * p.group;
+      const int64_t row = p.row_of(u), g0 = (int64_t)(u - (uint32_t)row * (uint32_t)p.groups) * p.group;
 #pragma unroll
       for (int i = 0; i < HOLD; ++i)
         if (lane + TEAM * i < nvec)
@@ -280,20 +287,22 @@ struct BlockParams {
   float alpha, eps;
 };
 
-// A CTA a row.  HOLD vectors of x, the gate and the residual a thread; r replaces them after the first sum.
-template <typename T, typename R, bool kGate, bool kVec, int HOLD>
-__global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
+// A CTA or, ROWS of them in a CTA, a warp a row.  HOLD vectors of x, the gate and the residual a thread; r replaces them
+// after the first sum.  ROWS > 1: rows are at most HOLD vectors a lane.
+template <typename T, typename R, bool kGate, bool kVec, int HOLD, int ROWS>
+__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : HOLD > 1 ? kHoldThreads : kMaxThreads)
     blocknorm_kernel(const __grid_constant__ BlockParams p) {
   griddep_launch_dependents();
   griddep_wait();
   __shared__ float part[2][32];
-  const int64_t row = blockIdx.x;
+  const int64_t row = ROWS > 1 ? (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 5) : blockIdx.x;
+  if (ROWS > 1 && row >= p.rows) return;
   const T* xr = static_cast<const T*>(p.x) + row * p.x_stride;
   const T* zr = static_cast<const T*>(p.z) + row * p.z_stride;
   const R* rr = static_cast<const R*>(p.residual) + row * p.width;
   R* ro = p.residual_out ? static_cast<R*>(p.residual_out) + row * p.width : nullptr;
   T* yr = static_cast<T*>(p.y) + row * p.width;
-  const int nvec = vectors<kVec>(p.width), tid = threadIdx.x, threads = blockDim.x;
+  const int nvec = vectors<kVec>(p.width), tid = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x, threads = ROWS > 1 ? 32 : blockDim.x;
   const auto joined = [&](const Eight<T, kVec>& x, const Eight<T, kVec>& z, const Eight<R, kVec>& res, int c, float rstd,
                           float (&r)[8]) {
     float w[8], e[8];
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
     load_columns<kVec>(xr, first_column<kVec>(i), p.width, v);
     add_squares(v, sum);
   }
-  const float rstd = rsqrtf(cta_sum(sum[0] + sum[1], part[0]) / (float)p.width + p.eps);
+  const float rstd = rsqrtf(row_sum<ROWS>(sum[0] + sum[1], part[0]) / (float)p.width + p.eps);
   // r of the vectors that a thread does not hold is computed twice: with residual_out in place of residual, it is written
   // with the second time
   const auto again = [&](int c, float (&r)[8]) {
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(HOLD > 1 ? kHoldThreads : kMaxThreads)
     again(first_column<kVec>(i), v);
     add_squares(v, sum);
   }
-  const float next = rsqrtf(cta_sum(sum[0] + sum[1], part[1]) / (float)p.width + p.eps);
+  const float next = rsqrtf(row_sum<ROWS>(sum[0] + sum[1], part[1]) / (float)p.width + p.eps);
   const auto output = [&](int c, const float (&r)[8]) {
     float w[8], o[8];
     load_columns<kVec>(p.next_weight, c, p.width, w);
@@ -384,8 +393,14 @@ cudaError_t launch_block_rows(const BlockParams& p, cudaStream_t s) {
     return launch_pdl(kernel, dim3((unsigned)p.rows), dim3((unsigned)(threads < kMaxThreads ? threads : kMaxThreads)), 0, s,
                       p);
   };
-  if (p.rows < kManyRows || nvec > 3 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 1>, 1);
-  return go(blocknorm_kernel<T, R, kGate, kVec, 3>, 3);
+  const auto warps = [&](auto kernel) {
+    return launch_pdl(kernel, dim3((unsigned)((p.rows + kWarpRows - 1) / kWarpRows)), dim3(32 * kWarpRows), 0, s, p);
+  };
+  if (p.rows < kManyRows || nvec > 4 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 1, 1>, 1);
+  if (nvec <= 32) return warps(blocknorm_kernel<T, R, kGate, kVec, 1, kWarpRows>);
+  if (nvec <= 96) return warps(blocknorm_kernel<T, R, kGate, kVec, 3, kWarpRows>);
+  if (nvec <= 3 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 3, 1>, 3);
+  return go(blocknorm_kernel<T, R, kGate, kVec, 4, 1>, 4);
 }
 
 template <typename T, typename R>
@@ -400,7 +415,10 @@ cudaError_t launch_gatednorm(const void* x, int64_t x_stride, const void* z, int
                              int weight_width, void* y, int64_t rows, int width, int group, bool gate_first, float eps,
                              ssm_dtype dtype, cudaStream_t s) {
   const int e = dtype == SSM_F32 ? 4 : 2;
-  const GatedParams p{x, z, x_stride, z_stride, weight, weight_width, y, rows, width, group, width / group, eps};
+  GatedParams p{x, z, x_stride, z_stride, weight, weight_width, y, rows, width, group, width / group, eps, 0, 0};
+  // magic below 2^32 needs 2^shift < groups: shift = ceil(log2 groups) - 1, exact for u below 2^31
+  while ((2u << p.shift) < (uint32_t)p.groups) ++p.shift;
+  if (p.groups > 1) p.magic = (uint32_t)((((uint64_t)1 << (32 + p.shift)) + p.groups - 1) / p.groups);
   const bool vec = group % 8 == 0 && aligned_rows(x, x_stride, 0, e, 16) && aligned_rows(z, z_stride, 0, e, 16) &&
                    aligned_rows(weight, 0, 0, 4, 16) && aligned_rows(y, width, 0, e, 16);
   return dtype == SSM_F32 ? launch_gated_type<float>(p, vec, gate_first, s)
