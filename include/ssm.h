@@ -638,10 +638,11 @@ SSM_API int64_t ssm_debug_scan_schedule(int64_t tiles, int row_tiles, int heads_
  * kernel of the one-kernel state pass with split chains), 9 conv (ssm_conv_fwd), 10 conv_step,
  * 11 selscan_piece (the first kernel of ssm_selscan_fwd with a split time axis), 12 selscan
  * (ssm_selscan_fwd), 13 selscan_step, 14 rmsnorm (both forms), 15 delta (ssm_delta_fwd, token by token), 16 delta_step,
- * 17 gatednorm, 18 blocknorm, 19 delta_prepare and 20 delta_chain (ssm_delta_fwd on the tensor cores).  Host-side only;
+ * 17 gatednorm, 18 blocknorm, 19 delta_prepare, 20 delta_chain, 21 delta_states and
+ * 22 delta_join (ssm_delta_fwd on the tensor cores; the latter two where chains are cut into pieces).  Host-side only;
  * process-global; not thread-safe.
  */
-#define SSM_PROFILE_KERNELS 21
+#define SSM_PROFILE_KERNELS 23
 #define SSM_PROFILE_END_KERNELS 9
 SSM_API ssm_status ssm_profile_begin(int max_launches);
 SSM_API ssm_status ssm_profile_end(double *ms_out, int64_t *launches_out);

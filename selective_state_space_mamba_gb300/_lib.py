@@ -31,7 +31,8 @@ EXPORTS = ("ssm_status_string", "ssm_version", "ssm_ssd_fwd_workspace_bytes", "s
 PROFILE_KERNELS = ("linscan_lookback", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",
                    "ssd_state_fused", "ssd_step", "linscan_baseline", "ssd_state_fixup", "conv", "conv_step",
                    "selscan_piece", "selscan", "selscan_step", "rmsnorm")
-PROFILE_KERNELS_MORE = ("delta", "delta_step", "gatednorm", "blocknorm", "delta_prepare", "delta_chain")  # the ids after those
+PROFILE_KERNELS_MORE = ("delta", "delta_step", "gatednorm", "blocknorm", "delta_prepare", "delta_chain",
+                        "delta_states", "delta_join")  # the ids after those
 SSM_ACT_NONE, SSM_ACT_SILU = 0, 1
 
 

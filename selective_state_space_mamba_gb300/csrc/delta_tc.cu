@@ -20,6 +20,11 @@
 //     O = Q diag(scale e^G) + D P^T        A = D (TMEM), B = P
 // Its bound is the chain of a chunk: three products, and the three conversions between them.
 //
+// Few chains leave most of the GPU idle, so they are cut into pieces that run at once.  A piece is linear in the state that
+// enters it: S_out = S_in M + N.  A first run of the chains (without outputs) gives N from a zero state, and M from
+// the unit matrix's rows and no values, as another tile of rows; delta_join multiplies the pieces up in f32, and
+// a second run, now with each piece's own state, gives the outputs.
+//
 // Rounding.  q, k and v are bf16 and enter as they are (lengths and decays are factors beside the products).  S is kept in f32
 // registers; as operands S, X, T and the D of the update are split into two bf16 halves (hi + lo, 2^-18 together; lo x lo is
 // left out of U), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P is rounded once.
@@ -49,6 +54,9 @@ struct Params {
   ssm_delta_args a;
   unsigned char* records;  // [batch][nheads][chunks of the segment]
   float* states;           // between segments: [batch][nheads][headdim][dstate]
+  int pieces, piece_chunks; // of a segment's chains (1: whole)
+  float* entering;         // [pieces - 1] like states: N of a piece, then what the next one enters with
+  float* passing;          // [pieces - 2][batch][nheads][dstate][dstate]: M of the pieces but the first and the last
   WsHeader* hdr;
   int first, chunks;       // of the segment
   int tiles;               // of a head's rows
@@ -532,7 +540,8 @@ struct Layout {
   static constexpr int kTotal = kBars + kNumBars * 8 + 16;
 };
 
-template <int DK>
+// kOutput: a piece with its outputs; else its N or M.
+template <int DK, bool kOutput>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_y,
@@ -547,12 +556,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const ssm_delta_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int m0 = (int)(blockIdx.x % p.tiles) * kM;
-  const int64_t bh = blockIdx.x / p.tiles;
+  // jobs of a chain: its pieces' tiles of rows; without outputs those of all pieces but the last, then the M of all but the first
+  const int tile_jobs = (kOutput ? p.pieces : p.pieces - 1) * p.tiles, jobs = kOutput ? tile_jobs : tile_jobs + p.pieces - 2;
+  const int job = (int)(blockIdx.x % jobs);
+  const int64_t bh = blockIdx.x / jobs, heads = a.batch * a.nheads;
+  const bool unit = job >= tile_jobs;
+  const int piece = unit ? job - tile_jobs + 1 : job / p.tiles, m0 = unit ? 0 : job % p.tiles * kM;
   const int h = (int)(bh % a.nheads), g = h / (a.nheads / a.ngroups);
   const int64_t b = bh / a.nheads;
-  const int rows = min(kM, a.headdim - m0);
-  const int v_boxes = rows > 64 ? 2 : 1;
+  const int rows = unit ? DK : min(kM, a.headdim - m0);
+  const int v_boxes = unit ? 0 : rows > 64 ? 2 : 1;
+  const int first = p.first + piece * p.piece_chunks, most = min(p.piece_chunks, p.first + p.chunks - first);  // chunks
+  const int64_t tile_at = (bh * a.headdim + m0) * DK, slot = heads * a.headdim * DK;
+  const float* from;
+  float* to;
+  if (unit) {
+    from = nullptr;
+    to = p.passing + ((piece - 1) * heads + bh) * DK * DK;
+  } else {
+    from = piece == 0 ? (p.begins ? a.h0 : p.states) : kOutput ? p.entering + (piece - 1) * slot : nullptr;
+    to = !kOutput ? p.entering + piece * slot : piece < p.pieces - 1 ? nullptr : p.ends ? a.h_final : p.states;
+    if (from) from += tile_at;
+    if (to) to += tile_at;
+  }
 
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
@@ -580,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
   const int64_t all_tokens = tokens_of(a, b);
-  const int64_t tokens = min(max(all_tokens - (int64_t)p.first * kC, (int64_t)0), (int64_t)p.chunks * kC);  // of the segment
+  const int64_t tokens = min(max(all_tokens - (int64_t)first * kC, (int64_t)0), (int64_t)most * kC);  // of the piece
   const int n = (int)((tokens + kC - 1) / kC);
 
   // A bounded wait, the same answer in every lane of a warp
@@ -610,16 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
     const int s_half = DK == 128 ? part >> 1 : 0;
     const bool have = row < rows;
-    const float* from = p.begins ? a.h0 : p.states;
-    float* to = p.ends ? a.h_final : p.states;
     float s[CW];
 #pragma unroll
-    for (int i = 0; i < CW; ++i) s[i] = 0.f;
+    for (int i = 0; i < CW; ++i) s[i] = unit && row == part * CW + i ? 1.f : 0.f;
     // States go through a stage's shared memory, in rows of kRowS floats: a thread's columns lie a row from its
     // neighbour's.  move(stage, f): f on each four floats of the tile, there and in global memory (its elements in order).
     constexpr int kRowS = DK + 4;
     static_assert(kM * kRowS * 4 <= L::kStage, "a state fits a stage");
-    const int64_t at = (bh * a.headdim + m0) * DK;
     const auto move = [&](int stage, auto f) {
       float* rows_at = reinterpret_cast<float*>(base + stage * L::kStage);
       for (int i = 4 * threadIdx.x; i < rows * DK; i += 4 * 32 * kStateWarps) f(rows_at + i / DK * kRowS + i % DK, i);
@@ -630,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (from) {
       const bool vec = reinterpret_cast<uintptr_t>(from) % 16 == 0;
       move(kStages - 1, [&](float* to, int i) {
-        const float* e = from + at + i;
+        const float* e = from + i;
         *reinterpret_cast<float4*>(to) = vec ? *reinterpret_cast<const float4*>(e) : make_float4(e[0], e[1], e[2], e[3]);
       });
       named_bar_sync(1, 32 * kStateWarps);
@@ -727,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kSReady + s_half);
-      if (c > 0) ok = ok && output(c - 1);
+      if (kOutput && c > 0) ok = ok && output(c - 1);
       // X, scaled, as an operand
       ok = ok && wait(kFull + st, c / kStages) && wait(kXFull, c);
       if (!ok) break;
@@ -758,7 +781,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       last = f.last[0];
       tc::tmem_st_wait();
       tc::fence_before_sync();
+      if (!kOutput) fence_proxy_async_smem();  // the factors are read before the stage's next copies
       arrive(kDReady);
+      if (!kOutput) continue;
       // D as it is, and Q scaled as what O adds to
       {
         uint32_t hi[8], lo[8];
@@ -785,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(kUFull, n - 1);
       tc::fence_after_sync();
       update();
-      ok = ok && output(n - 1);
+      if (kOutput) ok = ok && output(n - 1);
     }
     // the stage of the chunk that would be next: all that used it is done with the y of the chunk three before
     const int free_stage = n % kStages;
@@ -799,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool vec = reinterpret_cast<uintptr_t>(to) % 16 == 0;
       move(free_stage, [&](const float* mine, int i) {
         const float4 e = *reinterpret_cast<const float4*>(mine);
-        float* o = to + at + i;
+        float* o = to + i;
         if (vec)
           *reinterpret_cast<float4*>(o) = e;
         else
@@ -810,23 +835,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kCopyWarp) {
     // ------------------------------ copies -------------------------------------------------------------------
     if (lane == 0) {
-      const unsigned char* rec = p.records + bh * p.chunks * (int64_t)kRecord;
+      const unsigned char* rec = p.records + (bh * p.chunks + (first - p.first)) * (int64_t)kRecord;
       int c = 0;
       const int copies = p.ctl.stall_tile == ((int64_t)1 << 40) + blockIdx.x ? 0 : n;  // (the test hook)
       for (; c < copies; ++c) {
         const int st = c % kStages;
         if (c >= kStages && !wait_one(kEmpty + st, c / kStages - 1)) break;
-        if (c == kStages - 1 && (p.begins ? a.h0 : p.states) && !wait_one(kLoaded, 0)) break;  // the state came there
+        if (c == kStages - 1 && from && !wait_one(kLoaded, 0)) break;  // the state came there
         unsigned char* stage = base + st * L::kStage;
-        mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * 2 + v_boxes) * kTile + kRecordCopied);
+        mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * (kOutput ? 2 : 1) + v_boxes) * kTile + kRecordCopied);
         const auto load = [&](int place, const CUtensorMap* map, int x, uint32_t which) {
           const bool inner = (p.inner & which) != 0;
-          const int tok = (p.first + c) * kC;
+          const int tok = (first + c) * kC;
           tc::tma_load_3d(stage + place * kTile, map, x, inner ? (int)b : tok, inner ? tok : (int)b, &bars[kFull + st]);
         };
         for (int j = 0; j < kHalves; ++j) {
           load(2 * j, &map_k, g * DK + 64 * j, kMapK);
-          load(2 * j + 1, &map_q, g * DK + 64 * j, kMapQ);
+          if (kOutput) load(2 * j + 1, &map_q, g * DK + 64 * j, kMapQ);
         }
         bulk_g2s(stage + L::kT, rec + c * (int64_t)kRecord, kRecordCopied, &bars[kFull + st]);
         for (int j = 0; j < v_boxes; ++j) load(2 * kHalves + j, &map_v, h * a.headdim + m0 + 64 * j, kMapV);
@@ -836,10 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kStoreWarp) {
     // ------------------------------ y ------------------------------------------------------------------------
-    if (lane == 0) {
-      for (int c = 0; c < n && wait_one(kYReady, c); ++c) {
+    if constexpr (kOutput) {
+      for (int c = 0; lane == 0 && c < n && wait_one(kYReady, c); ++c) {
         for (int j = 0; j < v_boxes; ++j)
-          tma_store_4d(&map_y, base + c % kStages * L::kStage + L::kV + j * kTile, m0 + 64 * j, h, (p.first + c) * kC, (int)b);
+          tma_store_4d(&map_y, base + c % kStages * L::kStage + L::kV + j * kTile, m0 + 64 * j, h, (first + c) * kC, (int)b);
         bulk_commit();
         bulk_wait_read<0>();
         mbar_arrive(&bars[kEmpty + c % kStages]);  // every product of the chunk was done before its y
@@ -872,20 +897,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ks = 4 * x; ks < 4 * x + 4; ++ks) {
           const uint64_t d = k_major(kt, ks, 2 * kTile);
-          tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, id128, ks > 0);
-          tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, id128, true);
+          tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, kOutput ? id128 : id64, ks > 0);
+          tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, kOutput ? id128 : id64, true);
         }
       }
       if (!ok) break;
       tc::mma_commit(&bars[kXFull]);
+      if (!unit)
 #pragma unroll
-      for (int ks = 0; ks < kC / 16; ++ks)
-        tc::mma_bf16(tmem + kColD, tc::sdesc_sw128(vt + ks * 2048, kTile, 1024), k_major(th, ks, 0), id_v, ks > 0);
+        for (int ks = 0; ks < kC / 16; ++ks)
+          tc::mma_bf16(tmem + kColD, tc::sdesc_sw128(vt + ks * 2048, kTile, 1024), k_major(th, ks, 0), id_v, ks > 0);
       if (!(ok = wait_one(kXReady, c))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id128, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id128, ks > 0 || !unit);
         tc::mma_bf16_ts(tmem + kColD, tmem + kColOpLo + 8 * ks, k_major(th, ks, 0), id128, true);
       }
       tc::mma_commit(&bars[kDFull]);
@@ -898,6 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_bf16_ts(tmem + kColU, tmem + kColOpLo + 8 * ks, d, id_u, true);
       }
       tc::mma_commit(&bars[kUFull]);
+      if (!kOutput) {
+        tc::mma_commit(&bars[kEmpty + st]);
+        continue;
+      }
       if (!(ok = wait_one(kOReady, c))) break;
       tc::fence_after_sync();
 #pragma unroll
@@ -914,7 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto drained = [&](int bar, int count) {
       if (count > 0) mbar_wait(&bars[bar], (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
     };
-    drained(kXFull, c), drained(kDFull, c), drained(kUFull, c), drained(kDone, c);
+    drained(kXFull, c), drained(kDFull, c), drained(kUFull, c);
+    if (kOutput) drained(kDone, c);
+    if (!kOutput)
+      for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
   }
 
   tc::fence_before_sync();
@@ -925,17 +958,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // padding, or after a wait that ran out everything of the segment
   const bool lost = *abort_flag != 0;
-  const int64_t stored = min((int64_t)n * kC, a.seqlen - (int64_t)p.first * kC);
   if (lost && threadIdx.x == 0) record_error(p.hdr, p.ctl.epoch, SSM_ERR_TIMEOUT);
-  __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0;
-  const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
-  const int64_t end = p.ends ? a.seqlen : min(a.seqlen, (int64_t)(p.first + p.chunks) * kC);
-  for (int64_t j = ((int64_t)p.first * kC + (lost ? 0 : stored)) * rows + threadIdx.x; j < end * rows; j += kThreads)
-    yt[j / rows * a.nheads * a.headdim + j % rows] = fill;
-  float* to = p.ends ? a.h_final : p.states;
+  if (kOutput) {
+    __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0;
+    const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
+    const int64_t start = (int64_t)first * kC, end = min(a.seqlen, start + (int64_t)most * kC);
+    const int64_t stored = min((int64_t)n * kC, a.seqlen - start);
+    for (int64_t j = (start + (lost ? 0 : stored)) * rows + threadIdx.x; j < end * rows; j += kThreads)
+      yt[j / rows * a.nheads * a.headdim + j % rows] = fill;
+  }
   if (lost && to)
-    for (int j = threadIdx.x; j < rows * DK; j += kThreads)
-      to[(bh * a.headdim + m0) * DK + j] = __uint_as_float(0x7fc00000u);
+    for (int j = threadIdx.x; j < rows * DK; j += kThreads) to[j] = __uint_as_float(0x7fc00000u);
+}
+
+// ---------------------------------------------------------------------------------- delta_join
+
+// What the pieces but the first enter with, in place of the N before them: S_{p+1} = S_p M_p + N_p.  A CTA has kJoinRows rows of a
+// head.  A thread has a column and a quarter of the sum, whose 32 (16) elements of M it loads at once.
+constexpr int kJoinRows = 16, kJoinParts = 4;
+template <int DK>
+__global__ void __launch_bounds__(DK * kJoinParts) delta_join_kernel(const __grid_constant__ Params p) {
+  constexpr int KP = DK / kJoinParts, OWN = kJoinRows / kJoinParts;
+  __shared__ __align__(16) float s[kJoinRows][DK];
+  __shared__ float sums[kJoinParts][kJoinRows][DK];
+  griddep_launch_dependents();
+  griddep_wait();
+  const ssm_delta_args& a = p.a;
+  const int tiles = (a.headdim + kJoinRows - 1) / kJoinRows, col = threadIdx.x % DK, part = threadIdx.x / DK;
+  const int64_t bh = blockIdx.x / tiles, heads = a.batch * a.nheads;
+  const int row0 = (int)(blockIdx.x % tiles) * kJoinRows + OWN * part, rows = min(OWN, a.headdim - row0);  // the thread's rows
+  float* at = p.entering + (bh * a.headdim + row0) * DK + col;
+  const int64_t slot = heads * a.headdim * DK;
+#pragma unroll
+  for (int r = 0; r < OWN; ++r) s[OWN * part + r][col] = r < rows ? at[r * DK] : 0.f;
+  for (int piece = 1; piece < p.pieces - 1; ++piece) {
+    const float* m = p.passing + (((piece - 1) * heads + bh) * DK + part * KP) * DK + col;
+    at += slot;
+    float v[KP], next[OWN], acc[kJoinRows] = {};
+#pragma unroll
+    for (int k = 0; k < KP; ++k) v[k] = m[k * DK];
+#pragma unroll
+    for (int r = 0; r < OWN; ++r) next[r] = r < rows ? at[r * DK] : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KP; k += 4)
+#pragma unroll
+      for (int r = 0; r < kJoinRows; ++r) {
+        const float4 e = *reinterpret_cast<const float4*>(&s[r][part * KP + k]);
+        acc[r] = fmaf(e.x, v[k], acc[r]), acc[r] = fmaf(e.y, v[k + 1], acc[r]);
+        acc[r] = fmaf(e.z, v[k + 2], acc[r]), acc[r] = fmaf(e.w, v[k + 3], acc[r]);
+      }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) sums[part][r][col] = acc[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < OWN; ++r) {
+      const int row = OWN * part + r;
+      const float e = ((sums[0][row][col] + sums[1][row][col]) + (sums[2][row][col] + sums[3][row][col])) + next[r];
+      if (r < rows) at[r * DK] = e;
+      s[row][col] = e;
+    }
+  }
 }
 
 // How a tensor map takes a tensor's rows: the two outer dimensions in the order of their strides, which nest (see selscan.cu).
@@ -959,18 +1042,40 @@ Nesting nesting(const ssm_tokens& t, int64_t batch, int64_t seqlen, int64_t colu
 // Records of all chunks take kRecord bytes a chunk and head; a long prompt goes in segments whose records take at most this.
 constexpr int64_t kMaxRecords = (int64_t)1024 << 20;
 struct Segments {
-  int64_t chunks, of;  // of the prompt, of a segment
-  size_t records, total;
+  int64_t chunks, of;          // of the prompt, of a segment
+  int64_t pieces, piece;       // of a segment's chains, and their chunks
+  size_t records, states, entering, passing, total;  // bytes
 };
+// How many pieces chains of `chunks` chunks are cut into, in units of a chunk's time in a chain (2.7 us): one without outputs takes
+// 0.8, the kernels more of a cut chain about eight, and a piece's part in delta_join one.
+constexpr int kSms = 152;
+int64_t pieces_of(int64_t heads, int64_t tiles, int64_t chunks) {
+  const auto rounds = [](int64_t jobs) { return (jobs + kSms - 1) / kSms; };
+  int64_t best = 1;
+  double least = (double)(rounds(heads * tiles) * chunks);
+  for (int64_t n = 2; n <= 32 && n * 8 <= chunks && heads * n <= 4 * kSms; ++n) {
+    const int64_t of = (chunks + n - 1) / n;
+    if ((chunks + of - 1) / of != n) continue;  // (the last would be empty)
+    const double cost =
+        (double)of * (0.8 * (double)rounds(heads * ((n - 1) * tiles + n - 2)) + (double)rounds(heads * n * tiles)) + 8 + (double)n;
+    if (cost < least) least = cost, best = n;
+  }
+  return best;
+}
 Segments segments(const ssm_delta_args& a) {
   Segments g{};
-  const int64_t heads = a.batch * a.nheads;
+  const int64_t heads = a.batch * a.nheads, most = kMaxRecords / kRecord / heads;
   g.chunks = (a.seqlen + kC - 1) / kC;
-  const int64_t most = kMaxRecords / kRecord / heads;
   g.of = g.chunks <= most ? g.chunks : most;
+  g.pieces = pieces_of(heads, (a.headdim + kM - 1) / kM, g.of);
+  g.piece = (g.of + g.pieces - 1) / g.pieces;
+  const auto up = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
+  const size_t state = (size_t)heads * a.headdim * a.dstate * sizeof(float);
   g.records = (size_t)(heads * g.of) * kRecord;
-  g.total = kHeaderBytes + g.records;
-  if (g.of < g.chunks) g.total += (size_t)heads * a.headdim * a.dstate * sizeof(float);
+  g.states = g.of < g.chunks ? up(state) : 0;
+  g.entering = up((size_t)(g.pieces - 1) * state);
+  g.passing = g.pieces > 2 ? (size_t)((g.pieces - 2) * heads) * a.dstate * a.dstate * sizeof(float) : 0;
+  g.total = kHeaderBytes + g.records + g.states + g.entering + g.passing;
   return g;
 }
 
@@ -1000,22 +1105,32 @@ cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segme
   const ssm_delta_args& a = p.a;
   const size_t prep_bytes = sizeof(PrepShared<DK>) + 1024, chain_bytes = Layout<DK>::kTotal + 1024;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(delta_prepare_kernel<DK>), prep_bytes);
-  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK>), chain_bytes);
+  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK, true>), chain_bytes);
+  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK, false>), chain_bytes);
   if (e != cudaSuccess) return e;
   for (int64_t first = 0; first < g.chunks; first += g.of) {
     p.first = (int)first;
     p.chunks = (int)(g.chunks - first < g.of ? g.chunks - first : g.of);
     p.begins = first == 0;
     p.ends = first + g.of >= g.chunks;
-    const unsigned prep = (unsigned)(a.batch * p.chunks * a.ngroups * p.batches), chains = (unsigned)(a.batch * a.nheads * p.tiles);
+    p.piece_chunks = (int)g.piece;
+    p.pieces = (p.chunks + p.piece_chunks - 1) / p.piece_chunks;  // (of the last segment there may be fewer)
+    const int64_t heads = a.batch * a.nheads;
+    const auto chain = [&](auto kernel, int64_t jobs) {
+      return launch_pdl(kernel, dim3((unsigned)(heads * jobs)), dim3(kThreads), chain_bytes, s, maps[0], maps[1], maps[2], maps[3], p);
+    };
     e = timed(19, [&] {
-      return launch_pdl(delta_prepare_kernel<DK>, dim3(prep), dim3(kPrepThreads), prep_bytes, s, maps[0], maps[1], p);
+      return launch_pdl(delta_prepare_kernel<DK>, dim3((unsigned)(a.batch * p.chunks * a.ngroups * p.batches)), dim3(kPrepThreads),
+                        prep_bytes, s, maps[0], maps[1], p);
     });
-    if (e != cudaSuccess) return e;
-    e = timed(20, [&] {
-      return launch_pdl(delta_chain_kernel<DK>, dim3(chains), dim3(kThreads), chain_bytes, s, maps[0], maps[1], maps[2],
-                        maps[3], p);
-    });
+    if (e == cudaSuccess && p.pieces > 1) {
+      e = timed(21, [&] { return chain(delta_chain_kernel<DK, false>, (p.pieces - 1) * p.tiles + p.pieces - 2); });
+      if (e == cudaSuccess && p.pieces > 2)
+        e = timed(22, [&] {
+          return launch_pdl(delta_join_kernel<DK>, dim3((unsigned)(heads * ((a.headdim + kJoinRows - 1) / kJoinRows))), dim3(DK * kJoinParts), 0, s, p);
+        });
+    }
+    if (e == cudaSuccess) e = timed(20, [&] { return chain(delta_chain_kernel<DK, true>, p.pieces * p.tiles); });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1031,6 +1146,8 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
   p.hdr = static_cast<WsHeader*>(workspace);
   p.records = static_cast<unsigned char*>(workspace) + kHeaderBytes;
   p.states = reinterpret_cast<float*>(p.records + g.records);
+  p.entering = reinterpret_cast<float*>(p.records + g.records + g.states);
+  p.passing = reinterpret_cast<float*>(p.records + g.records + g.states + g.entering);
   p.tiles = (a.headdim + kM - 1) / kM;
   p.batches = (a.nheads / a.ngroups + kHeads - 1) / kHeads;
   p.ctl = ctl;

@@ -138,6 +138,32 @@ def test_prompt(case, dtype):
     assert none is None and np.array_equal(host(y2), host(y))
 
 
+PIECES = [  # b, L, nh, G, H, N, h0, lens: few chains of many chunks, which are cut into pieces that run at once
+    (1, 2661, 1, 1, 64, 128, True, None),
+    (2, 2700, 2, 1, 128, 64, True, [2700, 700]),      # a length inside a piece, empty pieces behind it
+    (3, 2624, 1, 1, 136, 128, False, [1, 2624, 0]),   # rows of two tiles
+    (1, 4100, 3, 3, 72, 64, True, None),
+]
+
+
+@pytest.mark.parametrize("case", PIECES, ids=str)
+def test_pieces(case):
+    import selective_state_space_mamba_gb300 as ssm
+    b, L, nh, G, H, N, h0, lens = case
+    s = inputs(rng_of("pieces", case), b, L, nh, G, H, N, "bf16", h0, slow=True)
+    y_ref, ey, h_ref, eh = od.delta(**s, lens=lens, split=SPLIT, out=OUT)
+    if lens is not None:
+        for i, n in enumerate(od._lens(lens, b, L)):
+            for k in ("q", "k", "v", "dt", "beta"):
+                s[k][i, n:] = np.nan
+    t = on_device(s, "bf16")
+    with ssm.KernelTimer() as timer:
+        y, h = ssm.delta_fwd(**t, h0=dev(s["h0"]), lens=ints(lens))
+    assert timer.launches["delta_states"] == 1
+    close(host(y), y_ref, ey, "y", "bf16")
+    rows_close(host(h), h_ref, eh, "h")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("options", [dict(softplus=False), dict(sigmoid=False), dict(l2norm=False), dict(scale=0.7),
                                      dict(softplus=False, sigmoid=False, l2norm=False, scale=-2.0)], ids=str)
