@@ -344,6 +344,10 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
         }
     }
     put(inv, I, I, sm.hi, sm.lo);
+    if (hh > 0) {  // the record of the head before is copied
+      if (threadIdx.x == 0) bulk_wait_read<0>();
+      __syncthreads();
+    }
     // ---- P
     {
       float f[2], fu[2];
@@ -403,9 +407,7 @@ __device__ __forceinline__ void prepare_rows(PrepShared<DK>& sm, const Params& p
       unsigned char* to = p.records + ((b * p.a.nheads + h0 + hh) * p.chunks + (c - p.first)) * (int64_t)kRecord;
       bulk_s2g(to, rec, kRecordCopied);
       bulk_commit();
-      bulk_wait_read<0>();
     }
-    if (hh + 1 < heads) __syncthreads();
   }
   if (threadIdx.x == 0) bulk_wait<0>();
 }
@@ -431,6 +433,16 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   const int first = (int)(blockIdx.x % per_chunk) % p.batches * kHeads, heads = min(kHeads, hpg - first), h0 = g * hpg + first;
   griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.begins) p.hdr->status = 0;
+  // gates, a warp a head, two neighbouring tokens a lane: all loads first (past the prompt's end the last token's)
+  const int h = h0 + min(warp, heads - 1);
+  __nv_bfloat16 dt_raw[2], beta_raw[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t at = min((int64_t)c * kC + 2 * lane + k, a.seqlen - 1);
+    dt_raw[k] = static_cast<const __nv_bfloat16*>(a.dt.ptr)[b * a.dt.batch_stride + at * a.dt.token_stride + h];
+    beta_raw[k] = static_cast<const __nv_bfloat16*>(a.beta.ptr)[b * a.beta.batch_stride + at * a.beta.token_stride + h];
+  }
+  const delta::Gate gate(a, h);
   const int64_t tokens = tokens_of(a, b) - (int64_t)c * kC;
   if (tokens <= 0) return;
   const int live = (int)min((int64_t)kC, tokens);
@@ -446,22 +458,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       load(sm.kq + (2 * j + 1) * kTile, &map_q, g * DK + 64 * j, kMapQ);
     }
   }
-  // gates: a warp a head, two neighbouring tokens a lane
   if (warp < heads) {
-    const int h = h0 + warp;
-    const delta::Gate gate(a, h);
     float gd[2], beta[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int tok = 2 * lane + k;
-      gd[k] = beta[k] = 0.f;
-      if (tok < live) {
-        const int64_t at = (int64_t)c * kC + tok;
-        gd[k] = gate.log2_decay(to_f32(
-            static_cast<const __nv_bfloat16*>(a.dt.ptr)[b * a.dt.batch_stride + at * a.dt.token_stride + h]));
-        beta[k] = gate.beta(to_f32(
-            static_cast<const __nv_bfloat16*>(a.beta.ptr)[b * a.beta.batch_stride + at * a.beta.token_stride + h]));
-      }
+      const bool in = 2 * lane + k < live;
+      gd[k] = in ? gate.log2_decay(to_f32(dt_raw[k])) : 0.f;
+      beta[k] = in ? gate.beta(to_f32(beta_raw[k])) : 0.f;
     }
     float sh = gd[0], sl = 0.f;  // of the lane's tokens, then of all up to them
     add_exact(sh, sl, gd[1], 0.f);
@@ -1053,7 +1056,7 @@ int64_t pieces_of(int64_t heads, int64_t tiles, int64_t chunks) {
   const auto rounds = [](int64_t jobs) { return (jobs + kSms - 1) / kSms; };
   int64_t best = 1;
   double least = (double)(rounds(heads * tiles) * chunks);
-  for (int64_t n = 2; n <= 32 && n * 8 <= chunks && heads * n <= 4 * kSms; ++n) {
+  for (int64_t n = 2; n <= 32 && n * 8 <= chunks && heads * tiles * n <= 4 * kSms; ++n) {
     const int64_t of = (chunks + n - 1) / n;
     if ((chunks + of - 1) / of != n) continue;  // (the last would be empty)
     const double cost =
