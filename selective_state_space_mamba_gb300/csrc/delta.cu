@@ -4,12 +4,12 @@
 // head over the whole prompt and keeps them in registers.  This is the path of f32 tokens, of rows that tensor
 // copies cannot read and of short prompts; delta_tc.cu has the tensor-core path.
 //
-// A row is LPR lanes' (each COLS = dstate / LPR of its columns), a lane has ROWS rows.  Both products of a token take the
-// old state, S k and S q at once:
-//     d = beta (v - a S k),   y = a S q + d (k.q),   S <- a S + d k,
-// so that one reduction over the lanes serves them both and the update does not wait for the output.  Four warps scan
-// a tile of kTile tokens in shared memory while four others bring the next one, normalised, and write the outputs of
-// the one before.  Its bound is the chain of a token: k and q of the next one are loaded before the reductions of this one.
+// A row is LPR lanes' (each COLS = dstate / LPR of its columns), a lane has ROWS rows.  The products of a token take an
+// older state, so that the sums over a row's lanes run beside the chain from one correction d to the next:
+//     d_t = beta_t v_t - beta_t a_t (S_{t-1} k_t),   S_{t-1} k_t = a_{t-1} (S_{t-2} k_t) + d_{t-1} (k_{t-1}.k_t),
+//     y_t = a_t (S_{t-1} q_t) + d_t (k_t.q_t),       S_t = a_t S_{t-1} + d_t k_t.
+// Four warps scan a tile of kTile tokens in shared memory while four others bring the next one, normalised, with the products
+// of neighbouring keys, and write the outputs of the one before.  Its bound is the latency of a token's instructions.
 #include "delta_common.cuh"
 
 namespace ssm {
@@ -21,13 +21,13 @@ constexpr int kScan = 128;  // threads that scan; as many bring tokens
 constexpr int kTile = 16;   // tokens
 constexpr int kOwn = kTile / 4;  // of a warp
 
-template <typename T, int DK, int LPR, int ROWS>
+template <typename T, int DK, int LPR, int ROWS, bool kAhead>
 __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_constant__ ssm_delta_args a) {
   constexpr int COLS = DK / LPR, GROUPS = kScan / LPR, CTA_ROWS = GROUPS * ROWS, V4 = COLS / 4;
   constexpr int VL = (CTA_ROWS + 31) / 32;  // v and y of a token a lane
   __shared__ __align__(16) float sk[2][kTile][DK], sq[2][kTile][DK];
-  __shared__ float sv[2][kTile][CTA_ROWS], sy[2][kTile][CTA_ROWS];
-  __shared__ float4 st[2][kTile];  // a, beta, k.q
+  __shared__ float sv[2][kTile][CTA_ROWS], sy[2][kTile][CTA_ROWS];  // beta v; y
+  __shared__ float4 st[2][kTile];  // a, beta a, k.q, k.(k of the token before)
   griddep_launch_dependents();
   griddep_wait();
   const int tiles = (a.headdim + CTA_ROWS - 1) / CTA_ROWS;
@@ -57,71 +57,134 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
     for (int64_t tile = 0; tile < count; ++tile) {
       __syncthreads();
       const int bf = (int)(tile & 1), m = (int)min((int64_t)kTile, n - tile * kTile);
-      float kt[COLS], qt[COLS], v[ROWS];
-      float4 c;
-      const auto load = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < V4; ++i) {
-          *reinterpret_cast<float4*>(&kt[4 * i]) = *reinterpret_cast<const float4*>(&sk[bf][t][4 * (sub + LPR * i)]);
-          *reinterpret_cast<float4*>(&qt[4 * i]) = *reinterpret_cast<const float4*>(&sq[bf][t][4 * (sub + LPR * i)]);
-        }
-        c = st[bf][t];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) v[r] = sv[bf][t][grp + GROUPS * r];
-      };
-      load(0);
-      const auto token = [&](int t) {
-        float dk[ROWS], dq[ROWS];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          float2 uk[2] = {}, uq[2] = {};
-#pragma unroll
-          for (int i = 0; i < COLS; i += 2) {
-            const float2 e = make_float2(s[r][i], s[r][i + 1]);
-            uk[i / 2 % 2] = __ffma2_rn(e, make_float2(kt[i], kt[i + 1]), uk[i / 2 % 2]);
-            uq[i / 2 % 2] = __ffma2_rn(e, make_float2(qt[i], qt[i + 1]), uq[i / 2 % 2]);
-          }
-          const float2 xk = __fadd2_rn(uk[0], uk[1]), xq = __fadd2_rn(uq[0], uq[1]);
-          dk[r] = xk.x + xk.y;
-          dq[r] = xq.x + xq.y;
-        }
-        const float decay = c.x, beta = c.y, kq = c.z;
-        float kd[COLS], vd[ROWS];
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) kd[i] = kt[i];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          vd[r] = v[r];
-#pragma unroll
-          for (int i = 0; i < COLS; i += 2) {
-            const float2 e = __fmul2_rn(make_float2(s[r][i], s[r][i + 1]), make_float2(decay, decay));
-            s[r][i] = e.x, s[r][i + 1] = e.y;
-          }
-        }
+      // the sum over a row's lanes
+      const auto joined = [&](float (&x)[ROWS]) {
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1)
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
-            dk[r] += __shfl_xor_sync(0xffffffffu, dk[r], o);
-            dq[r] += __shfl_xor_sync(0xffffffffu, dq[r], o);
-          }
-        load(min(t + 1, kTile - 1));
+          for (int r = 0; r < ROWS; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], o);
+      };
+      const auto columns = [&](const float (&row)[DK], float (&x)[COLS]) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          const float d = beta * fmaf(-decay, dk[r], vd[r]);
-          if (sub == 0) sy[bf][t][grp + GROUPS * r] = fmaf(decay, dq[r], d * kq);
+        for (int i = 0; i < V4; ++i)
+          *reinterpret_cast<float4*>(&x[4 * i]) = *reinterpret_cast<const float4*>(&row[4 * (sub + LPR * i)]);
+      };
+      const auto product = [&](const float (&row)[COLS], const float (&x)[COLS]) {
+        float2 u[2] = {};
+#pragma unroll
+        for (int i = 0; i < COLS; i += 2)
+          u[i / 2 % 2] = __ffma2_rn(make_float2(row[i], row[i + 1]), make_float2(x[i], x[i + 1]), u[i / 2 % 2]);
+        const float2 e = __fadd2_rn(u[0], u[1]);
+        return e.x + e.y;
+      };
+      const auto update = [&](const float (&k)[COLS], const float (&d)[ROWS], float decay) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
           for (int i = 0; i < COLS; i += 2) {
-            const float2 e = __ffma2_rn(make_float2(kd[i], kd[i + 1]), make_float2(d, d), make_float2(s[r][i], s[r][i + 1]));
-            s[r][i] = e.x, s[r][i + 1] = e.y;
+            const float2 e = __fmul2_rn(make_float2(s[r][i], s[r][i + 1]), make_float2(decay, decay));
+            const float2 v = __ffma2_rn(make_float2(k[i], k[i + 1]), make_float2(d[r], d[r]), e);
+            s[r][i] = v.x, s[r][i + 1] = v.y;
           }
-        }
       };
-      if (m == kTile) {
+      float kt[COLS], qt[COLS], v[ROWS];  // of the token
+      float4 c;
+      if constexpr (kAhead) {
+        // sums of the token before that are on their way, its d, a and k.q
+        float pk[ROWS], pq[ROWS] = {}, d[ROWS] = {}, decay = 1.f, kq = 0.f;
+        const auto round = [&](int o) {
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            pk[r] += __shfl_xor_sync(0xffffffffu, pk[r], o);
+            pq[r] += __shfl_xor_sync(0xffffffffu, pq[r], o);
+          }
+        };
+        columns(sk[bf][0], kt);
+        columns(sq[bf][0], qt);
+        c = st[bf][0];
+        c.w = 0.f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          v[r] = sv[bf][0][grp + GROUPS * r];
+          pk[r] = product(s[r], kt);
+        }
+        joined(pk);
+        const auto token = [&](int t) {
+          const int next = min(t + 1, kTile - 1);
+          float kn[COLS], xk[ROWS], xq[ROWS];
+          columns(sk[bf][next], kn);
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            xk[r] = product(s[r], kn);
+            xq[r] = product(s[r], qt);
+          }
+          // the token before: its last sums are there by now
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float sum = fmaf(decay, pk[r], d[r] * c.w);
+            if (sub == 0 && t > 0) sy[bf][t - 1][grp + GROUPS * r] = fmaf(decay, pq[r], d[r] * kq);
+            d[r] = fmaf(-c.y, sum, v[r]);
+            pk[r] = xk[r], pq[r] = xq[r];
+          }
+          round(LPR / 2);
+          update(kt, d, c.x);
+          decay = c.x, kq = c.z;
+          if (LPR > 4) round(LPR / 4);
+          columns(sq[bf][next], qt);
+          c = st[bf][next];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) v[r] = sv[bf][next][grp + GROUPS * r];
+          if (LPR > 2) round(LPR > 4 ? LPR / 8 : LPR / 4);
+#pragma unroll
+          for (int i = 0; i < COLS; ++i) kt[i] = kn[i];
+        };
+        static_assert(LPR == 2 || LPR == 4 || LPR == 8, "rounds");
+        if (m == kTile) {
 #pragma unroll 4
-        for (int t = 0; t < kTile; ++t) token(t);
+          for (int t = 0; t < kTile; ++t) token(t);
+        } else {
+          for (int t = 0; t < m; ++t) token(t);
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+          if (sub == 0) sy[bf][m - 1][grp + GROUPS * r] = fmaf(decay, pq[r], d[r] * kq);
       } else {
-        for (int t = 0; t < m; ++t) token(t);
+        const auto load = [&](int t) {
+          columns(sk[bf][t], kt);
+          columns(sq[bf][t], qt);
+          c = st[bf][t];
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) v[r] = sv[bf][t][grp + GROUPS * r];
+        };
+        load(0);
+        const auto token = [&](int t) {
+          float dk[ROWS], dq[ROWS], kd[COLS], vd[ROWS];
+          const float4 e = c;
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            dk[r] = product(s[r], kt);
+            dq[r] = product(s[r], qt);
+            vd[r] = v[r];
+          }
+#pragma unroll
+          for (int i = 0; i < COLS; ++i) kd[i] = kt[i];
+          joined(dk);
+          joined(dq);
+          load(min(t + 1, kTile - 1));
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float y = dq[r];
+            dk[r] = fmaf(-e.y, dk[r], vd[r]);
+            if (sub == 0) sy[bf][t][grp + GROUPS * r] = fmaf(e.x, y, dk[r] * e.z);
+          }
+          update(kd, dk, e.x);
+        };
+        if (m == kTile) {
+#pragma unroll 4
+          for (int t = 0; t < kTile; ++t) token(t);
+        } else {
+          for (int t = 0; t < m; ++t) token(t);
+        }
       }
     }
     __syncthreads();
@@ -148,8 +211,12 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
   T* yp = static_cast<T*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + row0 + lane;
   const int64_t y_stride = (int64_t)a.nheads * a.headdim;
   const delta::Gate gate(a, h);
-  T kv[kOwn][DK / 32], qv[kOwn][DK / 32], vv[kOwn][VL], dt, be;  // as they come; lane w has the gates of token w
+  // as they come, with the k before the first; lane w has the gates of token w
+  T kv[kOwn + 1][DK / 32], qv[kOwn][DK / 32], vv[kOwn][VL], dt, be;
   const auto fetch = [&](int64_t tile) {
+    const int64_t before = max(min(tile * kTile + kOwn * warp, n) - 1, (int64_t)0);
+#pragma unroll
+    for (int i = 0; i < DK / 32; ++i) kv[kOwn][i] = kp[before * a.k.token_stride + 32 * i];
 #pragma unroll
     for (int w = 0; w < kOwn; ++w) {
       const int64_t t = min(tile * kTile + kOwn * warp + w, n - 1);  // (past the end: not used)
@@ -167,7 +234,7 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
   };
   const auto bring = [&](int64_t tile) {
     const int bf = (int)(tile & 1);
-    float sum[4][kOwn];  // k.k, q.q, k.q of a token
+    float sum[4][kOwn], before = 0.f;  // k.k, q.q, k.q of a token, k.(k before); k.k of the one before the first
 #pragma unroll
     for (int w = 0; w < kOwn; ++w) {
 #pragma unroll
@@ -178,11 +245,16 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
         sum[0][w] = fmaf(k, k, sum[0][w]);
         sum[1][w] = fmaf(q, q, sum[1][w]);
         sum[2][w] = fmaf(k, q, sum[2][w]);
+        sum[3][w] = fmaf(k, to_f32(kv[w > 0 ? w - 1 : kOwn][i]), sum[3][w]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < DK / 32; ++i) before = fmaf(to_f32(kv[kOwn][i]), to_f32(kv[kOwn][i]), before);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     // halving rounds leave a lane with the sums of token lane % 4, plain ones join the rest of the lanes
 #pragma unroll
-    for (int v = 0; v < 3; ++v) {
+    for (int v = 0; v < 4; ++v) {
 #pragma unroll
       for (int half = kOwn / 2; half > 0; half /= 2) {
         const bool upper = (lane & half) != 0;
@@ -196,13 +268,15 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
       for (int o = kOwn; o < 32; o *= 2) sum[v][0] += __shfl_xor_sync(0xffffffffu, sum[v][0], o);
     }
     const float rk = gate.inverse_length(sum[0][0]), rq = gate.inverse_length(sum[1][0]) * a.scale;
+    const float from_left = __shfl_up_sync(0xffffffffu, rk, 1);
+    const float rk_before = lane % kOwn == 0 ? gate.inverse_length(before) : from_left;
+    const float decay = exp2_fast(gate.log2_decay(to_f32(dt))), beta = gate.beta(to_f32(be));
     if (lane < kOwn)
-      st[bf][kOwn * warp + lane] =
-          make_float4(exp2_fast(gate.log2_decay(to_f32(dt))), gate.beta(to_f32(be)), sum[2][0] * rk * rq, 0.f);
+      st[bf][kOwn * warp + lane] = make_float4(decay, beta * decay, sum[2][0] * rk * rq, sum[3][0] * rk * rk_before);
 #pragma unroll
     for (int w = 0; w < kOwn; ++w) {
       const int t = kOwn * warp + w;
-      const float fk = __shfl_sync(0xffffffffu, rk, w), fq = __shfl_sync(0xffffffffu, rq, w);
+      const float fk = __shfl_sync(0xffffffffu, rk, w), fq = __shfl_sync(0xffffffffu, rq, w), fv = __shfl_sync(0xffffffffu, beta, w);
 #pragma unroll
       for (int i = 0; i < DK / 32; ++i) {
         sk[bf][t][lane + 32 * i] = to_f32(kv[w][i]) * fk;
@@ -210,7 +284,7 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
       }
 #pragma unroll
       for (int i = 0; i < VL; ++i)
-        if (lane + 32 * i < CTA_ROWS) sv[bf][t][lane + 32 * i] = to_f32(vv[w][i]);
+        if (lane + 32 * i < CTA_ROWS) sv[bf][t][lane + 32 * i] = to_f32(vv[w][i]) * fv;
     }
   };
   const auto give = [&](int64_t tile) {
@@ -259,9 +333,9 @@ cudaError_t launch_type(const ssm_delta_args& a, cudaStream_t s) {
   };
   const bool few = delta_resident(a);
   switch (a.dstate) {
-    case 32: return go(delta_kernel<T, 32, 2, 1>, 64);
-    case 64: return few ? go(delta_kernel<T, 64, 8, 1>, 16) : go(delta_kernel<T, 64, 4, 1>, 32);
-    case 128: return few ? go(delta_kernel<T, 128, 8, 1>, 16) : go(delta_kernel<T, 128, 8, 2>, 32);
+    case 32: return go(delta_kernel<T, 32, 2, 1, true>, 64);
+    case 64: return few ? go(delta_kernel<T, 64, 8, 1, true>, 16) : go(delta_kernel<T, 64, 4, 1, false>, 32);
+    case 128: return few ? go(delta_kernel<T, 128, 8, 1, true>, 16) : go(delta_kernel<T, 128, 8, 2, false>, 32);
     default: return cudaErrorInvalidValue;
   }
 }
