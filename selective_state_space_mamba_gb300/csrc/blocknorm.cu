@@ -8,6 +8,12 @@
 // warp's 256, so that its lanes still access neighbouring elements.  A team of threads has a group (gatednorm) or a row,
 // and what its threads hold stays in registers between the sums of squares and the output; what they do not
 // hold of wider rows is read again.
+//   Narrow groups: teams of 8 to 32 lanes, four groups a team (32768 x 4096 bf16 in groups of 128: 114 us, 7.1 TB/s; with a CTA
+//       a group 1056 us, as the GPU starts about one CTA a ns; with a division for each group's row 126 us).
+//   Rows, wide groups: up to four (blocknorm: three, beyond 12288 columns four) vectors a thread, all loads in flight at once
+//       (gatednorm 8191 x 5120: 39 us, 6.4 TB/s; blocknorm 32768 x 2560 with a gate: 125 us, 6.7 TB/s).
+//   Narrow rows of blocknorm: a warp a row, four in a CTA (16384 x 256: 17 us with a CTA a row, 7 so).
+//   Few rows: one vector a thread, the shortest way through a row.
 #include "layer_common.cuh"
 
 namespace ssm {
@@ -265,6 +271,9 @@ cudaError_t launch_gated_rows(const GatedParams& p, cudaStream_t s) {
   if (nvec <= 32) return teams(gatednorm_team_kernel<T, kVec, kFirst, 32, 2, 1>, 8);
   if (p.rows * p.groups >= kManyRows && nvec <= 128) return teams(gatednorm_team_kernel<T, kVec, kFirst, 32, 1, 4>, 4);
   if (p.rows * p.groups < kManyRows || nvec > 4 * kHoldThreads) return go(gatednorm_kernel<T, kVec, kFirst, 1>, 1);
+  // Rows that are not aligned: two vectors a thread (32768 x 2561 bf16: 119 us, with four 190).
+  if constexpr (!kVec)
+    if (nvec <= 2 * kHoldThreads) return go(gatednorm_kernel<T, kVec, kFirst, 2>, 2);
   return go(gatednorm_kernel<T, kVec, kFirst, 4>, 4);
 }
 
@@ -399,6 +408,8 @@ cudaError_t launch_block_rows(const BlockParams& p, cudaStream_t s) {
   if (p.rows < kManyRows || nvec > 4 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 1, 1>, 1);
   if (nvec <= 32) return warps(blocknorm_kernel<T, R, kGate, kVec, 1, kWarpRows>);
   if (nvec <= 96) return warps(blocknorm_kernel<T, R, kGate, kVec, 3, kWarpRows>);
+  if constexpr (!kVec)  // (16384 x 4099 bf16 with a gate: 192 us, with three 241)
+    if (nvec <= 2 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 2, 1>, 2);
   if (nvec <= 3 * kHoldThreads) return go(blocknorm_kernel<T, R, kGate, kVec, 3, 1>, 3);
   return go(blocknorm_kernel<T, R, kGate, kVec, 4, 1>, 4);
 }
