@@ -28,7 +28,6 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
   __shared__ __align__(16) float sk[2][kTile][DK], sq[2][kTile][DK];
   __shared__ float sv[2][kTile][CTA_ROWS], sy[2][kTile][CTA_ROWS];  // beta v; y
   __shared__ float4 st[2][kTile];  // a, beta a, k.q, k.(k of the token before)
-  griddep_launch_dependents();
   griddep_wait();
   const int tiles = (a.headdim + CTA_ROWS - 1) / CTA_ROWS;
   const int row0 = (int)(blockIdx.x % tiles) * CTA_ROWS;
@@ -305,6 +304,9 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
   }
   for (int64_t tile = 0; tile < count; ++tile) {
     __syncthreads();  // tile is there, and the one before is scanned
+    // (let in at the start, the next kernel's CTAs take places beside this one's, and its own then share SMs beside empty
+    // ones: f32 b3 L517 69 us a call, 53 so)
+    if (tile + 1 == count) griddep_launch_dependents();
     if (tile + 1 < count) {
       bring(tile + 1);
       fetch(tile + 2);

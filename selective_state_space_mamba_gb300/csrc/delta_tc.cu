@@ -1084,12 +1084,12 @@ Segments segments(const ssm_delta_args& a) {
 
 }  // namespace
 
-// A prompt of one chunk takes 14 to 22 us; token by token (delta.cu) 16 tokens take 6 to 7 us and each more 0.2 us while all its
-// CTAs are resident (b1 nh24 and nh32: as long as a chunk at 58 and 62 tokens), from 0.3 to 0.6 us a token where they are
-// not (b4 nh32 128x128: at 29, b8 nh24 64x64: at 48).
+// A prompt of one chunk takes 14 to 22 us, of two 17 to 25; token by token (delta.cu) 16 tokens take 5.5 to 7 us and each more 0.13
+// to 0.23 us while all its CTAs are resident (b1 nh24 64x128: as long as chunks at 105 tokens, b1 nh32 128x128 at 61 and 72),
+// from 0.3 to 0.6 us a token where they are not (b4 nh32 128x128: at 29, b8 nh24 64x64: at 48).
 bool delta_tc_sizes(const ssm_delta_args& a) {
   return a.dtype == SSM_BF16 && (a.dstate == 64 || a.dstate == 128) && a.headdim % 8 == 0 &&
-         a.seqlen >= (delta_resident(a) ? 60 : 32) && a.seqlen <= 0x7fffffff - kC && a.batch * a.nheads <= kMaxRecords / kRecord;
+         a.seqlen >= (delta_resident(a) ? 72 : 32) && a.seqlen <= 0x7fffffff - kC && a.batch * a.nheads <= kMaxRecords / kRecord;
 }
 size_t delta_tc_workspace(const ssm_delta_args& a) { return segments(a).total; }
 

@@ -71,12 +71,13 @@ def test_delta_workspace(lib):
         assert f(*bad) == 0
     assert f(1, 64, 4, 64, 64, 2, 0) == 0 and f(1, 64, 4, 64, 32, 2, 1) == 0 and f(1, 64, 4, 60, 64, 2, 1) == 0
     assert f(1, 1, 4, 64, 64, 2, 1) == 0                       # one token
-    one, two = f(1, 64, 4, 64, 64, 2, 1), f(1, 65, 4, 64, 64, 2, 1)
-    assert two - one == one - 256 == 4 * 25600 and one % 256 == 0
+    assert f(1, 64, 4, 64, 64, 2, 1) == 0                      # few tokens
+    one, two = f(1, 128, 4, 64, 64, 2, 1), f(1, 129, 4, 64, 64, 2, 1)
+    assert two - one == 4 * 25600 and one == 256 + 2 * 4 * 25600
     long = f(4, 1 << 20, 32, 128, 128, 16, 1)                  # in segments, with the states between them
     assert 4 * 32 * 128 * 128 * 4 < long < 4 * 32 * (1 << 14) * 25600
-    assert delta(lib, ws=(None, 0)) == WORKSPACE and delta(lib, ws=(3 * FAR, 2 * one - 512)) == WORKSPACE
-    assert delta(lib, ws=(3 * FAR + 16, 1 << 40)) == ALIGNMENT
+    assert delta(lib, seqlen=128, ws=(None, 0)) == WORKSPACE and delta(lib, seqlen=128, ws=(3 * FAR, one)) == WORKSPACE
+    assert delta(lib, seqlen=128, ws=(3 * FAR + 16, 1 << 40)) == ALIGNMENT
 
 
 def gated(lib, **kw):

@@ -116,6 +116,11 @@ CASES = [  # b, L, nh, G, H, N, pad, h0, lens
     (1, 129, 3, 3, 16, 32, 1, False, None),
     (5, 128, 8, 4, 64, 64, 64, True, [128, 127, 65, 3, 0]),
     (2, 257, 6, 2, 128, 128, 0, False, [257, 192]),
+    # heads enough that short prompts go in chunks too: one chunk and its ends
+    (10, 33, 4, 2, 128, 128, 0, True, [33, 1, 32, 31, 0, 16, 17, 33, 33, 2]),
+    (10, 63, 4, 4, 128, 64, 8, False, None),
+    (10, 64, 4, 1, 128, 128, 0, True, [64, 63, 1, 64, 0, 65, 33, 32, 2, 64]),
+    (11, 65, 4, 2, 120, 128, 0, True, [65, 64, 63, 1, 0, 65, 33, 32, 2, 64, 66]),
 ]
 
 
