@@ -388,10 +388,12 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
  * States and sums are f32; a decay below 2^-150 is 0.
  * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing nheads, dstate in {32, 64, 128}, headdim >= 1,
  * nheads * headdim and ngroups * dstate <= 2^30.
- * bf16 prompts of at least 16 tokens, with dstate 64 or 128 and headdim a multiple of 8, whose q, k and v have rows on 16-byte
- * boundaries, go through the tensor cores in chunks of 64 tokens (one kernel for what does not depend on the
- * state, one for the chain of states); the others go token by token.  In chunks, a NaN or an infinity in a token may
- * reach the outputs of the up to 63 tokens before it in its chunk.
+ * bf16 prompts with dstate 64 or 128 and headdim a multiple of 8, whose q, k and v have rows on 16-byte boundaries, go
+ * through the tensor cores in chunks of 64 tokens from 72 tokens on (from 32 where batch * nheads * ceil(headdim / 16) is above
+ * 304; seqlen of the call, not lens): one kernel for what does not depend on the state, one for the chain of states.  The
+ * others go token by token.  In chunks, a NaN or an infinity in a token may reach the outputs of the up to 63 tokens
+ * before it in its chunk, and decays above 1 (A > 0, or a negative dt without the softplus) are taken as they are, but their
+ * product over 64 tokens has to stay in f32's range.
  * Workspace (0 bytes where the sizes need none): 25,600 bytes for each head and chunk, of long prompts for a segment at a
  * time.  It need not be zero-filled and carries nothing from call to call; a call that uses it clears the status word
  * and ssm_check_device_status reports its waits (bounded: after one that ran out y and h_final are NaN from there on).
