@@ -384,6 +384,7 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
  *   h0         [batch, nheads, headdim, dstate] f32 or NULL (zeros)
  *   y          [batch, seqlen, nheads * headdim] `dtype`, dense
  *   h_final    like h0, or NULL
+ * The sum of a vector's squares has to stay in f32's range (with l2norm).
  * lens as above: padding is not used, its outputs are 0, and the state is that after a sequence's last token.
  * States and sums are f32; a decay below 2^-150 is 0.
  * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing nheads, dstate in {32, 64, 128}, headdim >= 1,

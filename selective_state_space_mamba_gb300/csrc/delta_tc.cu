@@ -532,7 +532,9 @@ enum Bar {
   kFull = 0,                  // a chunk has landed
   kEmpty = kFull + kStages,   // ... and is read
   kSReady = kEmpty + kStages, // S as an operand, 64 of its columns each
-  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kYReady, kLoaded, kLast, kNumBars
+  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kLoaded, kLast,
+  kYReady,                    // y of a stage's chunk (one for each: the states may be a chunk ahead of the stores)
+  kNumBars = kYReady + kStages
 };
 
 template <int DK>
@@ -585,14 +587,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (to) to += tile_at;
   }
 
-  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     const auto init = [&](int first, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(&bars[first + i], count);
     };
     init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps / kHalves), init(kXFull, 1, 1);
     init(kXReady, 1, kStateWarps), init(kDFull, 1, 1), init(kDReady, 1, kStateWarps), init(kUFull, 1, 1);
-    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, 1, kStateWarps), init(kLoaded, 1, kStateWarps), init(kLast, 1, 1);
+    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, kStages, kStateWarps), init(kLoaded, 1, kStateWarps), init(kLast, 1, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -609,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();  // (not before: a next kernel's CTA on this SM must not take the TMEM that this one waits for)
   griddep_wait();
   const int64_t all_tokens = tokens_of(a, b);
   const int64_t tokens = min(max(all_tokens - (int64_t)first * kC, (int64_t)0), (int64_t)most * kC);  // of the piece
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint16_t*>(tile + j * 128 + ((((row & 63) >> 3) ^ (j & 7)) << 4) + (row & 7) * 2) =
             bf16_of(__uint_as_float(o[j]));
       fence_proxy_async_smem();
-      arrive(kYReady);
+      arrive(kYReady + c % kStages);
       return true;
     };
     // a part's 16 values, scaled, as an operand
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kStoreWarp) {
     // ------------------------------ y ------------------------------------------------------------------------
     if constexpr (kOutput) {
-      for (int c = 0; lane == 0 && c < n && wait_one(kYReady, c); ++c) {
+      for (int c = 0; lane == 0 && c < n && wait_one(kYReady + c % kStages, c / kStages); ++c) {
         for (int j = 0; j < v_boxes; ++j)
           tma_store_4d(&map_y, base + c % kStages * L::kStage + L::kV + j * kTile, m0 + 64 * j, h, (first + c) * kC, (int)b);
         bulk_commit();
