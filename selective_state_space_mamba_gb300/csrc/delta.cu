@@ -305,9 +305,10 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
   }
   for (int64_t tile = 0; tile < count; ++tile) {
     __syncthreads();  // tile is there, and the one before is scanned
-    // (let in at the start, the next kernel's CTAs take places beside this one's, and its own then share SMs beside empty
-    // ones: f32 b3 L517 69 us a call, 49 so)
-    if (tile + 1 == count) griddep_launch_dependents();
+    // Let in early, the next kernel's CTAs take places beside this one's, and its own then share SMs beside empty ones (f32 b3
+    // L517 from the start 69 us a call, from the last tile 63, not before the end 51.5; b1 L2048 nh24 348 and 276): only
+    // short prompts gain by it.
+    if (tile + 1 == count && count <= 8) griddep_launch_dependents();
     if (tile + 1 < count) {
       bring(tile + 1);
       fetch(tile + 2);
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
 }  // namespace
 
 // With 16 rows a CTA two CTAs an SM hold all of them: they have fewer instructions in a token's chain than with 32 (f32
-// b1 L2048 nh24 64x128: 313 us, with 32 rows 516 at the time).
+// b1 L2048 nh24 64x128: 276 us, with 32 rows 516 at the time).
 bool delta_resident(const ssm_delta_args& a) { return a.batch * a.nheads * ((a.headdim + 15) / 16) <= 2 * 152; }
 
 namespace {
