@@ -518,21 +518,28 @@ constexpr int kParts = 4;          // state threads of a row
 constexpr int kStateWarps = 4 * kParts, kCopyWarp = kStateWarps, kMmaWarp = kCopyWarp + 1, kStoreWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kStoreWarp + 1);
 
-// TMEM columns.  S as an operand (hi, lo) is dead once X and Q are there: X, then D of the update, as operands take its place.
-// D comes in two halves, from the inverse's hi and lo; U takes their place.
-constexpr uint32_t kColHi = 0, kColLo = 64;
-constexpr uint32_t kColOp = 0, kColOpLo = 32;
-constexpr uint32_t kColX = 128, kColQ = 192;
-constexpr uint32_t kColD = 256, kColDlo = 320, kColU = 256;
+// TMEM columns.  U takes the place of S as an operand: 16 columns of S are as hi and lo where the 16 columns of U are that
+// update them, so that a thread overwrites none but what it has read.  D of the update as an operand takes the place of X.
+constexpr uint32_t kColS = 0, kColU = 0;
+constexpr uint32_t kColX = 128, kColQ = 192, kColD = 256;
+constexpr uint32_t kColOp = 320, kColOpLo = 352;
 constexpr uint32_t kColDo = 384, kColDoLo = 416;  // D of the output
 constexpr uint32_t kColO = 448;
 constexpr uint32_t kTmemCols = 512;
 
+// True in one lane of the warp.  (The compiler then knows that what follows runs in one lane: it issues an MMA in 28 cycles,
+// behind lane == 0 in 80.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
 enum Bar {
   kFull = 0,                  // a chunk has landed
   kEmpty = kFull + kStages,   // ... and is read
-  kSReady = kEmpty + kStages, // S as an operand, 64 of its columns each
-  kXFull = kSReady + 2, kXReady, kDFull, kDReady, kUFull, kOReady, kDone, kLoaded, kLast,
+  kSReady = kEmpty + kStages, // S as an operand, half of each thread's columns
+  kXFull = kSReady + 2, kXReady, kQFull, kDFull, kDReady, kUFull, kOReady, kDone, kLoaded, kLast,
   kYReady,                    // y of a stage's chunk (one for each: the states may be a chunk ahead of the stores)
   kNumBars = kYReady + kStages
 };
@@ -591,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto init = [&](int first, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) mbar_init(&bars[first + i], count);
     };
-    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps / kHalves), init(kXFull, 1, 1);
+    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps), init(kXFull, 1, 1), init(kQFull, 1, 1);
     init(kXReady, 1, kStateWarps), init(kDFull, 1, 1), init(kDReady, 1, kStateWarps), init(kUFull, 1, 1);
     init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, kStages, kStateWarps), init(kLoaded, 1, kStateWarps), init(kLast, 1, 1);
     *abort_flag = 0;
@@ -641,7 +648,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int TW = kC / kParts;  // tokens of X, D and y a thread
     const int quad = warp & 3, part = warp >> 2, row = quad * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
-    const int s_half = DK == 128 ? part >> 1 : 0;
     const bool have = row < rows;
     float s[CW];
 #pragma unroll
@@ -673,17 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     float last = 1.f;  // e^(G_last) of the chunk before
 
-    // S <- last S + U
-    const auto update = [&]() {
-      uint32_t r[CW / 16][16];
-#pragma unroll
-      for (int q = 0; q < CW / 16; ++q) tc::tmem_ld16(tm + kColU + part * CW + 16 * q, r[q]);
+    // S <- last S + U, 16 columns
+    const auto update = [&](int q) {
+      uint32_t r[16];
+      tc::tmem_ld16(tm + kColU + part * CW + 16 * q, r);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < CW; j += 2) {
-        const float2 v = __ffma2_rn(make_float2(s[j], s[j + 1]), make_float2(last, last),
-                                    make_float2(__uint_as_float(r[j / 16][j % 16]), __uint_as_float(r[j / 16][j % 16 + 1])));
-        s[j] = v.x, s[j + 1] = v.y;
+      for (int j = 0; j < 16; j += 2) {
+        const float2 v = __ffma2_rn(make_float2(s[16 * q + j], s[16 * q + j + 1]), make_float2(last, last),
+                                    make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+        s[16 * q + j] = v.x, s[16 * q + j + 1] = v.y;
       }
     };
     // y of chunk c: this thread's row and tokens, into the chunk's V, which its products have read; 0 past the last token
@@ -706,9 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < TW; ++j)
         *reinterpret_cast<uint16_t*>(tile + j * 128 + ((((row & 63) >> 3) ^ (j & 7)) << 4) + (row & 7) * 2) =
             bf16_of(__uint_as_float(o[j]));
+      return true;
+    };
+    const auto give = [&](int c) {  // to the stores
       fence_proxy_async_smem();
       arrive(kYReady + c % kStages);
-      return true;
     };
     // a part's 16 values, scaled, as an operand
     const auto operand = [&](const uint32_t (&r)[16], const float* f) {
@@ -732,19 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* stage = base + st * L::kStage;
       const Factors& f = *reinterpret_cast<const Factors*>(stage + L::kF);
       const int live = (int)min((int64_t)kC, tokens - (int64_t)c * kC);
-      if (c > 0) {
-        ok = wait(kUFull, c - 1);
-        tc::fence_after_sync();
-        update();
-      }
-#pragma unroll
-      for (int q = 0; q < CW / 16; ++q) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split2(s[16 * q + 2 * j], s[16 * q + 2 * j + 1], hi[j], lo[j]);
-        tc::tmem_st8(tm + kColHi + (part * CW) / 2 + 8 * q, hi);
-        tc::tmem_st8(tm + kColLo + (part * CW) / 2 + 8 * q, lo);
-      }
       if (live < kC && ok) {  // the last chunk: zeros past the last token, before its first product
         ok = wait(kFull + st, c / kStages);
         constexpr int kRow = (L::kV + 2 * kTile) / kTile * 8;  // 16-byte units of a token
@@ -754,9 +748,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
       }
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      arrive(kSReady + s_half);
+      if (c > 0) {
+        ok = ok && wait(kUFull, c - 1);
+        tc::fence_after_sync();
+      }
+#pragma unroll
+      for (int q = 0; q < CW / 16; ++q) {  // X goes on with the first half while the second is converted
+        if (c > 0) update(q);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split2(s[16 * q + 2 * j], s[16 * q + 2 * j + 1], hi[j], lo[j]);
+        tc::tmem_st8(tm + kColS + part * CW + 16 * q, hi);
+        tc::tmem_st8(tm + kColS + part * CW + 16 * q + 8, lo);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        arrive(kSReady + q);
+      }
       if (kOutput && c > 0) ok = ok && output(c - 1);
       // X, scaled, as an operand
       ok = ok && wait(kFull + st, c / kStages) && wait(kXFull, c);
@@ -769,55 +776,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(kXReady);
+      if (kOutput && c > 0) give(c - 1);
       // D scaled as an operand of the update
       if (!(ok = wait(kDFull, c))) break;
       tc::fence_after_sync();
-      {
-        uint32_t e[16];
-        tc::tmem_ld16(tm + kColD + part * TW, r);
-        tc::tmem_ld16(tm + kColDlo + part * TW, e);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 v = __fadd2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                      make_float2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])));
-          r[j] = __float_as_uint(v.x), r[j + 1] = __float_as_uint(v.y);
-        }
-      }
+      tc::tmem_ld16(tm + kColD + part * TW, r);
+      tc::tmem_ld_wait();
       operand(r, f.u + part * TW);
       last = f.last[0];
       tc::tmem_st_wait();
       tc::fence_before_sync();
       if (!kOutput) fence_proxy_async_smem();  // the factors are read before the stage's next copies
       arrive(kDReady);
-      if (!kOutput) continue;
-      // D as it is, and Q scaled as what O adds to
-      {
-        uint32_t hi[8], lo[8];
+      if constexpr (kOutput) {
+        // D as it is, and Q scaled as what O adds to
+        {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), hi[j], lo[j]);
-        tc::tmem_st8(tm + kColDo + part * TW / 2, hi);
-        tc::tmem_st8(tm + kColDoLo + part * TW / 2, lo);
-      }
-      tc::tmem_ld16(tm + kColQ + part * TW, r);
-      tc::tmem_ld_wait();
+          for (int j = 0; j < 8; ++j) split2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), hi[j], lo[j]);
+          tc::tmem_st8(tm + kColDo + part * TW / 2, hi);
+          tc::tmem_st8(tm + kColDoLo + part * TW / 2, lo);
+        }
+        if (!(ok = wait(kQFull, c))) break;
+        tc::fence_after_sync();
+        tc::tmem_ld16(tm + kColQ + part * TW, r);
+        tc::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(&f.y[part * TW + j]);
-        r[j] = __float_as_uint(__uint_as_float(r[j]) * w.x), r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * w.y);
-        r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * w.z), r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * w.w);
+        for (int j = 0; j < 16; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&f.y[part * TW + j]);
+          r[j] = __float_as_uint(__uint_as_float(r[j]) * w.x), r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * w.y);
+          r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * w.z), r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * w.w);
+        }
+        tc::tmem_st16(tm + kColO + part * TW, r);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        fence_proxy_async_smem();  // the factors are read before the stage's next copies
+        arrive(kOReady);
       }
-      tc::tmem_st16(tm + kColO + part * TW, r);
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      fence_proxy_async_smem();  // the factors are read before the stage's next copies
-      arrive(kOReady);
     }
     if (n > 0 && ok) {
       ok = wait(kUFull, n - 1);
       tc::fence_after_sync();
-      update();
-      if (kOutput) ok = ok && output(n - 1);
+#pragma unroll
+      for (int q = 0; q < CW / 16; ++q) update(q);
+      if (kOutput && (ok = ok && output(n - 1))) give(n - 1);
     }
     // the stage of the chunk that would be next: all that used it is done with the y of the chunk three before
     const int free_stage = n % kStages;
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
   } else if (warp == kCopyWarp) {
     // ------------------------------ copies -------------------------------------------------------------------
-    if (lane == 0) {
+    if (elect_one()) {
       const unsigned char* rec = p.records + (bh * p.chunks + (first - p.first)) * (int64_t)kRecord;
       int c = 0;
       const int copies = p.ctl.stall_tile == ((int64_t)1 << 40) + blockIdx.x ? 0 : n;  // (the test hook)
@@ -869,7 +871,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kStoreWarp) {
     // ------------------------------ y ------------------------------------------------------------------------
     if constexpr (kOutput) {
-      for (int c = 0; lane == 0 && c < n && wait_one(kYReady + c % kStages, c / kStages); ++c) {
+      const bool one = elect_one();
+      for (int c = 0; one && c < n && wait_one(kYReady + c % kStages, c / kStages); ++c) {
         for (int j = 0; j < v_boxes; ++j)
           tma_store_4d(&map_y, base + c % kStages * L::kStage + L::kV + j * kTile, m0 + 64 * j, h, (first + c) * kC, (int)b);
         bulk_commit();
@@ -878,18 +881,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bulk_wait<0>();
     }
-  } else if (lane == 0 && n > 0) {
+  } else if (n > 0 && elect_one()) {
     // ------------------------------ MMAs ---------------------------------------------------------------------
-    // Products with 64 columns take as long as those with 128 (64 cycles a step of 16), so what shares an A goes in one:
-    // K with Q, the inverse's hi with its lo.
     constexpr uint32_t id64 = tc::idesc_bf16_f32(128, 64, false, false);  // A, B K-major
-    constexpr uint32_t id128 = tc::idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 128, true, false);  // A = V^T
+    constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 64, true, false);   // A = V^T
     constexpr uint32_t id_u = tc::idesc_bf16_f32(128, DK, false, true);   // B = K, columns of the state as N
     const uint32_t sb = smem_addr(base);
     // k-step ks of a K-major tile of 64-column blocks
     const auto k_major = [&](uint32_t at, int ks, uint32_t block) {
       return tc::sdesc_sw128(at + (ks >> 2) * block + (ks & 3) * 32, 16, 1024);
+    };
+    // S times a tile of K or Q: the k-steps of half `x` of each thread's columns
+    const auto product_s = [&](uint32_t to, uint32_t tile, int x) {
+#pragma unroll
+      for (int ks = x; ks < DK / 16; ks += kHalves) {
+        const uint64_t d = k_major(tile, ks, 2 * kTile);
+        tc::mma_bf16_ts(tmem + to, tmem + kColS + 16 * ks, d, id64, ks > 0);
+        tc::mma_bf16_ts(tmem + to, tmem + kColS + 16 * ks + 8, d, id64, true);
+      }
     };
     bool ok = true;
     int c = 0;  // chunks whose last commit was made
@@ -901,28 +910,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < kHalves && ok; ++x) {
         if (!(ok = wait_one(kSReady + x, c))) break;
         tc::fence_after_sync();
-#pragma unroll
-        for (int ks = 4 * x; ks < 4 * x + 4; ++ks) {
-          const uint64_t d = k_major(kt, ks, 2 * kTile);
-          tc::mma_bf16_ts(tmem + kColX, tmem + kColHi + 8 * ks, d, kOutput ? id128 : id64, ks > 0);
-          tc::mma_bf16_ts(tmem + kColX, tmem + kColLo + 8 * ks, d, kOutput ? id128 : id64, true);
-        }
+        product_s(kColX, kt, x);
       }
       if (!ok) break;
       tc::mma_commit(&bars[kXFull]);
       if (!unit)
 #pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks)
-          tc::mma_bf16(tmem + kColD, tc::sdesc_sw128(vt + ks * 2048, kTile, 1024), k_major(th, ks, 0), id_v, ks > 0);
+        for (int ks = 0; ks < kC / 16; ++ks) {
+          const uint64_t v = tc::sdesc_sw128(vt + ks * 2048, kTile, 1024);
+          tc::mma_bf16(tmem + kColD, v, k_major(th, ks, 0), id_v, ks > 0);
+          tc::mma_bf16(tmem + kColD, v, k_major(th + kTile, ks, 0), id_v, true);
+        }
       if (!(ok = wait_one(kXReady, c))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id128, ks > 0 || !unit);
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOpLo + 8 * ks, k_major(th, ks, 0), id128, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id64, ks > 0 || !unit);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th + kTile, ks, 0), id64, true);
+        tc::mma_bf16_ts(tmem + kColD, tmem + kColOpLo + 8 * ks, k_major(th, ks, 0), id64, true);
       }
       tc::mma_commit(&bars[kDFull]);
-      if (!(ok = wait_one(kDReady, c))) break;
+      if (kOutput) {  // while D becomes an operand
+#pragma unroll
+        for (int x = 0; x < kHalves; ++x) product_s(kColQ, kt + kTile, x);
+        tc::mma_commit(&bars[kQFull]);
+      }
+      if (!(ok = wait_one(kDReady, c) && (!kOutput || wait_one(kQFull, c)))) break;  // (U takes the place of S)
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
@@ -952,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (count > 0) mbar_wait(&bars[bar], (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
     };
     drained(kXFull, c), drained(kDFull, c), drained(kUFull, c);
-    if (kOutput) drained(kDone, c);
+    if (kOutput) drained(kQFull, c), drained(kDone, c);
     if (!kOutput)
       for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
   }
