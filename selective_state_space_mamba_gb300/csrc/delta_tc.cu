@@ -512,19 +512,10 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-constexpr int kM = 128;            // rows of a tile
-constexpr int kStages = 3;         // K, Q, V and the record of a chunk
+constexpr int kM = 128;            // rows of an MMA
 constexpr int kParts = 4;          // state threads of a row
-constexpr int kStateWarps = 4 * kParts, kCopyWarp = kStateWarps, kMmaWarp = kCopyWarp + 1, kStoreWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kStoreWarp + 1);
+constexpr int kStateWarps = 4 * kParts, kCopyWarp = kStateWarps, kStoreWarp = kCopyWarp + 1, kMmaWarp = kStoreWarp + 1;
 
-// TMEM columns.  U takes the place of S as an operand: 16 columns of S are as hi and lo where the 16 columns of U are that
-// update them, so that a thread overwrites none but what it has read.  D of the update as an operand takes the place of X.
-constexpr uint32_t kColS = 0, kColU = 0;
-constexpr uint32_t kColX = 128, kColQ = 192, kColD = 256;
-constexpr uint32_t kColOp = 320, kColOpLo = 352;
-constexpr uint32_t kColDo = 384, kColDoLo = 416;  // D of the output
-constexpr uint32_t kColO = 448;
 constexpr uint32_t kTmemCols = 512;
 
 // True in one lane of the warp.  (The compiler then knows that what follows runs in one lane: it issues an MMA in 28 cycles,
@@ -535,72 +526,136 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-enum Bar {
-  kFull = 0,                  // a chunk has landed
-  kEmpty = kFull + kStages,   // ... and is read
-  kSReady = kEmpty + kStages, // S as an operand, half of each thread's columns
-  kXFull = kSReady + 2, kXReady, kQFull, kDFull, kDReady, kUFull, kOReady, kDone, kLoaded, kLast,
-  kYReady,                    // y of a stage's chunk (one for each: the states may be a chunk ahead of the stores)
-  kNumBars = kYReady + kStages
+// What a CTA runs: one chain of up to 128 rows of a state, or (kPair) two chains of up to 64 rows, one in the MMAs' rows below 64 and
+// one in those above.  Each of a pair's chains has MMAs of its own, whose other rows nobody reads; they run while the other
+// chain converts.
+template <int DK, bool kPair>
+struct Layout {
+  static constexpr int kHalves = DK / 64, kSides = kPair ? 2 : 1, kRows = kM / kSides;
+  // TMEM columns.  16 columns of S are as hi and lo where the 16 columns of U are that update them, so that U may take the
+  // place of S as an operand: a thread overwrites none but what it has read.  D of the update as an operand takes the place of X.
+  // A pair's chains have their own accumulators, and so fewer of them: U takes the place of X and Q, D that of X, X as an operand
+  // that of O, and D as operands that of S (of 128 columns in turn, so that S can come in while D of the output is used).
+  static constexpr bool kTurn = kPair && DK == 128;
+  static constexpr uint32_t kColS = 0, kColX = 128, kColQ = 192, kColD = kPair ? 128 : 256, kColU = kPair ? 128 : 0;
+  static constexpr uint32_t kColXOp = kPair ? 256 : 320;
+  static constexpr uint32_t kColOp = kPair ? 0 : 320, kColDo = kTurn ? 16 : kPair ? 64 : 384;  // D of the update, of the output
+  // 16 tokens of X or D are as hi and lo in 16 columns: those of X where a thread has read its y
+  static constexpr uint32_t kOpStep = kTurn ? 32 : 16;  // of D's operands, from 16 tokens to the next
+  static constexpr uint32_t kColO = kPair ? 256 : 448;
+  static constexpr int kThreads = 32 * (kMmaWarp + kSides);
+  static constexpr uint32_t kColSide = 192;  // accumulators of one chain of a pair to those of the other
+  // A stage: [half][K rows, Q rows], [64 rows of S][tokens], and what comes of the record: T, P and the factors; of a pair
+  // only the factors, with one place for T and P behind the stages.
+  static constexpr int kStages = kPair ? 2 : 3;
+  static constexpr int kV = kHalves * 2 * kTile, kEnd = kV + kRows / 64 * kTile, kF = kPair ? kEnd : kEnd + 3 * kTile;
+  static constexpr int kStage = kF + 1024;
+  static constexpr int kT = kPair ? kStages * kStage : kEnd, kP = kT + 2 * kTile;
+  static constexpr int kSide = kStages * kStage + (kPair ? 3 * kTile : 0);
+  enum Bar {                    // of a chain
+    kFull = 0,                  // a chunk has landed
+    kEmpty = kFull + kStages,   // ... and is read
+    kSReady = kEmpty + kStages, // S as an operand, half of each thread's columns
+    kXFull = kSReady + 2, kXReady, kQFull, kDFull, kDReady, kUFull, kOReady, kDone, kLoaded, kLast,
+    kTFull, kPFull,             // (of a pair)
+    kYReady,                    // y of a stage's chunk (one for each: the states may be a chunk ahead of the stores)
+    kNumBars = kYReady + kStages
+  };
+  static constexpr int kBars = kSides * kSide;
+  static constexpr int kTotal = kBars + kSides * kNumBars * 8 + 16;
 };
 
-template <int DK>
-struct Layout {
-  static constexpr int kHalves = DK / 64;
-  // [half][K rows, Q rows], [64 rows of S][tokens], record
-  static constexpr int kV = kHalves * 2 * kTile, kT = kV + 2 * kTile, kP = kT + 2 * kTile, kF = kP + kTile;
-  static constexpr int kStage = kF + 1024;
-  static constexpr int kBars = kStages * kStage;
-  static constexpr int kTotal = kBars + kNumBars * 8 + 16;
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// What a chain of a CTA has to do.
+struct Job {
+  int64_t b, bh;
+  int h, g, m0, rows;
+  int piece, first, most;  // chunks: the piece's first, its most
+  int n;                   // its chunks with tokens
+  int64_t tokens;          // ... their tokens
+  bool unit;               // M of a piece
+  const float* from;
+  float* to;
 };
+template <int DK, bool kOutput, int kRows>
+__device__ __forceinline__ Job job_of(const Params& p, int64_t index) {
+  const ssm_delta_args& a = p.a;
+  // jobs of a chain: its pieces' tiles of rows; without outputs those of all pieces but the last, then the M of all but the first
+  constexpr int kUnits = (DK + kRows - 1) / kRows;
+  const int tile_jobs = (kOutput ? p.pieces : p.pieces - 1) * p.tiles, jobs = kOutput ? tile_jobs : tile_jobs + (p.pieces - 2) * kUnits;
+  const int64_t heads = a.batch * a.nheads;
+  const bool none = index >= heads * jobs;  // (the last CTA's second chain)
+  if (none) index = 0;
+  Job j;
+  const int job = (int)(index % jobs);
+  j.bh = index / jobs;
+  j.unit = job >= tile_jobs;
+  j.piece = j.unit ? (job - tile_jobs) / kUnits + 1 : job / p.tiles;
+  j.m0 = (j.unit ? (job - tile_jobs) % kUnits : job % p.tiles) * kRows;
+  j.h = (int)(j.bh % a.nheads);
+  j.g = j.h / (a.nheads / a.ngroups);
+  j.b = j.bh / a.nheads;
+  j.rows = none ? 0 : min(kRows, (j.unit ? DK : a.headdim) - j.m0);
+  j.first = p.first + j.piece * p.piece_chunks;
+  j.most = none ? 0 : min(p.piece_chunks, p.first + p.chunks - j.first);
+  const int64_t tile_at = (j.bh * a.headdim + j.m0) * DK, slot = heads * a.headdim * DK;
+  if (j.unit) {
+    j.from = nullptr;
+    j.to = p.passing + (((j.piece - 1) * heads + j.bh) * DK + j.m0) * DK;
+  } else {
+    j.from = j.piece == 0 ? (p.begins ? a.h0 : p.states) : kOutput ? p.entering + (j.piece - 1) * slot : nullptr;
+    j.to = !kOutput ? p.entering + j.piece * slot : j.piece < p.pieces - 1 ? nullptr : p.ends ? a.h_final : p.states;
+    if (j.from) j.from += tile_at;
+    if (j.to) j.to += tile_at;
+  }
+  if (none) j.from = nullptr, j.to = nullptr;
+  return j;
+}
+// ... and its tokens, which the kernels before may have written (lens)
+__device__ __forceinline__ void count_tokens(const Params& p, Job& j) {
+  j.tokens = min(max(tokens_of(p.a, j.b) - (int64_t)j.first * kC, (int64_t)0), (int64_t)j.most * kC);
+  j.n = (int)((j.tokens + kC - 1) / kC);
+}
 
 // kOutput: a piece with its outputs; else its N or M.
-template <int DK, bool kOutput>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DK, bool kOutput, bool kPair>
+__global__ void __launch_bounds__((Layout<DK, kPair>::kThreads), 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_y,
                        const __grid_constant__ Params p) {
-  using L = Layout<DK>;
-  constexpr int kHalves = L::kHalves;
+  using L = Layout<DK, kPair>;
+  constexpr int kHalves = L::kHalves, kStages = L::kStages, kSides = L::kSides, kRows = L::kRows, kSideWarps = kStateWarps / kSides;
+  constexpr int kThreads = L::kThreads;
+  constexpr uint32_t kColU = kPair && !kOutput ? L::kColQ : L::kColU;  // (without Q there is room beside X)
+  constexpr bool kXOverU = kPair && kOutput && kHalves > 1;
   extern __shared__ unsigned char raw[];
   unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kBars + kNumBars * 8);
+  uint64_t* const all_bars = reinterpret_cast<uint64_t*>(base + L::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L::kBars + kSides * L::kNumBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const ssm_delta_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // jobs of a chain: its pieces' tiles of rows; without outputs those of all pieces but the last, then the M of all but the first
-  const int tile_jobs = (kOutput ? p.pieces : p.pieces - 1) * p.tiles, jobs = kOutput ? tile_jobs : tile_jobs + p.pieces - 2;
-  const int job = (int)(blockIdx.x % jobs);
-  const int64_t bh = blockIdx.x / jobs, heads = a.batch * a.nheads;
-  const bool unit = job >= tile_jobs;
-  const int piece = unit ? job - tile_jobs + 1 : job / p.tiles, m0 = unit ? 0 : job % p.tiles * kM;
-  const int h = (int)(bh % a.nheads), g = h / (a.nheads / a.ngroups);
-  const int64_t b = bh / a.nheads;
-  const int rows = unit ? DK : min(kM, a.headdim - m0);
-  const int v_boxes = unit ? 0 : rows > 64 ? 2 : 1;
-  const int first = p.first + piece * p.piece_chunks, most = min(p.piece_chunks, p.first + p.chunks - first);  // chunks
-  const int64_t tile_at = (bh * a.headdim + m0) * DK, slot = heads * a.headdim * DK;
-  const float* from;
-  float* to;
-  if (unit) {
-    from = nullptr;
-    to = p.passing + ((piece - 1) * heads + bh) * DK * DK;
-  } else {
-    from = piece == 0 ? (p.begins ? a.h0 : p.states) : kOutput ? p.entering + (piece - 1) * slot : nullptr;
-    to = !kOutput ? p.entering + piece * slot : piece < p.pieces - 1 ? nullptr : p.ends ? a.h_final : p.states;
-    if (from) from += tile_at;
-    if (to) to += tile_at;
-  }
-
+  const auto job = [&](int side) { return job_of<DK, kOutput, kRows>(p, (int64_t)blockIdx.x * kSides + side); };
   if (threadIdx.x == 0) {
-    const auto init = [&](int first, int n, uint32_t count) {
-      for (int i = 0; i < n; ++i) mbar_init(&bars[first + i], count);
-    };
-    init(kFull, kStages, 1), init(kEmpty, kStages, 1), init(kSReady, 2, kStateWarps), init(kXFull, 1, 1), init(kQFull, 1, 1);
-    init(kXReady, 1, kStateWarps), init(kDFull, 1, 1), init(kDReady, 1, kStateWarps), init(kUFull, 1, 1);
-    init(kOReady, 1, kStateWarps), init(kDone, 1, 1), init(kYReady, kStages, kStateWarps), init(kLoaded, 1, kStateWarps), init(kLast, 1, 1);
+    for (int side = 0; side < kSides; ++side) {
+      const auto init = [&](int first, int n, uint32_t count) {
+        for (int i = 0; i < n; ++i) mbar_init(&all_bars[side * L::kNumBars + first + i], count);
+      };
+      init(L::kFull, kStages, 1), init(L::kEmpty, kStages, 1), init(L::kSReady, 2, kSideWarps), init(L::kXFull, 1, 1);
+      init(L::kXReady, 1, kSideWarps), init(L::kQFull, 1, 1), init(L::kDFull, 1, 1), init(L::kDReady, 1, kSideWarps);
+      init(L::kUFull, 1, 1), init(L::kOReady, 1, kSideWarps), init(L::kDone, 1, 1), init(L::kLoaded, 1, kSideWarps);
+      init(L::kLast, 1, 1), init(L::kTFull, 1, 1), init(L::kPFull, 1, 1), init(L::kYReady, kStages, kSideWarps);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -608,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
-  if (v_boxes == 1)  // rows that no copy brings
+  const auto v_boxes = [](const Job& j) { return j.unit ? 0 : j.rows > 64 ? 2 : 1; };
+  if (!kPair && v_boxes(job(0)) < 2)  // rows that no copy brings
     for (int i = threadIdx.x; i < kStages * kTile / 16; i += kThreads)
       *reinterpret_cast<uint4*>(base + i / (kTile / 16) * L::kStage + L::kV + kTile + i % (kTile / 16) * 16) =
           make_uint4(0u, 0u, 0u, 0u);
@@ -619,16 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();  // (not before: a next kernel's CTA on this SM must not take the TMEM that this one waits for)
   griddep_wait();
-  const int64_t all_tokens = tokens_of(a, b);
-  const int64_t tokens = min(max(all_tokens - (int64_t)first * kC, (int64_t)0), (int64_t)most * kC);  // of the piece
-  const int n = (int)((tokens + kC - 1) / kC);
 
-  // A bounded wait, the same answer in every lane of a warp
-  const auto wait_one = [&](int bar, int64_t phase) -> bool {
+  // A bounded wait
+  const auto wait_one = [&](uint64_t* bar, int64_t phase) -> bool {
     const uint32_t parity = (uint32_t)phase & 1u;
-    if (mbar_try_wait(&bars[bar], parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&bars[bar], parity)) {
+    while (!mbar_try_wait(bar, parity)) {
       if (*abort_flag || global_timer_ns() - t0 > p.ctl.spin_limit_ns) {
         *abort_flag = 1;
         return false;
@@ -636,32 +689,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  const auto wait = [&](int bar, int64_t phase) -> bool { return __all_sync(0xffffffffu, wait_one(bar, phase)); };
-  const auto arrive = [&](int bar) {  // one of a warp, after all its lanes
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[bar]);
+  const auto test = [&](uint64_t* bar, int64_t phase) { return mbar_test_wait(bar, (uint32_t)phase & 1u); };
+  // Whether one who polls has to give up: nothing has moved for longer than a wait may take (the clock is read at every 64th poll)
+  uint64_t since = 0;
+  uint32_t polls = 0;
+  const auto expired = [&](bool moved) -> bool {
+    if (moved) {
+      polls = 0;
+    } else if (++polls % 64 == 0) {
+      const uint64_t now = global_timer_ns();
+      if (polls == 64) since = now;
+      if (*abort_flag || now - since > p.ctl.spin_limit_ns) {
+        *abort_flag = 1;
+        return true;
+      }
+    }
+    return false;
   };
 
   if (warp < kStateWarps) {
     // ------------------------------ state: S in registers, the operands in TMEM ----------------------------
     constexpr int CW = DK / kParts;  // columns of S a thread
     constexpr int TW = kC / kParts;  // tokens of X, D and y a thread
-    const int quad = warp & 3, part = warp >> 2, row = quad * 32 + lane;
-    const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16);
+    const int quad = warp & 3, part = warp >> 2, side = kPair ? quad >> 1 : 0, row = (quad * 32 + lane) % kRows;
+    const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16), acc = tm + side * L::kColSide;
+    const int thread = part * kRows + row;  // of the side's
+    constexpr int kSideThreads = 32 * kSideWarps;
+    unsigned char* const mine = base + side * L::kSide;
+    uint64_t* const bars = all_bars + side * L::kNumBars;
+    Job j = job(side);
+    count_tokens(p, j);
+    const int n = j.n, rows = j.rows;
+    const int64_t tokens = j.tokens;
+    const float* const from = j.from;
+    float* const to = j.to;
+    // the same answer in every lane of a warp
+    const auto wait = [&](int bar, int64_t phase) -> bool { return __all_sync(0xffffffffu, wait_one(&bars[bar], phase)); };
+    const auto arrive = [&](int bar) {  // one of a warp, after all its lanes
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bar]);
+    };
     const bool have = row < rows;
     float s[CW];
 #pragma unroll
-    for (int i = 0; i < CW; ++i) s[i] = unit && row == part * CW + i ? 1.f : 0.f;
+    for (int i = 0; i < CW; ++i) s[i] = j.unit && j.m0 + row == part * CW + i ? 1.f : 0.f;
     // States go through a stage's shared memory, in rows of kRowS floats: a thread's columns lie a row from its
     // neighbour's.  move(stage, f): f on each four floats of the tile, there and in global memory (its elements in order).
     constexpr int kRowS = DK + 4;
-    static_assert(kM * kRowS * 4 <= L::kStage, "a state fits a stage");
+    static_assert(kRows * kRowS * 4 <= L::kStage, "a state fits a stage");
     const auto move = [&](int stage, auto f) {
-      float* rows_at = reinterpret_cast<float*>(base + stage * L::kStage);
-      for (int i = 4 * threadIdx.x; i < rows * DK; i += 4 * 32 * kStateWarps) f(rows_at + i / DK * kRowS + i % DK, i);
+      float* rows_at = reinterpret_cast<float*>(mine + stage * L::kStage);
+      for (int i = 4 * thread; i < rows * DK; i += 4 * kSideThreads) f(rows_at + i / DK * kRowS + i % DK, i);
     };
     const auto own = [&](int stage) {
-      return reinterpret_cast<float4*>(reinterpret_cast<float*>(base + stage * L::kStage) + row * kRowS + part * CW);
+      return reinterpret_cast<float4*>(reinterpret_cast<float*>(mine + stage * L::kStage) + row * kRowS + part * CW);
     };
     if (from) {
       const bool vec = reinterpret_cast<uintptr_t>(from) % 16 == 0;
@@ -669,20 +750,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* e = from + i;
         *reinterpret_cast<float4*>(to) = vec ? *reinterpret_cast<const float4*>(e) : make_float4(e[0], e[1], e[2], e[3]);
       });
-      named_bar_sync(1, 32 * kStateWarps);
+      named_bar_sync(1 + side, kSideThreads);
       if (have) {
 #pragma unroll
         for (int i = 0; i < CW; i += 4) *reinterpret_cast<float4*>(&s[i]) = own(kStages - 1)[i / 4];
       }
       fence_proxy_async_smem();
-      arrive(kLoaded);
+      arrive(L::kLoaded);
     }
     float last = 1.f;  // e^(G_last) of the chunk before
 
     // S <- last S + U, 16 columns
     const auto update = [&](int q) {
       uint32_t r[16];
-      tc::tmem_ld16(tm + kColU + part * CW + 16 * q, r);
+      tc::tmem_ld16(acc + kColU + part * CW + 16 * q, r);
       tc::tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; j += 2) {
@@ -693,10 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // y of chunk c: this thread's row and tokens, into the chunk's V, which its products have read; 0 past the last token
     const auto output = [&](int c) -> bool {
-      if (!wait(kDone, c)) return false;
+      if (!wait(L::kDone, c)) return false;
       tc::fence_after_sync();
       uint32_t o[TW];
-      tc::tmem_ld16(tm + kColO + part * TW, o);
+      tc::tmem_ld16(acc + L::kColO + part * TW, o);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       const int64_t left = tokens - ((int64_t)c * kC + part * TW);
@@ -706,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= left) o[j] = 0u;
       }
       // (the swizzle of a token's 16-byte units goes by token % 8, the same for all parts)
-      unsigned char* tile = base + c % kStages * L::kStage + L::kV + (row >> 6) * kTile + part * TW * 128;
+      unsigned char* tile = mine + c % kStages * L::kStage + L::kV + (row >> 6) * kTile + part * TW * 128;
 #pragma unroll
       for (int j = 0; j < TW; ++j)
         *reinterpret_cast<uint16_t*>(tile + j * 128 + ((((row & 63) >> 3) ^ (j & 7)) << 4) + (row & 7) * 2) =
@@ -715,10 +796,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const auto give = [&](int c) {  // to the stores
       fence_proxy_async_smem();
-      arrive(kYReady + c % kStages);
+      arrive(L::kYReady + c % kStages);
     };
     // a part's 16 values, scaled, as an operand
-    const auto operand = [&](const uint32_t (&r)[16], const float* f) {
+    const auto operand = [&](const uint32_t (&r)[16], const float* f, uint32_t at) {
       uint32_t hi[8], lo[8];
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -729,107 +810,116 @@ __global__ void __launch_bounds__(kThreads, 1)
         split2(v0.x, v0.y, hi[j], lo[j]);
         split2(v1.x, v1.y, hi[j + 1], lo[j + 1]);
       }
-      tc::tmem_st8(tm + kColOp + part * TW / 2, hi);
-      tc::tmem_st8(tm + kColOpLo + part * TW / 2, lo);
+      tc::tmem_st8(at, hi);
+      tc::tmem_st8(at + 8, lo);
     };
 
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
       const int st = c % kStages;
-      unsigned char* stage = base + st * L::kStage;
+      unsigned char* stage = mine + st * L::kStage;
       const Factors& f = *reinterpret_cast<const Factors*>(stage + L::kF);
       const int live = (int)min((int64_t)kC, tokens - (int64_t)c * kC);
       if (live < kC && ok) {  // the last chunk: zeros past the last token, before its first product
-        ok = wait(kFull + st, c / kStages);
-        constexpr int kRow = (L::kV + 2 * kTile) / kTile * 8;  // 16-byte units of a token
+        ok = wait(L::kFull + st, c / kStages);
+        constexpr int kRow = L::kEnd / kTile * 8;  // 16-byte units of a token
         if (ok)
-          for (int j = threadIdx.x; j < (kC - live) * kRow; j += 32 * kStateWarps)
+          for (int j = thread; j < (kC - live) * kRow; j += kSideThreads)
             *reinterpret_cast<uint4*>(stage + (j % kRow >> 3) * kTile + (live + j / kRow) * 128 + (j & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
       }
       if (c > 0) {
-        ok = ok && wait(kUFull, c - 1);
+        ok = ok && wait(L::kUFull, c - 1);
         tc::fence_after_sync();
       }
 #pragma unroll
       for (int q = 0; q < CW / 16; ++q) {  // X goes on with the first half while the second is converted
         if (c > 0) update(q);
+        if (L::kTurn && kOutput && q > 0 && c > 0) {
+          ok = ok && wait(L::kDone, c - 1);
+          tc::fence_after_sync();
+        }
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) split2(s[16 * q + 2 * j], s[16 * q + 2 * j + 1], hi[j], lo[j]);
-        tc::tmem_st8(tm + kColS + part * CW + 16 * q, hi);
-        tc::tmem_st8(tm + kColS + part * CW + 16 * q + 8, lo);
+        tc::tmem_st8(tm + L::kColS + part * CW + 16 * q, hi);
+        tc::tmem_st8(tm + L::kColS + part * CW + 16 * q + 8, lo);
         tc::tmem_st_wait();
         tc::fence_before_sync();
-        arrive(kSReady + q);
+        arrive(L::kSReady + q);
       }
       if (kOutput && c > 0) ok = ok && output(c - 1);
       // X, scaled, as an operand
-      ok = ok && wait(kFull + st, c / kStages) && wait(kXFull, c);
+      ok = ok && wait(L::kFull + st, c / kStages) && wait(L::kXFull, c);
       if (!ok) break;
       tc::fence_after_sync();
       uint32_t r[16];
-      tc::tmem_ld16(tm + kColX + part * TW, r);
+      tc::tmem_ld16(acc + L::kColX + part * TW, r);
       tc::tmem_ld_wait();
-      operand(r, f.x + part * TW);
+      operand(r, f.x + part * TW, acc + L::kColXOp + part * 16);
       tc::tmem_st_wait();
       tc::fence_before_sync();
-      arrive(kXReady);
+      arrive(L::kXReady);
       if (kOutput && c > 0) give(c - 1);
       // D scaled as an operand of the update
-      if (!(ok = wait(kDFull, c))) break;
+      if (!(ok = wait(L::kDFull, c))) break;
       tc::fence_after_sync();
-      tc::tmem_ld16(tm + kColD + part * TW, r);
+      uint32_t rq[16];
+      tc::tmem_ld16(acc + L::kColD + part * TW, r);
+      if (kPair && kOutput) tc::tmem_ld16(acc + L::kColQ + part * TW, rq);
       tc::tmem_ld_wait();
-      operand(r, f.u + part * TW);
+      operand(r, f.u + part * TW, tm + L::kColOp + part * L::kOpStep);
       last = f.last[0];
       tc::tmem_st_wait();
       tc::fence_before_sync();
       if (!kOutput) fence_proxy_async_smem();  // the factors are read before the stage's next copies
-      arrive(kDReady);
+      arrive(L::kDReady);
       if constexpr (kOutput) {
-        // D as it is, and Q scaled as what O adds to
+        // D as it is
         {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) split2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), hi[j], lo[j]);
-          tc::tmem_st8(tm + kColDo + part * TW / 2, hi);
-          tc::tmem_st8(tm + kColDoLo + part * TW / 2, lo);
+          tc::tmem_st8(tm + L::kColDo + part * L::kOpStep, hi);
+          tc::tmem_st8(tm + L::kColDo + part * L::kOpStep + 8, lo);
         }
-        if (!(ok = wait(kQFull, c))) break;
-        tc::fence_after_sync();
-        tc::tmem_ld16(tm + kColQ + part * TW, r);
-        tc::tmem_ld_wait();
+        if constexpr (!kPair) {
+          if (!(ok = wait(L::kQFull, c))) break;
+          tc::fence_after_sync();
+          tc::tmem_ld16(acc + L::kColQ + part * TW, rq);
+          tc::tmem_ld_wait();
+        }
+        // Q, scaled, as what O adds to
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 w = *reinterpret_cast<const float4*>(&f.y[part * TW + j]);
-          r[j] = __float_as_uint(__uint_as_float(r[j]) * w.x), r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * w.y);
-          r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * w.z), r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * w.w);
+          rq[j] = __float_as_uint(__uint_as_float(rq[j]) * w.x), rq[j + 1] = __float_as_uint(__uint_as_float(rq[j + 1]) * w.y);
+          rq[j + 2] = __float_as_uint(__uint_as_float(rq[j + 2]) * w.z), rq[j + 3] = __float_as_uint(__uint_as_float(rq[j + 3]) * w.w);
         }
-        tc::tmem_st16(tm + kColO + part * TW, r);
+        tc::tmem_st16(acc + L::kColO + part * TW, rq);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         fence_proxy_async_smem();  // the factors are read before the stage's next copies
-        arrive(kOReady);
+        arrive(L::kOReady);
       }
     }
     if (n > 0 && ok) {
-      ok = wait(kUFull, n - 1);
+      ok = wait(L::kUFull, n - 1);
       tc::fence_after_sync();
 #pragma unroll
       for (int q = 0; q < CW / 16; ++q) update(q);
       if (kOutput && (ok = ok && output(n - 1))) give(n - 1);
     }
-    // the stage of the chunk that would be next: all that used it is done with the y of the chunk three before
+    // the stage of the chunk that would be next: all that used it is done with the y of the chunk kStages before
     const int free_stage = n % kStages;
-    if (n >= kStages) ok = ok && wait(kEmpty + free_stage, n / kStages - 1);
-    if (to && !named_bar_any(1, 32 * kStateWarps, !ok)) {
+    if (n >= kStages) ok = ok && wait(L::kEmpty + free_stage, n / kStages - 1);
+    if (to && !named_bar_any(1 + side, kSideThreads, !ok)) {
       if (have) {
 #pragma unroll
         for (int i = 0; i < CW; i += 4) own(free_stage)[i / 4] = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
       }
-      named_bar_sync(1, 32 * kStateWarps);
+      named_bar_sync(1 + side, kSideThreads);
       const bool vec = reinterpret_cast<uintptr_t>(to) % 16 == 0;
       move(free_stage, [&](const float* mine, int i) {
         const float4 e = *reinterpret_cast<const float4*>(mine);
@@ -844,49 +934,138 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kCopyWarp) {
     // ------------------------------ copies -------------------------------------------------------------------
     if (elect_one()) {
-      const unsigned char* rec = p.records + (bh * p.chunks + (first - p.first)) * (int64_t)kRecord;
-      int c = 0;
-      const int copies = p.ctl.stall_tile == ((int64_t)1 << 40) + blockIdx.x ? 0 : n;  // (the test hook)
-      for (; c < copies; ++c) {
-        const int st = c % kStages;
-        if (c >= kStages && !wait_one(kEmpty + st, c / kStages - 1)) break;
-        if (c == kStages - 1 && from && !wait_one(kLoaded, 0)) break;  // the state came there
-        unsigned char* stage = base + st * L::kStage;
-        mbar_arrive_expect_tx(&bars[kFull + st], (kHalves * (kOutput ? 2 : 1) + v_boxes) * kTile + kRecordCopied);
-        const auto load = [&](int place, const CUtensorMap* map, int x, uint32_t which) {
+      const bool silent = p.ctl.stall_tile == ((int64_t)1 << 40) + blockIdx.x;  // (the test hook)
+      const auto record = [&](const Job& j, int c) {
+        return p.records + (j.bh * p.chunks + (j.first - p.first) + c) * (int64_t)kRecord;
+      };
+      // K, Q and V of chunk c into its stage, with as many bytes of its record to come
+      const auto load = [&](const Job& j, unsigned char* stage, uint64_t* full, int c, uint32_t bytes) {
+        mbar_arrive_expect_tx(full, (kHalves * (kOutput ? 2 : 1) + v_boxes(j)) * kTile + bytes);
+        const auto box = [&](int place, const CUtensorMap* map, int x, uint32_t which) {
           const bool inner = (p.inner & which) != 0;
-          const int tok = (first + c) * kC;
-          tc::tma_load_3d(stage + place * kTile, map, x, inner ? (int)b : tok, inner ? tok : (int)b, &bars[kFull + st]);
+          const int tok = (j.first + c) * kC;
+          tc::tma_load_3d(stage + place * kTile, map, x, inner ? (int)j.b : tok, inner ? tok : (int)j.b, full);
         };
-        for (int j = 0; j < kHalves; ++j) {
-          load(2 * j, &map_k, g * DK + 64 * j, kMapK);
-          if (kOutput) load(2 * j + 1, &map_q, g * DK + 64 * j, kMapQ);
+        for (int i = 0; i < kHalves; ++i) {
+          box(2 * i, &map_k, j.g * DK + 64 * i, kMapK);
+          if (kOutput) box(2 * i + 1, &map_q, j.g * DK + 64 * i, kMapQ);
         }
-        bulk_g2s(stage + L::kT, rec + c * (int64_t)kRecord, kRecordCopied, &bars[kFull + st]);
-        for (int j = 0; j < v_boxes; ++j) load(2 * kHalves + j, &map_v, h * a.headdim + m0 + 64 * j, kMapV);
+        for (int i = 0; i < v_boxes(j); ++i) box(2 * kHalves + i, &map_v, j.h * a.headdim + j.m0 + 64 * i, kMapV);
+      };
+      const auto landed = [&](uint64_t* bar, int count) {  // no copy is left in flight
+        if (count > 0) mbar_wait(bar, (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
+      };
+      if constexpr (!kPair) {
+        Job j = job(0);
+        count_tokens(p, j);
+        uint64_t* const bars = all_bars;
+        int c = 0;
+        for (; c < (silent ? 0 : j.n); ++c) {
+          const int st = c % kStages;
+          if (c >= kStages && !wait_one(&bars[L::kEmpty + st], c / kStages - 1)) break;
+          if (c == kStages - 1 && j.from && !wait_one(&bars[L::kLoaded], 0)) break;  // the state came there
+          unsigned char* stage = base + st * L::kStage;
+          load(j, stage, &bars[L::kFull + st], c, kRecordCopied);
+          bulk_g2s(stage + L::kT, record(j, c), kRecordCopied, &bars[L::kFull + st]);
+        }
+        for (int st = 0; st < kStages; ++st) landed(&bars[L::kFull + st], (c - st + kStages - 1) / kStages);
+      } else {
+        // Each chain's copies go as their places become free: K, Q, V and the factors a stage, T and P one place each.
+        Job jobs[2] = {job(0), job(1)};
+        int asked[2][3] = {};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          count_tokens(p, jobs[i]);
+          if (silent) jobs[i].n = 0;
+        }
+        for (;;) {
+          bool more = false, moved = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const Job& j = jobs[i];
+            uint64_t* const bars = all_bars + i * L::kNumBars;
+            unsigned char* const mine = base + i * L::kSide;
+            if (int c = asked[i][0]; c < j.n) {
+              more = true;
+              const int st = c % kStages;
+              if ((c < kStages || test(&bars[L::kEmpty + st], c / kStages - 1)) &&
+                  (c != kStages - 1 || !j.from || test(&bars[L::kLoaded], 0))) {
+                unsigned char* stage = mine + st * L::kStage;
+                load(j, stage, &bars[L::kFull + st], c, sizeof(Factors));
+                bulk_g2s(stage + L::kF, record(j, c) + 3 * kTile, sizeof(Factors), &bars[L::kFull + st]);
+                ++asked[i][0], moved = true;
+              }
+            }
+            if (int c = asked[i][1]; c < j.n) {
+              more = true;
+              if (c == 0 || test(&bars[L::kDFull], c - 1)) {
+                mbar_arrive_expect_tx(&bars[L::kTFull], 2 * kTile);
+                bulk_g2s(mine + L::kT, record(j, c), 2 * kTile, &bars[L::kTFull]);
+                ++asked[i][1], moved = true;
+              }
+            }
+            if (int c = asked[i][2]; kOutput && c < j.n) {
+              more = true;
+              if (c == 0 || test(&bars[L::kDone], c - 1)) {
+                mbar_arrive_expect_tx(&bars[L::kPFull], kTile);
+                bulk_g2s(mine + L::kP, record(j, c) + 2 * kTile, kTile, &bars[L::kPFull]);
+                ++asked[i][2], moved = true;
+              }
+            }
+          }
+          if (!more || expired(moved)) break;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint64_t* const bars = all_bars + i * L::kNumBars;
+          for (int st = 0; st < kStages; ++st) landed(&bars[L::kFull + st], (asked[i][0] - st + kStages - 1) / kStages);
+          landed(&bars[L::kTFull], asked[i][1]), landed(&bars[L::kPFull], asked[i][2]);
+        }
       }
-      for (int j = max(0, c - kStages); j < c; ++j)  // no copy is left in flight
-        mbar_wait(&bars[kFull + j % kStages], (uint32_t)(j / kStages) & 1u, p.ctl.spin_limit_ns);
     }
   } else if (warp == kStoreWarp) {
     // ------------------------------ y ------------------------------------------------------------------------
-    if constexpr (kOutput) {
-      const bool one = elect_one();
-      for (int c = 0; one && c < n && wait_one(kYReady + c % kStages, c / kStages); ++c) {
-        for (int j = 0; j < v_boxes; ++j)
-          tma_store_4d(&map_y, base + c % kStages * L::kStage + L::kV + j * kTile, m0 + 64 * j, h, (first + c) * kC, (int)b);
+    if (kOutput && elect_one()) {
+      Job jobs[kSides];
+      int done[kSides] = {};
+#pragma unroll
+      for (int i = 0; i < kSides; ++i) count_tokens(p, jobs[i] = job(i));
+      const auto store = [&](int i) {
+        const Job& j = jobs[i];
+        const int c = done[i]++;
+        for (int x = 0; x < v_boxes(j); ++x)
+          tma_store_4d(&map_y, base + i * L::kSide + c % kStages * L::kStage + L::kV + x * kTile, j.m0 + 64 * x, j.h,
+                       (j.first + c) * kC, (int)j.b);
         bulk_commit();
         bulk_wait_read<0>();
-        mbar_arrive(&bars[kEmpty + c % kStages]);  // every product of the chunk was done before its y
+        mbar_arrive(&all_bars[i * L::kNumBars + L::kEmpty + c % kStages]);  // every product of the chunk was done before its y
+      };
+      if constexpr (!kPair) {
+        while (done[0] < jobs[0].n && wait_one(&all_bars[L::kYReady + done[0] % kStages], done[0] / kStages)) store(0);
+      } else {
+        while (done[0] < jobs[0].n || done[1] < jobs[1].n) {
+          bool moved = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (done[i] < jobs[i].n && test(&all_bars[i * L::kNumBars + L::kYReady + done[i] % kStages], done[i] / kStages))
+              store(i), moved = true;
+          if (expired(moved)) break;
+        }
       }
       bulk_wait<0>();
     }
-  } else if (n > 0 && elect_one()) {
+  } else if (elect_one()) {
     // ------------------------------ MMAs ---------------------------------------------------------------------
     constexpr uint32_t id64 = tc::idesc_bf16_f32(128, 64, false, false);  // A, B K-major
     constexpr uint32_t id_v = tc::idesc_bf16_f32(128, 64, true, false);   // A = V^T
     constexpr uint32_t id_u = tc::idesc_bf16_f32(128, DK, false, true);   // B = K, columns of the state as N
-    const uint32_t sb = smem_addr(base);
+    const int side = warp - kMmaWarp;
+    const uint32_t sb = smem_addr(base) + side * L::kSide, acc = tmem + side * L::kColSide;
+    uint64_t* const bars = all_bars + side * L::kNumBars;
+    Job j = job(side);
+    count_tokens(p, j);
+    const int n = j.n;
+    const auto reached = [&](int bar, int64_t phase) { return wait_one(&bars[bar], phase); };
     // k-step ks of a K-major tile of 64-column blocks
     const auto k_major = [&](uint32_t at, int ks, uint32_t block) {
       return tc::sdesc_sw128(at + (ks >> 2) * block + (ks & 3) * 32, 16, 1024);
@@ -896,78 +1075,89 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int ks = x; ks < DK / 16; ks += kHalves) {
         const uint64_t d = k_major(tile, ks, 2 * kTile);
-        tc::mma_bf16_ts(tmem + to, tmem + kColS + 16 * ks, d, id64, ks > 0);
-        tc::mma_bf16_ts(tmem + to, tmem + kColS + 16 * ks + 8, d, id64, true);
+        tc::mma_bf16_ts(acc + to, tmem + L::kColS + 16 * ks, d, id64, ks > 0);
+        tc::mma_bf16_ts(acc + to, tmem + L::kColS + 16 * ks + 8, d, id64, true);
+      }
+    };
+    const auto product_q = [&](uint32_t kt) {
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x) product_s(L::kColQ, kt + kTile, x);
+    };
+    const auto product_v = [&](uint32_t vt, uint32_t th) {
+#pragma unroll
+      for (int ks = 0; ks < kC / 16; ++ks) {
+        const uint64_t v = tc::sdesc_sw128(vt + ks * 2048, kTile, 1024);
+        tc::mma_bf16(acc + L::kColD, v, k_major(th, ks, 0), id_v, ks > 0);
+        tc::mma_bf16(acc + L::kColD, v, k_major(th + kTile, ks, 0), id_v, true);
       }
     };
     bool ok = true;
     int c = 0;  // chunks whose last commit was made
     for (; c < n && ok; ++c) {
       const int st = c % kStages;
-      const uint32_t kt = sb + st * L::kStage, vt = kt + L::kV, th = kt + L::kT, pt = kt + L::kP;
-      if (!(ok = wait_one(kFull + st, c / kStages))) break;
+      // V^T is placed so that its rows are the chain's
+      const uint32_t kt = sb + st * L::kStage, vt = kt + L::kV - side * kTile, rec = kPair ? sb : kt, th = rec + L::kT, pt = rec + L::kP;
+      // (where X takes the place of U: that is read by the time that all of S is there)
+      if (!(ok = reached(L::kFull + st, c / kStages) && (!kXOverU || reached(L::kSReady + 1, c)))) break;
 #pragma unroll
       for (int x = 0; x < kHalves && ok; ++x) {
-        if (!(ok = wait_one(kSReady + x, c))) break;
+        if (!(ok = reached(L::kSReady + x, c))) break;
         tc::fence_after_sync();
-        product_s(kColX, kt, x);
+        product_s(L::kColX, kt, x);
       }
       if (!ok) break;
-      tc::mma_commit(&bars[kXFull]);
-      if (!unit)
-#pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks) {
-          const uint64_t v = tc::sdesc_sw128(vt + ks * 2048, kTile, 1024);
-          tc::mma_bf16(tmem + kColD, v, k_major(th, ks, 0), id_v, ks > 0);
-          tc::mma_bf16(tmem + kColD, v, k_major(th + kTile, ks, 0), id_v, true);
-        }
-      if (!(ok = wait_one(kXReady, c))) break;
+      tc::mma_commit(&bars[L::kXFull]);
+      if (!kPair && !j.unit) product_v(vt, th);
+      if (kPair && kOutput) product_q(kt);  // (D as an operand comes where S is)
+      if (!(ok = reached(L::kXReady, c) && (!kPair || reached(L::kTFull, c)))) break;
       tc::fence_after_sync();
+      if (kPair && !j.unit) product_v(vt, th);
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th, ks, 0), id64, ks > 0 || !unit);
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOp + 8 * ks, k_major(th + kTile, ks, 0), id64, true);
-        tc::mma_bf16_ts(tmem + kColD, tmem + kColOpLo + 8 * ks, k_major(th, ks, 0), id64, true);
+        const uint32_t x = acc + L::kColXOp + 16 * ks;
+        tc::mma_bf16_ts(acc + L::kColD, x, k_major(th, ks, 0), id64, ks > 0 || !j.unit);
+        tc::mma_bf16_ts(acc + L::kColD, x, k_major(th + kTile, ks, 0), id64, true);
+        tc::mma_bf16_ts(acc + L::kColD, x + 8, k_major(th, ks, 0), id64, true);
       }
-      tc::mma_commit(&bars[kDFull]);
-      if (kOutput) {  // while D becomes an operand
-#pragma unroll
-        for (int x = 0; x < kHalves; ++x) product_s(kColQ, kt + kTile, x);
-        tc::mma_commit(&bars[kQFull]);
+      tc::mma_commit(&bars[L::kDFull]);
+      if (kOutput && !kPair) {  // while D becomes an operand
+        product_q(kt);
+        tc::mma_commit(&bars[L::kQFull]);
       }
-      if (!(ok = wait_one(kDReady, c) && (!kOutput || wait_one(kQFull, c)))) break;  // (U takes the place of S)
+      if (!(ok = reached(L::kDReady, c) && (!kOutput || kPair || reached(L::kQFull, c)))) break;  // (U takes the place of S)
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
         const uint64_t d = tc::sdesc_sw128(kt + ks * 2048, 2 * kTile, 1024);
-        tc::mma_bf16_ts(tmem + kColU, tmem + kColOp + 8 * ks, d, id_u, ks > 0);
-        tc::mma_bf16_ts(tmem + kColU, tmem + kColOpLo + 8 * ks, d, id_u, true);
+        tc::mma_bf16_ts(acc + kColU, tmem + L::kColOp + L::kOpStep * ks, d, id_u, ks > 0);
+        tc::mma_bf16_ts(acc + kColU, tmem + L::kColOp + L::kOpStep * ks + 8, d, id_u, true);
       }
-      tc::mma_commit(&bars[kUFull]);
+      tc::mma_commit(&bars[L::kUFull]);
       if (!kOutput) {
-        tc::mma_commit(&bars[kEmpty + st]);
+        tc::mma_commit(&bars[L::kEmpty + st]);
         continue;
       }
-      if (!(ok = wait_one(kOReady, c))) break;
+      if (!(ok = reached(L::kOReady, c) && (!kPair || reached(L::kPFull, c)))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int ks = 0; ks < kC / 16; ++ks) {
         const uint64_t d = k_major(pt, ks, 0);
-        tc::mma_bf16_ts(tmem + kColO, tmem + kColDo + 8 * ks, d, id64, true);
-        tc::mma_bf16_ts(tmem + kColO, tmem + kColDoLo + 8 * ks, d, id64, true);
+        tc::mma_bf16_ts(acc + L::kColO, tmem + L::kColDo + L::kOpStep * ks, d, id64, true);
+        tc::mma_bf16_ts(acc + L::kColO, tmem + L::kColDo + L::kOpStep * ks + 8, d, id64, true);
       }
-      tc::mma_commit(&bars[kDone]);
+      tc::mma_commit(&bars[L::kDone]);
     }
     // Every MMA has completed, and no commit's arrival is still due.
-    tc::mma_commit(&bars[kLast]);
-    mbar_wait(&bars[kLast], 0, p.ctl.spin_limit_ns);
+    tc::mma_commit(&bars[L::kLast]);
+    mbar_wait(&bars[L::kLast], 0, p.ctl.spin_limit_ns);
     const auto drained = [&](int bar, int count) {
       if (count > 0) mbar_wait(&bars[bar], (uint32_t)(count - 1) & 1u, p.ctl.spin_limit_ns);
     };
-    drained(kXFull, c), drained(kDFull, c), drained(kUFull, c);
-    if (kOutput) drained(kQFull, c), drained(kDone, c);
+    drained(L::kXFull, c), drained(L::kDFull, c), drained(L::kUFull, c);
+    if (kOutput) drained(L::kDone, c);
+    if (kOutput && !kPair) drained(L::kQFull, c);
     if (!kOutput)
-      for (int x = 0; x < kStages; ++x) drained(kEmpty + x, (c - x + kStages - 1) / kStages);
+      for (int x = 0; x < kStages; ++x) drained(L::kEmpty + x, (c - x + kStages - 1) / kStages);
   }
 
   tc::fence_before_sync();
@@ -979,16 +1169,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // padding, or after a wait that ran out everything of the segment
   const bool lost = *abort_flag != 0;
   if (lost && threadIdx.x == 0) record_error(p.hdr, p.ctl.epoch, SSM_ERR_TIMEOUT);
-  if (kOutput) {
-    __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (b * a.seqlen * a.nheads + h) * a.headdim + m0;
-    const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
-    const int64_t start = (int64_t)first * kC, end = min(a.seqlen, start + (int64_t)most * kC);
-    const int64_t stored = min((int64_t)n * kC, a.seqlen - start);
-    for (int64_t j = (start + (lost ? 0 : stored)) * rows + threadIdx.x; j < end * rows; j += kThreads)
-      yt[j / rows * a.nheads * a.headdim + j % rows] = fill;
+#pragma unroll
+  for (int i = 0; i < kSides; ++i) {
+    Job j = job(i);
+    count_tokens(p, j);
+    if (kOutput) {
+      __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(a.y) + (j.b * a.seqlen * a.nheads + j.h) * a.headdim + j.m0;
+      const __nv_bfloat16 fill = __float2bfloat16_rn(lost ? __uint_as_float(0x7fc00000u) : 0.f);
+      const int64_t start = (int64_t)j.first * kC, end = min(a.seqlen, start + (int64_t)j.most * kC);
+      const int64_t stored = min((int64_t)j.n * kC, a.seqlen - start);
+      for (int64_t e = (start + (lost ? 0 : stored)) * j.rows + threadIdx.x; e < end * j.rows; e += kThreads)
+        yt[e / j.rows * a.nheads * a.headdim + e % j.rows] = fill;
+    }
+    if (lost && j.to)
+      for (int e = threadIdx.x; e < j.rows * DK; e += kThreads) j.to[e] = __uint_as_float(0x7fc00000u);
   }
-  if (lost && to)
-    for (int j = threadIdx.x; j < rows * DK; j += kThreads) to[j] = __uint_as_float(0x7fc00000u);
 }
 
 // ---------------------------------------------------------------------------------- delta_join
@@ -1064,21 +1259,34 @@ constexpr int64_t kMaxRecords = (int64_t)1024 << 20;
 struct Segments {
   int64_t chunks, of;          // of the prompt, of a segment
   int64_t pieces, piece;       // of a segment's chains, and their chunks
+  bool pair;                   // two chains in a CTA
   size_t records, states, entering, passing, total;  // bytes
 };
-// How many pieces chains of `chunks` chunks are cut into, in units of a chunk's time in a chain (2.7 us): one without outputs takes
-// 0.8, the kernels more of a cut chain about eight, and a piece's part in delta_join one.
+// How many pieces chains of `chunks` chunks are cut into, and whether chains go in pairs, in units of a chunk's time in a chain
+// (2.7 us): one without outputs takes 0.8, those of a pair kPairTime as long, the kernels more of a cut chain about eight, and a
+// piece's part in delta_join one.
 constexpr int kSms = 152;
-int64_t pieces_of(int64_t heads, int64_t tiles, int64_t chunks) {
-  const auto rounds = [](int64_t jobs) { return (jobs + kSms - 1) / kSms; };
-  int64_t best = 1;
-  double least = (double)(rounds(heads * tiles) * chunks);
-  for (int64_t n = 2; n <= 32 && n * 8 <= chunks && heads * tiles * n <= 4 * kSms; ++n) {
-    const int64_t of = (chunks + n - 1) / n;
-    if ((chunks + of - 1) / of != n) continue;  // (the last would be empty)
-    const double cost =
-        (double)of * (0.8 * (double)rounds(heads * ((n - 1) * tiles + n - 2)) + (double)rounds(heads * n * tiles)) + 8 + (double)n;
-    if (cost < least) least = cost, best = n;
+struct Cut {
+  int64_t pieces;
+  bool pair;
+};
+constexpr double kPairTime = 1.3;
+Cut cut_of(int64_t heads, int headdim, int dstate, int64_t chunks) {
+  Cut best{};
+  double least = 0.;
+  for (int pair = 0; pair < (headdim <= 64 ? 2 : 1); ++pair) {
+    const int64_t rows = pair ? kM / 2 : kM, tiles = (headdim + rows - 1) / rows, units = (dstate + rows - 1) / rows;
+    const auto time = [&](int64_t jobs) {
+      const int64_t slots = pair ? 2 * kSms : kSms;
+      return (double)((jobs + slots - 1) / slots) * (pair ? kPairTime : 1.);
+    };
+    for (int64_t n = 1; n <= 32 && (n == 1 || (n * 8 <= chunks && heads * tiles * n <= 4 * kSms)); ++n) {
+      const int64_t of = (chunks + n - 1) / n;
+      if ((chunks + of - 1) / of != n) continue;  // (the last would be empty)
+      const double cost = (double)of * time(heads * n * tiles) +
+                          (n > 1 ? (double)of * 0.8 * time(heads * ((n - 1) * tiles + (n - 2) * units)) + 8 + (double)n : 0.);
+      if (best.pieces == 0 || cost < least) least = cost, best = {n, pair != 0};
+    }
   }
   return best;
 }
@@ -1087,7 +1295,9 @@ Segments segments(const ssm_delta_args& a) {
   const int64_t heads = a.batch * a.nheads, most = kMaxRecords / kRecord / heads;
   g.chunks = (a.seqlen + kC - 1) / kC;
   g.of = g.chunks <= most ? g.chunks : most;
-  g.pieces = pieces_of(heads, (a.headdim + kM - 1) / kM, g.of);
+  const Cut cut = cut_of(heads, a.headdim, a.dstate, g.of);
+  g.pieces = cut.pieces;
+  g.pair = cut.pair;
   g.piece = (g.of + g.pieces - 1) / g.pieces;
   const auto up = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
   const size_t state = (size_t)heads * a.headdim * a.dstate * sizeof(float);
@@ -1120,14 +1330,14 @@ bool delta_tc_supported(const ssm_delta_args& a) {
 
 namespace {
 
-template <int DK>
+template <int DK, bool kPair>
 cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segments& g, void* workspace, cudaStream_t s,
                             const DeltaTimer& timed) {
   const ssm_delta_args& a = p.a;
-  const size_t prep_bytes = sizeof(PrepShared<DK>) + 1024, chain_bytes = Layout<DK>::kTotal + 1024;
+  const size_t prep_bytes = sizeof(PrepShared<DK>) + 1024, chain_bytes = Layout<DK, kPair>::kTotal + 1024;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(delta_prepare_kernel<DK>), prep_bytes);
-  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK, true>), chain_bytes);
-  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK, false>), chain_bytes);
+  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK, true, kPair>), chain_bytes);
+  if (e == cudaSuccess) e = ensure_smem_limit(reinterpret_cast<const void*>(delta_chain_kernel<DK, false, kPair>), chain_bytes);
   if (e != cudaSuccess) return e;
   for (int64_t first = 0; first < g.chunks; first += g.of) {
     p.first = (int)first;
@@ -1137,21 +1347,22 @@ cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segme
     p.piece_chunks = (int)g.piece;
     p.pieces = (p.chunks + p.piece_chunks - 1) / p.piece_chunks;  // (of the last segment there may be fewer)
     const int64_t heads = a.batch * a.nheads;
+    constexpr int kSides = Layout<DK, kPair>::kSides, kUnits = (DK + kM / kSides - 1) / (kM / kSides);
     const auto chain = [&](auto kernel, int64_t jobs) {
-      return launch_pdl(kernel, dim3((unsigned)(heads * jobs)), dim3(kThreads), chain_bytes, s, maps[0], maps[1], maps[2], maps[3], p);
+      return launch_pdl(kernel, dim3((unsigned)((heads * jobs + kSides - 1) / kSides)), dim3(Layout<DK, kPair>::kThreads), chain_bytes, s, maps[0], maps[1], maps[2], maps[3], p);
     };
     e = timed(19, [&] {
       return launch_pdl(delta_prepare_kernel<DK>, dim3((unsigned)(a.batch * p.chunks * a.ngroups * p.batches)), dim3(kPrepThreads),
                         prep_bytes, s, maps[0], maps[1], p);
     });
     if (e == cudaSuccess && p.pieces > 1) {
-      e = timed(21, [&] { return chain(delta_chain_kernel<DK, false>, (p.pieces - 1) * p.tiles + p.pieces - 2); });
+      e = timed(21, [&] { return chain(delta_chain_kernel<DK, false, kPair>, (p.pieces - 1) * p.tiles + (p.pieces - 2) * kUnits); });
       if (e == cudaSuccess && p.pieces > 2)
         e = timed(22, [&] {
           return launch_pdl(delta_join_kernel<DK>, dim3((unsigned)(heads * ((a.headdim + kJoinRows - 1) / kJoinRows))), dim3(DK * kJoinParts), 0, s, p);
         });
     }
-    if (e == cudaSuccess) e = timed(20, [&] { return chain(delta_chain_kernel<DK, true>, p.pieces * p.tiles); });
+    if (e == cudaSuccess) e = timed(20, [&] { return chain(delta_chain_kernel<DK, true, kPair>, p.pieces * p.tiles); });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1169,7 +1380,7 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
   p.states = reinterpret_cast<float*>(p.records + g.records);
   p.entering = reinterpret_cast<float*>(p.records + g.records + g.states);
   p.passing = reinterpret_cast<float*>(p.records + g.records + g.states + g.entering);
-  p.tiles = (a.headdim + kM - 1) / kM;
+  p.tiles = (a.headdim + kM - 1) / kM;  // (of a pair 1)
   p.batches = (a.nheads / a.ngroups + kHeads - 1) / kHeads;
   p.ctl = ctl;
   CUtensorMap maps[4];
@@ -1193,7 +1404,11 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
   const cudaError_t e =
       encode_tensor_map_4d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  return a.dstate == 64 ? launch_segments<64>(p, maps, g, workspace, s, timed) : launch_segments<128>(p, maps, g, workspace, s, timed);
+  if (g.pair)
+    return a.dstate == 64 ? launch_segments<64, true>(p, maps, g, workspace, s, timed)
+                          : launch_segments<128, true>(p, maps, g, workspace, s, timed);
+  return a.dstate == 64 ? launch_segments<64, false>(p, maps, g, workspace, s, timed)
+                        : launch_segments<128, false>(p, maps, g, workspace, s, timed);
 }
 
 }  // namespace ssm
