@@ -15,17 +15,19 @@
 // delta_chain runs the chunks of one head one after the other, a CTA a chain, for up to 128 rows of the state (the rows
 // of S do not touch one another).  Rows are the MMAs' M, so that S, S k and d stay in TMEM lanes, one row a lane,
 // and go from one product to the next without a transposition:
-//     X, Q = S [K; Q]^T                    A = S (TMEM), B = K and Q          128 x 128 x dstate
+//     X = S K^T, Q = S Q^T                 A = S (TMEM), B = K, Q             128 x 64 x dstate
 //     D = V^T T^T + (X diag(-e^G)) T^T     A = V^T (smem), then X (TMEM); B = T
 //     U = (D diag(e^(G_last - G))) K       A = D (TMEM), B = K: S' = e^(G_last) S + U
 //     O = Q diag(scale e^G) + D P^T        A = D (TMEM), B = P
-// Its bound is the chain of a chunk: three products, and the three conversions between them, 5500 cycles of which the tensor
-// cores work 2800 (the same prompt: 365 us for 128 chains of 128 chunks, both kernels 537 us; b8 L2048 nh24 64x128: 179 us).
+// Its bound is the chain of a chunk: three products (X, D, U), the three conversions between them, and six hand-overs by
+// barriers: 4900 cycles, of which the tensor cores work 2500 (the same prompt: 325 us for 128 chains of 128 chunks, both
+// kernels 504 us).  Where there are more chains than SMs, of at most 64 rows, two of them share a CTA: one converts
+// while the other's products run (a chunk of both: 7200 cycles; b8 L2048 nh24 64x128: 122 us, one by one 174).
 //
 // Few chains leave most of the GPU idle, so they are cut into pieces that run at once.  A piece is linear in the state that
 // enters it: S_out = S_in M + N.  A first run of the chains (without outputs) gives N from a zero state, and M from
 // the unit matrix's rows and no values, as another tile of rows; delta_join multiplies the pieces up in f32, and
-// a second run, now with each piece's own state, gives the outputs (b1 L65521 nh32 64x128: 3.08 ms whole, 1.97 ms so).
+// a second run, now with each piece's own state, gives the outputs (b1 L65521 nh32 64x128: 3.08 ms whole, 1.97 ms so at the time, 1.42 in pairs).
 //
 // Rounding.  q, k and v are bf16 and enter as they are (lengths and decays are factors beside the products).  S is kept in f32
 // registers; as operands S, X, T and the D of the update are split into two bf16 halves (hi + lo, 2^-18 together; lo x lo is
@@ -1263,8 +1265,9 @@ struct Segments {
   size_t records, states, entering, passing, total;  // bytes
 };
 // How many pieces chains of `chunks` chunks are cut into, and whether chains go in pairs, in units of a chunk's time in a chain
-// (2.7 us): one without outputs takes 0.8, those of a pair kPairTime as long, the kernels more of a cut chain about eight, and a
-// piece's part in delta_join one.
+// (2.5 us): one without outputs takes 0.8, those of a pair kPairTime as long, the kernels more of a cut chain about eight, and a
+// piece's part in delta_join one.  (Chains by themselves and in pairs: b4 L4096 nh32 64x128 170 and 215 us, b2 L8192 nh32 in
+// pieces 386 and 357, b4 L4096 nh48 64x64 279 and 190.)
 constexpr int kSms = 152;
 struct Cut {
   int64_t pieces;
