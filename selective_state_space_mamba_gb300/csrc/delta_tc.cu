@@ -851,7 +851,7 @@ __global__ void __launch_bounds__((Layout<DK, kPair>::kThreads), 1)
         tc::fence_before_sync();
         arrive(L::kSReady + q);
       }
-      if (kOutput && c > 0) ok = ok && output(c - 1);
+      if (kOutput && kPair && c > 0) ok = ok && output(c - 1);
       // X, scaled, as an operand
       ok = ok && wait(L::kFull + st, c / kStages) && wait(L::kXFull, c);
       if (!ok) break;
@@ -863,7 +863,8 @@ __global__ void __launch_bounds__((Layout<DK, kPair>::kThreads), 1)
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(L::kXReady);
-      if (kOutput && c > 0) give(c - 1);
+      if (kOutput && !kPair && c > 0) ok = ok && output(c - 1);
+      if (kOutput && c > 0 && ok) give(c - 1);
       // D scaled as an operand of the update
       if (!(ok = wait(L::kDFull, c))) break;
       tc::fence_after_sync();
