@@ -57,7 +57,10 @@ static_assert(sizeof(Factors) <= 1024 && kRecordCopied % 16 == 0, "record");
 struct Params {
   ssm_delta_args a;
   unsigned char* records;  // [batch][nheads][chunks of the segment]
-  float* states;           // between segments: [batch][nheads][headdim][dstate]
+  // [batch][nheads][headdim][dstate] each: what the segment enters with, what it leaves for the next one.  Two places, as the CTAs of
+  // a chain's first and last piece are not ordered.
+  const float* before;
+  float* after;
   int pieces, piece_chunks; // of a segment's chains (1: whole)
   float* entering;         // [pieces - 1] like states: N of a piece, then what the next one enters with
   float* passing;          // [pieces - 2][batch][nheads][dstate][dstate]: M of the pieces but the first and the last
@@ -614,8 +617,8 @@ __device__ __forceinline__ Job job_of(const Params& p, int64_t index) {
     j.from = nullptr;
     j.to = p.passing + (((j.piece - 1) * heads + j.bh) * DK + j.m0) * DK;
   } else {
-    j.from = j.piece == 0 ? (p.begins ? a.h0 : p.states) : kOutput ? p.entering + (j.piece - 1) * slot : nullptr;
-    j.to = !kOutput ? p.entering + j.piece * slot : j.piece < p.pieces - 1 ? nullptr : p.ends ? a.h_final : p.states;
+    j.from = j.piece == 0 ? (p.begins ? a.h0 : p.before) : kOutput ? p.entering + (j.piece - 1) * slot : nullptr;
+    j.to = !kOutput ? p.entering + j.piece * slot : j.piece < p.pieces - 1 ? nullptr : p.ends ? a.h_final : p.after;
     if (j.from) j.from += tile_at;
     if (j.to) j.to += tile_at;
   }
@@ -1263,7 +1266,8 @@ struct Segments {
   int64_t chunks, of;          // of the prompt, of a segment
   int64_t pieces, piece;       // of a segment's chains, and their chunks
   bool pair;                   // two chains in a CTA
-  size_t records, states, entering, passing, total;  // bytes
+  int places;                  // of the states between segments
+  size_t records, states, entering, passing, total;  // bytes (states: a place)
 };
 // How many pieces chains of `chunks` chunks are cut into, and whether chains go in pairs, in units of a chunk's time in a chain
 // (2.5 us): one without outputs takes 0.8, those of a pair kPairTime as long, the kernels more of a cut chain about eight, and a
@@ -1307,9 +1311,10 @@ Segments segments(const ssm_delta_args& a) {
   const size_t state = (size_t)heads * a.headdim * a.dstate * sizeof(float);
   g.records = (size_t)(heads * g.of) * kRecord;
   g.states = g.of < g.chunks ? up(state) : 0;
+  g.places = g.chunks > 2 * g.of ? 2 : g.of < g.chunks ? 1 : 0;  // (two segments: the one writes, the other reads)
   g.entering = up((size_t)(g.pieces - 1) * state);
   g.passing = g.pieces > 2 ? (size_t)((g.pieces - 2) * heads) * a.dstate * a.dstate * sizeof(float) : 0;
-  g.total = kHeaderBytes + g.records + g.states + g.entering + g.passing;
+  g.total = kHeaderBytes + g.records + g.places * g.states + g.entering + g.passing;
   return g;
 }
 
@@ -1335,8 +1340,7 @@ bool delta_tc_supported(const ssm_delta_args& a) {
 namespace {
 
 template <int DK, bool kPair>
-cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segments& g, void* workspace, cudaStream_t s,
-                            const DeltaTimer& timed) {
+cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segments& g, cudaStream_t s, const DeltaTimer& timed) {
   const ssm_delta_args& a = p.a;
   const size_t prep_bytes = sizeof(PrepShared<DK>) + 1024, chain_bytes = Layout<DK, kPair>::kTotal + 1024;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(delta_prepare_kernel<DK>), prep_bytes);
@@ -1348,6 +1352,11 @@ cudaError_t launch_segments(Params& p, const CUtensorMap (&maps)[4], const Segme
     p.chunks = (int)(g.chunks - first < g.of ? g.chunks - first : g.of);
     p.begins = first == 0;
     p.ends = first + g.of >= g.chunks;
+    const auto place = [&](int64_t segment) {  // of the states behind a segment
+      return reinterpret_cast<float*>(p.records + g.records + (g.places == 2 ? segment % 2 : 0) * g.states);
+    };
+    const int64_t segment = first / g.of;
+    p.before = place(segment + 1), p.after = place(segment);
     p.piece_chunks = (int)g.piece;
     p.pieces = (p.chunks + p.piece_chunks - 1) / p.piece_chunks;  // (of the last segment there may be fewer)
     const int64_t heads = a.batch * a.nheads;
@@ -1381,9 +1390,9 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
   p.a = a;
   p.hdr = static_cast<WsHeader*>(workspace);
   p.records = static_cast<unsigned char*>(workspace) + kHeaderBytes;
-  p.states = reinterpret_cast<float*>(p.records + g.records);
-  p.entering = reinterpret_cast<float*>(p.records + g.records + g.states);
-  p.passing = reinterpret_cast<float*>(p.records + g.records + g.states + g.entering);
+  unsigned char* const behind = p.records + g.records + g.places * g.states;
+  p.entering = reinterpret_cast<float*>(behind);
+  p.passing = reinterpret_cast<float*>(behind + g.entering);
   p.tiles = (a.headdim + kM - 1) / kM;  // (of a pair 1)
   p.batches = (a.nheads / a.ngroups + kHeads - 1) / kHeads;
   p.ctl = ctl;
@@ -1409,10 +1418,10 @@ cudaError_t launch_delta_tc(const ssm_delta_args& a, void* workspace, const Look
       encode_tensor_map_4d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   if (g.pair)
-    return a.dstate == 64 ? launch_segments<64, true>(p, maps, g, workspace, s, timed)
-                          : launch_segments<128, true>(p, maps, g, workspace, s, timed);
-  return a.dstate == 64 ? launch_segments<64, false>(p, maps, g, workspace, s, timed)
-                        : launch_segments<128, false>(p, maps, g, workspace, s, timed);
+    return a.dstate == 64 ? launch_segments<64, true>(p, maps, g, s, timed)
+                          : launch_segments<128, true>(p, maps, g, s, timed);
+  return a.dstate == 64 ? launch_segments<64, false>(p, maps, g, s, timed)
+                        : launch_segments<128, false>(p, maps, g, s, timed);
 }
 
 }  // namespace ssm
