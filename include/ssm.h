@@ -396,8 +396,9 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
  * before it in its chunk, and decays above 1 (A > 0, or a negative dt without the softplus) are taken as they are, but their
  * product over 64 tokens has to stay in f32's range.
  * Workspace (0 bytes where the sizes need none): 25,600 bytes for each head and chunk, of long prompts for a segment at a
- * time.  It need not be zero-filled and carries nothing from call to call; a call that uses it clears the status word
- * and ssm_check_device_status reports its waits (bounded: after one that ran out y and h_final are NaN from there on).
+ * time.  It need not be zero-filled and carries nothing from call to call.  Every call whose sizes need one clears its status
+ * word (one that goes token by token too), so ssm_check_device_status reports the waits of the last of them (bounded: after one that
+ * ran out every element of y and h_final is right or NaN).
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_WORKSPACE, SSM_ERR_CUDA.
  */
 typedef struct {

@@ -889,7 +889,8 @@ ssm_status ssm_delta_fwd(const ssm_delta_args* args, void* workspace, size_t wor
   out.dense(a.h_final, 4, {a.batch, a.nheads, a.headdim, a.dstate});
   if ((st = check_spans(in, out)) != SSM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (delta_tc_sizes(a)) {
+  const bool needs = delta_tc_sizes(a);
+  if (needs) {
     if (!workspace || workspace_bytes < delta_tc_workspace(a)) return SSM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SSM_ERR_ALIGNMENT;
     if (delta_tc_supported(a)) {
@@ -904,7 +905,7 @@ ssm_status ssm_delta_fwd(const ssm_delta_args* args, void* workspace, size_t wor
       return SSM_ERR_CUDA;
     }
   }
-  return launch_status(15, s, [&] { return launch_delta(a, s); });
+  return launch_status(15, s, [&] { return launch_delta(a, needs ? workspace : nullptr, s); });
 }
 
 ssm_status ssm_delta_step(const ssm_delta_args* args, const int32_t* slots, int64_t nslots, ssm_stream_t stream) {

@@ -23,13 +23,14 @@ constexpr int kTile = 16;   // tokens
 constexpr int kOwn = kTile / 4;  // of a warp
 
 template <typename T, int DK, int LPR, int ROWS, bool kAhead>
-__global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_constant__ ssm_delta_args a) {
+__global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_constant__ ssm_delta_args a, WsHeader* hdr) {
   constexpr int COLS = DK / LPR, GROUPS = kScan / LPR, CTA_ROWS = GROUPS * ROWS, V4 = COLS / 4;
   constexpr int VL = (CTA_ROWS + 31) / 32;  // v and y of a token a lane
   __shared__ __align__(16) float sk[2][kTile][DK], sq[2][kTile][DK];
   __shared__ float sv[2][kTile][CTA_ROWS], sy[2][kTile][CTA_ROWS];  // beta v; y
   __shared__ float4 st[2][kTile];  // a, beta a, k.q, k.(k of the token before)
   griddep_wait();
+  if (hdr && blockIdx.x == 0 && threadIdx.x == 0) hdr->status = 0;  // a workspace's status is this call's, which has no waits
   const int tiles = (a.headdim + CTA_ROWS - 1) / CTA_ROWS;
   const int row0 = (int)(blockIdx.x % tiles) * CTA_ROWS;
   const int64_t bh = blockIdx.x / tiles;
@@ -330,10 +331,10 @@ bool delta_resident(const ssm_delta_args& a) { return a.batch * a.nheads * ((a.h
 namespace {
 
 template <typename T>
-cudaError_t launch_type(const ssm_delta_args& a, cudaStream_t s) {
+cudaError_t launch_type(const ssm_delta_args& a, WsHeader* hdr, cudaStream_t s) {
   const auto go = [&](auto kernel, int cta_rows) {
     const int64_t tiles = (a.headdim + cta_rows - 1) / cta_rows;
-    return launch_pdl(kernel, dim3((unsigned)(a.batch * a.nheads * tiles)), dim3(2 * kScan), 0, s, a);
+    return launch_pdl(kernel, dim3((unsigned)(a.batch * a.nheads * tiles)), dim3(2 * kScan), 0, s, a, hdr);
   };
   const bool few = delta_resident(a);
   switch (a.dstate) {
@@ -348,8 +349,9 @@ cudaError_t launch_type(const ssm_delta_args& a, cudaStream_t s) {
 
 int64_t delta_ctas(const ssm_delta_args& a) { return a.batch * a.nheads * ((a.headdim + 15) / 16); }
 
-cudaError_t launch_delta(const ssm_delta_args& a, cudaStream_t s) {
-  return a.dtype == SSM_F32 ? launch_type<float>(a, s) : launch_type<__nv_bfloat16>(a, s);
+cudaError_t launch_delta(const ssm_delta_args& a, void* workspace, cudaStream_t s) {
+  WsHeader* const hdr = static_cast<WsHeader*>(workspace);
+  return a.dtype == SSM_F32 ? launch_type<float>(a, hdr, s) : launch_type<__nv_bfloat16>(a, hdr, s);
 }
 
 }  // namespace ssm

@@ -468,7 +468,7 @@ cudaError_t launch_rmsnorm(const void* x, int64_t x_stride, const float* weight,
 // The gated delta rule, and the norms with a gate and a residual (likewise).
 int64_t delta_ctas(const ssm_delta_args& a);  // CTAs that launch_delta takes at most
 bool delta_resident(const ssm_delta_args& a);  // whether all its CTAs run at once
-cudaError_t launch_delta(const ssm_delta_args& a, cudaStream_t s);
+cudaError_t launch_delta(const ssm_delta_args& a, void* workspace, cudaStream_t s);  // workspace: NULL, or one whose status it clears
 // delta_tc: the sizes that it takes, and the strides too; its workspace.  `timed` runs a launch of a kernel id.
 bool delta_tc_sizes(const ssm_delta_args& a);
 bool delta_tc_supported(const ssm_delta_args& a);
