@@ -360,14 +360,14 @@ def check_device_status(workspace: Workspace | None = None, kind: str = "ssd", d
     """Synchronise and return (and clear) the device status word of a workspace (0 = OK).
 
     Without a workspace: that of the last call of ``kind`` ("ssd", "linscan", "scan_" and a baseline's
-    name, or "selscan") that was given none."""
+    name, "selscan", or "delta") that was given none."""
     torch = _torch()
     lib = _lib.load()
     if workspace is None:
         dev = torch.device(device if device is not None else "cuda")
-        if kind == "selscan":
+        if kind in ("selscan", "delta"):
             from . import _layer
-            buf = _layer.kept_workspace(dev.index if dev.index is not None else torch.cuda.current_device())
+            buf = _layer.kept_workspace(dev.index if dev.index is not None else torch.cuda.current_device(), kind)
             return 0 if buf is None else int(lib.ssm_check_device_status(_ptr(buf), _stream_ptr(buf.device)))
         workspace = _default_ws.get((kind, dev.index if dev.index is not None else torch.cuda.current_device()))
         if workspace is None:

@@ -75,9 +75,10 @@ def selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups=1) -> i
     return int(_lib.load().ssm_selscan_fwd_workspace_bytes(batch, seqlen, channels, dstate, ngroups))
 
 
-def kept_workspace(device_index: int):
-    """The memory that the last selscan_fwd without a workspace allocated, or None (for check_device_status)."""
-    return (_native or _load()).kept_workspace(device_index)
+def kept_workspace(device_index: int, kind: str = "selscan"):
+    """The memory that the last selscan_fwd (kind "delta": delta_fwd) without a workspace allocated, or None (for
+    check_device_status)."""
+    return (_native or _load()).kept_workspace(device_index, kind == "delta")
 
 
 def selscan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lens=None, *, softplus: bool = True, y=None,
@@ -156,8 +157,9 @@ def delta_fwd(q, k, v, dt, beta, A, dt_bias=None, h0=None, lens=None, *, scale=N
     group h // (nh / G).  scale: None for N ** -0.5.  Without softplus the decay is exp(A (dt + dt_bias)), without
     sigmoid beta is taken as it is, without l2norm q and k are.  Returns (y, h_final): y [b, L, nh, H], 0 in
     the padding, and the float32 state after the last token (None when return_final_state is False).
-    Without a workspace (Workspace), one is allocated for the call where it is needed; with one,
-    check_device_status(workspace) tells whether a wait inside the last call that needed it ran out.
+    Without a workspace (Workspace), one is allocated for the call where it is needed, and kept until the next such call (up to
+    1 GiB and two states of all heads).  check_device_status(workspace), or check_device_status(kind="delta") without one,
+    tells whether a wait inside the last call that needed one ran out.
     """
     buf = None
     if workspace is not None:

@@ -256,8 +256,9 @@ ssm_selscan_args selscan_args(PyObject* const* v, const Like& like, const at::Te
   return a;
 }
 
-// The workspace of each device's last scan that was given none: its status can still be read (kept_workspace).
-PyObject* g_kept[C10_COMPILE_TIME_MAX_GPUS] = {};
+// The workspace of each device's last call of a kind that was given none: its status can still be read (kept_workspace).
+enum Kept { kSelscan, kDelta, kKinds };
+PyObject* g_kept[kKinds][C10_COMPILE_TIME_MAX_GPUS] = {};
 
 // u, dt, A, B, C, D, z, dt_bias, h0, lens, softplus, y, h_final, return_final_state, workspace buffer
 PyObject* selscan_fwd(PyObject* const* v) {
@@ -284,7 +285,7 @@ PyObject* selscan_fwd(PyObject* const* v) {
     const size_t need = g_fn.selscan_fwd_workspace_bytes(a.batch, a.seqlen, a.channels, a.dstate, a.ngroups);
     if (need) {
       ws = like.empty({(int64_t)need}, at::kByte);
-      PyObject*& kept = g_kept[like.device.index()];
+      PyObject*& kept = g_kept[kSelscan][like.device.index()];
       Py_XDECREF(kept);
       kept = THPVariable_Wrap(ws);
     }
@@ -350,10 +351,11 @@ struct Norm {
   }
 };
 
-PyObject* kept_workspace(PyObject* const* v) {  // device index
+PyObject* kept_workspace(PyObject* const* v) {  // device index, whether delta_fwd's
   const long i = PyLong_AsLong(v[0]);
   if (PyErr_Occurred()) return nullptr;
-  PyObject* o = i >= 0 && i < C10_COMPILE_TIME_MAX_GPUS && g_kept[i] ? g_kept[i] : Py_None;
+  const Kept kind = truth(v[1]) ? kDelta : kSelscan;
+  PyObject* o = i >= 0 && i < C10_COMPILE_TIME_MAX_GPUS && g_kept[kind][i] ? g_kept[kind][i] : Py_None;
   Py_INCREF(o);
   return o;
 }
@@ -448,6 +450,7 @@ PyObject* delta_fwd(PyObject* const* v) {
   if (truth(v[15])) h.set("h_final", v[14], state, at::kFloat, like);
   a.h_final = static_cast<float*>(h.ptr);
   at::Tensor ws;
+  PyObject** kept = nullptr;
   if (v[16] != Py_None) {
     ws = tensor("workspace", v[16]);
     if (ws.device() != like.device || ws.scalar_type() != at::kByte || !ws.is_contiguous())
@@ -455,11 +458,17 @@ PyObject* delta_fwd(PyObject* const* v) {
   } else {
     const size_t need =
         g_fn.delta_fwd_workspace_bytes(a.batch, a.seqlen, a.nheads, a.headdim, a.dstate, a.ngroups, like.code);
-    if (need) ws = like.empty({(int64_t)need}, at::kByte);
+    if (need) {
+      // the one before goes first: it may be of a gigabyte, and its memory then serves this call
+      kept = &g_kept[kDelta][like.device.index()];
+      Py_CLEAR(*kept);
+      ws = like.empty({(int64_t)need}, at::kByte);
+    }
   }
-  return result(g_fn.delta_fwd(&a, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0,
-                               like.stream()),
-                y, h);
+  const ssm_status st = g_fn.delta_fwd(&a, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0,
+                                       like.stream());
+  if (kept && st == SSM_OK) *kept = THPVariable_Wrap(ws);  // (a call that was refused has written no status)
+  return result(st, y, h);
 }
 
 // q, k, v, dt, beta, A, dt_bias, state, slots, scale, softplus, sigmoid, l2norm, y, state_out, inplace
@@ -592,7 +601,7 @@ PyMethodDef g_methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                            {"selscan_fwd", fast(entry<selscan_fwd, 15>), METH_FASTCALL, nullptr},
                            {"selscan_step", fast(entry<selscan_step, 14>), METH_FASTCALL, nullptr},
                            {"rmsnorm_fwd", fast(entry<rmsnorm_fwd, 6>), METH_FASTCALL, nullptr},
-                           {"kept_workspace", fast(entry<kept_workspace, 1>), METH_FASTCALL, nullptr},
+                           {"kept_workspace", fast(entry<kept_workspace, 2>), METH_FASTCALL, nullptr},
                            {"rmsnorm_fp8_fwd", fast(entry<rmsnorm_fp8_fwd, 8>), METH_FASTCALL, nullptr},
                            {"delta_fwd", fast(entry<delta_fwd, 17>), METH_FASTCALL, nullptr},
                            {"delta_step", fast(entry<delta_step, 16>), METH_FASTCALL, nullptr},
