@@ -22,7 +22,7 @@
 // Its bound is the chain of a chunk: three products (X, D, U), the three conversions between them, and six hand-overs by
 // barriers: 4900 cycles, of which the tensor cores work 2500 (the same prompt: 325 us for 128 chains of 128 chunks, both
 // kernels 504 us).  Where there are more chains than SMs, of at most 64 rows, two of them share a CTA: one converts
-// while the other's products run (a chunk of both: 7200 cycles; b8 L2048 nh24 64x128: 122 us, one by one 174).
+// while the other's products run (64x128: 3.4 us a chunk of both, one alone 2.5; b8 L2048 nh24 64x128: 122 us, one by one 174).
 //
 // Few chains leave most of the GPU idle, so they are cut into pieces that run at once.  A piece is linear in the state that
 // enters it: S_out = S_in M + N.  A first run of the chains (without outputs) gives N from a zero state, and M from
@@ -1271,14 +1271,16 @@ struct Segments {
 };
 // How many pieces chains of `chunks` chunks are cut into, and whether chains go in pairs, in units of a chunk's time in a chain
 // (2.5 us): one without outputs takes 0.8, those of a pair kPairTime as long, the kernels more of a cut chain about eight, and a
-// piece's part in delta_join one.  (Chains by themselves and in pairs: b4 L4096 nh32 64x128 170 and 215 us, b2 L8192 nh32 in
-// pieces 386 and 357, b4 L4096 nh48 64x64 279 and 190.)
+// piece's part in delta_join one.  kPairTime: 128 chains by themselves and 256 in pairs, L8192, take 321 and 434 us with 64x128, 268
+// and 372 with 64x64 (1.35 and 1.39 as long), without outputs 276 and 354, 233 and 290 (1.28 and 1.25).  Whole calls by themselves and in
+// pairs: b4 L4096 nh32 64x128 247 and 301 us, b2 L8192 nh32 in pieces 390 and 371, b4 L4096 nh48 64x64 377 and 297; 16 heads
+// L8192 64x128 in 6 pieces 155, in 8 of pairs 167 (kPairTime 1.3 takes those).
 constexpr int kSms = 152;
 struct Cut {
   int64_t pieces;
   bool pair;
 };
-constexpr double kPairTime = 1.3;
+constexpr double kPairTime = 1.35;
 Cut cut_of(int64_t heads, int headdim, int dstate, int64_t chunks) {
   Cut best{};
   double least = 0.;
