@@ -390,8 +390,8 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
  * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing nheads, dstate in {32, 64, 128}, headdim >= 1,
  * nheads * headdim and ngroups * dstate <= 2^30.
  * bf16 prompts with dstate 64 or 128 and headdim a multiple of 8, whose q, k and v have rows on 16-byte boundaries, go
- * through the tensor cores in chunks of 64 tokens from 72 tokens on (from 32 where batch * nheads * ceil(headdim / 16) is above
- * 304; seqlen of the call, not lens): one kernel for what does not depend on the state, one for the chain of states.  The
+ * through the tensor cores in chunks of 64 tokens from 112 tokens on (seqlen of the call, not lens; with n = batch * nheads *
+ * ceil(headdim / 16), from 72 where dstate is 128 and n above 152, from 56 for n above 304, 40 from 1024, 24 from 4096): one kernel for what does not depend on the state, one for the chain of states.  The
  * others go token by token.  In chunks, a NaN or an infinity in a token may reach the outputs of the up to 63 tokens
  * before it in its chunk, and decays above 1 (A > 0, or a negative dt without the softplus) are taken as they are, but their
  * product over 64 tokens has to stay in f32's range.

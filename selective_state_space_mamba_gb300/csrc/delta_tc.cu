@@ -1320,14 +1320,36 @@ Segments segments(const ssm_delta_args& a) {
   return g;
 }
 
+// The shortest prompt that goes in chunks.  One of one chunk takes 13 to 24 us, of two 15 to 30 (more sequences or heads: up to 87); token
+// by token (delta.cu) a prompt takes 0.10 (64 columns) to 0.14 us a token while there is a CTA an SM, to 0.25 with two, more where CTAs
+// wait for others.  Token by token / in chunks, us, and where the two are as long:
+//   CTAs of 16 rows                                tokens          as long at
+//   up to 152    b1 nh24 64x128                    96: 15.4/17.7   112
+//                b1 nh8 64x64                      112: 12.6/14.7  131
+//                b1 nh12 128x128                   112: 17.5/21.5  138
+//   to 304       b1 nh32 128x64                    96: 16.8/17.2   98
+//                b4 nh16 64x64                     112: 19.2/21.0  124
+//                b1 nh32 128x128 (128 columns)     72: 19.8/20.1   73
+//                b2 nh32 64x128                    96: 24.6/23.5   91
+//   to 1023      b8 nh24 64x64                     48: 19.5/21.3   52
+//                b3 nh32 64x128                    48: 17.5/16.9   46
+//                b5 nh16 64x128                    56: 20.6/21.6   59
+//   to 4095      b4 nh32 128x128                   32: 23.6/23.4   32
+//                b16 nh24 64x128                   40: 43.4/36.5   36
+//                b12 nh32 64x64                    40: 32.4/32.3   40
+//   more         b32 nh32 128x128                  24: 129/87      16
+//                b64 nh24 64x64                    24: 74.5/74.6   24
+int64_t chunks_from(const ssm_delta_args& a) {
+  const int64_t ctas = delta_ctas(a);
+  if (delta_resident(a)) return ctas > kSms && a.dstate == 128 ? 72 : 112;
+  return ctas < 1024 ? 56 : ctas < 4096 ? 40 : 24;
+}
+
 }  // namespace
 
-// A prompt of one chunk takes 14 to 22 us, of two 17 to 25; token by token (delta.cu) 16 tokens take 5.5 to 7 us and each more 0.13
-// to 0.23 us while all its CTAs are resident (b1 nh24 64x128: as long as chunks at 105 tokens, b1 nh32 128x128 at 61 and 72),
-// from 0.3 to 0.6 us a token where they are not (b4 nh32 128x128: at 29, b8 nh24 64x64: at 48).
 bool delta_tc_sizes(const ssm_delta_args& a) {
   return a.dtype == SSM_BF16 && (a.dstate == 64 || a.dstate == 128) && a.headdim % 8 == 0 &&
-         a.seqlen >= (delta_resident(a) ? 72 : 32) && a.seqlen <= 0x7fffffff - kC && a.batch * a.nheads <= kMaxRecords / kRecord;
+         a.seqlen >= chunks_from(a) && a.seqlen <= 0x7fffffff - kC && a.batch * a.nheads <= kMaxRecords / kRecord;
 }
 size_t delta_tc_workspace(const ssm_delta_args& a) { return segments(a).total; }
 

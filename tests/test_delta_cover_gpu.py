@@ -133,3 +133,62 @@ def test_long_prompts_token_by_token(case):
     assert launched(timer) == {"delta"}
     close(host(y), y_ref, ey, "y", dtype)
     rows_close(host(h), h_ref, eh, "h")
+
+
+# What test_delta_gpu.py has of options, heads of a group, and chunks of fewer than 64 tokens, at lengths that go in chunks.
+@pytest.mark.parametrize("options", [dict(softplus=False), dict(sigmoid=False), dict(l2norm=False), dict(scale=0.7),
+                                     dict(softplus=False, sigmoid=False, l2norm=False, scale=-2.0)], ids=str)
+def test_options_in_chunks(options):
+    import selective_state_space_mamba_gb300 as ssm
+    from test_delta_gpu import rounded
+    r = rng_of("options in chunks", options)
+    s = inputs(r, 2, 150, 2, 1, 64, 128, "bf16", bias=False)
+    if not options.get("softplus", True):
+        s["dt"] = np.abs(s["dt"]) * 0.125
+    if not options.get("sigmoid", True):
+        s["beta"] = rounded(r.uniform(0, 1, s["beta"].shape), "bf16")
+    if not options.get("l2norm", True):  # lengths below 1
+        s["q"], s["k"] = (rounded(v / (1.01 * np.linalg.norm(v, axis=-1, keepdims=True)), "bf16") for v in (s["q"], s["k"]))
+    y_ref, ey, h_ref, eh = od.delta(**s, **options, split=SPLIT, out=OUT)
+    with ssm.KernelTimer() as timer:
+        y, h = ssm.delta_fwd(**on_device(s, "bf16"), h0=dev(s["h0"]), **options)
+    assert launched(timer) == {"delta_prepare", "delta_chain"}
+    close(host(y), y_ref, ey, "y", "bf16")
+    rows_close(host(h), h_ref, eh, "h")
+
+
+CHUNKS = [  # b, L, nh, G, H, N, lens
+    (2, 120, 4, 4, 24, 64, None), (2, 120, 8, 1, 24, 64, None), (2, 113, 6, 1, 24, 64, [112, 65]), (2, 127, 10, 2, 24, 64, None),
+    (64, 24, 64, 16, 8, 64, None), (32, 33, 128, 8, 8, 64, [33, 1, 32, 31, 0, 16, 17, 33] * 4), (8, 56, 40, 4, 8, 128, [56, 1, 0, 55, 33, 32, 16, 2]),
+    (16, 40, 16, 2, 64, 128, [40, 1, 0, 39, 33, 32, 16, 2] * 2),
+]
+
+
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: str(c[:6]))
+def test_short_prompts_in_chunks(case):
+    import selective_state_space_mamba_gb300 as ssm
+    from test_delta_gpu import ints
+    b, L, nh, G, H, N, lens = case
+    s = inputs(rng_of("short", case), b, L, nh, G, H, N, "bf16")
+    y_ref, ey, h_ref, eh = od.delta(**s, lens=lens, split=SPLIT, out=OUT)
+    if lens is not None:  # padding may hold anything
+        for i, n in enumerate(od._lens(lens, b, L)):
+            for k in ("q", "k", "v", "dt", "beta"):
+                s[k][i, n:] = np.nan
+    with ssm.KernelTimer() as timer:
+        y, h = ssm.delta_fwd(**on_device(s, "bf16"), h0=dev(s["h0"]), lens=ints(lens))
+    assert launched(timer) == {"delta_prepare", "delta_chain"}
+    close(host(y), y_ref, ey, "y", "bf16")
+    rows_close(host(h), h_ref, eh, "h")
+
+
+def test_a_token_before_chunks():
+    """The last length that goes token by token."""
+    import selective_state_space_mamba_gb300 as ssm
+    s = inputs(rng_of("before chunks"), 2, 111, 4, 2, 24, 64, "bf16")
+    y_ref, ey, h_ref, eh = od.delta(**s)
+    with ssm.KernelTimer() as timer:
+        y, h = ssm.delta_fwd(**on_device(s, "bf16"), h0=dev(s["h0"]))
+    assert launched(timer) == {"delta"}
+    close(host(y), y_ref, ey, "y", "bf16")
+    rows_close(host(h), h_ref, eh, "h")

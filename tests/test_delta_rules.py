@@ -23,3 +23,11 @@ def test_chains_are_cut_as_measured():
     assert pieces(1, 64 * 512, 9, 64, 128) == 16   # 327, 24: 350
     assert pieces(1, 64 * 32, 32, 64, 64) == 3     # 77, 4: 81
     assert pieces(4, 4096, 32, 64, 128) == 1 and pieces(2, 8192, 32, 64, 128) == 3
+
+
+def test_prompts_go_in_chunks_where_that_is_shorter():
+    """From the first length on that is named; the measured times that it comes from stand beside the rule in csrc/delta_tc.cu."""
+    for b, nh, H, N, first in ((1, 24, 64, 128, 112), (1, 8, 64, 64, 112), (1, 32, 128, 64, 112), (1, 19, 128, 128, 112), (1, 20, 128, 128, 72),
+                               (1, 38, 128, 128, 72), (1, 39, 128, 128, 56), (8, 24, 64, 64, 56), (255, 1, 64, 64, 56), (256, 1, 64, 64, 40),
+                               (4, 32, 128, 128, 40), (1023, 1, 64, 128, 40), (1024, 1, 64, 128, 24), (32, 32, 128, 128, 24)):
+        assert need(b, first - 1, nh, H, N) == 0 and need(b, first, nh, H, N) > 0, (b, nh, H, N)
