@@ -389,16 +389,25 @@ SSM_API ssm_status ssm_rmsnorm_fp8_fwd(const void *x, int64_t x_stride, const fl
  * States and sums are f32; a decay below 2^-150 is 0.
  * Sizes: batch 0 .. 65535, seqlen >= 0, ngroups >= 1 dividing nheads, dstate in {32, 64, 128}, headdim >= 1,
  * nheads * headdim and ngroups * dstate <= 2^30.
- * bf16 prompts with dstate 64 or 128 and headdim a multiple of 8, whose q, k and v have rows on 16-byte boundaries, go
+ * bf16 prompts with dstate 64 or 128 and headdim a multiple of 8, whose y, q, k and v have rows on 16-byte boundaries, go
  * through the tensor cores in chunks of 64 tokens from 112 tokens on (seqlen of the call, not lens; with n = batch * nheads *
- * ceil(headdim / 16), from 72 where dstate is 128 and n above 152, from 56 for n above 304, 40 from 1024, 24 from 4096): one kernel for what does not depend on the state, one for the chain of states.  The
- * others go token by token.  In chunks, a NaN or an infinity in a token may reach the outputs of the up to 63 tokens
- * before it in its chunk, and decays above 1 (A > 0, or a negative dt without the softplus) are taken as they are, but their
- * product over 64 tokens has to stay in f32's range.
+ * ceil(headdim / 16), from 72 where dstate is 128 and n above 152, from 56 for n above 304, 40 from 1024, 24 from 4096): one
+ * kernel for what does not depend on the state, one for the chain of states.  The others go token by token at every length, and so
+ * do q, k or v whose two outer strides do not nest (the larger one a multiple of the smaller and as long as all its rows: a
+ * tensor map's condition), batch * nheads above 41943, and y of 2^39 elements and more.
+ * In chunks operands are pairs of bf16 (2^-18 together) and the weights of a chunk's output sums bf16: the state is off by
+ * about 4e-6 of its size, y by 1.4e-3 besides its own rounding; token by token all is f32 (a caller who wants that of a bf16 prompt
+ * passes its tokens as f32, which is exact).  In chunks, a NaN or an infinity in a
+ * token may reach the outputs of the up to 63 tokens before it in its chunk, of its heads (of v: of its row).  Decays above 1
+ * (A > 0, or a negative dt without the softplus) are taken as they are, but their product over 64 tokens has to stay in f32's
+ * range (over any tokens of a sequence where heads are few and the prompt is long: its chain of chunks is then cut into pieces,
+ * which have their product as a factor).
  * Workspace (0 bytes where the sizes need none): 25,600 bytes for each head and chunk, of long prompts for a segment at a
- * time.  It need not be zero-filled and carries nothing from call to call.  Every call whose sizes need one clears its status
- * word (one that goes token by token too), so ssm_check_device_status reports the waits of the last of them (bounded: after one that
- * ran out every element of y and h_final is right or NaN).
+ * time, with up to two states of all heads between segments, and where chains are cut a state and a map of states a piece and head.
+ * It need not be zero-filled and carries nothing from call to call, but holds anything afterwards: one that also serves an
+ * entry point which wants zeros is zero-filled again before that.  Every call whose sizes need one clears its status word (one that
+ * goes token by token too), so ssm_check_device_status reports the waits of the last of them (bounded: after one that ran out
+ * every element of y and h_final is right or NaN).
  * Errors: SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_ALIGNMENT, SSM_ERR_WORKSPACE, SSM_ERR_CUDA.
  */
 typedef struct {

@@ -157,6 +157,8 @@ def delta_fwd(q, k, v, dt, beta, A, dt_bias=None, h0=None, lens=None, *, scale=N
     group h // (nh / G).  scale: None for N ** -0.5.  Without softplus the decay is exp(A (dt + dt_bias)), without
     sigmoid beta is taken as it is, without l2norm q and k are.  Returns (y, h_final): y [b, L, nh, H], 0 in
     the padding, and the float32 state after the last token (None when return_final_state is False).
+    Long bfloat16 prompts go in chunks through the tensor cores, whose operands leave the state off by about 4e-6 of its size and y by
+    1.4e-3 besides its rounding; the same tokens as float32 are computed in float32 throughout.
     Without a workspace (Workspace), one is allocated for the call where it is needed, and kept until the next such call (up to
     1 GiB and two states of all heads).  check_device_status(workspace), or check_device_status(kind="delta") without one,
     tells whether a wait inside the last call that needed one ran out.

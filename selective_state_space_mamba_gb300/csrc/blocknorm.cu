@@ -116,7 +116,7 @@ struct GatedParams {
   int64_t rows;
   int width, group, groups;
   float eps;
-  // u / groups for u below 2^31: (u magic) >> (32 + shift), magic = ceil(2^(32 + shift) / groups), 2^shift >= groups
+  // u / groups for u below 2^31: (u magic) >> (32 + shift), magic = ceil(2^(32 + shift) / groups), 2^shift < groups <= 2^(shift + 1)
   uint32_t magic, shift;
   __device__ __forceinline__ uint32_t row_of(uint32_t u) const { return groups == 1 ? u : (__umulhi(u, magic)) >> shift; }
 };

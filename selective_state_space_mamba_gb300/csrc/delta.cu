@@ -10,7 +10,7 @@
 //     y_t = a_t (S_{t-1} q_t) + d_t (k_t.q_t),       S_t = a_t S_{t-1} + d_t k_t.
 // Four warps scan a tile of kTile tokens in shared memory while four others bring the next one, normalised, with the products
 // of neighbouring keys, and write the outputs of the one before.  Its bound is the latency of a token's instructions, about 175
-// cycles a token (f32 b3 L517 nh6 96x64: 49 us; bf16 b1 L19 nh24 64x128: 5.5 us).
+// cycles a token (f32 b3 L517 nh6 96x64: 50 us; bf16 b1 L19 nh24 64x128: 5.5 us).
 #include "delta_common.cuh"
 
 namespace ssm {
@@ -307,8 +307,7 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
   for (int64_t tile = 0; tile < count; ++tile) {
     __syncthreads();  // tile is there, and the one before is scanned
     // Let in early, the next kernel's CTAs take places beside this one's, and its own then share SMs beside empty ones (f32 b3
-    // L517 from the start 69 us a call, from the last tile 63, not before the end 51.5; b1 L2048 nh24 348 and 276): only
-    // short prompts gain by it.
+    // L517 from the last tile 64 us a call, not before the end 50; b1 L2048 nh24 363 and 274): only short prompts gain by it.
     if (tile + 1 == count && count <= 8) griddep_launch_dependents();
     if (tile + 1 < count) {
       bring(tile + 1);
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(2 * kScan, 2) delta_kernel(const __grid_consta
 }  // namespace
 
 // With 16 rows a CTA two CTAs an SM hold all of them: they have fewer instructions in a token's chain than with 32 (f32
-// b1 L2048 nh24 64x128: 276 us, with 32 rows 516 at the time).
+// b1 L2048 nh24 64x128: 274 us, with 32 rows 362).
 bool delta_resident(const ssm_delta_args& a) { return a.batch * a.nheads * ((a.headdim + 15) / 16) <= 2 * 152; }
 
 namespace {

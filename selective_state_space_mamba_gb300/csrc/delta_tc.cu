@@ -20,18 +20,21 @@
 //     U = (D diag(e^(G_last - G))) K       A = D (TMEM), B = K: S' = e^(G_last) S + U
 //     O = Q diag(scale e^G) + D P^T        A = D (TMEM), B = P
 // Its bound is the chain of a chunk: three products (X, D, U), the three conversions between them, and six hand-overs by
-// barriers: 4900 cycles, of which the tensor cores work 2500 (the same prompt: 325 us for 128 chains of 128 chunks, both
-// kernels 504 us).  Where there are more chains than SMs, of at most 64 rows, two of them share a CTA: one converts
+// barriers: 4900 cycles, of which the tensor cores work 2500 (the same prompt: 322 us for 128 chains of 128 chunks, both
+// kernels 500 us).  Where there are more chains than SMs, of at most 64 rows, two of them share a CTA: one converts
 // while the other's products run (64x128: 3.4 us a chunk of both, one alone 2.5; b8 L2048 nh24 64x128: 122 us, one by one 174).
 //
 // Few chains leave most of the GPU idle, so they are cut into pieces that run at once.  A piece is linear in the state that
 // enters it: S_out = S_in M + N.  A first run of the chains (without outputs) gives N from a zero state, and M from
 // the unit matrix's rows and no values, as another tile of rows; delta_join multiplies the pieces up in f32, and
-// a second run, now with each piece's own state, gives the outputs (b1 L65521 nh32 64x128: 3.08 ms whole, 1.97 ms so at the time, 1.42 in pairs).
+// a second run, now with each piece's own state, gives the outputs (b1 L65521 nh32 64x128: 2.77 ms whole, 1.77 in pieces, 1.42 in pieces whose
+// chains go in pairs).
 //
 // Rounding.  q, k and v are bf16 and enter as they are (lengths and decays are factors beside the products).  S is kept in f32
-// registers; as operands S, X, T and the D of the update are split into two bf16 halves (hi + lo, 2^-18 together; lo x lo is
-// left out of U), so that the state keeps what f32 gives it to about 2^-17.  The outputs are bf16: their P is rounded once.
+// registers; as operands S, X, T, N and D are split into two bf16 halves (hi + lo, 2^-18 together; where both operands are, in X T^T and in
+// the inversion, lo x lo is left out), so that the state is off by 4e-6 of its size (in f32 throughout: 2e-7).  The outputs are
+// bf16, and P is rounded to bf16 once: y is off by 2.2e-3 of its size, of which its own rounding is 1.7e-3.  P's lower halves would
+// be 8 KB more in each of the three stages of a chain, which have 219 of the 227 KB.
 //
 // Every wait is bounded; after one that ran out the CTA's outputs are NaN.
 #include "delta_common.cuh"
